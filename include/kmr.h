@@ -214,7 +214,127 @@ int kmr_decode_attn_noalloc(const float* q, const uint16_t* k_cache, const uint1
                             int B, int n_q_heads, int n_kv_heads, int head_dim, int max_len, int slots,
                             float scale, float* out, void* stream);
 
-/* Error word of the standalone kernels (kmr_int4_gemv, kmr_decode_attn) on the
+/* ------------------------------------------------------------------ 4-bit KV cache
+ * A static, slot-addressable KV cache like the bf16 one ("kaminari", §03 StaticKVCache: a
+ * physical row per slot, mutated in place) whose keys and values are 4-bit codes with a bf16
+ * scale s and base z per group of 32, 64 or 128 dims ("kaminari", §07's group-wise int4, applied
+ * to the cache: at long context or many rows K and V are most of a step's bytes):
+ *     value = c * s + z,  c in 0..15.
+ * Quantisation of a group: lo, hi = its extremes; s = bf16((hi - lo) / 15), or 0 where that is below
+ * 2^-126; z = bf16(lo); c = round-half-even((x - z) / s) held within 0..15, 0 where s is 0.  A group
+ * that holds a NaN or an infinity, or whose range overflows, stores s = 0, z = NaN and reads back as
+ * NaN.  A position and head take 2 * (d / 2 + 4 d / group) bytes (d = 128, group 32: 160; bf16: 512).
+ *
+ * Layout, nb = d / 32 (the codes' order follows the attention kernel's tensor-core fragments):
+ *   k_codes, v_codes  uint8 [slots][n_kv][max_len][d / 2], low nibble first.  A K row is
+ *       [4][nb][8] nibbles with dim 32 b + 8 t + i at [t][b][i], a V row [8][nb][4] nibbles with
+ *       dim 32 b + 4 u + j at [u][b][j].
+ *   k_sz, v_sz        uint32 [slots][n_kv][max_len][d / group]: bf16 z in the low half, bf16 s in the
+ *       high half.
+ * All four are device memory, 16-byte aligned, owned by the caller; d is 64 or 128, group at most d,
+ * max_len a multiple of 16 up to 2^28.  A cache that fails this gives KMR_ERR_INVALID_ARG (pointers)
+ * or KMR_ERR_SHAPE.  Positions of a row that no call has written may hold anything.
+ *
+ * The calls below take up to 1024 rows (KMR_ERR_BATCH), queue their work on `stream` without
+ * synchronising and allocate nothing; they can be captured into a graph once kmr_last_device_error()
+ * or one such call has run on the device.  A row that is found bad on the device is skipped
+ * and recorded in the error word that kmr_last_device_error() reads; the other rows are not affected. */
+typedef struct kmr_kv4_cache {
+    void* k_codes;
+    void* v_codes;
+    uint32_t* k_sz;
+    uint32_t* v_sz;
+    int slots;      /* physical rows                        */
+    int n_kv_heads; /* key/value heads                      */
+    int max_len;    /* positions per row, a multiple of 16  */
+    int head_dim;   /* d: 64 or 128                         */
+    int group;      /* dims that share s and z: 32, 64, 128 */
+} kmr_kv4_cache;
+
+/* New tokens into the cache ("kaminari", §03 Mrope / TextAttention, §04 per-step positions (3, B) and
+ * cache_position): per-head RMSNorm of q and k, 3-section M-RoPE of both (contiguous sections, pairs
+ * (i, i + d/2), frequency theta^(-2i/d), as the decode step), K and V quantised to 4 bits and written, q
+ * written out for kmr_decode_attn_kv4.  One launch.
+ *   qkv        device fp32 [B, T, (n_q + 2 n_kv) d]: raw projection rows [q heads; k heads; v heads]
+ *   positions  device int32 [3, B, T]: (T, H, W) ids; the angles are exact for any id
+ *   slot_ids, cache_position  device int32 [B]: token t of row b goes to position
+ *              cache_position[b] + t of slot slot_ids[b]
+ *   n_tokens   device int32 [B], 0..T: tokens of row b, the rest is padding: not read, q_out left as it
+ *              was (0: an idle row); NULL: T tokens in every row
+ *   q_norm, k_norm  device bf16 [d], or NULL: no norm
+ *   sections   host int [3], sum d / 2
+ *   q_out      device fp32 [B, T, n_q, d]
+ *   mass       device fp32 [slots][n_kv][max_len] or NULL: set to 0 at the written positions
+ * n_q is 1..8 times n_kv.  Where two rows of a call write the same position of a slot, the later row's
+ * values stay.  qkv, q_out and the norms are 16-byte aligned.  Errors: KMR_ERR_INVALID_ARG (pointers,
+ * eps, theta, T < 1), KMR_ERR_SHAPE (heads, sections), KMR_ERR_BATCH; on the device a row with n_tokens
+ * outside 0..T (KMR_ERR_INVALID_ARG), a slot out of range (KMR_ERR_SLOT_RANGE) or tokens that do not fit
+ * [0, max_len) (KMR_ERR_CACHE_FULL) writes nothing. */
+int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, const int32_t* positions,
+                   const int32_t* slot_ids, const int32_t* cache_position, const int32_t* n_tokens, int B, int T,
+                   int n_q_heads, const uint16_t* q_norm, const uint16_t* k_norm, float eps, float rope_theta,
+                   const int* sections, float* q_out, float* mass, void* stream);
+
+/* Spans of a bf16 cache (one layer [bf16_slots][n_kv][bf16_max_len][d] of K and of V, 16-byte aligned: for
+ * instance what kmr_prefill filled, kmr_model_kv_pointers) into the 4-bit cache, and back.  Span b is
+ * lengths[b] positions (0..max_tokens) from bf16_start[b] of bf16 row bf16_slot_ids[b] and from start[b]
+ * of 4-bit row slot_ids[b]; all five arrays are device int32 [B].  kmr_kv4_to_bf16 writes
+ * bf16(c * s + z); positions outside the spans keep their contents; where two spans write the same position,
+ * the later span's values stay.  Errors: KMR_ERR_INVALID_ARG (pointers, max_tokens < 1), KMR_ERR_SHAPE,
+ * KMR_ERR_BATCH; on the device KMR_ERR_INVALID_ARG (length), KMR_ERR_SLOT_RANGE, KMR_ERR_CACHE_FULL (a span
+ * that leaves either row). */
+int kmr_kv4_from_bf16(const kmr_kv4_cache* cache, const uint16_t* k_bf16, const uint16_t* v_bf16, int bf16_slots,
+                      int bf16_max_len, const int32_t* bf16_slot_ids, const int32_t* bf16_start,
+                      const int32_t* slot_ids, const int32_t* start, const int32_t* lengths, int B, int max_tokens,
+                      void* stream);
+int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf16, int bf16_slots,
+                    int bf16_max_len, const int32_t* bf16_slot_ids, const int32_t* bf16_start,
+                    const int32_t* slot_ids, const int32_t* start, const int32_t* lengths, int B, int max_tokens,
+                    void* stream);
+
+/* kmr_decode_attn over the 4-bit cache: out = softmax(q K^T scale) V of one token per row over positions
+ * 0..cache_position[b] of slot slot_ids[b].  The split plan depends on the row's own length only: a row's
+ * result does not depend on the other rows.
+ *   q     device fp32 [B, n_q, d], 16-byte aligned; n_q is 1..8 times n_kv, query head i reads KV head
+ *         i / (n_q / n_kv)
+ *   mass  device fp32 [slots][n_kv][max_len] or NULL: position p of a row's slot gains the sum of p's
+ *         softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows that
+ *         share a slot add in row order: the result does not change from run to run.
+ *   out   device fp32 [B, n_q, d]
+ *   workspace  device memory, 16-byte aligned, kmr_decode_attn_kv4_workspace_size(cache, B, n_q, mass != NULL)
+ *         bytes or more (0 for arguments that the call would refuse); no initialisation.  Calls that may
+ *         overlap on the device need workspaces of their own.
+ * Errors: KMR_ERR_INVALID_ARG (pointers, scale not finite), KMR_ERR_SHAPE, KMR_ERR_BATCH,
+ * KMR_ERR_BUFFER_SIZE; on the device a row whose slot (KMR_ERR_SLOT_RANGE) or position (KMR_ERR_CACHE_FULL)
+ * is out of range gets zeros and adds no mass. */
+size_t kmr_decode_attn_kv4_workspace_size(const kmr_kv4_cache* cache, int B, int n_q_heads, int with_mass);
+int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_t* slot_ids,
+                        const int32_t* cache_position, int B, int n_q_heads, float scale, float* mass, float* out,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* Eviction: row src_slot_ids[b] of `src`, lengths[b] positions filled, is cut to
+ * new_lengths[b] = min(lengths[b], keep) positions, moved to positions 0.. of row dst_slot_ids[b] of
+ * `dst` (another row of the same cache, or another cache of the same heads, head_dim and group).  Each KV head
+ * keeps its newest min(recent, new_lengths[b]) positions and, of the older ones, those of largest mass, the
+ * lower position first among equals (a NaN ranks below every number), all in ascending order; a row no
+ * longer than `keep` is moved whole.  Keys keep the rotation they were written with.
+ *   lengths     device int32 [B]
+ *   keep        1..dst's max_len;  recent  0..keep
+ *   mass        device fp32 [src slots][n_kv][src max_len]
+ *   dst_mass    device fp32 [dst slots][n_kv][dst max_len] or NULL: receives the kept positions' mass (with
+ *               dst = src it may be `mass` itself)
+ *   kept        device int32 [B, n_kv, keep]: the kept positions, then -1
+ *   new_lengths device int32 [B]
+ * Positions of the destination row past new_lengths[b] keep their contents.  Two caches of a call are the
+ * same cache or share no memory.  Errors: KMR_ERR_INVALID_ARG, KMR_ERR_SHAPE, KMR_ERR_BATCH,
+ * KMR_ERR_CACHE_FULL (keep > dst's max_len); on the device a row is refused (kept -1, new_lengths 0, nothing
+ * moved) where a slot is out of range or the destination is another row's destination or, in the same
+ * cache, any row's source (KMR_ERR_SLOT_RANGE), or its length is outside [0, max_len] (KMR_ERR_CACHE_FULL). */
+int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst, const int32_t* src_slot_ids,
+                  const int32_t* dst_slot_ids, const int32_t* lengths, int B, int keep, int recent,
+                  const float* mass, float* dst_mass, int32_t* kept, int32_t* new_lengths, void* stream);
+
+/* Error word of the standalone kernels (kmr_int4_gemv, kmr_decode_attn, the 4-bit cache) on the
  * current device: synchronises the device, returns the first recorded
  * KMR_ERR_* (or KMR_OK) and clears it. */
 int kmr_last_device_error(void);

@@ -25,7 +25,8 @@ __all__ = [
     "ModelConfig", "kmr_status_string", "kmr_layout_version", "kmr_packed_size", "kmr_pack_int4",
     "kmr_unpack_int4", "kmr_int4_gemv", "kmr_decode_attn_workspace_size",
     "kmr_decode_attn", "kmr_decode_attn_noalloc", "kmr_decode_attn_cascade_workspace_size",
-    "kmr_decode_attn_cascade", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
+    "kmr_decode_attn_cascade", "Kv4Cache", "kmr_kv4_append", "kmr_kv4_from_bf16", "kmr_kv4_to_bf16",
+    "kmr_decode_attn_kv4_workspace_size", "kmr_decode_attn_kv4", "kmr_kv4_evict", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
 ]
 
 KMR_OK = 0
@@ -72,6 +73,15 @@ class ModelConfig(ctypes.Structure):
     ]
 
 
+class Kv4CacheStruct(ctypes.Structure):
+    """Mirror of kmr_kv4_cache."""
+    _fields_ = [
+        ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p), ("k_sz", ctypes.c_void_p),
+        ("v_sz", ctypes.c_void_p), ("slots", ctypes.c_int), ("n_kv_heads", ctypes.c_int), ("max_len", ctypes.c_int),
+        ("head_dim", ctypes.c_int), ("group", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
@@ -89,6 +99,13 @@ _SIGNATURES = {
     "kmr_decode_attn_cascade_workspace_size": (_SZ, [_I, _I, _I, _I, _I]),
     "kmr_decode_attn_cascade": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _I, _I, _I, _I, _I, ctypes.c_float, _P, _P, _SZ,
                                      _P]),
+    "kmr_kv4_append": (_I, [_P, _P, _P, _P, _P, _P, _I, _I, _I, _P, _P, ctypes.c_float, ctypes.c_float, _P, _P, _P,
+                            _P]),
+    "kmr_kv4_from_bf16": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "kmr_kv4_to_bf16": (_I, [_P, _P, _P, _I, _I, _P, _P, _P, _P, _P, _I, _I, _P]),
+    "kmr_decode_attn_kv4_workspace_size": (_SZ, [_P, _I, _I, _I]),
+    "kmr_decode_attn_kv4": (_I, [_P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
+    "kmr_kv4_evict": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "kmr_last_device_error": (_I, []),
     "kmr_model_create": (_I, [ctypes.POINTER(ModelConfig), ctypes.POINTER(_P)]),
     "kmr_model_destroy": (_I, [_P]),
@@ -227,6 +244,97 @@ def kmr_decode_attn_cascade(q, k_cache, v_cache, slot_ids, cache_position, prefi
                                          _ptr(cache_position), prefix_slot, prefix_len, B, nq, nkv, d, max_len,
                                          slots, float(scale), _ptr(out), _ptr(workspace), workspace_bytes,
                                          _stream(stream)), "kmr_decode_attn_cascade")
+
+
+class Kv4Cache:
+    """A 4-bit KV cache (kmr_kv4_cache) over four device tensors that it keeps alive: codes uint8
+    [slots, n_kv, max_len, d / 2] of K and V, scale words int32 [slots, n_kv, max_len, d / group]
+    (layout: include/kmr.h)."""
+
+    def __init__(self, k_codes, v_codes, k_sz, v_sz):
+        slots, n_kv, max_len, half = k_codes.shape
+        groups = k_sz.shape[-1]
+        if groups < 1 or (2 * half) % groups:
+            raise ValueError("the scale words' last dimension must divide the head size")
+        for t, size, last in ((k_codes, 1, half), (v_codes, 1, half), (k_sz, 4, groups), (v_sz, 4, groups)):
+            if tuple(t.shape) != (slots, n_kv, max_len, last) or t.element_size() != size or not t.is_contiguous():
+                raise ValueError("a 4-bit cache takes contiguous codes [slots, n_kv, max_len, d / 2] of one byte and "
+                                 "scale words [slots, n_kv, max_len, d / group] of four")
+            if t.device != k_codes.device:
+                raise ValueError("the tensors of a 4-bit cache are on one device")
+        self.tensors = (k_codes, v_codes, k_sz, v_sz)
+        self.slots, self.n_kv_heads, self.max_len = slots, n_kv, max_len
+        self.head_dim, self.group = 2 * half, 2 * half // groups
+        self._struct = Kv4CacheStruct(k_codes.data_ptr(), v_codes.data_ptr(), k_sz.data_ptr(), v_sz.data_ptr(), slots,
+                                      n_kv, max_len, self.head_dim, self.group)
+        self._as_parameter_ = ctypes.addressof(self._struct)
+
+    @classmethod
+    def zeros(cls, slots: int, n_kv_heads: int, max_len: int, head_dim: int, group: int = 32,
+              device="cuda") -> "Kv4Cache":
+        """A cache of its own, every value 0."""
+        import torch
+        codes = [torch.zeros((slots, n_kv_heads, max_len, head_dim // 2), dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        words = [torch.zeros((slots, n_kv_heads, max_len, head_dim // group), dtype=torch.int32, device=device)
+                 for _ in range(2)]
+        return cls(*codes, *words)
+
+    @property
+    def nbytes(self) -> int:
+        return sum(t.numel() * t.element_size() for t in self.tensors)
+
+
+_SECTIONS: dict = {}        # M-RoPE sections as C arrays (kept: the call reads them on the host)
+
+
+def kmr_kv4_append(cache, qkv, positions, slot_ids, cache_position, n_tokens, B, T, nq, q_norm, k_norm, eps, rope_theta,
+                   sections, q_out, mass=None, stream=None) -> None:
+    """New tokens: q/k RMSNorm, M-RoPE, 4-bit K/V into the cache, rotated queries out (see include/kmr.h)."""
+    sec = _SECTIONS.get(sections) if isinstance(sections, tuple) else None
+    if sec is None:
+        if len(sections) != 3:
+            raise ValueError("three M-RoPE sections")
+        sec = _SECTIONS[tuple(sections)] = (ctypes.c_int * 3)(*sections)
+    _check(lib().kmr_kv4_append(cache, _ptr(qkv), _ptr(positions), _ptr(slot_ids), _ptr(cache_position), _ptr(n_tokens),
+                                B, T, nq, _ptr(q_norm), _ptr(k_norm), eps, rope_theta, sec, _ptr(q_out), _ptr(mass),
+                                _stream(stream)), "kmr_kv4_append")
+
+
+def kmr_kv4_from_bf16(cache, k_bf16, v_bf16, bf16_slots, bf16_max_len, bf16_slot_ids, bf16_start, slot_ids, start,
+                      lengths, B, max_tokens, stream=None) -> None:
+    """Spans of a bf16 cache into the 4-bit cache (see include/kmr.h)."""
+    _check(lib().kmr_kv4_from_bf16(cache, _ptr(k_bf16), _ptr(v_bf16), bf16_slots, bf16_max_len, _ptr(bf16_slot_ids),
+                                   _ptr(bf16_start), _ptr(slot_ids), _ptr(start), _ptr(lengths), B, max_tokens,
+                                   _stream(stream)), "kmr_kv4_from_bf16")
+
+
+def kmr_kv4_to_bf16(cache, k_bf16, v_bf16, bf16_slots, bf16_max_len, bf16_slot_ids, bf16_start, slot_ids, start,
+                    lengths, B, max_tokens, stream=None) -> None:
+    """Spans of the 4-bit cache into a bf16 cache (see include/kmr.h)."""
+    _check(lib().kmr_kv4_to_bf16(cache, _ptr(k_bf16), _ptr(v_bf16), bf16_slots, bf16_max_len, _ptr(bf16_slot_ids),
+                                 _ptr(bf16_start), _ptr(slot_ids), _ptr(start), _ptr(lengths), B, max_tokens,
+                                 _stream(stream)), "kmr_kv4_to_bf16")
+
+
+def kmr_decode_attn_kv4_workspace_size(cache, B, nq, with_mass=False) -> int:
+    return lib().kmr_decode_attn_kv4_workspace_size(cache, B, nq, int(bool(with_mass)))
+
+
+def kmr_decode_attn_kv4(cache, q, slot_ids, cache_position, B, nq, scale, mass, out, workspace, workspace_bytes,
+                        stream=None) -> None:
+    """Decode attention over the 4-bit cache; `mass` (or None) gains every position's weight (see include/kmr.h)."""
+    _check(lib().kmr_decode_attn_kv4(cache, _ptr(q), _ptr(slot_ids), _ptr(cache_position), B, nq, scale, _ptr(mass),
+                                     _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)),
+           "kmr_decode_attn_kv4")
+
+
+def kmr_kv4_evict(src, dst, src_slot_ids, dst_slot_ids, lengths, B, keep, recent, mass, dst_mass, kept, new_lengths,
+                  stream=None) -> None:
+    """Cut rows to their newest and heaviest positions, compacted into other rows (see include/kmr.h)."""
+    _check(lib().kmr_kv4_evict(src, dst, _ptr(src_slot_ids), _ptr(dst_slot_ids), _ptr(lengths), B, keep, recent,
+                               _ptr(mass), _ptr(dst_mass), _ptr(kept), _ptr(new_lengths), _stream(stream)),
+           "kmr_kv4_evict")
 
 
 def kmr_prefill_plan(N: int, K: int, M: int, sms: int) -> Tuple[int, int]:

@@ -1,0 +1,154 @@
+// The 4-bit KV cache: addressing, the group quantiser and the parameter blocks of its kernels.
+//
+// A cached vector (one slot, KV head and position; d = 64 or 128 dims) holds 4-bit codes c and,
+// for every group of 32, 64 or 128 dims, a bf16 scale s and a bf16 base z: value = c s + z.
+// Codes are ordered for the attention kernel's tensor-core fragments (kmr_kv4_attn.cu): with
+// nb = d / 32 blocks of 32 dims,
+//   K row: [4][nb][8] nibbles, dim 32 b + 8 t + i at [t][b][i]: lane t of a fragment's four lanes
+//          reads its 8 dims of every block in one load;
+//   V row: [8][nb][4] nibbles, dim 32 b + 4 u + j at [u][b][j]: likewise lane u of eight.
+#pragma once
+
+#include "kmr_internal.cuh"
+
+namespace kmr {
+
+constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at the others for clashes)
+constexpr int kKv4MaxRep = 8;            // query heads per KV head
+constexpr int kKv4MaxSplits = 32;
+constexpr int kKv4MinChunk = 128;        // positions per split, at least
+
+struct Kv4View {
+    uint8_t* kc;                         // [slots][nkv][S][d / 2]
+    uint8_t* vc;
+    uint32_t* ks;                        // [slots][nkv][S][d / g]: z in the low half, s in the high half
+    uint32_t* vs;
+    int slots, nkv, S, d, g;
+};
+
+// 16-bit unit (4 codes) of dims 4 q .. 4 q + 3 within a row.
+__host__ __device__ __forceinline__ int kv4_unit(int q, int nb, bool key) {
+    const int b = q >> 3, r = q & 7;
+    return key ? ((r >> 1) * nb + b) * 2 + (r & 1) : r * nb + b;
+}
+__device__ __forceinline__ float kv4_s(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+__device__ __forceinline__ float kv4_z(uint32_t w) { return __uint_as_float(w << 16); }
+
+// Four dims per lane of a group spread over g / 4 neighbouring lanes: the group's word (z, s) and
+// the lane's four codes.  lo, hi = the group's extremes; s = bf16((hi - lo) / 15), 0 below 2^-126
+// (its reciprocal would leave the normal range); z = bf16(lo); c = rint((x - z) / s) within 0..15,
+// 0 where s is 0.  The quotient is the correctly rounded one (Markstein 1990: with r = rn(1 / s),
+// q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value half-way between two codes is seen
+// as half-way and goes to the even one.  A group that holds a NaN or an infinity, or whose range
+// overflows, stores s = 0 and z = NaN: it reads back as NaN.
+__device__ __forceinline__ uint32_t kv4_quantize(const float (&x)[4], int lanes, uint32_t& word) {
+    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
+    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+    // a sum that is not finite marks the group: x - x is 0 for a finite x, NaN otherwise
+    float odd = __fadd_rn(__fadd_rn(__fsub_rn(x[0], x[0]), __fsub_rn(x[1], x[1])),
+                          __fadd_rn(__fsub_rn(x[2], x[2]), __fsub_rn(x[3], x[3])));
+    uint32_t bad = odd != 0.f ? 1u : 0u;
+    for (int o = 1; o < lanes; o <<= 1) {
+        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
+        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
+    }
+    uint32_t sb = f32_to_bf16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+    if (sb < 0x0080u) sb = 0u;                       // below 2^-126
+    uint32_t zb = f32_to_bf16_rn(lo);
+    if (bad || sb >= 0x7F80u || (zb & 0x7F80u) == 0x7F80u) {
+        sb = 0u;
+        zb = 0x7FC0u;
+    }
+    word = zb | (sb << 16);
+    const float s = __uint_as_float(sb << 16), z = __uint_as_float(zb << 16);
+    if (sb == 0u) return 0u;
+    const float r = __frcp_rn(s);
+    uint32_t c = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        const float a = __fsub_rn(x[e], z);
+        const float q0 = __fmul_rn(a, r);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
+        c |= uint32_t(fminf(fmaxf(rintf(q), 0.f), 15.f)) << (4 * e);
+    }
+    return c;
+}
+
+struct Kv4AppendParams {
+    Kv4View c;
+    const float* qkv;                    // [B][T][(nq + 2 nkv) d]
+    const int32_t* positions;            // [3][B][T]
+    const int32_t* slot_ids;             // [B]
+    const int32_t* cpos;                 // [B]: cache position of the row's token 0
+    const int32_t* n_tokens;             // [B] or null: T
+    int B, T, nq;
+    const uint16_t* qn_w;                // bf16 [d] or null
+    const uint16_t* kn_w;
+    float eps;
+    int sec0, sec1;
+    float* q_out;                        // [B][T][nq][d]
+    float* mass;                         // [slots][nkv][S] or null
+    int* err;
+    unsigned long long turn[64];         // frequency i in turns per position, as a 64-bit fraction
+};
+cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st);
+
+struct Kv4ConvertParams {
+    Kv4View c;
+    uint16_t* k16;                       // bf16 [slots16][nkv][S16][d]
+    uint16_t* v16;
+    int slots16, S16;
+    const int32_t* slot16;               // [B]
+    const int32_t* start16;
+    const int32_t* slot_ids;
+    const int32_t* start;
+    const int32_t* lengths;
+    int B, T;
+    int* err;
+};
+cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st);
+
+struct Kv4AttnParams {
+    Kv4View c;
+    const float* q;                      // [B][nq][d]
+    const int32_t* slot_ids;
+    const int32_t* cpos;
+    int B, nq;
+    float scale;
+    float* mass;                         // [slots][nkv][S] or null
+    float* out;                          // [B][nq][d]
+    float* part;                         // [B][nkv][nsplit][rep][d + 2]
+    float* scores;                       // [B][nkv][rep][S] base-2 scores (mass only)
+    int nsplit;                          // grid.x: the most splits a row of this cache can have
+    int* err;
+};
+size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit);
+int kv4_attn_splits(int S);
+cudaError_t kv4_attn_set_attributes();
+cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st);
+
+struct Kv4EvictParams {
+    Kv4View src, dst;
+    const int32_t* src_ids;              // [B]
+    const int32_t* dst_ids;
+    const int32_t* lengths;
+    int B, keep, recent;
+    int same;                            // source and destination are one cache (or one mass)
+    const float* mass;                   // [src.slots][nkv][src.S]
+    float* dst_mass;                     // [dst.slots][nkv][dst.S] or null
+    int32_t* kept;                       // [B][nkv][keep]
+    int32_t* new_lengths;                // [B]
+    int* err;
+};
+cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st);
+
+// Positions of a row are cut into splits of max(128, ceil(L / 32) rounded up to 16): by the row's own
+// length alone, so that a row's result does not depend on the others of the call.
+__host__ __device__ __forceinline__ void kv4_split_plan(int L, int& chunk, int& ns) {
+    chunk = (((L + kKv4MaxSplits - 1) / kKv4MaxSplits) + 15) & ~15;
+    if (chunk < kKv4MinChunk) chunk = kKv4MinChunk;
+    ns = (L + chunk - 1) / chunk;
+}
+
+}  // namespace kmr

@@ -1,0 +1,624 @@
+"""GPU parity of the 4-bit KV cache against its oracle: appended tokens, conversions, decode attention with
+the mass, eviction, and a run of them together."""
+import math
+
+import numpy as np
+import pytest
+
+from gpu_helpers import rel_l2, require_gpu
+import int4_weight_only_group_gb300 as kmr
+from oracle import kv4
+
+pytestmark = pytest.mark.gpu
+
+SECTIONS = {64: (8, 12, 12), 128: (16, 24, 24)}
+# fp32 scores: |error| <= (d + 4) 2^-24 sum|q k| scale, and with unit-variance q and k of 128 dims the sum is
+# about 0.64 * 128 * 128^-0.5 = 7, so a weight is off by at most 5e-5 of itself, and so is an output
+ATTN_TOL = 1e-4
+
+
+@pytest.fixture(scope="module")
+def torch():
+    return require_gpu()
+
+
+def i32(torch, a):
+    return torch.tensor(np.asarray(a), dtype=torch.int32, device="cuda")
+
+
+class Cache:
+    """A device cache and, beside it, the bf16-free truth: what each written position reads back as."""
+
+    def __init__(self, torch, r, slots, nkv, S, d, g, fill=None, shift=0.0, spread=1.0):
+        """fill: positions written per slot; the rest holds random codes with NaN scales."""
+        self.torch, self.shape = torch, (slots, nkv, S, d, g)
+        self.val, t = {}, {}
+        for key in ("k", "v"):
+            x = (r.standard_normal((slots, nkv, S, d)) * spread + shift).astype(np.float32)
+            c, sb, zb = kv4.quantize(x, g)
+            words = kv4.pack_words(sb, zb)
+            rows = kv4.pack_rows(c, key == "k")
+            self.val[key] = kv4.dequantize(c, sb, zb)
+            if fill is not None:
+                for s, n in enumerate(fill):
+                    rows[s, :, n:] = r.integers(0, 256, rows[s, :, n:].shape, dtype=np.uint8)
+                    words[s, :, n:] = kv4.pack_words(np.uint16([0x7FC0]), np.uint16([0x7FC0]))
+            t[key], t[key + "w"] = torch.from_numpy(rows).cuda(), torch.from_numpy(words).cuda()
+        self.dev = kmr.Kv4Cache(t["k"], t["v"], t["kw"], t["vw"])
+
+    def host(self):
+        return [t.cpu().numpy() for t in self.dev.tensors]
+
+
+def attend(torch, cache, q, ids, cpos, mass=None, stream=None, scale=None):
+    B, nq, d = q.shape
+    n = kmr.kmr_decode_attn_kv4_workspace_size(cache, B, nq, mass is not None)
+    assert n > 0
+    ws = torch.full((n // 4,), float("nan"), device="cuda")
+    out = torch.full((B, nq, d), float("nan"), device="cuda")
+    kmr.kmr_decode_attn_kv4(cache, torch.from_numpy(q).cuda(), i32(torch, ids), i32(torch, cpos), B, nq,
+                            scale or 1.0 / math.sqrt(d), mass, out, ws, n, stream or torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    return out.cpu().numpy()
+
+
+# ------------------------------------------------------------------ conversion
+@pytest.mark.parametrize("d,g", [(128, 32), (128, 64), (128, 128), (64, 32), (64, 64)])
+def test_from_and_to_bf16_bit_exact(torch, d, g):
+    """Spans of several lengths (0 and 1 among them), at odd starts, into scattered slots: the codes and scales
+    are the oracle's bit for bit, everything outside the spans keeps its bits, and the way back gives
+    bf16(c s + z)."""
+    r = np.random.default_rng(d + g)
+    nkv, S, S16, slots, slots16 = 3, 96, 77, 5, 4
+    n, start, start16, ids, ids16 = [0, 1, 33, 75], [5, 95, 17, 0], [70, 3, 11, 2], [4, 0, 2, 3], [0, 1, 3, 2]
+    x = [(r.standard_normal((slots16, nkv, S16, d)) * np.exp(r.standard_normal((slots16, nkv, S16, 1)))).astype(np.float32)
+         for _ in range(2)]
+    x[0][3, 0, 11] = 0.0                          # a constant row, ties, an infinity, a NaN, tiny and huge values
+    x[0][3, 1, 12] = np.tile(np.float32([0, 15, 0.5, 1.5]), d // 4)
+    x[1][3, 0, 13, 7] = np.inf
+    x[1][3, 0, 14, 9] = np.nan
+    x[1][3, 2, 15] *= np.float32(1e-38)
+    x[0][3, 2, 16] *= np.float32(1e30)
+    x[0][3, 2, 17, :2] = [3e38, -3e38]
+    bits = [kv4.bf16_bits(a) for a in x]
+    dev16 = [torch.from_numpy(b.view(np.int16)).cuda() for b in bits]
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    args = [i32(torch, a) for a in (ids16, start16, ids, start, n)]
+    kmr.kmr_kv4_from_bf16(c.dev, *dev16, slots16, S16, *args, 4, 80, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    want = [a.copy() for a in before]
+    for b in range(4):
+        for i, key in ((0, True), (1, False)):
+            codes, sb, zb = kv4.quantize(kv4.bf16_value(bits[i][ids16[b], :, start16[b]:start16[b] + n[b]]), g)
+            want[i][ids[b], :, start[b]:start[b] + n[b]] = kv4.pack_rows(codes, key)
+            want[2 + i][ids[b], :, start[b]:start[b] + n[b]] = kv4.pack_words(sb, zb)
+    for got, w in zip(c.host(), want):
+        assert np.array_equal(got, w)
+    back = [torch.full((slots16, nkv, S16, d), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kmr.kmr_kv4_to_bf16(c.dev, *back, slots16, S16, *args, 4, 80, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    for i in range(2):
+        expect = np.full((slots16, nkv, S16, d), 7.0, np.float32)
+        for b in range(4):
+            at = (ids16[b], slice(None), slice(start16[b], start16[b] + n[b]))
+            val = kv4.dequantize(*kv4.quantize(kv4.bf16_value(bits[i][at]), g))
+            with np.errstate(all="ignore"):
+                expect[at] = kv4.bf16_value(kv4.bf16_bits(val.astype(np.float32)))
+        assert np.array_equal(back[i].float().cpu().numpy(), expect, equal_nan=True)
+
+
+def test_convert_bad_and_clashing_spans(torch):
+    r = np.random.default_rng(3)
+    nkv, S, d, g, B = 2, 32, 64, 32, 6
+    src = [torch.from_numpy(kv4.bf16_bits(r.standard_normal((B, nkv, S, d)).astype(np.float32)).view(np.int16)).cuda()
+           for _ in range(2)]
+    c = Cache(torch, r, 3, nkv, S, d, g)
+    before = c.host()
+    # rows 0..3 are bad: length, slot, end of the 4-bit row, end of the bf16 row; 4 and 5 overlap at 8..11
+    ids, start, n = [0, 3, 0, 0, 1, 1], [0, 0, 30, 0, 4, 8], [17, 4, 4, 4, 8, 8]
+    ids16, start16 = [0, 1, 2, 3, 4, 5], [0, 0, 0, 30, 0, 0]
+    kmr.kmr_kv4_from_bf16(c.dev, *src, B, S, i32(torch, ids16), i32(torch, start16), i32(torch, ids), i32(torch, start),
+                          i32(torch, n), B, 16, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_INVALID_ARG, kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    assert kmr.kmr_last_device_error() == 0
+    after = c.host()
+    for a, b in zip(after, before):
+        assert np.array_equal(a[[0, 2]], b[[0, 2]]) and np.array_equal(a[1, :, :4], b[1, :, :4])
+    x = kv4.bf16_value(src[0].cpu().numpy().view(np.uint16))
+    for lo, hi, row, at in ((4, 8, 4, 0), (8, 16, 5, 0)):
+        codes, sb, zb = kv4.quantize(x[row, :, at:at + hi - lo], g)
+        assert np.array_equal(after[0][1, :, lo:hi], kv4.pack_rows(codes, True))
+        assert np.array_equal(after[2][1, :, lo:hi], kv4.pack_words(sb, zb))
+    # back: two spans onto one bf16 row
+    dst = [torch.zeros((1, nkv, S, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    z = i32(torch, [0, 0])
+    kmr.kmr_kv4_to_bf16(c.dev, *dst, 1, S, z, z, i32(torch, [0, 1]), i32(torch, [0, 4]), i32(torch, [8, 4]), 2, 8,
+                        torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    first = kv4.dequantize(*kv4.quantize(x[4, :, 0:4], g)).astype(np.float32)
+    assert np.array_equal(dst[0][0, :, :4].float().cpu().numpy(), kv4.bf16_value(kv4.bf16_bits(first)))
+    assert bool((dst[0][0, :, 8:] == 0).all()) and bool((dst[0][0, :, 4:8] != 0).any())
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("d,g,nq,nkv,T", [(128, 32, 16, 8, 1), (64, 64, 4, 2, 5), (128, 128, 3, 3, 3), (64, 32, 8, 1, 17),
+                                          (128, 64, 10, 5, 2), (64, 32, 7, 1, 1)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_append_matches_oracle(torch, d, g, nq, nkv, T, norm):
+    r = np.random.default_rng(d * g + nq + T)
+    B, S, slots, theta, eps = 4, 64, 5, 1e6, 1e-6
+    ids, cpos, n = [3, 0, 4, 1], [0, S - T, 20, 7], [T, T, max(0, T - 2), max(1, T // 2)]
+    qkv = (r.standard_normal((B, T, nq + 2 * nkv, d)) * 3).astype(np.float32)
+    pos = r.integers(-60, 200000, (3, B, T)).astype(np.int32)
+    pos[:, 0] = pos[:1, 0]
+    w = [1 + 0.1 * r.standard_normal(d).astype(np.float32) for _ in range(2)] if norm else [None, None]
+    wb = [kv4.bf16_bits(a) if norm else None for a in w]
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    q = torch.full((B, T, nq, d), 9.0, device="cuda")
+    mass = torch.full((slots, nkv, S), 5.0, device="cuda")
+    dev = [torch.from_numpy(a.view(np.int16)).cuda() if norm else None for a in wb]
+    kmr.kmr_kv4_append(c.dev, torch.from_numpy(qkv).cuda(), torch.from_numpy(pos).cuda(), i32(torch, ids), i32(torch, cpos),
+                       i32(torch, n), B, T, nq, dev[0], dev[1], eps, theta, SECTIONS[d], q, mass,
+                       torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    got, kq = c.host(), q.cpu().numpy()
+    mass = mass.cpu().numpy()
+    touched = np.zeros((slots, S), bool)
+    for b in range(B):
+        assert (kq[b, n[b]:] == 9.0).all()
+        for t in range(n[b]):
+            at = cpos[b] + t
+            touched[ids[b], at] = True
+            assert (mass[ids[b], :, at] == 0).all()
+            for h in range(nq + nkv):
+                x = qkv[b, t, h]
+                i = 0 if h < nq else 1
+                want = kv4.norm_rope(x, kv4.bf16_value(wb[i]) if norm else None, pos[:, b, t], eps, theta, SECTIONS[d])
+                plain = kv4.norm_rope(x, kv4.bf16_value(wb[i]) if norm else None, (0, 0, 0), eps, theta, SECTIONS[d])
+                # about 16 roundings of 2^-24 (sum of squares, rsqrt, three products, cosine and sine, their
+                # products and sum) of the pair's size
+                size = np.abs(plain) + np.abs(np.roll(plain, d // 2))
+                tol = 32 * 2.0 ** -24 * size
+                if h < nq:
+                    assert (np.abs(kq[b, t, h] - want) <= tol).all(), (b, t, h)
+                else:
+                    kvh = h - nq
+                    codes = kv4.unpack_rows(got[0][ids[b], kvh, at], True)
+                    u = got[2][ids[b], kvh, at].view(np.uint32)
+                    sb, zb = (u >> 16).astype(np.uint16), (u & 0xFFFF).astype(np.uint16)
+                    s, z = (np.repeat(kv4.bf16_value(a), g).astype(np.float64) for a in (sb, zb))
+                    off = np.abs(kv4.dequantize(codes, sb, zb) - want)
+                    assert (off <= s * (0.5 + 15 * 2.0 ** -9 * 1.01) + np.abs(z) * 2.0 ** -8 + tol).all()
+            codes, sb, zb = kv4.quantize(qkv[b, t, nq + nkv:], g)              # V is quantised as it came
+            assert np.array_equal(got[1][ids[b], :, at], kv4.pack_rows(codes, False))
+            assert np.array_equal(got[3][ids[b], :, at], kv4.pack_words(sb, zb))
+    for a, w0 in zip(got, before):
+        for s in range(slots):
+            assert np.array_equal(a[s][:, ~touched[s]], w0[s][:, ~touched[s]])
+    assert all((mass[s][:, ~touched[s]] == 5.0).all() for s in range(slots))
+
+
+def test_append_far_positions_keep_their_angle(torch):
+    """Angles of positions near 2^31 (both signs): the fastest pair turns by a radian per position."""
+    r = np.random.default_rng(8)
+    d, nkv, nq, T = 128, 1, 1, 8
+    pos1 = np.array([2 ** 31 - 1, -2 ** 31, 2 ** 30 + 12345, -7, 0, 1, 999999937, -123456789], np.int64)
+    pos = np.stack([pos1, pos1[::-1], np.roll(pos1, 3)])[:, None].astype(np.int32)
+    qkv = r.standard_normal((1, T, 3, d)).astype(np.float32)
+    c = kmr.Kv4Cache.zeros(1, nkv, 16, d, 32)
+    q = torch.zeros((1, T, nq, d), device="cuda")
+    kmr.kmr_kv4_append(c, torch.from_numpy(qkv).cuda(), torch.from_numpy(pos).cuda(), i32(torch, [0]), i32(torch, [0]),
+                       None, 1, T, nq, None, None, 1e-6, 1e6, SECTIONS[d], q, None, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    for t in range(T):
+        x = qkv[0, t, 0].astype(np.float64)
+        want = np.empty(d)
+        for i in range(d // 2):
+            axis = 0 if i < 16 else (1 if i < 40 else 2)
+            # in extended precision: a double's cosine at 2^31 radians is itself good to 2^-22 only in the frequency
+            a = np.longdouble(int(pos[axis, 0, t])) * np.longdouble(1e6) ** (np.longdouble(-2 * i) / d)
+            co, si = float(np.cos(a)), float(np.sin(a))
+            want[i], want[i + 64] = x[i] * co - x[i + 64] * si, x[i + 64] * co + x[i] * si
+        # the frequency in double (2^-53, 64 products) times 2^31 radians: 2^-53 * 64 * 2^31 = 2^-16 at worst,
+        # and less the slower the pair; the roundings of the rotation beside it
+        assert np.abs(q[0, t, 0].cpu().numpy() - want).max() <= 2.0 ** -16 * np.abs(x).max() * 2, t
+
+
+def test_append_bad_and_clashing_rows(torch):
+    r = np.random.default_rng(9)
+    B, T, nq, nkv, d, g, S, slots = 7, 4, 2, 1, 64, 32, 32, 3
+    qkv = r.standard_normal((B, T, nq + 2 * nkv, d)).astype(np.float32)
+    #   bad: tokens -1, tokens 5, slot 3, slot -1, end; rows 5 and 6 overlap at positions 6, 7
+    n, ids, cpos = [-1, 5, 4, 4, 4, 4, 4], [0, 0, 3, -1, 0, 1, 1], [0, 0, 0, 0, 29, 4, 6]
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    q = torch.full((B, T, nq, d), 9.0, device="cuda")
+    kmr.kmr_kv4_append(c.dev, torch.from_numpy(qkv).cuda(), torch.zeros((3, B, T), dtype=torch.int32, device="cuda"),
+                       i32(torch, ids), i32(torch, cpos), i32(torch, n), B, T, nq, None, None, 1e-6, 1e6, SECTIONS[d], q,
+                       None, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_INVALID_ARG, kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    got = c.host()
+    assert (q[:5] == 9.0).all().item()
+    assert np.array_equal(q[5:].cpu().numpy(), qkv[5:, :, :nq])          # position 0: no rotation; both rows' queries
+    for a, w in zip(got, before):
+        assert np.array_equal(a[[0, 2]], w[[0, 2]])
+    for row, lo, hi in ((5, 4, 6), (6, 6, 10)):
+        for i, off in ((0, nq), (1, nq + nkv)):
+            codes, sb, zb = kv4.quantize(qkv[row, :hi - lo, off:off + nkv].transpose(1, 0, 2), g)
+            assert np.array_equal(got[i][1, :, lo:hi], kv4.pack_rows(codes, i == 0)), (row, i)
+            assert np.array_equal(got[2 + i][1, :, lo:hi], kv4.pack_words(sb, zb))
+
+
+# ------------------------------------------------------------------ attention
+@pytest.mark.parametrize("d,g", [(128, 32), (128, 64), (128, 128), (64, 32), (64, 64)])
+@pytest.mark.parametrize("nq,nkv", [(16, 8), (4, 4), (8, 2), (3, 1), (5, 1), (16, 2), (7, 1)])
+def test_attention_matches_oracle(torch, d, g, nq, nkv):
+    r = np.random.default_rng(d + g + nq)
+    S, slots = 1104, 12
+    L = [1, 2, 15, 16, 17, 127, 128, 129, 600, 1023, 1104]
+    ids = [11, 3, 0, 5, 2, 7, 1, 9, 8, 10, 6]
+    fill = [0] * slots
+    for s, n in zip(ids, L):
+        fill[s] = n
+    c = Cache(torch, r, slots, nkv, S, d, g, fill)
+    q = r.standard_normal((len(L), nq, d)).astype(np.float32) * 1.5
+    mass0 = r.random((slots, nkv, S)).astype(np.float32)
+    mass = torch.from_numpy(mass0.copy()).cuda()
+    out = attend(torch, c.dev, q, ids, np.array(L) - 1, mass)
+    assert kmr.kmr_last_device_error() == 0
+    want = mass0.astype(np.float64)
+    for b, n in enumerate(L):
+        ref, m = kv4.attention(q[b], c.val["k"][ids[b], :, :n], c.val["v"][ids[b], :, :n], 1 / math.sqrt(d))
+        assert rel_l2(out[b], ref) <= ATTN_TOL, (n, rel_l2(out[b], ref))
+        want[ids[b], :, :n] += m
+    got = mass.cpu().numpy()
+    # a weight is off by ATTN_TOL of itself; the addition rounds once
+    assert (np.abs(got - want) <= ATTN_TOL * (want - mass0) + 2.0 ** -23 * want).all()
+    again = attend(torch, c.dev, q, ids, np.array(L) - 1)                  # without the mass: the same bits
+    assert np.array_equal(out, again)
+    for b in (0, 5, 10):                                                   # a row alone: the same bits
+        one = attend(torch, c.dev, q[b:b + 1], ids[b:b + 1], [L[b] - 1])
+        assert np.array_equal(one[0], out[b])
+
+
+@pytest.mark.parametrize("L", [4096, 4097, 8191, 40000])
+def test_attention_long_rows(torch, L):
+    r = np.random.default_rng(L)
+    S, nq, nkv, d, g = (L + 15) // 16 * 16, 4, 2, 128, 32
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    q = r.standard_normal((1, nq, d)).astype(np.float32) * 1.5
+    mass = torch.zeros((1, nkv, S), device="cuda")
+    out = attend(torch, c.dev, q, [0], [L - 1], mass)
+    ref, m = kv4.attention(q[0], c.val["k"][0, :, :L], c.val["v"][0, :, :L], 1 / math.sqrt(d))
+    assert rel_l2(out[0], ref) <= ATTN_TOL
+    got = mass.cpu().numpy()[0]
+    assert (got[:, L:] == 0).all() and (np.abs(got[:, :L] - m) <= ATTN_TOL * m + 1e-30).all()
+
+
+@pytest.mark.parametrize("spread,shift", [(1e-4, 0.0), (1e4, 0.0), (1.0, 50.0), (3e6, 0.0), (1e-12, 0.0)])
+def test_attention_value_ranges(torch, spread, shift):
+    """Values far from 1: the scales leave half precision's range on either side, or ride on a large base."""
+    r = np.random.default_rng(17)
+    S, L, nq, nkv, d, g = 512, 500, 4, 2, 128, 32
+    c = Cache(torch, r, 1, nkv, S, d, g, [L], shift, spread)
+    # outlier groups among them: ranges that differ by 10^4 within a row
+    q = (r.standard_normal((1, nq, d)) / max(spread, shift)).astype(np.float32)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    ref, _ = kv4.attention(q[0], c.val["k"][0, :, :L], c.val["v"][0, :, :L], 1 / math.sqrt(d))
+    # with a base of 50 the scores are sums of 128 terms of about 0.8 each, as in ATTN_TOL's arithmetic
+    assert rel_l2(out[0], ref) <= ATTN_TOL, rel_l2(out[0], ref)
+
+
+def test_attention_scales_that_vary_along_the_row(torch):
+    """A row whose values grow by 10^9 from first to last position, and one where they shrink: the early (late)
+    positions are nothing beside the others, and neither overflow."""
+    r = np.random.default_rng(18)
+    S, nq, nkv, d, g = 1024, 2, 1, 64, 32
+    for up in (True, False):
+        c = Cache(torch, r, 1, nkv, S, d, g)
+        ramp = np.exp(np.linspace(-10, 10, S) * (1 if up else -1))[None, :, None]
+        x = (r.standard_normal((1, nkv, S, d)) * ramp).astype(np.float32)
+        codes, sb, zb = kv4.quantize(x, g)
+        c.dev.tensors[1].copy_(torch.from_numpy(kv4.pack_rows(codes, False)))
+        c.dev.tensors[3].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+        q = r.standard_normal((1, nq, d)).astype(np.float32)
+        out = attend(torch, c.dev, q, [0], [S - 1])
+        ref, _ = kv4.attention(q[0], c.val["k"][0], kv4.dequantize(codes, sb, zb)[0], 1 / math.sqrt(d))
+        assert rel_l2(out[0], ref) <= ATTN_TOL
+
+
+def test_attention_sharp_and_flat_softmax(torch):
+    """One position that takes all the weight (scores apart by hundreds), and q = 0: the mean of V."""
+    r = np.random.default_rng(19)
+    S, L, nq, nkv, d, g = 256, 201, 4, 2, 64, 64
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    q = np.zeros((1, nq, d), np.float32)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    mean = c.val["v"][0, :, :L].mean(1).repeat(nq // nkv, 0)
+    assert np.abs(out[0] - mean).max() <= 2.0 ** -20
+    q = np.stack([c.val["k"][0, h // 2, 77] * 40 for h in range(nq)])[None].astype(np.float32)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    # the weight is 1 to single precision; codes times scale and the base: three roundings
+    assert np.abs(out[0] - c.val["v"][0, :, 77].repeat(nq // nkv, 0)).max() <= 2.0 ** -20
+
+
+def test_attention_bad_rows(torch):
+    r = np.random.default_rng(20)
+    S, nq, nkv, d, g, slots = 64, 4, 2, 128, 64, 3
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    q = r.standard_normal((6, nq, d)).astype(np.float32)
+    mass = torch.zeros((slots, nkv, S), device="cuda")
+    out = attend(torch, c.dev, q, [0, 3, -1, 1, 1, 2], [5, 5, 5, 64, -1, 63], mass)
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    assert not out[1:5].any() and (mass[1] == 0).all().item()
+    for b, s, n in ((0, 0, 6), (5, 2, 64)):
+        ref, m = kv4.attention(q[b], c.val["k"][s, :, :n], c.val["v"][s, :, :n], 1 / math.sqrt(d))
+        assert rel_l2(out[b], ref) <= ATTN_TOL
+        assert np.allclose(mass[s, :, :n].cpu().numpy(), m, rtol=2e-4, atol=0)
+
+
+def test_attention_rows_that_share_a_slot(torch):
+    """Several rows of one slot (several continuations of a prompt): each attends on its own, and the slot's mass
+    gains all of them, the same bits every run."""
+    r = np.random.default_rng(21)
+    S, nq, nkv, d, g = 512, 4, 2, 128, 32
+    c = Cache(torch, r, 2, nkv, S, d, g)
+    ids, n = [1, 0, 1, 1, 0, 9], [300, 40, 512, 7, 1, 5]
+    q = r.standard_normal((6, nq, d)).astype(np.float32)
+    runs = []
+    for _ in range(3):
+        mass = torch.zeros((2, nkv, S), device="cuda")
+        out = attend(torch, c.dev, q, ids, np.array(n) - 1, mass)
+        runs.append((out, mass.cpu().numpy()))
+    assert all(np.array_equal(a, runs[0][0]) and np.array_equal(m, runs[0][1]) for a, m in runs)
+    want = np.zeros((2, nkv, S))
+    for b in range(5):
+        ref, m = kv4.attention(q[b], c.val["k"][ids[b], :, :n[b]], c.val["v"][ids[b], :, :n[b]], 1 / math.sqrt(d))
+        assert rel_l2(runs[0][0][b], ref) <= ATTN_TOL
+        want[ids[b], :, :n[b]] += m
+    assert (np.abs(runs[0][1] - want) <= (ATTN_TOL + 4 * 2.0 ** -24) * want).all()
+    assert kmr.kmr_last_device_error() == kmr.KMR_ERR_SLOT_RANGE
+
+
+def test_attention_beyond_32_bit_offsets(torch):
+    """A slot whose codes start past 4 GB and whose elements pass 2^32."""
+    r = np.random.default_rng(22)
+    slots, nkv, S, d, g, L, nq = 9, 8, 1 << 20, 128, 128, 1000, 16
+    tens = [torch.empty((slots, nkv, S, d // 2), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    tens += [torch.empty((slots, nkv, S, d // g), dtype=torch.int32, device="cuda") for _ in range(2)]
+    small = Cache(torch, r, 1, nkv, 1008, d, g)
+    c = kmr.Kv4Cache(*tens)
+    for t, s in zip(tens, small.dev.tensors):
+        t[8, :, S - 1008:] = s[0]
+    src = [torch.empty((1, nkv, 1008, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kmr.kmr_kv4_to_bf16(c, *src, 1, 1008, i32(torch, [0]), i32(torch, [0]), i32(torch, [8]), i32(torch, [S - 1008]),
+                        i32(torch, [1008]), 1, 1008, torch.cuda.current_stream())
+    kmr.kmr_kv4_from_bf16(c, *src, 1, 1008, i32(torch, [0]), i32(torch, [0]), i32(torch, [8]), i32(torch, [0]),
+                          i32(torch, [1008]), 1, 1008, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    K, V = (a[0].float().cpu().numpy().astype(np.float64) for a in src)
+    for i, x in ((0, K), (1, V)):
+        codes, sb, zb = kv4.quantize(x, g)
+        assert np.array_equal(tens[i][8, :, :1008].cpu().numpy(), kv4.pack_rows(codes, i == 0))
+    vals = [kv4.dequantize(*kv4.quantize(x, g)) for x in (K, V)]
+    q = r.standard_normal((1, nq, d)).astype(np.float32)
+    out = attend(torch, c, q, [8], [L - 1])
+    ref, _ = kv4.attention(q[0], vals[0][:, :L], vals[1][:, :L], 1 / math.sqrt(d))
+    assert rel_l2(out[0], ref) <= ATTN_TOL
+
+
+# ------------------------------------------------------------------ eviction
+def evict(torch, src, dst, ids, dids, n, keep, recent, mass, dmass):
+    B, nkv = len(ids), src.n_kv_heads
+    kept = torch.full((B, nkv, keep), 77, dtype=torch.int32, device="cuda")
+    new = torch.full((B,), 77, dtype=torch.int32, device="cuda")
+    kmr.kmr_kv4_evict(src, dst, i32(torch, ids), i32(torch, dids), i32(torch, n), B, keep, recent, mass, dmass, kept, new,
+                      torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    return kept.cpu().numpy(), new.cpu().numpy()
+
+
+@pytest.mark.parametrize("d,g,nkv", [(128, 32, 8), (64, 64, 1), (128, 128, 2), (64, 32, 3)])
+@pytest.mark.parametrize("keep,recent", [(1, 0), (1, 1), (17, 5), (64, 64), (300, 33), (512, 0)])
+def test_evict_matches_oracle(torch, d, g, nkv, keep, recent):
+    r = np.random.default_rng(d + keep)
+    S, slots = 2064, 7
+    n, ids, dids = [0, 1, 300, 301, 2064, 511, 2063], [6, 0, 3, 1, 2, 5, 4], [1, 0, 2, 6, 5, 3, 4]
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    m = np.exp(2 * r.standard_normal((slots, nkv, S))).astype(np.float32)
+    m[r.random(m.shape) < 0.3] = 0.0                        # ties at zero
+    m[2, :, 100:1500] = np.float32(0.25)                    # a long run of equals
+    m[5, 0, :200] = np.nan
+    m[4, 0, 7], m[4, 0, 9], m[4, 0, 11] = np.inf, -np.inf, -0.0
+    D = (keep + 15) // 16 * 16 + 16
+    dst = Cache(torch, r, slots, nkv, D, d, g)
+    before = dst.host()
+    dm = torch.full((slots, nkv, D), 3.0, device="cuda")
+    kept, new = evict(torch, c.dev, dst.dev, ids, dids, n, keep, recent, torch.from_numpy(m).cuda(), dm)
+    assert kmr.kmr_last_device_error() == 0
+    got, dm, srch = dst.host(), dm.cpu().numpy(), c.host()
+    for b in range(len(n)):
+        assert new[b] == min(n[b], keep)
+        for h in range(nkv):
+            want = kv4.evict_positions(m[ids[b], h], n[b], keep, recent)
+            assert kept[b, h].tolist() == want + [-1] * (keep - len(want)), (b, h)
+            for a, w0, s in zip(got, before, srch):
+                assert np.array_equal(a[dids[b], h, :len(want)], s[ids[b], h, want])
+                assert np.array_equal(a[dids[b], h, len(want):], w0[dids[b], h, len(want):])
+            assert np.array_equal(dm[dids[b], h, :len(want)], m[ids[b], h, want], equal_nan=True)
+            assert (dm[dids[b], h, len(want):] == 3.0).all()
+
+
+@pytest.mark.parametrize("n", [60000, 131072])
+def test_evict_long_rows(torch, n):
+    r = np.random.default_rng(n)
+    S, nkv, d, g, keep, recent = (n + 15) // 16 * 16, 2, 64, 64, 5000, 100
+    src = kmr.Kv4Cache.zeros(1, nkv, S, d, g)
+    src.tensors[0].random_(0, 256)
+    m = np.exp(3 * r.standard_normal((1, nkv, S))).astype(np.float32)
+    m = (np.round(m * 64) / 64).astype(np.float32)          # many ties
+    dst = kmr.Kv4Cache.zeros(1, nkv, keep + 8, d, g)
+    kept, new = evict(torch, src, dst, [0], [0], [n], keep, recent, torch.from_numpy(m).cuda(), None)
+    assert kmr.kmr_last_device_error() == 0 and new.tolist() == [keep]
+    for h in range(nkv):
+        old = n - recent
+        top = np.lexsort((np.arange(old), -m[0, h, :old]))[:keep - recent]
+        want = np.concatenate([np.sort(top), np.arange(old, n)])
+        assert np.array_equal(kept[0, h], want)
+        assert np.array_equal(dst.tensors[0][0, h, :keep].cpu().numpy(), src.tensors[0][0, h].cpu().numpy()[want])
+
+
+def test_evict_within_one_cache_and_refused_rows(torch):
+    r = np.random.default_rng(31)
+    slots, nkv, S, d, g, keep = 8, 2, 64, 64, 32, 10
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    m = r.random((slots, nkv, S)).astype(np.float32)
+    mass = torch.from_numpy(m.copy()).cuda()
+    # row 0 is good (0 -> 7); 1: onto itself; 2 and 3: one destination; 4: onto row 0's source; 5: slot; 6: length
+    ids, dids, n = [0, 1, 2, 3, 4, 8, 5], [7, 1, 6, 6, 0, 7 - 2, 3 + 0], [40, 20, 20, 20, 20, 20, 65]
+    kept, new = evict(torch, c.dev, c.dev, ids, dids, n, keep, 3, mass, mass)
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    assert new.tolist() == [keep, 0, 0, 0, 0, 0, 0] and (kept[1:] == -1).all()
+    got = c.host()
+    for a, w in zip(got, before):
+        assert np.array_equal(a[:7], w[:7])
+        for h in range(nkv):
+            want = kv4.evict_positions(m[0, h], 40, keep, 3)
+            assert kept[0, h].tolist() == want
+            assert np.array_equal(a[7, h, :keep], w[0, h, want]) and np.array_equal(a[7, h, keep:], w[7, h, keep:])
+    gm = mass.cpu().numpy()
+    assert np.array_equal(gm[:7], m[:7]) and np.array_equal(gm[7, 0, :keep], m[0, 0, kept[0, 0]])
+
+
+# ------------------------------------------------------------------ together
+def test_decode_evict_decode(torch):
+    """As a program uses them: a prompt from a bf16 cache, tokens appended and attended with the mass gathered,
+    the rows cut, and decoding going on in the cut rows; against the oracle's cache, step by step."""
+    r = np.random.default_rng(41)
+    B, nq, nkv, d, g, S, T0, eps, theta = 3, 4, 2, 128, 32, 128, 50, 1e-6, 1e6
+    slots = 2 * B
+    prompt = [kv4.bf16_bits(r.standard_normal((B, nkv, S, d)).astype(np.float32)) for _ in range(2)]
+    lens = np.array([T0, T0 - 13, 1])
+    cache = kmr.Kv4Cache.zeros(slots, nkv, S, d, g)
+    st = torch.cuda.current_stream()
+    ids, zero, rows = np.array([4, 1, 2]), i32(torch, [0] * B), i32(torch, range(B))
+    kmr.kmr_kv4_from_bf16(cache, *[torch.from_numpy(p.view(np.int16)).cuda() for p in prompt], B, S, rows, zero,
+                          i32(torch, ids), zero, i32(torch, lens), B, T0, st)
+    K, V, M = {}, {}, {}
+    for b in range(B):
+        K[b], V[b] = (kv4.dequantize(*kv4.quantize(kv4.bf16_value(p[b, :, :lens[b]]), g)) for p in prompt)
+        M[b] = np.zeros((nkv, lens[b]))
+    mass = torch.zeros((slots, nkv, S), device="cuda")
+    wb = [kv4.bf16_bits(1 + 0.1 * r.standard_normal(d).astype(np.float32)) for _ in range(2)]
+    wdev = [torch.from_numpy(w.view(np.int16)).cuda() for w in wb]
+    n_ws = kmr.kmr_decode_attn_kv4_workspace_size(cache, B, nq, True)
+    ws = torch.empty(n_ws, dtype=torch.uint8, device="cuda")
+    q, out = torch.zeros((B, 1, nq, d), device="cuda"), torch.zeros((B, nq, d), device="cuda")
+    cur, pos0 = lens.copy(), lens + 100
+    dslots = ids.copy()
+    for step in range(24):
+        if step == 16:
+            keep, recent = 30, 8
+            free = np.array([s for s in range(slots) if s not in dslots])[:B]
+            kept, new = evict(torch, cache, cache, dslots, free, cur, keep, recent, mass, mass)
+            mh = mass.cpu().numpy()
+            for b in range(B):
+                total = min(cur[b], keep)
+                assert new[b] == total
+                K2, V2, M2 = [], [], []
+                for h in range(nkv):
+                    # the device's own mass decides: two masses that differ by rounding may rank either way
+                    want = kv4.evict_positions(mh[dslots[b], h], int(cur[b]), keep, recent)
+                    assert kept[b, h, :total].tolist() == want
+                    K2.append(K[b][h, want]), V2.append(V[b][h, want]), M2.append(M[b][h, want])
+                K[b], V[b], M[b] = np.stack(K2), np.stack(V2), np.stack(M2)
+            cur, dslots = new.astype(np.int64), free
+        qkv = r.standard_normal((B, 1, nq + 2 * nkv, d)).astype(np.float32) * 2
+        pos = np.stack([pos0 + step] * 3)[:, :, None].astype(np.int32)
+        sl, cp = i32(torch, dslots), i32(torch, cur)
+        kmr.kmr_kv4_append(cache, torch.from_numpy(qkv).cuda(), torch.from_numpy(pos).cuda(), sl, cp, None, B, 1, nq, *wdev,
+                           eps, theta, SECTIONS[d], q, mass, st)
+        kmr.kmr_decode_attn_kv4(cache, q, sl, cp, B, nq, 1 / math.sqrt(d), mass, out, ws, n_ws, st)
+        assert kmr.kmr_last_device_error() == 0
+        kc, vc, kw, vw = [t.cpu().numpy() for t in cache.tensors]
+        got, mh = out.cpu().numpy(), mass.cpu().numpy()
+        for b in range(B):
+            at, s = int(cur[b]), dslots[b]
+            rope = [kv4.norm_rope(qkv[b, 0, h], kv4.bf16_value(wb[0 if h < nq else 1]), pos[:, b, 0], eps, theta, SECTIONS[d])
+                    for h in range(nq + nkv)]
+            # the new key as the cache holds it (its codes may differ by one from the oracle's at a border)
+            u = kw[s, :, at].view(np.uint32)
+            kd = kv4.dequantize(kv4.unpack_rows(kc[s, :, at], True), (u >> 16).astype(np.uint16), (u & 0xFFFF).astype(np.uint16))
+            assert rel_l2(kd, np.stack(rope[nq:])) <= 0.2
+            vd = kv4.dequantize(*kv4.quantize(qkv[b, 0, nq + nkv:], g))
+            K[b], V[b] = np.concatenate([K[b], kd[:, None]], 1), np.concatenate([V[b], vd[:, None]], 1)
+            ref, m = kv4.attention(np.stack(rope[:nq]), K[b], V[b], 1 / math.sqrt(d))
+            assert rel_l2(got[b], ref) <= 2 * ATTN_TOL, (step, b)
+            M[b] = np.concatenate([M[b], np.zeros((nkv, 1))], 1) + m
+            assert np.allclose(mh[s, :, :at + 1], M[b], rtol=1e-3, atol=1e-6)
+        cur = cur + 1
+
+
+def test_captured_and_replayed_on_another_stream(torch):
+    """append + attention in one graph on a side stream: replays follow the state in place and equal eager calls."""
+    r = np.random.default_rng(51)
+    B, nq, nkv, d, g, S = 2, 16, 8, 128, 32, 256
+    eager, graphed = (Cache(torch, np.random.default_rng(52), B, nkv, S, d, g, [100, 31]).dev for _ in range(2))
+    n_ws = kmr.kmr_decode_attn_kv4_workspace_size(eager, B, nq, True)
+    steps = [r.standard_normal((B, 1, nq + 2 * nkv, d)).astype(np.float32) for _ in range(4)]
+    res = []
+    side = torch.cuda.Stream()
+    for cache, graph in ((eager, False), (graphed, True)):
+        with torch.cuda.stream(side):
+            qkv = torch.zeros((B, 1, (nq + 2 * nkv) * d), device="cuda")
+            pos, cpos = torch.zeros((3, B, 1), dtype=torch.int32, device="cuda"), i32(torch, [100, 31])
+            ids, ws = i32(torch, [0, 1]), torch.empty(n_ws, dtype=torch.uint8, device="cuda")
+            q, out, mass = torch.zeros((B, 1, nq, d), device="cuda"), torch.zeros((B, nq, d), device="cuda"), torch.zeros((B, nkv, S), device="cuda")
+
+            def one():
+                st = torch.cuda.current_stream()
+                kmr.kmr_kv4_append(cache, qkv, pos, ids, cpos, None, B, 1, nq, None, None, 1e-6, 1e6, SECTIONS[d], q, mass, st)
+                kmr.kmr_decode_attn_kv4(cache, q, ids, cpos, B, nq, 1 / math.sqrt(d), mass, out, ws, n_ws, st)
+                cpos.add_(1)
+                pos.add_(1)
+
+            if graph:
+                kmr.kmr_last_device_error()
+                G = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(G, stream=side):
+                    one()
+            got = []
+            for x in steps:
+                qkv.copy_(torch.from_numpy(x.reshape(B, 1, -1)))
+                G.replay() if graph else one()
+                got.append(out.clone())
+            side.synchronize()
+            res.append((torch.stack(got).cpu().numpy(), mass.cpu().numpy(), [t.cpu().numpy() for t in cache.tensors]))
+    assert kmr.kmr_last_device_error() == 0
+    assert np.array_equal(res[0][0], res[1][0]) and np.array_equal(res[0][1], res[1][1])
+    for a, b in zip(res[0][2], res[1][2]):
+        assert np.array_equal(a, b)
+
+
+def test_two_streams_with_their_own_workspaces(torch):
+    r = np.random.default_rng(61)
+    S, nq, nkv, d, g, B = 2048, 16, 8, 128, 32, 4
+    c = Cache(torch, r, B, nkv, S, d, g)
+    q = torch.from_numpy(r.standard_normal((2, B, nq, d)).astype(np.float32)).cuda()
+    ids, cpos = i32(torch, range(B)), i32(torch, [2047, 3, 700, 1500])
+    n = kmr.kmr_decode_attn_kv4_workspace_size(c.dev, B, nq)
+    out = torch.zeros((2, B, nq, d), device="cuda")
+    ref = torch.zeros_like(out)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    for i in range(2):
+        kmr.kmr_decode_attn_kv4(c.dev, q[i], ids, cpos, B, nq, 0.08, None, ref[i], ws[0], n, torch.cuda.current_stream())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(20):
+        for i in range(2):
+            kmr.kmr_decode_attn_kv4(c.dev, q[i], ids, cpos, B, nq, 0.08, None, out[i], ws[i], n, streams[i])
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref)
