@@ -297,7 +297,7 @@ int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf
  * result does not depend on the other rows.
  *   q     device fp32 [B, n_q, d], 16-byte aligned; n_q is 1..8 times n_kv, query head i reads KV head
  *         i / (n_q / n_kv)
- *   mass  device fp32 [slots][n_kv][max_len] or NULL: position p of a row's slot gains the sum of p's
+ *   mass  device fp32 [slots][n_kv][max_len], 16-byte aligned, or NULL: position p of a row's slot gains the sum of p's
  *         softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows that
  *         share a slot add in row order: the result does not change from run to run.
  *   out   device fp32 [B, n_q, d]

@@ -16,7 +16,7 @@ namespace kmr {
 constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at the others for clashes)
 constexpr int kKv4MaxRep = 8;            // query heads per KV head
 constexpr int kKv4MaxSplits = 32;
-constexpr int kKv4MinChunk = 128;        // positions per split, at least
+constexpr int kKv4MinChunk = 64;         // positions per split, at least
 
 struct Kv4View {
     uint8_t* kc;                         // [slots][nkv][S][d / 2]
@@ -143,7 +143,7 @@ struct Kv4EvictParams {
 };
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st);
 
-// Positions of a row are cut into splits of max(128, ceil(L / 32) rounded up to 16): by the row's own
+// Positions of a row are cut into splits of max(64, ceil(L / 32) rounded up to 16): by the row's own
 // length alone, so that a row's result does not depend on the others of the call.
 __host__ __device__ __forceinline__ void kv4_split_plan(int L, int& chunk, int& ns) {
     chunk = (((L + kKv4MaxSplits - 1) / kKv4MaxSplits) + 15) & ~15;

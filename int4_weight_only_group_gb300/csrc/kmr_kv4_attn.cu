@@ -3,8 +3,28 @@
 // out = softmax(q K^T scale) V over positions 0..cache_position of the row's slot, and, where a mass
 // is given, mass[slot][head][p] += the sum over the KV head's query heads of position p's weight.
 // Two launches: the splits of every (row, KV head) leave their softmax states (m, l, o) in base 2 in
-// the workspace (and, for the mass, every score); the second merges the states in split order and
-// turns the scores into weights.  Rows that share a slot add to its mass in row order.
+// the workspace (and, for the mass, every score); the second, a programmatic dependent of the first, merges the
+// states in split order and turns the scores into weights.  Rows that share a slot add to its mass in row order.
+//
+// The bound is HBM: 2 (d/2 + 4 d/g) bytes per position and KV head.  At d = 128, g = 32 an SM's share
+// of the bandwidth is about 36 codes per cycle, too many for dequantising and multiplying on the CUDA
+// cores, so both products run on the tensor cores (mma m16n8k16: at most 8 query heads leave a 128-row
+// tcgen05 tile 15/16 empty) with the codes as the A operand:
+//   * a nibble c under the exponent of 1024 is the fp16 1024 + c (from bits 4..7: 1024 + 16 c); one packed fp16
+//     operation takes the offset off again, exactly.  (As a bare subnormal c 2^-24 it would cost one operation
+//     less, but the tensor core aligns its sums by the operands' exponent fields and a subnormal code then
+//     loses up to 10 of the accumulator's bits: outputs of a 8191-position row were off by 1e-4.)
+//   * the other operand is fp32 split in two fp16 columns (high and low part, about 22 bits), so the result keeps
+//     single precision: columns 2 h and 2 h + 1 belong to query head h and land in one lane's accumulators.
+//   * scores: A = 16 positions x 16 dims, B = the query.  sum_j q_j (c_j s + z) = s sum q c + z sum q per group:
+//     the group's accumulators are folded with its s and z and the query's group sum (fp32).
+//   * output: A = 16 dims x 16 positions (two positions' units joined by a byte permute), B = weight times
+//     the group's s, split in two.  The codes are taken as c - 8 at half of the positions and c - 7 at the
+//     others (their mean is 7.5; fp16 has no 1031.5 to subtract), the base as z + 8 s or z + 7 s: a long
+//     row's output is small against the codes' offset, and the sum of the offset codes would lose its bits (at
+//     131072 positions an error of 5e-6 with c - 8 throughout).  The bases add per group in fp32.  The products are scaled by a power of two that follows the
+//     largest s seen, so that any bf16 scale fits fp16.
+#include <cuda_fp16.h>
 #include <math.h>
 
 #include "kmr_kv4.cuh"
@@ -13,7 +33,10 @@ namespace kmr {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kThr = 256, kWarps = 8;
+constexpr int kThr = 128, kWarps = 4;
+constexpr int kStagePos = 16 * kWarps;       // positions of a ring stage: a tile of 16 per warp
+constexpr int kStages = 4;
+constexpr int kMergeThr = 256;
 
 __device__ __forceinline__ int kv4_row_error(const Kv4AttnParams& p, int b) {
     const int slot = p.slot_ids[b], cp = p.cpos[b];
@@ -21,138 +44,562 @@ __device__ __forceinline__ int kv4_row_error(const Kv4AttnParams& p, int b) {
     return (cp < 0 || cp >= p.c.S) ? KMR_ERR_CACHE_FULL : KMR_OK;
 }
 
-template <int D>
-__global__ void __launch_bounds__(kThr) kv4_split_kernel(const Kv4AttnParams p) {
-    constexpr int NB = D / 32, LPR = D / 4, SUBS = 32 / LPR;
-    __shared__ float wm[kWarps * 2][kKv4MaxRep], wl[kWarps * 2][kKv4MaxRep];
-    __shared__ float wo[kWarps * SUBS][D];
-    const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
-    if (kv4_row_error(p, b) != KMR_OK) return;
-    const int L = p.cpos[b] + 1, rep = p.nq / p.c.nkv;
-    int chunk, ns;
-    kv4_split_plan(L, chunk, ns);
-    if (s >= ns) return;
-    const int t0 = s * chunk, t1 = min(L, t0 + chunk);
-    const int tid = threadIdx.x, warp = tid >> 5, wl32 = tid & 31, lane = wl32 % LPR, sub = warp * SUBS + wl32 / LPR;
-    const size_t row = (size_t(p.slot_ids[b]) * p.c.nkv + h) * p.c.S;
-    const int ng = D / p.c.g, gi = lane * 4 / p.c.g;
-    const float qs = p.scale * kLog2e;
-    for (int r = 0; r < rep; ++r) {
-        const float4 qv = *reinterpret_cast<const float4*>(p.q + (size_t(b) * p.nq + h * rep + r) * D + lane * 4);
-        float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-        float* sc = p.scores ? p.scores + ((size_t(b) * p.c.nkv + h) * rep + r) * p.c.S : nullptr;
-        for (int i0 = t0; i0 < t1; i0 += kWarps * SUBS) {
-            const int i = i0 + sub;
-            const size_t at = row + (i < t1 ? i : t0);
-            const uint32_t kc = reinterpret_cast<const uint16_t*>(p.c.kc + at * (D / 2))[kv4_unit(lane, NB, true)];
-            const uint32_t vc = reinterpret_cast<const uint16_t*>(p.c.vc + at * (D / 2))[kv4_unit(lane, NB, false)];
-            const uint32_t kw = p.c.ks[at * ng + gi], vw = p.c.vs[at * ng + gi];
-            const float s4 = kv4_s(kw), z4 = kv4_z(kw);
-            float a = qv.x * fmaf(float(kc & 15), s4, z4) + qv.y * fmaf(float((kc >> 4) & 15), s4, z4) +
-                      qv.z * fmaf(float((kc >> 8) & 15), s4, z4) + qv.w * fmaf(float(kc >> 12), s4, z4);
-            for (int off = 1; off < LPR; off <<= 1) a += __shfl_xor_sync(0xffffffffu, a, off);
-            if (i >= t1) continue;
-            a *= qs;
-            if (sc && lane == 0) sc[i] = a;
-            const float mn = fmaxf(m, a), cf = m == -INFINITY ? 0.f : exp2f(m - mn), w = exp2f(a - mn);
-            const float vs = kv4_s(vw), vz = kv4_z(vw);
-            m = mn;
-            l = l * cf + w;
-            for (int e = 0; e < 4; ++e) o[e] = o[e] * cf + w * fmaf(float((vc >> (4 * e)) & 15), vs, vz);
-        }
-        __syncthreads();
-        if (lane == 0) {
-            wm[sub][r] = m;
-            wl[sub][r] = l;
-        }
-        for (int e = 0; e < 4; ++e) wo[sub][lane * 4 + e] = o[e];
-        __syncthreads();
-        float* part = p.part + (((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep + r) * (D + 2);
-        for (int i = tid; i < D; i += kThr) {
-            float mx = -INFINITY, num = 0.f, den = 0.f;
-            for (int w = 0; w < kWarps * SUBS; ++w) mx = fmaxf(mx, wm[w][r]);
-            for (int w = 0; w < kWarps * SUBS; ++w) {
-                const float f = wm[w][r] == -INFINITY ? 0.f : exp2f(wm[w][r] - mx);
-                den += f * wl[w][r];
-                num += f * wo[w][i];
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// fp16 pair (low half a, high half b), rounded towards zero.
+__device__ __forceinline__ uint32_t pack_f16_rz(float a, float b) {
+    uint32_t r;
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(b), "f"(a));
+    return r;
+}
+// The high part of x (mask 0: x itself, which the cut to fp16 shortens to its leading 11 significant bits) or its
+// low part (mask 0xFFFFE000: what that cut leaves).
+__device__ __forceinline__ float part_of(float x, uint32_t mask) {
+    return __fsub_rn(x, __uint_as_float(__float_as_uint(x) & mask));
+}
+// The four codes of each half of a word as fp16 pairs c - OFF: nibbles (0, 4), (1, 5), (2, 6), (3, 7).
+template <int OFF>
+__device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&c)[4]) {
+    const __half2 low = __float2half2_rn(-1024.f - OFF), high = __float2half2_rn(-64.f - OFF);
+    const __half2 sixteenth = __float2half2_rn(0.0625f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        uint32_t a = and_or(w, 0x000F000Fu, 0x64006400u), b = and_or(w, 0x00F000F0u, 0x64006400u);
+        const __half2 x = __hadd2(*reinterpret_cast<__half2*>(&a), low);
+        const __half2 y = __hfma2(*reinterpret_cast<__half2*>(&b), sixteenth, high);
+        c[2 * i] = *reinterpret_cast<const uint32_t*>(&x);
+        c[2 * i + 1] = *reinterpret_cast<const uint32_t*>(&y);
+        w >>= 8;
+    }
+}
+template <int N>
+__device__ __forceinline__ void lds_words(const void* p, uint32_t (&w)[N]) {
+    if constexpr (N == 4) {
+        const uint4 u = *static_cast<const uint4*>(p);
+        w[0] = u.x; w[1] = u.y; w[2] = u.z; w[3] = u.w;
+    } else if constexpr (N == 2) {
+        const uint2 u = *static_cast<const uint2*>(p);
+        w[0] = u.x; w[1] = u.y;
+    } else {
+        w[0] = *static_cast<const uint32_t*>(p);
+    }
+}
+
+template <int D, int G>
+struct SplitSmem {
+    static constexpr int kCodes = kStagePos * D / 2, kWords = kStagePos * (D / G) * 4;
+    static constexpr int kStage = 2 * kCodes + 2 * kWords;
+    static constexpr int kRing = kStages * kStage;
+    static constexpr int merge(int rep) { return kWarps * rep * (D + 2) * 4; }
+    static constexpr int kQuery = 4 * (D / 32) + D / G + 1;         // words of a lane's query per n-tile
+    static constexpr int query(int rep) { return (rep <= 4 ? 1 : 2) * kQuery * 128; }
+    static constexpr int total(int rep) { return 128 + query(rep) + (kRing > merge(rep) ? kRing : merge(rep)); }
+};
+
+// Query fragments of the scores' B operand, the queries' group sums and the scores' factor (all of the KV head's
+// query heads; heads past rep are zero).
+template <int D, int G, int NT>
+__device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int lane,
+                                                uint32_t (&qf)[NT][D / 32][4], float (&qsum)[NT][D / G],
+                                                float (&fac)[NT]) {
+    constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int hq = 4 * n + (g >> 1);
+        float x[NB][8], mx = 0.f;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
+            if (hq < rep) {
+                const float4* src =
+                    reinterpret_cast<const float4*>(p.q + (size_t(b) * p.nq + h * rep + hq) * D + 32 * k + 8 * t);
+                u = src[0];
+                v = src[1];
             }
-            part[2 + i] = num;
-            if (i == 0) {
-                part[0] = mx;
-                part[1] = den;
+            x[k][0] = u.x; x[k][1] = u.y; x[k][2] = u.z; x[k][3] = u.w;
+            x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[k][e]));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        // largest |q| sigma in [2^13, 2^14): sigma = 2^(13 - e), held within the normal range
+        int e = int(__float_as_uint(mx) >> 23) - 127;
+        e = max(e, -113);
+        const float sig = __uint_as_float(uint32_t(13 - e + 127) << 23);
+        float gs[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) gs[i] = 0.f;
+        const uint32_t mask = (g & 1) ? 0xFFFFE000u : 0u;
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            float y[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                gs[k / BPG] += x[k][i];
+                y[i] = part_of(x[k][i] * sig, mask);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[n][k][i] = pack_f16_rz(y[i], y[i + 4]);
+        }
+        const float base2 = p.scale * kLog2e;
+        const float f = base2 * 0x1p-13f * exp2f(float(e));               // base2 / sigma
+        fac[n] = __shfl_sync(0xffffffffu, f, 8 * t);
+#pragma unroll
+        for (int i = 0; i < NG; ++i) {
+            float v = gs[i];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            qsum[n][i] = __shfl_sync(0xffffffffu, v * base2, 8 * t);
         }
     }
 }
 
-__global__ void __launch_bounds__(kThr) kv4_merge_kernel(const Kv4AttnParams p) {
+// NT: n-tiles of 4 query heads.
+template <int D, int G, int NT>
+__global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const Kv4AttnParams p) {
+    using M = SplitSmem<D, G>;
+    constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);              // [kStages]
+    uint64_t* empty = full + kStages;                                // [kStages]
+    uint8_t* ring = smem + 128 + NT * M::kQuery * 128;
+    const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    pdl_launch_dependents();
+    if (kv4_row_error(p, b) != KMR_OK) return;
+    const int rep = p.nq / p.c.nkv;
+    const int L = p.cpos[b] + 1;
+    int chunk, ns;
+    kv4_split_plan(L, chunk, ns);
+    if (s >= ns) return;
+    const int t0 = s * chunk, t1 = min(L, t0 + chunk);
+    const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
+    const size_t row = (size_t(p.slot_ids[b]) * p.c.nkv + h) * p.c.S;
+
+    if (tid == 0) {
+        for (int i = 0; i < kStages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], kWarps);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
+    // One stage: lanes 0..3 of the calling warp copy K codes, V codes, K words and V words of up to 128
+    // positions (rounded up to 16: within the row, whose length is a multiple of 16).
+    auto issue = [&](int st) {
+        uint8_t* buf = ring + (st % kStages) * M::kStage;
+        const int pa = t0 + st * kStagePos;
+        const uint32_t np = uint32_t(min(kStagePos, ((t1 - pa) + 15) & ~15));
+        if (lane == 0) mbar_arrive_expect_tx(&full[st % kStages], np * (D + 8 * NG));
+        __syncwarp();
+        if (lane < 4) {
+            const bool words = lane >= 2, key = !(lane & 1);
+            const void* src = words ? static_cast<const void*>((key ? p.c.ks : p.c.vs) + (row + pa) * NG)
+                                    : static_cast<const void*>((key ? p.c.kc : p.c.vc) + (row + pa) * (D / 2));
+            uint8_t* dst = buf + (words ? 2 * M::kCodes + (key ? 0 : M::kWords) : (key ? 0 : M::kCodes));
+            bulk_g2s(dst, src, np * (words ? 4 * NG : D / 2), &full[st % kStages]);
+        }
+        __syncwarp();
+    };
+    if (warp == 0)
+        for (int i = 0; i < nst && i < kStages; ++i) issue(i);
+
+    // ---- the query, prepared by warp 1 for all: column g of n-tile n is head 4 n + g / 2, its high part (g even)
+    // or low part.  fac and qsum belong to head 4 n + t.
+    uint32_t qf[NT][NB][4];
+    float qsum[NT][NG], fac[NT];
+    uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
+    if (warp == 1) {
+        query_fragments<D, G, NT>(p, b, h, rep, lane, qf, qsum, fac);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            uint32_t* at = qsh + n * M::kQuery * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < NB; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) at[(4 * k + i) * 32] = qf[n][k][i];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) at[(4 * NB + i) * 32] = __float_as_uint(qsum[n][i]);
+            at[(4 * NB + NG) * 32] = __float_as_uint(fac[n]);
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const uint32_t* at = qsh + n * M::kQuery * 32 + lane;
+#pragma unroll
+        for (int k = 0; k < NB; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[n][k][i] = at[(4 * k + i) * 32];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) qsum[n][i] = __uint_as_float(at[(4 * NB + i) * 32]);
+        fac[n] = __uint_as_float(at[(4 * NB + NG) * 32]);
+    }
+
+    float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][NG];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n] = -INFINITY;
+        l[n] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+#pragma unroll
+        for (int i = 0; i < NG; ++i) zo[n][i] = 0.f;
+    }
+    int eref = 13;                                // exponent that the output accumulators are scaled by
+    const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
+    float* sc_out = p.scores ? p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S : nullptr;
+
+    for (int st = 0; st < nst; ++st) {
+        const uint8_t* buf = ring + (st % kStages) * M::kStage;
+        mbar_wait(&full[st % kStages], uint32_t((st / kStages) & 1), p.err);
+        const int base = t0 + st * kStagePos + warp * 16;          // the tile's first position
+        if (base < t1) {
+            const bool whole = base + 16 <= t1;
+            const int i0 = warp * 16;
+            // ---- scores of positions g and g + 8 for head 4 n + t
+            uint32_t k0[NB], k1[NB], w0[NG], w1[NG];
+            lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
+            lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
+            lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG), w0);
+            lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG), w1);
+            float sc[NT][2], zc[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = zc[n][0] = zc[n][1] = 0.f;
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                float acc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+                for (int kb = 0; kb < BPG; ++kb) {
+                    const int k = gr * BPG + kb;
+                    uint32_t x[4], y[4];
+                    unpack_codes<0>(k0[k], x);
+                    unpack_codes<0>(k1[k], y);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
+                        mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    sc[n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[n][0]);
+                    sc[n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[n][1]);
+                    zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
+                    zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
+                }
+            }
+            // ---- V words of positions t, t + 4, t + 8, t + 12, and the largest scale among the tile's
+            uint32_t vw[4][NG], top = 0u;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lds_words(buf + 2 * M::kCodes + M::kWords + (i0 + t + 4 * i) * (4 * NG), vw[i]);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
+                    if (!whole && base + t + 4 * i >= t1) vw[i][gr] = 0u;
+                    top = max(top, vw[i][gr] & 0x7FFFFFFFu);
+                }
+            }
+            int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
+            // ---- running maximum; the states are rescaled only where a maximum or the scale's exponent moved
+            float mn[NT];
+            bool up = etop > eref;
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                sc[n][0] = __fmaf_rn(sc[n][0], fac[n], zc[n][0]);
+                sc[n][1] = __fmaf_rn(sc[n][1], fac[n], zc[n][1]);
+                if (!whole) {
+                    if (base + g >= t1) sc[n][0] = -INFINITY;
+                    if (base + g + 8 >= t1) sc[n][1] = -INFINITY;
+                }
+                if (sc_out && 4 * n + t < rep) {
+                    float* dst = sc_out + size_t(4 * n + t) * p.c.S + base + g;
+                    if (whole || base + g < t1) dst[0] = sc[n][0];
+                    if (whole || base + g + 8 < t1) dst[8] = sc[n][1];
+                }
+                float c = fmaxf(sc[n][0], sc[n][1]);
+                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
+                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
+                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
+                mn[n] = fmaxf(m[n], c);
+                up |= mn[n] > m[n];
+            }
+            if (__any_sync(0xffffffffu, up)) {
+                // room of two octaves, so that scales a little larger do not rescale again
+                const int en = etop > eref ? min(etop + 2, 254) : eref;
+                const float es = exp2f(float(eref - en));
+                eref = en;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float cf = m[n] == -INFINITY ? 0.f : exp2f(__fsub_rn(m[n], mn[n]));
+                    m[n] = mn[n];
+                    l[n] *= cf;
+                    const float ce = cf * es;
+#pragma unroll
+                    for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
+                    const float cg = __shfl_sync(0xffffffffu, cf, (lane & 28) | (g >> 1));
+#pragma unroll
+                    for (int i = 0; i < NG; ++i) zo[n][i] *= cg;
+                }
+            }
+            // ---- weights of head 4 n + g / 2 at the lane's four positions, and what the bases add
+            float mid[4][NG];
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    mid[i][gr] = __fmaf_rn(i < 2 ? 8.f : 7.f, kv4_s(vw[i][gr]), kv4_z(vw[i][gr]));
+            const float unit = __uint_as_float(uint32_t(267 - eref) << 23);      // 2^(13 - (eref - 127))
+            float w[NT][4];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const float mm = m[n] == -INFINITY ? 0.f : m[n];
+                const float p0 = exp2f(__fsub_rn(sc[n][0], mm)), p1 = exp2f(__fsub_rn(sc[n][1], mm));
+                l[n] += p0 + p1;
+                const int src = 4 * t + (g >> 1);
+                w[n][0] = __shfl_sync(0xffffffffu, p0, src);
+                w[n][1] = __shfl_sync(0xffffffffu, p0, src + 16);
+                w[n][2] = __shfl_sync(0xffffffffu, p1, src);
+                w[n][3] = __shfl_sync(0xffffffffu, p1, src + 16);
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) zo[n][gr] = __fmaf_rn(w[n][i], mid[i][gr], zo[n][gr]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[n][i] *= unit;
+            }
+            // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3)
+            uint32_t vc[4][NB / 2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
+#pragma unroll
+            for (int gr = 0; gr < NG; ++gr) {
+                uint32_t wf[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float a[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
+                    wf[n][0] = pack_f16_rz(a[0], a[1]);
+                    wf[n][1] = pack_f16_rz(a[2], a[3]);
+                }
+#pragma unroll
+                for (int kb = 0; kb < BPG; ++kb) {
+                    const int k = gr * BPG + kb;
+                    const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                    uint32_t x[4], y[4];
+                    unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
+                    unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
+                        mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                    }
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st % kStages]);
+        // refill the stage before this one (released by most warps a tile ago); the warps take turns
+        const int nx = st - 1 + kStages;
+        if (st > 0 && nx < nst && warp == (st & (kWarps - 1))) {
+            mbar_wait(&empty[(st - 1) % kStages], uint32_t(((st - 1) / kStages) & 1), p.err);
+            fence_proxy_async_smem();
+            issue(nx);
+        }
+    }
+    __syncthreads();                              // every copy has landed and been read: the ring is free
+
+    // ---- the warp's state: o[head][dim], m, l
+    float* wo = reinterpret_cast<float*>(ring);                       // [warp][rep][D]
+    float* wml = wo + kWarps * rep * D;                               // [warp][rep][2]
+    const float un = exp2f(float(eref - 127)) * 0x1p-13f;             // the products' scale, undone
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int hq = 4 * n + t;
+        float lt = l[n];
+        lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+        lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+        float zt[NG];
+#pragma unroll
+        for (int gr = 0; gr < NG; ++gr) {
+            float v = zo[n][gr];
+            v += __shfl_xor_sync(0xffffffffu, v, 1);
+            v += __shfl_xor_sync(0xffffffffu, v, 2);
+            zt[gr] = __shfl_sync(0xffffffffu, v, 8 * t);
+        }
+        if (hq < rep) {
+            if (g == 0) {
+                wml[(warp * rep + hq) * 2] = m[n];
+                wml[(warp * rep + hq) * 2 + 1] = lt;
+            }
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const float z = zt[k / BPG];
+                const float(&a)[4] = o[n][2 * k];
+                const float(&c)[4] = o[n][2 * k + 1];
+                const float4 v = make_float4(__fmaf_rn(a[0] + a[1], un, z), __fmaf_rn(a[2] + a[3], un, z),
+                                             __fmaf_rn(c[0] + c[1], un, z), __fmaf_rn(c[2] + c[3], un, z));
+                *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * k + 4 * g) = v;
+            }
+        }
+    }
+    __syncthreads();
+    float* part = p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
+    for (int i = tid; i < rep * D; i += kThr) {
+        const int hq = i / D, dim = i % D;
+        float mx = -INFINITY, num = 0.f, den = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wml[(w * rep + hq) * 2]);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float mw = wml[(w * rep + hq) * 2];
+            const float f = mw == -INFINITY ? 0.f : exp2f(__fsub_rn(mw, mx));
+            den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
+            num = __fmaf_rn(f, wo[(w * rep + hq) * D + dim], num);
+        }
+        part[hq * (D + 2) + 2 + dim] = num;
+        if (dim == 0) {
+            part[hq * (D + 2)] = mx;
+            part[hq * (D + 2) + 1] = den;
+        }
+    }
+}
+
+// Merge of a (row, KV head)'s split states, and the mass of kMassPos positions per further block.
+constexpr int kMassPos = kMergeThr * 4;
+
+__global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParams p) {
+    __shared__ float sm[kKv4MaxSplits * kKv4MaxRep], sl[kKv4MaxSplits * kKv4MaxRep];
+    __shared__ float hm[kKv4MaxRep], hl[kKv4MaxRep];
     const int h = blockIdx.y, b = blockIdx.z, d = p.c.d, rep = p.nq / p.c.nkv, tid = threadIdx.x;
     const int err = kv4_row_error(p, b);
-    float* out = p.out + (size_t(b) * p.nq + h * rep) * d;
-    if (err != KMR_OK) {
-        if (blockIdx.x == 0) {
+    const bool merge = blockIdx.x == 0;
+    const int pos = (int(blockIdx.x) - 1) * kMassPos + tid * 4;       // this thread's four positions
+    if (!merge && (err != KMR_OK || (int(blockIdx.x) - 1) * kMassPos > p.c.S)) return;
+    // split states of row r to shared memory, and each head's maximum and 1 / sum
+    auto states = [&](int r, int ns) {
+        const float* part = p.part + (size_t(r) * p.c.nkv + h) * p.nsplit * rep * (d + 2);
+        __syncthreads();
+        for (int i = tid; i < ns * rep; i += kMergeThr) {
+            sm[i] = part[size_t(i) * (d + 2)];
+            sl[i] = part[size_t(i) * (d + 2) + 1];
+        }
+        __syncthreads();
+        if (tid < rep) {
+            float mx = -INFINITY, den = 0.f;
+            for (int s = 0; s < ns; ++s) mx = fmaxf(mx, sm[s * rep + tid]);
+            for (int s = 0; s < ns; ++s) {
+                const float ms = sm[s * rep + tid];
+                const float f = ms == -INFINITY ? 0.f : exp2f(__fsub_rn(ms, mx));
+                den = __fmaf_rn(f, sl[s * rep + tid], den);
+                sm[s * rep + tid] = f;
+            }
+            hm[tid] = mx;
+            hl[tid] = __frcp_rn(den);
+        }
+        __syncthreads();
+    };
+    int chunk, ns;
+    if (merge) {
+        float* out = p.out + (size_t(b) * p.nq + h * rep) * d;
+        pdl_wait();
+        if (err != KMR_OK) {
             if (tid == 0 && h == 0) set_error(p.err, err);
-            for (int i = tid; i < rep * d; i += kThr) out[i] = 0.f;
+            for (int i = tid; i < rep * d; i += kMergeThr) out[i] = 0.f;
+            return;
+        }
+        kv4_split_plan(p.cpos[b] + 1, chunk, ns);
+        states(b, ns);
+        const float* part = p.part + (size_t(b) * p.c.nkv + h) * p.nsplit * rep * (d + 2);
+        for (int i = tid; i < rep * d; i += kMergeThr) {
+            const int hq = i / d;
+            const float* mine = part + size_t(hq) * (d + 2) + 2 + i % d;
+            float num = 0.f;
+#pragma unroll 8
+            for (int s = 0; s < ns; ++s) num = __fmaf_rn(sm[s * rep + hq], mine[size_t(s) * rep * (d + 2)], num);
+            out[i] = num * hl[hq];
         }
         return;
     }
-    int chunk, ns;
-    if (blockIdx.x == 0) {
-        kv4_split_plan(p.cpos[b] + 1, chunk, ns);
-        const float* part = p.part + (size_t(b) * p.c.nkv + h) * p.nsplit * rep * (d + 2);
-        for (int i = tid; i < rep * d; i += kThr) {
-            const float* mine = part + size_t(i / d) * (d + 2);
-            float mx = -INFINITY, num = 0.f, den = 0.f;
-            for (int s = 0; s < ns; ++s) mx = fmaxf(mx, mine[size_t(s) * rep * (d + 2)]);
-            for (int s = 0; s < ns; ++s) {
-                const float* q = mine + size_t(s) * rep * (d + 2);
-                const float f = q[0] == -INFINITY ? 0.f : exp2f(q[0] - mx);
-                den += f * q[1];
-                num += f * q[2 + i % d];
-            }
-            out[i] = num / den;
-        }
-    }
-    if (!p.mass) return;
     const int slot = p.slot_ids[b];
-    int before = 0;
-    for (int r = tid; r < b; r += kThr) before |= p.slot_ids[r] == slot && kv4_row_error(p, r) == KMR_OK;
-    if (__syncthreads_or(before)) return;            // the slot's first row adds for all of them
-    __shared__ float sm[kKv4MaxRep], sl[kKv4MaxRep];
-    const int i = blockIdx.x * kThr + tid;
-    float add = 0.f;
-    int most = 0;
+    int before = 0, most = 0;
+    for (int r = tid; r < p.B; r += kMergeThr) {
+        if (p.slot_ids[r] != slot || kv4_row_error(p, r) != KMR_OK) continue;
+        before |= r < b;
+        most |= p.cpos[r] >= (int(blockIdx.x) - 1) * kMassPos;
+    }
+    // the slot's first row adds for all of them; nothing to add past the longest
+    before = __syncthreads_or(before);
+    most = __syncthreads_or(most);
+    if (before || !most) return;
+    pdl_wait();
+    float add[4] = {0.f, 0.f, 0.f, 0.f};
+    int last = 0;
     for (int r = b; r < p.B; ++r) {
         if (p.slot_ids[r] != slot || kv4_row_error(p, r) != KMR_OK) continue;
         const int L = p.cpos[r] + 1;
-        most = max(most, L);
+        last = max(last, L);
         kv4_split_plan(L, chunk, ns);
-        __syncthreads();
-        if (tid < rep) {
-            const float* q = p.part + ((size_t(r) * p.c.nkv + h) * p.nsplit * rep + tid) * (d + 2);
-            float mx = -INFINITY, den = 0.f;
-            for (int s = 0; s < ns; ++s) mx = fmaxf(mx, q[size_t(s) * rep * (d + 2)]);
-            for (int s = 0; s < ns; ++s) {
-                const float m = q[size_t(s) * rep * (d + 2)];
-                den += m == -INFINITY ? 0.f : exp2f(m - mx) * q[size_t(s) * rep * (d + 2) + 1];
+        states(r, ns);
+        const float* sc = p.scores + (size_t(r) * p.c.nkv + h) * rep * p.c.S + pos;
+        if (pos < L) {
+            for (int k = 0; k < rep; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(sc + size_t(k) * p.c.S);
+                const float x[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (pos + e < L) add[e] = __fmaf_rn(exp2f(__fsub_rn(x[e], hm[k])), hl[k], add[e]);
             }
-            sm[tid] = mx;
-            sl[tid] = 1.f / den;
-        }
-        __syncthreads();
-        if (i < L) {
-            const float* sc = p.scores + (size_t(r) * p.c.nkv + h) * rep * p.c.S + i;
-            for (int k = 0; k < rep; ++k) add += exp2f(sc[size_t(k) * p.c.S] - sm[k]) * sl[k];
         }
     }
-    if (i < most) p.mass[(size_t(slot) * p.c.nkv + h) * p.c.S + i] += add;
+    float* mass = p.mass + (size_t(slot) * p.c.nkv + h) * p.c.S + pos;
+    if (pos + 4 <= last) {
+        float4 v = *reinterpret_cast<float4*>(mass);
+        v.x += add[0]; v.y += add[1]; v.z += add[2]; v.w += add[3];
+        *reinterpret_cast<float4*>(mass) = v;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (pos + e < last) mass[e] += add[e];
+    }
+}
+
+template <int D, int G>
+const void* split_fn(int rep) {
+    return rep <= 4 ? (const void*)kv4_split_kernel<D, G, 1> : (const void*)kv4_split_kernel<D, G, 2>;
+}
+struct SplitVariant {
+    const void* fn;
+    int smem;
+};
+SplitVariant split_variant(int d, int g, int rep) {
+    if (d == 64) {
+        if (g == 32) return {split_fn<64, 32>(rep), SplitSmem<64, 32>::total(rep)};
+        return {split_fn<64, 64>(rep), SplitSmem<64, 64>::total(rep)};
+    }
+    if (g == 32) return {split_fn<128, 32>(rep), SplitSmem<128, 32>::total(rep)};
+    if (g == 64) return {split_fn<128, 64>(rep), SplitSmem<128, 64>::total(rep)};
+    return {split_fn<128, 128>(rep), SplitSmem<128, 128>::total(rep)};
 }
 
 }  // namespace
 
 int kv4_attn_splits(int S) {
-    int chunk, ns;
-    kv4_split_plan(S, chunk, ns);
     // a shorter row can have more splits than the longest (the chunk is rounded up), never more than 32
     const int most = (S + kKv4MinChunk - 1) / kKv4MinChunk;
     return most < kKv4MaxSplits ? most : kKv4MaxSplits;
@@ -160,18 +607,39 @@ int kv4_attn_splits(int S) {
 size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit) {
     return (size_t(B) * nq * nsplit * (d + 2) * 4 + 15) & ~size_t(15);
 }
-cudaError_t kv4_attn_set_attributes() { return cudaSuccess; }
+cudaError_t kv4_attn_set_attributes() {
+    const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
+    for (const auto& sh : shapes)
+        for (int rep : {4, 8}) {
+            const SplitVariant v = split_variant(sh[0], sh[1], rep);
+            cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+            if (e != cudaSuccess) return e;
+            e = cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+            if (e != cudaSuccess) return e;
+        }
+    return cudaSuccess;
+}
 
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
-    const dim3 grid(p.nsplit, p.c.nkv, p.B);
-    if (p.c.d == 64)
-        kv4_split_kernel<64><<<grid, kThr, 0, st>>>(p);
-    else
-        kv4_split_kernel<128><<<grid, kThr, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    const SplitVariant v = split_variant(p.c.d, p.c.g, p.nq / p.c.nkv);
+    Kv4AttnParams q = p;
+    void* args[] = {&q};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.nsplit, p.c.nkv, p.B);
+    cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = v.smem;
+    cfg.stream = st;
+    cudaError_t e = cudaLaunchKernelExC(&cfg, v.fn, args);
     if (e != cudaSuccess) return e;
-    kv4_merge_kernel<<<dim3(p.mass ? (p.c.S + kThr - 1) / kThr : 1, p.c.nkv, p.B), kThr, 0, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(p.mass ? 1 + (p.c.S + kMassPos - 1) / kMassPos : 1, p.c.nkv, p.B);
+    cfg.blockDim = dim3(kMergeThr);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, (const void*)kv4_merge_kernel, args);
 }
 
 }  // namespace kmr

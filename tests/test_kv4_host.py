@@ -78,7 +78,7 @@ def test_bad_caches(L, name):
     ("kmr_kv4_to_bf16", dict(k=None), -1), ("kmr_kv4_to_bf16", dict(start=None), -1),
     ("kmr_kv4_to_bf16", dict(B=1025), -9), ("kmr_kv4_to_bf16", dict(T=-1), -1),
     ("kmr_decode_attn_kv4", dict(q=None), -1), ("kmr_decode_attn_kv4", dict(out=None), -1),
-    ("kmr_decode_attn_kv4", dict(ws=None), -1), ("kmr_decode_attn_kv4", dict(q=8), -1),
+    ("kmr_decode_attn_kv4", dict(ws=None), -1), ("kmr_decode_attn_kv4", dict(q=8), -1), ("kmr_decode_attn_kv4", dict(mass=4), -1),
     ("kmr_decode_attn_kv4", dict(scale=float("nan")), -1), ("kmr_decode_attn_kv4", dict(scale=float("inf")), -1),
     ("kmr_decode_attn_kv4", dict(B=0), -9), ("kmr_decode_attn_kv4", dict(nq=20), -2),
     ("kmr_decode_attn_kv4", dict(nq=72), -2), ("kmr_decode_attn_kv4", dict(n=16), -8),
