@@ -300,7 +300,7 @@ int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf
  *   mass  device fp32 [slots][n_kv][max_len], 16-byte aligned, or NULL: position p of a row's slot gains the sum of p's
  *         softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows that
  *         share a slot add in row order: the result does not change from run to run.
- *   out   device fp32 [B, n_q, d]
+ *   out   device fp32 [B, n_q, d], 16-byte aligned
  *   workspace  device memory, 16-byte aligned, kmr_decode_attn_kv4_workspace_size(cache, B, n_q, mass != NULL)
  *         bytes or more (0 for arguments that the call would refuse); no initialisation.  Calls that may
  *         overlap on the device need workspaces of their own.

@@ -15,7 +15,7 @@ namespace kmr {
 
 constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at the others for clashes)
 constexpr int kKv4MaxRep = 8;            // query heads per KV head
-constexpr int kKv4MaxSplits = 32;
+constexpr int kKv4MaxSplits = 76;        // of a row: with 8 KV heads, four CTAs for each of 152 SMs
 constexpr int kKv4MinChunk = 64;         // positions per split, at least
 
 struct Kv4View {
@@ -143,11 +143,15 @@ struct Kv4EvictParams {
 };
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st);
 
-// Positions of a row are cut into splits of max(64, ceil(L / 32) rounded up to 16): by the row's own
-// length alone, so that a row's result does not depend on the others of the call.
+// Positions of a row are cut into splits of `chunk` positions (a multiple of 16), by the row's own length
+// alone, so that a row's result does not depend on the others of the call: 64 for short rows (a tile of 16 for
+// each of a CTA's warps), growing to 256 by 4096 positions, and beyond 76 splits with the length.
 __host__ __device__ __forceinline__ void kv4_split_plan(int L, int& chunk, int& ns) {
-    chunk = (((L + kKv4MaxSplits - 1) / kKv4MaxSplits) + 15) & ~15;
+    const int grow = (L + 15) >> 4;
+    chunk = (L + kKv4MaxSplits - 1) / kKv4MaxSplits;
     if (chunk < kKv4MinChunk) chunk = kKv4MinChunk;
+    if (grow > chunk) chunk = grow < 256 ? grow : (chunk < 256 ? 256 : chunk);
+    chunk = (chunk + 15) & ~15;
     ns = (L + chunk - 1) / chunk;
 }
 

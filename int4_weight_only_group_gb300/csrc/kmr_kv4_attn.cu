@@ -77,6 +77,11 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&c)[4]) {
         w >>= 8;
     }
 }
+__device__ __forceinline__ float exp2_approx(float x) {               // 2 ulp; 0 below 2^-126
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
 template <int N>
 __device__ __forceinline__ void lds_words(const void* p, uint32_t (&w)[N]) {
     if constexpr (N == 4) {
@@ -253,7 +258,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
         for (int i = 0; i < NG; ++i) zo[n][i] = 0.f;
     }
-    int eref = 13;                                // exponent that the output accumulators are scaled by
+    int eref = 5;                                 // exponent that the output accumulators are scaled by
     const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
     float* sc_out = p.scores ? p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S : nullptr;
 
@@ -298,20 +303,36 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                     zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
                 }
             }
-            // ---- V words of positions t, t + 4, t + 8, t + 12, and the largest scale among the tile's
-            uint32_t vw[4][NG], top = 0u;
+            // ---- V words: of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights), and the
+            // largest scale of the tile
+            const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
+            uint32_t v0[NG], v1[NG], vw[4][NG], mine[(NG + 1) / 2];
+            lds_words(words + g * (4 * NG), v0);
+            lds_words(words + (g + 8) * (4 * NG), v1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                lds_words(buf + 2 * M::kCodes + M::kWords + (i0 + t + 4 * i) * (4 * NG), vw[i]);
+            for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG), vw[i]);
+            const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
+            lds_words(words + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
+            if (!whole) {
+                // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
 #pragma unroll
                 for (int gr = 0; gr < NG; ++gr) {
-                    // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
-                    if (!whole && base + t + 4 * i >= t1) vw[i][gr] = 0u;
-                    top = max(top, vw[i][gr] & 0x7FFFFFFFu);
+                    if (base + g >= t1) v0[gr] = 0u;
+                    if (base + g + 8 >= t1) v1[gr] = 0u;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
+                }
+                if (base + wpos >= t1) {
+#pragma unroll
+                    for (int i = 0; i < (NG + 1) / 2; ++i) mine[i] = 0u;
                 }
             }
-            int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
-            // ---- running maximum; the states are rescaled only where a maximum or the scale's exponent moved
+            uint32_t top = mine[0] & 0x7FFFFFFFu;
+            if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
+            const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
+            // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
+            // above, so that most tiles rescale nothing; weights stay below 2^8
             float mn[NT];
             bool up = etop > eref;
 #pragma unroll
@@ -332,7 +353,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
                 mn[n] = fmaxf(m[n], c);
-                up |= mn[n] > m[n];
+                up |= mn[n] > m[n] + 8.f;
             }
             if (__any_sync(0xffffffffu, up)) {
                 // room of two octaves, so that scales a little larger do not rescale again
@@ -341,7 +362,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 eref = en;
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    const float cf = m[n] == -INFINITY ? 0.f : exp2f(__fsub_rn(m[n], mn[n]));
+                    const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
                     m[n] = mn[n];
                     l[n] *= cf;
                     const float ce = cf * es;
@@ -349,36 +370,30 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                     for (int i = 0; i < 2 * NB; ++i)
 #pragma unroll
                         for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
-                    const float cg = __shfl_sync(0xffffffffu, cf, (lane & 28) | (g >> 1));
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) zo[n][i] *= cg;
+                    for (int i = 0; i < NG; ++i) zo[n][i] *= cf;
                 }
             }
-            // ---- weights of head 4 n + g / 2 at the lane's four positions, and what the bases add
-            float mid[4][NG];
-#pragma unroll
-            for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    mid[i][gr] = __fmaf_rn(i < 2 ? 8.f : 7.f, kv4_s(vw[i][gr]), kv4_z(vw[i][gr]));
-            const float unit = __uint_as_float(uint32_t(267 - eref) << 23);      // 2^(13 - (eref - 127))
+            // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of head
+            // 4 n + g / 2 at the lane's four positions
+            const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
             float w[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float mm = m[n] == -INFINITY ? 0.f : m[n];
-                const float p0 = exp2f(__fsub_rn(sc[n][0], mm)), p1 = exp2f(__fsub_rn(sc[n][1], mm));
+                const float p0 = exp2_approx(__fsub_rn(sc[n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[n][1], mm));
                 l[n] += p0 + p1;
+#pragma unroll
+                for (int gr = 0; gr < NG; ++gr) {
+                    zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
+                    zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
+                }
+                const float u0 = p0 * unit, u1 = p1 * unit;
                 const int src = 4 * t + (g >> 1);
-                w[n][0] = __shfl_sync(0xffffffffu, p0, src);
-                w[n][1] = __shfl_sync(0xffffffffu, p0, src + 16);
-                w[n][2] = __shfl_sync(0xffffffffu, p1, src);
-                w[n][3] = __shfl_sync(0xffffffffu, p1, src + 16);
-#pragma unroll
-                for (int gr = 0; gr < NG; ++gr)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) zo[n][gr] = __fmaf_rn(w[n][i], mid[i][gr], zo[n][gr]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[n][i] *= unit;
+                w[n][0] = __shfl_sync(0xffffffffu, u0, src);
+                w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
+                w[n][2] = __shfl_sync(0xffffffffu, u1, src);
+                w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
             }
             // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3)
             uint32_t vc[4][NB / 2];
@@ -426,7 +441,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     // ---- the warp's state: o[head][dim], m, l
     float* wo = reinterpret_cast<float*>(ring);                       // [warp][rep][D]
     float* wml = wo + kWarps * rep * D;                               // [warp][rep][2]
-    const float un = exp2f(float(eref - 127)) * 0x1p-13f;             // the products' scale, undone
+    const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int hq = 4 * n + t;
@@ -438,9 +453,9 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
         for (int gr = 0; gr < NG; ++gr) {
             float v = zo[n][gr];
-            v += __shfl_xor_sync(0xffffffffu, v, 1);
-            v += __shfl_xor_sync(0xffffffffu, v, 2);
-            zt[gr] = __shfl_sync(0xffffffffu, v, 8 * t);
+            v += __shfl_xor_sync(0xffffffffu, v, 4);
+            v += __shfl_xor_sync(0xffffffffu, v, 8);
+            zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
         }
         if (hq < rep) {
             if (g == 0) {
@@ -460,88 +475,110 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     }
     __syncthreads();
     float* part = p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
-    for (int i = tid; i < rep * D; i += kThr) {
-        const int hq = i / D, dim = i % D;
-        float mx = -INFINITY, num = 0.f, den = 0.f;
+    for (int i = tid; i < rep * (D / 4); i += kThr) {
+        const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
+        float mw[kWarps], mx = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, wml[(w * rep + hq) * 2]);
+        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
+        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-            const float mw = wml[(w * rep + hq) * 2];
-            const float f = mw == -INFINITY ? 0.f : exp2f(__fsub_rn(mw, mx));
+            const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
+            const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
             den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
-            num = __fmaf_rn(f, wo[(w * rep + hq) * D + dim], num);
+            num.x = __fmaf_rn(f, v.x, num.x);
+            num.y = __fmaf_rn(f, v.y, num.y);
+            num.z = __fmaf_rn(f, v.z, num.z);
+            num.w = __fmaf_rn(f, v.w, num.w);
         }
-        part[hq * (D + 2) + 2 + dim] = num;
-        if (dim == 0) {
-            part[hq * (D + 2)] = mx;
-            part[hq * (D + 2) + 1] = den;
-        }
+        float* dst = part + hq * (D + 2);
+        *reinterpret_cast<float2*>(dst + 2 + dim) = make_float2(num.x, num.y);
+        *reinterpret_cast<float2*>(dst + 4 + dim) = make_float2(num.z, num.w);
+        if (dim == 0) *reinterpret_cast<float2*>(dst) = make_float2(mx, den);
     }
 }
 
-// Merge of a (row, KV head)'s split states, and the mass of kMassPos positions per further block.
+// Second launch, grid (rep + position blocks, KV head, row): block x < rep merges the splits of query head x, the
+// others add the mass of kMassPos positions each.
 constexpr int kMassPos = kMergeThr * 4;
 
+// One query head's split states by one warp: weight[s] = 2^(m_s - max m) (if given), and max m and 1 / sum l.
+__device__ __forceinline__ void merge_states(const float* part, size_t stride, int ns, int lane, float* weight, float& mx,
+                                             float& inv) {
+    float m[(kKv4MaxSplits + 31) / 32], l[(kKv4MaxSplits + 31) / 32];
+    mx = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < (kKv4MaxSplits + 31) / 32; ++i) {
+        const int s = lane + 32 * i;
+        float2 v = make_float2(-INFINITY, 0.f);
+        if (s < ns) v = *reinterpret_cast<const float2*>(part + s * stride);
+        m[i] = v.x;
+        l[i] = v.y;
+        mx = fmaxf(mx, v.x);
+    }
+    mx = warp_max(mx);
+    float den = 0.f;
+#pragma unroll
+    for (int i = 0; i < (kKv4MaxSplits + 31) / 32; ++i) {
+        const float f = m[i] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[i], mx));
+        if (weight && lane + 32 * i < ns) weight[lane + 32 * i] = f;
+        den = __fmaf_rn(f, l[i], den);
+    }
+    inv = __frcp_rn(warp_sum(den));
+}
+
 __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParams p) {
-    __shared__ float sm[kKv4MaxSplits * kKv4MaxRep], sl[kKv4MaxSplits * kKv4MaxRep];
-    __shared__ float hm[kKv4MaxRep], hl[kKv4MaxRep];
-    const int h = blockIdx.y, b = blockIdx.z, d = p.c.d, rep = p.nq / p.c.nkv, tid = threadIdx.x;
+    __shared__ float weight[kKv4MaxSplits], hm[kKv4MaxRep], hl[kKv4MaxRep];
+    __shared__ float2 acc[kMergeThr];
+    const int h = blockIdx.y, b = blockIdx.z, d = p.c.d, rep = p.nq / p.c.nkv;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int err = kv4_row_error(p, b);
-    const bool merge = blockIdx.x == 0;
-    const int pos = (int(blockIdx.x) - 1) * kMassPos + tid * 4;       // this thread's four positions
-    if (!merge && (err != KMR_OK || (int(blockIdx.x) - 1) * kMassPos > p.c.S)) return;
-    // split states of row r to shared memory, and each head's maximum and 1 / sum
-    auto states = [&](int r, int ns) {
-        const float* part = p.part + (size_t(r) * p.c.nkv + h) * p.nsplit * rep * (d + 2);
-        __syncthreads();
-        for (int i = tid; i < ns * rep; i += kMergeThr) {
-            sm[i] = part[size_t(i) * (d + 2)];
-            sl[i] = part[size_t(i) * (d + 2) + 1];
-        }
-        __syncthreads();
-        if (tid < rep) {
-            float mx = -INFINITY, den = 0.f;
-            for (int s = 0; s < ns; ++s) mx = fmaxf(mx, sm[s * rep + tid]);
-            for (int s = 0; s < ns; ++s) {
-                const float ms = sm[s * rep + tid];
-                const float f = ms == -INFINITY ? 0.f : exp2f(__fsub_rn(ms, mx));
-                den = __fmaf_rn(f, sl[s * rep + tid], den);
-                sm[s * rep + tid] = f;
-            }
-            hm[tid] = mx;
-            hl[tid] = __frcp_rn(den);
-        }
-        __syncthreads();
-    };
+    const size_t stride = size_t(rep) * (d + 2);              // between the splits of a head
     int chunk, ns;
-    if (merge) {
-        float* out = p.out + (size_t(b) * p.nq + h * rep) * d;
+    if (int(blockIdx.x) < rep) {
+        const int hq = blockIdx.x;
+        float2* out = reinterpret_cast<float2*>(p.out + (size_t(b) * p.nq + h * rep + hq) * d);
         pdl_wait();
+        const int pairs = d / 2, groups = kMergeThr / pairs, i = tid % pairs, grp = tid / pairs;
         if (err != KMR_OK) {
-            if (tid == 0 && h == 0) set_error(p.err, err);
-            for (int i = tid; i < rep * d; i += kMergeThr) out[i] = 0.f;
+            if (tid == 0 && h == 0 && hq == 0) set_error(p.err, err);
+            if (grp == 0) out[i] = make_float2(0.f, 0.f);
             return;
         }
         kv4_split_plan(p.cpos[b] + 1, chunk, ns);
-        states(b, ns);
-        const float* part = p.part + (size_t(b) * p.c.nkv + h) * p.nsplit * rep * (d + 2);
-        for (int i = tid; i < rep * d; i += kMergeThr) {
-            const int hq = i / d;
-            const float* mine = part + size_t(hq) * (d + 2) + 2 + i % d;
-            float num = 0.f;
-#pragma unroll 8
-            for (int s = 0; s < ns; ++s) num = __fmaf_rn(sm[s * rep + hq], mine[size_t(s) * rep * (d + 2)], num);
-            out[i] = num * hl[hq];
+        const float* part = p.part + (size_t(b) * p.c.nkv + h) * p.nsplit * stride + size_t(hq) * (d + 2);
+        if (warp == 0) {
+            float mx, inv;
+            merge_states(part, stride, ns, lane, weight, mx, inv);
+            if (lane == 0) hl[0] = inv;
         }
+        __syncthreads();
+        // the splits in 4 (d = 128) or 8 interleaved groups, each in split order, then the groups in order
+        float2 num = make_float2(0.f, 0.f);
+#pragma unroll 8
+        for (int s = grp; s < ns; s += groups) {
+            const float2 v = *reinterpret_cast<const float2*>(part + s * stride + 2 + 2 * i);
+            num.x = __fmaf_rn(weight[s], v.x, num.x);
+            num.y = __fmaf_rn(weight[s], v.y, num.y);
+        }
+        acc[tid] = num;
+        __syncthreads();
+        if (grp) return;
+        for (int k = 1; k < groups; ++k) {
+            num.x += acc[i + k * pairs].x;
+            num.y += acc[i + k * pairs].y;
+        }
+        out[i] = make_float2(num.x * hl[0], num.y * hl[0]);
         return;
     }
+    if (err != KMR_OK) return;
+    const int block0 = (int(blockIdx.x) - rep) * kMassPos, pos = block0 + tid * 4;       // this thread's four positions
     const int slot = p.slot_ids[b];
     int before = 0, most = 0;
     for (int r = tid; r < p.B; r += kMergeThr) {
         if (p.slot_ids[r] != slot || kv4_row_error(p, r) != KMR_OK) continue;
         before |= r < b;
-        most |= p.cpos[r] >= (int(blockIdx.x) - 1) * kMassPos;
+        most |= p.cpos[r] >= block0;
     }
     // the slot's first row adds for all of them; nothing to add past the longest
     before = __syncthreads_or(before);
@@ -555,15 +592,26 @@ __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParam
         const int L = p.cpos[r] + 1;
         last = max(last, L);
         kv4_split_plan(L, chunk, ns);
-        states(r, ns);
+        __syncthreads();
+        if (warp < rep) {
+            float mx, inv;
+            merge_states(p.part + (size_t(r) * p.c.nkv + h) * p.nsplit * stride + size_t(warp) * (d + 2), stride, ns, lane,
+                         nullptr, mx, inv);
+            if (lane == 0) {
+                hm[warp] = mx;
+                hl[warp] = inv;
+            }
+        }
+        __syncthreads();
         const float* sc = p.scores + (size_t(r) * p.c.nkv + h) * rep * p.c.S + pos;
         if (pos < L) {
+#pragma unroll 2
             for (int k = 0; k < rep; ++k) {
                 const float4 v = *reinterpret_cast<const float4*>(sc + size_t(k) * p.c.S);
                 const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    if (pos + e < L) add[e] = __fmaf_rn(exp2f(__fsub_rn(x[e], hm[k])), hl[k], add[e]);
+                    if (pos + e < L) add[e] = __fmaf_rn(exp2_approx(__fsub_rn(x[e], hm[k])), hl[k], add[e]);
             }
         }
     }
@@ -578,6 +626,7 @@ __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParam
             if (pos + e < last) mass[e] += add[e];
     }
 }
+static_assert(kMergeThr / 32 >= kKv4MaxRep, "a warp per query head");
 
 template <int D, int G>
 const void* split_fn(int rep) {
@@ -600,8 +649,10 @@ SplitVariant split_variant(int d, int g, int rep) {
 }  // namespace
 
 int kv4_attn_splits(int S) {
-    // a shorter row can have more splits than the longest (the chunk is rounded up), never more than 32
-    const int most = (S + kKv4MinChunk - 1) / kKv4MinChunk;
+    // a shorter row can have more splits than the longest: 16 at most until the chunk is 256 (4096 positions),
+    // then one per 256 up to 76
+    const int small = (S + kKv4MinChunk - 1) / kKv4MinChunk, large = (S + 255) / 256;
+    const int most = small < 16 ? small : (large > 16 ? large : 16);
     return most < kKv4MaxSplits ? most : kKv4MaxSplits;
 }
 size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit) {
@@ -634,7 +685,7 @@ cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(p.mass ? 1 + (p.c.S + kMassPos - 1) / kMassPos : 1, p.c.nkv, p.B);
+    cfg.gridDim = dim3(p.nq / p.c.nkv + (p.mass ? (p.c.S + kMassPos - 1) / kMassPos : 0), p.c.nkv, p.B);
     cfg.blockDim = dim3(kMergeThr);
     cfg.dynamicSmemBytes = 0;
     cfg.attrs = &attr;
