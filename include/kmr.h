@@ -232,7 +232,7 @@ int kmr_decode_attn_noalloc(const float* q, const uint16_t* k_cache, const uint1
  *   k_sz, v_sz        uint32 [slots][n_kv][max_len][d / group]: bf16 z in the low half, bf16 s in the
  *       high half.
  * All four are device memory, 16-byte aligned, owned by the caller; d is 64 or 128, group at most d,
- * max_len a multiple of 16 up to 2^28.  A cache that fails this gives KMR_ERR_INVALID_ARG (pointers)
+ * n_kv at most 1024, max_len a multiple of 16 up to 2^28.  A cache that fails this gives KMR_ERR_INVALID_ARG (pointers)
  * or KMR_ERR_SHAPE.  Positions of a row that no call has written may hold anything.
  *
  * The calls below take up to 1024 rows (KMR_ERR_BATCH), queue their work on `stream` without

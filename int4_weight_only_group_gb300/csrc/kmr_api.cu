@@ -26,6 +26,7 @@ cudaError_t gemv_set_attributes();
 cudaError_t head_set_attributes();
 cudaError_t attn_set_attributes();
 cudaError_t kv4_attn_set_attributes();
+cudaError_t kv4_set_attributes();
 
 __device__ int g_standalone_err;
 
@@ -60,6 +61,7 @@ cudaError_t ensure_kernel_attributes() {
     if ((e = head_set_attributes()) != cudaSuccess) return e;
     if ((e = attn_set_attributes()) != cudaSuccess) return e;
     if ((e = kv4_attn_set_attributes()) != cudaSuccess) return e;
+    if ((e = kv4_set_attributes()) != cudaSuccess) return e;
     if ((e = poison_set_attributes()) != cudaSuccess) return e;
     if ((e = gemm_set_attributes()) != cudaSuccess) return e;
     if ((e = tc_gemm_set_attributes()) != cudaSuccess) return e;

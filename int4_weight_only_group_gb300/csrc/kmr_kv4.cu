@@ -1,16 +1,146 @@
 // Writes of the 4-bit KV cache: new tokens (q/k RMSNorm, M-RoPE and quantisation in one pass),
 // conversions from and to a bf16 cache, and eviction into another row.  The format and the
 // quantiser are in kmr_kv4.cuh.
+#include <type_traits>
+
 #include "kmr_kv4.cuh"
 
 namespace kmr {
 namespace {
 
-constexpr int kThr = 256;
+constexpr int kThr = 128;
 
-// Whether a later row of the call writes this (slot, position) too: then that row's values stay.
+// ------------------------------------------------------------------ a vector on four lanes
+// Every kernel here holds a vector of D dims on four neighbouring lanes: lane l has dims 32 b + 8 l .. + 7 of each
+// of the NB = D / 32 blocks.  That is one 16-byte piece of a bf16 row per block, both halves of every rotation
+// pair (dim i + D / 2 is block b + NB / 2), and 4 NB contiguous bytes of a row of codes: lane l's words of
+// a K row, lanes 2 l and 2 l + 1's units of a V row.
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+// (w << 8) | codes hi, lo held within 0..15
+__device__ __forceinline__ uint32_t pack_code(int hi, int lo, uint32_t w) {
+    uint32_t r;
+    asm("cvt.pack.sat.u4.s32.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(hi), "r"(lo), "r"(w));
+    return r;
+}
+
+// The lane's codes (word b: dims 32 b + 8 l + i in nibble i) and the vector's group words (z, s).
+// lo, hi = the group's extremes; s = bf16((hi - lo) / 15), 0 below 2^-126 (its reciprocal would leave the normal
+// range); z = bf16(lo); c = rint((x - z) / s) within 0..15, 0 where s is 0.  Both quotients are the correctly
+// rounded ones (Markstein 1990: with r near 1 / s, q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value
+// half-way between two codes is seen as half-way and goes to the even one.  A group that holds a NaN or an
+// infinity, or whose range overflows, stores s = 0 and z = NaN: it reads back as NaN.
+template <int D, int G>
+__device__ __forceinline__ void quantize(const float (&x)[D / 32][8], uint32_t (&w)[D / 32], uint32_t (&word)[D / G]) {
+    constexpr int NG = D / G, BPG = G / 32;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        float lo = x[gr * BPG][0], hi = lo;
+#pragma unroll
+        for (int k = 0; k < BPG; ++k)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                lo = min_nan(lo, x[gr * BPG + k][i]);
+                hi = max_nan(hi, x[gr * BPG + k][i]);
+            }
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
+        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+        const float range = __fsub_rn(hi, lo), fifteenth = 1.f / 15.f;
+        const float s0 = __fmul_rn(range, fifteenth);
+        const float s1 = __fmaf_rn(__fmaf_rn(-15.f, s0, range), fifteenth, s0);
+        uint32_t u;
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(s1), "f"(lo));
+        if (u < 0x00800000u) u &= 0xFFFFu;
+        const bool bad = (u & 0x7F800000u) == 0x7F800000u || (u & 0x7F80u) == 0x7F80u;
+        if (bad) u = 0x7FC0u;
+        word[gr] = u;
+        const float s = kv4_s(u), z = bad ? 0.f : kv4_z(u);
+        float r = 0.f;
+        if (s > 0.f) {
+            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+            r = __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
+        }
+#pragma unroll
+        for (int k = 0; k < BPG; ++k) {
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = __fsub_rn(x[gr * BPG + k][i], z);
+                const float q0 = __fmul_rn(a, r);
+                const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
+                // 1.5 * 2^23 + q rounds q to a whole number (half to even) in the low bits
+                c[i] = __float_as_int(__fadd_rn(q, 12582912.f)) - 0x4B400000;
+            }
+            uint32_t v = pack_code(c[7], c[6], 0u);
+            v = pack_code(c[5], c[4], v);
+            v = pack_code(c[3], c[2], v);
+            v = pack_code(c[1], c[0], v);
+            w[gr * BPG + k] = bad ? 0u : v;
+        }
+    }
+}
+
+// Words of a lane <-> its 4 NB bytes of a row of codes.
+template <int NB>
+__device__ __forceinline__ void store_codes(uint8_t* row, const uint32_t (&w)[NB], bool key, int l) {
+    uint32_t v[NB];
+#pragma unroll
+    for (int i = 0; i < NB; ++i) v[i] = w[i];
+    if (!key) {
+        // units of dims 8 l .. 8 l + 3 of all blocks, then those of 8 l + 4 .. 8 l + 7
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            v[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+            v[NB / 2 + i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+        }
+    }
+    if constexpr (NB == 4)
+        *reinterpret_cast<uint4*>(row + l * 16) = make_uint4(v[0], v[1], v[2], v[3]);
+    else
+        *reinterpret_cast<uint2*>(row + l * 8) = make_uint2(v[0], v[1]);
+}
+template <int NB>
+__device__ __forceinline__ void load_codes(const uint8_t* row, uint32_t (&w)[NB], bool key, int l) {
+    uint32_t v[NB];
+    if constexpr (NB == 4) {
+        const uint4 u = *reinterpret_cast<const uint4*>(row + l * 16);
+        v[0] = u.x; v[1] = u.y; v[2] = u.z; v[3] = u.w;
+    } else {
+        const uint2 u = *reinterpret_cast<const uint2*>(row + l * 8);
+        v[0] = u.x; v[1] = u.y;
+    }
+#pragma unroll
+    for (int i = 0; i < NB; ++i) w[i] = v[i];
+    if (!key) {
+#pragma unroll
+        for (int i = 0; i < NB / 2; ++i) {
+            w[2 * i] = __byte_perm(v[i], v[NB / 2 + i], 0x5410);
+            w[2 * i + 1] = __byte_perm(v[i], v[NB / 2 + i], 0x7632);
+        }
+    }
+}
+// Group words of a vector, one by each lane that has one to write.
+template <int NG>
+__device__ __forceinline__ void store_words(uint32_t* row, const uint32_t (&word)[NG], int l) {
+#pragma unroll
+    for (int i = 0; i < NG; ++i)
+        if (l == i) row[i] = word[i];
+}
+
+// Whether a later row of the call writes one of positions [p0, p1) of the slot too: its values stay.
 // Uniform over the CTA (every thread takes part).
-__device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int pos, const int32_t* slots,
+__device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int p0, int p1, const int32_t* slots,
                                                  const int32_t* start, const int32_t* len, int T, int S) {
     if (b + 1 >= B) return false;
     int hit = 0;
@@ -18,7 +148,7 @@ __device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int pos
         if (slots[r] != slot) continue;
         const int s0 = start[r], n = len ? len[r] : T;
         if (n < 0 || n > T || s0 < 0 || s0 > S - n) continue;      // a refused row writes nothing
-        hit |= pos >= s0 && pos < s0 + n;
+        hit |= p1 > s0 && p0 < s0 + n;
     }
     return __syncthreads_or(hit) != 0;
 }
@@ -26,135 +156,195 @@ __device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int pos
 // ------------------------------------------------------------------ new tokens
 // One CTA per token.  The token's angles are formed once: frequency i advances by theta^(-2i/d) / 2 pi
 // turns per position, held as a 64-bit fraction, so that position x fraction mod 1 is exact for any
-// position and the angle keeps its bits far into a long context.  Then d / 4 lanes take a head at a
-// time, four dims each: the rotation's partner dim is d / 8 lanes away.
+// position and the angle keeps its bits far into a long context.  Then each warp takes eight heads at a time.
+template <int D, int G>
 __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
-    __shared__ float cs[64], sn[64];
-    const int t = blockIdx.x, b = blockIdx.y;
-    const int d = p.c.d, nkv = p.c.nkv;
+    constexpr int NB = D / 32, NG = D / G;
+    __shared__ __align__(16) float cs[D / 2], sn[D / 2];
+    const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int nkv = p.c.nkv;
     const int n = p.n_tokens ? p.n_tokens[b] : p.T;
     const int slot = p.slot_ids[b], c0 = p.cpos[b];
     const bool bad_n = n < 0 || n > p.T, bad_slot = slot < 0 || slot >= p.c.slots;
     const bool bad_pos = !bad_n && (c0 < 0 || c0 > p.c.S - n);
     if (bad_n || (n > 0 && (bad_slot || bad_pos))) {
-        if (t == 0 && threadIdx.x == 0)
+        if (t == 0 && tid == 0)
             set_error(p.err, bad_n ? KMR_ERR_INVALID_ARG : (bad_slot ? KMR_ERR_SLOT_RANGE : KMR_ERR_CACHE_FULL));
         return;
     }
     if (t >= n) return;
     const int pos = c0 + t;
-    if (threadIdx.x < d / 2) {
-        const int f = threadIdx.x, axis = f < p.sec0 ? 0 : (f < p.sec0 + p.sec1 ? 1 : 2);
+    const int heads = p.nq + 2 * nkv, l = tid & 3;
+    const float* row = p.qkv + (size_t(b) * p.T + t) * heads * D;
+    if (tid < D / 2) {
+        const int axis = tid < p.sec0 ? 0 : (tid < p.sec0 + p.sec1 ? 1 : 2);
         const long long x = p.positions[(size_t(axis) * p.B + b) * p.T + t];
-        const unsigned long long turn = (unsigned long long)x * p.turn[f];
-        const float frac = float(int(turn >> 32)) * 0x1p-31f;          // half turns in [-1, 1)
-        sincospif(frac, &sn[f], &cs[f]);
+        const unsigned long long turn = (unsigned long long)x * p.turn[tid];
+        const float half_turns = float(int(turn >> 32)) * 0x1p-31f;    // in [-1, 1]
+        sincospif(half_turns, &sn[tid], &cs[tid]);
     }
+    const bool lose = later_row_writes(b, p.B, slot, pos, pos + 1, p.slot_ids, p.cpos, p.n_tokens, p.T, p.c.S);
     __syncthreads();
-    const bool lose = later_row_writes(b, p.B, slot, pos, p.slot_ids, p.cpos, p.n_tokens, p.T, p.c.S);
-    const int lpr = d / 4, lane = threadIdx.x % lpr, sub = threadIdx.x / lpr, nsub = kThr / lpr;
-    const int heads = p.nq + 2 * nkv, nb = d / 32, ng = d / p.c.g;
-    const float* row = p.qkv + (size_t(b) * p.T + t) * heads * d;
     // every lane of a warp runs the same number of rounds, so that the shuffles are complete
-    for (int h0 = 0; h0 < heads; h0 += nsub) {
-        const int hh = h0 + sub;
+    for (int h0 = 0; h0 < heads; h0 += kThr / 4) {
+        const int hh = h0 + tid / 4;
         const bool on = hh < heads;
         const int h = on ? hh : heads - 1;
         const bool isq = h < p.nq, isk = !isq && h < p.nq + nkv;
-        const float4 v = *reinterpret_cast<const float4*>(row + size_t(h) * d + lane * 4);
-        float x[4] = {v.x, v.y, v.z, v.w};
+        float x[NB][8];
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+            const float4* src = reinterpret_cast<const float4*>(row + size_t(h) * D + 32 * k + 8 * l);
+            const float4 u = __ldcs(src), v = __ldcs(src + 1);
+            x[k][0] = u.x; x[k][1] = u.y; x[k][2] = u.z; x[k][3] = u.w;
+            x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
+        }
         const uint16_t* w = isq ? p.qn_w : p.kn_w;
         float ss = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ss = __fmaf_rn(x[e], x[e], ss);
-        for (int o = 1; o < lpr; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if ((isq || isk) && w) {
-            const float r = rsqrtf(ss / float(d) + p.eps);
-            const uint2 wv = *reinterpret_cast<const uint2*>(w + lane * 4);
-            x[0] = x[0] * r * bf16_lo(wv.x);
-            x[1] = x[1] * r * bf16_hi(wv.x);
-            x[2] = x[2] * r * bf16_lo(wv.y);
-            x[3] = x[3] * r * bf16_hi(wv.y);
-        }
-        float y[4];
+        for (int k = 0; k < NB; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __shfl_xor_sync(0xffffffffu, x[e], lpr / 2);
+            for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[k][i], x[k][i], ss);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 1);
+        ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         if (isq || isk) {
-            const bool lo = lane < lpr / 2;
+            if (w) {
+                const float r = rsqrtf(ss / float(D) + p.eps);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const int f = (lane * 4 + e) % (d / 2);
-                x[e] = lo ? x[e] * cs[f] - y[e] * sn[f] : x[e] * cs[f] + y[e] * sn[f];
+                for (int k = 0; k < NB; ++k) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(w + 32 * k + 8 * l);
+                    const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        x[k][2 * i] = x[k][2 * i] * r * bf16_lo(wv[i]);
+                        x[k][2 * i + 1] = x[k][2 * i + 1] * r * bf16_hi(wv[i]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < NB / 2; ++k)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float c = cs[32 * k + 8 * l + i], s = sn[32 * k + 8 * l + i];
+                    const float lo = x[k][i], hi = x[k + NB / 2][i];
+                    x[k][i] = lo * c - hi * s;
+                    x[k + NB / 2][i] = hi * c + lo * s;
+                }
+        }
+        if (isq && on) {
+            float4* dst = reinterpret_cast<float4*>(p.q_out + ((size_t(b) * p.T + t) * p.nq + h) * D + 8 * l);
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                dst[8 * k] = make_float4(x[k][0], x[k][1], x[k][2], x[k][3]);
+                dst[8 * k + 1] = make_float4(x[k][4], x[k][5], x[k][6], x[k][7]);
             }
         }
-        uint32_t word;
-        const uint32_t c = kv4_quantize(x, p.c.g / 4, word);
-        if (!on) continue;
-        if (isq) {
-            *reinterpret_cast<float4*>(p.q_out + ((size_t(b) * p.T + t) * p.nq + h) * d + lane * 4) =
-                make_float4(x[0], x[1], x[2], x[3]);
-            continue;
-        }
-        if (lose) continue;
+        if (__all_sync(0xffffffffu, isq)) continue;
+        uint32_t codes[NB], word[NG];
+        quantize<D, G>(x, codes, word);
+        if (!on || isq || lose) continue;
         const int kvh = isk ? h - p.nq : h - p.nq - nkv;
         const size_t at = (size_t(slot) * nkv + kvh) * p.c.S + pos;
-        uint16_t* codes = reinterpret_cast<uint16_t*>((isk ? p.c.kc : p.c.vc) + at * (d / 2));
-        codes[kv4_unit(lane, nb, isk)] = uint16_t(c);
-        if (lane % (p.c.g / 4) == 0) (isk ? p.c.ks : p.c.vs)[at * ng + lane * 4 / p.c.g] = word;
-        if (isk && p.mass && lane == 0) p.mass[at] = 0.f;
+        store_codes<NB>((isk ? p.c.kc : p.c.vc) + at * (D / 2), codes, isk, l);
+        store_words<NG>((isk ? p.c.ks : p.c.vs) + at * NG, word, l);
+        if (isk && p.mass && l == 0) p.mass[at] = 0.f;
     }
 }
 
 // ------------------------------------------------------------------ bf16 <-> 4 bits
-template <bool TO16>
+// Grid (positions / kSpan, 2 n_kv, span): a warp takes eight neighbouring positions of K or V of one head at a time.
+constexpr int kSpan = 64;
+
+__device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+
+template <int D, int G, bool TO16>
 __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParams p) {
-    const int b = blockIdx.y, t = blockIdx.x;
-    const int d = p.c.d, nkv = p.c.nkv, n = p.lengths[b];
+    constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+    const int b = blockIdx.z, tid = threadIdx.x, l = tid & 3;
+    const int nkv = p.c.nkv, n = p.lengths[b];
     const int slot = p.slot_ids[b], s0 = p.start[b], slot16 = p.slot16[b], s16 = p.start16[b];
     const bool bad_n = n < 0 || n > p.T;
     const bool bad_slot = slot < 0 || slot >= p.c.slots || slot16 < 0 || slot16 >= p.slots16;
     const bool bad_pos = !bad_n && (s0 < 0 || s0 > p.c.S - n || s16 < 0 || s16 > p.S16 - n);
     if (bad_n || (n > 0 && (bad_slot || bad_pos))) {
-        if (t == 0 && threadIdx.x == 0)
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
             set_error(p.err, bad_n ? KMR_ERR_INVALID_ARG : (bad_slot ? KMR_ERR_SLOT_RANGE : KMR_ERR_CACHE_FULL));
         return;
     }
-    if (t >= n) return;
-    if (TO16 ? later_row_writes(b, p.B, slot16, s16 + t, p.slot16, p.start16, p.lengths, p.T, p.S16)
-             : later_row_writes(b, p.B, slot, s0 + t, p.slot_ids, p.start, p.lengths, p.T, p.c.S))
-        return;
-    const int lpr = d / 4, lane = threadIdx.x % lpr, sub = threadIdx.x / lpr, nsub = kThr / lpr;
-    const int nb = d / 32, ng = d / p.c.g;
-    for (int h0 = 0; h0 < 2 * nkv; h0 += nsub) {
-        const int hh = h0 + sub;
-        const bool on = hh < 2 * nkv;
-        const int h = on ? hh : 0, kvh = h % nkv;
-        const bool isk = h < nkv;
-        const size_t at = (size_t(slot) * nkv + kvh) * p.c.S + s0 + t;
-        const size_t at16 = ((size_t(slot16) * nkv + kvh) * p.S16 + s16 + t) * d + lane * 4;
-        uint16_t* codes = reinterpret_cast<uint16_t*>((isk ? p.c.kc : p.c.vc) + at * (d / 2)) + kv4_unit(lane, nb, isk);
-        uint32_t* words = (isk ? p.c.ks : p.c.vs) + at * ng + lane * 4 / p.c.g;
-        uint2* vals = reinterpret_cast<uint2*>((isk ? p.k16 : p.v16) + at16);
+    const int t0 = blockIdx.x * kSpan, t1 = min(n, t0 + kSpan);
+    if (t0 >= t1) return;
+    const int wslot = TO16 ? slot16 : slot, w0 = TO16 ? s16 : s0, wS = TO16 ? p.S16 : p.c.S;
+    const int32_t* wslots = TO16 ? p.slot16 : p.slot_ids;
+    const int32_t* wstart = TO16 ? p.start16 : p.start;
+    const bool clash = later_row_writes(b, p.B, wslot, w0 + t0, w0 + t1, wslots, wstart, p.lengths, p.T, wS);
+    const bool key = int(blockIdx.y) < nkv;
+    const int kvh = key ? blockIdx.y : blockIdx.y - nkv;
+    const size_t row = (size_t(slot) * nkv + kvh) * p.c.S + s0, row16 = (size_t(slot16) * nkv + kvh) * p.S16 + s16;
+#pragma unroll 2
+    for (int i0 = t0; i0 < t1; i0 += kThr / 4) {
+        const int t = i0 + tid / 4;
+        bool on = t < t1;
+        if (clash && on) {
+            for (int r = b + 1; r < p.B; ++r) {
+                const int m = p.lengths[r], q = wstart[r];
+                if (wslots[r] == wslot && m >= 0 && m <= p.T && q >= 0 && q <= wS - m && w0 + t >= q && w0 + t < q + m)
+                    on = false;
+            }
+        }
+        const size_t at = row + (t < t1 ? t : t0), at16 = (row16 + (t < t1 ? t : t0)) * D + 8 * l;
+        uint4* vals = reinterpret_cast<uint4*>((key ? p.k16 : p.v16) + at16);
+        uint8_t* codes = (key ? p.c.kc : p.c.vc) + at * (D / 2);
+        uint32_t* words = (key ? p.c.ks : p.c.vs) + at * NG;
         if constexpr (TO16) {
+            uint32_t w[NB], word[NG];
+            load_codes<NB>(codes, w, key, l);
+#pragma unroll
+            for (int i = 0; i < NG; ++i) word[i] = words[i];
             if (!on) continue;
-            const uint32_t c = *codes, w = *words;
-            const float s = kv4_s(w), z = kv4_z(w);
-            *vals = make_uint2(pack_bf16x2(__fmaf_rn(float(c & 15), s, z), __fmaf_rn(float((c >> 4) & 15), s, z)),
-                               pack_bf16x2(__fmaf_rn(float((c >> 8) & 15), s, z), __fmaf_rn(float(c >> 12), s, z)));
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint32_t u = word[k / BPG];
+                const uint32_t s2 = __byte_perm(u, 0u, 0x3232), z2 = __byte_perm(u, 0u, 0x1010);
+                uint32_t y[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // a nibble under the exponent of 128 is the bf16 128 + c; nibbles (i, i + 4)
+                    const uint32_t c = fma_bf16x2(and_or(w[k] >> (4 * i), 0x000F000Fu, 0x43004300u), 0x3F803F80u,
+                                                  0xC300C300u);
+                    y[i] = fma_bf16x2(c, s2, z2);
+                }
+                __stcs(vals + 4 * k, make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
+                                                __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
+            }
         } else {
-            const uint2 u = *vals;
-            const float x[4] = {bf16_lo(u.x), bf16_hi(u.x), bf16_lo(u.y), bf16_hi(u.y)};
-            uint32_t word;
-            const uint32_t c = kv4_quantize(x, p.c.g / 4, word);
+            float x[NB][8];
+#pragma unroll
+            for (int k = 0; k < NB; ++k) {
+                const uint4 u = __ldcs(vals + 4 * k);
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    x[k][2 * i] = bf16_lo(v[i]);
+                    x[k][2 * i + 1] = bf16_hi(v[i]);
+                }
+            }
+            uint32_t w[NB], word[NG];
+            quantize<D, G>(x, w, word);
             if (!on) continue;
-            *codes = uint16_t(c);
-            if (lane % (p.c.g / 4) == 0) *words = word;
+            store_codes<NB>(codes, w, key, l);
+            store_words<NG>(words, word, l);
         }
     }
 }
 
 // ------------------------------------------------------------------ eviction
 constexpr int kSelThr = 1024;
+constexpr int kSelBins = 2048;
+constexpr int kSelCache = 48 * 1024;      // keys held in shared memory (192 KB); longer rows read them again each pass
 
 // Order-preserving integer of a mass: larger mass, larger key; -0 counts as 0, NaN below everything.
 __device__ __forceinline__ uint32_t mass_key(float m) {
@@ -177,14 +367,17 @@ __device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
 }
 
 // Positions kept of one (row, head): the newest `recent`, and of the older ones the heaviest, the
-// lower index first among equals.  The smallest kept key is found digit by digit (8 bits at a time,
-// a histogram each), then one ordered pass writes the kept indices in ascending order.
+// lower index first among equals.  The smallest kept key is found digit by digit (11, 11 and 10 bits: a
+// histogram each, searched from the top by a scan over the CTA), then one ordered pass writes the kept
+// indices in ascending order.  The keys are formed once and kept in shared memory.  What bounds it is the chain
+// of some fifteen barriers: a row of 8192 masses is 32 KB.
 __global__ void __launch_bounds__(kSelThr) kv4_select_kernel(const Kv4EvictParams p) {
-    __shared__ int hist[256];
+    extern __shared__ uint32_t keys[];
+    __shared__ int hist[kSelBins];
     __shared__ int wsum[2][32];
-    __shared__ uint32_t sh_prefix;
-    __shared__ int sh_need;
+    __shared__ int found[2];
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_launch_dependents();
     const int bad = evict_row_error(p, b);
     int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
     const int n = bad ? 0 : p.lengths[b];
@@ -202,33 +395,50 @@ __global__ void __launch_bounds__(kSelThr) kv4_select_kernel(const Kv4EvictParam
     for (int i = tid; i < newest; i += kSelThr) kept[need + i] = old + i;
     if (need == 0) return;
     const float* m = p.mass + (size_t(p.src_ids[b]) * p.src.nkv + h) * p.src.S;
+    const bool cached = old <= kSelCache;
+    if (cached)
+        for (int i = tid; i < old; i += kSelThr) keys[i] = mass_key(m[i]);
+    auto key_at = [&](int i) { return cached ? keys[i] : mass_key(m[i]); };
     uint32_t prefix = 0;
     int left = need;                                 // how many of the keys that share the prefix are kept
-    for (int shift = 24; shift >= 0; shift -= 8) {
-        if (tid < 256) hist[tid] = 0;
-        __syncthreads();
-        const uint32_t above = shift == 24 ? 0u : 0xFFFFFFFFu << (shift + 8);
+#pragma unroll
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : (pass == 1 ? 10 : 0), bits = pass < 2 ? 11 : 10;
+        const uint32_t above = pass == 0 ? 0u : 0xFFFFFFFFu << (shift + bits), digits = (1u << bits) - 1u;
+        hist[tid] = 0;
+        hist[tid + kSelThr] = 0;
+        __syncthreads();                             // (also: the keys are there)
         for (int i = tid; i < old; i += kSelThr) {
-            const uint32_t k = mass_key(m[i]);
-            if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & 255], 1);
+            const uint32_t k = key_at(i);
+            if ((k & above) == prefix) atomicAdd(&hist[(k >> shift) & digits], 1);
         }
         __syncthreads();
-        if (tid == 0) {
-            int got = 0, dig = 255;
-            while (dig > 0 && got + hist[dig] < left) got += hist[dig--];
-            sh_prefix = prefix | (uint32_t(dig) << shift);
-            sh_need = left - got;
+        // thread i holds bins 2047 - 2 i and 2046 - 2 i: an inclusive scan counts from the top
+        const int top = kSelBins - 1 - 2 * tid, c0 = hist[top], c1 = hist[top - 1];
+        int sum = c0 + c1;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += v;
+        }
+        if (lane == 31) wsum[0][warp] = sum;
+        __syncthreads();
+        int before = sum - c0 - c1;
+        for (int w = 0; w < warp; ++w) before += wsum[0][w];
+        if (before < left && left <= before + c0 + c1) {
+            const bool second = before + c0 < left;
+            found[0] = second ? top - 1 : top;
+            found[1] = left - before - (second ? c0 : 0);
         }
         __syncthreads();
-        prefix = sh_prefix;
-        left = sh_need;
+        prefix |= uint32_t(found[0]) << shift;
+        left = found[1];
     }
     // keys above `prefix` are kept, and the first `left` of those equal to it
-    const int per = ((old + 1023) / 1024) * 32;      // positions of a warp, a multiple of 32
+    const int per = ((old + kSelThr - 1) / kSelThr) * 32;      // positions of a warp, a multiple of 32
     const int i0 = warp * per, i1 = min(old, i0 + per);
     int gt = 0, eq = 0;
     for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = mass_key(m[i]);
+        const uint32_t k = key_at(i);
         gt += k > prefix;
         eq += k == prefix;
     }
@@ -239,14 +449,12 @@ __global__ void __launch_bounds__(kSelThr) kv4_select_kernel(const Kv4EvictParam
         wsum[1][warp] = eq;
     }
     __syncthreads();
-    gt = eq = 0;
-    for (int w = 0; w < warp; ++w) {
-        gt += wsum[0][w];
-        eq += wsum[1][w];
-    }
+    gt = warp_sum(lane < warp ? wsum[0][lane] : 0);
+    eq = warp_sum(lane < warp ? wsum[1][lane] : 0);
     for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? mass_key(m[i + lane]) : 0u;
-        const bool in = i + lane < i1, isg = in && k > prefix, ise = in && k == prefix;
+        const bool in = i + lane < i1;
+        const uint32_t k = in ? key_at(i + lane) : 0u;
+        const bool isg = in && k > prefix, ise = in && k == prefix;
         const uint32_t mg = __ballot_sync(0xffffffffu, isg), me = __ballot_sync(0xffffffffu, ise);
         const uint32_t below = (1u << lane) - 1u;
         const int g0 = gt + __popc(mg & below), e0 = eq + __popc(me & below);
@@ -256,54 +464,101 @@ __global__ void __launch_bounds__(kSelThr) kv4_select_kernel(const Kv4EvictParam
     }
 }
 
-// The kept positions' codes, scales and mass, moved to positions 0, 1, ... of the destination row.
+// The kept positions' codes, scales and mass, moved to positions 0, 1, ... of the destination row: four lanes
+// a position (as above), kMove positions of a lane in flight.  A programmatic dependent of the selection.
+constexpr int kMove = 4;
+
+template <int D, int G>
 __global__ void __launch_bounds__(kThr) kv4_gather_kernel(const Kv4EvictParams p) {
-    const int h = blockIdx.y, b = blockIdx.z;
-    const int d = p.src.d, ng = d / p.src.g, units = d / 32;       // 16-byte units of a row of codes
+    constexpr int NG = D / G;
+    using Piece = typename std::conditional<D == 128, uint4, uint2>::type;
+    const int h = blockIdx.y, b = blockIdx.z, l = threadIdx.x & 3;
     const int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
+    pdl_wait();
     const int total = p.new_lengths[b];
-    if (total == 0) return;
+    const int j0 = blockIdx.x * (kThr / 4 * kMove) + threadIdx.x / 4;
+    if (j0 >= total) return;
     const size_t srow = (size_t(p.src_ids[b]) * p.src.nkv + h) * p.src.S;
     const size_t drow = (size_t(p.dst_ids[b]) * p.src.nkv + h) * p.dst.S;
-    for (int j = blockIdx.x * kThr + threadIdx.x; j < total; j += gridDim.x * kThr) {
-        const size_t s = srow + kept[j], t = drow + j;
-        const uint4* ksrc = reinterpret_cast<const uint4*>(p.src.kc + s * (d / 2));
-        const uint4* vsrc = reinterpret_cast<const uint4*>(p.src.vc + s * (d / 2));
-        uint4* kdst = reinterpret_cast<uint4*>(p.dst.kc + t * (d / 2));
-        uint4* vdst = reinterpret_cast<uint4*>(p.dst.vc + t * (d / 2));
-        for (int u = 0; u < units; ++u) {
-            kdst[u] = ksrc[u];
-            vdst[u] = vsrc[u];
-        }
-        for (int u = 0; u < ng; ++u) {
-            p.dst.ks[t * ng + u] = p.src.ks[s * ng + u];
-            p.dst.vs[t * ng + u] = p.src.vs[s * ng + u];
-        }
-        if (p.dst_mass) p.dst_mass[t] = p.mass[s];
+    size_t from[kMove];
+    Piece k[kMove], v[kMove];
+    uint32_t kw[kMove], vw[kMove];
+    float m[kMove];
+#pragma unroll
+    for (int i = 0; i < kMove; ++i) {
+        const int j = j0 + i * (kThr / 4);
+        from[i] = srow + kept[j < total ? j : j0];
     }
+#pragma unroll
+    for (int i = 0; i < kMove; ++i) {
+        k[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.kc + from[i] * (D / 2)) + l);
+        v[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.vc + from[i] * (D / 2)) + l);
+        kw[i] = l < NG ? __ldcs(p.src.ks + from[i] * NG + l) : 0u;
+        vw[i] = l < NG ? __ldcs(p.src.vs + from[i] * NG + l) : 0u;
+        m[i] = l == 0 ? p.mass[from[i]] : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < kMove; ++i) {
+        const int j = j0 + i * (kThr / 4);
+        if (j >= total) return;
+        const size_t to = drow + j;
+        reinterpret_cast<Piece*>(p.dst.kc + to * (D / 2))[l] = k[i];
+        reinterpret_cast<Piece*>(p.dst.vc + to * (D / 2))[l] = v[i];
+        if (l < NG) {
+            p.dst.ks[to * NG + l] = kw[i];
+            p.dst.vs[to * NG + l] = vw[i];
+        }
+        if (l == 0 && p.dst_mass) p.dst_mass[to] = m[i];
+    }
+}
+
+template <int D, int G>
+const void* write_fn(int which) {
+    if (which == 0) return (const void*)kv4_append_kernel<D, G>;
+    if (which == 3) return (const void*)kv4_gather_kernel<D, G>;
+    return which == 1 ? (const void*)kv4_convert_kernel<D, G, false> : (const void*)kv4_convert_kernel<D, G, true>;
+}
+const void* write_fn(int d, int g, int which) {
+    if (d == 64) return g == 32 ? write_fn<64, 32>(which) : write_fn<64, 64>(which);
+    return g == 32 ? write_fn<128, 32>(which) : (g == 64 ? write_fn<128, 64>(which) : write_fn<128, 128>(which));
 }
 
 }  // namespace
 
 cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st) {
-    kv4_append_kernel<<<dim3(p.T, p.B), kThr, 0, st>>>(p);
-    return cudaGetLastError();
+    void* args[] = {const_cast<Kv4AppendParams*>(&p)};
+    return cudaLaunchKernel(write_fn(p.c.d, p.c.g, 0), dim3(p.T, p.B), dim3(kThr), args, 0, st);
 }
 
 cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st) {
-    if (to_bf16)
-        kv4_convert_kernel<true><<<dim3(p.T, p.B), kThr, 0, st>>>(p);
-    else
-        kv4_convert_kernel<false><<<dim3(p.T, p.B), kThr, 0, st>>>(p);
-    return cudaGetLastError();
+    void* args[] = {const_cast<Kv4ConvertParams*>(&p)};
+    return cudaLaunchKernel(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B),
+                            dim3(kThr), args, 0, st);
+}
+
+cudaError_t kv4_set_attributes() {
+    return cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st) {
-    kv4_select_kernel<<<dim3(p.src.nkv, p.B), kSelThr, 0, st>>>(p);
-    cudaError_t e = cudaGetLastError();
+    Kv4EvictParams q = p;
+    void* args[] = {&q};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.src.nkv, p.B);
+    cfg.blockDim = dim3(kSelThr);
+    cfg.dynamicSmemBytes = size_t(p.src.S < kSelCache ? p.src.S : kSelCache) * 4;
+    cfg.stream = st;
+    cudaError_t e = cudaLaunchKernelExC(&cfg, (const void*)kv4_select_kernel, args);
     if (e != cudaSuccess) return e;
-    kv4_gather_kernel<<<dim3((p.keep + kThr - 1) / kThr, p.src.nkv, p.B), kThr, 0, st>>>(p);
-    return cudaGetLastError();
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3((p.keep + kThr / 4 * kMove - 1) / (kThr / 4 * kMove), p.src.nkv, p.B);
+    cfg.blockDim = dim3(kThr);
+    cfg.dynamicSmemBytes = 0;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelExC(&cfg, write_fn(p.src.d, p.src.g, 3), args);
 }
 
 }  // namespace kmr

@@ -14,6 +14,7 @@
 namespace kmr {
 
 constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at the others for clashes)
+constexpr int kKv4MaxHeads = 1024;       // KV heads
 constexpr int kKv4MaxRep = 8;            // query heads per KV head
 constexpr int kKv4MaxSplits = 76;        // of a row: with 8 KV heads, four CTAs for each of 152 SMs
 constexpr int kKv4MinChunk = 64;         // positions per split, at least
@@ -26,54 +27,8 @@ struct Kv4View {
     int slots, nkv, S, d, g;
 };
 
-// 16-bit unit (4 codes) of dims 4 q .. 4 q + 3 within a row.
-__host__ __device__ __forceinline__ int kv4_unit(int q, int nb, bool key) {
-    const int b = q >> 3, r = q & 7;
-    return key ? ((r >> 1) * nb + b) * 2 + (r & 1) : r * nb + b;
-}
 __device__ __forceinline__ float kv4_s(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 __device__ __forceinline__ float kv4_z(uint32_t w) { return __uint_as_float(w << 16); }
-
-// Four dims per lane of a group spread over g / 4 neighbouring lanes: the group's word (z, s) and
-// the lane's four codes.  lo, hi = the group's extremes; s = bf16((hi - lo) / 15), 0 below 2^-126
-// (its reciprocal would leave the normal range); z = bf16(lo); c = rint((x - z) / s) within 0..15,
-// 0 where s is 0.  The quotient is the correctly rounded one (Markstein 1990: with r = rn(1 / s),
-// q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value half-way between two codes is seen
-// as half-way and goes to the even one.  A group that holds a NaN or an infinity, or whose range
-// overflows, stores s = 0 and z = NaN: it reads back as NaN.
-__device__ __forceinline__ uint32_t kv4_quantize(const float (&x)[4], int lanes, uint32_t& word) {
-    float lo = fminf(fminf(x[0], x[1]), fminf(x[2], x[3]));
-    float hi = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-    // a sum that is not finite marks the group: x - x is 0 for a finite x, NaN otherwise
-    float odd = __fadd_rn(__fadd_rn(__fsub_rn(x[0], x[0]), __fsub_rn(x[1], x[1])),
-                          __fadd_rn(__fsub_rn(x[2], x[2]), __fsub_rn(x[3], x[3])));
-    uint32_t bad = odd != 0.f ? 1u : 0u;
-    for (int o = 1; o < lanes; o <<= 1) {
-        lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-        bad |= __shfl_xor_sync(0xffffffffu, bad, o);
-    }
-    uint32_t sb = f32_to_bf16_rn(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
-    if (sb < 0x0080u) sb = 0u;                       // below 2^-126
-    uint32_t zb = f32_to_bf16_rn(lo);
-    if (bad || sb >= 0x7F80u || (zb & 0x7F80u) == 0x7F80u) {
-        sb = 0u;
-        zb = 0x7FC0u;
-    }
-    word = zb | (sb << 16);
-    const float s = __uint_as_float(sb << 16), z = __uint_as_float(zb << 16);
-    if (sb == 0u) return 0u;
-    const float r = __frcp_rn(s);
-    uint32_t c = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float a = __fsub_rn(x[e], z);
-        const float q0 = __fmul_rn(a, r);
-        const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
-        c |= uint32_t(fminf(fmaxf(rintf(q), 0.f), 15.f)) << (4 * e);
-    }
-    return c;
-}
 
 struct Kv4AppendParams {
     Kv4View c;
@@ -92,6 +47,7 @@ struct Kv4AppendParams {
     int* err;
     unsigned long long turn[64];         // frequency i in turns per position, as a 64-bit fraction
 };
+cudaError_t kv4_set_attributes();
 cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st);
 
 struct Kv4ConvertParams {

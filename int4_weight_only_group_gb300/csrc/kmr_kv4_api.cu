@@ -14,7 +14,7 @@ int view_of(const kmr_kv4_cache* c, Kv4View* v) {
     if (!c || !c->k_codes || !c->v_codes || !c->k_sz || !c->v_sz) return KMR_ERR_INVALID_ARG;
     if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_sz) || !aligned16(c->v_sz))
         return KMR_ERR_INVALID_ARG;
-    if (c->slots < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 65535) return KMR_ERR_SHAPE;
+    if (c->slots < 1 || c->n_kv_heads < 1 || c->n_kv_heads > kKv4MaxHeads) return KMR_ERR_SHAPE;
     if (c->max_len < 16 || c->max_len % 16 || c->max_len > (1 << 28)) return KMR_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return KMR_ERR_SHAPE;
     if ((c->group != 32 && c->group != 64 && c->group != 128) || c->group > c->head_dim) return KMR_ERR_SHAPE;
@@ -169,6 +169,7 @@ extern "C" int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst,
     // one cache has one shape, and one mass only together with it
     if (p.same && (p.src.slots != p.dst.slots || p.src.S != p.dst.S)) return KMR_ERR_SHAPE;
     if (!p.same && mass == dst_mass) return KMR_ERR_INVALID_ARG;
+    if (ensure_kernel_attributes() != cudaSuccess) return KMR_ERR_CUDA;
     if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.src_ids = src_slot_ids;
     p.dst_ids = dst_slot_ids;

@@ -27,7 +27,7 @@ BAD_CACHES = [(dict(k_codes=None), kmr.KMR_ERR_INVALID_ARG), (dict(v_codes=None)
               (dict(k_sz=None), kmr.KMR_ERR_INVALID_ARG), (dict(v_sz=None), kmr.KMR_ERR_INVALID_ARG),
               (dict(k_codes=24), kmr.KMR_ERR_INVALID_ARG), (dict(v_sz=4), kmr.KMR_ERR_INVALID_ARG),
               (dict(slots=0), kmr.KMR_ERR_SHAPE), (dict(n_kv_heads=0), kmr.KMR_ERR_SHAPE),
-              (dict(n_kv_heads=65536), kmr.KMR_ERR_SHAPE), (dict(max_len=0), kmr.KMR_ERR_SHAPE),
+              (dict(n_kv_heads=1025), kmr.KMR_ERR_SHAPE), (dict(max_len=0), kmr.KMR_ERR_SHAPE),
               (dict(max_len=40), kmr.KMR_ERR_SHAPE), (dict(max_len=(1 << 28) + 16), kmr.KMR_ERR_SHAPE),
               (dict(head_dim=96), kmr.KMR_ERR_SHAPE), (dict(group=16), kmr.KMR_ERR_SHAPE),
               (dict(head_dim=64, group=128), kmr.KMR_ERR_SHAPE)]
