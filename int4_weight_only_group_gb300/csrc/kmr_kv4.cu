@@ -371,7 +371,7 @@ __device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
 // histogram each, searched from the top by a scan over the CTA), then one ordered pass writes the kept
 // indices in ascending order.  The keys are formed once and kept in shared memory.  What bounds it is the chain
 // of some fifteen barriers: a row of 8192 masses is 32 KB.
-__global__ void __launch_bounds__(kSelThr) kv4_select_kernel(const Kv4EvictParams p) {
+__global__ void __launch_bounds__(kSelThr, 1) kv4_select_kernel(const Kv4EvictParams p) {
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kSelBins];
     __shared__ int wsum[2][32];

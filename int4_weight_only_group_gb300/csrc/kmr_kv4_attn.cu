@@ -24,6 +24,11 @@
 //     row's output is small against the codes' offset, and the sum of the offset codes would lose its bits (at
 //     131072 positions an error of 5e-6 with c - 8 throughout).  The bases add per group in fp32.  The products are scaled by a power of two that follows the
 //     largest s seen, so that any bf16 scale fits fp16.
+// Few query heads (rep <= 2) leave half of the columns empty.  With two groups or more the columns' halves then
+// stand for the halves of the head's dims: column 4 f + 2 h + part is query head h in half f.  A step of the scores
+// has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
+// dims of either half in its upper and lower rows.  The products are as many, but each lane folds, weighs and
+// splits for its half's groups only: 481 -> @@ instructions per tile of 16 positions at d = 128, g = 32.
 #include <cuda_fp16.h>
 #include <math.h>
 
@@ -106,24 +111,28 @@ struct SplitSmem {
     static constexpr int total(int rep) { return 128 + query(rep) + (kRing > merge(rep) ? kRing : merge(rep)); }
 };
 
-// Query fragments of the scores' B operand, the queries' group sums and the scores' factor (all of the KV head's
-// query heads; heads past rep are zero).
-template <int D, int G, int NT>
-__device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int lane,
-                                                uint32_t (&qf)[NT][D / 32][4], float (&qsum)[NT][D / G],
-                                                float (&fac)[NT]) {
-    constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+// Query head, half of the dims and part (0 high, 1 low) of an n-tile's column.
+template <bool PAIR>
+__device__ __forceinline__ int column_head(int g) { return PAIR ? (g >> 1) & 1 : g >> 1; }
+template <bool PAIR>
+__device__ __forceinline__ int column_half(int g) { return PAIR ? g >> 2 : 0; }
+
+// Query fragments of the scores' B operand (this lane's column), and the queries' group sums and the scores' factor of
+// the head and half whose accumulators the lane holds (columns 2 t, 2 t + 1).  Heads past rep are zero.
+template <int D, int G, int NT, bool PAIR>
+__device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int lane, uint32_t* out) {
+    constexpr int NB = D / 32 / (PAIR ? 2 : 1), NG = D / G / (PAIR ? 2 : 1), BPG = G / 32;     // of one half
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int hq = 4 * n + (g >> 1);
+        const int hq = 4 * n + column_head<PAIR>(g);
         float x[NB][8], mx = 0.f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
             if (hq < rep) {
-                const float4* src =
-                    reinterpret_cast<const float4*>(p.q + (size_t(b) * p.nq + h * rep + hq) * D + 32 * k + 8 * t);
+                const float4* src = reinterpret_cast<const float4*>(p.q + (size_t(b) * p.nq + h * rep + hq) * D +
+                                                                    32 * (k + NB * column_half<PAIR>(g)) + 8 * t);
                 u = src[0];
                 v = src[1];
             }
@@ -134,6 +143,7 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
         }
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        if (PAIR) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
         // largest |q| sigma in [2^13, 2^14): sigma = 2^(13 - e), held within the normal range
         int e = int(__float_as_uint(mx) >> 23) - 127;
         e = max(e, -113);
@@ -142,6 +152,7 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
 #pragma unroll
         for (int i = 0; i < NG; ++i) gs[i] = 0.f;
         const uint32_t mask = (g & 1) ? 0xFFFFE000u : 0u;
+        uint32_t* at = out + n * (4 * NB + NG + 1) * 32 + lane;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             float y[8];
@@ -151,26 +162,29 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
                 y[i] = part_of(x[k][i] * sig, mask);
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[n][k][i] = pack_f16_rz(y[i], y[i + 4]);
+            for (int i = 0; i < 4; ++i) at[(4 * k + i) * 32] = pack_f16_rz(y[i], y[i + 4]);
         }
         const float base2 = p.scale * kLog2e;
         const float f = base2 * 0x1p-13f * exp2f(float(e));               // base2 / sigma
-        fac[n] = __shfl_sync(0xffffffffu, f, 8 * t);
+        // columns 2 t, 2 t + 1 are lane 8 t's
+        at[(4 * NB + NG) * 32] = __float_as_uint(__shfl_sync(0xffffffffu, f, 8 * t));
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             float v = gs[i];
             v += __shfl_xor_sync(0xffffffffu, v, 1);
             v += __shfl_xor_sync(0xffffffffu, v, 2);
-            qsum[n][i] = __shfl_sync(0xffffffffu, v * base2, 8 * t);
+            at[(4 * NB + i) * 32] = __float_as_uint(__shfl_sync(0xffffffffu, v * base2, 8 * t));
         }
     }
 }
 
-// NT: n-tiles of 4 query heads.
-template <int D, int G, int NT>
+// NT: n-tiles of 4 query heads; PAIR: one n-tile of 2 heads whose halves' groups are kept apart (see above).
+template <int D, int G, int NT, bool PAIR>
 __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const Kv4AttnParams p) {
     using M = SplitSmem<D, G>;
     constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+    constexpr int HB = PAIR ? NB / 2 : NB, HG = PAIR ? NG / 2 : NG;  // blocks and groups of a lane's half
+    static_assert(!PAIR || (NT == 1 && NG >= 2), "two halves of whole groups");
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);              // [kStages]
     uint64_t* empty = full + kStages;                                // [kStages]
@@ -216,39 +230,34 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     if (warp == 0)
         for (int i = 0; i < nst && i < kStages; ++i) issue(i);
 
-    // ---- the query, prepared by warp 1 for all: column g of n-tile n is head 4 n + g / 2, its high part (g even)
-    // or low part.  fac and qsum belong to head 4 n + t.
-    uint32_t qf[NT][NB][4];
-    float qsum[NT][NG], fac[NT];
+    // ---- the query, prepared by warp 1 for all
     uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
-    if (warp == 1) {
-        query_fragments<D, G, NT>(p, b, h, rep, lane, qf, qsum, fac);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            uint32_t* at = qsh + n * M::kQuery * 32 + lane;
-#pragma unroll
-            for (int k = 0; k < NB; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) at[(4 * k + i) * 32] = qf[n][k][i];
-#pragma unroll
-            for (int i = 0; i < NG; ++i) at[(4 * NB + i) * 32] = __float_as_uint(qsum[n][i]);
-            at[(4 * NB + NG) * 32] = __float_as_uint(fac[n]);
-        }
-    }
+    if (warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
     __syncthreads();
+    const int cgh = column_half<PAIR>(g), cth = PAIR ? t >> 1 : 0;   // halves of the lane's column and accumulators
+    uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
+    float qsum[NT][HG], fac[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const uint32_t* at = qsh + n * M::kQuery * 32 + lane;
+        const uint32_t* at = qsh + n * (4 * HB + HG + 1) * 32 + lane;
 #pragma unroll
-        for (int k = 0; k < NB; ++k)
+        for (int k = 0; k < HB; ++k)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) qf[n][k][i] = at[(4 * k + i) * 32];
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t v = at[(4 * k + i) * 32];
+                if constexpr (PAIR) {
+                    qf[n][k][i] = cgh ? 0u : v;
+                    qf[n][k + HB][i] = cgh ? v : 0u;
+                } else {
+                    qf[n][k][i] = v;
+                }
+            }
 #pragma unroll
-        for (int i = 0; i < NG; ++i) qsum[n][i] = __uint_as_float(at[(4 * NB + i) * 32]);
-        fac[n] = __uint_as_float(at[(4 * NB + NG) * 32]);
+        for (int i = 0; i < HG; ++i) qsum[n][i] = __uint_as_float(at[(4 * HB + i) * 32]);
+        fac[n] = __uint_as_float(at[(4 * HB + HG) * 32]);
     }
 
-    float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][NG];
+    float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][HG];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         m[n] = -INFINITY;
@@ -256,7 +265,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
         for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
 #pragma unroll
-        for (int i = 0; i < NG; ++i) zo[n][i] = 0.f;
+        for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
     }
     int eref = 5;                                 // exponent that the output accumulators are scaled by
     const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
@@ -270,16 +279,16 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             const bool whole = base + 16 <= t1;
             const int i0 = warp * 16;
             // ---- scores of positions g and g + 8 for head 4 n + t
-            uint32_t k0[NB], k1[NB], w0[NG], w1[NG];
+            uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
             lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
             lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
-            lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG), w0);
-            lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG), w1);
+            lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
+            lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
             float sc[NT][2], zc[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = zc[n][0] = zc[n][1] = 0.f;
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
+            for (int gr = 0; gr < HG; ++gr) {
                 float acc[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
@@ -289,10 +298,18 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                     uint32_t x[4], y[4];
                     unpack_codes<0>(k0[k], x);
                     unpack_codes<0>(k1[k], y);
+                    if constexpr (PAIR) {
+                        uint32_t u[4], v[4];
+                        unpack_codes<0>(k0[k + HB], u);
+                        unpack_codes<0>(k1[k + HB], v);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
-                        mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                        for (int i = 0; i < 4; ++i) mma_f16(acc[0], x[i], y[i], u[i], v[i], qf[0][k][i], qf[0][k + HB][i]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
+                            mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                        }
                     }
                 }
 #pragma unroll
@@ -306,17 +323,17 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             // ---- V words: of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights), and the
             // largest scale of the tile
             const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
-            uint32_t v0[NG], v1[NG], vw[4][NG], mine[(NG + 1) / 2];
-            lds_words(words + g * (4 * NG), v0);
-            lds_words(words + (g + 8) * (4 * NG), v1);
+            uint32_t v0[HG], v1[HG], vw[4][HG], mine[(NG + 1) / 2];
+            lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
+            lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG), vw[i]);
+            for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
             const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
             lds_words(words + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
             if (!whole) {
                 // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
+                for (int gr = 0; gr < HG; ++gr) {
                     if (base + g >= t1) v0[gr] = 0u;
                     if (base + g + 8 >= t1) v1[gr] = 0u;
 #pragma unroll
@@ -339,11 +356,16 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             for (int n = 0; n < NT; ++n) {
                 sc[n][0] = __fmaf_rn(sc[n][0], fac[n], zc[n][0]);
                 sc[n][1] = __fmaf_rn(sc[n][1], fac[n], zc[n][1]);
+                if constexpr (PAIR) {
+                    // the other half's part is two lanes away; both lanes add the same two numbers
+                    sc[n][0] += __shfl_xor_sync(0xffffffffu, sc[n][0], 2);
+                    sc[n][1] += __shfl_xor_sync(0xffffffffu, sc[n][1], 2);
+                }
                 if (!whole) {
                     if (base + g >= t1) sc[n][0] = -INFINITY;
                     if (base + g + 8 >= t1) sc[n][1] = -INFINITY;
                 }
-                if (sc_out && 4 * n + t < rep) {
+                if (sc_out && 4 * n + t < rep) {                // (PAIR: rep <= 2, the lanes of half 0)
                     float* dst = sc_out + size_t(4 * n + t) * p.c.S + base + g;
                     if (whole || base + g < t1) dst[0] = sc[n][0];
                     if (whole || base + g + 8 < t1) dst[8] = sc[n][1];
@@ -371,7 +393,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
                         for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
 #pragma unroll
-                    for (int i = 0; i < NG; ++i) zo[n][i] *= cf;
+                    for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
                 }
             }
             // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of head
@@ -384,24 +406,30 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 const float p0 = exp2_approx(__fsub_rn(sc[n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[n][1], mm));
                 l[n] += p0 + p1;
 #pragma unroll
-                for (int gr = 0; gr < NG; ++gr) {
+                for (int gr = 0; gr < HG; ++gr) {
                     zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
                     zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
                 }
                 const float u0 = p0 * unit, u1 = p1 * unit;
-                const int src = 4 * t + (g >> 1);
+                const int src = 4 * t + column_head<PAIR>(g);
                 w[n][0] = __shfl_sync(0xffffffffu, u0, src);
                 w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
                 w[n][2] = __shfl_sync(0xffffffffu, u1, src);
                 w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
             }
-            // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3)
+            // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j of half
+            // 0 in rows g, of half 1 in rows g + 8
             uint32_t vc[4][NB / 2];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
+            auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
+                const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
+                unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+            };
 #pragma unroll
-            for (int gr = 0; gr < NG; ++gr) {
+            for (int gr = 0; gr < HG; ++gr) {
                 uint32_t wf[NT][2];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
@@ -414,14 +442,19 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
                 for (int kb = 0; kb < BPG; ++kb) {
                     const int k = gr * BPG + kb;
-                    const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
                     uint32_t x[4], y[4];
-                    unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
-                    unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+                    unpack_block(k, x, y);
+                    if constexpr (PAIR) {
+                        uint32_t u[4], v[4];
+                        unpack_block(k + HB, u, v);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
-                        mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                        for (int i = 0; i < 4; ++i) mma_f16(o[0][4 * k + i], x[i], u[i], y[i], v[i], wf[0][0], wf[0][1]);
+                    } else {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
+                            mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                        }
                     }
                 }
             }
@@ -444,32 +477,41 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int hq = 4 * n + t;
+        const int hq = PAIR ? t & 1 : 4 * n + t;
         float lt = l[n];
         lt += __shfl_xor_sync(0xffffffffu, lt, 4);
         lt += __shfl_xor_sync(0xffffffffu, lt, 8);
         lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-        float zt[NG];
+        float zt[HG];
 #pragma unroll
-        for (int gr = 0; gr < NG; ++gr) {
+        for (int gr = 0; gr < HG; ++gr) {
             float v = zo[n][gr];
             v += __shfl_xor_sync(0xffffffffu, v, 4);
             v += __shfl_xor_sync(0xffffffffu, v, 8);
             zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
         }
         if (hq < rep) {
-            if (g == 0) {
+            if (g == 0 && cth == 0) {
                 wml[(warp * rep + hq) * 2] = m[n];
                 wml[(warp * rep + hq) * 2 + 1] = lt;
             }
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
+            for (int k = 0; k < HB; ++k) {
                 const float z = zt[k / BPG];
-                const float(&a)[4] = o[n][2 * k];
-                const float(&c)[4] = o[n][2 * k + 1];
-                const float4 v = make_float4(__fmaf_rn(a[0] + a[1], un, z), __fmaf_rn(a[2] + a[3], un, z),
-                                             __fmaf_rn(c[0] + c[1], un, z), __fmaf_rn(c[2] + c[3], un, z));
-                *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * k + 4 * g) = v;
+                float v[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if constexpr (PAIR) {
+                        const float(&a)[4] = o[n][4 * k + i];
+                        v[i] = cth ? a[2] + a[3] : a[0] + a[1];
+                    } else {
+                        const float(&a)[4] = o[n][2 * k + i / 2];
+                        v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
+                    }
+                    v[i] = __fmaf_rn(v[i], un, z);
+                }
+                *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
+                    make_float4(v[0], v[1], v[2], v[3]);
             }
         }
     }
@@ -630,7 +672,9 @@ static_assert(kMergeThr / 32 >= kKv4MaxRep, "a warp per query head");
 
 template <int D, int G>
 const void* split_fn(int rep) {
-    return rep <= 4 ? (const void*)kv4_split_kernel<D, G, 1> : (const void*)kv4_split_kernel<D, G, 2>;
+    constexpr bool kPair = G < D;                // two groups or more
+    if (kPair && rep <= 2) return (const void*)kv4_split_kernel<D, G, 1, kPair>;
+    return rep <= 4 ? (const void*)kv4_split_kernel<D, G, 1, false> : (const void*)kv4_split_kernel<D, G, 2, false>;
 }
 struct SplitVariant {
     const void* fn;
@@ -661,7 +705,7 @@ size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit) {
 cudaError_t kv4_attn_set_attributes() {
     const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
     for (const auto& sh : shapes)
-        for (int rep : {4, 8}) {
+        for (int rep : {2, 4, 8}) {
             const SplitVariant v = split_variant(sh[0], sh[1], rep);
             cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
             if (e != cudaSuccess) return e;
