@@ -153,8 +153,13 @@ def lib() -> ctypes.CDLL:
 
 # ------------------------------------------------------------------ marshalling
 def _ptr(a) -> Optional[int]:
-    if a is None:
-        return None
+    if a is None or type(a) is int:
+        return a
+    try:                                 # a contiguous torch.Tensor, at the least cost
+        if a.is_contiguous():
+            return a.data_ptr()
+    except AttributeError:
+        pass
     if isinstance(a, int):
         return a
     if hasattr(a, "data_ptr"):           # torch.Tensor

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
     constexpr int NB = D / 32, NG = D / G;
     __shared__ __align__(16) float cs[D / 2], sn[D / 2];
     const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    pdl_wait();
     const int nkv = p.c.nkv;
     const int n = p.n_tokens ? p.n_tokens[b] : p.T;
     const int slot = p.slot_ids[b], c0 = p.cpos[b];
@@ -265,6 +266,7 @@ template <int D, int G, bool TO16>
 __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParams p) {
     constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
     const int b = blockIdx.z, tid = threadIdx.x, l = tid & 3;
+    pdl_wait();
     const int nkv = p.c.nkv, n = p.lengths[b];
     const int slot = p.slot_ids[b], s0 = p.start[b], slot16 = p.slot16[b], s16 = p.start16[b];
     const bool bad_n = n < 0 || n > p.T;
@@ -377,6 +379,7 @@ __global__ void __launch_bounds__(kSelThr, 1) kv4_select_kernel(const Kv4EvictPa
     __shared__ int wsum[2][32];
     __shared__ int found[2];
     const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_wait();
     pdl_launch_dependents();
     const int bad = evict_row_error(p, b);
     int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
@@ -525,15 +528,30 @@ const void* write_fn(int d, int g, int which) {
 
 }  // namespace
 
+// Every kernel of the cache is launched as a programmatic dependent of whatever ran before it on the stream, and
+// waits for that at its start: the launch itself overlaps the end of the previous kernel.
+static cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void* params, cudaStream_t st) {
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    void* args[] = {params};
+    return cudaLaunchKernelExC(&cfg, fn, args);
+}
+
 cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st) {
-    void* args[] = {const_cast<Kv4AppendParams*>(&p)};
-    return cudaLaunchKernel(write_fn(p.c.d, p.c.g, 0), dim3(p.T, p.B), dim3(kThr), args, 0, st);
+    return launch(write_fn(p.c.d, p.c.g, 0), dim3(p.T, p.B), kThr, 0, const_cast<Kv4AppendParams*>(&p), st);
 }
 
 cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st) {
-    void* args[] = {const_cast<Kv4ConvertParams*>(&p)};
-    return cudaLaunchKernel(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B),
-                            dim3(kThr), args, 0, st);
+    return launch(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B), kThr, 0,
+                  const_cast<Kv4ConvertParams*>(&p), st);
 }
 
 cudaError_t kv4_set_attributes() {
@@ -542,23 +560,11 @@ cudaError_t kv4_set_attributes() {
 
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st) {
     Kv4EvictParams q = p;
-    void* args[] = {&q};
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.src.nkv, p.B);
-    cfg.blockDim = dim3(kSelThr);
-    cfg.dynamicSmemBytes = size_t(p.src.S < kSelCache ? p.src.S : kSelCache) * 4;
-    cfg.stream = st;
-    cudaError_t e = cudaLaunchKernelExC(&cfg, (const void*)kv4_select_kernel, args);
+    const cudaError_t e = launch((const void*)kv4_select_kernel, dim3(p.src.nkv, p.B), kSelThr,
+                                 size_t(p.src.S < kSelCache ? p.src.S : kSelCache) * 4, &q, st);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3((p.keep + kThr / 4 * kMove - 1) / (kThr / 4 * kMove), p.src.nkv, p.B);
-    cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = 0;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelExC(&cfg, write_fn(p.src.d, p.src.g, 3), args);
+    return launch(write_fn(p.src.d, p.src.g, 3), dim3((p.keep + kThr / 4 * kMove - 1) / (kThr / 4 * kMove), p.src.nkv, p.B),
+                  kThr, 0, &q, st);
 }
 
 }  // namespace kmr

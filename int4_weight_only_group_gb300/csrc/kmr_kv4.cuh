@@ -17,7 +17,9 @@ constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at 
 constexpr int kKv4MaxHeads = 1024;       // KV heads
 constexpr int kKv4MaxRep = 8;            // query heads per KV head
 constexpr int kKv4MaxSplits = 76;        // of a row: with 8 KV heads, four CTAs for each of 152 SMs
-constexpr int kKv4MinChunk = 64;         // positions per split, at least
+constexpr int kKv4ClusterSplits = 8;     // of a row of a short cache: one cluster
+constexpr int kKv4ClusterLen = 4096;     // longest max_len of a short cache
+constexpr int kKv4MinChunk = 128;        // positions per split, at least
 
 struct Kv4View {
     uint8_t* kc;                         // [slots][nkv][S][d / 2]
@@ -76,7 +78,8 @@ struct Kv4AttnParams {
     float* out;                          // [B][nq][d]
     float* part;                         // [B][nkv][nsplit][rep][d + 2]
     float* scores;                       // [B][nkv][rep][S] base-2 scores (mass only)
-    int nsplit;                          // grid.x: the most splits a row of this cache can have
+    int nsplit;                          // the most splits a row of a long cache can have (0: a short cache)
+    int chunk_max;                       // short cache: the longest split
     int* err;
 };
 size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit);
@@ -100,14 +103,20 @@ struct Kv4EvictParams {
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st);
 
 // Positions of a row are cut into splits of `chunk` positions (a multiple of 16), by the row's own length
-// alone, so that a row's result does not depend on the others of the call: 64 for short rows (a tile of 16 for
-// each of a CTA's warps), growing to 256 by 4096 positions, and beyond 76 splits with the length.
+// (and, through the form chosen, by max_len) alone, so that a row's result does not depend on the others of the call.
+// Long caches: 128 for short rows, growing to 256 by 4096 positions, and beyond 76 splits with the length.
 __host__ __device__ __forceinline__ void kv4_split_plan(int L, int& chunk, int& ns) {
     const int grow = (L + 15) >> 4;
     chunk = (L + kKv4MaxSplits - 1) / kKv4MaxSplits;
     if (chunk < kKv4MinChunk) chunk = kKv4MinChunk;
     if (grow > chunk) chunk = grow < 256 ? grow : (chunk < 256 ? 256 : chunk);
     chunk = (chunk + 15) & ~15;
+    ns = (L + chunk - 1) / chunk;
+}
+// Short caches: at most `ranks` splits.
+__host__ __device__ __forceinline__ void kv4_cluster_plan(int L, int ranks, int& chunk, int& ns) {
+    chunk = ((L + ranks - 1) / ranks + 15) & ~15;
+    if (chunk < kKv4MinChunk) chunk = kKv4MinChunk;
     ns = (L + chunk - 1) / chunk;
 }
 

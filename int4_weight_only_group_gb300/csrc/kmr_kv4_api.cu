@@ -121,7 +121,9 @@ extern "C" int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uin
 extern "C" size_t kmr_decode_attn_kv4_workspace_size(const kmr_kv4_cache* cache, int B, int nq, int with_mass) {
     Kv4View v;
     if (view_of(cache, &v) != KMR_OK || B < 1 || B > kKv4MaxRows || !heads_ok(nq, v.nkv)) return 0;
-    return kv4_attn_part_bytes(B, nq, v.d, kv4_attn_splits(v.S)) + (with_mass ? size_t(B) * nq * v.S * 4 : 0);
+    const int ns = kv4_attn_splits(v.S);
+    if (ns == 0) return 16;                       // merged on chip: any buffer will do
+    return kv4_attn_part_bytes(B, nq, v.d, ns) + (with_mass ? size_t(B) * nq * v.S * 4 : 0);
 }
 
 extern "C" int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_t* slot_ids,

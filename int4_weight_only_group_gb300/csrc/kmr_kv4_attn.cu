@@ -2,9 +2,13 @@
 //
 // out = softmax(q K^T scale) V over positions 0..cache_position of the row's slot, and, where a mass
 // is given, mass[slot][head][p] += the sum over the KV head's query heads of position p's weight.
-// Two launches: the splits of every (row, KV head) leave their softmax states (m, l, o) in base 2 in
-// the workspace (and, for the mass, every score); the second, a programmatic dependent of the first, merges the
-// states in split order and turns the scores into weights.  Rows that share a slot add to its mass in row order.
+// A (row, KV head) is cut into splits, whose softmax states (m, l, o) in base 2 merge in split order:
+//   * caches of up to 4096 positions: one launch, the up to 8 splits are a thread-block cluster.  Each pushes its
+//     state into the others' shared memory; after one cluster barrier each merges a slice of the output and
+//     turns the scores of its own positions, kept in shared memory, into mass.  Of rows that share a slot the
+//     first one's cluster takes all in turn, so that the mass gains them in row order.
+//   * longer caches: up to 76 splits leave their states in the workspace (and, for the mass, every score); a
+//     second launch, a programmatic dependent of the first, merges and adds, again in row order.
 //
 // The bound is HBM: 2 (d/2 + 4 d/g) bytes per position and KV head.  At d = 128, g = 32 an SM's share
 // of the bandwidth is about 36 codes per cycle, too many for dequantising and multiplying on the CUDA
@@ -29,18 +33,19 @@
 // has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
 // dims of either half in its upper and lower rows.  The products are as many, but each lane folds, weighs and
 // splits for its half's groups only: 481 -> @@ instructions per tile of 16 positions at d = 128, g = 32.
+#include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
 
 #include "kmr_kv4.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace kmr {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThr = 128, kWarps = 4;
-constexpr int kStagePos = 16 * kWarps;       // positions of a ring stage: a tile of 16 per warp
-constexpr int kStages = 4;
 constexpr int kMergeThr = 256;
 
 __device__ __forceinline__ int kv4_row_error(const Kv4AttnParams& p, int b) {
@@ -82,6 +87,8 @@ __device__ __forceinline__ void unpack_codes(uint32_t w, uint32_t (&c)[4]) {
         w >>= 8;
     }
 }
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ float exp2_approx(float x) {               // 2 ulp; 0 below 2^-126
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -100,16 +107,24 @@ __device__ __forceinline__ void lds_words(const void* p, uint32_t (&w)[N]) {
     }
 }
 
-template <int D, int G>
+// A ring stage holds TT tiles of 16 positions for each warp.
+template <int D, int G, int TT>
 struct SplitSmem {
+    static constexpr int kStagePos = 16 * kWarps * TT, kStages = TT == 2 ? 2 : 4;
     static constexpr int kCodes = kStagePos * D / 2, kWords = kStagePos * (D / G) * 4;
     static constexpr int kStage = 2 * kCodes + 2 * kWords;
     static constexpr int kRing = kStages * kStage;
-    static constexpr int merge(int rep) { return kWarps * rep * (D + 2) * 4; }
+    __host__ __device__ static constexpr int merge(int rep) { return kWarps * rep * (D + 2) * 4; }
     static constexpr int kQuery = 4 * (D / 32) + D / G + 1;         // words of a lane's query per n-tile
-    static constexpr int query(int rep) { return (rep <= 4 ? 1 : 2) * kQuery * 128; }
-    static constexpr int total(int rep) { return 128 + query(rep) + (kRing > merge(rep) ? kRing : merge(rep)); }
+    __host__ __device__ static constexpr int query(int rep) { return (rep <= 4 ? 1 : 2) * kQuery * 128; }
+    __host__ __device__ static constexpr int base(int rep) { return 128 + query(rep) + (kRing > merge(rep) ? kRing : merge(rep)); }
+    // a cluster's additions: the states pushed here (a slice of o from every split; every m and l), the scores
+    __host__ __device__ static constexpr int state(int rep) { return rep * D * 4 + kKv4ClusterSplits * rep * 8; }
+    __host__ __device__ static constexpr int total(int rep, int chunk) { return base(rep) + state(rep) + rep * chunk * 4; }
 };
+
+// Tiles that a warp takes together: two chains of products to interleave where the registers allow it.
+__host__ __device__ constexpr int tiles_of(int NT) { return NT == 1 ? 2 : 1; }
 
 // Query head, half of the dims and part (0 high, 1 low) of an n-tile's column.
 template <bool PAIR>
@@ -179,9 +194,11 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
 }
 
 // NT: n-tiles of 4 query heads; PAIR: one n-tile of 2 heads whose halves' groups are kept apart (see above).
-template <int D, int G, int NT, bool PAIR>
+template <int D, int G, int NT, bool PAIR, bool CL>
 __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const Kv4AttnParams p) {
-    using M = SplitSmem<D, G>;
+    constexpr int TT = tiles_of(NT);
+    using M = SplitSmem<D, G, TT>;
+    constexpr int kStagePos = M::kStagePos, kStages = M::kStages;
     constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
     constexpr int HB = PAIR ? NB / 2 : NB, HG = PAIR ? NG / 2 : NG;  // blocks and groups of a lane's half
     static_assert(!PAIR || (NT == 1 && NG >= 2), "two halves of whole groups");
@@ -189,19 +206,28 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);              // [kStages]
     uint64_t* empty = full + kStages;                                // [kStages]
     uint8_t* ring = smem + 128 + NT * M::kQuery * 128;
-    const int s = blockIdx.x, h = blockIdx.y, b = blockIdx.z;
+    const int s = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    pdl_wait();                                   // nothing of the previous kernel's is read before
     pdl_launch_dependents();
-    if (kv4_row_error(p, b) != KMR_OK) return;
     const int rep = p.nq / p.c.nkv;
-    const int L = p.cpos[b] + 1;
-    int chunk, ns;
-    kv4_split_plan(L, chunk, ns);
-    if (s >= ns) return;
-    const int t0 = s * chunk, t1 = min(L, t0 + chunk);
-    const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
-    const size_t row = (size_t(p.slot_ids[b]) * p.c.nkv + h) * p.c.S;
-
+    const int bad = kv4_row_error(p, b0);
+    if (bad != KMR_OK) {                          // the same for the whole cluster
+        if (CL && s == 0) {
+            if (tid == 0 && h == 0) set_error(p.err, bad);
+            for (int i = tid; i < rep * D; i += kThr) p.out[(size_t(b0) * p.nq + h * rep) * D + i] = 0.f;
+        }
+        return;
+    }
+    const int slot = p.slot_ids[b0];
+    const size_t row = (size_t(slot) * p.c.nkv + h) * p.c.S;
+    if (CL && p.mass) {
+        // rows that share a slot belong to the first one's cluster
+        int before = 0;
+        for (int r = tid; r < b0; r += kThr) before |= p.slot_ids[r] == slot && kv4_row_error(p, r) == KMR_OK;
+        if (__syncthreads_or(before)) return;
+    }
+    if (CL) cluster_arrive();                     // waited for before the first push: the others have started
     if (tid == 0) {
         for (int i = 0; i < kStages; ++i) {
             mbar_init(&full[i], 1);
@@ -210,20 +236,43 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         fence_mbar_init();
     }
     __syncthreads();
+    const int cgh = column_half<PAIR>(g), cth = PAIR ? t >> 1 : 0;   // halves of the lane's column and accumulators
+    const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
+    uint32_t uses = 0;                            // stages filled so far: stage k of them was use k / kStages of its buffer
+    bool first = true;
+
+    for (int b = b0; b < p.B; ++b) {
+    if (CL && b != b0 && (!p.mass || p.slot_ids[b] != slot || kv4_row_error(p, b) != KMR_OK)) continue;
+    const int L = p.cpos[b] + 1;
+    int chunk, ns;
+    if (CL)
+        kv4_cluster_plan(L, int(gridDim.x), chunk, ns);
+    else
+        kv4_split_plan(L, chunk, ns);
+    if (!CL && s >= ns) return;
+    const int t0 = min(s * chunk, L), t1 = min(L, t0 + chunk);       // a cluster's spare splits are empty
+    const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
+    if (CL && !first) {
+        cluster_arrive();
+        cluster_wait();                           // what the last row pushed has been read, and the ring
+        fence_proxy_async_smem();
+    }
+
     // One stage: lanes 0..3 of the calling warp copy K codes, V codes, K words and V words of up to 128
     // positions (rounded up to 16: within the row, whose length is a multiple of 16).
     auto issue = [&](int st) {
-        uint8_t* buf = ring + (st % kStages) * M::kStage;
+        const uint32_t slot_of = (uses + st) % kStages;
+        uint8_t* buf = ring + slot_of * M::kStage;
         const int pa = t0 + st * kStagePos;
         const uint32_t np = uint32_t(min(kStagePos, ((t1 - pa) + 15) & ~15));
-        if (lane == 0) mbar_arrive_expect_tx(&full[st % kStages], np * (D + 8 * NG));
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot_of], np * (D + 8 * NG));
         __syncwarp();
         if (lane < 4) {
             const bool words = lane >= 2, key = !(lane & 1);
             const void* src = words ? static_cast<const void*>((key ? p.c.ks : p.c.vs) + (row + pa) * NG)
                                     : static_cast<const void*>((key ? p.c.kc : p.c.vc) + (row + pa) * (D / 2));
             uint8_t* dst = buf + (words ? 2 * M::kCodes + (key ? 0 : M::kWords) : (key ? 0 : M::kCodes));
-            bulk_g2s(dst, src, np * (words ? 4 * NG : D / 2), &full[st % kStages]);
+            bulk_g2s(dst, src, np * (words ? 4 * NG : D / 2), &full[slot_of]);
         }
         __syncwarp();
     };
@@ -232,9 +281,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 
     // ---- the query, prepared by warp 1 for all
     uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
-    if (warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
+    if (warp == 1 && nst > 0) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
     __syncthreads();
-    const int cgh = column_half<PAIR>(g), cth = PAIR ? t >> 1 : 0;   // halves of the lane's column and accumulators
     uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
     float qsum[NT][HG], fac[NT];
 #pragma unroll
@@ -268,85 +316,99 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
     }
     int eref = 5;                                 // exponent that the output accumulators are scaled by
-    const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
-    float* sc_out = p.scores ? p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S : nullptr;
+    // base-2 scores for the mass: [head][position], in shared memory from the split's first position on
+    float* sc_out = nullptr;
+    size_t sc_ld = p.c.S;
+    if (CL && p.mass) {
+        sc_ld = p.chunk_max;
+        sc_out = reinterpret_cast<float*>(smem + M::base(rep) + M::state(rep)) - t0;
+    } else if (!CL && p.scores) {
+        sc_out = p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S;
+    }
 
     for (int st = 0; st < nst; ++st) {
-        const uint8_t* buf = ring + (st % kStages) * M::kStage;
-        mbar_wait(&full[st % kStages], uint32_t((st / kStages) & 1), p.err);
-        const int base = t0 + st * kStagePos + warp * 16;          // the tile's first position
-        if (base < t1) {
-            const bool whole = base + 16 <= t1;
-            const int i0 = warp * 16;
-            // ---- scores of positions g and g + 8 for head 4 n + t
-            uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
-            lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
-            lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
-            lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
-            lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
-            float sc[NT][2], zc[NT][2];
+        const uint32_t slot_of = (uses + st) % kStages, phase = ((uses + st) / kStages) & 1u;
+        const uint8_t* buf = ring + slot_of * M::kStage;
+        mbar_wait(&full[slot_of], phase, p.err);
+        const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
+        if (base0 < t1) {
+            // a tile is whole but for the row's last ones; one past the end counts for nothing
+            const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
+            // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
+            float sc[TT][NT][2];
+            uint32_t top = 0u;
 #pragma unroll
-            for (int n = 0; n < NT; ++n) sc[n][0] = sc[n][1] = zc[n][0] = zc[n][1] = 0.f;
+            for (int u = 0; u < TT; ++u) {
+                const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
+                lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
+                lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
+                lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
+                lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
+                float zc[NT][2];
 #pragma unroll
-            for (int gr = 0; gr < HG; ++gr) {
-                float acc[NT][4];
+                for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = zc[n][0] = zc[n][1] = 0.f;
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+                for (int gr = 0; gr < HG; ++gr) {
+                    float acc[NT][4];
 #pragma unroll
-                for (int kb = 0; kb < BPG; ++kb) {
-                    const int k = gr * BPG + kb;
-                    uint32_t x[4], y[4];
-                    unpack_codes<0>(k0[k], x);
-                    unpack_codes<0>(k1[k], y);
-                    if constexpr (PAIR) {
-                        uint32_t u[4], v[4];
-                        unpack_codes<0>(k0[k + HB], u);
-                        unpack_codes<0>(k1[k + HB], v);
+                    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f16(acc[0], x[i], y[i], u[i], v[i], qf[0][k][i], qf[0][k + HB][i]);
-                    } else {
+                    for (int kb = 0; kb < BPG; ++kb) {
+                        const int k = gr * BPG + kb;
+                        uint32_t x[4], y[4];
+                        unpack_codes<0>(k0[k], x);
+                        unpack_codes<0>(k1[k], y);
+                        if constexpr (PAIR) {
+                            uint32_t xh[4], yh[4];
+                            unpack_codes<0>(k0[k + HB], xh);
+                            unpack_codes<0>(k1[k + HB], yh);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
-                            mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                            for (int i = 0; i < 4; ++i)
+                                mma_f16(acc[0], x[i], y[i], xh[i], yh[i], qf[0][k][i], qf[0][k + HB][i]);
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
+                                mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                            }
                         }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
+                        sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
+                        zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
+                        zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
                     }
                 }
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    sc[n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[n][0]);
-                    sc[n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[n][1]);
-                    zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
-                    zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
+                    sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
+                    sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
+                    if constexpr (PAIR) {
+                        // the other half's part is two lanes away; both lanes add the same two numbers
+                        sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);
+                        sc[u][n][1] += __shfl_xor_sync(0xffffffffu, sc[u][n][1], 2);
+                    }
+                    if (!whole) {
+                        if (base + g >= t1) sc[u][n][0] = -INFINITY;
+                        if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
+                    }
+                    if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
+                        float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
+                        if (whole || base + g < t1) dst[0] = sc[u][n][0];
+                        if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
+                    }
+                }
+                uint32_t mine[(NG + 1) / 2];
+                const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
+                lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
+                if (whole || base + wpos < t1) {
+                    top = max(top, mine[0] & 0x7FFFFFFFu);
+                    if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
                 }
             }
-            // ---- V words: of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights), and the
-            // largest scale of the tile
-            const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
-            uint32_t v0[HG], v1[HG], vw[4][HG], mine[(NG + 1) / 2];
-            lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
-            lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
-            const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
-            lds_words(words + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
-            if (!whole) {
-                // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
-#pragma unroll
-                for (int gr = 0; gr < HG; ++gr) {
-                    if (base + g >= t1) v0[gr] = 0u;
-                    if (base + g + 8 >= t1) v1[gr] = 0u;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
-                }
-                if (base + wpos >= t1) {
-#pragma unroll
-                    for (int i = 0; i < (NG + 1) / 2; ++i) mine[i] = 0u;
-                }
-            }
-            uint32_t top = mine[0] & 0x7FFFFFFFu;
-            if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
             const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
             // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
             // above, so that most tiles rescale nothing; weights stay below 2^8
@@ -354,23 +416,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             bool up = etop > eref;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                sc[n][0] = __fmaf_rn(sc[n][0], fac[n], zc[n][0]);
-                sc[n][1] = __fmaf_rn(sc[n][1], fac[n], zc[n][1]);
-                if constexpr (PAIR) {
-                    // the other half's part is two lanes away; both lanes add the same two numbers
-                    sc[n][0] += __shfl_xor_sync(0xffffffffu, sc[n][0], 2);
-                    sc[n][1] += __shfl_xor_sync(0xffffffffu, sc[n][1], 2);
-                }
-                if (!whole) {
-                    if (base + g >= t1) sc[n][0] = -INFINITY;
-                    if (base + g + 8 >= t1) sc[n][1] = -INFINITY;
-                }
-                if (sc_out && 4 * n + t < rep) {                // (PAIR: rep <= 2, the lanes of half 0)
-                    float* dst = sc_out + size_t(4 * n + t) * p.c.S + base + g;
-                    if (whole || base + g < t1) dst[0] = sc[n][0];
-                    if (whole || base + g + 8 < t1) dst[8] = sc[n][1];
-                }
-                float c = fmaxf(sc[n][0], sc[n][1]);
+                float c = fmaxf(sc[0][n][0], sc[0][n][1]);
+                if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
@@ -396,79 +443,102 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                     for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
                 }
             }
-            // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of head
-            // 4 n + g / 2 at the lane's four positions
             const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
-            float w[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const float mm = m[n] == -INFINITY ? 0.f : m[n];
-                const float p0 = exp2_approx(__fsub_rn(sc[n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[n][1], mm));
-                l[n] += p0 + p1;
+            for (int u = 0; u < TT; ++u) {
+                const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
+                const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
+                uint32_t v0[HG], v1[HG], vw[4][HG];
+                lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
+                lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
 #pragma unroll
-                for (int gr = 0; gr < HG; ++gr) {
-                    zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
-                    zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
+                for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
+                if (!whole) {
+                    // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
+#pragma unroll
+                    for (int gr = 0; gr < HG; ++gr) {
+                        if (base + g >= t1) v0[gr] = 0u;
+                        if (base + g + 8 >= t1) v1[gr] = 0u;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
+                    }
                 }
-                const float u0 = p0 * unit, u1 = p1 * unit;
-                const int src = 4 * t + column_head<PAIR>(g);
-                w[n][0] = __shfl_sync(0xffffffffu, u0, src);
-                w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
-                w[n][2] = __shfl_sync(0xffffffffu, u1, src);
-                w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
-            }
-            // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j of half
-            // 0 in rows g, of half 1 in rows g + 8
-            uint32_t vc[4][NB / 2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
-            auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
-                const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
-                unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
-                unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
-            };
-#pragma unroll
-            for (int gr = 0; gr < HG; ++gr) {
-                uint32_t wf[NT][2];
+                // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
+                // column's head at the lane's four positions
+                float w[NT][4];
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    float a[4];
+                    const float mm = m[n] == -INFINITY ? 0.f : m[n];
+                    const float p0 = exp2_approx(__fsub_rn(sc[u][n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[u][n][1], mm));
+                    l[n] += p0 + p1;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
-                    wf[n][0] = pack_f16_rz(a[0], a[1]);
-                    wf[n][1] = pack_f16_rz(a[2], a[3]);
+                    for (int gr = 0; gr < HG; ++gr) {
+                        zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
+                        zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
+                    }
+                    const float u0 = p0 * unit, u1 = p1 * unit;
+                    const int src = 4 * t + column_head<PAIR>(g);
+                    w[n][0] = __shfl_sync(0xffffffffu, u0, src);
+                    w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
+                    w[n][2] = __shfl_sync(0xffffffffu, u1, src);
+                    w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
                 }
+                // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
+                // of half 0 in rows g, of half 1 in rows g + 8
+                uint32_t vc[4][NB / 2];
 #pragma unroll
-                for (int kb = 0; kb < BPG; ++kb) {
-                    const int k = gr * BPG + kb;
-                    uint32_t x[4], y[4];
-                    unpack_block(k, x, y);
-                    if constexpr (PAIR) {
-                        uint32_t u[4], v[4];
-                        unpack_block(k + HB, u, v);
+                for (int i = 0; i < 4; ++i)
+                    lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
+                auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
+                    const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                    unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
+                    unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+                };
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) mma_f16(o[0][4 * k + i], x[i], u[i], y[i], v[i], wf[0][0], wf[0][1]);
-                    } else {
+                for (int gr = 0; gr < HG; ++gr) {
+                    uint32_t wf[NT][2];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
-                            mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        float a[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
+                        wf[n][0] = pack_f16_rz(a[0], a[1]);
+                        wf[n][1] = pack_f16_rz(a[2], a[3]);
+                    }
+#pragma unroll
+                    for (int kb = 0; kb < BPG; ++kb) {
+                        const int k = gr * BPG + kb;
+                        uint32_t x[4], y[4];
+                        unpack_block(k, x, y);
+                        if constexpr (PAIR) {
+                            uint32_t xh[4], yh[4];
+                            unpack_block(k + HB, xh, yh);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                mma_f16(o[0][4 * k + i], x[i], xh[i], y[i], yh[i], wf[0][0], wf[0][1]);
+                        } else {
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
+                                mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                            }
                         }
                     }
                 }
             }
         }
+        // the warps take turns to refill the stage once all are done with it
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[st % kStages]);
-        // refill the stage before this one (released by most warps a tile ago); the warps take turns
-        const int nx = st - 1 + kStages;
-        if (st > 0 && nx < nst && warp == (st & (kWarps - 1))) {
-            mbar_wait(&empty[(st - 1) % kStages], uint32_t(((st - 1) / kStages) & 1), p.err);
+        if (lane == 0) mbar_arrive(&empty[slot_of]);
+        if (st + kStages < nst && warp == (st & (kWarps - 1))) {
+            mbar_wait(&empty[slot_of], phase, p.err);
             fence_proxy_async_smem();
-            issue(nx);
+            issue(st + kStages);
         }
     }
+    uses += nst;
     __syncthreads();                              // every copy has landed and been read: the ring is free
 
     // ---- the warp's state: o[head][dim], m, l
@@ -516,27 +586,79 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         }
     }
     __syncthreads();
-    float* part = p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
-    for (int i = tid; i < rep * (D / 4); i += kThr) {
-        const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
-        float mw[kWarps], mx = -INFINITY, den = 0.f;
+    float* part = CL ? nullptr : p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
+    const int ranks = CL ? int(gridDim.x) : 1, slice = rep * D / ranks;         // of the output, for each rank
+    float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [source][slice]
+    float* recv_ml = recv + rep * D;                                             // [source][head][m, l]
+    if (CL && first) cluster_wait();
+    if (s < ns) {
+        for (int i = tid; i < rep * (D / 4); i += kThr) {
+            const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
+            float mw[kWarps], mx = -INFINITY, den = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
-        float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
+            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-            const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
-            const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
-            den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
-            num.x = __fmaf_rn(f, v.x, num.x);
-            num.y = __fmaf_rn(f, v.y, num.y);
-            num.z = __fmaf_rn(f, v.z, num.z);
-            num.w = __fmaf_rn(f, v.w, num.w);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
+                const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
+                den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
+                num.x = __fmaf_rn(f, v.x, num.x);
+                num.y = __fmaf_rn(f, v.y, num.y);
+                num.z = __fmaf_rn(f, v.z, num.z);
+                num.w = __fmaf_rn(f, v.w, num.w);
+            }
+            if constexpr (CL) {
+                const int at = hq * D + dim;
+                float* to = cg::this_cluster().map_shared_rank(recv, at / slice);
+                *reinterpret_cast<float4*>(to + s * slice + at % slice) = num;
+                if (dim == 0)
+                    for (int r = 0; r < ranks; ++r)
+                        *reinterpret_cast<float2*>(cg::this_cluster().map_shared_rank(recv_ml, r) + (s * rep + hq) * 2) =
+                            make_float2(mx, den);
+            } else {
+                float* dst = part + hq * (D + 2);
+                *reinterpret_cast<float2*>(dst + 2 + dim) = make_float2(num.x, num.y);
+                *reinterpret_cast<float2*>(dst + 4 + dim) = make_float2(num.z, num.w);
+                if (dim == 0) *reinterpret_cast<float2*>(dst) = make_float2(mx, den);
+            }
         }
-        float* dst = part + hq * (D + 2);
-        *reinterpret_cast<float2*>(dst + 2 + dim) = make_float2(num.x, num.y);
-        *reinterpret_cast<float2*>(dst + 4 + dim) = make_float2(num.z, num.w);
-        if (dim == 0) *reinterpret_cast<float2*>(dst) = make_float2(mx, den);
+    }
+    if (!CL) return;
+    // ---- every split's state is here: this rank's slice of the output, and its own positions' mass
+    cluster_arrive();
+    cluster_wait();
+    for (int i = tid; i < slice; i += kThr) {
+        const int hq = (s * slice + i) / D;
+        float mx = -INFINITY, num = 0.f, den = 0.f;
+        for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + hq) * 2]);
+        for (int r = 0; r < ns; ++r) {
+            const float mr = recv_ml[(r * rep + hq) * 2];
+            const float f = mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx));
+            den = __fmaf_rn(f, recv_ml[(r * rep + hq) * 2 + 1], den);
+            num = __fmaf_rn(f, recv[r * slice + i], num);
+        }
+        p.out[(size_t(b) * p.nq + h * rep) * D + s * slice + i] = num * __frcp_rn(den);
+    }
+    if (!p.mass) return;
+    __shared__ float hm[kKv4MaxRep], hl[kKv4MaxRep];
+    if (tid < rep) {
+        float mx = -INFINITY, den = 0.f;
+        for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + tid) * 2]);
+        for (int r = 0; r < ns; ++r) {
+            const float mr = recv_ml[(r * rep + tid) * 2];
+            den = __fmaf_rn(mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx)), recv_ml[(r * rep + tid) * 2 + 1], den);
+        }
+        hm[tid] = mx;
+        hl[tid] = __frcp_rn(den);
+    }
+    __syncthreads();
+    for (int i = t0 + tid; i < t1; i += kThr) {
+        float add = 0.f;
+        for (int k = 0; k < rep; ++k) add = __fmaf_rn(exp2_approx(__fsub_rn(sc_out[k * sc_ld + i], hm[k])), hl[k], add);
+        __stcg(p.mass + row + i, __ldcg(p.mass + row + i) + add);    // (another SM's, of the row before)
+    }
+    first = false;
     }
 }
 
@@ -671,32 +793,39 @@ __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParam
 static_assert(kMergeThr / 32 >= kKv4MaxRep, "a warp per query head");
 
 template <int D, int G>
-const void* split_fn(int rep) {
+const void* split_fn(int rep, bool cl) {
     constexpr bool kPair = G < D;                // two groups or more
-    if (kPair && rep <= 2) return (const void*)kv4_split_kernel<D, G, 1, kPair>;
-    return rep <= 4 ? (const void*)kv4_split_kernel<D, G, 1, false> : (const void*)kv4_split_kernel<D, G, 2, false>;
+    if (kPair && rep <= 2)
+        return cl ? (const void*)kv4_split_kernel<D, G, 1, kPair, true> : (const void*)kv4_split_kernel<D, G, 1, kPair, false>;
+    if (rep <= 4)
+        return cl ? (const void*)kv4_split_kernel<D, G, 1, false, true> : (const void*)kv4_split_kernel<D, G, 1, false, false>;
+    return cl ? (const void*)kv4_split_kernel<D, G, 2, false, true> : (const void*)kv4_split_kernel<D, G, 2, false, false>;
 }
 struct SplitVariant {
     const void* fn;
     int smem;
 };
-SplitVariant split_variant(int d, int g, int rep) {
-    if (d == 64) {
-        if (g == 32) return {split_fn<64, 32>(rep), SplitSmem<64, 32>::total(rep)};
-        return {split_fn<64, 64>(rep), SplitSmem<64, 64>::total(rep)};
-    }
-    if (g == 32) return {split_fn<128, 32>(rep), SplitSmem<128, 32>::total(rep)};
-    if (g == 64) return {split_fn<128, 64>(rep), SplitSmem<128, 64>::total(rep)};
-    return {split_fn<128, 128>(rep), SplitSmem<128, 128>::total(rep)};
+// chunk: positions whose scores a cluster's split keeps (0: none, or no cluster)
+template <int D, int G>
+SplitVariant split_variant(int rep, bool cl, int chunk) {
+    using S1 = SplitSmem<D, G, tiles_of(1)>;
+    using S2 = SplitSmem<D, G, tiles_of(2)>;
+    const int smem = rep <= 4 ? (cl ? S1::total(rep, chunk) : S1::base(rep)) : (cl ? S2::total(rep, chunk) : S2::base(rep));
+    return {split_fn<D, G>(rep, cl), smem};
+}
+SplitVariant split_variant(int d, int g, int rep, bool cl, int chunk) {
+    if (d == 64) return g == 32 ? split_variant<64, 32>(rep, cl, chunk) : split_variant<64, 64>(rep, cl, chunk);
+    if (g == 32) return split_variant<128, 32>(rep, cl, chunk);
+    return g == 64 ? split_variant<128, 64>(rep, cl, chunk) : split_variant<128, 128>(rep, cl, chunk);
 }
 
 }  // namespace
 
 int kv4_attn_splits(int S) {
+    if (S <= kKv4ClusterLen) return 0;            // merged inside a cluster
     // a shorter row can have more splits than the longest: 16 at most until the chunk is 256 (4096 positions),
     // then one per 256 up to 76
-    const int small = (S + kKv4MinChunk - 1) / kKv4MinChunk, large = (S + 255) / 256;
-    const int most = small < 16 ? small : (large > 16 ? large : 16);
+    const int large = (S + 255) / 256, most = large > 16 ? large : 16;
     return most < kKv4MaxSplits ? most : kKv4MaxSplits;
 }
 size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit) {
@@ -705,35 +834,51 @@ size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit) {
 cudaError_t kv4_attn_set_attributes() {
     const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
     for (const auto& sh : shapes)
-        for (int rep : {2, 4, 8}) {
-            const SplitVariant v = split_variant(sh[0], sh[1], rep);
-            cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
-            if (e != cudaSuccess) return e;
-            e = cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
-            if (e != cudaSuccess) return e;
-        }
+        for (int rep : {2, 4, 8})
+            for (bool cl : {false, true}) {
+                const SplitVariant v = split_variant(sh[0], sh[1], rep, cl, kKv4ClusterLen / kKv4ClusterSplits);
+                cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
+                if (e != cudaSuccess) return e;
+                e = cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+                if (e != cudaSuccess) return e;
+            }
     return cudaSuccess;
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
-    const SplitVariant v = split_variant(p.c.d, p.c.g, p.nq / p.c.nkv);
     Kv4AttnParams q = p;
     void* args[] = {&q};
+    const int rep = p.nq / p.c.nkv;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.nsplit, p.c.nkv, p.B);
     cfg.blockDim = dim3(kThr);
-    cfg.dynamicSmemBytes = v.smem;
     cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (p.c.S <= kKv4ClusterLen) {
+        int ranks = 1, ns;                        // 1, 2, 4 or 8 splits: as many as the longest row fills
+        while (ranks < kKv4ClusterSplits && ranks * kKv4MinChunk < p.c.S) ranks *= 2;
+        kv4_cluster_plan(p.c.S, ranks, q.chunk_max, ns);
+        const SplitVariant v = split_variant(p.c.d, p.c.g, rep, true, p.mass ? q.chunk_max : 0);
+        cfg.gridDim = dim3(ranks, p.c.nkv, p.B);
+        cfg.dynamicSmemBytes = v.smem;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = ranks;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelExC(&cfg, v.fn, args);
+    }
+    const SplitVariant v = split_variant(p.c.d, p.c.g, rep, false, 0);
+    cfg.gridDim = dim3(p.nsplit, p.c.nkv, p.B);
+    cfg.dynamicSmemBytes = v.smem;
     cudaError_t e = cudaLaunchKernelExC(&cfg, v.fn, args);
     if (e != cudaSuccess) return e;
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(p.nq / p.c.nkv + (p.mass ? (p.c.S + kMassPos - 1) / kMassPos : 0), p.c.nkv, p.B);
+    cfg.gridDim = dim3(rep + (p.mass ? (p.c.S + kMassPos - 1) / kMassPos : 0), p.c.nkv, p.B);
     cfg.blockDim = dim3(kMergeThr);
     cfg.dynamicSmemBytes = 0;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     return cudaLaunchKernelExC(&cfg, (const void*)kv4_merge_kernel, args);
 }
 

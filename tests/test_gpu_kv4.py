@@ -254,10 +254,11 @@ def test_append_bad_and_clashing_rows(torch):
 # ------------------------------------------------------------------ attention
 @pytest.mark.parametrize("d,g", [(128, 32), (128, 64), (128, 128), (64, 32), (64, 64)])
 @pytest.mark.parametrize("nq,nkv", [(16, 8), (4, 4), (8, 2), (3, 1), (5, 1), (16, 2), (7, 1)])
-def test_attention_matches_oracle(torch, d, g, nq, nkv):
+@pytest.mark.parametrize("S", [1104, 4112])                   # splits merged in a cluster, and through the workspace
+def test_attention_matches_oracle(torch, d, g, nq, nkv, S):
     r = np.random.default_rng(d + g + nq)
-    S, slots = 1104, 12
-    L = [1, 2, 15, 16, 17, 127, 128, 129, 600, 1023, 1104]
+    slots = 12
+    L = [1, 2, 15, 16, 17, 127, 128, 129, 600, 1023, S]
     ids = [11, 3, 0, 5, 2, 7, 1, 9, 8, 10, 6]
     fill = [0] * slots
     for s, n in zip(ids, L):
@@ -283,7 +284,7 @@ def test_attention_matches_oracle(torch, d, g, nq, nkv):
         assert np.array_equal(one[0], out[b])
 
 
-@pytest.mark.parametrize("L", [4096, 4097, 8191, 40000])
+@pytest.mark.parametrize("L", [4095, 4096, 4097, 8191, 40000])
 def test_attention_long_rows(torch, L):
     r = np.random.default_rng(L)
     S, nq, nkv, d, g = (L + 15) // 16 * 16, 4, 2, 128, 32
@@ -298,10 +299,11 @@ def test_attention_long_rows(torch, L):
 
 
 @pytest.mark.parametrize("spread,shift", [(1e-4, 0.0), (1e4, 0.0), (1.0, 50.0), (3e6, 0.0), (1e-12, 0.0)])
-def test_attention_value_ranges(torch, spread, shift):
+@pytest.mark.parametrize("S", [512, 4112])
+def test_attention_value_ranges(torch, spread, shift, S):
     """Values far from 1: the scales leave half precision's range on either side, or ride on a large base."""
     r = np.random.default_rng(17)
-    S, L, nq, nkv, d, g = 512, 500, 4, 2, 128, 32
+    L, nq, nkv, d, g = S - 12, 4, 2, 128, 32
     c = Cache(torch, r, 1, nkv, S, d, g, [L], shift, spread)
     # outlier groups among them: ranges that differ by 10^4 within a row
     q = (r.standard_normal((1, nq, d)) / max(spread, shift)).astype(np.float32)
@@ -344,28 +346,30 @@ def test_attention_sharp_and_flat_softmax(torch):
     assert np.abs(out[0] - c.val["v"][0, :, 77].repeat(nq // nkv, 0)).max() <= 2.0 ** -20
 
 
-def test_attention_bad_rows(torch):
+@pytest.mark.parametrize("S", [64, 4112])
+def test_attention_bad_rows(torch, S):
     r = np.random.default_rng(20)
-    S, nq, nkv, d, g, slots = 64, 4, 2, 128, 64, 3
+    nq, nkv, d, g, slots = 4, 2, 128, 64, 3
     c = Cache(torch, r, slots, nkv, S, d, g)
     q = r.standard_normal((6, nq, d)).astype(np.float32)
     mass = torch.zeros((slots, nkv, S), device="cuda")
-    out = attend(torch, c.dev, q, [0, 3, -1, 1, 1, 2], [5, 5, 5, 64, -1, 63], mass)
+    out = attend(torch, c.dev, q, [0, 3, -1, 1, 1, 2], [5, 5, 5, S, -1, S - 1], mass)
     assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
     assert not out[1:5].any() and (mass[1] == 0).all().item()
-    for b, s, n in ((0, 0, 6), (5, 2, 64)):
+    for b, s, n in ((0, 0, 6), (5, 2, S)):
         ref, m = kv4.attention(q[b], c.val["k"][s, :, :n], c.val["v"][s, :, :n], 1 / math.sqrt(d))
         assert rel_l2(out[b], ref) <= ATTN_TOL
         assert np.allclose(mass[s, :, :n].cpu().numpy(), m, rtol=2e-4, atol=0)
 
 
-def test_attention_rows_that_share_a_slot(torch):
+@pytest.mark.parametrize("S", [512, 4112])
+def test_attention_rows_that_share_a_slot(torch, S):
     """Several rows of one slot (several continuations of a prompt): each attends on its own, and the slot's mass
     gains all of them, the same bits every run."""
     r = np.random.default_rng(21)
-    S, nq, nkv, d, g = 512, 4, 2, 128, 32
+    nq, nkv, d, g = 4, 2, 128, 32
     c = Cache(torch, r, 2, nkv, S, d, g)
-    ids, n = [1, 0, 1, 1, 0, 9], [300, 40, 512, 7, 1, 5]
+    ids, n = [1, 0, 1, 1, 0, 9], [300, 40, S, 7, 1, 5]
     q = r.standard_normal((6, nq, d)).astype(np.float32)
     runs = []
     for _ in range(3):

@@ -81,7 +81,7 @@ def test_bad_caches(L, name):
     ("kmr_decode_attn_kv4", dict(ws=None), -1), ("kmr_decode_attn_kv4", dict(q=8), -1), ("kmr_decode_attn_kv4", dict(mass=4), -1),
     ("kmr_decode_attn_kv4", dict(scale=float("nan")), -1), ("kmr_decode_attn_kv4", dict(scale=float("inf")), -1),
     ("kmr_decode_attn_kv4", dict(B=0), -9), ("kmr_decode_attn_kv4", dict(nq=20), -2),
-    ("kmr_decode_attn_kv4", dict(nq=72), -2), ("kmr_decode_attn_kv4", dict(n=16), -8),
+    ("kmr_decode_attn_kv4", dict(nq=72), -2), ("kmr_decode_attn_kv4", dict(n=15), -8),
     ("kmr_kv4_evict", dict(dst=None), -1), ("kmr_kv4_evict", dict(ids=None), -1), ("kmr_kv4_evict", dict(dids=None), -1),
     ("kmr_kv4_evict", dict(n=None), -1), ("kmr_kv4_evict", dict(mass=None), -1), ("kmr_kv4_evict", dict(kept=None), -1),
     ("kmr_kv4_evict", dict(new=None), -1), ("kmr_kv4_evict", dict(keep=0), -1), ("kmr_kv4_evict", dict(recent=-1), -1),
@@ -103,11 +103,12 @@ def test_evict_between_caches(L):
 
 def test_workspace_size(L):
     W = L.kmr_decode_attn_kv4_workspace_size
-    c = cache(max_len=1024)
+    c = cache(max_len=8192)
     a = ctypes.addressof(c)
-    assert 0 < W(a, 1, 16, 0) < W(a, 4, 16, 0) and W(a, 1, 16, 1) == W(a, 1, 16, 0) + 16 * 1024 * 4
+    assert 0 < W(a, 1, 16, 0) < W(a, 4, 16, 0) and W(a, 1, 16, 1) == W(a, 1, 16, 0) + 16 * 8192 * 4
     assert W(a, 0, 16, 0) == W(a, 1, 12, 0) == W(a, 1025, 16, 0) == W(None, 1, 16, 0) == 0
     assert W(ctypes.addressof(cache(group=48)), 1, 16, 0) == 0
+    assert W(ctypes.addressof(cache(max_len=4096)), 4, 16, 1) == 16           # short caches merge on chip
 
 
 def test_binding_checks_the_cache_tensors(L):
