@@ -373,15 +373,12 @@ __device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
 // histogram each, searched from the top by a scan over the CTA), then one ordered pass writes the kept
 // indices in ascending order.  The keys are formed once and kept in shared memory.  What bounds it is the chain
 // of some fifteen barriers: a row of 8192 masses is 32 KB.
-__global__ void __launch_bounds__(kSelThr, 1) kv4_select_kernel(const Kv4EvictParams p) {
+__device__ __forceinline__ void select_positions(const Kv4EvictParams& p, int h, int b, int bad) {
     extern __shared__ uint32_t keys[];
     __shared__ int hist[kSelBins];
     __shared__ int wsum[2][32];
     __shared__ int found[2];
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int bad = evict_row_error(p, b);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
     const int n = bad ? 0 : p.lengths[b];
     const int total = n < p.keep ? n : p.keep, newest = p.recent < total ? p.recent : total;
@@ -467,58 +464,70 @@ __global__ void __launch_bounds__(kSelThr, 1) kv4_select_kernel(const Kv4EvictPa
     }
 }
 
-// The kept positions' codes, scales and mass, moved to positions 0, 1, ... of the destination row: four lanes
-// a position (as above), kMove positions of a lane in flight.  A programmatic dependent of the selection.
-constexpr int kMove = 4;
+// One (row, head) per thread-block cluster: its first CTA selects, then all move the kept positions' codes, scales
+// and mass to positions 0, 1, ... of the destination row: four lanes a position (as above), kMove positions of a
+// lane in flight.  The cluster is as large as the SMs allow (up to 8): a call of few rows needs more than one SM's
+// bandwidth for a row, one of many rows has an SM for each.
+constexpr int kMove = 2;
 
 template <int D, int G>
-__global__ void __launch_bounds__(kThr) kv4_gather_kernel(const Kv4EvictParams p) {
+__global__ void __launch_bounds__(kSelThr, 1) kv4_evict_kernel(const Kv4EvictParams p) {
     constexpr int NG = D / G;
     using Piece = typename std::conditional<D == 128, uint4, uint2>::type;
     const int h = blockIdx.y, b = blockIdx.z, l = threadIdx.x & 3;
-    const int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
     pdl_wait();
-    const int total = p.new_lengths[b];
-    const int j0 = blockIdx.x * (kThr / 4 * kMove) + threadIdx.x / 4;
-    if (j0 >= total) return;
+    const int bad = evict_row_error(p, b);
+    if (blockIdx.x == 0) select_positions(p, h, b, bad);
+    if (gridDim.x > 1) {
+        asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+        asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    if (bad) return;
+    const int32_t* kept = p.kept + (size_t(b) * p.src.nkv + h) * p.keep;
+    const int n = p.lengths[b], total = n < p.keep ? n : p.keep;
     const size_t srow = (size_t(p.src_ids[b]) * p.src.nkv + h) * p.src.S;
     const size_t drow = (size_t(p.dst_ids[b]) * p.src.nkv + h) * p.dst.S;
-    size_t from[kMove];
-    Piece k[kMove], v[kMove];
-    uint32_t kw[kMove], vw[kMove];
-    float m[kMove];
+    constexpr int kLanes = kSelThr / 4;
+    for (int j0 = int(blockIdx.x) * kLanes * kMove + threadIdx.x / 4; j0 < total; j0 += gridDim.x * kLanes * kMove) {
+        size_t from[kMove];
+        Piece k[kMove], v[kMove];
+        uint32_t kw[kMove], vw[kMove];
+        float m[kMove];
 #pragma unroll
-    for (int i = 0; i < kMove; ++i) {
-        const int j = j0 + i * (kThr / 4);
-        from[i] = srow + kept[j < total ? j : j0];
-    }
-#pragma unroll
-    for (int i = 0; i < kMove; ++i) {
-        k[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.kc + from[i] * (D / 2)) + l);
-        v[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.vc + from[i] * (D / 2)) + l);
-        kw[i] = l < NG ? __ldcs(p.src.ks + from[i] * NG + l) : 0u;
-        vw[i] = l < NG ? __ldcs(p.src.vs + from[i] * NG + l) : 0u;
-        m[i] = l == 0 ? p.mass[from[i]] : 0.f;
-    }
-#pragma unroll
-    for (int i = 0; i < kMove; ++i) {
-        const int j = j0 + i * (kThr / 4);
-        if (j >= total) return;
-        const size_t to = drow + j;
-        reinterpret_cast<Piece*>(p.dst.kc + to * (D / 2))[l] = k[i];
-        reinterpret_cast<Piece*>(p.dst.vc + to * (D / 2))[l] = v[i];
-        if (l < NG) {
-            p.dst.ks[to * NG + l] = kw[i];
-            p.dst.vs[to * NG + l] = vw[i];
+        for (int i = 0; i < kMove; ++i) {
+            const int j = j0 + i * kLanes;
+            from[i] = srow + __ldcg(kept + (j < total ? j : j0));
         }
-        if (l == 0 && p.dst_mass) p.dst_mass[to] = m[i];
+#pragma unroll
+        for (int i = 0; i < kMove; ++i) {
+            k[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.kc + from[i] * (D / 2)) + l);
+            v[i] = __ldcs(reinterpret_cast<const Piece*>(p.src.vc + from[i] * (D / 2)) + l);
+            kw[i] = l < NG ? __ldcs(p.src.ks + from[i] * NG + l) : 0u;
+            vw[i] = l < NG ? __ldcs(p.src.vs + from[i] * NG + l) : 0u;
+            m[i] = l == 0 ? p.mass[from[i]] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < kMove; ++i) {
+            const int j = j0 + i * kLanes;
+            if (j >= total) break;
+            const size_t to = drow + j;
+            reinterpret_cast<Piece*>(p.dst.kc + to * (D / 2))[l] = k[i];
+            reinterpret_cast<Piece*>(p.dst.vc + to * (D / 2))[l] = v[i];
+            if (l < NG) {
+                p.dst.ks[to * NG + l] = kw[i];
+                p.dst.vs[to * NG + l] = vw[i];
+            }
+            if (l == 0 && p.dst_mass) p.dst_mass[to] = m[i];
+        }
     }
 }
 
 template <int D, int G>
 const void* write_fn(int which) {
     if (which == 0) return (const void*)kv4_append_kernel<D, G>;
-    if (which == 3) return (const void*)kv4_gather_kernel<D, G>;
+    if (which == 3) return (const void*)kv4_evict_kernel<D, G>;
     return which == 1 ? (const void*)kv4_convert_kernel<D, G, false> : (const void*)kv4_convert_kernel<D, G, true>;
 }
 const void* write_fn(int d, int g, int which) {
@@ -530,41 +539,50 @@ const void* write_fn(int d, int g, int which) {
 
 // Every kernel of the cache is launched as a programmatic dependent of whatever ran before it on the stream, and
 // waits for that at its start: the launch itself overlaps the end of the previous kernel.
-static cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, void* params, cudaStream_t st) {
-    cudaLaunchAttribute attr;
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+static cudaError_t launch(const void* fn, dim3 grid, int threads, size_t smem, int cluster, const void* params,
+                          cudaStream_t st) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = unsigned(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = dim3(threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    void* args[] = {params};
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    void* args[] = {const_cast<void*>(params)};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st) {
-    return launch(write_fn(p.c.d, p.c.g, 0), dim3(p.T, p.B), kThr, 0, const_cast<Kv4AppendParams*>(&p), st);
+    return launch(write_fn(p.c.d, p.c.g, 0), dim3(p.T, p.B), kThr, 0, 1, &p, st);
 }
 
 cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st) {
-    return launch(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B), kThr, 0,
-                  const_cast<Kv4ConvertParams*>(&p), st);
+    return launch(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B), kThr, 0, 1,
+                  &p, st);
 }
 
 cudaError_t kv4_set_attributes() {
-    return cudaFuncSetAttribute(kv4_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
+    const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
+    for (const auto& sh : shapes) {
+        const cudaError_t e = cudaFuncSetAttribute(write_fn(sh[0], sh[1], 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                   kSelCache * 4);
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 cudaError_t launch_kv4_evict(const Kv4EvictParams& p, cudaStream_t st) {
-    Kv4EvictParams q = p;
-    const cudaError_t e = launch((const void*)kv4_select_kernel, dim3(p.src.nkv, p.B), kSelThr,
-                                 size_t(p.src.S < kSelCache ? p.src.S : kSelCache) * 4, &q, st);
-    if (e != cudaSuccess) return e;
-    return launch(write_fn(p.src.d, p.src.g, 3), dim3((p.keep + kThr / 4 * kMove - 1) / (kThr / 4 * kMove), p.src.nkv, p.B),
-                  kThr, 0, &q, st);
+    int cluster = 8;
+    while (cluster > 1 && (long long)cluster * p.src.nkv * p.B > num_sms()) cluster /= 2;
+    return launch(write_fn(p.src.d, p.src.g, 3), dim3(cluster, p.src.nkv, p.B), kSelThr,
+                  size_t(p.src.S < kSelCache ? p.src.S : kSelCache) * 4, cluster, &p, st);
 }
 
 }  // namespace kmr

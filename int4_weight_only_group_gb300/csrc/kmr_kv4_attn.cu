@@ -211,6 +211,9 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     pdl_wait();                                   // nothing of the previous kernel's is read before
     pdl_launch_dependents();
     const int rep = p.nq / p.c.nkv;
+    // warp 1 prepares the query for all while warp 0 looks up the row and starts its copies
+    uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
+    if (warp == 1) query_fragments<D, G, NT, PAIR>(p, b0, h, rep, lane, qsh);
     const int bad = kv4_row_error(p, b0);
     if (bad != KMR_OK) {                          // the same for the whole cluster
         if (CL && s == 0) {
@@ -235,7 +238,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         }
         fence_mbar_init();
     }
-    __syncthreads();
+    __syncwarp();                                 // the other warps see the barriers after the first block barrier
     const int cgh = column_half<PAIR>(g), cth = PAIR ? t >> 1 : 0;   // halves of the lane's column and accumulators
     const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
     uint32_t uses = 0;                            // stages filled so far: stage k of them was use k / kStages of its buffer
@@ -279,9 +282,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     if (warp == 0)
         for (int i = 0; i < nst && i < kStages; ++i) issue(i);
 
-    // ---- the query, prepared by warp 1 for all
-    uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
-    if (warp == 1 && nst > 0) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
+    if (CL && !first && warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
     __syncthreads();
     uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
     float qsum[NT][HG], fac[NT];
