@@ -33,12 +33,51 @@ __device__ __forceinline__ uint32_t pack_code(int hi, int lo, uint32_t w) {
     return r;
 }
 
-// The lane's codes (word b: dims 32 b + 8 l + i in nibble i) and the vector's group words (z, s).
-// lo, hi = the group's extremes; s = bf16((hi - lo) / 15), 0 below 2^-126 (its reciprocal would leave the normal
-// range); z = bf16(lo); c = rint((x - z) / s) within 0..15, 0 where s is 0.  Both quotients are the correctly
-// rounded ones (Markstein 1990: with r near 1 / s, q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value
-// half-way between two codes is seen as half-way and goes to the even one.  A group that holds a NaN or an
-// infinity, or whose range overflows, stores s = 0 and z = NaN: it reads back as NaN.
+// s and z of a group from its extremes, as the group's word, and the lane's codes (word k: dims 32 k + 8 l + i in nibble
+// i).  s = bf16((hi - lo) / 15), 0 below 2^-126 (its reciprocal would leave the normal range); z = bf16(lo);
+// c = rint((x - z) / s) within 0..15, 0 where s is 0.  Both quotients are the correctly rounded ones (Markstein 1990:
+// with r near 1 / s, q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value half-way between two codes is seen
+// as half-way and goes to the even one.  A group that holds a NaN or an infinity, or whose range overflows, stores
+// s = 0 and z = NaN: it reads back as NaN.
+template <int BPG>
+__device__ __forceinline__ uint32_t quantize_group(const float (*x)[8], float lo, float hi, uint32_t* w) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+    const float range = __fsub_rn(hi, lo), fifteenth = 1.f / 15.f;
+    const float s0 = __fmul_rn(range, fifteenth);
+    const float s1 = __fmaf_rn(__fmaf_rn(-15.f, s0, range), fifteenth, s0);
+    uint32_t u;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(s1), "f"(lo));
+    if (u < 0x00800000u) u &= 0xFFFFu;
+    const bool bad = (u & 0x7F800000u) == 0x7F800000u || (u & 0x7F80u) == 0x7F80u;
+    if (bad) u = 0x7FC0u;
+    const float s = kv4_s(u), z = bad ? 0.f : kv4_z(u);
+    float r = 0.f;
+    if (s > 0.f) {
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+        r = __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
+    }
+#pragma unroll
+    for (int k = 0; k < BPG; ++k) {
+        int c[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float a = __fsub_rn(x[k][i], z);
+            const float q0 = __fmul_rn(a, r);
+            const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
+            // 1.5 * 2^23 + q rounds q to a whole number (half to even) in the low bits
+            c[i] = __float_as_int(__fadd_rn(q, 12582912.f)) - 0x4B400000;
+        }
+        uint32_t v = pack_code(c[7], c[6], 0u);
+        v = pack_code(c[5], c[4], v);
+        v = pack_code(c[3], c[2], v);
+        v = pack_code(c[1], c[0], v);
+        w[k] = bad ? 0u : v;
+    }
+    return u;
+}
 template <int D, int G>
 __device__ __forceinline__ void quantize(const float (&x)[D / 32][8], uint32_t (&w)[D / 32], uint32_t (&word)[D / G]) {
     constexpr int NG = D / G, BPG = G / 32;
@@ -52,42 +91,31 @@ __device__ __forceinline__ void quantize(const float (&x)[D / 32][8], uint32_t (
                 lo = min_nan(lo, x[gr * BPG + k][i]);
                 hi = max_nan(hi, x[gr * BPG + k][i]);
             }
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-        lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
-        hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
-        const float range = __fsub_rn(hi, lo), fifteenth = 1.f / 15.f;
-        const float s0 = __fmul_rn(range, fifteenth);
-        const float s1 = __fmaf_rn(__fmaf_rn(-15.f, s0, range), fifteenth, s0);
-        uint32_t u;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(s1), "f"(lo));
-        if (u < 0x00800000u) u &= 0xFFFFu;
-        const bool bad = (u & 0x7F800000u) == 0x7F800000u || (u & 0x7F80u) == 0x7F80u;
-        if (bad) u = 0x7FC0u;
-        word[gr] = u;
-        const float s = kv4_s(u), z = bad ? 0.f : kv4_z(u);
-        float r = 0.f;
-        if (s > 0.f) {
-            asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
-            r = __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
-        }
+        word[gr] = quantize_group<BPG>(x + gr * BPG, lo, hi, w + gr * BPG);
+    }
+}
+// The same of bf16 pairs, whose extremes are found two at a time.
+template <int D, int G>
+__device__ __forceinline__ void quantize_bf16(const uint4 (&raw)[D / 32], uint32_t (&w)[D / 32], uint32_t (&word)[D / G]) {
+    constexpr int NG = D / G, BPG = G / 32;
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        float x[BPG][8];
+        uint32_t lo2 = raw[gr * BPG].x, hi2 = lo2;
 #pragma unroll
         for (int k = 0; k < BPG; ++k) {
-            int c[8];
+            const uint4 u = raw[gr * BPG + k];
+            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float a = __fsub_rn(x[gr * BPG + k][i], z);
-                const float q0 = __fmul_rn(a, r);
-                const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
-                // 1.5 * 2^23 + q rounds q to a whole number (half to even) in the low bits
-                c[i] = __float_as_int(__fadd_rn(q, 12582912.f)) - 0x4B400000;
+            for (int i = 0; i < 4; ++i) {
+                asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo2) : "r"(v[i]));
+                asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi2) : "r"(v[i]));
+                x[k][2 * i] = bf16_lo(v[i]);
+                x[k][2 * i + 1] = bf16_hi(v[i]);
             }
-            uint32_t v = pack_code(c[7], c[6], 0u);
-            v = pack_code(c[5], c[4], v);
-            v = pack_code(c[3], c[2], v);
-            v = pack_code(c[1], c[0], v);
-            w[gr * BPG + k] = bad ? 0u : v;
         }
+        word[gr] = quantize_group<BPG>(x, min_nan(bf16_lo(lo2), bf16_hi(lo2)), max_nan(bf16_lo(hi2), bf16_hi(hi2)),
+                                       w + gr * BPG);
     }
 }
 
@@ -253,8 +281,10 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
 }
 
 // ------------------------------------------------------------------ bf16 <-> 4 bits
-// Grid (positions / kSpan, 2 n_kv, span): a warp takes eight neighbouring positions of K or V of one head at a time.
-constexpr int kSpan = 64;
+// Grid (positions / span, 2 n_kv, row): a warp takes eight neighbouring positions of K or V of one head at a time.  A CTA's
+// span is long where that still gives every SM four of them (the loads of the row's state, some 2 us, are paid per
+// CTA), short otherwise.
+constexpr int kSpanLong = 256, kSpanShort = 64;
 
 __device__ __forceinline__ uint32_t fma_bf16x2(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t r;
@@ -277,7 +307,7 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
             set_error(p.err, bad_n ? KMR_ERR_INVALID_ARG : (bad_slot ? KMR_ERR_SLOT_RANGE : KMR_ERR_CACHE_FULL));
         return;
     }
-    const int t0 = blockIdx.x * kSpan, t1 = min(n, t0 + kSpan);
+    const int t0 = blockIdx.x * p.span, t1 = min(n, t0 + p.span);
     if (t0 >= t1) return;
     const int wslot = TO16 ? slot16 : slot, w0 = TO16 ? s16 : s0, wS = TO16 ? p.S16 : p.c.S;
     const int32_t* wslots = TO16 ? p.slot16 : p.slot_ids;
@@ -286,27 +316,28 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
     const bool key = int(blockIdx.y) < nkv;
     const int kvh = key ? blockIdx.y : blockIdx.y - nkv;
     const size_t row = (size_t(slot) * nkv + kvh) * p.c.S + s0, row16 = (size_t(slot16) * nkv + kvh) * p.S16 + s16;
-#pragma unroll 2
-    for (int i0 = t0; i0 < t1; i0 += kThr / 4) {
-        const int t = i0 + tid / 4;
-        bool on = t < t1;
-        if (clash && on) {
+    auto mine = [&](int t) {
+        if (t >= t1) return false;
+        if (clash)
             for (int r = b + 1; r < p.B; ++r) {
                 const int m = p.lengths[r], q = wstart[r];
                 if (wslots[r] == wslot && m >= 0 && m <= p.T && q >= 0 && q <= wS - m && w0 + t >= q && w0 + t < q + m)
-                    on = false;
+                    return false;
             }
-        }
-        const size_t at = row + (t < t1 ? t : t0), at16 = (row16 + (t < t1 ? t : t0)) * D + 8 * l;
-        uint4* vals = reinterpret_cast<uint4*>((key ? p.k16 : p.v16) + at16);
-        uint8_t* codes = (key ? p.c.kc : p.c.vc) + at * (D / 2);
-        uint32_t* words = (key ? p.c.ks : p.c.vs) + at * NG;
-        if constexpr (TO16) {
+        return true;
+    };
+    uint16_t* vals0 = (key ? p.k16 : p.v16) + row16 * D + 8 * l;
+    uint8_t* codes0 = (key ? p.c.kc : p.c.vc) + row * (D / 2);
+    uint32_t* words0 = (key ? p.c.ks : p.c.vs) + row * NG;
+    if constexpr (TO16) {
+#pragma unroll 2
+        for (int t = t0 + tid / 4; t < t1; t += kThr / 4) {
             uint32_t w[NB], word[NG];
-            load_codes<NB>(codes, w, key, l);
+            load_codes<NB>(codes0 + size_t(t) * (D / 2), w, key, l);
 #pragma unroll
-            for (int i = 0; i < NG; ++i) word[i] = words[i];
-            if (!on) continue;
+            for (int i = 0; i < NG; ++i) word[i] = words0[size_t(t) * NG + i];
+            if (!mine(t)) continue;
+            uint4* vals = reinterpret_cast<uint4*>(vals0 + size_t(t) * D);
 #pragma unroll
             for (int k = 0; k < NB; ++k) {
                 const uint32_t u = word[k / BPG];
@@ -322,23 +353,27 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
                 __stcs(vals + 4 * k, make_uint4(__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[2], y[3], 0x5410),
                                                 __byte_perm(y[0], y[1], 0x7632), __byte_perm(y[2], y[3], 0x7632)));
             }
-        } else {
-            float x[NB][8];
+        }
+    } else {
+        // every lane of a warp runs the same number of rounds (the shuffles); the next round's loads are in flight
+        uint4 next[NB];
+        auto load = [&](int t) {
+            const uint4* vals = reinterpret_cast<const uint4*>(vals0 + size_t(t < t1 ? t : t0) * D);
 #pragma unroll
-            for (int k = 0; k < NB; ++k) {
-                const uint4 u = __ldcs(vals + 4 * k);
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+            for (int k = 0; k < NB; ++k) next[k] = __ldcs(vals + 4 * k);
+        };
+        load(t0 + tid / 4);
+        for (int i0 = t0; i0 < t1; i0 += kThr / 4) {
+            const int t = i0 + tid / 4;
+            uint4 raw[NB];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[k][2 * i] = bf16_lo(v[i]);
-                    x[k][2 * i + 1] = bf16_hi(v[i]);
-                }
-            }
+            for (int k = 0; k < NB; ++k) raw[k] = next[k];
+            if (i0 + kThr / 4 < t1) load(t + kThr / 4);
             uint32_t w[NB], word[NG];
-            quantize<D, G>(x, w, word);
-            if (!on) continue;
-            store_codes<NB>(codes, w, key, l);
-            store_words<NG>(words, word, l);
+            quantize_bf16<D, G>(raw, w, word);
+            if (!mine(t)) continue;
+            store_codes<NB>(codes0 + size_t(t) * (D / 2), w, key, l);
+            store_words<NG>(words0 + size_t(t) * NG, word, l);
         }
     }
 }
@@ -564,8 +599,11 @@ cudaError_t launch_kv4_append(const Kv4AppendParams& p, cudaStream_t st) {
 }
 
 cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st) {
-    return launch(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + kSpan - 1) / kSpan, 2 * p.c.nkv, p.B), kThr, 0, 1,
-                  &p, st);
+    Kv4ConvertParams q = p;
+    const long long ctas = (long long)((p.T + kSpanLong - 1) / kSpanLong) * 2 * p.c.nkv * p.B;
+    q.span = ctas >= 4LL * num_sms() ? kSpanLong : kSpanShort;
+    return launch(write_fn(p.c.d, p.c.g, to_bf16 ? 2 : 1), dim3((p.T + q.span - 1) / q.span, 2 * p.c.nkv, p.B), kThr, 0, 1,
+                  &q, st);
 }
 
 cudaError_t kv4_set_attributes() {

@@ -63,6 +63,7 @@ struct Kv4ConvertParams {
     const int32_t* start;
     const int32_t* lengths;
     int B, T;
+    int span;                            // positions of a CTA (set by the launch)
     int* err;
 };
 cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStream_t st);
