@@ -33,90 +33,137 @@ __device__ __forceinline__ uint32_t pack_code(int hi, int lo, uint32_t w) {
     return r;
 }
 
-// s and z of a group from its extremes, as the group's word, and the lane's codes (word k: dims 32 k + 8 l + i in nibble
-// i).  s = bf16((hi - lo) / 15), 0 below 2^-126 (its reciprocal would leave the normal range); z = bf16(lo);
-// c = rint((x - z) / s) within 0..15, 0 where s is 0.  Both quotients are the correctly rounded ones (Markstein 1990:
-// with r near 1 / s, q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value half-way between two codes is seen
-// as half-way and goes to the even one.  A group that holds a NaN or an infinity, or whose range overflows, stores
-// s = 0 and z = NaN: it reads back as NaN.
-template <int BPG>
-__device__ __forceinline__ uint32_t quantize_group(const float (*x)[8], float lo, float hi, uint32_t* w) {
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 1));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 1));
-    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, 2));
-    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, 2));
+// Extremes of a vector's NG groups over its four lanes, as v = min over lanes of each; lane l ends with group l
+// (NG 4), l / 2 (NG 2) or the only one: each lane then works out one group's scale instead of all of them.
+template <int NG, typename T, typename Min>
+__device__ __forceinline__ T lane_group_min(const T (&v)[NG], int l, Min&& mn) {
+    T u[NG > 1 ? NG / 2 : 1];
+    if constexpr (NG == 1) {
+        u[0] = mn(v[0], T(__shfl_xor_sync(0xffffffffu, v[0], 2)));
+    } else {
+        const bool up = (l & 2) != 0;
+#pragma unroll
+        for (int i = 0; i < NG / 2; ++i) {
+            const T keep = up ? v[i + NG / 2] : v[i], send = up ? v[i] : v[i + NG / 2];
+            u[i] = mn(keep, T(__shfl_xor_sync(0xffffffffu, send, 2)));
+        }
+    }
+    if constexpr (NG < 4) return mn(u[0], T(__shfl_xor_sync(0xffffffffu, u[0], 1)));
+    const bool odd = (l & 1) != 0;
+    const T keep = odd ? u[NG / 2 - 1] : u[0], send = odd ? u[0] : u[NG / 2 - 1];
+    return mn(keep, T(__shfl_xor_sync(0xffffffffu, send, 1)));
+}
+
+// A group's word (z, s) and reciprocal from its extremes.  s = bf16((hi - lo) / 15), 0 below 2^-126 (its reciprocal would
+// leave the normal range); z = bf16(lo).  A group that holds a NaN or an infinity, or whose range overflows, stores
+// s = 0 and z = NaN (kBadWord): it reads back as NaN.  The quotient by 15 is the correctly rounded one (as below).
+constexpr uint32_t kBadWord = 0x7FC0u;
+__device__ __forceinline__ uint32_t group_word(float lo, float hi, float& r) {
     const float range = __fsub_rn(hi, lo), fifteenth = 1.f / 15.f;
     const float s0 = __fmul_rn(range, fifteenth);
     const float s1 = __fmaf_rn(__fmaf_rn(-15.f, s0, range), fifteenth, s0);
     uint32_t u;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(u) : "f"(s1), "f"(lo));
     if (u < 0x00800000u) u &= 0xFFFFu;
-    const bool bad = (u & 0x7F800000u) == 0x7F800000u || (u & 0x7F80u) == 0x7F80u;
-    if (bad) u = 0x7FC0u;
-    const float s = kv4_s(u), z = bad ? 0.f : kv4_z(u);
-    float r = 0.f;
+    if ((u & 0x7F800000u) == 0x7F800000u || (u & 0x7F80u) == 0x7F80u) u = kBadWord;
+    const float s = kv4_s(u);
+    r = 0.f;
     if (s > 0.f) {
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
         r = __fmaf_rn(__fmaf_rn(-s, r, 1.f), r, r);
     }
-#pragma unroll
-    for (int k = 0; k < BPG; ++k) {
-        int c[8];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float a = __fsub_rn(x[k][i], z);
-            const float q0 = __fmul_rn(a, r);
-            const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
-            // 1.5 * 2^23 + q rounds q to a whole number (half to even) in the low bits
-            c[i] = __float_as_int(__fadd_rn(q, 12582912.f)) - 0x4B400000;
-        }
-        uint32_t v = pack_code(c[7], c[6], 0u);
-        v = pack_code(c[5], c[4], v);
-        v = pack_code(c[3], c[2], v);
-        v = pack_code(c[1], c[0], v);
-        w[k] = bad ? 0u : v;
-    }
     return u;
 }
+
+// The lane's codes (word k: dims 32 k + 8 l + i in nibble i) under the vector's group words: c = rint((x - z) / s)
+// within 0..15, 0 where s is 0.  The quotient is the correctly rounded one (Markstein 1990: with r near 1 / s,
+// q0 = rn(a r), e = a - q0 s exactly, rn(q0 + e r)), so a value half-way between two codes is seen as half-way and goes
+// to the even one.  own, r: the word and reciprocal of the lane's group (lane_group_min).
 template <int D, int G>
-__device__ __forceinline__ void quantize(const float (&x)[D / 32][8], uint32_t (&w)[D / 32], uint32_t (&word)[D / G]) {
+__device__ __forceinline__ void code_words(const float (&x)[D / 32][8], uint32_t own, float own_r, uint32_t (&w)[D / 32]) {
     constexpr int NG = D / G, BPG = G / 32;
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-        float lo = x[gr * BPG][0], hi = lo;
+        const uint32_t u = NG == 1 ? own : __shfl_sync(0xffffffffu, own, gr * (4 / NG), 4);
+        const float r = NG == 1 ? own_r : __shfl_sync(0xffffffffu, own_r, gr * (4 / NG), 4);
+        const float s = kv4_s(u), z = kv4_z(u);
+#pragma unroll
+        for (int kb = 0; kb < BPG; ++kb) {
+            const int k = gr * BPG + kb;
+            int c[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float a = __fsub_rn(x[k][i], z);
+                const float q0 = __fmul_rn(a, r);
+                const float q = __fmaf_rn(__fmaf_rn(-q0, s, a), r, q0);
+                // 1.5 * 2^23 + q rounds q to a whole number (half to even) in the low bits
+                c[i] = __float_as_int(__fadd_rn(q, 12582912.f)) - 0x4B400000;
+            }
+            uint32_t v = pack_code(c[7], c[6], 0u);
+            v = pack_code(c[5], c[4], v);
+            v = pack_code(c[3], c[2], v);
+            v = pack_code(c[1], c[0], v);
+            w[k] = u == kBadWord ? 0u : v;
+        }
+    }
+}
+// Codes of a vector and the word of the lane's group.
+template <int D, int G>
+__device__ __forceinline__ uint32_t quantize(const float (&x)[D / 32][8], int l, uint32_t (&w)[D / 32]) {
+    constexpr int NG = D / G, BPG = G / 32;
+    float lo[NG], hi[NG];
+#pragma unroll
+    for (int gr = 0; gr < NG; ++gr) {
+        lo[gr] = hi[gr] = x[gr * BPG][0];
 #pragma unroll
         for (int k = 0; k < BPG; ++k)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                lo = min_nan(lo, x[gr * BPG + k][i]);
-                hi = max_nan(hi, x[gr * BPG + k][i]);
+                lo[gr] = min_nan(lo[gr], x[gr * BPG + k][i]);
+                hi[gr] = max_nan(hi[gr], x[gr * BPG + k][i]);
             }
-        word[gr] = quantize_group<BPG>(x + gr * BPG, lo, hi, w + gr * BPG);
     }
+    const float mylo = lane_group_min<NG>(lo, l, [](float a, float b) { return min_nan(a, b); });
+    const float myhi = lane_group_min<NG>(hi, l, [](float a, float b) { return max_nan(a, b); });
+    float r;
+    const uint32_t own = group_word(mylo, myhi, r);
+    code_words<D, G>(x, own, r, w);
+    return own;
 }
-// The same of bf16 pairs, whose extremes are found two at a time.
+// The same of bf16 pairs, whose extremes are found two at a time and cross the lanes as one pair (lo, -hi).
+__device__ __forceinline__ uint32_t min2_nan(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
 template <int D, int G>
-__device__ __forceinline__ void quantize_bf16(const uint4 (&raw)[D / 32], uint32_t (&w)[D / 32], uint32_t (&word)[D / G]) {
-    constexpr int NG = D / G, BPG = G / 32;
+__device__ __forceinline__ uint32_t quantize_bf16(const uint4 (&raw)[D / 32], int l, uint32_t (&w)[D / 32]) {
+    constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
+    float x[NB][8];
+    uint32_t ends[NG];
 #pragma unroll
     for (int gr = 0; gr < NG; ++gr) {
-        float x[BPG][8];
         uint32_t lo2 = raw[gr * BPG].x, hi2 = lo2;
 #pragma unroll
-        for (int k = 0; k < BPG; ++k) {
-            const uint4 u = raw[gr * BPG + k];
-            const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        for (int kb = 0; kb < BPG; ++kb) {
+            const int k = gr * BPG + kb;
+            const uint32_t v[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                asm("min.NaN.bf16x2 %0, %0, %1;" : "+r"(lo2) : "r"(v[i]));
+                lo2 = min2_nan(lo2, v[i]);
                 asm("max.NaN.bf16x2 %0, %0, %1;" : "+r"(hi2) : "r"(v[i]));
                 x[k][2 * i] = bf16_lo(v[i]);
                 x[k][2 * i + 1] = bf16_hi(v[i]);
             }
         }
-        word[gr] = quantize_group<BPG>(x, min_nan(bf16_lo(lo2), bf16_hi(lo2)), max_nan(bf16_lo(hi2), bf16_hi(hi2)),
-                                       w + gr * BPG);
+        hi2 ^= 0x80008000u;
+        ends[gr] = min2_nan(__byte_perm(lo2, hi2, 0x5410), __byte_perm(lo2, hi2, 0x7632));
     }
+    const uint32_t mine = lane_group_min<NG>(ends, l, [](uint32_t a, uint32_t b) { return min2_nan(a, b); });
+    float r;
+    const uint32_t own = group_word(bf16_lo(mine), -bf16_hi(mine), r);
+    code_words<D, G>(x, own, r, w);
+    return own;
 }
 
 // Words of a lane <-> its 4 NB bytes of a row of codes.
@@ -158,12 +205,10 @@ __device__ __forceinline__ void load_codes(const uint8_t* row, uint32_t (&w)[NB]
         }
     }
 }
-// Group words of a vector, one by each lane that has one to write.
+// Group words of a vector: each by (one of) the lanes that worked it out.
 template <int NG>
-__device__ __forceinline__ void store_words(uint32_t* row, const uint32_t (&word)[NG], int l) {
-#pragma unroll
-    for (int i = 0; i < NG; ++i)
-        if (l == i) row[i] = word[i];
+__device__ __forceinline__ void store_word(uint32_t* row, uint32_t own, int l) {
+    if (NG == 4 || (l & (4 / NG - 1)) == 0) row[l / (4 / NG)] = own;
 }
 
 // Whether a later row of the call writes one of positions [p0, p1) of the slot too: its values stay.
@@ -269,13 +314,13 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
             }
         }
         if (__all_sync(0xffffffffu, isq)) continue;
-        uint32_t codes[NB], word[NG];
-        quantize<D, G>(x, codes, word);
+        uint32_t codes[NB];
+        const uint32_t word = quantize<D, G>(x, l, codes);
         if (!on || isq || lose) continue;
         const int kvh = isk ? h - p.nq : h - p.nq - nkv;
         const size_t at = (size_t(slot) * nkv + kvh) * p.c.S + pos;
         store_codes<NB>((isk ? p.c.kc : p.c.vc) + at * (D / 2), codes, isk, l);
-        store_words<NG>((isk ? p.c.ks : p.c.vs) + at * NG, word, l);
+        store_word<NG>((isk ? p.c.ks : p.c.vs) + at * NG, word, l);
         if (isk && p.mass && l == 0) p.mass[at] = 0.f;
     }
 }
@@ -369,11 +414,11 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
 #pragma unroll
             for (int k = 0; k < NB; ++k) raw[k] = next[k];
             if (i0 + kThr / 4 < t1) load(t + kThr / 4);
-            uint32_t w[NB], word[NG];
-            quantize_bf16<D, G>(raw, w, word);
+            uint32_t w[NB];
+            const uint32_t word = quantize_bf16<D, G>(raw, l, w);
             if (!mine(t)) continue;
             store_codes<NB>(codes0 + size_t(t) * (D / 2), w, key, l);
-            store_words<NG>(words0 + size_t(t) * NG, word, l);
+            store_word<NG>(words0 + size_t(t) * NG, word, l);
         }
     }
 }
