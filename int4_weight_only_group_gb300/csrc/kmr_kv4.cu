@@ -227,6 +227,30 @@ __device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int p0,
 }
 
 // ------------------------------------------------------------------ new tokens
+// Cosine and sine of an angle of turn / 2^32 turns, to a little over half a step of single precision: the nearest
+// quarter turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, and the Taylor series' later
+// terms (at most a tenth of the sum) are added to the leading ones at the end, the roundings of which are kept.
+__device__ __forceinline__ void cos_sin_turn(int turn, float& c, float& s) {
+    const int quarter = int((unsigned(turn) + (1u << 29)) >> 30);
+    const int rem = int(unsigned(turn) - (unsigned(quarter) << 30));       // [-2^29, 2^29)
+    constexpr double kUnit = 6.283185307179586477 / 4294967296.0;
+    const float uh = float(kUnit), ul = float(kUnit - double(uh));
+    const float rh = __int2float_rn(rem), rl = __int2float_rn(rem - __float2int_rn(rh));
+    const float th = __fmul_rn(rh, uh);
+    const float tl = __fmaf_rn(rl, uh, __fmaf_rn(rh, ul, __fmaf_rn(rh, uh, -th)));
+    const float u = __fmul_rn(th, th);
+    const float u2 = __fmaf_rn(2.f * th, tl, __fmaf_rn(th, th, -u));       // th + tl squared is u + u2
+    const float ps = __fmaf_rn(u, __fmaf_rn(u, __fmaf_rn(u, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
+    const float sn = __fadd_rn(th, __fmaf_rn(__fmul_rn(th, u), ps, __fmaf_rn(-0.5f * u, tl, tl)));
+    const float pc = __fmaf_rn(u, __fmaf_rn(u, __fmaf_rn(u, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+    const float lead = __fmaf_rn(-0.5f, u, 1.f);
+    const float left = __fmaf_rn(-0.5f, u, __fsub_rn(1.f, lead));          // what rounding `lead` lost
+    const float cn = __fadd_rn(lead, __fmaf_rn(__fmul_rn(u, u), pc, __fmaf_rn(-0.5f, u2, left)));
+    const float a = (quarter & 1) ? sn : cn, b = (quarter & 1) ? cn : sn;
+    c = ((quarter + 1) & 2) ? -a : a;
+    s = (quarter & 2) ? -b : b;
+}
+
 // One CTA per token.  The token's angles are formed once: frequency i advances by theta^(-2i/d) / 2 pi
 // turns per position, held as a 64-bit fraction, so that position x fraction mod 1 is exact for any
 // position and the angle keeps its bits far into a long context.  Then each warp takes eight heads at a time.
@@ -254,8 +278,7 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
         const int axis = tid < p.sec0 ? 0 : (tid < p.sec0 + p.sec1 ? 1 : 2);
         const long long x = p.positions[(size_t(axis) * p.B + b) * p.T + t];
         const unsigned long long turn = (unsigned long long)x * p.turn[tid];
-        const float half_turns = float(int(turn >> 32)) * 0x1p-31f;    // in [-1, 1]
-        sincospif(half_turns, &sn[tid], &cs[tid]);
+        cos_sin_turn(int(turn >> 32), cs[tid], sn[tid]);
     }
     const bool lose = later_row_writes(b, p.B, slot, pos, pos + 1, p.slot_ids, p.cpos, p.n_tokens, p.T, p.c.S);
     __syncthreads();
@@ -274,24 +297,31 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
             x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
         }
         const uint16_t* w = isq ? p.qn_w : p.kn_w;
-        float ss = 0.f;
+        // the sum of squares as a tree: the codes hang on the last bits of what is quantised
+        float part[NB];
 #pragma unroll
-        for (int k = 0; k < NB; ++k)
+        for (int k = 0; k < NB; ++k) {
+            float q[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss = __fmaf_rn(x[k][i], x[k][i], ss);
+            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[k][i], x[k][i]);
+            part[k] = __fadd_rn(__fadd_rn(__fadd_rn(q[0], q[1]), __fadd_rn(q[2], q[3])),
+                                __fadd_rn(__fadd_rn(q[4], q[5]), __fadd_rn(q[6], q[7])));
+        }
+        float ss = __fadd_rn(part[0], part[1]);
+        if constexpr (NB == 4) ss = __fadd_rn(ss, __fadd_rn(part[2], part[3]));
         ss += __shfl_xor_sync(0xffffffffu, ss, 1);
         ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         if (isq || isk) {
             if (w) {
-                const float r = rsqrtf(ss / float(D) + p.eps);
+                const float r = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.f / float(D)), p.eps));     // D is a power of two
 #pragma unroll
                 for (int k = 0; k < NB; ++k) {
                     const uint4 u = *reinterpret_cast<const uint4*>(w + 32 * k + 8 * l);
                     const uint32_t wv[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        x[k][2 * i] = x[k][2 * i] * r * bf16_lo(wv[i]);
-                        x[k][2 * i + 1] = x[k][2 * i + 1] * r * bf16_hi(wv[i]);
+                        x[k][2 * i] = __fmul_rn(__fmul_rn(x[k][2 * i], r), bf16_lo(wv[i]));
+                        x[k][2 * i + 1] = __fmul_rn(__fmul_rn(x[k][2 * i + 1], r), bf16_hi(wv[i]));
                     }
                 }
             }
@@ -301,8 +331,8 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
                 for (int i = 0; i < 8; ++i) {
                     const float c = cs[32 * k + 8 * l + i], s = sn[32 * k + 8 * l + i];
                     const float lo = x[k][i], hi = x[k + NB / 2][i];
-                    x[k][i] = lo * c - hi * s;
-                    x[k + NB / 2][i] = hi * c + lo * s;
+                    x[k][i] = __fsub_rn(__fmul_rn(lo, c), __fmul_rn(hi, s));
+                    x[k + NB / 2][i] = __fadd_rn(__fmul_rn(hi, c), __fmul_rn(lo, s));
                 }
         }
         if (isq && on) {

@@ -26,8 +26,8 @@
 //     the group's s, split in two.  The codes are taken as c - 8 at half of the positions and c - 7 at the
 //     others (their mean is 7.5; fp16 has no 1031.5 to subtract), the base as z + 8 s or z + 7 s: a long
 //     row's output is small against the codes' offset, and the sum of the offset codes would lose its bits (at
-//     131072 positions an error of 5e-6 with c - 8 throughout).  The bases add per group in fp32.  The products are scaled by a power of two that follows the
-//     largest s seen, so that any bf16 scale fits fp16.
+//     131072 positions an error of 5e-6 with c - 8 throughout).  The bases add per group in fp32.  The products
+//     are scaled by a power of two that follows the largest s seen, so that any bf16 scale fits fp16.
 // Few query heads (rep <= 2) leave half of the columns empty.  With two groups or more the columns' halves then
 // stand for the halves of the head's dims: column 4 f + 2 h + part is query head h in half f.  A step of the scores
 // has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     const int s = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();                                   // nothing of the previous kernel's is read before
-    pdl_launch_dependents();
+    if (!CL) pdl_launch_dependents();             // the merge, which waits for this kernel's end
     const int rep = p.nq / p.c.nkv;
     // warp 1 prepares the query for all while warp 0 looks up the row and starts its copies
     uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
@@ -245,421 +245,421 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     bool first = true;
 
     for (int b = b0; b < p.B; ++b) {
-    if (CL && b != b0 && (!p.mass || p.slot_ids[b] != slot || kv4_row_error(p, b) != KMR_OK)) continue;
-    const int L = p.cpos[b] + 1;
-    int chunk, ns;
-    if (CL)
-        kv4_cluster_plan(L, int(gridDim.x), chunk, ns);
-    else
-        kv4_split_plan(L, chunk, ns);
-    if (!CL && s >= ns) return;
-    const int t0 = min(s * chunk, L), t1 = min(L, t0 + chunk);       // a cluster's spare splits are empty
-    const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
-    if (CL && !first) {
-        cluster_arrive();
-        cluster_wait();                           // what the last row pushed has been read, and the ring
-        fence_proxy_async_smem();
-    }
-
-    // One stage: lanes 0..3 of the calling warp copy K codes, V codes, K words and V words of up to 128
-    // positions (rounded up to 16: within the row, whose length is a multiple of 16).
-    auto issue = [&](int st) {
-        const uint32_t slot_of = (uses + st) % kStages;
-        uint8_t* buf = ring + slot_of * M::kStage;
-        const int pa = t0 + st * kStagePos;
-        const uint32_t np = uint32_t(min(kStagePos, ((t1 - pa) + 15) & ~15));
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot_of], np * (D + 8 * NG));
-        __syncwarp();
-        if (lane < 4) {
-            const bool words = lane >= 2, key = !(lane & 1);
-            const void* src = words ? static_cast<const void*>((key ? p.c.ks : p.c.vs) + (row + pa) * NG)
-                                    : static_cast<const void*>((key ? p.c.kc : p.c.vc) + (row + pa) * (D / 2));
-            uint8_t* dst = buf + (words ? 2 * M::kCodes + (key ? 0 : M::kWords) : (key ? 0 : M::kCodes));
-            bulk_g2s(dst, src, np * (words ? 4 * NG : D / 2), &full[slot_of]);
-        }
-        __syncwarp();
-    };
-    if (warp == 0)
-        for (int i = 0; i < nst && i < kStages; ++i) issue(i);
-
-    if (CL && !first && warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
-    __syncthreads();
-    uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
-    float qsum[NT][HG], fac[NT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const uint32_t* at = qsh + n * (4 * HB + HG + 1) * 32 + lane;
-#pragma unroll
-        for (int k = 0; k < HB; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint32_t v = at[(4 * k + i) * 32];
-                if constexpr (PAIR) {
-                    qf[n][k][i] = cgh ? 0u : v;
-                    qf[n][k + HB][i] = cgh ? v : 0u;
-                } else {
-                    qf[n][k][i] = v;
-                }
-            }
-#pragma unroll
-        for (int i = 0; i < HG; ++i) qsum[n][i] = __uint_as_float(at[(4 * HB + i) * 32]);
-        fac[n] = __uint_as_float(at[(4 * HB + HG) * 32]);
-    }
-
-    float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][HG];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        m[n] = -INFINITY;
-        l[n] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
-    }
-    int eref = 5;                                 // exponent that the output accumulators are scaled by
-    // base-2 scores for the mass: [head][position], in shared memory from the split's first position on
-    float* sc_out = nullptr;
-    size_t sc_ld = p.c.S;
-    if (CL && p.mass) {
-        sc_ld = p.chunk_max;
-        sc_out = reinterpret_cast<float*>(smem + M::base(rep) + M::state(rep)) - t0;
-    } else if (!CL && p.scores) {
-        sc_out = p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S;
-    }
-
-    for (int st = 0; st < nst; ++st) {
-        const uint32_t slot_of = (uses + st) % kStages, phase = ((uses + st) / kStages) & 1u;
-        const uint8_t* buf = ring + slot_of * M::kStage;
-        mbar_wait(&full[slot_of], phase, p.err);
-        const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
-        if (base0 < t1) {
-            // a tile is whole but for the row's last ones; one past the end counts for nothing
-            const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
-            // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
-            float sc[TT][NT][2];
-            uint32_t top = 0u;
-#pragma unroll
-            for (int u = 0; u < TT; ++u) {
-                const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
-                uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
-                lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
-                lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
-                lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
-                lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
-                float zc[NT][2];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = zc[n][0] = zc[n][1] = 0.f;
-#pragma unroll
-                for (int gr = 0; gr < HG; ++gr) {
-                    float acc[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-                    for (int kb = 0; kb < BPG; ++kb) {
-                        const int k = gr * BPG + kb;
-                        uint32_t x[4], y[4];
-                        unpack_codes<0>(k0[k], x);
-                        unpack_codes<0>(k1[k], y);
-                        if constexpr (PAIR) {
-                            uint32_t xh[4], yh[4];
-                            unpack_codes<0>(k0[k + HB], xh);
-                            unpack_codes<0>(k1[k + HB], yh);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_f16(acc[0], x[i], y[i], xh[i], yh[i], qf[0][k][i], qf[0][k + HB][i]);
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
-                                mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
-                        sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
-                        zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
-                        zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
-                    }
-                }
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
-                    sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
-                    if constexpr (PAIR) {
-                        // the other half's part is two lanes away; both lanes add the same two numbers
-                        sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);
-                        sc[u][n][1] += __shfl_xor_sync(0xffffffffu, sc[u][n][1], 2);
-                    }
-                    if (!whole) {
-                        if (base + g >= t1) sc[u][n][0] = -INFINITY;
-                        if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
-                    }
-                    if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
-                        float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
-                        if (whole || base + g < t1) dst[0] = sc[u][n][0];
-                        if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
-                    }
-                }
-                uint32_t mine[(NG + 1) / 2];
-                const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
-                lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
-                if (whole || base + wpos < t1) {
-                    top = max(top, mine[0] & 0x7FFFFFFFu);
-                    if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
-                }
-            }
-            const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
-            // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
-            // above, so that most tiles rescale nothing; weights stay below 2^8
-            float mn[NT];
-            bool up = etop > eref;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float c = fmaxf(sc[0][n][0], sc[0][n][1]);
-                if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
-                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
-                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
-                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
-                mn[n] = fmaxf(m[n], c);
-                up |= mn[n] > m[n] + 8.f;
-            }
-            if (__any_sync(0xffffffffu, up)) {
-                // room of two octaves, so that scales a little larger do not rescale again
-                const int en = etop > eref ? min(etop + 2, 254) : eref;
-                const float es = exp2f(float(eref - en));
-                eref = en;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
-                    m[n] = mn[n];
-                    l[n] *= cf;
-                    const float ce = cf * es;
-#pragma unroll
-                    for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-                        for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
-#pragma unroll
-                    for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
-                }
-            }
-            const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
-#pragma unroll
-            for (int u = 0; u < TT; ++u) {
-                const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
-                // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
-                const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
-                uint32_t v0[HG], v1[HG], vw[4][HG];
-                lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
-                lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
-                if (!whole) {
-                    // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
-#pragma unroll
-                    for (int gr = 0; gr < HG; ++gr) {
-                        if (base + g >= t1) v0[gr] = 0u;
-                        if (base + g + 8 >= t1) v1[gr] = 0u;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
-                    }
-                }
-                // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
-                // column's head at the lane's four positions
-                float w[NT][4];
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    const float mm = m[n] == -INFINITY ? 0.f : m[n];
-                    const float p0 = exp2_approx(__fsub_rn(sc[u][n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[u][n][1], mm));
-                    l[n] += p0 + p1;
-#pragma unroll
-                    for (int gr = 0; gr < HG; ++gr) {
-                        zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
-                        zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
-                    }
-                    const float u0 = p0 * unit, u1 = p1 * unit;
-                    const int src = 4 * t + column_head<PAIR>(g);
-                    w[n][0] = __shfl_sync(0xffffffffu, u0, src);
-                    w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
-                    w[n][2] = __shfl_sync(0xffffffffu, u1, src);
-                    w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
-                }
-                // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
-                // of half 0 in rows g, of half 1 in rows g + 8
-                uint32_t vc[4][NB / 2];
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
-                auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
-                    const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
-                    unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
-                    unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
-                };
-#pragma unroll
-                for (int gr = 0; gr < HG; ++gr) {
-                    uint32_t wf[NT][2];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        float a[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
-                        wf[n][0] = pack_f16_rz(a[0], a[1]);
-                        wf[n][1] = pack_f16_rz(a[2], a[3]);
-                    }
-#pragma unroll
-                    for (int kb = 0; kb < BPG; ++kb) {
-                        const int k = gr * BPG + kb;
-                        uint32_t x[4], y[4];
-                        unpack_block(k, x, y);
-                        if constexpr (PAIR) {
-                            uint32_t xh[4], yh[4];
-                            unpack_block(k + HB, xh, yh);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                mma_f16(o[0][4 * k + i], x[i], xh[i], y[i], yh[i], wf[0][0], wf[0][1]);
-                        } else {
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
-                                mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
-                            }
-                        }
-                    }
-                }
-            }
-        }
-        // the warps take turns to refill the stage once all are done with it
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[slot_of]);
-        if (st + kStages < nst && warp == (st & (kWarps - 1))) {
-            mbar_wait(&empty[slot_of], phase, p.err);
+        if (CL && b != b0 && (!p.mass || p.slot_ids[b] != slot || kv4_row_error(p, b) != KMR_OK)) continue;
+        const int L = p.cpos[b] + 1;
+        int chunk, ns;
+        if (CL)
+            kv4_cluster_plan(L, int(gridDim.x), chunk, ns);
+        else
+            kv4_split_plan(L, chunk, ns);
+        if (!CL && s >= ns) return;
+        const int t0 = min(s * chunk, L), t1 = min(L, t0 + chunk);       // a cluster's spare splits are empty
+        const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
+        if (CL && !first) {
+            cluster_arrive();
+            cluster_wait();                           // what the last row pushed has been read, and the ring
             fence_proxy_async_smem();
-            issue(st + kStages);
         }
-    }
-    uses += nst;
-    __syncthreads();                              // every copy has landed and been read: the ring is free
 
-    // ---- the warp's state: o[head][dim], m, l
-    float* wo = reinterpret_cast<float*>(ring);                       // [warp][rep][D]
-    float* wml = wo + kWarps * rep * D;                               // [warp][rep][2]
-    const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        const int hq = PAIR ? t & 1 : 4 * n + t;
-        float lt = l[n];
-        lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-        lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-        float zt[HG];
-#pragma unroll
-        for (int gr = 0; gr < HG; ++gr) {
-            float v = zo[n][gr];
-            v += __shfl_xor_sync(0xffffffffu, v, 4);
-            v += __shfl_xor_sync(0xffffffffu, v, 8);
-            zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
-        }
-        if (hq < rep) {
-            if (g == 0 && cth == 0) {
-                wml[(warp * rep + hq) * 2] = m[n];
-                wml[(warp * rep + hq) * 2 + 1] = lt;
+        // One stage: lanes 0..3 of the calling warp copy K codes, V codes, K words and V words of up to
+        // kStagePos positions (rounded up to 16: within the row, whose length is a multiple of 16).
+        auto issue = [&](int st) {
+            const uint32_t slot_of = (uses + st) % kStages;
+            uint8_t* buf = ring + slot_of * M::kStage;
+            const int pa = t0 + st * kStagePos;
+            const uint32_t np = uint32_t(min(kStagePos, ((t1 - pa) + 15) & ~15));
+            if (lane == 0) mbar_arrive_expect_tx(&full[slot_of], np * (D + 8 * NG));
+            __syncwarp();
+            if (lane < 4) {
+                const bool words = lane >= 2, key = !(lane & 1);
+                const void* src = words ? static_cast<const void*>((key ? p.c.ks : p.c.vs) + (row + pa) * NG)
+                                        : static_cast<const void*>((key ? p.c.kc : p.c.vc) + (row + pa) * (D / 2));
+                uint8_t* dst = buf + (words ? 2 * M::kCodes + (key ? 0 : M::kWords) : (key ? 0 : M::kCodes));
+                bulk_g2s(dst, src, np * (words ? 4 * NG : D / 2), &full[slot_of]);
             }
+            __syncwarp();
+        };
+        if (warp == 0)
+            for (int i = 0; i < nst && i < kStages; ++i) issue(i);
+
+        if (CL && !first && warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
+        __syncthreads();
+        uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
+        float qsum[NT][HG], fac[NT];
 #pragma unroll
-            for (int k = 0; k < HB; ++k) {
-                const float z = zt[k / BPG];
-                float v[4];
+        for (int n = 0; n < NT; ++n) {
+            const uint32_t* at = qsh + n * (4 * HB + HG + 1) * 32 + lane;
+#pragma unroll
+            for (int k = 0; k < HB; ++k)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
+                    const uint32_t v = at[(4 * k + i) * 32];
                     if constexpr (PAIR) {
-                        const float(&a)[4] = o[n][4 * k + i];
-                        v[i] = cth ? a[2] + a[3] : a[0] + a[1];
+                        qf[n][k][i] = cgh ? 0u : v;
+                        qf[n][k + HB][i] = cgh ? v : 0u;
                     } else {
-                        const float(&a)[4] = o[n][2 * k + i / 2];
-                        v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
+                        qf[n][k][i] = v;
                     }
-                    v[i] = __fmaf_rn(v[i], un, z);
                 }
-                *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
-                    make_float4(v[0], v[1], v[2], v[3]);
-            }
-        }
-    }
-    __syncthreads();
-    float* part = CL ? nullptr : p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
-    const int ranks = CL ? int(gridDim.x) : 1, slice = rep * D / ranks;         // of the output, for each rank
-    float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [source][slice]
-    float* recv_ml = recv + rep * D;                                             // [source][head][m, l]
-    if (CL && first) cluster_wait();
-    if (s < ns) {
-        for (int i = tid; i < rep * (D / 4); i += kThr) {
-            const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
-            float mw[kWarps], mx = -INFINITY, den = 0.f;
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
-            float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < HG; ++i) qsum[n][i] = __uint_as_float(at[(4 * HB + i) * 32]);
+            fac[n] = __uint_as_float(at[(4 * HB + HG) * 32]);
+        }
+
+        float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][HG];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
-                const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
-                den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
-                num.x = __fmaf_rn(f, v.x, num.x);
-                num.y = __fmaf_rn(f, v.y, num.y);
-                num.z = __fmaf_rn(f, v.z, num.z);
-                num.w = __fmaf_rn(f, v.w, num.w);
+        for (int n = 0; n < NT; ++n) {
+            m[n] = -INFINITY;
+            l[n] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+#pragma unroll
+            for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
+        }
+        int eref = 5;                                 // exponent that the output accumulators are scaled by
+        // base-2 scores for the mass: [head][position], in shared memory from the split's first position on
+        float* sc_out = nullptr;
+        size_t sc_ld = p.c.S;
+        if (CL && p.mass) {
+            sc_ld = p.chunk_max;
+            sc_out = reinterpret_cast<float*>(smem + M::base(rep) + M::state(rep)) - t0;
+        } else if (!CL && p.scores) {
+            sc_out = p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S;
+        }
+
+        for (int st = 0; st < nst; ++st) {
+            const uint32_t slot_of = (uses + st) % kStages, phase = ((uses + st) / kStages) & 1u;
+            const uint8_t* buf = ring + slot_of * M::kStage;
+            mbar_wait(&full[slot_of], phase, p.err);
+            const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
+            if (base0 < t1) {
+                // a tile is whole but for the row's last ones; one past the end counts for nothing
+                const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
+                // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
+                float sc[TT][NT][2];
+                uint32_t top = 0u;
+#pragma unroll
+                for (int u = 0; u < TT; ++u) {
+                    const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                    uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
+                    lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
+                    lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
+                    lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
+                    lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
+                    float zc[NT][2];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = zc[n][0] = zc[n][1] = 0.f;
+#pragma unroll
+                    for (int gr = 0; gr < HG; ++gr) {
+                        float acc[NT][4];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+                        for (int kb = 0; kb < BPG; ++kb) {
+                            const int k = gr * BPG + kb;
+                            uint32_t x[4], y[4];
+                            unpack_codes<0>(k0[k], x);
+                            unpack_codes<0>(k1[k], y);
+                            if constexpr (PAIR) {
+                                uint32_t xh[4], yh[4];
+                                unpack_codes<0>(k0[k + HB], xh);
+                                unpack_codes<0>(k1[k + HB], yh);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_f16(acc[0], x[i], y[i], xh[i], yh[i], qf[0][k][i], qf[0][k + HB][i]);
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
+                                    mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
+                            sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
+                            zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
+                            zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
+                        sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
+                        if constexpr (PAIR) {
+                            // the other half's part is two lanes away; both lanes add the same two numbers
+                            sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);
+                            sc[u][n][1] += __shfl_xor_sync(0xffffffffu, sc[u][n][1], 2);
+                        }
+                        if (!whole) {
+                            if (base + g >= t1) sc[u][n][0] = -INFINITY;
+                            if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
+                        }
+                        if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
+                            float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
+                            if (whole || base + g < t1) dst[0] = sc[u][n][0];
+                            if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
+                        }
+                    }
+                    uint32_t mine[(NG + 1) / 2];
+                    const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
+                    lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
+                    if (whole || base + wpos < t1) {
+                        top = max(top, mine[0] & 0x7FFFFFFFu);
+                        if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
+                    }
+                }
+                const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
+                // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
+                // above, so that most tiles rescale nothing; weights stay below 2^8
+                float mn[NT];
+                bool up = etop > eref;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float c = fmaxf(sc[0][n][0], sc[0][n][1]);
+                    if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
+                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
+                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
+                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
+                    mn[n] = fmaxf(m[n], c);
+                    up |= mn[n] > m[n] + 8.f;
+                }
+                if (__any_sync(0xffffffffu, up)) {
+                    // room of two octaves, so that scales a little larger do not rescale again
+                    const int en = etop > eref ? min(etop + 2, 254) : eref;
+                    const float es = exp2f(float(eref - en));
+                    eref = en;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
+                        m[n] = mn[n];
+                        l[n] *= cf;
+                        const float ce = cf * es;
+#pragma unroll
+                        for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
+#pragma unroll
+                        for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
+                    }
+                }
+                const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
+#pragma unroll
+                for (int u = 0; u < TT; ++u) {
+                    const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                    // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
+                    const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
+                    uint32_t v0[HG], v1[HG], vw[4][HG];
+                    lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
+                    lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
+                    if (!whole) {
+                        // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            if (base + g >= t1) v0[gr] = 0u;
+                            if (base + g + 8 >= t1) v1[gr] = 0u;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
+                        }
+                    }
+                    // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
+                    // column's head at the lane's four positions
+                    float w[NT][4];
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        const float mm = m[n] == -INFINITY ? 0.f : m[n];
+                        const float p0 = exp2_approx(__fsub_rn(sc[u][n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[u][n][1], mm));
+                        l[n] += p0 + p1;
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
+                            zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
+                        }
+                        const float u0 = p0 * unit, u1 = p1 * unit;
+                        const int src = 4 * t + column_head<PAIR>(g);
+                        w[n][0] = __shfl_sync(0xffffffffu, u0, src);
+                        w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
+                        w[n][2] = __shfl_sync(0xffffffffu, u1, src);
+                        w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
+                    }
+                    // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
+                    // of half 0 in rows g, of half 1 in rows g + 8
+                    uint32_t vc[4][NB / 2];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
+                    auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
+                        const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                        unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
+                        unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+                    };
+#pragma unroll
+                    for (int gr = 0; gr < HG; ++gr) {
+                        uint32_t wf[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float a[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
+                            wf[n][0] = pack_f16_rz(a[0], a[1]);
+                            wf[n][1] = pack_f16_rz(a[2], a[3]);
+                        }
+#pragma unroll
+                        for (int kb = 0; kb < BPG; ++kb) {
+                            const int k = gr * BPG + kb;
+                            uint32_t x[4], y[4];
+                            unpack_block(k, x, y);
+                            if constexpr (PAIR) {
+                                uint32_t xh[4], yh[4];
+                                unpack_block(k + HB, xh, yh);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    mma_f16(o[0][4 * k + i], x[i], xh[i], y[i], yh[i], wf[0][0], wf[0][1]);
+                            } else {
+#pragma unroll
+                                for (int n = 0; n < NT; ++n) {
+                                    mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
+                                    mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                                }
+                            }
+                        }
+                    }
+                }
             }
-            if constexpr (CL) {
-                const int at = hq * D + dim;
-                float* to = cg::this_cluster().map_shared_rank(recv, at / slice);
-                *reinterpret_cast<float4*>(to + s * slice + at % slice) = num;
-                if (dim == 0)
-                    for (int r = 0; r < ranks; ++r)
-                        *reinterpret_cast<float2*>(cg::this_cluster().map_shared_rank(recv_ml, r) + (s * rep + hq) * 2) =
-                            make_float2(mx, den);
-            } else {
-                float* dst = part + hq * (D + 2);
-                *reinterpret_cast<float2*>(dst + 2 + dim) = make_float2(num.x, num.y);
-                *reinterpret_cast<float2*>(dst + 4 + dim) = make_float2(num.z, num.w);
-                if (dim == 0) *reinterpret_cast<float2*>(dst) = make_float2(mx, den);
+            // the warps take turns to refill the stage once all are done with it
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[slot_of]);
+            if (st + kStages < nst && warp == (st & (kWarps - 1))) {
+                mbar_wait(&empty[slot_of], phase, p.err);
+                fence_proxy_async_smem();
+                issue(st + kStages);
             }
         }
-    }
-    if (!CL) return;
-    // ---- every split's state is here: this rank's slice of the output, and its own positions' mass
-    cluster_arrive();
-    cluster_wait();
-    for (int i = tid; i < slice; i += kThr) {
-        const int hq = (s * slice + i) / D;
-        float mx = -INFINITY, num = 0.f, den = 0.f;
-        for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + hq) * 2]);
-        for (int r = 0; r < ns; ++r) {
-            const float mr = recv_ml[(r * rep + hq) * 2];
-            const float f = mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx));
-            den = __fmaf_rn(f, recv_ml[(r * rep + hq) * 2 + 1], den);
-            num = __fmaf_rn(f, recv[r * slice + i], num);
+        uses += nst;
+        __syncthreads();                              // every copy has landed and been read: the ring is free
+
+        // ---- the warp's state: o[head][dim], m, l
+        float* wo = reinterpret_cast<float*>(ring);                       // [warp][rep][D]
+        float* wml = wo + kWarps * rep * D;                               // [warp][rep][2]
+        const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int hq = PAIR ? t & 1 : 4 * n + t;
+            float lt = l[n];
+            lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+            lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+            float zt[HG];
+#pragma unroll
+            for (int gr = 0; gr < HG; ++gr) {
+                float v = zo[n][gr];
+                v += __shfl_xor_sync(0xffffffffu, v, 4);
+                v += __shfl_xor_sync(0xffffffffu, v, 8);
+                zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
+            }
+            if (hq < rep) {
+                if (g == 0 && cth == 0) {
+                    wml[(warp * rep + hq) * 2] = m[n];
+                    wml[(warp * rep + hq) * 2 + 1] = lt;
+                }
+#pragma unroll
+                for (int k = 0; k < HB; ++k) {
+                    const float z = zt[k / BPG];
+                    float v[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (PAIR) {
+                            const float(&a)[4] = o[n][4 * k + i];
+                            v[i] = cth ? a[2] + a[3] : a[0] + a[1];
+                        } else {
+                            const float(&a)[4] = o[n][2 * k + i / 2];
+                            v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
+                        }
+                        v[i] = __fmaf_rn(v[i], un, z);
+                    }
+                    *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
+                        make_float4(v[0], v[1], v[2], v[3]);
+                }
+            }
         }
-        p.out[(size_t(b) * p.nq + h * rep) * D + s * slice + i] = num * __frcp_rn(den);
-    }
-    if (!p.mass) return;
-    __shared__ float hm[kKv4MaxRep], hl[kKv4MaxRep];
-    if (tid < rep) {
-        float mx = -INFINITY, den = 0.f;
-        for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + tid) * 2]);
-        for (int r = 0; r < ns; ++r) {
-            const float mr = recv_ml[(r * rep + tid) * 2];
-            den = __fmaf_rn(mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx)), recv_ml[(r * rep + tid) * 2 + 1], den);
+        __syncthreads();
+        float* part = CL ? nullptr : p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
+        const int ranks = CL ? int(gridDim.x) : 1, slice = rep * D / ranks;         // of the output, for each rank
+        float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [source][slice]
+        float* recv_ml = recv + rep * D;                                             // [source][head][m, l]
+        if (CL && first) cluster_wait();
+        if (s < ns) {
+            for (int i = tid; i < rep * (D / 4); i += kThr) {
+                const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
+                float mw[kWarps], mx = -INFINITY, den = 0.f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
+                float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) {
+                    const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
+                    const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
+                    den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
+                    num.x = __fmaf_rn(f, v.x, num.x);
+                    num.y = __fmaf_rn(f, v.y, num.y);
+                    num.z = __fmaf_rn(f, v.z, num.z);
+                    num.w = __fmaf_rn(f, v.w, num.w);
+                }
+                if constexpr (CL) {
+                    const int at = hq * D + dim;
+                    float* to = cg::this_cluster().map_shared_rank(recv, at / slice);
+                    *reinterpret_cast<float4*>(to + s * slice + at % slice) = num;
+                    if (dim == 0)
+                        for (int r = 0; r < ranks; ++r)
+                            *reinterpret_cast<float2*>(cg::this_cluster().map_shared_rank(recv_ml, r) + (s * rep + hq) * 2) =
+                                make_float2(mx, den);
+                } else {
+                    float* dst = part + hq * (D + 2);
+                    *reinterpret_cast<float2*>(dst + 2 + dim) = make_float2(num.x, num.y);
+                    *reinterpret_cast<float2*>(dst + 4 + dim) = make_float2(num.z, num.w);
+                    if (dim == 0) *reinterpret_cast<float2*>(dst) = make_float2(mx, den);
+                }
+            }
         }
-        hm[tid] = mx;
-        hl[tid] = __frcp_rn(den);
-    }
-    __syncthreads();
-    for (int i = t0 + tid; i < t1; i += kThr) {
-        float add = 0.f;
-        for (int k = 0; k < rep; ++k) add = __fmaf_rn(exp2_approx(__fsub_rn(sc_out[k * sc_ld + i], hm[k])), hl[k], add);
-        __stcg(p.mass + row + i, __ldcg(p.mass + row + i) + add);    // (another SM's, of the row before)
-    }
-    first = false;
+        if (!CL) return;
+        // ---- every split's state is here: this rank's slice of the output, and its own positions' mass
+        cluster_arrive();
+        cluster_wait();
+        for (int i = tid; i < slice; i += kThr) {
+            const int hq = (s * slice + i) / D;
+            float mx = -INFINITY, num = 0.f, den = 0.f;
+            for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + hq) * 2]);
+            for (int r = 0; r < ns; ++r) {
+                const float mr = recv_ml[(r * rep + hq) * 2];
+                const float f = mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx));
+                den = __fmaf_rn(f, recv_ml[(r * rep + hq) * 2 + 1], den);
+                num = __fmaf_rn(f, recv[r * slice + i], num);
+            }
+            p.out[(size_t(b) * p.nq + h * rep) * D + s * slice + i] = num * __frcp_rn(den);
+        }
+        if (!p.mass) return;
+        __shared__ float hm[kKv4MaxRep], hl[kKv4MaxRep];
+        if (tid < rep) {
+            float mx = -INFINITY, den = 0.f;
+            for (int r = 0; r < ns; ++r) mx = fmaxf(mx, recv_ml[(r * rep + tid) * 2]);
+            for (int r = 0; r < ns; ++r) {
+                const float mr = recv_ml[(r * rep + tid) * 2];
+                den = __fmaf_rn(mr == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mr, mx)), recv_ml[(r * rep + tid) * 2 + 1], den);
+            }
+            hm[tid] = mx;
+            hl[tid] = __frcp_rn(den);
+        }
+        __syncthreads();
+        for (int i = t0 + tid; i < t1; i += kThr) {
+            float add = 0.f;
+            for (int k = 0; k < rep; ++k) add = __fmaf_rn(exp2_approx(__fsub_rn(sc_out[k * sc_ld + i], hm[k])), hl[k], add);
+            __stcg(p.mass + row + i, __ldcg(p.mass + row + i) + add);    // (another SM's, of the row before)
+        }
+        first = false;
     }
 }
 
