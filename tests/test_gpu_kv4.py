@@ -626,3 +626,159 @@ def test_two_streams_with_their_own_workspaces(torch):
             kmr.kmr_decode_attn_kv4(c.dev, q[i], ids, cpos, B, nq, 0.08, None, out[i], ws[i], n, streams[i])
     torch.cuda.synchronize()
     assert torch.equal(out, ref)
+
+
+# ------------------------------------------------------------------ limits, leftovers, the framework's own cache
+def test_shared_memory_leftovers_do_not_matter(torch):
+    """Shared memory filled with NaN bits before every call: the same bits as without."""
+    r = np.random.default_rng(71)
+    for S, L, nq, nkv, d, g in ((1024, [1, 70, 129, 1000], 16, 8, 128, 32), (4112, [1, 70, 300, 4100], 8, 1, 64, 64)):
+        c = Cache(torch, r, 4, nkv, S, d, g, L)
+        q = r.standard_normal((4, nq, d)).astype(np.float32)
+        res = []
+        for poison in (None, 0xFFFFFFFF, 0x7F800000):
+            mass = torch.zeros((4, nkv, S), device="cuda")
+            if poison is not None:
+                kmr.kmr_smem_poison(poison, torch.cuda.current_stream())
+            out = attend(torch, c.dev, q, range(4), np.array(L) - 1, mass)
+            if poison is not None:
+                kmr.kmr_smem_poison(poison, torch.cuda.current_stream())
+            dst = Cache(torch, np.random.default_rng(1), 4, nkv, 64, d, g)
+            kept, new = evict(torch, c.dev, dst.dev, range(4), range(4), L, 50, 5, mass, None)
+            res.append([out, mass.cpu().numpy(), kept, new] + dst.host())
+        for other in res[1:]:
+            assert all(np.array_equal(a, b) for a, b in zip(res[0], other))
+
+
+@pytest.mark.parametrize("S", [16, 4112])
+def test_the_most_rows(torch, S):
+    """1024 rows in one call: appended, attended (a quarter of them sharing slots) and evicted."""
+    r = np.random.default_rng(72)
+    B, nq, nkv, d, g = 1024, 2, 1, 64, 64
+    slots = 768
+    ids = np.concatenate([np.arange(768), r.integers(0, 768, 256)])
+    cache = kmr.Kv4Cache.zeros(slots, nkv, S, d, g)
+    qkv = r.standard_normal((B, 1, nq + 2 * nkv, d)).astype(np.float32)
+    q = torch.zeros((B, 1, nq, d), device="cuda")
+    sl, zero = i32(torch, ids), i32(torch, [0] * B)
+    kmr.kmr_kv4_append(cache, torch.from_numpy(qkv).cuda(), torch.zeros((3, B, 1), dtype=torch.int32, device="cuda"), sl, zero,
+                       None, B, 1, nq, None, None, 1e-6, 1e6, SECTIONS[d], q, None, torch.cuda.current_stream())
+    last = {s: b for b, s in enumerate(ids)}                          # the later row's token stays
+    V = kv4.dequantize(*kv4.quantize(qkv[:, 0, nq + nkv:], g))
+    mass = torch.zeros((slots, nkv, S), device="cuda")
+    out = attend(torch, cache, q.cpu().numpy()[:, 0], ids, [0] * B, mass)
+    want = np.stack([V[last[s]] for s in ids]).repeat(nq, 1)
+    assert kmr.kmr_last_device_error() == 0
+    # one position: weight 1, and a code times its scale plus a base
+    assert np.abs(out - want).max() <= 2.0 ** -20
+    m = mass.cpu().numpy()[:, 0, 0]
+    assert np.array_equal(m, nq * np.bincount(ids, minlength=slots).astype(np.float32))
+    dst = kmr.Kv4Cache.zeros(B, nkv, 16, d, g)
+    kept, new = evict(torch, cache, dst, ids, np.arange(B)[::-1].copy(), [1] * B, 3, 1, mass, None)
+    assert kmr.kmr_last_device_error() == 0
+    assert (new == 1).all() and (kept[:, 0] == [0, -1, -1]).all()
+    got = dst.tensors[1][:, 0, 0].cpu().numpy()[::-1]
+    assert np.array_equal(got, cache.tensors[1][ids.tolist(), 0, 0].cpu().numpy())
+
+
+def test_convert_long_spans(torch):
+    """Many long spans (a CTA takes 256 positions), two of them onto the same positions of a slot."""
+    r = np.random.default_rng(73)
+    B, nkv, d, g, S = 16, 8, 128, 32, 1024
+    x = r.standard_normal((2, B, nkv, S, d)).astype(np.float32)
+    bits = kv4.bf16_bits(x)
+    dev16 = [torch.from_numpy(b.view(np.int16)).cuda() for b in bits]
+    cache = kmr.Kv4Cache.zeros(B, nkv, S, d, g)
+    n = [1024, 1000, 257, 256, 255, 1, 0, 700] * 2
+    ids = list(range(B))
+    start = [0] * B
+    ids[15], start[15] = 8, 324                                       # row 15: 324.. of row 8's slot, over its values
+    rows, zero = i32(torch, range(B)), i32(torch, [0] * B)
+    kmr.kmr_kv4_from_bf16(cache, *dev16, B, S, rows, zero, i32(torch, ids), i32(torch, start), i32(torch, n), B, S,
+                          torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    for i in range(2):
+        codes, sb, zb = kv4.quantize(kv4.bf16_value(bits[i]), g)
+        want, words = np.zeros((B, nkv, S, d // 2), np.uint8), np.zeros((B, nkv, S, d // g), np.int32)
+        for b in range(B):
+            at = (ids[b], slice(None), slice(start[b], start[b] + n[b]))
+            want[at], words[at] = kv4.pack_rows(codes[b, :, :n[b]], i == 0), kv4.pack_words(sb[b, :, :n[b]], zb[b, :, :n[b]])
+        assert np.array_equal(cache.tensors[i].cpu().numpy(), want)
+        assert np.array_equal(cache.tensors[2 + i].cpu().numpy(), words)
+    back = [torch.zeros((B, nkv, S, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    kmr.kmr_kv4_to_bf16(cache, *back, B, S, rows, zero, rows, zero, i32(torch, [S] * B), B, S, torch.cuda.current_stream())
+    val = kv4.dequantize(kv4.unpack_rows(cache.tensors[0].cpu().numpy(), True), *(
+        (cache.tensors[2].cpu().numpy().view(np.uint32) >> k).astype(np.uint16) for k in (16, 0)))
+    assert np.array_equal(back[0].float().cpu().numpy(), kv4.bf16_value(kv4.bf16_bits(val.astype(np.float32))))
+
+
+def test_poisoned_group_reaches_its_own_dims_only(torch):
+    """An infinity in one position's V: NaN in that group's dims of the rows that attend it, nothing elsewhere."""
+    r = np.random.default_rng(74)
+    S, nq, nkv, d, g = 64, 2, 1, 128, 32
+    x = r.standard_normal((2, 1, nkv, S, d)).astype(np.float32)
+    x[1, 0, 0, 9, 40] = np.inf
+    cache = kmr.Kv4Cache.zeros(1, nkv, S, d, g)
+    z = i32(torch, [0])
+    kmr.kmr_kv4_from_bf16(cache, *[torch.from_numpy(kv4.bf16_bits(a).view(np.int16)).cuda() for a in x], 1, S, z, z, z, z,
+                          i32(torch, [S]), 1, S, torch.cuda.current_stream())
+    q = r.standard_normal((2, nq, d)).astype(np.float32)
+    out = attend(torch, cache, q, [0, 0], [8, 9])
+    assert np.isfinite(out[0]).all()
+    assert np.isnan(out[1][:, 32:64]).all() and np.isfinite(np.delete(out[1], range(32, 64), 1)).all()
+
+
+def test_prefilled_model_cache_to_4_bits(torch):
+    """kmr_prefill fills the model's bf16 cache; its rows go to 4 bits (kmr_model_kv_pointers) and are attended."""
+    from gpu_helpers import d2h_bytes
+    from int4_weight_only_group_gb300 import driver
+    from workloads import SyntheticModel, tiny_workload
+    wl = tiny_workload()
+    cfg = wl.cfg
+    m = kmr.Model.from_config(cfg, max_batch=1)
+    driver.load_weights(m, SyntheticModel(cfg, wl.seed), cfg.n_layers, cfg.qk_norm)
+    T, nkv, d, S = 40, cfg.n_kv_heads, cfg.head_dim, cfg.max_len
+    m.reserve_prefill(T)
+    r = np.random.default_rng(75)
+    state = [torch.zeros(n, dtype=t, device="cuda") for n, t in ((1, torch.int32), (3, torch.int32), (1, torch.int32), (1, torch.uint8))]
+    m.prefill(torch.from_numpy(r.integers(1, cfg.vocab - 1, T).astype(np.int32)).cuda(),
+              torch.arange(T, dtype=torch.int32, device="cuda").repeat(3, 1).contiguous(), T, 0, 0, *state, None,
+              torch.cuda.current_stream())
+    assert m.sync_status() == 0
+    z = i32(torch, [0])
+    for layer in range(cfg.n_layers):
+        cache = kmr.Kv4Cache.zeros(1, nkv, S, d, 32)
+        kp, vp = m.kv_pointers(layer)
+        kmr.kmr_kv4_from_bf16(cache, kp, vp, cfg.slots, S, z, z, z, z, i32(torch, [T]), 1, T, torch.cuda.current_stream())
+        q = r.standard_normal((1, cfg.n_q_heads, d)).astype(np.float32)
+        out = attend(torch, cache, q, [0], [T - 1])
+        assert kmr.kmr_last_device_error() == 0
+        K, V = (kv4.bf16_value(d2h_bytes(p, nkv * S * d * 2).view(np.uint16)).reshape(nkv, S, d)[:, :T] for p in (kp, vp))
+        ref, _ = kv4.attention(q[0], *(kv4.dequantize(*kv4.quantize(a, 32)) for a in (K, V)), 1 / math.sqrt(d))
+        assert rel_l2(out[0], ref) <= ATTN_TOL
+    m.close()
+
+
+def test_two_streams_long_rows(torch):
+    r = np.random.default_rng(76)
+    S, nq, nkv, d, g, B = 5008, 4, 2, 64, 32, 3
+    c = Cache(torch, r, B, nkv, S, d, g)
+    q = torch.from_numpy(r.standard_normal((2, B, nq, d)).astype(np.float32)).cuda()
+    ids, cpos = i32(torch, range(B)), i32(torch, [5007, 3, 2700])
+    n = kmr.kmr_decode_attn_kv4_workspace_size(c.dev, B, nq, True)
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    out, mass = torch.zeros((3, 2, B, nq, d), device="cuda"), torch.zeros((3, 2, B, nkv, S), device="cuda")
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for run in range(3):
+        for i in range(2):
+            kmr.kmr_decode_attn_kv4(c.dev, q[i], ids, cpos, B, nq, 0.1, mass[run, i], out[run, i], ws[i], n, streams[i])
+        if run == 0:
+            torch.cuda.synchronize()
+    torch.cuda.synchronize()
+    assert torch.equal(out[1], out[0]) and torch.equal(out[2], out[0]) and torch.equal(mass[1], mass[0])
+    for i in range(2):
+        for b, L in enumerate((5008, 4, 2701)):
+            ref, m = kv4.attention(q[i, b].cpu().numpy(), c.val["k"][b, :, :L], c.val["v"][b, :, :L], 0.1)
+            assert rel_l2(out[0, i, b].cpu().numpy(), ref) <= ATTN_TOL
+            assert np.allclose(mass[0, i, b, :, :L].cpu().numpy(), m, rtol=2e-4, atol=1e-30)
