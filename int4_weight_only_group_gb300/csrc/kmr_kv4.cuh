@@ -80,7 +80,8 @@ struct Kv4AttnParams {
     float* part;                         // [B][nkv][nsplit][rep][d + 2]
     float* scores;                       // [B][nkv][rep][S] base-2 scores (mass only)
     int nsplit;                          // the most splits a row of a long cache can have (0: a short cache)
-    int chunk_max;                       // short cache: the longest split
+    int per;                             // short cache: splits of a CTA (this and the next: set by the launch)
+    int score_ld;                        // short cache: positions whose scores a CTA keeps
     int* err;
 };
 size_t kv4_attn_part_bytes(int B, int nq, int d, int nsplit);
@@ -114,9 +115,9 @@ __host__ __device__ __forceinline__ void kv4_split_plan(int L, int& chunk, int& 
     chunk = (chunk + 15) & ~15;
     ns = (L + chunk - 1) / chunk;
 }
-// Short caches: at most `ranks` splits.
-__host__ __device__ __forceinline__ void kv4_cluster_plan(int L, int ranks, int& chunk, int& ns) {
-    chunk = ((L + ranks - 1) / ranks + 15) & ~15;
+// Short caches: 128 to 256 positions, at most 8 splits.
+__host__ __device__ __forceinline__ void kv4_cluster_plan(int L, int& chunk, int& ns) {
+    chunk = ((L + kKv4ClusterSplits - 1) / kKv4ClusterSplits + 15) & ~15;
     if (chunk < kKv4MinChunk) chunk = kKv4MinChunk;
     ns = (L + chunk - 1) / chunk;
 }

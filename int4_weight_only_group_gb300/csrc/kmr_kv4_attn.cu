@@ -117,10 +117,14 @@ struct SplitSmem {
     __host__ __device__ static constexpr int merge(int rep) { return kWarps * rep * (D + 2) * 4; }
     static constexpr int kQuery = 4 * (D / 32) + D / G + 1;         // words of a lane's query per n-tile
     __host__ __device__ static constexpr int query(int rep) { return (rep <= 4 ? 1 : 2) * kQuery * 128; }
-    __host__ __device__ static constexpr int base(int rep) { return 128 + query(rep) + (kRing > merge(rep) ? kRing : merge(rep)); }
-    // a cluster's additions: the states pushed here (a slice of o from every split; every m and l), the scores
-    __host__ __device__ static constexpr int state(int rep) { return rep * D * 4 + kKv4ClusterSplits * rep * 8; }
-    __host__ __device__ static constexpr int total(int rep, int chunk) { return base(rep) + state(rep) + rep * chunk * 4; }
+    __host__ __device__ static constexpr int base(int rep) { return 128 + query(rep) + kRing + merge(rep); }
+    // a cluster's additions: the states pushed here (a slice of o of every split; every m and l), the scores
+    __host__ __device__ static constexpr int state(int rep, int ranks) {
+        return kKv4ClusterSplits * (rep * D / ranks * 4 + rep * 8);
+    }
+    __host__ __device__ static constexpr int total(int rep, int ranks, int positions) {
+        return base(rep) + state(rep, ranks) + rep * positions * 4;
+    }
 };
 
 // Tiles that a warp takes together: two chains of products to interleave where the registers allow it.
@@ -249,12 +253,14 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         const int L = p.cpos[b] + 1;
         int chunk, ns;
         if (CL)
-            kv4_cluster_plan(L, int(gridDim.x), chunk, ns);
+            kv4_cluster_plan(L, chunk, ns);
         else
             kv4_split_plan(L, chunk, ns);
-        if (!CL && s >= ns) return;
-        const int t0 = min(s * chunk, L), t1 = min(L, t0 + chunk);       // a cluster's spare splits are empty
-        const int nst = (t1 - t0 + kStagePos - 1) / kStagePos;
+        // this CTA's splits, and the stages of all of them (a cluster's spare CTAs have none); one, beyond a cluster
+        const int u0 = CL ? s * p.per : s, u1 = CL ? min(ns, u0 + p.per) : s + 1;
+        if (!CL && u0 >= ns) return;
+        const int end = min(L, u1 * chunk), per_split = (chunk + kStagePos - 1) / kStagePos;
+        const int nst = u0 < u1 ? (u1 - u0 - 1) * per_split + (end - (u1 - 1) * chunk + kStagePos - 1) / kStagePos : 0;
         if (CL && !first) {
             cluster_arrive();
             cluster_wait();                           // what the last row pushed has been read, and the ring
@@ -263,11 +269,12 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 
         // One stage: lanes 0..3 of the calling warp copy K codes, V codes, K words and V words of up to
         // kStagePos positions (rounded up to 16: within the row, whose length is a multiple of 16).
-        auto issue = [&](int st) {
-            const uint32_t slot_of = (uses + st) % kStages;
+        auto issue = [&](int k) {
+            const uint32_t slot_of = (uses + k) % kStages;
             uint8_t* buf = ring + slot_of * M::kStage;
-            const int pa = t0 + st * kStagePos;
-            const uint32_t np = uint32_t(min(kStagePos, ((t1 - pa) + 15) & ~15));
+            const int split0 = CL ? (u0 + k / per_split) * chunk : u0 * chunk;
+            const int pa = split0 + (CL ? k % per_split : k) * kStagePos;
+            const uint32_t np = uint32_t(min(kStagePos, (min(L, split0 + chunk) - pa + 15) & ~15));
             if (lane == 0) mbar_arrive_expect_tx(&full[slot_of], np * (D + 8 * NG));
             __syncwarp();
             if (lane < 4) {
@@ -306,293 +313,294 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             fac[n] = __uint_as_float(at[(4 * HB + HG) * 32]);
         }
 
-        float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][HG];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            m[n] = -INFINITY;
-            l[n] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
-#pragma unroll
-            for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
-        }
-        int eref = 5;                                 // exponent that the output accumulators are scaled by
-        // base-2 scores for the mass: [head][position], in shared memory from the split's first position on
+        // base-2 scores for the mass: [head][position], in shared memory from the CTA's first position on
         float* sc_out = nullptr;
         size_t sc_ld = p.c.S;
         if (CL && p.mass) {
-            sc_ld = p.chunk_max;
-            sc_out = reinterpret_cast<float*>(smem + M::base(rep) + M::state(rep)) - t0;
+            sc_ld = p.score_ld;
+            sc_out = reinterpret_cast<float*>(smem + M::base(rep) + M::state(rep, int(gridDim.x))) - u0 * chunk;
         } else if (!CL && p.scores) {
             sc_out = p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S;
         }
 
-        for (int st = 0; st < nst; ++st) {
-            const uint32_t slot_of = (uses + st) % kStages, phase = ((uses + st) / kStages) & 1u;
-            const uint8_t* buf = ring + slot_of * M::kStage;
-            mbar_wait(&full[slot_of], phase, p.err);
-            const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
-            if (base0 < t1) {
-                // a tile is whole but for the row's last ones; one past the end counts for nothing
-                const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
-                // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
-                float sc[TT][NT][2];
-                uint32_t top = 0u;
-#pragma unroll
-                for (int u = 0; u < TT; ++u) {
-                    const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
-                    uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
-                    lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
-                    lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
-                    lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
-                    lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
-                    float zc[NT][2];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = zc[n][0] = zc[n][1] = 0.f;
-#pragma unroll
-                    for (int gr = 0; gr < HG; ++gr) {
-                        float acc[NT][4];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
-#pragma unroll
-                        for (int kb = 0; kb < BPG; ++kb) {
-                            const int k = gr * BPG + kb;
-                            uint32_t x[4], y[4];
-                            unpack_codes<0>(k0[k], x);
-                            unpack_codes<0>(k1[k], y);
-                            if constexpr (PAIR) {
-                                uint32_t xh[4], yh[4];
-                                unpack_codes<0>(k0[k + HB], xh);
-                                unpack_codes<0>(k1[k + HB], yh);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    mma_f16(acc[0], x[i], y[i], xh[i], yh[i], qf[0][k][i], qf[0][k + HB][i]);
-                            } else {
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
-                                    mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
-                            sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
-                            zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
-                            zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
-                        }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
-                        sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
-                        if constexpr (PAIR) {
-                            // the other half's part is two lanes away; both lanes add the same two numbers
-                            sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);
-                            sc[u][n][1] += __shfl_xor_sync(0xffffffffu, sc[u][n][1], 2);
-                        }
-                        if (!whole) {
-                            if (base + g >= t1) sc[u][n][0] = -INFINITY;
-                            if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
-                        }
-                        if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
-                            float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
-                            if (whole || base + g < t1) dst[0] = sc[u][n][0];
-                            if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
-                        }
-                    }
-                    uint32_t mine[(NG + 1) / 2];
-                    const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
-                    lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
-                    if (whole || base + wpos < t1) {
-                        top = max(top, mine[0] & 0x7FFFFFFFu);
-                        if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
-                    }
-                }
-                const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
-                // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
-                // above, so that most tiles rescale nothing; weights stay below 2^8
-                float mn[NT];
-                bool up = etop > eref;
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float c = fmaxf(sc[0][n][0], sc[0][n][1]);
-                    if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
-                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
-                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
-                    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
-                    mn[n] = fmaxf(m[n], c);
-                    up |= mn[n] > m[n] + 8.f;
-                }
-                if (__any_sync(0xffffffffu, up)) {
-                    // room of two octaves, so that scales a little larger do not rescale again
-                    const int en = etop > eref ? min(etop + 2, 254) : eref;
-                    const float es = exp2f(float(eref - en));
-                    eref = en;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
-                        m[n] = mn[n];
-                        l[n] *= cf;
-                        const float ce = cf * es;
-#pragma unroll
-                        for (int i = 0; i < 2 * NB; ++i)
-#pragma unroll
-                            for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
-#pragma unroll
-                        for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
-                    }
-                }
-                const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
-#pragma unroll
-                for (int u = 0; u < TT; ++u) {
-                    const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
-                    // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
-                    const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
-                    uint32_t v0[HG], v1[HG], vw[4][HG];
-                    lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
-                    lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
-                    if (!whole) {
-                        // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
-#pragma unroll
-                        for (int gr = 0; gr < HG; ++gr) {
-                            if (base + g >= t1) v0[gr] = 0u;
-                            if (base + g + 8 >= t1) v1[gr] = 0u;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i)
-                                if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
-                        }
-                    }
-                    // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
-                    // column's head at the lane's four positions
-                    float w[NT][4];
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        const float mm = m[n] == -INFINITY ? 0.f : m[n];
-                        const float p0 = exp2_approx(__fsub_rn(sc[u][n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[u][n][1], mm));
-                        l[n] += p0 + p1;
-#pragma unroll
-                        for (int gr = 0; gr < HG; ++gr) {
-                            zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
-                            zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
-                        }
-                        const float u0 = p0 * unit, u1 = p1 * unit;
-                        const int src = 4 * t + column_head<PAIR>(g);
-                        w[n][0] = __shfl_sync(0xffffffffu, u0, src);
-                        w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
-                        w[n][2] = __shfl_sync(0xffffffffu, u1, src);
-                        w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
-                    }
-                    // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
-                    // of half 0 in rows g, of half 1 in rows g + 8
-                    uint32_t vc[4][NB / 2];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
-                    auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
-                        const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
-                        unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
-                        unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
-                    };
-#pragma unroll
-                    for (int gr = 0; gr < HG; ++gr) {
-                        uint32_t wf[NT][2];
-#pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            float a[4];
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
-                            wf[n][0] = pack_f16_rz(a[0], a[1]);
-                            wf[n][1] = pack_f16_rz(a[2], a[3]);
-                        }
-#pragma unroll
-                        for (int kb = 0; kb < BPG; ++kb) {
-                            const int k = gr * BPG + kb;
-                            uint32_t x[4], y[4];
-                            unpack_block(k, x, y);
-                            if constexpr (PAIR) {
-                                uint32_t xh[4], yh[4];
-                                unpack_block(k + HB, xh, yh);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    mma_f16(o[0][4 * k + i], x[i], xh[i], y[i], yh[i], wf[0][0], wf[0][1]);
-                            } else {
-#pragma unroll
-                                for (int n = 0; n < NT; ++n) {
-                                    mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
-                                    mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
-                                }
-                            }
-                        }
-                    }
-                }
-            }
-            // the warps take turns to refill the stage once all are done with it
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&empty[slot_of]);
-            if (st + kStages < nst && warp == (st & (kWarps - 1))) {
-                mbar_wait(&empty[slot_of], phase, p.err);
-                fence_proxy_async_smem();
-                issue(st + kStages);
-            }
-        }
-        uses += nst;
-        __syncthreads();                              // every copy has landed and been read: the ring is free
-
-        // ---- the warp's state: o[head][dim], m, l
-        float* wo = reinterpret_cast<float*>(ring);                       // [warp][rep][D]
-        float* wml = wo + kWarps * rep * D;                               // [warp][rep][2]
-        const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int hq = PAIR ? t & 1 : 4 * n + t;
-            float lt = l[n];
-            lt += __shfl_xor_sync(0xffffffffu, lt, 4);
-            lt += __shfl_xor_sync(0xffffffffu, lt, 8);
-            lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-            float zt[HG];
-#pragma unroll
-            for (int gr = 0; gr < HG; ++gr) {
-                float v = zo[n][gr];
-                v += __shfl_xor_sync(0xffffffffu, v, 4);
-                v += __shfl_xor_sync(0xffffffffu, v, 8);
-                zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
-            }
-            if (hq < rep) {
-                if (g == 0 && cth == 0) {
-                    wml[(warp * rep + hq) * 2] = m[n];
-                    wml[(warp * rep + hq) * 2 + 1] = lt;
-                }
-#pragma unroll
-                for (int k = 0; k < HB; ++k) {
-                    const float z = zt[k / BPG];
-                    float v[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        if constexpr (PAIR) {
-                            const float(&a)[4] = o[n][4 * k + i];
-                            v[i] = cth ? a[2] + a[3] : a[0] + a[1];
-                        } else {
-                            const float(&a)[4] = o[n][2 * k + i / 2];
-                            v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
-                        }
-                        v[i] = __fmaf_rn(v[i], un, z);
-                    }
-                    *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
-                        make_float4(v[0], v[1], v[2], v[3]);
-                }
-            }
-        }
-        __syncthreads();
-        float* part = CL ? nullptr : p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + s) * rep * (D + 2);
+        float* wo = reinterpret_cast<float*>(ring + M::kRing);           // [warp][rep][D]
+        float* wml = wo + kWarps * rep * D;                              // [warp][rep][2]
         const int ranks = CL ? int(gridDim.x) : 1, slice = rep * D / ranks;         // of the output, for each rank
-        float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [source][slice]
-        float* recv_ml = recv + rep * D;                                             // [source][head][m, l]
-        if (CL && first) cluster_wait();
-        if (s < ns) {
+        float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [split][slice]
+        float* recv_ml = recv + kKv4ClusterSplits * slice;                           // [split][head][m, l]
+        int k = 0;                                    // stage of the CTA
+        for (int u = u0; u < u1; ++u) {
+            const int t0 = u * chunk, t1 = min(L, t0 + chunk);
+            float m[NT], l[NT], o[NT][2 * NB][4], zo[NT][HG];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                m[n] = -INFINITY;
+                l[n] = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2 * NB; ++i) o[n][i][0] = o[n][i][1] = o[n][i][2] = o[n][i][3] = 0.f;
+#pragma unroll
+                for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
+            }
+            int eref = 5;                                 // exponent that the output accumulators are scaled by
+            for (int st = 0; t0 + st * kStagePos < t1; ++st, ++k) {
+                const uint32_t slot_of = (uses + k) % kStages, phase = ((uses + k) / kStages) & 1u;
+                const uint8_t* buf = ring + slot_of * M::kStage;
+                mbar_wait(&full[slot_of], phase, p.err);
+                const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
+                if (base0 < t1) {
+                    // a tile is whole but for the row's last ones; one past the end counts for nothing
+                    const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
+                    // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
+                    float sc[TT][NT][2];
+                    uint32_t top = 0u;
+#pragma unroll
+                    for (int u = 0; u < TT; ++u) {
+                        const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                        uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
+                        lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
+                        lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
+                        lds_words(buf + 2 * M::kCodes + (i0 + g) * (4 * NG) + cth * (4 * HG), w0);
+                        lds_words(buf + 2 * M::kCodes + (i0 + g + 8) * (4 * NG) + cth * (4 * HG), w1);
+                        float zc[NT][2];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) sc[u][n][0] = sc[u][n][1] = zc[n][0] = zc[n][1] = 0.f;
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            float acc[NT][4];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
+#pragma unroll
+                            for (int kb = 0; kb < BPG; ++kb) {
+                                const int k = gr * BPG + kb;
+                                uint32_t x[4], y[4];
+                                unpack_codes<0>(k0[k], x);
+                                unpack_codes<0>(k1[k], y);
+                                if constexpr (PAIR) {
+                                    uint32_t xh[4], yh[4];
+                                    unpack_codes<0>(k0[k + HB], xh);
+                                    unpack_codes<0>(k1[k + HB], yh);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        mma_f16(acc[0], x[i], y[i], xh[i], yh[i], qf[0][k][i], qf[0][k + HB][i]);
+                                } else {
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        mma_f16(acc[n], x[0], y[0], x[1], y[1], qf[n][k][0], qf[n][k][1]);
+                                        mma_f16(acc[n], x[2], y[2], x[3], y[3], qf[n][k][2], qf[n][k][3]);
+                                    }
+                                }
+                            }
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
+                                sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
+                                zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
+                                zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
+                            }
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
+                            sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
+                            if constexpr (PAIR) {
+                                // the other half's part is two lanes away; both lanes add the same two numbers
+                                sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);
+                                sc[u][n][1] += __shfl_xor_sync(0xffffffffu, sc[u][n][1], 2);
+                            }
+                            if (!whole) {
+                                if (base + g >= t1) sc[u][n][0] = -INFINITY;
+                                if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
+                            }
+                            if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
+                                float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
+                                if (whole || base + g < t1) dst[0] = sc[u][n][0];
+                                if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
+                            }
+                        }
+                        uint32_t mine[(NG + 1) / 2];
+                        const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
+                        lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
+                        if (whole || base + wpos < t1) {
+                            top = max(top, mine[0] & 0x7FFFFFFFu);
+                            if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
+                        }
+                    }
+                    const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
+                    // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
+                    // above, so that most tiles rescale nothing; weights stay below 2^8
+                    float mn[NT];
+                    bool up = etop > eref;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        float c = fmaxf(sc[0][n][0], sc[0][n][1]);
+                        if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
+                        c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
+                        c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
+                        c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
+                        mn[n] = fmaxf(m[n], c);
+                        up |= mn[n] > m[n] + 8.f;
+                    }
+                    if (__any_sync(0xffffffffu, up)) {
+                        // room of two octaves, so that scales a little larger do not rescale again
+                        const int en = etop > eref ? min(etop + 2, 254) : eref;
+                        const float es = exp2f(float(eref - en));
+                        eref = en;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
+                            m[n] = mn[n];
+                            l[n] *= cf;
+                            const float ce = cf * es;
+#pragma unroll
+                            for (int i = 0; i < 2 * NB; ++i)
+#pragma unroll
+                                for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
+#pragma unroll
+                            for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
+                        }
+                    }
+                    const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
+#pragma unroll
+                    for (int u = 0; u < TT; ++u) {
+                        const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                        // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
+                        const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
+                        uint32_t v0[HG], v1[HG], vw[4][HG];
+                        lds_words(words + g * (4 * NG) + cth * (4 * HG), v0);
+                        lds_words(words + (g + 8) * (4 * NG) + cth * (4 * HG), v1);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) lds_words(words + (t + 4 * i) * (4 * NG) + cgh * (4 * HG), vw[i]);
+                        if (!whole) {
+                            // past the row's end the words are leftovers, and may be NaN: weight 0 would not hide that
+#pragma unroll
+                            for (int gr = 0; gr < HG; ++gr) {
+                                if (base + g >= t1) v0[gr] = 0u;
+                                if (base + g + 8 >= t1) v1[gr] = 0u;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
+                            }
+                        }
+                        // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
+                        // column's head at the lane's four positions
+                        float w[NT][4];
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const float mm = m[n] == -INFINITY ? 0.f : m[n];
+                            const float p0 = exp2_approx(__fsub_rn(sc[u][n][0], mm)), p1 = exp2_approx(__fsub_rn(sc[u][n][1], mm));
+                            l[n] += p0 + p1;
+#pragma unroll
+                            for (int gr = 0; gr < HG; ++gr) {
+                                zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
+                                zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
+                            }
+                            const float u0 = p0 * unit, u1 = p1 * unit;
+                            const int src = 4 * t + column_head<PAIR>(g);
+                            w[n][0] = __shfl_sync(0xffffffffu, u0, src);
+                            w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
+                            w[n][2] = __shfl_sync(0xffffffffu, u1, src);
+                            w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
+                        }
+                        // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
+                        // of half 0 in rows g, of half 1 in rows g + 8
+                        uint32_t vc[4][NB / 2];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            lds_words(buf + M::kCodes + (i0 + t + 4 * i) * (D / 2) + g * (2 * NB), vc[i]);
+                        auto unpack_block = [&](int k, uint32_t (&x)[4], uint32_t (&y)[4]) {
+                            const uint32_t sel = (k & 1) ? 0x7632u : 0x5410u;
+                            unpack_codes<8>(__byte_perm(vc[0][k >> 1], vc[1][k >> 1], sel), x);
+                            unpack_codes<7>(__byte_perm(vc[2][k >> 1], vc[3][k >> 1], sel), y);
+                        };
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            uint32_t wf[NT][2];
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                float a[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
+                                wf[n][0] = pack_f16_rz(a[0], a[1]);
+                                wf[n][1] = pack_f16_rz(a[2], a[3]);
+                            }
+#pragma unroll
+                            for (int kb = 0; kb < BPG; ++kb) {
+                                const int k = gr * BPG + kb;
+                                uint32_t x[4], y[4];
+                                unpack_block(k, x, y);
+                                if constexpr (PAIR) {
+                                    uint32_t xh[4], yh[4];
+                                    unpack_block(k + HB, xh, yh);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i)
+                                        mma_f16(o[0][4 * k + i], x[i], xh[i], y[i], yh[i], wf[0][0], wf[0][1]);
+                                } else {
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        mma_f16(o[n][2 * k], x[0], x[1], y[0], y[1], wf[n][0], wf[n][1]);
+                                        mma_f16(o[n][2 * k + 1], x[2], x[3], y[2], y[3], wf[n][0], wf[n][1]);
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+                // the warps take turns to refill the stage once all are done with it
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[slot_of]);
+                if (k + kStages < nst && warp == (k & (kWarps - 1))) {
+                    mbar_wait(&empty[slot_of], phase, p.err);
+                    fence_proxy_async_smem();
+                    issue(k + kStages);
+                }
+            }
+
+            // ---- the warp's state: o[head][dim], m, l
+            if (u > u0) __syncthreads();                  // the split before this one has been merged
+            const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int hq = PAIR ? t & 1 : 4 * n + t;
+                float lt = l[n];
+                lt += __shfl_xor_sync(0xffffffffu, lt, 4);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 8);
+                lt += __shfl_xor_sync(0xffffffffu, lt, 16);
+                float zt[HG];
+#pragma unroll
+                for (int gr = 0; gr < HG; ++gr) {
+                    float v = zo[n][gr];
+                    v += __shfl_xor_sync(0xffffffffu, v, 4);
+                    v += __shfl_xor_sync(0xffffffffu, v, 8);
+                    zt[gr] = v + __shfl_xor_sync(0xffffffffu, v, 16);
+                }
+                if (hq < rep) {
+                    if (g == 0 && cth == 0) {
+                        wml[(warp * rep + hq) * 2] = m[n];
+                        wml[(warp * rep + hq) * 2 + 1] = lt;
+                    }
+#pragma unroll
+                    for (int k = 0; k < HB; ++k) {
+                        const float z = zt[k / BPG];
+                        float v[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            if constexpr (PAIR) {
+                                const float(&a)[4] = o[n][4 * k + i];
+                                v[i] = cth ? a[2] + a[3] : a[0] + a[1];
+                            } else {
+                                const float(&a)[4] = o[n][2 * k + i / 2];
+                                v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
+                            }
+                            v[i] = __fmaf_rn(v[i], un, z);
+                        }
+                        *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
+                            make_float4(v[0], v[1], v[2], v[3]);
+                    }
+                }
+            }
+            __syncthreads();
+            float* part = CL ? nullptr : p.part + ((size_t(b) * p.c.nkv + h) * p.nsplit + u) * rep * (D + 2);
+            if (CL && first && u == u0) cluster_wait();
             for (int i = tid; i < rep * (D / 4); i += kThr) {
                 const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
                 float mw[kWarps], mx = -INFINITY, den = 0.f;
@@ -612,10 +620,10 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 if constexpr (CL) {
                     const int at = hq * D + dim;
                     float* to = cg::this_cluster().map_shared_rank(recv, at / slice);
-                    *reinterpret_cast<float4*>(to + s * slice + at % slice) = num;
+                    *reinterpret_cast<float4*>(to + u * slice + at % slice) = num;
                     if (dim == 0)
                         for (int r = 0; r < ranks; ++r)
-                            *reinterpret_cast<float2*>(cg::this_cluster().map_shared_rank(recv_ml, r) + (s * rep + hq) * 2) =
+                            *reinterpret_cast<float2*>(cg::this_cluster().map_shared_rank(recv_ml, r) + (u * rep + hq) * 2) =
                                 make_float2(mx, den);
                 } else {
                     float* dst = part + hq * (D + 2);
@@ -625,6 +633,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 }
             }
         }
+        uses += nst;
+        if (CL && first && u0 >= u1) cluster_wait();
         if (!CL) return;
         // ---- every split's state is here: this rank's slice of the output, and its own positions' mass
         cluster_arrive();
@@ -654,7 +664,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             hl[tid] = __frcp_rn(den);
         }
         __syncthreads();
-        for (int i = t0 + tid; i < t1; i += kThr) {
+        for (int i = u0 * chunk + tid; i < end; i += kThr) {
             float add = 0.f;
             for (int k = 0; k < rep; ++k) add = __fmaf_rn(exp2_approx(__fsub_rn(sc_out[k * sc_ld + i], hm[k])), hl[k], add);
             __stcg(p.mass + row + i, __ldcg(p.mass + row + i) + add);    // (another SM's, of the row before)
@@ -806,18 +816,22 @@ struct SplitVariant {
     const void* fn;
     int smem;
 };
-// chunk: positions whose scores a cluster's split keeps (0: none, or no cluster)
+// A cluster of `ranks` CTAs whose scores, `positions` of each, stay in shared memory (0: no mass); ranks 0: no cluster.
 template <int D, int G>
-SplitVariant split_variant(int rep, bool cl, int chunk) {
+SplitVariant split_variant(int rep, int ranks, int positions) {
     using S1 = SplitSmem<D, G, tiles_of(1)>;
     using S2 = SplitSmem<D, G, tiles_of(2)>;
-    const int smem = rep <= 4 ? (cl ? S1::total(rep, chunk) : S1::base(rep)) : (cl ? S2::total(rep, chunk) : S2::base(rep));
-    return {split_fn<D, G>(rep, cl), smem};
+    int smem;
+    if (rep <= 4)
+        smem = ranks ? S1::total(rep, ranks, positions) : S1::base(rep);
+    else
+        smem = ranks ? S2::total(rep, ranks, positions) : S2::base(rep);
+    return {split_fn<D, G>(rep, ranks > 0), smem};
 }
-SplitVariant split_variant(int d, int g, int rep, bool cl, int chunk) {
-    if (d == 64) return g == 32 ? split_variant<64, 32>(rep, cl, chunk) : split_variant<64, 64>(rep, cl, chunk);
-    if (g == 32) return split_variant<128, 32>(rep, cl, chunk);
-    return g == 64 ? split_variant<128, 64>(rep, cl, chunk) : split_variant<128, 128>(rep, cl, chunk);
+SplitVariant split_variant(int d, int g, int rep, int ranks, int positions) {
+    if (d == 64) return g == 32 ? split_variant<64, 32>(rep, ranks, positions) : split_variant<64, 64>(rep, ranks, positions);
+    if (g == 32) return split_variant<128, 32>(rep, ranks, positions);
+    return g == 64 ? split_variant<128, 64>(rep, ranks, positions) : split_variant<128, 128>(rep, ranks, positions);
 }
 
 }  // namespace
@@ -836,11 +850,12 @@ cudaError_t kv4_attn_set_attributes() {
     const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
     for (const auto& sh : shapes)
         for (int rep : {2, 4, 8})
-            for (bool cl : {false, true}) {
-                const SplitVariant v = split_variant(sh[0], sh[1], rep, cl, kKv4ClusterLen / kKv4ClusterSplits);
+            for (int ranks : {0, 1}) {
+                const SplitVariant v = split_variant(sh[0], sh[1], rep, ranks, kKv4ClusterLen);
                 cudaError_t e = cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem);
                 if (e != cudaSuccess) return e;
-                e = cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+                e = cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                         cudaSharedmemCarveoutMaxShared);
                 if (e != cudaSuccess) return e;
             }
     return cudaSuccess;
@@ -859,10 +874,17 @@ cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.c.S <= kKv4ClusterLen) {
-        int ranks = 1, ns;                        // 1, 2, 4 or 8 splits: as many as the longest row fills
-        while (ranks < kKv4ClusterSplits && ranks * kKv4MinChunk < p.c.S) ranks *= 2;
-        kv4_cluster_plan(p.c.S, ranks, q.chunk_max, ns);
-        const SplitVariant v = split_variant(p.c.d, p.c.g, rep, true, p.mass ? q.chunk_max : 0);
+        int chunk, splits, ranks = 1;
+        kv4_cluster_plan(p.c.S, chunk, splits);
+        while (ranks < splits) ranks *= 2;
+        // CTAs that run at a time: more than that only queue, and pay their start and end each, so then a CTA takes
+        // several splits of its row, one after the other, which changes no result (16 rows of 1024: 13.2 -> 10.3 us; the
+        // longer caches' splits of 256 gained nothing by it, 47.4 against 48.2 us for 16 rows of 8192)
+        const long long slots = (rep <= 4 ? 4LL : 2LL) * num_sms(), rows = (long long)p.c.nkv * p.B;
+        while (ranks > 1 && ranks * rows > slots) ranks /= 2;
+        q.per = (splits + ranks - 1) / ranks;
+        q.score_ld = q.per * chunk;
+        const SplitVariant v = split_variant(p.c.d, p.c.g, rep, ranks, p.mass ? q.score_ld : 0);
         cfg.gridDim = dim3(ranks, p.c.nkv, p.B);
         cfg.dynamicSmemBytes = v.smem;
         attr[1].id = cudaLaunchAttributeClusterDimension;
@@ -872,7 +894,7 @@ cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
         cfg.numAttrs = 2;
         return cudaLaunchKernelExC(&cfg, v.fn, args);
     }
-    const SplitVariant v = split_variant(p.c.d, p.c.g, rep, false, 0);
+    const SplitVariant v = split_variant(p.c.d, p.c.g, rep, 0, 0);
     cfg.gridDim = dim3(p.nsplit, p.c.nkv, p.B);
     cfg.dynamicSmemBytes = v.smem;
     cudaError_t e = cudaLaunchKernelExC(&cfg, v.fn, args);
