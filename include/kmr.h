@@ -294,7 +294,7 @@ int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf
 
 /* kmr_decode_attn over the 4-bit cache: out = softmax(q K^T scale) V of one token per row over positions
  * 0..cache_position[b] of slot slot_ids[b].  The split plan depends on the row's own length and on max_len
- * (up to 4096 positions the splits of a row are one thread-block cluster and the call one launch, beyond it is
+ * (up to 2048 the splits of a row merge in a thread-block cluster and the call is one launch, beyond it is
  * two): a row's result does not depend on the other rows.
  *   q     device fp32 [B, n_q, d], 16-byte aligned; n_q is 1..8 times n_kv, query head i reads KV head
  *         i / (n_q / n_kv)

@@ -1,4 +1,4 @@
-// The 4-bit KV cache: addressing, the group quantiser and the parameter blocks of its kernels.
+// The 4-bit KV cache: its format, the attention's split plans and the parameter blocks of its kernels.
 //
 // A cached vector (one slot, KV head and position; d = 64 or 128 dims) holds 4-bit codes c and,
 // for every group of 32, 64 or 128 dims, a bf16 scale s and a bf16 base z: value = c s + z.

@@ -133,7 +133,8 @@ extern "C" int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, c
     const int rc = view_of(cache, &p.c);
     if (rc != KMR_OK) return rc;
     if (!q || !slot_ids || !cache_position || !out || !workspace) return KMR_ERR_INVALID_ARG;
-    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned16(mass) || !std::isfinite(scale)) return KMR_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(out) || !aligned16(workspace) || !aligned16(mass) || !std::isfinite(scale))
+        return KMR_ERR_INVALID_ARG;
     if (B < 1 || B > kKv4MaxRows) return KMR_ERR_BATCH;
     if (!heads_ok(nq, p.c.nkv)) return KMR_ERR_SHAPE;
     if (workspace_bytes < kmr_decode_attn_kv4_workspace_size(cache, B, nq, mass != nullptr)) return KMR_ERR_BUFFER_SIZE;

@@ -3,12 +3,14 @@
 // out = softmax(q K^T scale) V over positions 0..cache_position of the row's slot, and, where a mass
 // is given, mass[slot][head][p] += the sum over the KV head's query heads of position p's weight.
 // A (row, KV head) is cut into splits, whose softmax states (m, l, o) in base 2 merge in split order:
-//   * caches of up to 4096 positions: one launch, the up to 8 splits are a thread-block cluster.  Each pushes its
-//     state into the others' shared memory; after one cluster barrier each merges a slice of the output and
-//     turns the scores of its own positions, kept in shared memory, into mass.  Of rows that share a slot the
+//   * caches of up to 2048 positions: one launch, the CTAs of a row's up to 8 splits are a thread-block cluster.  Each
+//     pushes its states into the others' shared memory; after one cluster barrier each merges a slice of the output
+//     and turns the scores of its own positions, kept in shared memory, into mass.  Of rows that share a slot the
 //     first one's cluster takes all in turn, so that the mass gains them in row order.
 //   * longer caches: up to 76 splits leave their states in the workspace (and, for the mass, every score); a
 //     second launch, a programmatic dependent of the first, merges and adds, again in row order.
+// One launch against two, 16/8 heads of 128, us: 5.0 / 5.6 (1 row of 1024), 5.4 / 7.9 (4 rows), 6.1 / 6.0 and 6.6 / 8.6 at
+// 2048, 8.4 / 7.2 and 9.5 / 11.0 at 4096, where eight CTAs a head begin to be too few.
 //
 // The bound is HBM: 2 (d/2 + 4 d/g) bytes per position and KV head.  At d = 128, g = 32 an SM's share
 // of the bandwidth is about 36 codes per cycle, too many for dequantising and multiplying on the CUDA
@@ -16,8 +18,8 @@
 // tcgen05 tile 15/16 empty) with the codes as the A operand:
 //   * a nibble c under the exponent of 1024 is the fp16 1024 + c (from bits 4..7: 1024 + 16 c); one packed fp16
 //     operation takes the offset off again, exactly.  (As a bare subnormal c 2^-24 it would cost one operation
-//     less, but the tensor core aligns its sums by the operands' exponent fields and a subnormal code then
-//     loses up to 10 of the accumulator's bits: outputs of a 8191-position row were off by 1e-4.)
+//     less, but a subnormal code was found to lose up to 10 of the accumulator's bits: outputs of a row of 8191
+//     positions were off by 1e-4.)
 //   * the other operand is fp32 split in two fp16 columns (high and low part, about 22 bits), so the result keeps
 //     single precision: columns 2 h and 2 h + 1 belong to query head h and land in one lane's accumulators.
 //   * scores: A = 16 positions x 16 dims, B = the query.  sum_j q_j (c_j s + z) = s sum q c + z sum q per group:
@@ -32,7 +34,14 @@
 // stand for the halves of the head's dims: column 4 f + 2 h + part is query head h in half f.  A step of the scores
 // has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
 // dims of either half in its upper and lower rows.  The products are as many, but each lane folds, weighs and
-// splits for its half's groups only: 481 -> @@ instructions per tile of 16 positions at d = 128, g = 32.
+// splits for its half's groups only: 413 instructions per tile of 16 positions at d = 128, g = 32 instead of 481 (385 with two
+// tiles taken together).
+//
+// Measured, 16/8 heads of 128: 16 rows of 8192, group 32, 47.4 us (168 MB: 3.5 TB/s, 0.53 of the measured copy rate); one
+// row of 131072, 43.2 us (0.58), group 128, 38.6 us (143 MB, 0.55).  What bounds it now is the arithmetic: with the
+// tiles' work left out the same copies take 34 us, with every row in L2 the whole kernel 44.  The ALU pipe is busy 55% of
+// the time, no pipe more; leaving the V codes' unpacking out gains 6 us, the K codes' 3, the weights' splitting 1.4, the
+// products nothing.  Five CTAs an SM (96 registers) or three (a third stage) instead of four measure the same or worse.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -127,7 +136,8 @@ struct SplitSmem {
     }
 };
 
-// Tiles that a warp takes together: two chains of products to interleave where the registers allow it.
+// Tiles that a warp takes together: two chains of products to interleave where the registers allow it (one row of 8192:
+// 9.1 -> 8.0 us; 16 rows 53.4 -> 47.4).
 __host__ __device__ constexpr int tiles_of(int NT) { return NT == 1 ? 2 : 1; }
 
 // Query head, half of the dims and part (0 high, 1 low) of an n-tile's column.
@@ -197,7 +207,9 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
     }
 }
 
-// NT: n-tiles of 4 query heads; PAIR: one n-tile of 2 heads whose halves' groups are kept apart (see above).
+// One CTA of four warps, a ring of stages of 16 TT positions a warp filled by bulk copies (four lanes, one array each).
+// A stage's four warps meet only at its barriers; a row's last tile masks by select, since what lies past the row's end
+// may be NaN.  NT: n-tiles of 4 query heads; PAIR: one n-tile of 2 heads whose halves' groups are kept apart (see above).
 template <int D, int G, int NT, bool PAIR, bool CL>
 __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const Kv4AttnParams p) {
     constexpr int TT = tiles_of(NT);
@@ -674,7 +686,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 }
 
 // Second launch, grid (rep + position blocks, KV head, row): block x < rep merges the splits of query head x, the
-// others add the mass of kMassPos positions each.
+// others add the mass of kMassPos positions each.  Reads the states (1 KB per split and pair of heads) and, for the mass,
+// the scores from L2: 3 to 4 us, most of it the launch.
 constexpr int kMassPos = kMergeThr * 4;
 
 // One query head's split states by one warp: weight[s] = 2^(m_s - max m) (if given), and max m and 1 / sum l.

@@ -108,7 +108,7 @@ def test_workspace_size(L):
     assert 0 < W(a, 1, 16, 0) < W(a, 4, 16, 0) and W(a, 1, 16, 1) == W(a, 1, 16, 0) + 16 * 8192 * 4
     assert W(a, 0, 16, 0) == W(a, 1, 12, 0) == W(a, 1025, 16, 0) == W(None, 1, 16, 0) == 0
     assert W(ctypes.addressof(cache(group=48)), 1, 16, 0) == 0
-    assert W(ctypes.addressof(cache(max_len=4096)), 4, 16, 1) == 16           # short caches merge on chip
+    assert W(ctypes.addressof(cache(max_len=2048)), 4, 16, 1) == 16           # short caches merge on chip
 
 
 def test_binding_checks_the_cache_tensors(L):
