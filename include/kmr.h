@@ -232,8 +232,8 @@ int kmr_decode_attn_noalloc(const float* q, const uint16_t* k_cache, const uint1
  *   k_sz, v_sz        uint32 [slots][n_kv][max_len][d / group]: bf16 z in the low half, bf16 s in the
  *       high half.
  * All four are device memory, 16-byte aligned, owned by the caller; d is 64 or 128, group at most d,
- * n_kv at most 1024, max_len a multiple of 16 up to 2^28.  A cache that fails this gives KMR_ERR_INVALID_ARG (pointers)
- * or KMR_ERR_SHAPE.  Positions of a row that no call has written may hold anything.
+ * n_kv at most 1024, max_len a multiple of 16 up to 2^28.  A cache that fails this gives KMR_ERR_INVALID_ARG
+ * (pointers) or KMR_ERR_SHAPE.  Positions of a row that no call has written may hold anything.
  *
  * The calls below take up to 1024 rows (KMR_ERR_BATCH), queue their work on `stream` without
  * synchronising and allocate nothing; they can be captured into a graph once kmr_last_device_error()
@@ -298,16 +298,17 @@ int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf
  * two): a row's result does not depend on the other rows.
  *   q     device fp32 [B, n_q, d], 16-byte aligned; n_q is 1..8 times n_kv, query head i reads KV head
  *         i / (n_q / n_kv)
- *   mass  device fp32 [slots][n_kv][max_len], 16-byte aligned, or NULL: position p of a row's slot gains the sum of p's
- *         softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows that
- *         share a slot add in row order: the result does not change from run to run.
+ *   mass  device fp32 [slots][n_kv][max_len], 16-byte aligned, or NULL: position p of a row's slot gains the sum
+ *         of p's softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows
+ *         that share a slot add in row order: the result does not change from run to run.
  *   out   device fp32 [B, n_q, d], 16-byte aligned
  *   workspace  device memory, 16-byte aligned, kmr_decode_attn_kv4_workspace_size(cache, B, n_q, mass != NULL)
  *         bytes or more (0 for arguments that the call would refuse); no initialisation.  Calls that may
  *         overlap on the device need workspaces of their own.
  * Errors: KMR_ERR_INVALID_ARG (pointers, scale not finite), KMR_ERR_SHAPE, KMR_ERR_BATCH,
- * KMR_ERR_BUFFER_SIZE; on the device a row whose slot (KMR_ERR_SLOT_RANGE) or position (KMR_ERR_CACHE_FULL)
- * is out of range gets zeros and adds no mass. */
+ * KMR_ERR_BUFFER_SIZE.  A row of cache_position -1 is idle: zeros, no mass, its slot is not looked at.  On the
+ * device a row whose slot (KMR_ERR_SLOT_RANGE) or position (KMR_ERR_CACHE_FULL) is out of range gets zeros and adds
+ * no mass. */
 size_t kmr_decode_attn_kv4_workspace_size(const kmr_kv4_cache* cache, int B, int n_q_heads, int with_mass);
 int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_t* slot_ids,
                         const int32_t* cache_position, int B, int n_q_heads, float scale, float* mass, float* out,
@@ -319,7 +320,7 @@ int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_
  * keeps its newest min(recent, new_lengths[b]) positions and, of the older ones, those of largest mass, the
  * lower position first among equals (a NaN ranks below every number), all in ascending order; a row no
  * longer than `keep` is moved whole.  Keys keep the rotation they were written with.
- *   lengths     device int32 [B]
+ *   lengths     device int32 [B]; 0: an idle row, whose slots are not looked at
  *   keep        1..dst's max_len;  recent  0..keep
  *   mass        device fp32 [src slots][n_kv][src max_len]
  *   dst_mass    device fp32 [dst slots][n_kv][dst max_len] or NULL: receives the kept positions' mass (with

@@ -471,11 +471,13 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Whether the row may be evicted: -1, or the error code.  Uniform over the CTA.
+// Whether the row may be evicted: KMR_OK or the error.  Uniform over the CTA.
 __device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
     const int src = p.src_ids[b], dst = p.dst_ids[b], n = p.lengths[b];
+    if (n == 0) return KMR_OK;                       // an idle row: nothing moves
     int clash = 0;
     for (int r = threadIdx.x; r < p.B; r += blockDim.x) {
+        if (p.lengths[r] == 0) continue;
         clash |= r != b && p.dst_ids[r] == dst;
         clash |= p.same && p.src_ids[r] == dst;
     }

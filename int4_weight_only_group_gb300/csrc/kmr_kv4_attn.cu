@@ -57,8 +57,11 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kThr = 128, kWarps = 4;
 constexpr int kMergeThr = 256;
 
+// KMR_OK, the row's error, or kEmptyRow: nothing to attend, which is no error.
+constexpr int kEmptyRow = 1;
 __device__ __forceinline__ int kv4_row_error(const Kv4AttnParams& p, int b) {
     const int slot = p.slot_ids[b], cp = p.cpos[b];
+    if (cp == -1) return kEmptyRow;
     if (slot < 0 || slot >= p.c.slots) return KMR_ERR_SLOT_RANGE;
     return (cp < 0 || cp >= p.c.S) ? KMR_ERR_CACHE_FULL : KMR_OK;
 }
@@ -233,7 +236,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     const int bad = kv4_row_error(p, b0);
     if (bad != KMR_OK) {                          // the same for the whole cluster
         if (CL && s == 0) {
-            if (tid == 0 && h == 0) set_error(p.err, bad);
+            if (tid == 0 && h == 0 && bad != kEmptyRow) set_error(p.err, bad);
             for (int i = tid; i < rep * D; i += kThr) p.out[(size_t(b0) * p.nq + h * rep) * D + i] = 0.f;
         }
         return;
@@ -729,7 +732,7 @@ __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParam
         pdl_wait();
         const int pairs = d / 2, groups = kMergeThr / pairs, i = tid % pairs, grp = tid / pairs;
         if (err != KMR_OK) {
-            if (tid == 0 && h == 0 && hq == 0) set_error(p.err, err);
+            if (tid == 0 && h == 0 && hq == 0 && err != kEmptyRow) set_error(p.err, err);
             if (grp == 0) out[i] = make_float2(0.f, 0.f);
             return;
         }

@@ -782,3 +782,70 @@ def test_two_streams_long_rows(torch):
             ref, m = kv4.attention(q[i, b].cpu().numpy(), c.val["k"][b, :, :L], c.val["v"][b, :, :L], 0.1)
             assert rel_l2(out[0, i, b].cpu().numpy(), ref) <= ATTN_TOL
             assert np.allclose(mass[0, i, b, :, :L].cpu().numpy(), m, rtol=2e-4, atol=1e-30)
+
+
+@pytest.mark.parametrize("S", [1024, 2048, 2064])
+def test_a_row_s_bits_do_not_depend_on_the_batch(torch, S):
+    """Few rows have a CTA for every split, many rows several splits a CTA: the same output and mass, bit for bit."""
+    r = np.random.default_rng(S)
+    nq, nkv, d, g, slots = 16, 8, 128, 32, 128
+    L = r.integers(1, S + 1, slots)
+    L[:4] = [S, S - 1, 129, 1]
+    c = kmr.Kv4Cache.zeros(slots, nkv, S, d, g)
+    for t in c.tensors[:2]:
+        t.random_(0, 256)
+    for t in c.tensors[2:]:                                           # scales of about 1/4, bases of about -2
+        t.copy_(torch.from_numpy(kv4.pack_words(kv4.bf16_bits(r.uniform(0.2, 0.3, t.shape).astype(np.float32)),
+                                                kv4.bf16_bits(r.uniform(-2.2, -1.8, t.shape).astype(np.float32)))))
+    q = r.standard_normal((slots, nq, d)).astype(np.float32)
+    res = []
+    for B in (2, 16, 40, 128):
+        mass = torch.zeros((slots, nkv, S), device="cuda")
+        out = attend(torch, c, q[:B], range(B), L[:B] - 1, mass)
+        plain = attend(torch, c, q[:B], range(B), L[:B] - 1)
+        assert np.array_equal(out, plain)
+        res.append((out, mass[:B].cpu().numpy()))
+    assert kmr.kmr_last_device_error() == 0
+    for out, mass in res[:-1]:
+        assert np.array_equal(out, res[-1][0][:len(out)]) and np.array_equal(mass, res[-1][1][:len(out)])
+    vals = [kv4.dequantize(kv4.unpack_rows(t[:3].cpu().numpy(), i == 0), *((w[:3].cpu().numpy().view(np.uint32) >> k).astype(np.uint16)
+            for k in (16, 0))) for i, (t, w) in enumerate(zip(c.tensors[:2], c.tensors[2:]))]
+    for b in range(3):
+        ref, m = kv4.attention(q[b], vals[0][b, :, :L[b]], vals[1][b, :, :L[b]], 1 / math.sqrt(d))
+        assert rel_l2(res[-1][0][b], ref) <= ATTN_TOL
+        assert np.allclose(res[-1][1][b, :, :L[b]], m, rtol=2e-4, atol=1e-30)
+
+
+@pytest.mark.parametrize("S", [64, 4112])
+def test_idle_rows(torch, S):
+    """A padded batch: idle rows (no token, position -1, length 0) with slots that are out of range or somebody
+    else's change nothing and raise nothing."""
+    r = np.random.default_rng(80)
+    nq, nkv, d, g, slots = 2, 1, 64, 32, 3
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    qkv = r.standard_normal((3, 1, nq + 2 * nkv, d)).astype(np.float32)
+    qo = torch.full((3, 1, nq, d), 4.0, device="cuda")
+    mass = torch.ones((slots, nkv, S), device="cuda")
+    ids = [0, 99, 0]
+    kmr.kmr_kv4_append(c.dev, torch.from_numpy(qkv).cuda(), torch.zeros((3, 3, 1), dtype=torch.int32, device="cuda"),
+                       i32(torch, ids), i32(torch, [5, 5, 5]), i32(torch, [1, 0, 0]), 3, 1, nq, None, None, 1e-6, 1e6,
+                       SECTIONS[d], qo, mass, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    assert (qo[1:] == 4.0).all().item() and mass[0, 0, 5].item() == 0 and mass.sum().item() == slots * S - 1
+    got = c.host()
+    for a, w in zip(got, before):
+        assert np.array_equal(np.delete(a[0], 5, 1), np.delete(w[0], 5, 1)) and np.array_equal(a[1:], w[1:])
+    q = r.standard_normal((3, nq, d)).astype(np.float32)
+    mass.zero_()
+    out = attend(torch, c.dev, q, ids, [5, -1, -1], mass)
+    assert kmr.kmr_last_device_error() == 0
+    one = torch.zeros_like(mass)
+    alone = attend(torch, c.dev, q[:1], [0], [5], one)
+    assert np.array_equal(out[0], alone[0]) and not out[1:].any() and torch.equal(mass, one)
+    assert abs(mass.sum().item() - nq) <= 1e-5
+    dst = Cache(torch, r, 2, nkv, 16, d, g)
+    kept, new = evict(torch, c.dev, dst.dev, [0, 99, 0], [1, 1, -5], [6, 0, 0], 4, 1, mass, None)
+    assert kmr.kmr_last_device_error() == 0
+    assert new.tolist() == [4, 0, 0] and (kept[1:] == -1).all()
+    assert kept[0, 0].tolist() == kv4.evict_positions(mass[0, 0].cpu().numpy(), 6, 4, 1)
