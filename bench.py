@@ -626,9 +626,9 @@ ATTN_SWEEP = [(B, L) for B in (1, 4, 16) for L in (256, 1024, 4096, 8192)]
 
 def sweep() -> None:
     """Standalone kernel sweeps of the measurement plan: kmr_int4_gemv at M in {1,2,4,8,16}
-    over the decoder's projection shapes and the int4 vocabulary shape, and kmr_decode_attn
-    (16 q / 8 kv heads x 128) at B in {1,4,16} rows x {256,1024,4096,8192} cached positions
-    (every row full).  Each point rotates through enough distinct weight / cache copies to
+    over the decoder's projection shapes and the int4 vocabulary shape, and kmr_decode_attn and
+    kmr_decode_attn_kv4 (16 q / 8 kv heads x 128) at B in {1,4,16} rows x {256,1024,4096,8192} cached
+    positions (every row full).  Each point rotates through enough distinct weight / cache copies to
     exceed L2 by 2x, so every launch streams from HBM.  Prints one JSON line: per point the
     algorithmic bytes, mean launch time and achieved GB/s against the measured copy bandwidth."""
     import math
@@ -658,7 +658,7 @@ def sweep() -> None:
             gemv.append({"N": N, "K": K, "M": M, "bytes": nbytes, "us": round(us, 2),
                          "gbs": round(nbytes / (us * 1e3), 1), "frac": round(nbytes / (us * 1e3) / hbm, 3)})
         del bufs, one
-    attn = []
+    attn, attn4 = [], []
     nq, nkv, d = 16, 8, 128
     for B, L in ATTN_SWEEP:
         per = B * nkv * L * d * 2
@@ -678,9 +678,24 @@ def sweep() -> None:
         nbytes = 2 * per
         attn.append({"B": B, "cached": L, "bytes": nbytes, "us": round(us, 2),
                      "gbs": round(nbytes / (us * 1e3), 1), "frac": round(nbytes / (us * 1e3) / hbm, 3)})
-        del caches
+        # the same over the 4-bit cache (group 32), converted from these
+        per4 = B * nkv * L * 2 * (d // 2 + 4 * (d // 32))
+        zero, lens = torch.zeros_like(slot_ids), torch.full_like(slot_ids, L)
+        caches4 = []
+        for i in range(max(2, math.ceil(300e6 / per4))):
+            c4 = kmr.Kv4Cache.zeros(B, nkv, L, d, 32)
+            kmr.kmr_kv4_from_bf16(c4, *caches[i % copies], B, L, slot_ids, zero, slot_ids, zero, lens, B, L, stream)
+            caches4.append(c4)
+        ws4 = kmr.kmr_decode_attn_kv4_workspace_size(caches4[0], B, nq)
+        ws4b = torch.empty(ws4, dtype=torch.uint8, device="cuda")
+        us = launch_time_us(torch, lambda i: kmr.kmr_decode_attn_kv4(caches4[i], qv, slot_ids, cpos, B, nq,
+                                                                     1.0 / math.sqrt(d), None, out, ws4b, ws4, stream),
+                            len(caches4), 50)
+        attn4.append({"B": B, "cached": L, "bytes": per4, "us": round(us, 2),
+                      "gbs": round(per4 / (us * 1e3), 1), "frac": round(per4 / (us * 1e3) / hbm, 3)})
+        del caches, caches4
     assert kmr.kmr_last_device_error() == 0
-    print(json.dumps({"sweep": {"int4_gemv": gemv, "decode_attn": attn, "peak_gbs": hbm,
+    print(json.dumps({"sweep": {"int4_gemv": gemv, "decode_attn": attn, "decode_attn_kv4": attn4, "peak_gbs": hbm,
                                 "peak_source": peak["source"], "l2": "rotating copies > 2x L2"}}))
 
 
