@@ -119,17 +119,31 @@ __device__ __forceinline__ void lds_words(const void* p, uint32_t (&w)[N]) {
     }
 }
 
-// A ring stage holds TT tiles of 16 positions for each warp.
-template <int D, int G, int TT>
+// How a CTA's four warps share the work.  Two tiles of 16 positions a warp at a time give two chains of products to
+// interleave (one row of 8192: 9.1 -> 8.0 us; 16 rows 53.4 -> 47.4).  Up to 4 query heads a KV head fill one n-tile.  5 to 8
+// need two: with heads of 64 every warp keeps both; with heads of 128 that takes 240 registers and two CTAs an SM, so
+// warps 0, 1 have the first four heads and warps 2, 3 the others, over the same stage, and unpack it twice (16 rows of
+// 8192, group 32: 8 heads on each of 4 KV heads 55.9 -> 48.6 us, 6 on each of 8 101 -> 87; one row of 4096 9.5 -> 10.3).
+enum HeadClass { HEADS_2 = 0, HEADS_4 = 1, HEADS_8 = 2 };
+template <int D, int HC>
+struct Share {
+    static constexpr int kHeadWarps = HC == HEADS_8 && D == 128 ? 2 : 1;       // groups of warps with heads of their own
+    static constexpr int kTileWarps = kWarps / kHeadWarps;                     // warps that share out the tiles
+    static constexpr int kNTiles = HC == HEADS_8 && D == 64 ? 2 : 1;           // n-tiles of a warp
+    static constexpr int kTiles = 2;                                           // tiles of a warp at a time
+    static constexpr int kCtas = kNTiles == 1 ? 4 : 3;                         // of an SM
+};
+template <int D, int G, int HC>
 struct SplitSmem {
-    static constexpr int kStagePos = 16 * kWarps * TT, kStages = TT == 2 ? 2 : 4;
+    using S = Share<D, HC>;
+    static constexpr int kStagePos = 16 * S::kTileWarps * S::kTiles, kStages = 256 / kStagePos;
     static constexpr int kCodes = kStagePos * D / 2, kWords = kStagePos * (D / G) * 4;
     static constexpr int kStage = 2 * kCodes + 2 * kWords;
     static constexpr int kRing = kStages * kStage;
-    __host__ __device__ static constexpr int merge(int rep) { return kWarps * rep * (D + 2) * 4; }
+    __host__ __device__ static constexpr int merge(int rep) { return S::kTileWarps * rep * (D + 2) * 4; }
     static constexpr int kQuery = 4 * (D / 32) + D / G + 1;         // words of a lane's query per n-tile
-    __host__ __device__ static constexpr int query(int rep) { return (rep <= 4 ? 1 : 2) * kQuery * 128; }
-    __host__ __device__ static constexpr int base(int rep) { return 128 + query(rep) + kRing + merge(rep); }
+    static constexpr int kQueryBytes = S::kHeadWarps * S::kNTiles * kQuery * 128;
+    __host__ __device__ static constexpr int base(int rep) { return 128 + kQueryBytes + kRing + merge(rep); }
     // a cluster's additions: the states pushed here (a slice of o of every split; every m and l), the scores
     __host__ __device__ static constexpr int state(int rep, int ranks) {
         return kKv4ClusterSplits * (rep * D / ranks * 4 + rep * 8);
@@ -139,10 +153,6 @@ struct SplitSmem {
     }
 };
 
-// Tiles that a warp takes together: two chains of products to interleave where the registers allow it (one row of 8192:
-// 9.1 -> 8.0 us; 16 rows 53.4 -> 47.4).
-__host__ __device__ constexpr int tiles_of(int NT) { return NT == 1 ? 2 : 1; }
-
 // Query head, half of the dims and part (0 high, 1 low) of an n-tile's column.
 template <bool PAIR>
 __device__ __forceinline__ int column_head(int g) { return PAIR ? (g >> 1) & 1 : g >> 1; }
@@ -150,14 +160,15 @@ template <bool PAIR>
 __device__ __forceinline__ int column_half(int g) { return PAIR ? g >> 2 : 0; }
 
 // Query fragments of the scores' B operand (this lane's column), and the queries' group sums and the scores' factor of
-// the head and half whose accumulators the lane holds (columns 2 t, 2 t + 1).  Heads past rep are zero.
+// the head and half whose accumulators the lane holds (columns 2 t, 2 t + 1).  Heads from head0 on; past rep, zero.
 template <int D, int G, int NT, bool PAIR>
-__device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int lane, uint32_t* out) {
+__device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int head0, int lane,
+                                                uint32_t* out) {
     constexpr int NB = D / 32 / (PAIR ? 2 : 1), NG = D / G / (PAIR ? 2 : 1), BPG = G / 32;     // of one half
     const int g = lane >> 2, t = lane & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        const int hq = 4 * n + column_head<PAIR>(g);
+        const int hq = head0 + 4 * n + column_head<PAIR>(g);
         float x[NB][8], mx = 0.f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
@@ -212,11 +223,14 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
 
 // One CTA of four warps, a ring of stages of 16 TT positions a warp filled by bulk copies (four lanes, one array each).
 // A stage's four warps meet only at its barriers; a row's last tile masks by select, since what lies past the row's end
-// may be NaN.  NT: n-tiles of 4 query heads; PAIR: one n-tile of 2 heads whose halves' groups are kept apart (see above).
-template <int D, int G, int NT, bool PAIR, bool CL>
-__global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const Kv4AttnParams p) {
-    constexpr int TT = tiles_of(NT);
-    using M = SplitSmem<D, G, TT>;
+// may be NaN.  HC: the most query heads a KV head; with 2 and several groups the halves' groups are kept apart (PAIR,
+// see above).
+template <int D, int G, int HC, bool CL>
+__global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(const Kv4AttnParams p) {
+    using M = SplitSmem<D, G, HC>;
+    using S = Share<D, HC>;
+    constexpr int TT = S::kTiles, NT = S::kNTiles, kTileWarps = S::kTileWarps, kHeadWarps = S::kHeadWarps;
+    constexpr bool PAIR = HC == HEADS_2 && G < D;
     constexpr int kStagePos = M::kStagePos, kStages = M::kStages;
     constexpr int NB = D / 32, NG = D / G, BPG = G / 32;
     constexpr int HB = PAIR ? NB / 2 : NB, HG = PAIR ? NG / 2 : NG;  // blocks and groups of a lane's half
@@ -224,15 +238,22 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
     extern __shared__ __align__(128) uint8_t smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);              // [kStages]
     uint64_t* empty = full + kStages;                                // [kStages]
-    uint8_t* ring = smem + 128 + NT * M::kQuery * 128;
+    uint8_t* ring = smem + 128 + M::kQueryBytes;
     const int s = blockIdx.x, h = blockIdx.y, b0 = blockIdx.z;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     pdl_wait();                                   // nothing of the previous kernel's is read before
     if (!CL) pdl_launch_dependents();             // the merge, which waits for this kernel's end
     const int rep = p.nq / p.c.nkv;
-    // warp 1 prepares the query for all while warp 0 looks up the row and starts its copies
-    uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [value][lane]
-    if (warp == 1) query_fragments<D, G, NT, PAIR>(p, b0, h, rep, lane, qsh);
+    // warp 1 (and 2, for the second group of heads) prepares the query for all while warp 0 looks up the row and starts
+    // its copies
+    constexpr int kQueryWords = (4 * HB + HG + 1) * 32;              // of an n-tile
+    uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [head group][n-tile][value][lane]
+    const int hw = warp / kTileWarps, wt = warp % kTileWarps, head0 = 4 * NT * hw;
+    auto prepare_query = [&](int b) {
+        if (warp >= 1 && warp <= kHeadWarps)
+            query_fragments<D, G, NT, PAIR>(p, b, h, rep, 4 * NT * (warp - 1), lane, qsh + (warp - 1) * NT * kQueryWords);
+    };
+    prepare_query(b0);
     const int bad = kv4_row_error(p, b0);
     if (bad != KMR_OK) {                          // the same for the whole cluster
         if (CL && s == 0) {
@@ -304,13 +325,13 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
         if (warp == 0)
             for (int i = 0; i < nst && i < kStages; ++i) issue(i);
 
-        if (CL && !first && warp == 1) query_fragments<D, G, NT, PAIR>(p, b, h, rep, lane, qsh);
+        if (CL && !first) prepare_query(b);
         __syncthreads();
         uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
         float qsum[NT][HG], fac[NT];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint32_t* at = qsh + n * (4 * HB + HG + 1) * 32 + lane;
+            const uint32_t* at = qsh + (hw * NT + n) * kQueryWords + lane;
 #pragma unroll
             for (int k = 0; k < HB; ++k)
 #pragma unroll
@@ -338,8 +359,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             sc_out = p.scores + (size_t(b) * p.c.nkv + h) * rep * p.c.S;
         }
 
-        float* wo = reinterpret_cast<float*>(ring + M::kRing);           // [warp][rep][D]
-        float* wml = wo + kWarps * rep * D;                              // [warp][rep][2]
+        float* wo = reinterpret_cast<float*>(ring + M::kRing);           // [warp of a head][rep][D]
+        float* wml = wo + kTileWarps * rep * D;                          // [warp][rep][2]
         const int ranks = CL ? int(gridDim.x) : 1, slice = rep * D / ranks;         // of the output, for each rank
         float* recv = reinterpret_cast<float*>(smem + M::base(rep));                 // [split][slice]
         float* recv_ml = recv + kKv4ClusterSplits * slice;                           // [split][head][m, l]
@@ -361,16 +382,16 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 const uint32_t slot_of = (uses + k) % kStages, phase = ((uses + k) / kStages) & 1u;
                 const uint8_t* buf = ring + slot_of * M::kStage;
                 mbar_wait(&full[slot_of], phase, p.err);
-                const int base0 = t0 + st * kStagePos + warp * 16;         // the first tile's first position
+                const int base0 = t0 + st * kStagePos + wt * 16;         // the first tile's first position
                 if (base0 < t1) {
                     // a tile is whole but for the row's last ones; one past the end counts for nothing
-                    const bool whole = base0 + (TT - 1) * (16 * kWarps) + 16 <= t1;
+                    const bool whole = base0 + (TT - 1) * (16 * kTileWarps) + 16 <= t1;
                     // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
                     float sc[TT][NT][2];
                     uint32_t top = 0u;
 #pragma unroll
                     for (int u = 0; u < TT; ++u) {
-                        const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                        const int i0 = (u * kTileWarps + wt) * 16, base = base0 + u * (16 * kTileWarps);
                         uint32_t k0[NB], k1[NB], w0[HG], w1[HG];
                         lds_words(buf + (i0 + g) * (D / 2) + t * (4 * NB), k0);
                         lds_words(buf + (i0 + g + 8) * (D / 2) + t * (4 * NB), k1);
@@ -426,8 +447,9 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                                 if (base + g >= t1) sc[u][n][0] = -INFINITY;
                                 if (base + g + 8 >= t1) sc[u][n][1] = -INFINITY;
                             }
-                            if (sc_out && 4 * n + t < rep) {            // (PAIR: rep <= 2, the lanes of half 0)
-                                float* dst = sc_out + (4 * n + t) * sc_ld + base + g;
+                            const int hq = head0 + 4 * n + t;           // (PAIR: rep <= 2, the lanes of half 0)
+                            if (sc_out && hq < rep) {
+                                float* dst = sc_out + hq * sc_ld + base + g;
                                 if (whole || base + g < t1) dst[0] = sc[u][n][0];
                                 if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
                             }
@@ -448,7 +470,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float c = fmaxf(sc[0][n][0], sc[0][n][1]);
-                        if constexpr (TT == 2) c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
+                        c = fmaxf(c, fmaxf(sc[TT - 1][n][0], sc[TT - 1][n][1]));
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
@@ -477,7 +499,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                     const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
 #pragma unroll
                     for (int u = 0; u < TT; ++u) {
-                        const int i0 = (u * kWarps + warp) * 16, base = base0 + u * (16 * kWarps);
+                        const int i0 = (u * kTileWarps + wt) * 16, base = base0 + u * (16 * kTileWarps);
                         // ---- V words of positions g, g + 8 (the bases' sum) and t, t + 4, t + 8, t + 12 (the weights)
                         const uint8_t* words = buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG);
                         uint32_t v0[HG], v1[HG], vw[4][HG];
@@ -575,7 +597,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int hq = PAIR ? t & 1 : 4 * n + t;
+                const int hq = PAIR ? t & 1 : head0 + 4 * n + t;
                 float lt = l[n];
                 lt += __shfl_xor_sync(0xffffffffu, lt, 4);
                 lt += __shfl_xor_sync(0xffffffffu, lt, 8);
@@ -590,8 +612,8 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                 }
                 if (hq < rep) {
                     if (g == 0 && cth == 0) {
-                        wml[(warp * rep + hq) * 2] = m[n];
-                        wml[(warp * rep + hq) * 2 + 1] = lt;
+                        wml[(wt * rep + hq) * 2] = m[n];
+                        wml[(wt * rep + hq) * 2 + 1] = lt;
                     }
 #pragma unroll
                     for (int k = 0; k < HB; ++k) {
@@ -608,7 +630,7 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
                             }
                             v[i] = __fmaf_rn(v[i], un, z);
                         }
-                        *reinterpret_cast<float4*>(wo + (warp * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
+                        *reinterpret_cast<float4*>(wo + (wt * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
                             make_float4(v[0], v[1], v[2], v[3]);
                     }
                 }
@@ -618,12 +640,12 @@ __global__ void __launch_bounds__(kThr, NT == 1 ? 4 : 2) kv4_split_kernel(const 
             if (CL && first && u == u0) cluster_wait();
             for (int i = tid; i < rep * (D / 4); i += kThr) {
                 const int hq = i / (D / 4), dim = (i % (D / 4)) * 4;
-                float mw[kWarps], mx = -INFINITY, den = 0.f;
+                float mw[kTileWarps], mx = -INFINITY, den = 0.f;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
+                for (int w = 0; w < kTileWarps; ++w) mx = fmaxf(mx, mw[w] = wml[(w * rep + hq) * 2]);
                 float4 num = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) {
+                for (int w = 0; w < kTileWarps; ++w) {
                     const float f = mw[w] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(mw[w], mx));
                     const float4 v = *reinterpret_cast<const float4*>(wo + (w * rep + hq) * D + dim);
                     den = __fmaf_rn(f, wml[(w * rep + hq) * 2 + 1], den);
@@ -819,30 +841,27 @@ __global__ void __launch_bounds__(kMergeThr) kv4_merge_kernel(const Kv4AttnParam
 }
 static_assert(kMergeThr / 32 >= kKv4MaxRep, "a warp per query head");
 
-template <int D, int G>
-const void* split_fn(int rep, bool cl) {
-    constexpr bool kPair = G < D;                // two groups or more
-    if (kPair && rep <= 2)
-        return cl ? (const void*)kv4_split_kernel<D, G, 1, kPair, true> : (const void*)kv4_split_kernel<D, G, 1, kPair, false>;
-    if (rep <= 4)
-        return cl ? (const void*)kv4_split_kernel<D, G, 1, false, true> : (const void*)kv4_split_kernel<D, G, 1, false, false>;
-    return cl ? (const void*)kv4_split_kernel<D, G, 2, false, true> : (const void*)kv4_split_kernel<D, G, 2, false, false>;
+template <int D, int G, int HC>
+const void* split_fn(bool cl) {
+    return cl ? (const void*)kv4_split_kernel<D, G, HC, true> : (const void*)kv4_split_kernel<D, G, HC, false>;
 }
 struct SplitVariant {
     const void* fn;
-    int smem;
+    int smem, ctas;                              // CTAs of an SM
 };
 // A cluster of `ranks` CTAs whose scores, `positions` of each, stay in shared memory (0: no mass); ranks 0: no cluster.
+template <int D, int G, int HC>
+SplitVariant split_variant(int rep, int ranks, int positions) {
+    using M = SplitSmem<D, G, HC>;
+    return {split_fn<D, G, HC>(ranks > 0), ranks ? M::total(rep, ranks, positions) : M::base(rep), Share<D, HC>::kCtas};
+}
 template <int D, int G>
 SplitVariant split_variant(int rep, int ranks, int positions) {
-    using S1 = SplitSmem<D, G, tiles_of(1)>;
-    using S2 = SplitSmem<D, G, tiles_of(2)>;
-    int smem;
-    if (rep <= 4)
-        smem = ranks ? S1::total(rep, ranks, positions) : S1::base(rep);
-    else
-        smem = ranks ? S2::total(rep, ranks, positions) : S2::base(rep);
-    return {split_fn<D, G>(rep, ranks > 0), smem};
+    if constexpr (G < D) {
+        if (rep <= 2) return split_variant<D, G, HEADS_2>(rep, ranks, positions);
+    }
+    if (rep <= 4) return split_variant<D, G, HEADS_4>(rep, ranks, positions);
+    return split_variant<D, G, HEADS_8>(rep, ranks, positions);
 }
 SplitVariant split_variant(int d, int g, int rep, int ranks, int positions) {
     if (d == 64) return g == 32 ? split_variant<64, 32>(rep, ranks, positions) : split_variant<64, 64>(rep, ranks, positions);
@@ -896,7 +915,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
         // CTAs that run at a time: more than that only queue, and pay their start and end each, so then a CTA takes
         // several splits of its row, one after the other, which changes no result (16 rows of 1024: 13.2 -> 10.3 us; the
         // longer caches' splits of 256 gained nothing by it, 47.4 against 48.2 us for 16 rows of 8192)
-        const long long slots = (rep <= 4 ? 4LL : 2LL) * num_sms(), rows = (long long)p.c.nkv * p.B;
+        const long long slots = (long long)split_variant(p.c.d, p.c.g, rep, 1, 0).ctas * num_sms();
+        const long long rows = (long long)p.c.nkv * p.B;
         while (ranks > 1 && ranks * rows > slots) ranks /= 2;
         q.per = (splits + ranks - 1) / ranks;
         q.score_ld = q.per * chunk;
