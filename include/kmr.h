@@ -267,7 +267,7 @@ typedef struct kmr_kv4_cache {
  *   mass       device fp32 [slots][n_kv][max_len] or NULL: set to 0 at the written positions
  * n_q is 1..8 times n_kv.  Where two rows of a call write the same position of a slot, the later row's
  * values stay.  qkv, q_out and the norms are 16-byte aligned.  Errors: KMR_ERR_INVALID_ARG (pointers,
- * eps, theta, T < 1), KMR_ERR_SHAPE (heads, sections), KMR_ERR_BATCH; on the device a row with n_tokens
+ * eps, theta, T outside 1..2^28), KMR_ERR_SHAPE (heads, sections), KMR_ERR_BATCH; on the device a row with n_tokens
  * outside 0..T (KMR_ERR_INVALID_ARG), a slot out of range (KMR_ERR_SLOT_RANGE) or tokens that do not fit
  * [0, max_len) (KMR_ERR_CACHE_FULL) writes nothing. */
 int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, const int32_t* positions,
@@ -280,7 +280,7 @@ int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, const int32_t* 
  * lengths[b] positions (0..max_tokens) from bf16_start[b] of bf16 row bf16_slot_ids[b] and from start[b]
  * of 4-bit row slot_ids[b]; all five arrays are device int32 [B].  kmr_kv4_to_bf16 writes
  * bf16(c * s + z); positions outside the spans keep their contents; where two spans write the same position,
- * the later span's values stay.  Errors: KMR_ERR_INVALID_ARG (pointers, max_tokens < 1), KMR_ERR_SHAPE,
+ * the later span's values stay.  Errors: KMR_ERR_INVALID_ARG (pointers, max_tokens outside 1..2^28), KMR_ERR_SHAPE,
  * KMR_ERR_BATCH; on the device KMR_ERR_INVALID_ARG (length), KMR_ERR_SLOT_RANGE, KMR_ERR_CACHE_FULL (a span
  * that leaves either row). */
 int kmr_kv4_from_bf16(const kmr_kv4_cache* cache, const uint16_t* k_bf16, const uint16_t* v_bf16, int bf16_slots,

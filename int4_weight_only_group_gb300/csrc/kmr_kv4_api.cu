@@ -15,7 +15,7 @@ int view_of(const kmr_kv4_cache* c, Kv4View* v) {
     if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_sz) || !aligned16(c->v_sz))
         return KMR_ERR_INVALID_ARG;
     if (c->slots < 1 || c->n_kv_heads < 1 || c->n_kv_heads > kKv4MaxHeads) return KMR_ERR_SHAPE;
-    if (c->max_len < 16 || c->max_len % 16 || c->max_len > (1 << 28)) return KMR_ERR_SHAPE;
+    if (c->max_len < 16 || c->max_len % 16 || c->max_len > kKv4MaxLen) return KMR_ERR_SHAPE;
     if (c->head_dim != 64 && c->head_dim != 128) return KMR_ERR_SHAPE;
     if ((c->group != 32 && c->group != 64 && c->group != 128) || c->group > c->head_dim) return KMR_ERR_SHAPE;
     v->kc = static_cast<uint8_t*>(c->k_codes);
@@ -39,7 +39,7 @@ int convert(const kmr_kv4_cache* cache, uint16_t* k16, uint16_t* v16, int slots1
     const int rc = view_of(cache, &p.c);
     if (rc != KMR_OK) return rc;
     if (!k16 || !v16 || !slot16 || !start16 || !slot_ids || !start || !lengths) return KMR_ERR_INVALID_ARG;
-    if (!aligned16(k16) || !aligned16(v16) || T < 1) return KMR_ERR_INVALID_ARG;
+    if (!aligned16(k16) || !aligned16(v16) || T < 1 || T > kKv4MaxLen) return KMR_ERR_INVALID_ARG;
     if (slots16 < 1 || max_len16 < 1) return KMR_ERR_SHAPE;
     if (B < 1 || B > kKv4MaxRows) return KMR_ERR_BATCH;
     if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
@@ -68,7 +68,7 @@ extern "C" int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, cons
     if (rc != KMR_OK) return rc;
     if (!qkv || !positions || !slot_ids || !cache_position || !sections || !q_out) return KMR_ERR_INVALID_ARG;
     if (!aligned16(qkv) || !aligned16(q_out) || !aligned16(q_norm) || !aligned16(k_norm)) return KMR_ERR_INVALID_ARG;
-    if (!(eps >= 0.f) || std::isinf(eps) || !(rope_theta > 0.f) || std::isinf(rope_theta) || T < 1)
+    if (!(eps >= 0.f) || std::isinf(eps) || !(rope_theta > 0.f) || std::isinf(rope_theta) || T < 1 || T > kKv4MaxLen)
         return KMR_ERR_INVALID_ARG;
     if (B < 1 || B > kKv4MaxRows) return KMR_ERR_BATCH;
     if (!heads_ok(nq, p.c.nkv)) return KMR_ERR_SHAPE;

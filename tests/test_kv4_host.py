@@ -68,12 +68,12 @@ def test_bad_caches(L, name):
     ("kmr_kv4_append", dict(qkv=8), -1), ("kmr_kv4_append", dict(q=4), -1), ("kmr_kv4_append", dict(wq=2), -1),
     ("kmr_kv4_append", dict(eps=-1.0), -1), ("kmr_kv4_append", dict(eps=float("nan")), -1),
     ("kmr_kv4_append", dict(theta=0.0), -1), ("kmr_kv4_append", dict(theta=float("inf")), -1),
-    ("kmr_kv4_append", dict(T=0), -1), ("kmr_kv4_append", dict(B=0), -9), ("kmr_kv4_append", dict(B=1025), -9),
+    ("kmr_kv4_append", dict(T=0), -1), ("kmr_kv4_append", dict(T=(1 << 28) + 1), -1), ("kmr_kv4_append", dict(B=0), -9), ("kmr_kv4_append", dict(B=1025), -9),
     ("kmr_kv4_append", dict(nq=12), -2), ("kmr_kv4_append", dict(nq=72), -2), ("kmr_kv4_append", dict(nq=0), -2),
     ("kmr_kv4_append", dict(sections=(16, 24, 23)), -2), ("kmr_kv4_append", dict(sections=(-16, 56, 24)), -2),
     ("kmr_kv4_from_bf16", dict(k=None), -1), ("kmr_kv4_from_bf16", dict(v=8), -1),
     ("kmr_kv4_from_bf16", dict(ids16=None), -1), ("kmr_kv4_from_bf16", dict(n=None), -1),
-    ("kmr_kv4_from_bf16", dict(T=0), -1), ("kmr_kv4_from_bf16", dict(B=0), -9),
+    ("kmr_kv4_from_bf16", dict(T=0), -1), ("kmr_kv4_from_bf16", dict(T=(1 << 31) - 1), -1), ("kmr_kv4_from_bf16", dict(B=0), -9),
     ("kmr_kv4_from_bf16", dict(slots16=0), -2), ("kmr_kv4_from_bf16", dict(len16=0), -2),
     ("kmr_kv4_to_bf16", dict(k=None), -1), ("kmr_kv4_to_bf16", dict(start=None), -1),
     ("kmr_kv4_to_bf16", dict(B=1025), -9), ("kmr_kv4_to_bf16", dict(T=-1), -1),
