@@ -236,9 +236,9 @@ int kmr_decode_attn_noalloc(const float* q, const uint16_t* k_cache, const uint1
  * (pointers) or KMR_ERR_SHAPE.  Positions of a row that no call has written may hold anything.
  *
  * The calls below take up to 1024 rows (KMR_ERR_BATCH), queue their work on `stream` without
- * synchronising and allocate nothing; they can be captured into a graph once kmr_last_device_error()
- * or one such call has run on the device.  A row that is found bad on the device is skipped
- * and recorded in the error word that kmr_last_device_error() reads; the other rows are not affected. */
+ * synchronising and allocate nothing; they can be captured into a graph once any one of them has run on the
+ * device (the first loads the kernels).  A row that is found bad on the device is skipped and recorded in the
+ * error word that kmr_last_device_error() reads; the other rows are not affected. */
 typedef struct kmr_kv4_cache {
     void* k_codes;
     void* v_codes;

@@ -689,11 +689,15 @@ cudaError_t launch_kv4_convert(const Kv4ConvertParams& p, bool to_bf16, cudaStre
                   &q, st);
 }
 
+// Also loads every kernel, so that a later call can be captured into a graph whatever its shape.
 cudaError_t kv4_set_attributes() {
     const int shapes[5][2] = {{64, 32}, {64, 64}, {128, 32}, {128, 64}, {128, 128}};
     for (const auto& sh : shapes) {
-        const cudaError_t e = cudaFuncSetAttribute(write_fn(sh[0], sh[1], 3), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   kSelCache * 4);
+        cudaFuncAttributes a;
+        cudaError_t e;
+        for (int which = 0; which < 3; ++which)
+            if ((e = cudaFuncGetAttributes(&a, write_fn(sh[0], sh[1], which))) != cudaSuccess) return e;
+        e = cudaFuncSetAttribute(write_fn(sh[0], sh[1], 3), cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCache * 4);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

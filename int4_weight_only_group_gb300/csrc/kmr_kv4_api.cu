@@ -42,7 +42,7 @@ int convert(const kmr_kv4_cache* cache, uint16_t* k16, uint16_t* v16, int slots1
     if (!aligned16(k16) || !aligned16(v16) || T < 1 || T > kKv4MaxLen) return KMR_ERR_INVALID_ARG;
     if (slots16 < 1 || max_len16 < 1) return KMR_ERR_SHAPE;
     if (B < 1 || B > kKv4MaxRows) return KMR_ERR_BATCH;
-    if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
+    if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.k16 = k16;
     p.v16 = v16;
     p.slots16 = slots16;
@@ -76,7 +76,7 @@ extern "C" int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, cons
     if (sections[0] < 0 || sections[1] < 0 || sections[2] < 0 || sections[0] > half || sections[1] > half ||
         sections[2] > half || sections[0] + sections[1] + sections[2] != half)
         return KMR_ERR_SHAPE;
-    if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
+    if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.qkv = qkv;
     p.positions = positions;
     p.slot_ids = slot_ids;
@@ -138,8 +138,7 @@ extern "C" int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, c
     if (B < 1 || B > kKv4MaxRows) return KMR_ERR_BATCH;
     if (!heads_ok(nq, p.c.nkv)) return KMR_ERR_SHAPE;
     if (workspace_bytes < kmr_decode_attn_kv4_workspace_size(cache, B, nq, mass != nullptr)) return KMR_ERR_BUFFER_SIZE;
-    if (ensure_kernel_attributes() != cudaSuccess) return KMR_ERR_CUDA;
-    if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
+    if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.q = q;
     p.slot_ids = slot_ids;
     p.cpos = cache_position;
@@ -172,8 +171,7 @@ extern "C" int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst,
     // one cache has one shape, and one mass only together with it
     if (p.same && (p.src.slots != p.dst.slots || p.src.S != p.dst.S)) return KMR_ERR_SHAPE;
     if (!p.same && mass == dst_mass) return KMR_ERR_INVALID_ARG;
-    if (ensure_kernel_attributes() != cudaSuccess) return KMR_ERR_CUDA;
-    if (!(p.err = standalone_error_word())) return KMR_ERR_CUDA;
+    if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.src_ids = src_slot_ids;
     p.dst_ids = dst_slot_ids;
     p.lengths = lengths;

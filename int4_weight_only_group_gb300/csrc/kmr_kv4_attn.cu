@@ -893,7 +893,8 @@ cudaError_t kv4_attn_set_attributes() {
                                          cudaSharedmemCarveoutMaxShared);
                 if (e != cudaSuccess) return e;
             }
-    return cudaSuccess;
+    cudaFuncAttributes a;
+    return cudaFuncGetAttributes(&a, kv4_merge_kernel);
 }
 
 cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {

@@ -849,3 +849,63 @@ def test_idle_rows(torch, S):
     assert kmr.kmr_last_device_error() == 0
     assert new.tolist() == [4, 0, 0] and (kept[1:] == -1).all()
     assert kept[0, 0].tolist() == kv4.evict_positions(mass[0, 0].cpu().numpy(), 6, 4, 1)
+
+
+FRESH = """
+import math, sys
+sys.path[:0] = [{root!r}, {root!r} + "/tests"]
+import numpy as np, torch
+import int4_weight_only_group_gb300 as kmr
+i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")
+one = kmr.Kv4Cache.zeros(1, 1, 16, 64, 32)
+q0 = torch.zeros((1, 1, 1, 64), device="cuda")
+kmr.kmr_kv4_append(one, torch.zeros((1, 1, 3, 64), device="cuda"), torch.zeros((3, 1, 1), dtype=torch.int32, device="cuda"),
+                   i32([0]), i32([0]), None, 1, 1, 1, None, None, 1e-6, 1e6, (8, 12, 12), q0, None, torch.cuda.current_stream())
+torch.cuda.synchronize()
+for S in (256, 4112):
+    B, nq, nkv, d, g = 2, 8, 2, 128, 64
+    gen = torch.Generator(device="cuda").manual_seed(S)
+    src = [torch.randn((B, nkv, S, d), generator=gen, device="cuda").bfloat16() for _ in range(2)]
+    q = torch.randn((B, nq, d), generator=gen, device="cuda")
+    rows, zero, n = i32([0, 1]), i32([0, 0]), i32([S, S - 9])
+    res = []
+    for captured in (True, False):
+        c, dst = kmr.Kv4Cache.zeros(B, nkv, S, d, g), kmr.Kv4Cache.zeros(B, nkv, 64, d, g)
+        mass, out = torch.zeros((B, nkv, S), device="cuda"), torch.zeros((B, nq, d), device="cuda")
+        nb = kmr.kmr_decode_attn_kv4_workspace_size(c, B, nq, True)
+        ws = torch.empty(nb, dtype=torch.uint8, device="cuda")
+        kept, new = torch.zeros((B, nkv, 50), dtype=torch.int32, device="cuda"), i32([0, 0])
+        back = [torch.zeros((B, nkv, 64, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        last = n - 1
+        def run():
+            st = torch.cuda.current_stream()
+            kmr.kmr_kv4_from_bf16(c, src[0], src[1], B, S, rows, zero, rows, zero, n, B, S, st)
+            kmr.kmr_decode_attn_kv4(c, q, rows, last, B, nq, 1 / math.sqrt(d), mass, out, ws, nb, st)
+            kmr.kmr_kv4_evict(c, dst, rows, rows, n, B, 50, 7, mass, None, kept, new, st)
+            kmr.kmr_kv4_to_bf16(dst, back[0], back[1], B, 64, rows, zero, rows, zero, new, B, 50, st)
+        if captured:
+            G = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(G):
+                run()
+            G.replay()
+        else:
+            run()
+        torch.cuda.synchronize()
+        res.append([out, mass, kept, new] + back)
+    assert all(torch.equal(a, b) for a, b in zip(*res)), S
+    assert res[0][0].abs().sum().item() > 0 and int(res[0][3][0]) == 50
+assert kmr.kmr_last_device_error() == 0
+print("fresh ok")
+"""
+
+
+def test_first_calls_of_other_shapes_inside_a_capture(torch):
+    """In a process whose only earlier call was another operator of another shape, every operator is captured and
+    replayed: the same bits as eager calls."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FRESH.replace("{root!r}", repr(root))], capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0 and "fresh ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
