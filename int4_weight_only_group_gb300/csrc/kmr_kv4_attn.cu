@@ -377,7 +377,9 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
 #pragma unroll
                 for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
             }
-            int eref = 5;                                 // exponent that the output accumulators are scaled by
+            // exponent that the output accumulators are scaled by: from 13 on, so that a weight of up to 2^8 times the scaling
+            // stays finite before a V scale (0 where a group's values are all alike) multiplies it
+            int eref = 13;
             for (int st = 0; t0 + st * kStagePos < t1; ++st, ++k) {
                 const uint32_t slot_of = (uses + k) % kStages, phase = ((uses + k) / kStages) & 1u;
                 const uint8_t* buf = ring + slot_of * M::kStage;

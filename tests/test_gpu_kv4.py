@@ -909,3 +909,48 @@ def test_first_calls_of_other_shapes_inside_a_capture(torch):
     r = subprocess.run([sys.executable, "-c", FRESH.replace("{root!r}", repr(root))], capture_output=True, text=True,
                        timeout=300)
     assert r.returncode == 0 and "fresh ok" in r.stdout, r.stdout[-2000:] + r.stderr[-2000:]
+
+
+# ------------------------------------------------------------------ values that the codes' scales do not reach alike
+def set_values(torch, c, x, g):
+    """The cache's V from x (float32 [slots, nkv, S, d]); returns what it reads back as."""
+    codes, sb, zb = kv4.quantize(x, g)
+    c.dev.tensors[1].copy_(torch.from_numpy(kv4.pack_rows(codes, False)))
+    c.dev.tensors[3].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+    return kv4.dequantize(codes, sb, zb)
+
+
+@pytest.mark.parametrize("d,g,nq,nkv,S,L", [(128, 32, 16, 8, 1104, 1100), (128, 32, 4, 1, 1104, 1100), (64, 32, 2, 1, 1104, 1100),
+                                            (128, 128, 2, 1, 4112, 4100), (128, 32, 16, 8, 4112, 4100), (64, 64, 8, 1, 4112, 4100),
+                                            (128, 64, 8, 1, 208, 200), (128, 32, 7, 1, 4112, 4100)])
+def test_constant_values(torch, d, g, nq, nkv, S, L):
+    """V constant over every group (scale 0): the output is the base, whatever the keys; with V = 0 it is 0.  Keys whose
+    best score rises by a few octaves along the row, as random ones do."""
+    r = np.random.default_rng(L + d + nq)
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    q = (r.standard_normal((1, nq, d)) * 3).astype(np.float32)
+    for value in (1.0, 0.0, -3.5, None):
+        x = np.full((1, nkv, S, d), value if value is not None else 0.0, np.float32)
+        if value is None:                                    # a base of its own for every group
+            x += np.repeat(np.arange(1, d // g + 1, dtype=np.float32) * [1, -2, 4, -8][:d // g], g)
+        set_values(torch, c, x, g)
+        out = attend(torch, c.dev, q, [0], [L - 1])
+        # the weights' sum and the weights times the base: at most 128 roundings of 2^-24 in either
+        want = x[0, 0, 0]
+        assert (np.abs(out[0] - want) <= 256 * 2.0 ** -24 * np.abs(want)).all(), value
+    assert kmr.kmr_last_device_error() == 0
+
+
+@pytest.mark.parametrize("S,L", [(1104, 1100), (4112, 4100)])
+def test_tiny_values(torch, S, L):
+    """V of about 2^-118: what it adds to the weights' scaling stays finite."""
+    r = np.random.default_rng(S)
+    nq, nkv, d, g = 4, 2, 128, 32
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    V = set_values(torch, c, (r.standard_normal((1, nkv, S, d)) * 2.0 ** -118).astype(np.float32), g)
+    q = (r.standard_normal((1, nq, d)) * 3).astype(np.float32)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    ref, _ = kv4.attention(q[0], c.val["k"][0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+    # scales of about 2^-120: a weight below 2^-5 times one leaves the normal range, at 2^-149 of 2^-118 (the output is
+    # some 2^-4 of V) 2^-27 each
+    assert rel_l2(out[0].astype(np.float64) * 2.0 ** 118, ref * 2.0 ** 118) <= ATTN_TOL
