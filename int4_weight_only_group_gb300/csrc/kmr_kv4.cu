@@ -217,19 +217,39 @@ __device__ __forceinline__ void store_word(uint32_t* row, uint32_t own, int l) {
     if (NG == 4 || (l & (4 / NG - 1)) == 0) row[l / (4 / NG)] = own;
 }
 
-// Whether a later row of the call writes one of positions [p0, p1) of the slot too: its values stay.
+// Whether a later row of the call writes one of positions [p0, p1) of the slot too: its values stay.  `refused(r)`
+// says whether row r is refused, for whatever reason: such a row writes nothing and claims nothing.
 // Uniform over the CTA (every thread takes part).
+template <typename Refused>
 __device__ __forceinline__ bool later_row_writes(int b, int B, int slot, int p0, int p1, const int32_t* slots,
-                                                 const int32_t* start, const int32_t* len, int T, int S) {
+                                                 const int32_t* start, const int32_t* len, int T, Refused&& refused) {
     if (b + 1 >= B) return false;
     int hit = 0;
     for (int r = b + 1 + threadIdx.x; r < B; r += blockDim.x) {
-        if (slots[r] != slot) continue;
+        if (slots[r] != slot || refused(r)) continue;
         const int s0 = start[r], n = len ? len[r] : T;
-        if (n < 0 || n > T || s0 < 0 || s0 > S - n) continue;      // a refused row writes nothing
         hit |= p1 > s0 && p0 < s0 + n;
     }
     return __syncthreads_or(hit) != 0;
+}
+
+// KMR_OK or why row b of an append is refused; a row of no tokens never is.
+__device__ __forceinline__ int append_row_error(const Kv4AppendParams& p, int b) {
+    const int n = p.n_tokens ? p.n_tokens[b] : p.T;
+    if (n < 0 || n > p.T) return KMR_ERR_INVALID_ARG;
+    if (n == 0) return KMR_OK;
+    const int slot = p.slot_ids[b], c0 = p.cpos[b];
+    if (slot < 0 || slot >= p.c.slots) return KMR_ERR_SLOT_RANGE;
+    return c0 < 0 || c0 > p.c.S - n ? KMR_ERR_CACHE_FULL : KMR_OK;
+}
+// The same of a conversion's span b, which both caches have to hold.
+__device__ __forceinline__ int convert_row_error(const Kv4ConvertParams& p, int b) {
+    const int n = p.lengths[b];
+    if (n < 0 || n > p.T) return KMR_ERR_INVALID_ARG;
+    if (n == 0) return KMR_OK;
+    const int slot = p.slot_ids[b], s0 = p.start[b], slot16 = p.slot16[b], s16 = p.start16[b];
+    if (slot < 0 || slot >= p.c.slots || slot16 < 0 || slot16 >= p.slots16) return KMR_ERR_SLOT_RANGE;
+    return s0 < 0 || s0 > p.c.S - n || s16 < 0 || s16 > p.S16 - n ? KMR_ERR_CACHE_FULL : KMR_OK;
 }
 
 // ------------------------------------------------------------------ new tokens
@@ -267,13 +287,9 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
     const int t = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
     pdl_wait();
     const int nkv = p.c.nkv;
-    const int n = p.n_tokens ? p.n_tokens[b] : p.T;
-    const int slot = p.slot_ids[b], c0 = p.cpos[b];
-    const bool bad_n = n < 0 || n > p.T, bad_slot = slot < 0 || slot >= p.c.slots;
-    const bool bad_pos = !bad_n && (c0 < 0 || c0 > p.c.S - n);
-    if (bad_n || (n > 0 && (bad_slot || bad_pos))) {
-        if (t == 0 && tid == 0)
-            set_error(p.err, bad_n ? KMR_ERR_INVALID_ARG : (bad_slot ? KMR_ERR_SLOT_RANGE : KMR_ERR_CACHE_FULL));
+    const int n = p.n_tokens ? p.n_tokens[b] : p.T, slot = p.slot_ids[b], c0 = p.cpos[b];
+    if (const int bad = append_row_error(p, b)) {
+        if (t == 0 && tid == 0) set_error(p.err, bad);
         return;
     }
     if (t >= n) return;
@@ -286,7 +302,8 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
         const unsigned long long turn = (unsigned long long)x * p.turn[tid];
         cos_sin_turn(int(turn >> 32), cs[tid], sn[tid]);
     }
-    const bool lose = later_row_writes(b, p.B, slot, pos, pos + 1, p.slot_ids, p.cpos, p.n_tokens, p.T, p.c.S);
+    const bool lose = later_row_writes(b, p.B, slot, pos, pos + 1, p.slot_ids, p.cpos, p.n_tokens, p.T,
+                                       [&](int r) { return append_row_error(p, r) != KMR_OK; });
     __syncthreads();
     // every lane of a warp runs the same number of rounds, so that the shuffles are complete
     for (int h0 = 0; h0 < heads; h0 += kThr / 4) {
@@ -380,20 +397,17 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
     pdl_wait();
     const int nkv = p.c.nkv, n = p.lengths[b];
     const int slot = p.slot_ids[b], s0 = p.start[b], slot16 = p.slot16[b], s16 = p.start16[b];
-    const bool bad_n = n < 0 || n > p.T;
-    const bool bad_slot = slot < 0 || slot >= p.c.slots || slot16 < 0 || slot16 >= p.slots16;
-    const bool bad_pos = !bad_n && (s0 < 0 || s0 > p.c.S - n || s16 < 0 || s16 > p.S16 - n);
-    if (bad_n || (n > 0 && (bad_slot || bad_pos))) {
-        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0)
-            set_error(p.err, bad_n ? KMR_ERR_INVALID_ARG : (bad_slot ? KMR_ERR_SLOT_RANGE : KMR_ERR_CACHE_FULL));
+    if (const int bad = convert_row_error(p, b)) {
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) set_error(p.err, bad);
         return;
     }
     const int t0 = blockIdx.x * p.span, t1 = min(n, t0 + p.span);
     if (t0 >= t1) return;
-    const int wslot = TO16 ? slot16 : slot, w0 = TO16 ? s16 : s0, wS = TO16 ? p.S16 : p.c.S;
+    const int wslot = TO16 ? slot16 : slot, w0 = TO16 ? s16 : s0;
     const int32_t* wslots = TO16 ? p.slot16 : p.slot_ids;
     const int32_t* wstart = TO16 ? p.start16 : p.start;
-    const bool clash = later_row_writes(b, p.B, wslot, w0 + t0, w0 + t1, wslots, wstart, p.lengths, p.T, wS);
+    const bool clash = later_row_writes(b, p.B, wslot, w0 + t0, w0 + t1, wslots, wstart, p.lengths, p.T,
+                                        [&](int r) { return convert_row_error(p, r) != KMR_OK; });
     const bool key = int(blockIdx.y) < nkv;
     const int kvh = key ? blockIdx.y : blockIdx.y - nkv;
     const size_t row = (size_t(slot) * nkv + kvh) * p.c.S + s0, row16 = (size_t(slot16) * nkv + kvh) * p.S16 + s16;
@@ -402,8 +416,7 @@ __global__ void __launch_bounds__(kThr) kv4_convert_kernel(const Kv4ConvertParam
         if (clash)
             for (int r = b + 1; r < p.B; ++r) {
                 const int m = p.lengths[r], q = wstart[r];
-                if (wslots[r] == wslot && m >= 0 && m <= p.T && q >= 0 && q <= wS - m && w0 + t >= q && w0 + t < q + m)
-                    return false;
+                if (wslots[r] == wslot && convert_row_error(p, r) == KMR_OK && w0 + t >= q && w0 + t < q + m) return false;
             }
         return true;
     };

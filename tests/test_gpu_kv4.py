@@ -954,3 +954,40 @@ def test_tiny_values(torch, S, L):
     # scales of about 2^-120: a weight below 2^-5 times one leaves the normal range, at 2^-149 of 2^-118 (the output is
     # some 2^-4 of V) 2^-27 each
     assert rel_l2(out[0].astype(np.float64) * 2.0 ** 118, ref * 2.0 ** 118) <= ATTN_TOL
+
+
+# ------------------------------------------------------------------ refused rows claim nothing
+@pytest.mark.parametrize("to_bf16", [False, True])
+@pytest.mark.parametrize("T", [20, 300])                        # short and long spans of a CTA
+def test_refused_later_spans_leave_the_earlier_ones_alone(torch, to_bf16, T):
+    """Later rows that would write the same positions but are refused, each for another reason, those of the side
+    that is only read among them: the good row's span is written whole."""
+    r = np.random.default_rng(90 + T)
+    nkv, d, g, S, slots = 16, 64, 32, 320, 3
+    src = [torch.from_numpy(kv4.bf16_bits(r.standard_normal((slots, nkv, S, d)).astype(np.float32)).view(np.int16)).cuda()
+           for _ in range(2)]
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    big = 2 ** 31 - 1
+    # (length, slot, start) of the written and of the read side
+    bad = [(T, (1, 5), (7, 0)), (T, (1, 5), (-1, 0)), (T, (1, 5), (0, S - T + 1)), (T, (1, 5), (0, -1)), (T, (1, 5), (0, big)),
+           (-1, (1, 5), (0, 0)), (T + 1, (1, 5), (0, 0)), (T, (1, S - T + 1), (0, 0)), (T, (1, -1), (0, 0)), (T, (1, big), (0, 0))]
+    rows = [(T, (1, 5), (2, 3))] + bad
+    n = i32(torch, [a[0] for a in rows])
+    w, rd = ([i32(torch, [a[side][k] for a in rows]) for k in (0, 1)] for side in (1, 2))
+    B, st = len(rows), torch.cuda.current_stream()
+    if to_bf16:
+        dst = [torch.zeros((slots, nkv, S, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+        kmr.kmr_kv4_to_bf16(c.dev, *dst, slots, S, *w, *rd, n, B, T, st)
+    else:
+        kmr.kmr_kv4_from_bf16(c.dev, *src, slots, S, *rd, *w, n, B, T, st)
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_INVALID_ARG, kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    for i, key in ((0, "k"), (1, "v")):
+        if to_bf16:
+            want = np.zeros((slots, nkv, S, d), np.float32)
+            want[1, :, 5:5 + T] = kv4.bf16_value(kv4.bf16_bits(c.val[key][2, :, 3:3 + T].astype(np.float32)))
+            assert np.array_equal(dst[i].float().cpu().numpy(), want)
+        else:
+            codes, sb, zb = kv4.quantize(kv4.bf16_value(src[i].cpu().numpy().view(np.uint16)[2, :, 3:3 + T]), g)
+            got = c.host()
+            assert np.array_equal(got[i][1, :, 5:5 + T], kv4.pack_rows(codes, key == "k"))
+            assert np.array_equal(got[2 + i][1, :, 5:5 + T], kv4.pack_words(sb, zb))
