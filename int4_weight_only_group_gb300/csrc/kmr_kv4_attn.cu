@@ -29,7 +29,7 @@
 //     others (their mean is 7.5; fp16 has no 1031.5 to subtract), the base as z + 8 s or z + 7 s: a long
 //     row's output is small against the codes' offset, and the sum of the offset codes would lose its bits (at
 //     131072 positions an error of 5e-6 with c - 8 throughout).  The bases add per group in fp32.  The products
-//     are scaled by a power of two that follows the largest s seen, so that any bf16 scale fits fp16.
+//     are scaled by a power of two per query head and group (fit_unit).
 // Few query heads (rep <= 2) leave half of the columns empty.  With two groups or more the columns' halves then
 // stand for the halves of the head's dims: column 4 f + 2 h + part is query head h in half f.  A step of the scores
 // has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
@@ -83,6 +83,13 @@ __device__ __forceinline__ uint32_t pack_f16_rz(float a, float b) {
 // low part (mask 0xFFFFE000: what that cut leaves).
 __device__ __forceinline__ float part_of(float x, uint32_t mask) {
     return __fsub_rn(x, __uint_as_float(__float_as_uint(x) & mask));
+}
+// The scale of a word times a power of two, which as a pair of bf16 is (0, itself): one operation instead of taking the
+// base off and multiplying.  The sum with zero keeps a negative base from leaving -0 in the low half.
+__device__ __forceinline__ float scaled_s(uint32_t word, float unit) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(word), "r"(__float_as_uint(unit)), "r"(0u));
+    return __uint_as_float(r);
 }
 // The four codes of each half of a word as fp16 pairs c - OFF: nibbles (0, 4), (1, 5), (2, 6), (3, 7).
 template <int OFF>
@@ -158,6 +165,41 @@ template <bool PAIR>
 __device__ __forceinline__ int column_head(int g) { return PAIR ? (g >> 1) & 1 : g >> 1; }
 template <bool PAIR>
 __device__ __forceinline__ int column_half(int g) { return PAIR ? g >> 2 : 0; }
+
+// The scaling of the output's weights times scales: a power of two from 2^-126 to 2^126 for each query head and group, so that
+// neither a group beside others of far larger values nor a position of large values and no weight costs bits.  A product
+// has to stay below 2^15 (fp16); its two parts hold 22 bits of it from 2^-2 on, and 2^-24 below.
+//   * The scaling goes by the largest scale seen, brought to [2^kTop, 2^(kTop + 1)): weights are at most 2^kLag, so scales up
+//     to twice as large (limit_of) need no look at the weights.
+//   * Where that leaves the tiles' largest product below 2^-3, because the large scale has no weight, the scaling goes by
+//     the product, brought to [2^7, 2^8).  Tiles with a scale that may be too large are then looked at each.
+//   * As the reference rises by `oct` whole octaves, what was added before falls by as much, and the scaling may rise by it.
+// One scaling for all groups, as it was, kept 22 bits of the largest group only: beside one 10^4 (10^6) times larger
+// a group was off by 3e-4 (2e-2).  This costs 0 to 2% (16 rows of 8192, group 32: 47.7 -> 48.7 us, 8 query heads a KV head 48.5 ->
+// 48.7; one row of 131072, group 128: 38.5 -> 39.4); checking the products themselves in every tile cost 4 to 9%.
+constexpr int kLag = 8, kTop = 13 - kLag;
+__device__ __forceinline__ int unit_exponent(float u) { return int(__float_as_uint(u) >> 23); }
+// The scaling that brings x to [2^top, 2^(top + 1)).
+__device__ __forceinline__ float unit_for(float x, int top) {
+    return __uint_as_float(uint32_t(min(max(254 + top - unit_exponent(x), 1), 253)) << 23);
+}
+__device__ __forceinline__ float fit_unit(float was, float smax, float pmax, float oct, bool first) {
+    const float by_scale = unit_for(smax, kTop);
+    // (at most 2^126 / smax: a weight of 0 times an infinity would be no number)
+    const float cap = by_scale < 0x1p10f ? by_scale * 0x1p116f : 0x1p126f, by_product = fminf(unit_for(pmax, 7), cap);
+    const bool enough = pmax * by_scale >= 0x1p-3f || pmax == 0.f;
+    if (first) return enough ? by_scale : by_product;
+    if (smax * was >= float(1 << (kTop + 2))) return enough ? by_scale : (pmax * was >= 0x1p15f ? by_product : fminf(was, cap));
+    return pmax * was < 0x1p-3f ? fmaxf(was, fminf(by_scale, was * exp2f(oct))) : was;
+}
+// Scales from here on (as bits) may be too large for a scaling: 2^(kTop + 2) / it.
+__device__ __forceinline__ uint32_t limit_of(float u) { return uint32_t(min(256 + kTop - unit_exponent(u), 255)) << 23; }
+// The largest over the lanes of one t, which hold the tile's rows.
+__device__ __forceinline__ float max_over_rows(float v) {
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+    return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+}
 
 // Query fragments of the scores' B operand (this lane's column), and the queries' group sums and the scores' factor of
 // the head and half whose accumulators the lane holds (columns 2 t, 2 t + 1).  Heads from head0 on; past rep, zero.
@@ -283,6 +325,12 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
     const uint32_t wmask = (g & 1) ? 0xFFFFE000u : 0u;
     uint32_t uses = 0;                            // stages filled so far: stage k of them was use k / kStages of its buffer
     bool first = true;
+    // a lane looks through words of V of one position of a tile: of one group, or (d / g = 4) of two
+    constexpr int kLook = (NG + 1) / 2;
+    const int look_row = NG == 1 ? (lane & 15) : lane >> 1;
+    auto look = [&](const uint8_t* buf, int i0, uint32_t (&mine)[kLook]) {
+        lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * look_row : lane * (2 * NG)), mine);
+    };
 
     for (int b = b0; b < p.B; ++b) {
         if (CL && b != b0 && (!p.mass || p.slot_ids[b] != slot || kv4_row_error(p, b) != KMR_OK)) continue;
@@ -377,9 +425,16 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
 #pragma unroll
                 for (int i = 0; i < HG; ++i) zo[n][i] = 0.f;
             }
-            // exponent that the output accumulators are scaled by: from 13 on, so that a weight of up to 2^8 times the scaling
-            // stays finite before a V scale (0 where a group's values are all alike) multiplies it
-            int eref = 13;
+            // the column's scaling in each of its groups, and the smallest V scale (as bits) of the groups whose words the
+            // lane looks through that may be too large for it: both set by the first tiles
+            float unit[NT][HG];
+            uint32_t limit[kLook];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < HG; ++i) unit[n][i] = 1.f;
+#pragma unroll
+            for (int i = 0; i < kLook; ++i) limit[i] = 0u;
             for (int st = 0; t0 + st * kStagePos < t1; ++st, ++k) {
                 const uint32_t slot_of = (uses + k) % kStages, phase = ((uses + k) / kStages) & 1u;
                 const uint8_t* buf = ring + slot_of * M::kStage;
@@ -388,9 +443,9 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                 if (base0 < t1) {
                     // a tile is whole but for the row's last ones; one past the end counts for nothing
                     const bool whole = base0 + (TT - 1) * (16 * kTileWarps) + 16 <= t1;
-                    // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scale of the tiles' V
+                    // ---- scores of positions g and g + 8 of each tile for head 4 n + t, and the largest scales of the tiles' V
                     float sc[TT][NT][2];
-                    uint32_t top = 0u;
+                    uint32_t top[kLook] = {};
 #pragma unroll
                     for (int u = 0; u < TT; ++u) {
                         const int i0 = (u * kTileWarps + wt) * 16, base = base0 + u * (16 * kTileWarps);
@@ -456,19 +511,19 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                                 if (whole || base + g + 8 < t1) dst[8] = sc[u][n][1];
                             }
                         }
-                        uint32_t mine[(NG + 1) / 2];
-                        const int wpos = NG == 1 ? (lane & 15) : lane >> 1;
-                        lds_words(buf + 2 * M::kCodes + M::kWords + i0 * (4 * NG) + (NG == 1 ? 4 * wpos : lane * (2 * NG)), mine);
-                        if (whole || base + wpos < t1) {
-                            top = max(top, mine[0] & 0x7FFFFFFFu);
-                            if constexpr (NG == 4) top = max(top, mine[1] & 0x7FFFFFFFu);
+                        uint32_t mine[kLook];
+                        look(buf, i0, mine);
+                        if (whole || base + look_row < t1) {
+#pragma unroll
+                            for (int i = 0; i < kLook; ++i) top[i] = max(top[i], mine[i] & 0x7FFFFFFFu);
                         }
                     }
-                    const int etop = int(__reduce_max_sync(0xffffffffu, top) >> 23);
-                    // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is 8 octaves
-                    // above, so that most tiles rescale nothing; weights stay below 2^8
+                    // ---- running reference of the weights, 2^(score - m): it follows the maximum once that is kLag octaves above,
+                    // so that most tiles change neither it nor the scaling; weights stay below 2^kLag
                     float mn[NT];
-                    bool up = etop > eref;
+                    bool over = false;
+#pragma unroll
+                    for (int i = 0; i < kLook; ++i) over |= top[i] >= limit[i];
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         float c = fmaxf(sc[0][n][0], sc[0][n][1]);
@@ -476,29 +531,109 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
                         c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 16));
-                        mn[n] = fmaxf(m[n], c);
-                        up |= mn[n] > m[n] + 8.f;
+                        mn[n] = c > m[n] + float(kLag) ? c : m[n];
+                        over |= mn[n] != m[n];
                     }
-                    if (__any_sync(0xffffffffu, up)) {
-                        // room of two octaves, so that scales a little larger do not rescale again
-                        const int en = etop > eref ? min(etop + 2, 254) : eref;
-                        const float es = exp2f(float(eref - en));
-                        eref = en;
+                    if (st == 0) {
+                        // where every scale is more than 2^-8 of its group's largest, so is that of each head's best position, whose
+                        // weight is 1: the scaling goes by the scales
+                        float by_scale[NG];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            const float cf = m[n] == -INFINITY ? 0.f : exp2_approx(__fsub_rn(m[n], mn[n]));
-                            m[n] = mn[n];
-                            l[n] *= cf;
-                            const float ce = cf * es;
+                        for (int gr = 0; gr < NG; ++gr) {
+                            const uint32_t v = NG == 1 || (lane & 1) == gr / kLook ? top[gr % kLook] : 0u;
+                            by_scale[gr] = unit_for(__uint_as_float(__reduce_max_sync(0xffffffffu, v)), kTop);
+                        }
 #pragma unroll
-                            for (int i = 0; i < 2 * NB; ++i)
+                        for (int n = 0; n < NT; ++n)
 #pragma unroll
-                                for (int c = 0; c < 4; ++c) o[n][i][c] *= ce;
+                            for (int gr = 0; gr < HG; ++gr) unit[n][gr] = cgh ? by_scale[NG - HG + gr] : by_scale[gr];
+                        over = false;
 #pragma unroll
-                            for (int i = 0; i < HG; ++i) zo[n][i] *= cf;
+                        for (int i = 0; i < kLook; ++i) limit[i] = limit_of(NG > 1 && (lane & 1) ? by_scale[NG - kLook + i] : by_scale[i]);
+#pragma unroll
+                        for (int u = 0; u < TT; ++u) {
+                            uint32_t mine[kLook];
+                            look(buf, (u * kTileWarps + wt) * 16, mine);
+#pragma unroll
+                            for (int i = 0; i < kLook; ++i)
+                                over |= (whole || base0 + u * (16 * kTileWarps) + look_row < t1) &&
+                                        (mine[i] & 0x7FFFFFFFu) + (uint32_t(kTop + 5) << 23) < limit[i];
                         }
                     }
-                    const float unit = __uint_as_float(uint32_t(259 - eref) << 23);      // 2^(5 - (eref - 127))
+                    if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {
+                        // the tiles' largest scale, and largest weight times scale of the lane's head, in each group
+                        float smax[HG], pmax[NT][HG];
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            smax[gr] = 0.f;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) pmax[n][gr] = 0.f;
+                        }
+#pragma unroll
+                        for (int u = 0; u < TT; ++u) {
+                            const int i0 = (u * kTileWarps + wt) * 16, base = base0 + u * (16 * kTileWarps);
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                uint32_t v[HG];
+                                lds_words(buf + 2 * M::kCodes + M::kWords + (i0 + g + 8 * e) * (4 * NG) + cth * (4 * HG), v);
+#pragma unroll
+                                for (int gr = 0; gr < HG; ++gr) {
+                                    const float vs = base + g + 8 * e < t1 ? fabsf(kv4_s(v[gr])) : 0.f;
+                                    smax[gr] = fmaxf(smax[gr], vs);
+#pragma unroll
+                                    for (int n = 0; n < NT; ++n) {
+                                        const float mm = mn[n] == -INFINITY ? 0.f : mn[n];
+                                        pmax[n][gr] = fmaxf(pmax[n][gr], exp2_approx(__fsub_rn(sc[u][n][e], mm)) * vs);
+                                    }
+                                }
+                            }
+                        }
+                        float most[HG];                              // largest scaling of any head
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            smax[gr] = max_over_rows(smax[gr]);
+                            most[gr] = 0.f;
+                        }
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            const bool same = mn[n] == m[n];
+                            const float fall = same ? 0.f : mn[n] - m[n], oct = same ? 0.f : floorf(mn[n]) - floorf(m[n]);
+                            const float cf = exp2_approx(-fall);
+                            l[n] *= cf;
+#pragma unroll
+                            for (int gr = 0; gr < HG; ++gr) {
+                                const float was = __shfl_sync(0xffffffffu, unit[n][gr], 8 * t);      // column 2 t's
+                                const float now = fit_unit(was, smax[gr], max_over_rows(pmax[n][gr]), oct, st == 0);
+                                const float ce = exp2_approx(float(unit_exponent(now) - unit_exponent(was)) - fall);
+                                zo[n][gr] *= cf;
+                                constexpr int kEach = 2 * NB / HG;
+#pragma unroll
+                                for (int i = 0; i < kEach; ++i)
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c) o[n][gr * kEach + i][c] *= ce;
+                                most[gr] = fmaxf(most[gr], now);
+                                unit[n][gr] = __shfl_sync(0xffffffffu, now, 2 * cgh + column_head<PAIR>(g));
+                            }
+                        }
+                        uint32_t lim[HG];
+#pragma unroll
+                        for (int gr = 0; gr < HG; ++gr) {
+                            most[gr] = fmaxf(most[gr], __shfl_xor_sync(0xffffffffu, most[gr], 1));
+                            if (!PAIR) most[gr] = fmaxf(most[gr], __shfl_xor_sync(0xffffffffu, most[gr], 2));
+                            lim[gr] = limit_of(most[gr]);
+                        }
+#pragma unroll
+                        for (int i = 0; i < kLook; ++i) {
+                            if constexpr (PAIR)
+                                limit[i] = __shfl_sync(0xffffffffu, lim[i], 2 * (lane & 1));
+                            else if constexpr (NG == 1)
+                                limit[i] = lim[0];
+                            else
+                                limit[i] = (lane & 1) ? lim[NG / 2 + i] : lim[i];
+                        }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) m[n] = mn[n];
 #pragma unroll
                     for (int u = 0; u < TT; ++u) {
                         const int i0 = (u * kTileWarps + wt) * 16, base = base0 + u * (16 * kTileWarps);
@@ -520,8 +655,8 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                                     if (base + t + 4 * i >= t1) vw[i][gr] = 0u;
                             }
                         }
-                        // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then, scaled, of the lane's
-                        // column's head at the lane's four positions
+                        // ---- weights of head 4 n + t at positions g, g + 8 and what the bases add; then of the lane's column's head at
+                        // the lane's four positions
                         float w[NT][4];
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
@@ -533,12 +668,11 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                                 zo[n][gr] = __fmaf_rn(p0, __fmaf_rn(8.f, kv4_s(v0[gr]), kv4_z(v0[gr])), zo[n][gr]);
                                 zo[n][gr] = __fmaf_rn(p1, __fmaf_rn(7.f, kv4_s(v1[gr]), kv4_z(v1[gr])), zo[n][gr]);
                             }
-                            const float u0 = p0 * unit, u1 = p1 * unit;
                             const int src = 4 * t + column_head<PAIR>(g);
-                            w[n][0] = __shfl_sync(0xffffffffu, u0, src);
-                            w[n][1] = __shfl_sync(0xffffffffu, u0, src + 16);
-                            w[n][2] = __shfl_sync(0xffffffffu, u1, src);
-                            w[n][3] = __shfl_sync(0xffffffffu, u1, src + 16);
+                            w[n][0] = __shfl_sync(0xffffffffu, p0, src);
+                            w[n][1] = __shfl_sync(0xffffffffu, p0, src + 16);
+                            w[n][2] = __shfl_sync(0xffffffffu, p1, src);
+                            w[n][3] = __shfl_sync(0xffffffffu, p1, src + 16);
                         }
                         // ---- output: dims 32 k + 4 g + j in rows g (j = 0, 2) and g + 8 (j = 1, 3); PAIR: dims 32 k + 4 g + j
                         // of half 0 in rows g, of half 1 in rows g + 8
@@ -558,7 +692,7 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                             for (int n = 0; n < NT; ++n) {
                                 float a[4];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * kv4_s(vw[i][gr]), wmask);
+                                for (int i = 0; i < 4; ++i) a[i] = part_of(w[n][i] * scaled_s(vw[i][gr], unit[n][gr]), wmask);
                                 wf[n][0] = pack_f16_rz(a[0], a[1]);
                                 wf[n][1] = pack_f16_rz(a[2], a[3]);
                             }
@@ -596,7 +730,6 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
 
             // ---- the warp's state: o[head][dim], m, l
             if (u > u0) __syncthreads();                  // the split before this one has been merged
-            const float un = exp2f(float(eref - 127)) * 0x1p-5f;              // the products' scale, undone
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int hq = PAIR ? t & 1 : head0 + 4 * n + t;
@@ -604,9 +737,10 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                 lt += __shfl_xor_sync(0xffffffffu, lt, 4);
                 lt += __shfl_xor_sync(0xffffffffu, lt, 8);
                 lt += __shfl_xor_sync(0xffffffffu, lt, 16);
-                float zt[HG];
+                float zt[HG], un[HG];                                         // un: the products' scaling, undone
 #pragma unroll
                 for (int gr = 0; gr < HG; ++gr) {
+                    un[gr] = __uint_as_float(0x7F000000u - __float_as_uint(__shfl_sync(0xffffffffu, unit[n][gr], 8 * t)));
                     float v = zo[n][gr];
                     v += __shfl_xor_sync(0xffffffffu, v, 4);
                     v += __shfl_xor_sync(0xffffffffu, v, 8);
@@ -630,7 +764,7 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                                 const float(&a)[4] = o[n][2 * k + i / 2];
                                 v[i] = (i & 1) ? a[2] + a[3] : a[0] + a[1];
                             }
-                            v[i] = __fmaf_rn(v[i], un, z);
+                            v[i] = __fmaf_rn(v[i], un[k / BPG], z);
                         }
                         *reinterpret_cast<float4*>(wo + (wt * rep + hq) * D + 32 * (k + cth * HB) + 4 * g) =
                             make_float4(v[0], v[1], v[2], v[3]);

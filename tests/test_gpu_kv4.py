@@ -991,3 +991,120 @@ def test_refused_later_spans_leave_the_earlier_ones_alone(torch, to_bf16, T):
             got = c.host()
             assert np.array_equal(got[i][1, :, 5:5 + T], kv4.pack_rows(codes, key == "k"))
             assert np.array_equal(got[2 + i][1, :, 5:5 + T], kv4.pack_words(sb, zb))
+
+
+# ------------------------------------------------------------------ groups and positions of very different scale
+# Keys here give scores of a few units, off by some 20 roundings of partial sums of about 20 (base 2), 2^-25 of them each
+# and of either sign: 20 * 20^0.5 * 2^-25 = 3e-6 of a weight; outputs of independent weights are off by as much of
+# their size, and the values' own parts (22 bits, cut towards zero) by 2^-22.  Three times that:
+GROUP_TOL = 1e-5
+
+
+def group_errors(out, ref, g):
+    """Relative L2 of every (query head, group)."""
+    a, b = (np.asarray(x, np.float64).reshape(*x.shape[:-1], -1, g) for x in (out, ref))
+    return np.linalg.norm(a - b, axis=-1) / np.linalg.norm(b, axis=-1)
+
+
+GROUP_SHAPES = [(128, 32, 2, 1), (128, 32, 16, 8), (128, 32, 4, 1), (128, 32, 7, 1), (128, 64, 2, 1), (128, 64, 3, 1), (64, 32, 2, 1),
+                (64, 32, 4, 1), (64, 32, 8, 1), (128, 64, 6, 1)]
+
+
+@pytest.mark.parametrize("d,g,nq,nkv", GROUP_SHAPES)
+@pytest.mark.parametrize("S", [1104, 4112])
+def test_groups_of_different_scale(torch, d, g, nq, nkv, S):
+    """Channel groups of V whose scales lie up to 10^12 apart: every group keeps its own precision."""
+    r = np.random.default_rng(d + g + nq + S)
+    L = S - 5
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    q = r.standard_normal((1, nq, d)).astype(np.float32)
+    for sizes in ([1, 1e2, 1e3, 1e4], [1e6, 1, 1e-6, 1e2], [1e-12, 1, 1e-4, 1e-8], [0, 1, 1e8, 1e4]):
+        x = r.standard_normal((1, nkv, S, d)).astype(np.float32) * np.repeat(np.float32(sizes)[:d // g], g)
+        V = set_values(torch, c, x, g)
+        out = attend(torch, c.dev, q, [0], [L - 1])
+        ref, _ = kv4.attention(q[0], c.val["k"][0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+        zero = np.repeat(np.float32(sizes)[:d // g] == 0, g)
+        assert not out[0][:, zero].any()
+        err = group_errors(out[0], np.where(zero, 1.0, ref), g)[:, np.float32(sizes)[:d // g] != 0]
+        assert (err <= GROUP_TOL).all(), (sizes, err.max(0))
+
+
+@pytest.mark.parametrize("d,g,nq,nkv", GROUP_SHAPES + [(128, 128, 2, 1), (128, 128, 8, 1), (64, 64, 8, 1)])
+@pytest.mark.parametrize("S", [1104, 4112])
+@pytest.mark.parametrize("size", [1e6, 1e9])
+def test_large_values_of_no_weight(torch, d, g, nq, nkv, S, size):
+    """One position whose V is 10^6 or 10^9 times the others' and whose weight is 2^-60 or less, first, in the middle or last in
+    the row: nothing of it is seen in the output."""
+    r = np.random.default_rng(d + g + nq + S)
+    L = S - 5
+    q = r.standard_normal((1, nq, d)).astype(np.float32)
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    kx, vx = ((r.standard_normal((1, nkv, S, d))).astype(np.float32) for _ in range(2))
+    for at in (0, 77, L - 1):
+        k1, v1 = kx.copy(), vx.copy()
+        v1[:, :, at] *= np.float32(size)
+        for h in range(nkv):                                  # against all of the KV head's queries
+            mine = q[0, h * (nq // nkv):(h + 1) * (nq // nkv)].astype(np.float64)
+            away = np.linalg.lstsq(mine, np.full(len(mine), -60.0 * math.sqrt(d)), rcond=None)[0]
+            k1[0, h, at] = away
+        codes, sb, zb = kv4.quantize(k1, g)
+        c.dev.tensors[0].copy_(torch.from_numpy(kv4.pack_rows(codes, True)))
+        c.dev.tensors[2].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+        K, V = kv4.dequantize(codes, sb, zb), set_values(torch, c, v1, g)
+        out = attend(torch, c.dev, q, [0], [L - 1])
+        ref, m = kv4.attention(q[0], K[0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+        assert m[:, at].max() <= 2.0 ** -58
+        assert group_errors(out[0], ref, g).max() <= GROUP_TOL, at
+
+
+@pytest.mark.parametrize("d,g,nq", [(128, 32, 2), (128, 32, 4), (128, 32, 8), (128, 128, 4), (64, 64, 8), (64, 32, 5)])
+@pytest.mark.parametrize("S", [1104, 4112])
+def test_large_values_that_one_head_looks_at(torch, d, g, nq, S):
+    """A position of large V to which the first query head gives its weight and the others none: either kind of head is right."""
+    r = np.random.default_rng(d + g + nq + S + 1)
+    L, at = S - 5, 300
+    q = r.standard_normal((1, nq, d)).astype(np.float32)
+    c = Cache(torch, r, 1, 1, S, d, g, [L])
+    kx, vx = ((r.standard_normal((1, 1, S, d))).astype(np.float32) for _ in range(2))
+    vx[:, :, at] *= np.float32(1e8)
+    goal = np.full(nq, -60.0 * math.sqrt(d))
+    goal[0] = 6.0 * math.sqrt(d)
+    kx[0, 0, at] = np.linalg.lstsq(q[0].astype(np.float64), goal, rcond=None)[0]
+    codes, sb, zb = kv4.quantize(kx, g)
+    c.dev.tensors[0].copy_(torch.from_numpy(kv4.pack_rows(codes, True)))
+    c.dev.tensors[2].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+    K, V = kv4.dequantize(codes, sb, zb), set_values(torch, c, vx, g)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    ref, m = kv4.attention(q[0], K[0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+    assert np.abs(ref[0]).max() >= 1e5 and np.abs(ref[1:]).max() <= 100
+    # the key that answers 6 to one query and -60 to the others is long: its score's terms are some 8 times the others'
+    err = group_errors(out[0], ref, g).max(-1)
+    assert err[0] <= 8 * GROUP_TOL and err[1:].max() <= GROUP_TOL
+
+
+@pytest.mark.parametrize("d,g,nq", [(128, 32, 2), (128, 32, 3), (128, 128, 2), (128, 64, 8), (64, 64, 6), (64, 32, 2)])
+@pytest.mark.parametrize("S", [1104, 4112])
+@pytest.mark.parametrize("rise", [60.0, -60.0, 400.0])
+def test_scores_that_rise_while_values_fall(torch, d, g, nq, S, rise):
+    """Scores that climb by `rise` octaves along the row while V falls by 10^12 (or the other way round): the positions that
+    count are small beside what the row held before."""
+    r = np.random.default_rng(d + g + nq + S + 2)
+    L = S - 5
+    # one dim of each key and query carries the score: a code of 0 or 15 under an exact scale, so that the
+    # score itself is rounded three times, 2^-24 * 400 * ln 2 each at most
+    ramp = np.linspace(0, rise, S).astype(np.float32)
+    kx = np.zeros((1, 1, S, d), np.float32)
+    step = kv4.bf16_value(kv4.bf16_bits(np.abs(ramp) / 15)) * 15
+    kx[0, 0, :, 3] = np.sign(rise) * step
+    q = np.zeros((1, nq, d), np.float32)
+    q[0, :, 3] = math.log(2) * math.sqrt(d)
+    fall = np.exp2(np.linspace(0, -40, S) * np.sign(rise)).astype(np.float32)
+    vx = r.standard_normal((1, 1, S, d)).astype(np.float32) * fall[None, None, :, None]
+    c = Cache(torch, r, 1, 1, S, d, g, [L])
+    codes, sb, zb = kv4.quantize(kx, g)
+    c.dev.tensors[0].copy_(torch.from_numpy(kv4.pack_rows(codes, True)))
+    c.dev.tensors[2].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+    K, V = kv4.dequantize(codes, sb, zb), set_values(torch, c, vx, g)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    ref, _ = kv4.attention(q[0], K[0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+    assert group_errors(out[0], ref, g).max() <= GROUP_TOL + 4 * 2.0 ** -24 * abs(rise) * math.log(2)
