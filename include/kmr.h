@@ -327,7 +327,8 @@ int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_
  *               dst = src it may be `mass` itself)
  *   kept        device int32 [B, n_kv, keep]: the kept positions, then -1
  *   new_lengths device int32 [B]
- * Positions of the destination row past new_lengths[b] keep their contents.  Two caches of a call are the
+ * kept and new_lengths share memory neither with each other nor with the ids and lengths (KMR_ERR_INVALID_ARG): an update
+ * in place goes through another array.  Positions of the destination row past new_lengths[b] keep their contents.  Two caches of a call are the
  * same cache or share no memory.  Errors: KMR_ERR_INVALID_ARG, KMR_ERR_SHAPE, KMR_ERR_BATCH,
  * KMR_ERR_CACHE_FULL (keep > dst's max_len); on the device a row is refused (kept -1, new_lengths 0, nothing
  * moved) where a slot is out of range or the destination is another row's destination or, in the same

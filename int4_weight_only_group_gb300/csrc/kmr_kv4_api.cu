@@ -1,6 +1,7 @@
 // C ABI of the 4-bit KV cache (declared in kmr.h): argument checks, then the launches of kmr_kv4.cu
 // and kmr_kv4_attn.cu.
 #include <cmath>
+#include <initializer_list>
 
 #include "kmr_kv4.cuh"
 
@@ -28,6 +29,11 @@ int view_of(const kmr_kv4_cache* c, Kv4View* v) {
     v->d = c->head_dim;
     v->g = c->group;
     return KMR_OK;
+}
+
+bool overlap(const void* a, size_t abytes, const void* b, size_t bbytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + bbytes && y < x + abytes;
 }
 
 bool heads_ok(int nq, int nkv) { return nq >= 1 && nq % nkv == 0 && nq / nkv <= kKv4MaxRep; }
@@ -171,6 +177,11 @@ extern "C" int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst,
     // one cache has one shape, and one mass only together with it
     if (p.same && (p.src.slots != p.dst.slots || p.src.S != p.dst.S)) return KMR_ERR_SHAPE;
     if (!p.same && mass == dst_mass) return KMR_ERR_INVALID_ARG;
+    // every head's CTAs read the row's ids and length, each row those of the others: what is written lies elsewhere
+    const size_t ids = size_t(B) * 4, list = ids * p.src.nkv * keep;
+    for (const int32_t* in : {src_slot_ids, dst_slot_ids, lengths})
+        if (overlap(new_lengths, ids, in, ids) || overlap(kept, list, in, ids)) return KMR_ERR_INVALID_ARG;
+    if (overlap(kept, list, new_lengths, ids)) return KMR_ERR_INVALID_ARG;
     if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
     p.src_ids = src_slot_ids;
     p.dst_ids = dst_slot_ids;

@@ -126,3 +126,12 @@ def test_binding_checks_the_cache_tensors(L):
     with pytest.raises(kmr.KmrError) as e:
         kmr.kmr_kv4_append(c, 16, 16, 16, 16, None, 1, 1, 3, None, None, 1e-6, 1e6, (16, 16, 1), 16)
     assert e.value.code == kmr.KMR_ERR_SHAPE
+
+
+def test_evict_outputs_share_no_memory_with_what_is_read(L):
+    """`lengths` cut in place, for instance: another head's CTAs would read the cut length.  4 rows, 8 heads, 8 kept."""
+    at = dict(ids=0x1000, dids=0x2000, n=0x3000, kept=0x4000, new=0x5000, B=4)
+    for kw in (dict(new=0x3000), dict(new=0x1000), dict(new=0x2000), dict(new=0x300C), dict(new=0x2FF4), dict(kept=0x3000),
+               dict(kept=0x1004), dict(kept=0x2000), dict(kept=0x3000 - 4 * 8 * 8 * 4 + 4), dict(new=0x4000), dict(kept=0x500C),
+               dict(new=0x4000 + 4 * 8 * 8 * 4 - 4)):
+        assert call(L, "kmr_kv4_evict", cache(), **{**at, **kw}) == kmr.KMR_ERR_INVALID_ARG, kw
