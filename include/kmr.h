@@ -256,7 +256,8 @@ typedef struct kmr_kv4_cache {
  * (i, i + d/2), frequency theta^(-2i/d), as the decode step), K and V quantised to 4 bits and written, q
  * written out for kmr_decode_attn_kv4.  One launch.
  *   qkv        device fp32 [B, T, (n_q + 2 n_kv) d]: raw projection rows [q heads; k heads; v heads]
- *   positions  device int32 [3, B, T]: (T, H, W) ids; the angles are exact for any id
+ *   positions  device int32 [3, B, T]: (T, H, W) ids, any int32; an angle is off by |id| 2^-65 turns, its cosine and sine
+ *              by 0.7 ulp (below 2^-28 turns by 2^-23 of themselves)
  *   slot_ids, cache_position  device int32 [B]: token t of row b goes to position
  *              cache_position[b] + t of slot slot_ids[b]
  *   n_tokens   device int32 [B], 0..T: tokens of row b, the rest is padding: not read, q_out left as it

@@ -253,15 +253,17 @@ __device__ __forceinline__ int convert_row_error(const Kv4ConvertParams& p, int 
 }
 
 // ------------------------------------------------------------------ new tokens
-// Cosine and sine of an angle of turn / 2^32 turns, to a little over half a step of single precision: the nearest
-// quarter turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, and the Taylor series' later
-// terms (at most a tenth of the sum) are added to the leading ones at the end, the roundings of which are kept.
-__device__ __forceinline__ void cos_sin_turn(int turn, float& c, float& s) {
-    const int quarter = int((unsigned(turn) + (1u << 29)) >> 30);
-    const int rem = int(unsigned(turn) - (unsigned(quarter) << 30));       // [-2^29, 2^29)
+// Cosine and sine of an angle of turn / 2^64 turns, to 0.7 ulp (below 2^-28 turns 2^-23 of themselves): the nearest quarter
+// turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, and the Taylor series' later terms
+// (at most a tenth of the sum) are added to the leading ones at the end, the roundings of which are kept.
+__device__ __forceinline__ void cos_sin_turn(unsigned long long turn, float& c, float& s) {
+    const uint32_t high = uint32_t(turn >> 32), low = uint32_t(turn);
+    const int quarter = int((high + (1u << 29)) >> 30);
+    const int rem = int(high - (uint32_t(quarter) << 30));                // [-2^29, 2^29), and low / 2^32
     constexpr double kUnit = 6.283185307179586477 / 4294967296.0;
     const float uh = float(kUnit), ul = float(kUnit - double(uh));
-    const float rh = __int2float_rn(rem), rl = __int2float_rn(rem - __float2int_rn(rh));
+    const float rh = __int2float_rn(rem);
+    const float rl = __fmaf_rn(__uint2float_rn(low), 0x1p-32f, __int2float_rn(rem - __float2int_rn(rh)));
     const float th = __fmul_rn(rh, uh);
     const float tl = __fmaf_rn(rl, uh, __fmaf_rn(rh, ul, __fmaf_rn(rh, uh, -th)));
     const float u = __fmul_rn(th, th);
@@ -278,8 +280,8 @@ __device__ __forceinline__ void cos_sin_turn(int turn, float& c, float& s) {
 }
 
 // One CTA per token.  The token's angles are formed once: frequency i advances by theta^(-2i/d) / 2 pi
-// turns per position, held as a 64-bit fraction, so that position x fraction mod 1 is exact for any
-// position and the angle keeps its bits far into a long context.  Then each warp takes eight heads at a time.
+// turns per position, held as a 64-bit fraction, so that position x fraction mod 1 needs no rounding: the angle of
+// position p is off by |p| 2^-65 turns, 2^-34 (4e-10 radians) at most.  Then each warp takes eight heads at a time.
 template <int D, int G>
 __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant__ Kv4AppendParams p) {
     constexpr int NB = D / 32, NG = D / G;
@@ -299,8 +301,7 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
     if (tid < D / 2) {
         const int axis = tid < p.sec0 ? 0 : (tid < p.sec0 + p.sec1 ? 1 : 2);
         const long long x = p.positions[(size_t(axis) * p.B + b) * p.T + t];
-        const unsigned long long turn = (unsigned long long)x * p.turn[tid];
-        cos_sin_turn(int(turn >> 32), cs[tid], sn[tid]);
+        cos_sin_turn((unsigned long long)x * p.turn[tid], cs[tid], sn[tid]);
     }
     const bool lose = later_row_writes(b, p.B, slot, pos, pos + 1, p.slot_ids, p.cpos, p.n_tokens, p.T,
                                        [&](int r) { return append_row_error(p, r) != KMR_OK; });

@@ -63,6 +63,45 @@ int convert(const kmr_kv4_cache* cache, uint16_t* k16, uint16_t* v16, int slots1
     return launch_kv4_convert(p, to_bf16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KMR_OK : KMR_ERR_CUDA;
 }
 
+// A number as the sum of two doubles, some 2^-104 of it (Dekker 1971; products by an exact fused multiply-add).
+struct Two {
+    double hi, lo;
+};
+Two sum_of(double a, double b) {                        // |a| >= |b|
+    const double s = a + b;
+    return {s, b - (s - a)};
+}
+Two operator*(Two a, Two b) {
+    const double p = a.hi * b.hi, e = std::fma(a.hi, b.hi, -p);
+    return sum_of(p, e + (a.hi * b.lo + a.lo * b.hi));
+}
+Two root(Two a) {
+    const double x = std::sqrt(a.hi), e = std::fma(-x, x, a.hi);
+    return sum_of(x, (e + a.lo) / (2.0 * x));
+}
+// The fraction of x, rounded to 2^-64.
+unsigned long long fraction_of(Two x) {
+    const double top = (x.hi - std::floor(x.hi)) * 0x1p64, whole = std::floor(top);      // exact
+    const double rest = (x.lo - std::floor(x.lo + 0.5)) * 0x1p64 + (top - whole);
+    return (unsigned long long)whole + (unsigned long long)std::llrint(std::fmin(rest, 0x1.fffffffffffffp62));
+}
+
+// theta^(-i / half) / 2 pi turns per position, modulo one turn, as 64-bit fractions: half is 32 or 64, so the step
+// theta^(-1 / half) is five or six square roots.
+void rope_turns(float theta, int half, unsigned long long* turn) {
+    const double t = theta, q = 1.0 / t;
+    Two step = {q, std::fma(-q, t, 1.0) / t};
+    for (int n = half; n > 1; n /= 2) step = root(step);
+    constexpr int kChains = 8;
+    Two v[kChains] = {{0.15915494309189535, -9.839338337591243e-18}}, far = step;
+    for (int i = 1; i < kChains; ++i) v[i] = v[i - 1] * step;
+    for (int n = 1; n < kChains; n *= 2) far = far * far;
+    for (int i = 0; i < half; ++i) {
+        turn[i] = fraction_of(v[i % kChains]);
+        v[i % kChains] = v[i % kChains] * far;
+    }
+}
+
 }  // namespace
 
 extern "C" int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, const int32_t* positions,
@@ -98,13 +137,7 @@ extern "C" int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, cons
     p.sec1 = sections[1];
     p.q_out = q_out;
     p.mass = mass;
-    // theta^(-2i/d) / 2 pi turns per position, modulo one turn, as a 64-bit fraction
-    const double step = std::pow(double(rope_theta), -2.0 / p.c.d);
-    double turn = 0.15915494309189533577;
-    for (int i = 0; i < half; ++i, turn *= step) {
-        const double f = turn - std::floor(turn);
-        p.turn[i] = (unsigned long long)(std::ldexp(f, 63)) << 1;
-    }
+    rope_turns(rope_theta, half, p.turn);
     return launch_kv4_append(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KMR_OK : KMR_ERR_CUDA;
 }
 

@@ -1108,3 +1108,66 @@ def test_scores_that_rise_while_values_fall(torch, d, g, nq, S, rise):
     out = attend(torch, c.dev, q, [0], [L - 1])
     ref, _ = kv4.attention(q[0], K[0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
     assert group_errors(out[0], ref, g).max() <= GROUP_TOL + 4 * 2.0 ** -24 * abs(rise) * math.log(2)
+
+
+# ------------------------------------------------------------------ angles
+def exact_angles(theta, half):
+    """theta^(-i / half) / 2 pi as Decimals of 60 digits, and 2 pi."""
+    import decimal
+    decimal.getcontext().prec = 60
+    two_pi = 2 * decimal.Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    ln = decimal.Decimal(float(np.float32(theta))).ln()
+    return [(ln * -i / half).exp() / two_pi for i in range(half)], two_pi
+
+
+@pytest.mark.parametrize("d,theta", [(128, 1e6), (64, 1e6), (128, 1e4), (64, 5e5)])
+def test_append_cosines_and_sines(torch, d, theta):
+    """Queries whose first half is 1 and whose second half is 0 come out as the cosines and sines: to 0.7 ulp of themselves, plus
+    the angle's own error of |position| 2^-65 turns, for any position, the slow pairs' tiny sines among them."""
+    half, nq = d // 2, 1
+    pos = np.array([0, 1, 2, 3, 17, -1, -5, 100, 4095, 131071, -99999, 2 ** 20 + 1, 999999937, -123456789, 2 ** 31 - 1, -2 ** 31],
+                   np.int64)
+    T = len(pos)
+    qkv = np.zeros((1, T, 3, d), np.float32)
+    qkv[0, :, 0, :half] = 1.0
+    c = kmr.Kv4Cache.zeros(1, 1, 16, d, 32)
+    q = torch.zeros((1, T, nq, d), device="cuda")
+    p3 = np.broadcast_to(pos.astype(np.int32), (3, 1, T)).copy()
+    kmr.kmr_kv4_append(c, torch.from_numpy(qkv).cuda(), torch.from_numpy(p3).cuda(), i32(torch, [0]), i32(torch, [0]), None, 1, T, nq,
+                       None, None, 1e-6, theta, SECTIONS[d], q, None, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    got = q.cpu().numpy()[0, :, 0].astype(np.float64)
+    turns, two_pi = exact_angles(theta, half)
+    for t, p in enumerate(pos):
+        for i in range(half):
+            a = turns[i] * int(p)
+            a = float((a - a.to_integral_value()) * two_pi)            # within half a turn
+            off = abs(int(p)) * 2.0 ** -65 * 2 * math.pi
+            for have, want in ((got[t, i], math.cos(a)), (got[t, half + i], math.sin(a))):
+                assert abs(have - want) <= 0.75 * np.spacing(np.float32(abs(want))) + 1.01 * off, (p, i, have, want)
+
+
+def test_append_rotations_far_and_near(torch):
+    """Random pairs at positions of every size: cosine and sine to 0.7 ulp, two products and their sum, each rounded
+    once, of the pair's size."""
+    r = np.random.default_rng(91)
+    d, nq, T = 128, 2, 64
+    pos = (r.choice([-1, 1], (3, 1, T)) * np.floor(2.0 ** r.uniform(0, 31, (3, 1, T)))).astype(np.int64).clip(-2 ** 31, 2 ** 31 - 1)
+    qkv = r.standard_normal((1, T, nq + 2, d)).astype(np.float32)
+    c = kmr.Kv4Cache.zeros(1, 1, T, d, 32)
+    q = torch.zeros((1, T, nq, d), device="cuda")
+    kmr.kmr_kv4_append(c, torch.from_numpy(qkv).cuda(), torch.from_numpy(pos.astype(np.int32)).cuda(), i32(torch, [0]), i32(torch, [0]),
+                       None, 1, T, nq, None, None, 1e-6, 1e6, SECTIONS[d], q, None, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    got = q.cpu().numpy()[0].astype(np.float64)
+    turns, two_pi = exact_angles(1e6, 64)
+    for t in range(T):
+        for i in range(64):
+            axis = 0 if i < 16 else (1 if i < 40 else 2)
+            a = turns[i] * int(pos[axis, 0, t])
+            a = float((a - a.to_integral_value()) * two_pi)
+            x, y = (qkv[0, t, :nq, k].astype(np.float64) for k in (i, i + 64))
+            # 0.7 ulp (2^-23 at most of the value), a product and the sum: 2^-24 each; the angle 2^-34 turns
+            tol = (0.75 * 2.0 ** -23 + 2 * 2.0 ** -24 + 2.0 ** -34 * 2 * math.pi) * (np.abs(x) + np.abs(y))
+            assert (np.abs(got[t, :, i] - (x * math.cos(a) - y * math.sin(a))) <= tol).all(), (t, i)
+            assert (np.abs(got[t, :, i + 64] - (y * math.cos(a) + x * math.sin(a))) <= tol).all(), (t, i)
