@@ -148,7 +148,7 @@ struct SplitSmem {
     static constexpr int kStage = 2 * kCodes + 2 * kWords;
     static constexpr int kRing = kStages * kStage;
     __host__ __device__ static constexpr int merge(int rep) { return S::kTileWarps * rep * (D + 2) * 4; }
-    static constexpr int kQuery = 4 * (D / 32) + D / G + 1;         // words of a lane's query per n-tile
+    static constexpr int kQuery = 4 * (D / 32) + 2 * (D / G);         // words of a lane's query per n-tile
     static constexpr int kQueryBytes = S::kHeadWarps * S::kNTiles * kQuery * 128;
     __host__ __device__ static constexpr int base(int rep) { return 128 + kQueryBytes + kRing + merge(rep); }
     // a cluster's additions: the states pushed here (a slice of o of every split; every m and l), the scores
@@ -201,8 +201,10 @@ __device__ __forceinline__ float max_over_rows(float v) {
     return fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
 }
 
-// Query fragments of the scores' B operand (this lane's column), and the queries' group sums and the scores' factor of
-// the head and half whose accumulators the lane holds (columns 2 t, 2 t + 1).  Heads from head0 on; past rep, zero.
+// Query fragments of the scores' B operand (this lane's column), and the queries' group sums and factors of the head and
+// half whose accumulators the lane holds (columns 2 t, 2 t + 1).  A head's query is scaled by a power of two per group, so that
+// a group keeps its 22 bits beside others of far larger queries (with one for all, a K group 10^8 times larger where the
+// query is as much smaller put outputs off by 1e-3); the group's s takes it back.  Heads from head0 on; past rep, zero.
 template <int D, int G, int NT, bool PAIR>
 __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, int h, int rep, int head0, int lane,
                                                 uint32_t* out) {
@@ -211,7 +213,9 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int hq = head0 + 4 * n + column_head<PAIR>(g);
-        float x[NB][8], mx = 0.f;
+        float x[NB][8], mx[NG];
+#pragma unroll
+        for (int i = 0; i < NG; ++i) mx[i] = 0.f;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             float4 u = make_float4(0.f, 0.f, 0.f, 0.f), v = u;
@@ -224,41 +228,42 @@ __device__ __forceinline__ void query_fragments(const Kv4AttnParams& p, int b, i
             x[k][0] = u.x; x[k][1] = u.y; x[k][2] = u.z; x[k][3] = u.w;
             x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[k][e]));
+            for (int e = 0; e < 8; ++e) mx[k / BPG] = fmaxf(mx[k / BPG], fabsf(x[k][e]));
         }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        if (PAIR) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-        // largest |q| sigma in [2^13, 2^14): sigma = 2^(13 - e), held within the normal range
-        int e = int(__float_as_uint(mx) >> 23) - 127;
-        e = max(e, -113);
-        const float sig = __uint_as_float(uint32_t(13 - e + 127) << 23);
-        float gs[NG];
+        // each group's largest |q| sigma in [2^13, 2^14): sigma = 2^(13 - e), held within the normal range
+        float gs[NG], sig[NG];
+        uint32_t ex[NG];                                              // 2^e
 #pragma unroll
-        for (int i = 0; i < NG; ++i) gs[i] = 0.f;
+        for (int i = 0; i < NG; ++i) {
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+            mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+            const uint32_t e = max(__float_as_uint(mx[i]) >> 23, 14u);
+            ex[i] = e << 23;
+            sig[i] = __uint_as_float((267u - e) << 23);
+            gs[i] = 0.f;
+        }
         const uint32_t mask = (g & 1) ? 0xFFFFE000u : 0u;
-        uint32_t* at = out + n * (4 * NB + NG + 1) * 32 + lane;
+        uint32_t* at = out + n * (4 * NB + 2 * NG) * 32 + lane;
 #pragma unroll
         for (int k = 0; k < NB; ++k) {
             float y[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 gs[k / BPG] += x[k][i];
-                y[i] = part_of(x[k][i] * sig, mask);
+                y[i] = part_of(x[k][i] * sig[k / BPG], mask);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) at[(4 * k + i) * 32] = pack_f16_rz(y[i], y[i + 4]);
         }
         const float base2 = p.scale * kLog2e;
-        const float f = base2 * 0x1p-13f * exp2f(float(e));               // base2 / sigma
         // columns 2 t, 2 t + 1 are lane 8 t's
-        at[(4 * NB + NG) * 32] = __float_as_uint(__shfl_sync(0xffffffffu, f, 8 * t));
 #pragma unroll
         for (int i = 0; i < NG; ++i) {
             float v = gs[i];
             v += __shfl_xor_sync(0xffffffffu, v, 1);
             v += __shfl_xor_sync(0xffffffffu, v, 2);
             at[(4 * NB + i) * 32] = __float_as_uint(__shfl_sync(0xffffffffu, v * base2, 8 * t));
+            at[(4 * NB + NG + i) * 32] = __shfl_sync(0xffffffffu, ex[i], 8 * t);
         }
     }
 }
@@ -288,8 +293,11 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
     const int rep = p.nq / p.c.nkv;
     // warp 1 (and 2, for the second group of heads) prepares the query for all while warp 0 looks up the row and starts
     // its copies
-    constexpr int kQueryWords = (4 * HB + HG + 1) * 32;              // of an n-tile
+    constexpr int kQueryWords = (4 * HB + 2 * HG) * 32;              // of an n-tile
     uint32_t* qsh = reinterpret_cast<uint32_t*>(smem + 128);         // [head group][n-tile][value][lane]
+    // four groups' factors of the query are read from there each time where two warps have heads of their own (16 rows of
+    // 8192, 6 heads a KV head: 89.2 us against 90.4 with them in registers; up to 4 heads, 4 KV heads: 32.8 against 32.3)
+    constexpr bool kSharedExps = HG == 4 && kHeadWarps > 1;
     const int hw = warp / kTileWarps, wt = warp % kTileWarps, head0 = 4 * NT * hw;
     auto prepare_query = [&](int b) {
         if (warp >= 1 && warp <= kHeadWarps)
@@ -376,7 +384,8 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
         if (CL && !first) prepare_query(b);
         __syncthreads();
         uint32_t qf[NT][NB][4];                       // PAIR: [half][block of the half], zero for the other half
-        float qsum[NT][HG], fac[NT];
+        float qsum[NT][HG], qex[NT][HG];
+        const float unscore = p.scale * kLog2e * 0x1p-13f;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const uint32_t* at = qsh + (hw * NT + n) * kQueryWords + lane;
@@ -393,8 +402,10 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                     }
                 }
 #pragma unroll
-            for (int i = 0; i < HG; ++i) qsum[n][i] = __uint_as_float(at[(4 * HB + i) * 32]);
-            fac[n] = __uint_as_float(at[(4 * HB + HG) * 32]);
+            for (int i = 0; i < HG; ++i) {
+                qsum[n][i] = __uint_as_float(at[(4 * HB + i) * 32]);
+                if constexpr (!kSharedExps) qex[n][i] = __uint_as_float(at[(4 * HB + HG + i) * 32]);
+            }
         }
 
         // base-2 scores for the mass: [head][position], in shared memory from the CTA's first position on
@@ -485,16 +496,18 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                             }
 #pragma unroll
                             for (int n = 0; n < NT; ++n) {
-                                sc[u][n][0] = __fmaf_rn(kv4_s(w0[gr]), acc[n][0] + acc[n][1], sc[u][n][0]);
-                                sc[u][n][1] = __fmaf_rn(kv4_s(w1[gr]), acc[n][2] + acc[n][3], sc[u][n][1]);
+                                const float ex = kSharedExps ? __uint_as_float(qsh[(hw * NT + n) * kQueryWords + lane + (4 * HB + HG + gr) * 32])
+                                                             : qex[n][gr];
+                                sc[u][n][0] = __fmaf_rn(scaled_s(w0[gr], ex), acc[n][0] + acc[n][1], sc[u][n][0]);
+                                sc[u][n][1] = __fmaf_rn(scaled_s(w1[gr], ex), acc[n][2] + acc[n][3], sc[u][n][1]);
                                 zc[n][0] = __fmaf_rn(kv4_z(w0[gr]), qsum[n][gr], zc[n][0]);
                                 zc[n][1] = __fmaf_rn(kv4_z(w1[gr]), qsum[n][gr], zc[n][1]);
                             }
                         }
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            sc[u][n][0] = __fmaf_rn(sc[u][n][0], fac[n], zc[n][0]);
-                            sc[u][n][1] = __fmaf_rn(sc[u][n][1], fac[n], zc[n][1]);
+                            sc[u][n][0] = __fmaf_rn(sc[u][n][0], unscore, zc[n][0]);
+                            sc[u][n][1] = __fmaf_rn(sc[u][n][1], unscore, zc[n][1]);
                             if constexpr (PAIR) {
                                 // the other half's part is two lanes away; both lanes add the same two numbers
                                 sc[u][n][0] += __shfl_xor_sync(0xffffffffu, sc[u][n][0], 2);

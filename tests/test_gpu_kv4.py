@@ -1171,3 +1171,22 @@ def test_append_rotations_far_and_near(torch):
             tol = (0.75 * 2.0 ** -23 + 2 * 2.0 ** -24 + 2.0 ** -34 * 2 * math.pi) * (np.abs(x) + np.abs(y))
             assert (np.abs(got[t, :, i] - (x * math.cos(a) - y * math.sin(a))) <= tol).all(), (t, i)
             assert (np.abs(got[t, :, i + 64] - (y * math.cos(a) + x * math.sin(a))) <= tol).all(), (t, i)
+
+
+@pytest.mark.parametrize("d,g,nq,nkv", GROUP_SHAPES + [(128, 128, 2, 1), (64, 64, 8, 1)])
+@pytest.mark.parametrize("S", [1104, 4112])
+def test_key_groups_of_different_scale(torch, d, g, nq, nkv, S):
+    """Channel groups of K up to 10^16 apart, met by queries that are as much smaller there, so that every group has its say
+    in the scores: they are off by no more than those of groups alike."""
+    r = np.random.default_rng(d + g + nq + S + 3)
+    L = S - 5
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    for sizes in ([1, 1e8, 1e-8, 1e4], [1e-6, 1, 1e6, 1e10], [3e-12, 3e4, 1, 1e-3]):
+        size = np.repeat(np.float32(sizes)[:d // g], g)
+        codes, sb, zb = kv4.quantize(r.standard_normal((1, nkv, S, d)).astype(np.float32) * size, g)
+        c.dev.tensors[0].copy_(torch.from_numpy(kv4.pack_rows(codes, True)))
+        c.dev.tensors[2].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+        q = (r.standard_normal((1, nq, d)).astype(np.float32) / size).astype(np.float32)
+        out = attend(torch, c.dev, q, [0], [L - 1])
+        ref, _ = kv4.attention(q[0], kv4.dequantize(codes, sb, zb)[0, :, :L], c.val["v"][0, :, :L], 1 / math.sqrt(d))
+        assert group_errors(out[0], ref, g).max() <= GROUP_TOL, sizes
