@@ -135,3 +135,52 @@ def test_evict_outputs_share_no_memory_with_what_is_read(L):
                dict(kept=0x1004), dict(kept=0x2000), dict(kept=0x3000 - 4 * 8 * 8 * 4 + 4), dict(new=0x4000), dict(kept=0x500C),
                dict(new=0x4000 + 4 * 8 * 8 * 4 - 4)):
         assert call(L, "kmr_kv4_evict", cache(), **{**at, **kw}) == kmr.KMR_ERR_INVALID_ARG, kw
+
+
+CALLS = {
+    "kmr_kv4_append": ("qkv positions slot_ids cache_position n_tokens q_norm k_norm q_out mass",
+                       lambda c, a: kmr.kmr_kv4_append(c, a["qkv"], a["positions"], a["slot_ids"], a["cache_position"], a["n_tokens"],
+                                                       0, 3, 6, a["q_norm"], a["k_norm"], 1e-6, 1e6, (8, 12, 12), a["q_out"], a["mass"])),
+    "kmr_kv4_from_bf16": ("k_bf16 v_bf16 bf16_slot_ids bf16_start slot_ids start lengths",
+                          lambda c, a: kmr.kmr_kv4_from_bf16(c, a["k_bf16"], a["v_bf16"], 4, 20, a["bf16_slot_ids"], a["bf16_start"],
+                                                             a["slot_ids"], a["start"], a["lengths"], 0, 5)),
+    "kmr_kv4_to_bf16": ("k_bf16 v_bf16 bf16_slot_ids bf16_start slot_ids start lengths",
+                        lambda c, a: kmr.kmr_kv4_to_bf16(c, a["k_bf16"], a["v_bf16"], 4, 20, a["bf16_slot_ids"], a["bf16_start"],
+                                                         a["slot_ids"], a["start"], a["lengths"], 0, 5)),
+    "kmr_decode_attn_kv4": ("q slot_ids cache_position mass out",
+                            lambda c, a: kmr.kmr_decode_attn_kv4(c, a["q"], a["slot_ids"], a["cache_position"], 0, 6, 0.1, a["mass"],
+                                                                 a["out"], 16, 16)),
+    "kmr_kv4_evict": ("src_slot_ids dst_slot_ids lengths mass dst_mass kept new_lengths",
+                      lambda c, a: kmr.kmr_kv4_evict(c, c, a["src_slot_ids"], a["dst_slot_ids"], a["lengths"], 0, 7, 2, a["mass"],
+                                                     a["dst_mass"], a["kept"], a["new_lengths"])),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_binding_checks_the_types(L, name):
+    """A tensor of another type (an int64 index, a bf16 query) or with gaps is refused by name; the right types go through
+    to the library, which refuses the call for its batch of 0 before it looks at anything else."""
+    torch = pytest.importorskip("torch")
+    names, run = CALLS[name]
+    cache_on = kmr.Kv4Cache.zeros(4, 3, 32, 64, 32, device="cpu")
+    names = names.split()
+    kinds = {k: torch.float32 if k in ("qkv", "q_out", "mass", "dst_mass", "q", "out") else
+             torch.bfloat16 if k in ("q_norm", "k_norm", "k_bf16", "v_bf16") else torch.int32 for k in names}
+    # (a tensor of its own for each: the library compares the addresses)
+    good = {k: torch.zeros(64, dtype=kinds[k]) for k in names}
+    others = {torch.float32: (torch.bfloat16, torch.float64, torch.int32), torch.int32: (torch.int64, torch.int16, torch.float32),
+              torch.bfloat16: (torch.float16, torch.float32)}
+    for key in names:
+        for t in others[kinds[key]]:
+            with pytest.raises(ValueError, match=key + " is torch"):
+                run(cache_on, {**good, key: torch.zeros(64, dtype=t)})
+        with pytest.raises(ValueError, match=key + " must be contiguous"):
+            run(cache_on, {**good, key: torch.zeros(128, dtype=kinds[key])[::2]})
+        with pytest.raises(TypeError, match=key):
+            run(cache_on, {**good, key: "text"})
+    for key in names:
+        if kinds[key] == torch.bfloat16:                        # also as its bits
+            good[key] = good[key].view(torch.int16)
+    with pytest.raises(kmr.KmrError) as e:
+        run(cache_on, good)
+    assert e.value.code == kmr.KMR_ERR_BATCH
