@@ -281,9 +281,11 @@ int kmr_kv4_append(const kmr_kv4_cache* cache, const float* qkv, const int32_t* 
  * lengths[b] positions (0..max_tokens) from bf16_start[b] of bf16 row bf16_slot_ids[b] and from start[b]
  * of 4-bit row slot_ids[b]; all five arrays are device int32 [B].  kmr_kv4_to_bf16 writes
  * bf16(c * s + z); positions outside the spans keep their contents; where two spans write the same position,
- * the later span's values stay.  Errors: KMR_ERR_INVALID_ARG (pointers, max_tokens outside 1..2^28), KMR_ERR_SHAPE,
- * KMR_ERR_BATCH; on the device KMR_ERR_INVALID_ARG (length), KMR_ERR_SLOT_RANGE, KMR_ERR_CACHE_FULL (a span
- * that leaves either row). */
+ * the later span's values stay.  Neither call touches a mass: a slot that is filled anew from a bf16 cache still has the
+ * mass of the sequence before it, by which kmr_kv4_evict would rank the new positions, so the caller sets the slot's
+ * mass to 0 (kmr_kv4_append does so for what it writes).  Errors: KMR_ERR_INVALID_ARG (pointers, max_tokens outside 1..2^28),
+ * KMR_ERR_SHAPE, KMR_ERR_BATCH; on the device KMR_ERR_INVALID_ARG (length), KMR_ERR_SLOT_RANGE, KMR_ERR_CACHE_FULL (a
+ * span that leaves either row). */
 int kmr_kv4_from_bf16(const kmr_kv4_cache* cache, const uint16_t* k_bf16, const uint16_t* v_bf16, int bf16_slots,
                       int bf16_max_len, const int32_t* bf16_slot_ids, const int32_t* bf16_start,
                       const int32_t* slot_ids, const int32_t* start, const int32_t* lengths, int B, int max_tokens,

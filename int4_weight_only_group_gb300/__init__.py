@@ -341,7 +341,8 @@ def kmr_kv4_append(cache, qkv, positions, slot_ids, cache_position, n_tokens, B,
 
 def kmr_kv4_from_bf16(cache, k_bf16, v_bf16, bf16_slots, bf16_max_len, bf16_slot_ids, bf16_start, slot_ids, start,
                       lengths, B, max_tokens, stream=None) -> None:
-    """Spans of a bf16 cache into the 4-bit cache (see include/kmr.h)."""
+    """Spans of a bf16 cache into the 4-bit cache; the mass of a slot that was in use is the caller's to clear (see
+    include/kmr.h)."""
     _check(lib().kmr_kv4_from_bf16(cache, _dev(k_bf16, _BF16, "k_bf16"), _dev(v_bf16, _BF16, "v_bf16"), bf16_slots, bf16_max_len,
                                    _dev(bf16_slot_ids, _I32, "bf16_slot_ids"), _dev(bf16_start, _I32, "bf16_start"),
                                    _dev(slot_ids, _I32, "slot_ids"), _dev(start, _I32, "start"), _dev(lengths, _I32, "lengths"),

@@ -1190,3 +1190,38 @@ def test_key_groups_of_different_scale(torch, d, g, nq, nkv, S):
         out = attend(torch, c.dev, q, [0], [L - 1])
         ref, _ = kv4.attention(q[0], kv4.dequantize(codes, sb, zb)[0, :, :L], c.val["v"][0, :, :L], 1 / math.sqrt(d))
         assert group_errors(out[0], ref, g).max() <= GROUP_TOL, sizes
+
+
+@pytest.mark.parametrize("S", [256, 4112])
+def test_a_used_slot_filled_anew(torch, S):
+    """A slot serves one sequence, then another that is converted into it: with its mass set to 0, as the conversion asks
+    for, eviction ranks the new positions by their own weights only; the conversion itself leaves the mass alone."""
+    r = np.random.default_rng(S + 7)
+    slots, nkv, d, g, nq, L, keep, recent = 3, 2, 64, 32, 4, 200, 40, 5
+    cache = kmr.Kv4Cache.zeros(slots, nkv, S, d, g)
+    mass = torch.zeros((slots, nkv, S), device="cuda")
+    ids, zero, st = i32(torch, [1]), i32(torch, [0]), torch.cuda.current_stream()
+    for turn in range(2):
+        bits = [kv4.bf16_bits(r.standard_normal((1, nkv, L, d)).astype(np.float32)) for _ in range(2)]
+        dev16 = [torch.from_numpy(b.view(np.int16)).cuda() for b in bits]
+        if turn:
+            left = mass.clone()
+            kmr.kmr_kv4_from_bf16(cache, *dev16, 1, L, zero, zero, ids, zero, i32(torch, [L]), 1, L, st)
+            assert torch.equal(mass, left) and mass[1, :, :L].min().item() > 0
+            mass.index_fill_(0, ids.long(), 0.0)
+        else:
+            kmr.kmr_kv4_from_bf16(cache, *dev16, 1, L, zero, zero, ids, zero, i32(torch, [L]), 1, L, st)
+        vals = [kv4.dequantize(*kv4.quantize(kv4.bf16_value(b[0]), g)) for b in bits]
+        total = np.zeros((nkv, L))
+        for _ in range(3):
+            q = r.standard_normal((1, nq, d)).astype(np.float32) * 2
+            attend(torch, cache, q, [1], [L - 1], mass)
+            total += kv4.attention(q[0], vals[0], vals[1], 1 / math.sqrt(d))[1]
+        assert kmr.kmr_last_device_error() == 0
+        got = mass[1, :, :L].cpu().numpy()
+        assert np.allclose(got, total, rtol=4 * ATTN_TOL, atol=1e-30)
+        dst = kmr.Kv4Cache.zeros(1, nkv, 48, d, g)
+        kept, new = evict(torch, cache, dst, [1], [0], [L], keep, recent, mass, None)
+        assert kmr.kmr_last_device_error() == 0
+        for h in range(nkv):
+            assert kept[0, h].tolist() == kv4.evict_positions(got[h], L, keep, recent)
