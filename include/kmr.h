@@ -334,8 +334,9 @@ int kmr_decode_attn_kv4(const kmr_kv4_cache* cache, const float* q, const int32_
  * in place goes through another array.  Positions of the destination row past new_lengths[b] keep their contents.  Two caches of a call are the
  * same cache or share no memory.  Errors: KMR_ERR_INVALID_ARG, KMR_ERR_SHAPE, KMR_ERR_BATCH,
  * KMR_ERR_CACHE_FULL (keep > dst's max_len); on the device a row is refused (kept -1, new_lengths 0, nothing
- * moved) where a slot is out of range or the destination is another row's destination or, in the same
- * cache, any row's source (KMR_ERR_SLOT_RANGE), or its length is outside [0, max_len] (KMR_ERR_CACHE_FULL). */
+ * moved) where a slot is out of range (KMR_ERR_SLOT_RANGE), its length is outside [0, max_len] (KMR_ERR_CACHE_FULL), or its
+ * destination is the destination or, in the same cache, the source of a row that is not refused for one of these
+ * (KMR_ERR_SLOT_RANGE). */
 int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst, const int32_t* src_slot_ids,
                   const int32_t* dst_slot_ids, const int32_t* lengths, int B, int keep, int recent,
                   const float* mass, float* dst_mass, int32_t* kept, int32_t* new_lengths, void* stream);

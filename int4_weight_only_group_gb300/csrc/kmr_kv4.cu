@@ -485,19 +485,25 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Whether the row may be evicted: KMR_OK or the error.  Uniform over the CTA.
-__device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
+// KMR_OK or why a row of some length is refused for itself.
+__device__ __forceinline__ int evict_own_error(const Kv4EvictParams& p, int b) {
     const int src = p.src_ids[b], dst = p.dst_ids[b], n = p.lengths[b];
-    if (n == 0) return KMR_OK;                       // an idle row: nothing moves
+    if (src < 0 || src >= p.src.slots || dst < 0 || dst >= p.dst.slots) return KMR_ERR_SLOT_RANGE;
+    return n < 0 || n > p.src.S ? KMR_ERR_CACHE_FULL : KMR_OK;
+}
+// Whether the row may be evicted: KMR_OK or the error.  A row that is refused for itself moves nothing, so it stands in no
+// other's way.  Uniform over the CTA.
+__device__ __forceinline__ int evict_row_error(const Kv4EvictParams& p, int b) {
+    if (p.lengths[b] == 0) return KMR_OK;            // an idle row: nothing moves
+    const int own = evict_own_error(p, b), dst = p.dst_ids[b];
     int clash = 0;
     for (int r = threadIdx.x; r < p.B; r += blockDim.x) {
-        if (p.lengths[r] == 0) continue;
+        if (p.lengths[r] == 0 || evict_own_error(p, r) != KMR_OK) continue;
         clash |= r != b && p.dst_ids[r] == dst;
         clash |= p.same && p.src_ids[r] == dst;
     }
     clash = __syncthreads_or(clash);
-    if (src < 0 || src >= p.src.slots || dst < 0 || dst >= p.dst.slots || clash) return KMR_ERR_SLOT_RANGE;
-    return (n < 0 || n > p.src.S) ? KMR_ERR_CACHE_FULL : KMR_OK;
+    return own != KMR_OK ? own : (clash ? KMR_ERR_SLOT_RANGE : KMR_OK);
 }
 
 // Positions kept of one (row, head): the newest `recent`, and of the older ones the heaviest, the

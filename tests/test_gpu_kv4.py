@@ -1225,3 +1225,26 @@ def test_a_used_slot_filled_anew(torch, S):
         assert kmr.kmr_last_device_error() == 0
         for h in range(nkv):
             assert kept[0, h].tolist() == kv4.evict_positions(got[h], L, keep, recent)
+
+
+def test_evict_refused_rows_stand_in_no_way(torch):
+    """Rows refused for their own slots or length name a good row's destination and, as sources, another's: both move."""
+    r = np.random.default_rng(95)
+    slots, nkv, S, d, g, keep = 8, 2, 64, 64, 32, 10
+    c = Cache(torch, r, slots, nkv, S, d, g)
+    before = c.host()
+    m = r.random((slots, nkv, S)).astype(np.float32)
+    big = 2 ** 31 - 1
+    #      good  good   length  length  slot     slot    source of a refused row is a good row's destination
+    ids, dids, n = [0, 1, 2, 3, 8, -1, 7, 6], [7, 6, 7, 6, 7, 6, 2, big], [40, 5, 65, -1, 20, 20, 65, 20]
+    kept, new = evict(torch, c.dev, c.dev, ids, dids, n, keep, 3, torch.from_numpy(m.copy()).cuda(), None)
+    assert kmr.kmr_last_device_error() in (kmr.KMR_ERR_SLOT_RANGE, kmr.KMR_ERR_CACHE_FULL)
+    assert new.tolist() == [keep, 5, 0, 0, 0, 0, 0, 0] and (kept[2:] == -1).all()
+    got = c.host()
+    for a, w in zip(got, before):
+        assert np.array_equal(a[:6], w[:6])
+        for src, dst, k, b in ((0, 7, keep, 0), (1, 6, 5, 1)):
+            for h in range(nkv):
+                want = kv4.evict_positions(m[src, h], n[b], keep, 3)
+                assert kept[b, h, :k].tolist() == want
+                assert np.array_equal(a[dst, h, :k], w[src, h, want]) and np.array_equal(a[dst, h, k:], w[dst, h, k:])
