@@ -171,13 +171,16 @@ __device__ __forceinline__ int column_half(int g) { return PAIR ? g >> 2 : 0; }
 // has to stay below 2^15 (fp16); its two parts hold 22 bits of it from 2^-2 on, and 2^-24 below.
 //   * The scaling goes by the largest scale seen, brought to [2^kTop, 2^(kTop + 1)): weights are at most 2^kLag, so scales up
 //     to twice as large (limit_of) need no look at the weights.
-//   * Where that leaves the tiles' largest product below 2^-3, because the large scale has no weight, the scaling goes by
-//     the product, brought to [2^7, 2^8).  Tiles with a scale that may be too large are then looked at each.
+//   * Where that leaves the tiles' largest product below kEnough (what a long row's products lose below 2^-24 would begin to
+//     show), because the large scale has no weight, the scaling goes by the product, brought to [2^7, 2^8).  Tiles with a
+//     scale that may be too large are then looked at each (16 rows of 8192 whose V scales differ by up to 2^20 from
+//     position to position: 48.8 -> 52.6 us).
 //   * As the reference rises by `oct` whole octaves, what was added before falls by as much, and the scaling may rise by it.
 // One scaling for all groups, as it was, kept 22 bits of the largest group only: beside one 10^4 (10^6) times larger
 // a group was off by 3e-4 (2e-2).  This costs 0 to 2% (16 rows of 8192, group 32: 47.7 -> 48.7 us, 8 query heads a KV head 48.5 ->
 // 48.7; one row of 131072, group 128: 38.5 -> 39.4); checking the products themselves in every tile cost 4 to 9%.
 constexpr int kLag = 8, kTop = 13 - kLag;
+constexpr float kEnough = 2.f;
 __device__ __forceinline__ int unit_exponent(float u) { return int(__float_as_uint(u) >> 23); }
 // The scaling that brings x to [2^top, 2^(top + 1)).
 __device__ __forceinline__ float unit_for(float x, int top) {
@@ -187,10 +190,12 @@ __device__ __forceinline__ float fit_unit(float was, float smax, float pmax, flo
     const float by_scale = unit_for(smax, kTop);
     // (at most 2^126 / smax: a weight of 0 times an infinity would be no number)
     const float cap = by_scale < 0x1p10f ? by_scale * 0x1p116f : 0x1p126f, by_product = fminf(unit_for(pmax, 7), cap);
-    const bool enough = pmax * by_scale >= 0x1p-3f || pmax == 0.f;
-    if (first) return enough ? by_scale : by_product;
-    if (smax * was >= float(1 << (kTop + 2))) return enough ? by_scale : (pmax * was >= 0x1p15f ? by_product : fminf(was, cap));
-    return pmax * was < 0x1p-3f ? fmaxf(was, fminf(by_scale, was * exp2f(oct))) : was;
+    const bool enough = pmax * by_scale >= kEnough || pmax == 0.f;
+    const float target = enough ? by_scale : by_product;
+    if (first || (enough && smax * was >= float(1 << (kTop + 2)))) return target;
+    if (pmax * was >= 0x1p15f) return by_product;
+    was = fminf(was, cap);
+    return pmax * was < kEnough ? fmaxf(was, fminf(target, was * exp2f(oct))) : was;
 }
 // Scales from here on (as bits) may be too large for a scaling: 2^(kTop + 2) / it.
 __device__ __forceinline__ uint32_t limit_of(float u) { return uint32_t(min(256 + kTop - unit_exponent(u), 255)) << 23; }
@@ -548,7 +553,7 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
                         over |= mn[n] != m[n];
                     }
                     if (st == 0) {
-                        // where every scale is more than 2^-8 of its group's largest, so is that of each head's best position, whose
+                        // where every scale is 2^-4 of its group's largest or more, so is that of each head's best position, whose
                         // weight is 1: the scaling goes by the scales
                         float by_scale[NG];
 #pragma unroll
@@ -570,7 +575,7 @@ __global__ void __launch_bounds__(kThr, Share<D, HC>::kCtas) kv4_split_kernel(co
 #pragma unroll
                             for (int i = 0; i < kLook; ++i)
                                 over |= (whole || base0 + u * (16 * kTileWarps) + look_row < t1) &&
-                                        (mine[i] & 0x7FFFFFFFu) + (uint32_t(kTop + 5) << 23) < limit[i];
+                                        (mine[i] & 0x7FFFFFFFu) + (uint32_t(kTop + 1) << 23) < limit[i];
                         }
                     }
                     if (__builtin_expect(__any_sync(0xffffffffu, over), 0)) {

@@ -1248,3 +1248,69 @@ def test_evict_refused_rows_stand_in_no_way(torch):
                 want = kv4.evict_positions(m[src, h], n[b], keep, 3)
                 assert kept[b, h, :k].tolist() == want
                 assert np.array_equal(a[dst, h, :k], w[src, h, want]) and np.array_equal(a[dst, h, k:], w[dst, h, k:])
+
+
+@pytest.mark.parametrize("d,g,nq", [(128, 32, 2), (128, 32, 4), (128, 32, 8), (128, 64, 1), (128, 128, 6), (64, 64, 8), (64, 32, 3)])
+@pytest.mark.parametrize("S", [512, 1104, 4112])
+def test_scores_that_step_up_beside_large_values_of_no_weight(torch, d, g, nq, S):
+    """Two steps of 40 octaves in the scores where V falls by 2^30, and in every 16 positions one of no weight whose V is 2^40: what
+    counts is small beside what the row held before and beside what it holds now."""
+    r = np.random.default_rng(d + g + nq + S + 4)
+    L = S - 5
+    octaves = np.floor(np.arange(S) * 3 / S) * 40.0
+    out_of = np.arange(S) % 16 == 5
+    octaves[out_of] = -120.0
+    # one dim carries the score, as a code of 0 or 15 under an exact scale
+    kx = np.zeros((1, 1, S, d), np.float32)
+    kx[0, 0, :, 3] = np.sign(octaves) * kv4.bf16_value(kv4.bf16_bits((np.abs(octaves) / 15).astype(np.float32))) * 15
+    q = np.zeros((1, nq, d), np.float32)
+    q[0, :, 3] = math.log(2) * math.sqrt(d)
+    vx = r.standard_normal((1, 1, S, d)).astype(np.float32)
+    vx[0, 0] *= np.exp2(np.where(out_of, 40, -30 * np.floor(np.arange(S) * 3 / S))).astype(np.float32)[:, None]
+    c = Cache(torch, r, 1, 1, S, d, g, [L])
+    codes, sb, zb = kv4.quantize(kx, g)
+    c.dev.tensors[0].copy_(torch.from_numpy(kv4.pack_rows(codes, True)))
+    c.dev.tensors[2].copy_(torch.from_numpy(kv4.pack_words(sb, zb)))
+    K, V = kv4.dequantize(codes, sb, zb), set_values(torch, c, vx, g)
+    out = attend(torch, c.dev, q, [0], [L - 1])
+    ref, _ = kv4.attention(q[0], K[0, :, :L], V[0, :, :L], 1 / math.sqrt(d))
+    # scores of 80 octaves, rounded three times; outputs of positions that count alike
+    assert group_errors(out[0], ref, g).max() <= GROUP_TOL + 4 * 2.0 ** -24 * 80 * math.log(2)
+
+
+@pytest.mark.parametrize("seed", range(40))
+def test_attention_of_wild_scales(torch, seed):
+    """Random shapes; V scales that differ by up to 2^60 between positions, groups or both, rows and groups of zeros or
+    constants among them; scores of up to 100 octaves."""
+    r = np.random.default_rng(seed + 1000)
+    d = int(r.choice([64, 128]))
+    g = int(r.choice([x for x in (32, 64, 128) if x <= d]))
+    nkv, rep, S = int(r.choice([1, 2])), int(r.integers(1, 9)), int(r.choice([64, 208, 512, 1104, 2064, 4112]))
+    L, ng, nq = int(r.integers(S // 2, S + 1)), d // g, nkv * rep
+    c = Cache(torch, r, 1, nkv, S, d, g, [L])
+    e = np.zeros((1, nkv, S, ng))
+    if seed % 4 in (1, 3):
+        e = e + r.uniform(-30, 30, (1, 1, 1, ng))
+    if seed % 4 in (2, 3):
+        e = e + r.uniform(-30, 30, (1, nkv, S, 1 if seed % 8 < 4 else ng))
+    x = (r.standard_normal((1, nkv, S, d)) * np.exp2(np.repeat(e, g, -1))).astype(np.float32)
+    if seed % 3 == 0:
+        x[r.random((1, nkv, S)) < 0.5] = 0
+    if seed % 5 == 0:
+        x = np.where(np.repeat(r.random((1, nkv, S, ng)) < 0.3, g, -1), np.float32(1.5), x)
+    V = set_values(torch, c, x, g)[0, :, :L]
+    q = (r.standard_normal((1, nq, d)) * r.choice([0.1, 1, 3, 10])).astype(np.float32)
+    out = attend(torch, c.dev, q, [0], [L - 1])[0]
+    K = c.val["k"][0, :, :L]
+    ref, _ = kv4.attention(q[0], K, V, 1 / math.sqrt(d))
+    assert np.isfinite(out).all()
+    for i in range(nq):
+        h = i // rep
+        # a score is a sum of codes (not centred: up to 15 s beside the base, so twice the group's largest |k|) times the query,
+        # off by some 3 * 2^-22 of the terms' size; a weight by as much of itself; the values' parts and sums by 3e-6
+        big = np.abs(K[h]).reshape(L, ng, g).max(-1).repeat(g, -1) * 2
+        off = 3e-6 + 3 * 2.0 ** -22 * (big @ np.abs(q[0, i].astype(np.float64))).max() / math.sqrt(d) / math.log(2)
+        a = K[h] @ q[0, i].astype(np.float64) / math.sqrt(d)
+        p = np.exp(a - a.max())
+        size = (p / p.sum()) @ np.abs(V[h]).reshape(L, ng, g).max(-1)
+        assert (np.abs(out[i] - ref[i]) <= off * np.repeat(size, g) + 1e-37).all(), (i, d, g, rep, S, L)
