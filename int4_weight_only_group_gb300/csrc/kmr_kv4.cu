@@ -2,11 +2,11 @@
 // conversions from and to a bf16 cache, and eviction into another row.  The format is in kmr_kv4.cuh.
 //
 // All are bound by HBM where there is enough to move; measured at d = 128, group 32, 8 KV heads, against the measured
-// copy rate of 6.67 TB/s:
-//   append, a prompt of 8192 (16 query heads): 36.8 us for 212 MB, 5.8 TB/s (0.87); one token: 3.1 us, most of it launch
-//   bf16 -> 4 bits, 16 rows of up to 8192 (96 thousand positions): 89 us for 515 MB, 5.8 TB/s (0.87)
-//   4 bits -> bf16, the same: 82 us, 6.3 TB/s (0.94)
-//   evict, 16 rows of up to 8192 to 2048: 28 us for 90 MB (3.2 TB/s, 0.48); the selection alone (2 kept) takes 10 us
+// copy rate of 6.75 TB/s:
+//   append, a prompt of 8192 (16 query heads): 37.7 us for 212 MB, 5.6 TB/s (0.83); one token: 3.2 us, most of it launch
+//   bf16 -> 4 bits, 16 rows of up to 8192 (96 thousand positions): 86.6 us for 516 MB, 6.0 TB/s (0.88)
+//   4 bits -> bf16, the same: 82.1 us, 6.3 TB/s (0.93)
+//   evict, 16 rows of up to 8192 to 2048: 29.2 us for 90 MB (3.1 TB/s, 0.46); the selection alone (2 kept) takes 10.7 us
 #include <type_traits>
 
 #include "kmr_kv4.cuh"

@@ -17,7 +17,7 @@ constexpr int kKv4MaxRows = 1024;        // rows of one call (each row looks at 
 constexpr int kKv4MaxHeads = 1024;       // KV heads
 constexpr int kKv4MaxLen = 1 << 28;      // positions of a row
 constexpr int kKv4MaxRep = 8;            // query heads per KV head
-constexpr int kKv4MaxSplits = 76;        // of a row: with 8 KV heads, four CTAs for each of 152 SMs
+constexpr int kKv4MaxSplits = 76;        // of a row: with 8 KV heads, four CTAs for each of 152 SMs (fewer heads fill fewer)
 constexpr int kKv4ClusterSplits = 8;     // of a row of a short cache: one cluster
 constexpr int kKv4ClusterLen = 2048;     // longest max_len of a short cache (measured: kmr_kv4_attn.cu)
 constexpr int kKv4MinChunk = 128;        // positions per split, at least

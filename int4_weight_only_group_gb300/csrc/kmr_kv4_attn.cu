@@ -9,13 +9,14 @@
 //     first one's cluster takes all in turn, so that the mass gains them in row order.
 //   * longer caches: up to 76 splits leave their states in the workspace (and, for the mass, every score); a
 //     second launch, a programmatic dependent of the first, merges and adds, again in row order.
-// One launch against two, 16/8 heads of 128, us: 5.0 / 5.6 (1 row of 1024), 5.4 / 7.9 (4 rows), 6.1 / 6.0 and 6.6 / 8.6 at
-// 2048, 8.4 / 7.2 and 9.5 / 11.0 at 4096, where eight CTAs a head begin to be too few.
+// One launch against two, 16/8 heads of 128, us: 5.6 / 5.6 (1 row of 1024), 6.0 / 8.1 (4 rows), 6.8 / 6.0 and 7.7 / 8.9 at
+// 2048, 9.7 / 7.2 and 11.1 / 11.1 at 4096, where eight CTAs a head begin to be too few.
 //
 // The bound is HBM: 2 (d/2 + 4 d/g) bytes per position and KV head.  At d = 128, g = 32 an SM's share
 // of the bandwidth is about 36 codes per cycle, too many for dequantising and multiplying on the CUDA
-// cores, so both products run on the tensor cores (mma m16n8k16: at most 8 query heads leave a 128-row
-// tcgen05 tile 15/16 empty) with the codes as the A operand:
+// cores, so both products run on the tensor cores, with the codes as the A operand.  mma m16n8k16 takes them from the
+// registers in which a warp has unpacked them; a tcgen05 tile (128 positions as its rows, the heads' columns as N = 16)
+// would be full as well, but wants the unpacked codes in shared or tensor memory first.  It has not been tried.
 //   * a nibble c under the exponent of 1024 is the fp16 1024 + c (from bits 4..7: 1024 + 16 c); one packed fp16
 //     operation takes the offset off again, exactly.  (As a bare subnormal c 2^-24 it would cost one operation
 //     less, but a subnormal code was found to lose up to 10 of the accumulator's bits: outputs of a row of 8191
@@ -34,14 +35,15 @@
 // stand for the halves of the head's dims: column 4 f + 2 h + part is query head h in half f.  A step of the scores
 // has 8 dims of either half (each half's columns are zero against the other's dims), a tile of the output 8
 // dims of either half in its upper and lower rows.  The products are as many, but each lane folds, weighs and
-// splits for its half's groups only: 413 instructions per tile of 16 positions at d = 128, g = 32 instead of 481 (385 with two
-// tiles taken together).
+// splits for its half's groups only: 413 instructions per tile of 16 positions at d = 128, g = 32 instead of 481 (one tile
+// at a time; 392 now, two together).
 //
-// Measured, 16/8 heads of 128: 16 rows of 8192, group 32, 47.4 us (168 MB: 3.5 TB/s, 0.53 of the measured copy rate); one
-// row of 131072, 43.2 us (0.58), group 128, 38.6 us (143 MB, 0.55).  What bounds it now is the arithmetic: with the
-// tiles' work left out the same copies take 34 us, with every row in L2 the whole kernel 44.  The ALU pipe is busy 55% of
-// the time, no pipe more; leaving the V codes' unpacking out gains 6 us, the K codes' 3, the weights' splitting 1.4, the
-// products nothing.  Five CTAs an SM (96 registers) or three (a third stage) instead of four measure the same or worse.
+// Measured, 16/8 heads of 128: 16 rows of 8192, group 32, 48.8 us (168 MB: 3.4 TB/s, 0.51 of the measured copy rate of 6.75); one
+// row of 131072, 43.0 us (0.58), group 128, 39.2 us (143 MB, 0.54).  With the tiles' work left out the copies alone take 32 us
+// for the long row (34 for 16 rows), with every row in L2 the 16 rows take 45.  No pipe is saturated (ALU 50% of the time, FMA
+// 37%, tensor 21%): leaving the V codes' unpacking out gains 5.8 us of the long row's, the weights' splitting 1.3, the
+// bases' sum and the shuffles 0.9 each, the K codes' unpacking 0.6, the products nothing.  Registers are at the 128 that
+// four CTAs an SM allow; heads of 128 in groups of 32 with 3 or more query heads a KV head spill 12 to 80 bytes.
 #include <cooperative_groups.h>
 #include <cuda_fp16.h>
 #include <math.h>
@@ -127,10 +129,11 @@ __device__ __forceinline__ void lds_words(const void* p, uint32_t (&w)[N]) {
 }
 
 // How a CTA's four warps share the work.  Two tiles of 16 positions a warp at a time give two chains of products to
-// interleave (one row of 8192: 9.1 -> 8.0 us; 16 rows 53.4 -> 47.4).  Up to 4 query heads a KV head fill one n-tile.  5 to 8
+// interleave (when taken, one row of 8192: 9.1 -> 8.0 us; 16 rows 53.4 -> 47.4).  Up to 4 query heads a KV head fill one n-tile.  5 to 8
 // need two: with heads of 64 every warp keeps both; with heads of 128 that takes 240 registers and two CTAs an SM, so
 // warps 0, 1 have the first four heads and warps 2, 3 the others, over the same stage, and unpack it twice (16 rows of
-// 8192, group 32: 8 heads on each of 4 KV heads 55.9 -> 48.6 us, 6 on each of 8 101 -> 87; one row of 4096 9.5 -> 10.3).
+// 8192, group 32, when taken: 8 heads on each of 4 KV heads 55.9 -> 48.6 us, 6 on each of 8 101 -> 87; one row of 4096 9.5 -> 10.3;
+// now 49.6 and 89).
 enum HeadClass { HEADS_2 = 0, HEADS_4 = 1, HEADS_8 = 2 };
 template <int D, int HC>
 struct Share {
@@ -1068,8 +1071,8 @@ cudaError_t launch_kv4_attn(const Kv4AttnParams& p, cudaStream_t st) {
         kv4_cluster_plan(p.c.S, chunk, splits);
         while (ranks < splits) ranks *= 2;
         // CTAs that run at a time: more than that only queue, and pay their start and end each, so then a CTA takes
-        // several splits of its row, one after the other, which changes no result (16 rows of 1024: 13.2 -> 10.3 us; the
-        // longer caches' splits of 256 gained nothing by it, 47.4 against 48.2 us for 16 rows of 8192)
+        // several splits of its row, one after the other, which changes no result (16 rows of 1024, when taken: 13.2 -> 10.3
+        // us, 10.9 now; the longer caches' splits of 256 gained nothing by it, 47.4 against 48.2 us for 16 rows of 8192)
         const long long slots = (long long)split_variant(p.c.d, p.c.g, rep, 1, 0).ctas * num_sms();
         const long long rows = (long long)p.c.nkv * p.B;
         while (ranks > 1 && ranks * rows > slots) ranks /= 2;
