@@ -257,7 +257,7 @@ typedef struct kmr_kv4_cache {
  * written out for kmr_decode_attn_kv4.  One launch.
  *   qkv        device fp32 [B, T, (n_q + 2 n_kv) d]: raw projection rows [q heads; k heads; v heads]
  *   positions  device int32 [3, B, T]: (T, H, W) ids, any int32; an angle is off by |id| 2^-65 turns, its cosine and sine
- *              by 0.7 ulp (below 2^-28 turns by 2^-23 of themselves)
+ *              by 0.7 ulp (a sine of less than 2^-28 turns by 2^-22 of itself)
  *   slot_ids, cache_position  device int32 [B]: token t of row b goes to position
  *              cache_position[b] + t of slot slot_ids[b]
  *   n_tokens   device int32 [B], 0..T: tokens of row b, the rest is padding: not read, q_out left as it

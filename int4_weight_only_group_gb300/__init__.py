@@ -198,6 +198,8 @@ def _dev_refused(a, kind, name):
         _I32.add(torch.int32)
         _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
         return _dev(a, kind, name)
+    if isinstance(a, int):
+        return int(a)
     if not isinstance(a, torch.Tensor):
         raise TypeError(f"cannot pass {type(a).__name__} as {name}")
     if a.dtype not in kind:

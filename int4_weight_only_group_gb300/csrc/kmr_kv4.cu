@@ -253,17 +253,19 @@ __device__ __forceinline__ int convert_row_error(const Kv4ConvertParams& p, int 
 }
 
 // ------------------------------------------------------------------ new tokens
-// Cosine and sine of an angle of turn / 2^64 turns, to 0.7 ulp (below 2^-28 turns 2^-23 of themselves): the nearest quarter
+// Cosine and sine of an angle of turn / 2^64 turns, to 0.7 ulp (a sine below 2^-28 turns to 2^-22 of itself): the nearest quarter
 // turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, and the Taylor series' later terms
 // (at most a tenth of the sum) are added to the leading ones at the end, the roundings of which are kept.
 __device__ __forceinline__ void cos_sin_turn(unsigned long long turn, float& c, float& s) {
-    const uint32_t high = uint32_t(turn >> 32), low = uint32_t(turn);
+    // the nearest 2^-32 turns and what is left, of either sign: a small negative angle is no difference of large parts
+    const int low = int(uint32_t(turn));
+    const uint32_t high = uint32_t(turn >> 32) + (uint32_t(low) >> 31);
     const int quarter = int((high + (1u << 29)) >> 30);
     const int rem = int(high - (uint32_t(quarter) << 30));                // [-2^29, 2^29), and low / 2^32
     constexpr double kUnit = 6.283185307179586477 / 4294967296.0;
     const float uh = float(kUnit), ul = float(kUnit - double(uh));
     const float rh = __int2float_rn(rem);
-    const float rl = __fmaf_rn(__uint2float_rn(low), 0x1p-32f, __int2float_rn(rem - __float2int_rn(rh)));
+    const float rl = __fmaf_rn(__int2float_rn(low), 0x1p-32f, __int2float_rn(rem - __float2int_rn(rh)));
     const float th = __fmul_rn(rh, uh);
     const float tl = __fmaf_rn(rl, uh, __fmaf_rn(rh, ul, __fmaf_rn(rh, uh, -th)));
     const float u = __fmul_rn(th, th);
