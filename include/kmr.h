@@ -257,7 +257,7 @@ typedef struct kmr_kv4_cache {
  * written out for kmr_decode_attn_kv4.  One launch.
  *   qkv        device fp32 [B, T, (n_q + 2 n_kv) d]: raw projection rows [q heads; k heads; v heads]
  *   positions  device int32 [3, B, T]: (T, H, W) ids, any int32; an angle is off by |id| 2^-65 turns, its cosine and sine
- *              by 0.7 ulp (a sine of less than 2^-28 turns by 2^-22 of itself)
+ *              by 0.53 ulp (a sine of less than 2^-28 turns by 2^-22 of itself)
  *   slot_ids, cache_position  device int32 [B]: token t of row b goes to position
  *              cache_position[b] + t of slot slot_ids[b]
  *   n_tokens   device int32 [B], 0..T: tokens of row b, the rest is padding: not read, q_out left as it
@@ -304,7 +304,8 @@ int kmr_kv4_to_bf16(const kmr_kv4_cache* cache, uint16_t* k_bf16, uint16_t* v_bf
  *   mass  device fp32 [slots][n_kv][max_len], 16-byte aligned, or NULL: position p of a row's slot gains the sum
  *         of p's softmax weights over the KV head's query heads (what kmr_kv4_evict ranks positions by).  Rows
  *         that share a slot add in row order: the result does not change from run to run.
- *   out   device fp32 [B, n_q, d], 16-byte aligned
+ *   out   device fp32 [B, n_q, d], 16-byte aligned: every group of every head to single precision, whatever the others hold
+ *         (weighted values are summed before they are divided: beyond some 1e34 over the row's length they overflow)
  *   workspace  device memory, 16-byte aligned, kmr_decode_attn_kv4_workspace_size(cache, B, n_q, mass != NULL)
  *         bytes or more (0 for arguments that the call would refuse); no initialisation.  Calls that may
  *         overlap on the device need workspaces of their own.

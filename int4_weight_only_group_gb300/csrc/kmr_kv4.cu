@@ -253,9 +253,9 @@ __device__ __forceinline__ int convert_row_error(const Kv4ConvertParams& p, int 
 }
 
 // ------------------------------------------------------------------ new tokens
-// Cosine and sine of an angle of turn / 2^64 turns, to 0.7 ulp (a sine below 2^-28 turns to 2^-22 of itself): the nearest quarter
-// turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, and the Taylor series' later terms
-// (at most a tenth of the sum) are added to the leading ones at the end, the roundings of which are kept.
+// Cosine and sine of an angle of turn / 2^64 turns, to 0.53 ulp (a sine below 2^-28 turns to 2^-22 of itself): the nearest quarter
+// turn is taken off exactly, the rest (at most pi / 4) is a pair of floats th + tl, the Taylor series' first terms are
+// formed as pairs too, and one addition at the end rounds.
 __device__ __forceinline__ void cos_sin_turn(unsigned long long turn, float& c, float& s) {
     // the nearest 2^-32 turns and what is left, of either sign: a small negative angle is no difference of large parts
     const int low = int(uint32_t(turn));
@@ -269,13 +269,24 @@ __device__ __forceinline__ void cos_sin_turn(unsigned long long turn, float& c, 
     const float th = __fmul_rn(rh, uh);
     const float tl = __fmaf_rn(rl, uh, __fmaf_rn(rh, ul, __fmaf_rn(rh, uh, -th)));
     const float u = __fmul_rn(th, th);
-    const float u2 = __fmaf_rn(2.f * th, tl, __fmaf_rn(th, th, -u));       // th + tl squared is u + u2
-    const float ps = __fmaf_rn(u, __fmaf_rn(u, __fmaf_rn(u, 1.f / 362880.f, -1.f / 5040.f), 1.f / 120.f), -1.f / 6.f);
-    const float sn = __fadd_rn(th, __fmaf_rn(__fmul_rn(th, u), ps, __fmaf_rn(-0.5f * u, tl, tl)));
-    const float pc = __fmaf_rn(u, __fmaf_rn(u, __fmaf_rn(u, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f), 1.f / 24.f);
+    const float ul2 = __fmaf_rn(th, th, -u), u2 = __fmaf_rn(2.f * th, tl, ul2);        // th squared is u + ul2, th + tl squared u + u2
+    // a constant as two floats, and x times it as product and what its rounding lost
+    constexpr float k6 = float(-1.0 / 6), k6l = float(-1.0 / 6 - double(k6)), k24 = float(1.0 / 24), k24l = float(1.0 / 24 - double(k24));
+    // sine: th - th^3 / 6 and the rest
+    const float c3 = __fmul_rn(th, u), p3 = __fmul_rn(c3, k6);
+    const float c3l = __fmaf_rn(th, ul2, __fmaf_rn(th, u, -c3));
+    const float p3l = __fmaf_rn(c3l, k6, __fmaf_rn(c3, k6l, __fmaf_rn(c3, k6, -p3)));
+    const float ps = __fmul_rn(u, __fmaf_rn(u, __fmaf_rn(u, __fmaf_rn(u, -1.f / 39916800.f, 1.f / 362880.f), -1.f / 5040.f), 1.f / 120.f));
+    const float s0 = __fadd_rn(th, p3), s0l = __fadd_rn(p3, -__fsub_rn(s0, th));
+    const float sn = __fadd_rn(s0, __fadd_rn(s0l, __fmaf_rn(c3, ps, __fadd_rn(p3l, __fmaf_rn(-0.5f * u, tl, tl)))));
+    // cosine: 1 - th^2 / 2 + th^4 / 24 and the rest
     const float lead = __fmaf_rn(-0.5f, u, 1.f);
-    const float left = __fmaf_rn(-0.5f, u, __fsub_rn(1.f, lead));          // what rounding `lead` lost
-    const float cn = __fadd_rn(lead, __fmaf_rn(__fmul_rn(u, u), pc, __fmaf_rn(-0.5f, u2, left)));
+    const float left = __fmaf_rn(-0.5f, u2, __fmaf_rn(-0.5f, u, __fsub_rn(1.f, lead)));
+    const float c4 = __fmul_rn(u, u), p4 = __fmul_rn(c4, k24);
+    const float p4l = __fmaf_rn(__fmaf_rn(2.f * u, u2, __fmaf_rn(u, u, -c4)), k24, __fmaf_rn(c4, k24l, __fmaf_rn(c4, k24, -p4)));
+    const float pc = __fmul_rn(u, __fmaf_rn(u, __fmaf_rn(u, -1.f / 3628800.f, 1.f / 40320.f), -1.f / 720.f));
+    const float c0 = __fadd_rn(lead, p4), c0l = __fadd_rn(p4, -__fsub_rn(c0, lead));
+    const float cn = __fadd_rn(c0, __fadd_rn(c0l, __fmaf_rn(c4, pc, __fadd_rn(p4l, left))));
     const float a = (quarter & 1) ? sn : cn, b = (quarter & 1) ? cn : sn;
     c = ((quarter + 1) & 2) ? -a : a;
     s = (quarter & 2) ? -b : b;
@@ -323,18 +334,18 @@ __global__ void __launch_bounds__(kThr) kv4_append_kernel(const __grid_constant_
             x[k][4] = v.x; x[k][5] = v.y; x[k][6] = v.z; x[k][7] = v.w;
         }
         const uint16_t* w = isq ? p.qn_w : p.kn_w;
-        // the sum of squares as a tree: the codes hang on the last bits of what is quantised
-        float part[NB];
+        // the sum of squares: over the blocks first, then a tree of neighbours, as a plain reduction by a warp of one dim a lane
+        // has it.  The codes hang on the last bits of what is quantised: in this order 0.1% of the values differ from those of
+        // a plain norm and rotation in their last bit (by the cosines' rounding), in another order of as many additions 12%.
+        float part[8];
 #pragma unroll
-        for (int k = 0; k < NB; ++k) {
-            float q[8];
+        for (int i = 0; i < 8; ++i) {
+            part[i] = __fmul_rn(x[0][i], x[0][i]);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) q[i] = __fmul_rn(x[k][i], x[k][i]);
-            part[k] = __fadd_rn(__fadd_rn(__fadd_rn(q[0], q[1]), __fadd_rn(q[2], q[3])),
-                                __fadd_rn(__fadd_rn(q[4], q[5]), __fadd_rn(q[6], q[7])));
+            for (int k = 1; k < NB; ++k) part[i] = __fadd_rn(part[i], __fmul_rn(x[k][i], x[k][i]));
         }
-        float ss = __fadd_rn(part[0], part[1]);
-        if constexpr (NB == 4) ss = __fadd_rn(ss, __fadd_rn(part[2], part[3]));
+        float ss = __fadd_rn(__fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3])),
+                             __fadd_rn(__fadd_rn(part[4], part[5]), __fadd_rn(part[6], part[7])));
         ss += __shfl_xor_sync(0xffffffffu, ss, 1);
         ss += __shfl_xor_sync(0xffffffffu, ss, 2);
         if (isq || isk) {
