@@ -207,8 +207,10 @@ def _lora(st):
     T, K, N = c["T"], c["K"], c["N"]
     if own:
         import int4_weight_only_group_gb300 as kmr
-        kmr.kmr_lora_apply(st["lora"], st["x"], st["base"], st["y"], st["dtype"], st["ids"], T, K, N, torch.cuda.current_stream())
-        return [st["y"]]
+        # fp32 rows are added to in place, as the plain form adds to them; bf16 ones go to rows of their own
+        y = st["y"] if c["bf16"] else st["base"]
+        kmr.kmr_lora_apply(st["lora"], st["x"], st["base"], y, st["dtype"], st["ids"], T, K, N, torch.cuda.current_stream())
+        return [y]
     y = st["base"].float()
     x = st["x"].float()
     for a in torch.unique(st["ids"]).tolist():
