@@ -342,7 +342,80 @@ int kmr_kv4_evict(const kmr_kv4_cache* src, const kmr_kv4_cache* dst, const int3
                   const int32_t* dst_slot_ids, const int32_t* lengths, int B, int keep, int recent,
                   const float* mass, float* dst_mass, int32_t* kept, int32_t* new_lengths, void* stream);
 
-/* Error word of the standalone kernels (kmr_int4_gemv, kmr_decode_attn, the 4-bit cache) on the
+/* ------------------------------------------------------------------ products whose weights each token chooses
+ * Beside kmr_int4_gemv, whose one matrix serves every row: an expert layer, in which each token goes to a few of many
+ * int4 MLPs, and low-rank adapters, one per request, on any projection.  The pages have neither; the experts are §07's int4
+ * linears ("kaminari", §07 int4 sidecar quantization) in the shape of its MLP.
+ * The calls take 1..2^20 tokens (KMR_ERR_BATCH), queue their work on `stream` without synchronising and allocate
+ * nothing; they can be captured into a graph once any one of them has run on the device (the first loads the
+ * kernels).  A bad id found on the device is taken as -1 and recorded in the error word that
+ * kmr_last_device_error() reads. */
+#define KMR_F32   0   /* activations in fp32 */
+#define KMR_BF16  1   /* activations in bf16 */
+
+/* Expert router: the top_k largest of each token's logits, the lower index first among equals, and their softmax
+ * weights p_i = exp(l_i) / sum_j exp(l_j) over all experts or, with renormalise, over the chosen ones.  Logits of -inf
+ * (masked) and NaN take no part; where fewer than top_k are left the remaining places get id -1 and weight 0.
+ * Logits of +inf share the weight equally.
+ *   logits   device [T, experts] fp32 or bf16 (dtype)
+ *   ids      device int32 [T, top_k];  weights  device fp32 [T, top_k]: in descending order of the logits
+ * experts 1..1024, top_k 1..32 and at most experts (KMR_ERR_SHAPE); KMR_ERR_INVALID_ARG (pointers, dtype). */
+int kmr_moe_route(const void* logits, int dtype, int T, int experts, int top_k, int renormalise, int32_t* ids,
+                  float* weights, void* stream);
+
+/* An expert layer's weights: `experts` int4 MLPs of one shape, each matrix packed by itself (kmr_pack_int4) and the
+ * packed matrices one behind the other.  Device memory, 16-byte aligned, owned by the caller. */
+typedef struct kmr_moe {
+    const void* gate_up;   /* experts x kmr_packed_size(2 intermediate, hidden): [gate; up], KMR_PACK_GATE_UP */
+    const void* down;      /* experts x kmr_packed_size(hidden, intermediate)                                 */
+    int experts;           /* 1..1024                                                                         */
+    int hidden;            /* H: a multiple of 128 up to 8192                                                 */
+    int intermediate;      /* I: likewise                                                                     */
+    int group;             /* 128                                                                             */
+} kmr_moe;
+
+/* y[t] = sum_j weights[t, j] down_e(silu(gate_e x[t]) * up_e x[t]), e = ids[t, j] (KMR_EPI_NONE), or y[t] plus that
+ * (KMR_EPI_RESIDUAL).
+ *   x, y      device [T, H] of dtype; y may be x
+ *   ids       device int32 [T, top_k]: an expert, or -1 for a place without one (a token whose places are all -1, for
+ *             instance padding, gets zeros); the same expert may stand in several places
+ *   weights   device fp32 [T, top_k]; those of places without an expert are not read
+ *   workspace device memory, 16-byte aligned, kmr_moe_experts_workspace_size(moe, dtype, T, top_k) bytes or more (0 for
+ *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
+ *             workspaces of their own.
+ * Sums are held in fp32; a token's result does not depend on the other tokens.  top_k 1..32.  Errors:
+ * KMR_ERR_INVALID_ARG (pointers, dtype, epilogue), KMR_ERR_SHAPE, KMR_ERR_BATCH, KMR_ERR_BUFFER_SIZE; on the device
+ * KMR_ERR_INVALID_ARG (an id outside -1..experts - 1). */
+size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, int T, int top_k);
+int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, const int32_t* ids, const float* weights, int T,
+                    int top_k, void* y, int epilogue, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Low-rank adapters of one projection: adapter a adds scale_a B_a A_a to its matrix [outputs, inputs].  Device
+ * memory, a and b 16-byte aligned, owned by the caller. */
+typedef struct kmr_lora {
+    const uint16_t* a;       /* bf16 [adapters][max_rank][inputs]                                         */
+    const uint16_t* b;       /* bf16 [adapters][outputs][max_rank]                                        */
+    const int32_t* ranks;    /* [adapters] or NULL (max_rank): the ranks in use; what lies past them is   */
+                             /* not used, whatever it holds (values outside 0..max_rank are held within)  */
+    const float* scales;     /* [adapters] or NULL (1)                                                    */
+    int adapters;
+    int inputs, outputs;     /* K, N: multiples of 16                                                     */
+    int max_rank;            /* a multiple of 8 up to 128                                                 */
+} kmr_lora;
+
+/* y[t] = base[t] + scale_a B_a (A_a x[t]) with a = adapter_ids[t], beside the projection that gave base (base NULL:
+ * zeros): requests of one batch, each with its own adapter or none.  One launch.
+ *   x            device, rows of K values of dtype, ldx values apart
+ *   base, y      device, rows of N values of dtype, ldy values apart; y may be base (in place).  y may be some columns of
+ *                a fused projection's rows (the v part of QKV, say); what lies between its rows is left as it was
+ *   adapter_ids  device int32 [T]; -1: y[t] = base[t]
+ * x, base and y are 16-byte aligned, ldx >= K and ldy >= N multiples of 8.  fp32 operands are multiplied to single
+ * precision (magnitudes below 3.38e38).  Errors: KMR_ERR_INVALID_ARG (pointers, dtype), KMR_ERR_SHAPE, KMR_ERR_BATCH; on
+ * the device KMR_ERR_INVALID_ARG (an id outside -1..adapters - 1, whose row is treated as -1). */
+int kmr_lora_apply(const kmr_lora* lora, const void* x, const void* base, void* y, int dtype,
+                   const int32_t* adapter_ids, int T, long long ldx, long long ldy, void* stream);
+
+/* Error word of the standalone kernels (kmr_int4_gemv, kmr_decode_attn, the 4-bit cache, experts and adapters) on the
  * current device: synchronises the device, returns the first recorded
  * KMR_ERR_* (or KMR_OK) and clears it. */
 int kmr_last_device_error(void);

@@ -26,7 +26,8 @@ __all__ = [
     "kmr_unpack_int4", "kmr_int4_gemv", "kmr_decode_attn_workspace_size",
     "kmr_decode_attn", "kmr_decode_attn_noalloc", "kmr_decode_attn_cascade_workspace_size",
     "kmr_decode_attn_cascade", "Kv4Cache", "kmr_kv4_append", "kmr_kv4_from_bf16", "kmr_kv4_to_bf16",
-    "kmr_decode_attn_kv4_workspace_size", "kmr_decode_attn_kv4", "kmr_kv4_evict", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
+    "kmr_decode_attn_kv4_workspace_size", "kmr_decode_attn_kv4", "kmr_kv4_evict", "KMR_F32", "KMR_BF16", "kmr_moe_route",
+    "Moe", "kmr_moe_experts_workspace_size", "kmr_moe_experts", "Lora", "kmr_lora_apply", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
 ]
 
 KMR_OK = 0
@@ -42,6 +43,7 @@ KMR_ERR_BATCH = -9
 KMR_PACK_GATE_UP = 1
 KMR_EPI_NONE, KMR_EPI_RESIDUAL, KMR_EPI_SILU_MUL = 0, 1, 2
 KMR_W_QKV, KMR_W_O, KMR_W_GATE_UP, KMR_W_DOWN = 0, 1, 2, 3
+KMR_F32, KMR_BF16 = 0, 1
 KMR_N_INPUT, KMR_N_POST, KMR_N_Q, KMR_N_K = 0, 1, 2, 3
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -82,6 +84,22 @@ class Kv4CacheStruct(ctypes.Structure):
     ]
 
 
+class MoeStruct(ctypes.Structure):
+    """Mirror of kmr_moe."""
+    _fields_ = [
+        ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p), ("experts", ctypes.c_int), ("hidden", ctypes.c_int),
+        ("intermediate", ctypes.c_int), ("group", ctypes.c_int),
+    ]
+
+
+class LoraStruct(ctypes.Structure):
+    """Mirror of kmr_lora."""
+    _fields_ = [
+        ("a", ctypes.c_void_p), ("b", ctypes.c_void_p), ("ranks", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+        ("adapters", ctypes.c_int), ("inputs", ctypes.c_int), ("outputs", ctypes.c_int), ("max_rank", ctypes.c_int),
+    ]
+
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _SZ = ctypes.c_size_t
@@ -106,6 +124,10 @@ _SIGNATURES = {
     "kmr_decode_attn_kv4_workspace_size": (_SZ, [_P, _I, _I, _I]),
     "kmr_decode_attn_kv4": (_I, [_P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "kmr_kv4_evict": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
+    "kmr_moe_route": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "kmr_moe_experts_workspace_size": (_SZ, [_P, _I, _I, _I]),
+    "kmr_moe_experts": (_I, [_P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P]),
+    "kmr_lora_apply": (_I, [_P, _P, _P, _P, _I, _P, _I, ctypes.c_longlong, ctypes.c_longlong, _P]),
     "kmr_last_device_error": (_I, []),
     "kmr_model_create": (_I, [ctypes.POINTER(ModelConfig), ctypes.POINTER(_P)]),
     "kmr_model_destroy": (_I, [_P]),
@@ -380,6 +402,91 @@ def kmr_kv4_evict(src, dst, src_slot_ids, dst_slot_ids, lengths, B, keep, recent
                                _dev(lengths, _I32, "lengths"), B, keep, recent, _dev(mass, _F32, "mass"),
                                _dev(dst_mass, _F32, "dst_mass"), _dev(kept, _I32, "kept"), _dev(new_lengths, _I32, "new_lengths"),
                                _stream(stream)), "kmr_kv4_evict")
+
+
+# ------------------------------------------------------------------ products whose weights each token chooses
+def _act(dtype: int) -> set:
+    """The tensor types of an activation argument."""
+    return _BF16 if dtype == KMR_BF16 else _F32
+
+
+class Moe:
+    """An expert layer's weights (kmr_moe) over two device tensors that it keeps alive: the packed gate_up matrices
+    (kmr_pack_int4 with KMR_PACK_GATE_UP) and the packed down matrices of `experts` MLPs, one behind the other."""
+
+    def __init__(self, gate_up, down, experts: int, hidden: int, intermediate: int, group: int = 128, stream=None):
+        for t, name, size in ((gate_up, "gate_up", kmr_packed_size(2 * intermediate, hidden, group)),
+                              (down, "down", kmr_packed_size(hidden, intermediate, group))):
+            if size == 0:
+                raise ValueError("hidden and intermediate are multiples of the group, which is 128")
+            if t.element_size() != 1 or not t.is_contiguous() or t.numel() != experts * size:
+                raise ValueError(f"{name} is not {experts} packed matrices of {size} bytes")
+        if gate_up.device != down.device:
+            raise ValueError("the tensors of an expert layer are on one device")
+        self.tensors = (gate_up, down)
+        self.experts, self.hidden, self.intermediate, self.group = experts, hidden, intermediate, group
+        self._struct = MoeStruct(gate_up.data_ptr(), down.data_ptr(), experts, hidden, intermediate, group)
+        self._as_parameter_ = ctypes.addressof(self._struct)
+
+
+class Lora:
+    """Low-rank adapters of one projection (kmr_lora) over the device tensors a bf16 [adapters, max_rank, inputs],
+    b bf16 [adapters, outputs, max_rank], ranks int32 [adapters] or None and scales fp32 [adapters] or None, kept alive."""
+
+    def __init__(self, a, b, ranks=None, scales=None):
+        adapters, rank, inputs = a.shape
+        if b.dim() != 3 or b.shape[0] != adapters or b.shape[2] != rank:
+            raise ValueError("adapters take a [adapters, max_rank, inputs] and b [adapters, outputs, max_rank]")
+        for t in (ranks, scales):
+            if t is not None and tuple(t.shape) != (adapters,):
+                raise ValueError("ranks and scales have one value per adapter")
+        if len({t.device for t in (a, b, ranks, scales) if t is not None}) > 1:
+            raise ValueError("the tensors of the adapters are on one device")
+        self.tensors = (a, b, ranks, scales)
+        self.adapters, self.inputs, self.outputs, self.max_rank = adapters, inputs, b.shape[1], rank
+        self._struct = LoraStruct(_dev(a, _BF16, "a"), _dev(b, _BF16, "b"), _dev(ranks, _I32, "ranks"),
+                                  _dev(scales, _F32, "scales"), adapters, inputs, self.outputs, rank)
+        self._as_parameter_ = ctypes.addressof(self._struct)
+
+
+def _rows(a, kind: set, ld: int, name: str) -> Optional[int]:
+    """Device address of rows that lie ld values apart: as _dev, or a matrix with that stride."""
+    if a is None or type(a) is int:
+        return a
+    try:
+        if a.dtype in kind and a.dim() == 2 and a.stride(1) == 1 and (a.shape[0] == 1 or a.stride(0) == ld):
+            return a.data_ptr()
+        if a.dtype in kind and a.dim() == 2:
+            raise ValueError(f"{name} has rows {a.stride(0)} values apart (and values {a.stride(1)}), not {ld} (and 1)")
+    except AttributeError:
+        pass
+    return _dev(a, kind, name)
+
+
+def kmr_moe_route(logits, dtype, T, experts, top_k, renormalise, ids, weights, stream=None) -> None:
+    """Each token's top_k experts and their softmax weights (see include/kmr.h)."""
+    _check(lib().kmr_moe_route(_dev(logits, _act(dtype), "logits"), dtype, T, experts, top_k, int(bool(renormalise)),
+                               _dev(ids, _I32, "ids"), _dev(weights, _F32, "weights"), _stream(stream)), "kmr_moe_route")
+
+
+def kmr_moe_experts_workspace_size(moe, dtype, T, top_k) -> int:
+    return lib().kmr_moe_experts_workspace_size(moe, dtype, T, top_k)
+
+
+def kmr_moe_experts(moe, x, dtype, ids, weights, T, top_k, y, epilogue, workspace, workspace_bytes, stream=None) -> None:
+    """The weighted sum of each token's int4 experts (see include/kmr.h)."""
+    kind = _act(dtype)
+    _check(lib().kmr_moe_experts(moe, _dev(x, kind, "x"), dtype, _dev(ids, _I32, "ids"), _dev(weights, _F32, "weights"), T,
+                                 top_k, _dev(y, kind, "y"), epilogue, _ptr(workspace), workspace_bytes, _stream(stream)),
+           "kmr_moe_experts")
+
+
+def kmr_lora_apply(lora, x, base, y, dtype, adapter_ids, T, ldx, ldy, stream=None) -> None:
+    """base plus each row's low-rank adapter (see include/kmr.h).  x, base and y may be columns of wider matrices, whose
+    rows lie ldx or ldy values apart."""
+    kind = _act(dtype)
+    _check(lib().kmr_lora_apply(lora, _rows(x, kind, ldx, "x"), _rows(base, kind, ldy, "base"), _rows(y, kind, ldy, "y"), dtype,
+                                _dev(adapter_ids, _I32, "adapter_ids"), T, ldx, ldy, _stream(stream)), "kmr_lora_apply")
 
 
 def kmr_prefill_plan(N: int, K: int, M: int, sms: int) -> Tuple[int, int]:

@@ -27,6 +27,9 @@ cudaError_t head_set_attributes();
 cudaError_t attn_set_attributes();
 cudaError_t kv4_attn_set_attributes();
 cudaError_t kv4_set_attributes();
+cudaError_t moe_route_set_attributes();
+cudaError_t moe_small_set_attributes();
+cudaError_t lora_set_attributes();
 
 __device__ int g_standalone_err;
 
@@ -62,6 +65,9 @@ cudaError_t ensure_kernel_attributes() {
     if ((e = attn_set_attributes()) != cudaSuccess) return e;
     if ((e = kv4_attn_set_attributes()) != cudaSuccess) return e;
     if ((e = kv4_set_attributes()) != cudaSuccess) return e;
+    if ((e = moe_route_set_attributes()) != cudaSuccess) return e;
+    if ((e = moe_small_set_attributes()) != cudaSuccess) return e;
+    if ((e = lora_set_attributes()) != cudaSuccess) return e;
     if ((e = poison_set_attributes()) != cudaSuccess) return e;
     if ((e = gemm_set_attributes()) != cudaSuccess) return e;
     if ((e = tc_gemm_set_attributes()) != cudaSuccess) return e;
