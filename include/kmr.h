@@ -372,7 +372,14 @@ typedef struct kmr_moe {
     int hidden;            /* H: a multiple of 128 up to 8192                                                 */
     int intermediate;      /* I: likewise                                                                     */
     int group;             /* 128                                                                             */
+    float* factors;        /* kmr_moe_factors_size() bytes that kmr_moe_prepare fills                         */
 } kmr_moe;
+
+/* What the grouped products need to know of the weights (powers of two that fit each row into fp16's range, and bounds of the
+ * rows' norms): kmr_moe_prepare fills moe->factors from the packed matrices, once after they have been packed and before the
+ * first kmr_moe_experts on them.  The size is 0 for a shape that the calls refuse. */
+size_t kmr_moe_factors_size(int experts, int hidden, int intermediate);
+int kmr_moe_prepare(const kmr_moe* moe, void* stream);
 
 /* y[t] = sum_j weights[t, j] down_e(silu(gate_e x[t]) * up_e x[t]), e = ids[t, j] (KMR_EPI_NONE), or y[t] plus that
  * (KMR_EPI_RESIDUAL).
@@ -383,7 +390,9 @@ typedef struct kmr_moe {
  *   workspace device memory, 16-byte aligned, kmr_moe_experts_workspace_size(moe, dtype, T, top_k) bytes or more (0 for
  *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
  *             workspaces of their own.
- * Sums are held in fp32; a token's result does not depend on the other tokens.  top_k 1..32.  Errors:
+ * Products are exact and sums are held in fp32, whatever the type; between gate_up and down the activations keep 22 bits (fp32)
+ * or 11 (bf16).  Up to 32 places (T top_k) are two launches, more are five for every 65536 places; within either form a
+ * token's result does not depend on the other tokens.  top_k 1..32.  Errors:
  * KMR_ERR_INVALID_ARG (pointers, dtype, epilogue), KMR_ERR_SHAPE, KMR_ERR_BATCH, KMR_ERR_BUFFER_SIZE; on the device
  * KMR_ERR_INVALID_ARG (an id outside -1..experts - 1). */
 size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, int T, int top_k);

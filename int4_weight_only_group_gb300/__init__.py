@@ -27,7 +27,7 @@ __all__ = [
     "kmr_decode_attn", "kmr_decode_attn_noalloc", "kmr_decode_attn_cascade_workspace_size",
     "kmr_decode_attn_cascade", "Kv4Cache", "kmr_kv4_append", "kmr_kv4_from_bf16", "kmr_kv4_to_bf16",
     "kmr_decode_attn_kv4_workspace_size", "kmr_decode_attn_kv4", "kmr_kv4_evict", "KMR_F32", "KMR_BF16", "kmr_moe_route",
-    "Moe", "kmr_moe_experts_workspace_size", "kmr_moe_experts", "Lora", "kmr_lora_apply", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
+    "Moe", "kmr_moe_factors_size", "kmr_moe_prepare", "kmr_moe_experts_workspace_size", "kmr_moe_experts", "Lora", "kmr_lora_apply", "kmr_last_device_error", "kmr_smem_poison", "kmr_selftest_wait_timeout", "Model",
 ]
 
 KMR_OK = 0
@@ -88,7 +88,7 @@ class MoeStruct(ctypes.Structure):
     """Mirror of kmr_moe."""
     _fields_ = [
         ("gate_up", ctypes.c_void_p), ("down", ctypes.c_void_p), ("experts", ctypes.c_int), ("hidden", ctypes.c_int),
-        ("intermediate", ctypes.c_int), ("group", ctypes.c_int),
+        ("intermediate", ctypes.c_int), ("group", ctypes.c_int), ("factors", ctypes.c_void_p),
     ]
 
 
@@ -125,6 +125,8 @@ _SIGNATURES = {
     "kmr_decode_attn_kv4": (_I, [_P, _P, _P, _P, _I, _I, ctypes.c_float, _P, _P, _P, _SZ, _P]),
     "kmr_kv4_evict": (_I, [_P, _P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P, _P]),
     "kmr_moe_route": (_I, [_P, _I, _I, _I, _I, _I, _P, _P, _P]),
+    "kmr_moe_factors_size": (_SZ, [_I, _I, _I]),
+    "kmr_moe_prepare": (_I, [_P, _P]),
     "kmr_moe_experts_workspace_size": (_SZ, [_P, _I, _I, _I]),
     "kmr_moe_experts": (_I, [_P, _P, _I, _P, _P, _I, _I, _P, _I, _P, _SZ, _P]),
     "kmr_lora_apply": (_I, [_P, _P, _P, _P, _I, _P, _I, ctypes.c_longlong, ctypes.c_longlong, _P]),
@@ -412,7 +414,8 @@ def _act(dtype: int) -> set:
 
 class Moe:
     """An expert layer's weights (kmr_moe) over two device tensors that it keeps alive: the packed gate_up matrices
-    (kmr_pack_int4 with KMR_PACK_GATE_UP) and the packed down matrices of `experts` MLPs, one behind the other."""
+    (kmr_pack_int4 with KMR_PACK_GATE_UP) and the packed down matrices of `experts` MLPs, one behind the other.  They are
+    packed before the object is made: kmr_moe_prepare runs here, on `stream`."""
 
     def __init__(self, gate_up, down, experts: int, hidden: int, intermediate: int, group: int = 128, stream=None):
         for t, name, size in ((gate_up, "gate_up", kmr_packed_size(2 * intermediate, hidden, group)),
@@ -423,10 +426,13 @@ class Moe:
                 raise ValueError(f"{name} is not {experts} packed matrices of {size} bytes")
         if gate_up.device != down.device:
             raise ValueError("the tensors of an expert layer are on one device")
-        self.tensors = (gate_up, down)
+        import torch
+        factors = torch.empty(kmr_moe_factors_size(experts, hidden, intermediate), dtype=torch.uint8, device=gate_up.device)
+        self.tensors = (gate_up, down, factors)
         self.experts, self.hidden, self.intermediate, self.group = experts, hidden, intermediate, group
-        self._struct = MoeStruct(gate_up.data_ptr(), down.data_ptr(), experts, hidden, intermediate, group)
+        self._struct = MoeStruct(gate_up.data_ptr(), down.data_ptr(), experts, hidden, intermediate, group, factors.data_ptr())
         self._as_parameter_ = ctypes.addressof(self._struct)
+        kmr_moe_prepare(self, stream)
 
 
 class Lora:
@@ -467,6 +473,15 @@ def kmr_moe_route(logits, dtype, T, experts, top_k, renormalise, ids, weights, s
     """Each token's top_k experts and their softmax weights (see include/kmr.h)."""
     _check(lib().kmr_moe_route(_dev(logits, _act(dtype), "logits"), dtype, T, experts, top_k, int(bool(renormalise)),
                                _dev(ids, _I32, "ids"), _dev(weights, _F32, "weights"), _stream(stream)), "kmr_moe_route")
+
+
+def kmr_moe_factors_size(experts, hidden, intermediate) -> int:
+    return lib().kmr_moe_factors_size(experts, hidden, intermediate)
+
+
+def kmr_moe_prepare(moe, stream=None) -> None:
+    """Fills the weights' factors (see include/kmr.h); Moe does so when it is made."""
+    _check(lib().kmr_moe_prepare(moe, _stream(stream)), "kmr_moe_prepare")
 
 
 def kmr_moe_experts_workspace_size(moe, dtype, T, top_k) -> int:

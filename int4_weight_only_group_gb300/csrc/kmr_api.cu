@@ -29,6 +29,7 @@ cudaError_t kv4_attn_set_attributes();
 cudaError_t kv4_set_attributes();
 cudaError_t moe_route_set_attributes();
 cudaError_t moe_small_set_attributes();
+cudaError_t moe_tc_set_attributes();
 cudaError_t lora_set_attributes();
 
 __device__ int g_standalone_err;
@@ -67,6 +68,7 @@ cudaError_t ensure_kernel_attributes() {
     if ((e = kv4_set_attributes()) != cudaSuccess) return e;
     if ((e = moe_route_set_attributes()) != cudaSuccess) return e;
     if ((e = moe_small_set_attributes()) != cudaSuccess) return e;
+    if ((e = moe_tc_set_attributes()) != cudaSuccess) return e;
     if ((e = lora_set_attributes()) != cudaSuccess) return e;
     if ((e = poison_set_attributes()) != cudaSuccess) return e;
     if ((e = gemm_set_attributes()) != cudaSuccess) return e;

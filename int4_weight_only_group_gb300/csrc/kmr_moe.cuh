@@ -44,6 +44,39 @@ struct MoeSmallParams {
 cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaStream_t st);
 cudaError_t moe_small_set_attributes();
 
+// Grouped form (kmr_moe_tc.cu).
+constexpr int kMoeChunkPlaces = 65536;       // places of one pass
+struct MoeTcParams {
+    MoeView w;
+    const float* rho_gate_up;                // [E][2I] row factors, packed row order
+    const float* rho_down;                   // [E][H]
+    const float* norms;                      // [E][2] bounds of the gate and up rows' norms
+    const void* x;                           // [T][H]
+    const int32_t* ids;                      // [T][k]
+    const float* weights;                    // [T][k]
+    int T, k, cap;                           // tokens of a tile: 16, 32, 64 or 128
+    int* ntiles;
+    int4* tiles;                             // (expert, first position, tokens, -)
+    int32_t* pos;                            // [T][k]: the place's position, or -1
+    float* isx;                              // [P] 1 / scale of the position's inputs
+    float* sact;                             // [P] scale of its activations
+    uint8_t* xs;                             // staged inputs
+    uint8_t* as;                             // staged activations
+    float* out;                              // [P][H]
+    void* y;                                 // [T][H]
+    int resid;
+    int* err;
+};
+// Byte offsets into the workspace (the tile count comes first).
+struct MoeTcSizes {
+    size_t tiles, pos, isx, sact, xs, as, out, total;
+};
+int moe_tc_cap(long long places, int E, bool bf16);
+MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k);
+cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t st);
+cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_down, float* norms, cudaStream_t st);
+cudaError_t moe_tc_set_attributes();
+
 // ------------------------------------------------------------------ adapters
 constexpr int kLoraMaxRank = 128;
 struct LoraParams {

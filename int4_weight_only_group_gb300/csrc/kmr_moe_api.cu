@@ -1,5 +1,5 @@
 // C ABI of the products whose weights each token chooses (declared in kmr.h): argument checks, then the launches of
-// kmr_moe_route.cu, kmr_moe_small.cu and kmr_lora.cu.
+// kmr_moe_route.cu, kmr_moe_small.cu, kmr_moe_tc.cu and kmr_lora.cu.
 #include "kmr_moe.cuh"
 
 using namespace kmr;
@@ -8,13 +8,13 @@ namespace {
 
 bool aligned(const void* p, unsigned n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 bool dtype_ok(int dtype) { return dtype == KMR_F32 || dtype == KMR_BF16; }
+bool dim_ok(int n) { return n >= 128 && n <= kMoeMaxDim && n % 128 == 0; }
 
 int view_of(const kmr_moe* m, MoeView* v) {
-    if (!m || !m->gate_up || !m->down) return KMR_ERR_INVALID_ARG;
-    if (!aligned(m->gate_up, 16) || !aligned(m->down, 16)) return KMR_ERR_INVALID_ARG;
+    if (!m || !m->gate_up || !m->down || !m->factors) return KMR_ERR_INVALID_ARG;
+    if (!aligned(m->gate_up, 16) || !aligned(m->down, 16) || !aligned(m->factors, 16)) return KMR_ERR_INVALID_ARG;
     if (m->experts < 1 || m->experts > kMoeMaxExperts || m->group != 128) return KMR_ERR_SHAPE;
-    for (const int n : {m->hidden, m->intermediate})
-        if (n < 128 || n > kMoeMaxDim || n % 128) return KMR_ERR_SHAPE;
+    if (!dim_ok(m->hidden) || !dim_ok(m->intermediate)) return KMR_ERR_SHAPE;
     v->gate_up = static_cast<const uint8_t*>(m->gate_up);
     v->down = static_cast<const uint8_t*>(m->down);
     v->E = m->experts;
@@ -26,6 +26,23 @@ int view_of(const kmr_moe* m, MoeView* v) {
 int counts_ok(int T, int top_k) {
     if (T < 1 || T > kMoeMaxTokens) return KMR_ERR_BATCH;
     return top_k < 1 || top_k > kMoeMaxTopK ? KMR_ERR_SHAPE : KMR_OK;
+}
+
+// The few-token form takes the calls whose places fit a warp's lanes.
+bool small(int T, int top_k) { return (long long)T * top_k <= kMoeSmallPlaces; }
+// Tokens of one pass of the grouped form: bounds the workspace.
+int chunk_of(int T, int top_k) {
+    const int most = kMoeChunkPlaces / top_k;
+    return T < most ? T : most;
+}
+
+struct Factors {
+    float *gate_up, *down, *norms;
+};
+Factors factors_of(const kmr_moe* m) {
+    float* f = m->factors;
+    const size_t gate_up = size_t(m->experts) * 2 * m->intermediate;
+    return {f, f + gate_up, f + gate_up + size_t(m->experts) * m->hidden};
 }
 
 }  // namespace
@@ -48,16 +65,31 @@ extern "C" int kmr_moe_route(const void* logits, int dtype, int T, int experts, 
     return launch_moe_route(p, dtype == KMR_BF16, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KMR_OK : KMR_ERR_CUDA;
 }
 
+extern "C" size_t kmr_moe_factors_size(int experts, int hidden, int intermediate) {
+    if (experts < 1 || experts > kMoeMaxExperts || !dim_ok(hidden) || !dim_ok(intermediate)) return 0;
+    return size_t(experts) * (2 * size_t(intermediate) + hidden + 2) * 4;
+}
+
+extern "C" int kmr_moe_prepare(const kmr_moe* moe, void* stream) {
+    MoeView v;
+    const int rc = view_of(moe, &v);
+    if (rc != KMR_OK) return rc;
+    if (ensure_kernel_attributes() != cudaSuccess) return KMR_ERR_CUDA;
+    const Factors f = factors_of(moe);
+    return launch_moe_factors(v, f.gate_up, f.down, f.norms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? KMR_OK : KMR_ERR_CUDA;
+}
+
 extern "C" size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, int T, int top_k) {
     MoeView v;
     if (view_of(moe, &v) != KMR_OK || !dtype_ok(dtype) || counts_ok(T, top_k) != KMR_OK) return 0;
-    return size_t(kMoeSmallPlaces) * v.I * 4;
+    if (small(T, top_k)) return size_t(kMoeSmallPlaces) * v.I * 4;
+    return moe_tc_sizes(v, dtype == KMR_BF16, chunk_of(T, top_k), top_k).total;
 }
 
 extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, const int32_t* ids, const float* weights, int T,
                                int top_k, void* y, int epilogue, void* workspace, size_t workspace_bytes, void* stream) {
-    MoeSmallParams p = {};
-    int rc = view_of(moe, &p.w);
+    MoeView v;
+    int rc = view_of(moe, &v);
     if (rc != KMR_OK) return rc;
     if (!x || !ids || !weights || !y || !workspace || !dtype_ok(dtype)) return KMR_ERR_INVALID_ARG;
     if (!aligned(x, 16) || !aligned(y, 16) || !aligned(workspace, 16) || !aligned(ids, 4) || !aligned(weights, 4))
@@ -65,20 +97,53 @@ extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, con
     if (epilogue != KMR_EPI_NONE && epilogue != KMR_EPI_RESIDUAL) return KMR_ERR_INVALID_ARG;
     if ((rc = counts_ok(T, top_k)) != KMR_OK) return rc;
     if (workspace_bytes < kmr_moe_experts_workspace_size(moe, dtype, T, top_k)) return KMR_ERR_BUFFER_SIZE;
-    if (ensure_kernel_attributes() != cudaSuccess || !(p.err = standalone_error_word())) return KMR_ERR_CUDA;
+    int* err = nullptr;
+    if (ensure_kernel_attributes() != cudaSuccess || !(err = standalone_error_word())) return KMR_ERR_CUDA;
     const bool bf16 = dtype == KMR_BF16;
-    const size_t row = size_t(p.w.H) * (bf16 ? 2 : 4);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (small(T, top_k)) {
+        MoeSmallParams p = {};
+        p.w = v;
+        p.x = x;
+        p.ids = ids;
+        p.weights = weights;
+        p.T = T;
+        p.k = top_k;
+        p.act = static_cast<float*>(workspace);
+        p.y = y;
+        p.resid = epilogue == KMR_EPI_RESIDUAL;
+        p.err = err;
+        return launch_moe_small(p, bf16, num_sms(), st) == cudaSuccess ? KMR_OK : KMR_ERR_CUDA;
+    }
+    const size_t row = size_t(v.H) * (bf16 ? 2 : 4);
+    const int chunk = chunk_of(T, top_k);
+    const MoeTcSizes z = moe_tc_sizes(v, bf16, chunk, top_k);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    const Factors f = factors_of(moe);
+    MoeTcParams p = {};
+    p.w = v;
+    p.rho_gate_up = f.gate_up;
+    p.rho_down = f.down;
+    p.norms = f.norms;
     p.k = top_k;
-    p.act = static_cast<float*>(workspace);
+    p.ntiles = reinterpret_cast<int*>(ws);
+    p.tiles = reinterpret_cast<int4*>(ws + z.tiles);
+    p.pos = reinterpret_cast<int32_t*>(ws + z.pos);
+    p.isx = reinterpret_cast<float*>(ws + z.isx);
+    p.sact = reinterpret_cast<float*>(ws + z.sact);
+    p.xs = ws + z.xs;
+    p.as = ws + z.as;
+    p.out = reinterpret_cast<float*>(ws + z.out);
     p.resid = epilogue == KMR_EPI_RESIDUAL;
-    const int chunk = kMoeSmallPlaces / top_k;
+    p.err = err;
     for (int t = 0; t < T; t += chunk) {
         p.x = static_cast<const uint8_t*>(x) + t * row;
         p.ids = ids + size_t(t) * top_k;
         p.weights = weights + size_t(t) * top_k;
         p.y = static_cast<uint8_t*>(y) + t * row;
         p.T = T - t < chunk ? T - t : chunk;
-        if (launch_moe_small(p, bf16, num_sms(), static_cast<cudaStream_t>(stream)) != cudaSuccess) return KMR_ERR_CUDA;
+        p.cap = moe_tc_cap((long long)p.T * top_k, v.E, bf16);
+        if (launch_moe_tc(p, bf16, num_sms(), st) != cudaSuccess) return KMR_ERR_CUDA;
     }
     return KMR_OK;
 }

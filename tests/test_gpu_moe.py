@@ -119,7 +119,8 @@ def rows_close(got, want, tol):
 SHAPES = [  # E, H, I, T, k
     (8, 256, 128, 1, 2), (1, 128, 128, 3, 1), (16, 512, 384, 33, 4), (5, 384, 256, 7, 8), (4, 2048, 768, 2, 3), (60, 256, 128, 100, 4),
     (2, 2176, 128, 5, 2), (2, 256, 2176, 5, 2), (1, 8192, 128, 2, 1), (1, 128, 8192, 2, 1), (2, 4096, 4096, 1, 2), (3, 640, 1408, 40, 2),
-    (8, 512, 256, 300, 2), (2, 256, 384, 257, 1),
+    (8, 512, 256, 300, 2), (2, 256, 384, 257, 1), (2, 8192, 128, 40, 1), (2, 128, 8192, 40, 1), (3, 256, 2176, 700, 2),
+    (40, 256, 128, 1200, 8), (200, 128, 128, 64, 6), (4, 2048, 768, 90, 2), (1, 128, 128, 2081, 32),
 ]
 
 

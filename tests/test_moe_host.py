@@ -22,7 +22,7 @@ ARGS = {
     "kmr_moe_experts": dict(moe=None, x=P, dtype=0, ids=P, weights=P, T=4, k=2, y=P, epi=0, ws=P, n=1 << 40),
     "kmr_lora_apply": dict(lora=None, x=P, base=P, y=P, dtype=0, ids=P, T=4, ldx=64, ldy=32),
 }
-MOE = dict(gate_up=P, down=P, experts=8, hidden=256, intermediate=128, group=128)
+MOE = dict(gate_up=P, down=P, experts=8, hidden=256, intermediate=128, group=128, factors=P)
 LORA = dict(a=P, b=P, ranks=None, scales=None, adapters=3, inputs=64, outputs=32, max_rank=16)
 
 
@@ -67,7 +67,7 @@ def test_bad_arguments(L, name, kw, code):
     ("kmr_moe_experts", dict(gate_up=24), -1), ("kmr_moe_experts", dict(experts=0), -2), ("kmr_moe_experts", dict(experts=1025), -2),
     ("kmr_moe_experts", dict(hidden=192), -2), ("kmr_moe_experts", dict(hidden=8320), -2), ("kmr_moe_experts", dict(hidden=0), -2),
     ("kmr_moe_experts", dict(intermediate=64), -2), ("kmr_moe_experts", dict(intermediate=8320), -2),
-    ("kmr_moe_experts", dict(group=64), -2),
+    ("kmr_moe_experts", dict(group=64), -2), ("kmr_moe_experts", dict(factors=None), -1), ("kmr_moe_experts", dict(factors=8), -1),
     ("kmr_lora_apply", False, -1), ("kmr_lora_apply", dict(a=None), -1), ("kmr_lora_apply", dict(b=None), -1),
     ("kmr_lora_apply", dict(a=8), -1), ("kmr_lora_apply", dict(b=8), -1), ("kmr_lora_apply", dict(ranks=2), -1),
     ("kmr_lora_apply", dict(scales=2), -1), ("kmr_lora_apply", dict(adapters=0), -2), ("kmr_lora_apply", dict(inputs=40), -2),
@@ -76,6 +76,16 @@ def test_bad_arguments(L, name, kw, code):
 ])
 def test_bad_weights(L, name, kw, code):
     assert call(L, name, kw) == code
+
+
+def test_prepare_and_factors(L):
+    assert L.kmr_moe_prepare(None, None) == -1
+    for kw, code in ((dict(gate_up=None), -1), (dict(factors=None), -1), (dict(hidden=100), -2), (dict(group=32), -2)):
+        m = kmr.MoeStruct(**{**MOE, **kw})
+        assert L.kmr_moe_prepare(ctypes.addressof(m), None) == code
+    F = L.kmr_moe_factors_size
+    assert F(3, 256, 128) == 3 * (2 * 128 + 256 + 2) * 4
+    assert F(0, 256, 128) == F(1025, 256, 128) == F(3, 200, 128) == F(3, 256, 8320) == 0
 
 
 def test_workspace_size(L):
