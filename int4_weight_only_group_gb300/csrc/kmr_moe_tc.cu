@@ -11,8 +11,8 @@
 // The product, D[row][token] = sum_k w[row][k] x[token][k], w = (q - 8) s + z:
 //   * A = (q - 8) s rho: a 4-bit integer times a bf16 scale has 11 significant bits, so fp16 holds it exactly once a power of two
 //     rho per row (laid out once, moe_factors_kernel) has brought the row's scales into fp16's range.
-//   * the zero points' share sum_g z_g X_g, X_g = sum of the group's inputs, goes through the same accumulator as a few more
-//     inputs: z rho 2^6 against X 2^-6 for every 64 inputs, X in two fp16 terms.
+//   * the zero points' share sum_g z_g X_g, X_g = sum of the group's inputs, goes through the same accumulator as one more MMA for
+//     every two groups: z rho 2^6 against X 2^-6 for every 64 inputs, X in two fp16 terms.
 //   * B = x sigma (a power of two per row): exact for bf16 inputs, two terms (the fp16 rounding and what it left, two
 //     MMAs on the same A) for fp32 ones.  So products are exact and sums are fp32 in both types.
 //   * the activation's scale must be known before its row is complete: |silu(g) u| <= |g| |u| <= (|x| max |gate row|)
@@ -35,10 +35,10 @@ namespace {
 
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                        // packed weight rows of a product (the MMA's M)
-constexpr uint32_t kWBytes = 8 * kGroupBytes;     // a group of eight KMR4 tiles
-constexpr uint32_t kBRing = 128 * 1024;
-constexpr int kAQ = 4;                            // dequantised groups in tensor memory, 64 columns each
-constexpr int kMaxStages = 16;
+constexpr uint32_t kWBytes = 16 * kGroupBytes;    // two groups of eight KMR4 tiles
+constexpr int kAQ = 2;                            // pairs of dequantised groups in tensor memory, 128 columns each
+constexpr int kMaxStages = 8;
+constexpr int kMaxAcc = 8;                        // accumulators: as many as 256 columns hold
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(max(1, min(253, e + 127))) << 23); }
 // e such that |v| < 2^e, for v >= 0 (128 or more for what is not finite)
@@ -123,27 +123,24 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
 }
 
 // ------------------------------------------------------------------ operand layout
-// Staged rows: blocks of 8 rows; within one, per group of 128 inputs NP (terms) x 2 atoms of [8 rows][64 inputs] fp16 with the
-// 16-byte pieces of a row swizzled by the row (the MMA's 128-byte swizzle), then the sums' atoms, first terms and remainders.
+// Staged rows: blocks of 8 rows; within one, for each of the NP terms every group of 128 inputs as 2 atoms of [8 rows][64 inputs]
+// fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte swizzle), then for every pair of groups the
+// sums of their four 64 inputs, [8 rows][8]: per group the first terms of its two sums and their remainders.
 // Input k of 16 sits at 2 (k % 8) - k % 2 + 2 (k / 8) (the order of A's columns in tensor memory).
-__host__ __device__ constexpr int sum_atoms(int K) { return (K / 64 + 63) / 64; }
-__host__ __device__ constexpr size_t block_bytes(int K, int np) {
-    return size_t(K / 128) * np * 2048 + size_t(2) * sum_atoms(K) * 1024;
-}
+__host__ __device__ constexpr size_t sums_at(int K, int np) { return size_t(K / 128) * np * 2048; }
+__host__ __device__ constexpr size_t block_bytes(int K, int np) { return sums_at(K, np) + size_t(K / 128 + 1) / 2 * 128; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
-// Sum number h (of 64 inputs) of a row: its two terms.  `sums` is the block's first sum atom.
-__device__ __forceinline__ void put_sum(uint8_t* sums, int K, int row, int h, float X) {
+// Sum number h (of 64 inputs) of a row: its two terms.  `sums` are the block's.
+__device__ __forceinline__ void put_sum(uint8_t* sums, int row, int h, float X) {
     const float x = X * 0.015625f;
     const __half hi = __float2half_rn(x);
-    const __half lo = __float2half_rn(__fsub_rn(x, __half2float(hi)));
-    uint8_t* at = sums + (h >> 6) * 1024 + piece(row, (h & 63) >> 3) + (h & 7) * 2;
-    *reinterpret_cast<__half*>(at) = hi;
-    *reinterpret_cast<__half*>(at + sum_atoms(K) * 1024) = lo;
+    __half* at = reinterpret_cast<__half*>(sums + (h >> 2) * 128 + row * 16) + ((h >> 1) & 1) * 4 + (h & 1);
+    at[0] = hi;
+    at[2] = __float2half_rn(__fsub_rn(x, __half2float(hi)));
 }
-// The places of sums past the last that an MMA step covers.
-__device__ __forceinline__ void clear_sums(uint8_t* sums, int K, int row, int i) {
-    const int h = K / 64 + i;
-    if (h < ((K / 64 + 15) & ~15)) put_sum(sums, K, row, h, 0.f);
+// An odd number of groups leaves half of the last pair's sums.
+__device__ __forceinline__ void clear_sums(uint8_t* sums, int K, int row) {
+    if ((K >> 7) & 1) *reinterpret_cast<uint2*>(sums + (K >> 8) * 128 + row * 16 + 8) = make_uint2(0u, 0u);
 }
 
 // ------------------------------------------------------------------ stage
@@ -224,20 +221,16 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
         for (int j = 0; j < n; ++j) {
             const int at = pos[j], row = at & 7;
             uint8_t* blk = p.xs + size_t(at >> 3) * bb;
-            uint8_t* to = blk + size_t(k >> 7) * NP * 2048 + ((k >> 6) & 1) * 1024 +
-                          piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
+            uint8_t* to = blk + size_t(k >> 6) * 1024 + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * 2048) = out[q];
-            if ((lane & 15) == 0) put_sum(blk + size_t(K >> 7) * NP * 2048, K, row, k >> 6, X);
+            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + size_t(q) * K * 16) = out[q];
+            if ((lane & 15) == 0) put_sum(blk + sums_at(K, NP), row, k >> 6, X);
         }
     }
     ss = warp_sum(ss);
     if (lane == 0) red[1][warp] = ss;
     __syncthreads();
-    for (int i = tid; i < n * 16; i += kStageThr) {
-        const int at = pos[i >> 4];
-        clear_sums(p.xs + size_t(at >> 3) * bb + size_t(K >> 7) * NP * 2048, K, at & 7, i & 15);
-    }
+    if (tid < n) clear_sums(p.xs + size_t(pos[tid] >> 3) * bb + sums_at(K, NP), K, pos[tid] & 7);
     if (tid < p.k) {
         const int at = p.pos[size_t(t) * p.k + tid];
         if (at < 0) return;
@@ -254,53 +247,88 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
 // ------------------------------------------------------------------ the grouped product
 constexpr int kUnpackWarps = 8, kTokenWarp = 10, kEpiWarp = 11, kEpiWarps = 4;
 constexpr int kThr = (kEpiWarp + kEpiWarps) * 32;
+constexpr uint32_t kSmem = 227 * 1024;
 
+// The tensor cores cut a running sum off rather than round it, so a chain of n steps of 16 inputs comes out some n 2^-25 too
+// small (measured: 1040 steps, 2.3e-5).  bf16 results do not show it.  For fp32 the epilogue warps add up the groups' sums (8
+// steps) in registers, which limits a tile to 64 tokens: its two terms are 128 columns of one MMA.  (Four groups at a
+// time: 3.7e-6 of the result.)
+template <int NP>
+constexpr int kTileTokens = NP == 2 ? 64 : 128;
+
+// Shared memory: the token ring, [gate_up: a tile of activations], the zero points (of two pairs of groups) and 2 KB of zeros behind
+// them, barriers, the tokens' factors, the weight ring.
+constexpr uint32_t kRing = 136 * 1024;
+constexpr uint32_t kZBytes = kRows * 16;
 struct Layout {
-    uint32_t tile, w, z, bar, fac, psum, total;
+    uint32_t tile, z, bar, fac, w, total;
 };
-__host__ __device__ constexpr int w_stages(int np, bool gate) { return gate && np == 2 ? 5 : 7; }
-__host__ __device__ constexpr uint32_t z_pitch(int K) { return uint32_t((K / 128 + 7) & ~7) * 2; }   // bytes of a row's zeros
-__host__ __device__ constexpr Layout layout(int np, bool gate, int K) {
+constexpr int kWS = 3;                             // weight stages
+__host__ __device__ constexpr Layout layout(bool gate) {
     Layout l = {};
-    l.tile = kBRing;
-    l.w = l.tile + (gate ? 16384u * np : 0u);
-    l.z = l.w + w_stages(np, gate) * kWBytes;
-    l.bar = l.z + kRows * z_pitch(K);
+    l.tile = kRing;
+    l.z = l.tile + (gate ? 16384u : 0u);          // (128 rows of one term or 64 of two)
+    l.bar = l.z + 3 * kZBytes;
     l.fac = l.bar + 512;
-    l.psum = l.fac + 2 * 2 * 128 * 4;
-    l.total = l.psum + (gate ? 4 * 128 * 4 : 0);
+    l.w = l.fac + 2 * 2 * 128 * 4;
+    l.total = l.w + kWS * kWBytes;
     return l;
 }
-static_assert(layout(1, true, kMoeMaxDim).total <= 227 * 1024 && layout(2, true, kMoeMaxDim).total <= 227 * 1024 &&
-              layout(1, false, kMoeMaxDim).total <= 227 * 1024, "shared memory");
+static_assert(layout(true).total <= kSmem, "shared memory");
+// A stage of the token ring: two groups of `cap` tokens, and their sums.
+__host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 512u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
 
 // Shared-memory matrix descriptor: K-major, 128-byte swizzle, `stride` bytes between blocks of 8 rows.
 __device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t stride) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t((stride >> 4) & 0x3FFFu) << 32) |
            (uint64_t(1) << 46) | (uint64_t(2) << 61);
 }
+// ... no swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
+__device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t further) {
+    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((further >> 4) & 0x3FFFu) << 16) | (uint64_t(128 >> 4) << 32) |
+           (uint64_t(1) << 46);
+}
+// D += A B^T for one K = 16 step, both in shared memory.
+__device__ __forceinline__ void mma_ss(uint32_t taddr, uint64_t ad, uint64_t bd, uint32_t idesc) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(taddr),
+                 "l"(ad), "l"(bd), "r"(idesc)
+                 : "memory");
+}
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
+// silu(x) * up.  bf16 results: the hardware's exponential and reciprocal, each good to 2^-21 or better.
+template <bool FAST>
 __device__ __forceinline__ float silu_mul(float x, float up) {
+    if (FAST) return __fmul_rn(__fdividef(x, __fadd_rn(1.f, __expf(-x))), up);
     return __fmul_rn(__fdiv_rn(x, __fadd_rn(1.f, expf(-x))), up);
 }
-__device__ __forceinline__ void tmem_store(uint32_t taddr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
-    asm volatile("tcgen05.st.sync.aligned.16x256b.x1.b32 [%0], {%1, %2, %3, %4};" ::"r"(taddr), "r"(a), "r"(b), "r"(c), "r"(d)
-                 : "memory");
+// Four steps of 8 columns at once.
+__device__ __forceinline__ void tmem_store4(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x256b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(
+            taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
+        "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
 }
+// Bounded wait; gives up at once when another warp has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err) {
+    if (mbar_try_wait(b, parity)) return true;
+    const long long c0 = clock64();
+    for (uint32_t it = 1; it < (1u << 28); ++it) {
+        if (mbar_try_wait(b, parity)) return true;
+        if (*abort_flag) return false;
+        if (clock64() - c0 > 4000000000ll) break;
+    }
+    set_error(err, KMR_ERR_DEVICE_TIMEOUT);
+    *abort_flag = 1;
+    return false;
+}
 
-// The tensor cores cut a running sum off rather than round it, so a chain of n steps of 16 inputs comes out some n 2^-25 too
-// small (measured: 1040 steps, 2.3e-5).  bf16 results do not show it.  For fp32 (two MMAs a step) the epilogue warps add
-// up chunks of kChunk groups (64 steps: 1.4e-6) in registers, which limits a tile to 64 tokens.
-constexpr int kChunk = 4;
-template <int NP>
-constexpr int kTileTokens = NP == 2 ? 64 : 128;
-__device__ __forceinline__ bool chunk_end(int np, int g) { return np == 2 && g % kChunk == kChunk - 1; }
-
-// A stage of a ring and the parity of its current round.
+// A stage of a ring and how often the ring has come round.
 struct Turn {
     int s = 0;
     uint32_t round = 0;
@@ -315,33 +343,37 @@ struct Turn {
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
+// Roles.  Bulk copies overlap only within one instruction (some 0.33 us each otherwise, whatever their size), so a
+// producer's instruction fetches two groups, a lane per copy.  The unpack warps are two sets of four (one warp per quarter of
+// the tensor memory's lanes), one for each group of a pair: the chain wait - load - convert - store - hand over of one group
+// takes longer than its share of the issue slots, and two of them overlap.
 template <int NP, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int K = GATE ? p.w.H : p.w.I, N = GATE ? 2 * p.w.I : p.w.H, G = K >> 7;
     const int R = N / kRows;                               // row tiles of an expert
-    const Layout L = layout(NP, GATE, K);
-    constexpr int WS = w_stages(NP, GATE);
-    const uint32_t bstage = uint32_t(p.cap) * 256u * NP;
-    const int BS = min(kMaxStages, int(kBRing / bstage));
-    const int ZA = sum_atoms(K), ZK = (K / 64 + 15) / 16;  // atoms and MMA steps of the sums
+    constexpr Layout L = layout(GATE);
+    const uint32_t bstage = stage_bytes(p.cap, NP);
+    const int BS = min(kMaxStages, int(kRing / bstage));
+    const int DB = min(kMaxAcc, 256 / (p.cap * NP));       // accumulators
+    const uint32_t dcols = uint32_t(p.cap) * NP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
-    uint64_t* w_empty = w_full + WS;
-    uint64_t* b_full = w_empty + WS;
+    uint64_t* w_empty = w_full + kWS;
+    uint64_t* b_full = w_empty + kWS;
     uint64_t* b_empty = b_full + kMaxStages;
     uint64_t* a_full = b_empty + kMaxStages;
     uint64_t* a_empty = a_full + kAQ;
     uint64_t* d_full = a_empty + kAQ;
-    uint64_t* d_empty = d_full + 2;
-    uint32_t* tslot = reinterpret_cast<uint32_t*>(d_empty + 2);
+    uint64_t* d_empty = d_full + kMaxAcc;
+    uint32_t* tslot = reinterpret_cast<uint32_t*>(d_empty + kMaxAcc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    static_assert((2 * 7 + 2 * kMaxStages + 2 * kAQ + 4) * 8 + 8 <= 512, "barrier area");
+    static_assert(2 * (kWS + kMaxStages + kAQ + kMaxAcc) * 8 + 8 <= 512, "barrier area");
     const uint32_t sbase = smem_u32(smem);
 
     if (tid == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < WS; ++s) {
+        for (int s = 0; s < kWS; ++s) {
             mbar_init(&w_full[s], 1);
             mbar_init(&w_empty[s], kUnpackWarps);
         }
@@ -353,209 +385,232 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             mbar_init(&a_full[s], kUnpackWarps);
             mbar_init(&a_empty[s], 1);
         }
-        for (int s = 0; s < 2; ++s) {
+        for (int s = 0; s < DB; ++s) {
             mbar_init(&d_full[s], 1);
             mbar_init(&d_empty[s], kEpiWarps);
         }
         fence_mbar_init();
     }
     if (warp == 0) tc_alloc(tslot, 512);
-    for (int i = tid; i < kRows * int(z_pitch(K)) / 4; i += kThr) reinterpret_cast<uint32_t*>(smem + L.z)[i] = 0u;
+    for (int i = tid; i < int(kZBytes) / 4; i += kThr) reinterpret_cast<uint32_t*>(smem + L.z + 2 * kZBytes)[i] = 0u;
+    fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t taddr = *tslot;
     pdl_wait();
     pdl_launch_dependents();
-    auto fail = [&]() { *abort_flag = 1; };
-    // lane 0 waits, the warp follows its verdict
+    // a warp waits as one
     auto warp_wait = [&](uint64_t* b, uint32_t parity) {
-        int ok = 0;
-        if (lane == 0) {
-            ok = !*abort_flag && spin_wait(b, parity, p.err);
-            if (!ok) fail();
-        }
-        return __shfl_sync(kFull, ok, 0) != 0;
+        return __all_sync(kFull, wait_or_abort(b, parity, abort_flag, p.err)) != 0;
     };
-    const int items = *p.ntiles * R;
+    const int items = *p.ntiles * R, step = int(gridDim.x);
     const uint8_t* wsrc = GATE ? p.w.gate_up : p.w.down;
     const uint8_t* bsrc = GATE ? p.xs : p.as;
+    const float* rho = GATE ? p.rho_gate_up : p.rho_down;
     const size_t bb = block_bytes(K, NP);
+    // what the tile of item `it` is (the next item's is always fetched ahead)
+    auto tile_of = [&](int it) { return it < items ? p.tiles[it / R] : make_int4(0, 0, 0, 0); };
     Turn tw, tb;                                           // the producers' own rings (also for draining)
     bool ok = true;
 
     if (warp == 0) {
-        // ---- weights: lanes 0..7 copy a group's eight blocks
+        // ---- weights: lane t < 8 copies two groups of tile t (they are neighbours in memory)
         const uint64_t pol = policy_evict_first();
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-            const int4 tile = p.tiles[it / R];
+        int4 tile = tile_of(blockIdx.x);
+        for (int it = blockIdx.x; it < items && ok; it += step) {
+            const int4 ahead = tile_of(it + step);
             const uint8_t* src = wsrc + (size_t(tile.x) * (N / 16) + (it % R) * 8 + (lane & 7)) * G * kGroupBytes;
-            for (int g = 0; g < G; ++g) {
+            for (int g = 0; g < G; g += 2) {
                 if (tw.waits() && !(ok = warp_wait(&w_empty[tw.s], tw.empty()))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&w_full[tw.s], kWBytes);
+                const uint32_t bytes = uint32_t(min(2, G - g)) * kGroupBytes;
+                if (lane == 0) mbar_arrive_expect_tx(&w_full[tw.s], 8 * bytes);
                 __syncwarp();
                 fence_proxy_async_smem();                  // the unpack warps' reads of the stage come first
                 if (lane < 8)
-                    bulk_g2s_stream(smem + L.w + tw.s * kWBytes + lane * kGroupBytes, src + size_t(g) * kGroupBytes, kGroupBytes,
-                                    &w_full[tw.s], pol);
-                tw.next(WS);
+                    bulk_g2s_stream(smem + L.w + tw.s * kWBytes + lane * bytes, src + size_t(g) * kGroupBytes, bytes, &w_full[tw.s],
+                                    pol);
+                tw.next(kWS);
             }
+            tile = ahead;
         }
     } else if (warp == kTokenWarp) {
-        // ---- staged tokens: one lane per block of 8 rows
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-            const int4 tile = p.tiles[it / R];
+        // ---- staged tokens: a lane copies two groups of a block of 8 rows and term (lanes 0..15) or their sums (16..31)
+        const int pairs = (G + 1) / 2;
+        const int block = NP == 2 && lane < 16 ? lane & 7 : lane & 15, term = NP == 2 ? (lane >> 3) & 1 : 0;
+        int4 tile = tile_of(blockIdx.x);
+        for (int it = blockIdx.x; it < items && ok; it += step) {
+            const int4 ahead = tile_of(it + step);
             const int nb = tile.z >> 3;
-            const uint8_t* src = bsrc + size_t((tile.y >> 3) + lane) * bb;
-            auto copy = [&](size_t from, uint32_t bytes) {
-                if (tb.waits() && !warp_wait(&b_empty[tb.s], tb.empty())) return false;
-                if (lane == 0) mbar_arrive_expect_tx(&b_full[tb.s], bytes * nb);
+            const uint8_t* src = bsrc + size_t((tile.y >> 3) + block) * bb + (lane < 16 ? size_t(term) * G * 2048 : sums_at(K, NP));
+            for (int u = 0; u < pairs; ++u) {
+                if (tb.waits() && !(ok = warp_wait(&b_empty[tb.s], tb.empty()))) break;
+                const uint32_t bytes = uint32_t(min(2, G - 2 * u)) * 2048u;
+                if (lane == 0) mbar_arrive_expect_tx(&b_full[tb.s], (bytes * NP + 128u) * nb);
                 __syncwarp();
-                if (lane < nb) bulk_g2s(smem + size_t(tb.s) * bstage + lane * bytes, src + from, bytes, &b_full[tb.s]);
+                if (block < nb) {
+                    uint8_t* to = smem + size_t(tb.s) * bstage;
+                    if (lane < 16) to += (term * nb + block) * bytes;
+                    else to += dcols * 512u + block * 128u;
+                    bulk_g2s(to, src + size_t(u) * (lane < 16 ? 4096 : 128), lane < 16 ? bytes : 128u, &b_full[tb.s]);
+                }
                 tb.next(BS);
-                return true;
-            };
-            for (int g = 0; g < G && ok; ++g) ok = copy(size_t(g) * NP * 2048, NP * 2048);
-            for (int h = 0; h < 2 / NP && ok; ++h) ok = copy(size_t(G) * NP * 2048 + h * ZA * 1024, NP * ZA * 1024);
+            }
+            tile = ahead;
         }
     } else if (warp == 1) {
-        // ---- MMA issue
-        if (lane == 0) {
+        // ---- MMA issue, by one elected thread (elect.sync: with `lane == 0` the compiler does not know that the operands are
+        // uniform, and an MMA takes 55 cycles to issue instead of 6)
+        if (elect_one()) {
             Turn ta, tt, td;
-            for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-                const uint32_t idesc = tc_idesc(kRows, p.tiles[it / R].z);
-                bool begun = false;                        // the accumulator holds something of this chunk
-                for (int g = 0; g <= G && ok; ++g) {
-                    if (!begun && td.waits()) ok = spin_wait(&d_empty[td.s], td.empty(), p.err);
-                    ok = ok && !*abort_flag && spin_wait(&a_full[ta.s], ta.full(), p.err);
-                    const uint32_t acc = taddr + td.s * 128;
-                    const int steps = g < G ? 8 : ZK;
-                    const uint32_t a = taddr + 256 + ta.s * 64;
-                    // the sums' first terms and remainders fill one stage (NP = 2) or two
-                    for (int part = 0; part < (g < G ? 1 : 2 / NP) && ok; ++part) {
-                        ok = spin_wait(&b_full[tt.s], tt.full(), p.err);
-                        if (!ok) break;
+            int4 tile = tile_of(blockIdx.x);
+            auto wait = [&](uint64_t* b, uint32_t parity) { return wait_or_abort(b, parity, abort_flag, p.err); };
+            for (int it = blockIdx.x; it < items && ok; it += step) {
+                const int4 ahead = tile_of(it + step);
+                const uint32_t idesc = tc_idesc(kRows, NP * tile.z), sums = tc_idesc(kRows, tile.z);
+                uint32_t begun = 0;                        // the accumulator holds something
+                for (int g = 0; g < G && ok; g += 2) {
+                    const int both = min(2, G - g);
+                    ok = wait(&b_full[tt.s], tt.full()) && wait(&a_full[ta.s], ta.full());
+                    for (int h = 0; h < both && ok; ++h) {
+                        if (!begun && td.waits() && !(ok = wait(&d_empty[td.s], td.empty()))) break;
                         tc_fence_after();
-                        const uint32_t b = sbase + tt.s * bstage;
-                        const uint32_t term = g < G ? 2048u : uint32_t(ZA) * 1024u;
+                        const uint32_t b = sbase + tt.s * bstage, a = taddr + 256 + ta.s * 128 + h * 64, acc = taddr + td.s * dcols;
+                        const uint64_t desc = swizzled_desc(b + h * 2048u, both * 2048u);
 #pragma unroll
-                        for (int q = 0; q < NP; ++q)
-                            for (int ks = 0; ks < steps; ++ks)
-                                tc_mma_ta(acc, a + ks * 8, swizzled_desc(b + q * term + (ks >> 2) * 1024 + (ks & 3) * 32, NP * term),
-                                          idesc, (begun || ks > 0 || q > 0) ? 1u : 0u);
-                        begun = true;
-                        tc_commit(&b_empty[tt.s]);
-                        tt.next(BS);
+                        for (int ks = 0; ks < 8; ++ks)
+                            tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
+                        if (h == both - 1) {               // the pair's zero points (to the first terms' columns)
+                            const uint32_t z = sbase + L.z, zeros = z + 2 * kZBytes, x = b + dcols * 512u;
+                            mma_ss(acc, plain_desc(z + ta.s * kZBytes, (2 - ta.s) * kZBytes), plain_desc(x, zeros - x), sums);
+                        }
+                        begun = 1;
+                        if (NP == 2 || g + h + 1 == G) {
+                            tc_commit(&d_full[td.s]);
+                            td.next(DB);
+                            begun = 0;
+                        }
                     }
                     tc_commit(&a_empty[ta.s]);
+                    tc_commit(&b_empty[tt.s]);
                     ta.next(kAQ);
-                    if (g == G || (chunk_end(NP, g) && g + 1 < G)) {
-                        tc_commit(&d_full[td.s]);
-                        td.next(2);
-                        begun = false;
-                    }
+                    tt.next(BS);
                 }
-                if (!ok) fail();
+                tile = ahead;
             }
         }
     } else if (warp < kTokenWarp) {
-        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, half of a group's k-steps
-        const int lq = warp & 3, kj = (warp - 2) >> 2, g8 = lane >> 2, t = lane & 3;
-        const float* rho = GATE ? p.rho_gate_up : p.rho_down;
-        uint8_t* zb = smem + L.z + (32 * lq + g8) * z_pitch(K);
+        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, one group of each pair
+        const int lq = warp & 3, set = (warp - 2) >> 2, g8 = lane >> 2;
         const __half2 m8 = __float2half2_rn(-1032.f), c16 = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
-        Turn ta, tt;
-        for (int it = blockIdx.x; it < items && ok; it += gridDim.x) {
-            const int4 tile = p.tiles[it / R];
-            float rr[4];                                   // of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter
+        // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero point this lane writes)
+        auto factors = [&](int it, const int4& tile, float (&to)[5]) {
+            const float* at = rho + size_t(tile.x) * N + (it % R) * kRows + 32 * lq;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) rr[i] = rho[size_t(tile.x) * N + (it % R) * kRows + 32 * lq + g8 + 8 * i];
-            for (int g = 0; g < G; ++g) {
+            for (int i = 0; i < 4; ++i) to[i] = at[g8 + 8 * i];
+            to[4] = at[lane];
+        };
+        uint8_t* zto = smem + L.z + (4 * lq + (lane >> 3)) * 128 + (lane & 7) * 16 + set * 8;
+        Turn tt, ta;
+        float rr[5] = {1.f, 1.f, 1.f, 1.f, 1.f}, rnext[5] = {1.f, 1.f, 1.f, 1.f, 1.f};
+        int4 ahead = tile_of(blockIdx.x);
+        if (int(blockIdx.x) < items) factors(blockIdx.x, ahead, rnext);
+        for (int it = blockIdx.x; it < items && ok; it += step) {
+#pragma unroll
+            for (int i = 0; i < 5; ++i) rr[i] = rnext[i];
+            ahead = tile_of(it + step);
+            for (int g0 = 0; g0 < G && ok; g0 += 2) {
+                const int both = min(2, G - g0), g = g0 + set;
+                if (g0 + 2 >= G && it + step < items) factors(it + step, ahead, rnext);
                 if (!(ok = warp_wait(&w_full[tt.s], tt.full()))) break;
-                if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
-                tc_fence_after();
-                const uint8_t* wst = smem + L.w + tt.s * kWBytes + (2 * lq) * kGroupBytes;
+                const uint8_t* wst = smem + L.w + tt.s * kWBytes + (2 * lq * both + set) * kGroupBytes;
+                uint32_t sz[4], zrow = 0u;
+                uint4 wq[4];
+                if (g < G) {
+                    zrow = *reinterpret_cast<const uint32_t*>(wst + (lane >> 4) * both * kGroupBytes + 1024 + (lane & 15) * 4);
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint8_t* blk = wst + h * kGroupBytes;
-                    const uint32_t sz0 = *reinterpret_cast<const uint32_t*>(blk + 1024 + g8 * 4);
-                    const uint32_t sz1 = *reinterpret_cast<const uint32_t*>(blk + 1024 + (g8 + 8) * 4);
-                    const __half2 s0 = __float2half2_rn(__fmul_rn(bf16_lo(sz0), rr[2 * h]));
-                    const __half2 s1 = __float2half2_rn(__fmul_rn(bf16_lo(sz1), rr[2 * h + 1]));
-                    if (kj == 0 && t == (g & 3)) {
-                        *reinterpret_cast<uint16_t*>(zb + (16 * h) * z_pitch(K) + g * 2) = uint16_t(sz0 >> 16);
-                        *reinterpret_cast<uint16_t*>(zb + (16 * h + 8) * z_pitch(K) + g * 2) = uint16_t(sz1 >> 16);
-                    }
-                    const uint32_t acol = taddr + 256 + ta.s * 64 + (uint32_t(32 * lq + 16 * h) << 16);
-                    const uint4 wq = *reinterpret_cast<const uint4*>(blk + kj * 512 + lane * 16);
-                    const uint32_t w4[4] = {wq.x, wq.y, wq.z, wq.w};
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t w = w4[k], wh = w >> 8;
-                        const __half2 qa = __hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), m8);
-                        const __half2 qb = __hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), c16, m72);
-                        const __half2 qc = __hadd2(h2(and_or(wh, 0x000F000Fu, 0x64006400u)), m8);
-                        const __half2 qd = __hfma2(h2(and_or(wh, 0x00F000F0u, 0x64006400u)), c16, m72);
-                        tmem_store(acol + (4 * kj + k) * 8, u2(__hmul2(qa, s0)), u2(__hmul2(qc, s0)), u2(__hmul2(qb, s1)),
-                                   u2(__hmul2(qd, s1)));
+                    for (int h = 0; h < 2; ++h) {
+                        const uint8_t* blk = wst + h * both * kGroupBytes;
+                        sz[2 * h] = *reinterpret_cast<const uint32_t*>(blk + 1024 + g8 * 4);
+                        sz[2 * h + 1] = *reinterpret_cast<const uint32_t*>(blk + 1024 + (g8 + 8) * 4);
+                        wq[2 * h] = *reinterpret_cast<const uint4*>(blk + lane * 16);
+                        wq[2 * h + 1] = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
                     }
                 }
+                if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
+                const uint32_t z2 = u2(__float2half2_rn(__fmul_rn(bf16_hi(zrow), 64.f * rr[4])));
+                *reinterpret_cast<uint2*>(zto + ta.s * kZBytes) = make_uint2(z2, z2);
+                fence_proxy_async_smem();                  // (before the hand-over: the MMA reads them through the async proxy)
+                if (g < G) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const __half2 s0 = __float2half2_rn(__fmul_rn(bf16_lo(sz[2 * h]), rr[2 * h]));
+                        const __half2 s1 = __float2half2_rn(__fmul_rn(bf16_lo(sz[2 * h + 1]), rr[2 * h + 1]));
+                        const uint32_t acol = taddr + 256 + ta.s * 128 + set * 64 + (uint32_t(32 * lq + 16 * h) << 16);
+#pragma unroll
+                        for (int kj = 0; kj < 2; ++kj) {
+                            const uint4 q4 = wq[2 * h + kj];
+                            const uint32_t w4[4] = {q4.x, q4.y, q4.z, q4.w};
+                            uint32_t v[16];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const uint32_t w = w4[k], wh = w >> 8;
+                                const __half2 qa = __hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), m8);
+                                const __half2 qb = __hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), c16, m72);
+                                const __half2 qc = __hadd2(h2(and_or(wh, 0x000F000Fu, 0x64006400u)), m8);
+                                const __half2 qd = __hfma2(h2(and_or(wh, 0x00F000F0u, 0x64006400u)), c16, m72);
+                                v[4 * k] = u2(__hmul2(qa, s0));
+                                v[4 * k + 1] = u2(__hmul2(qc, s0));
+                                v[4 * k + 2] = u2(__hmul2(qb, s1));
+                                v[4 * k + 3] = u2(__hmul2(qd, s1));
+                            }
+                            tmem_store4(acol + kj * 32, v);
+                        }
+                    }
+                }
+                if (lane == 0) mbar_arrive(&w_empty[tt.s]);    // (all lanes' loads have been used by the stores above)
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&a_full[ta.s]);
-                    mbar_arrive(&w_empty[tt.s]);
-                }
-                tt.next(WS);
+                if (lane == 0) mbar_arrive(&a_full[ta.s]);
+                tt.next(kWS);
                 ta.next(kAQ);
             }
-            if (!ok) break;
-            // the zero points: word column c of a step is group 8 step + c, twice
-            if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
-            tc_fence_after();
-            if (kj == 0) {
-                __syncwarp();
-                auto dup = [&](uint32_t bits, float r) { return u2(__float2half2_rn(__fmul_rn(__uint_as_float(bits << 16), 64.f * r))); };
-                for (int ks = 0; ks < ZK; ++ks) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t z0 = *reinterpret_cast<const uint32_t*>(zb + (16 * h) * z_pitch(K) + (8 * ks + 2 * t) * 2);
-                        const uint32_t z1 = *reinterpret_cast<const uint32_t*>(zb + (16 * h + 8) * z_pitch(K) + (8 * ks + 2 * t) * 2);
-                        tmem_store(taddr + 256 + ta.s * 64 + (uint32_t(32 * lq + 16 * h) << 16) + ks * 8, dup(z0 & 0xFFFFu, rr[2 * h]),
-                                   dup(z0 >> 16, rr[2 * h]), dup(z1 & 0xFFFFu, rr[2 * h + 1]), dup(z1 >> 16, rr[2 * h + 1]));
-                    }
-                }
-                tc_wait_st();
-                __syncwarp();                              // (the zeros are read before the next tile's come)
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&a_full[ta.s]);
-            ta.next(kAQ);
         }
     } else if (warp >= kEpiWarp) {
         // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its weight rows), all tokens
         const int q = warp & 3, et = tid - kEpiWarp * 32;
         float* fac = reinterpret_cast<float*>(smem + L.fac);       // [2][2][128]
-        float* psum = reinterpret_cast<float*>(smem + L.psum);     // [4][128]
         uint8_t* tbuf = smem + L.tile;
-        const float* rho = GATE ? p.rho_gate_up : p.rho_down;
         Turn td;
         int turn = 0;
-        for (int it = blockIdx.x; it < items; it += gridDim.x, turn ^= 1) {
-            const int4 tile = p.tiles[it / R];
+        int4 tile = tile_of(blockIdx.x), ahead;
+        float f0 = 0.f, f1 = 0.f, irho = 1.f;
+        auto factors = [&](int it, const int4& tl) {
+            if (et < tl.z) {
+                f0 = GATE ? p.isx[tl.y + et] : p.sact[tl.y + et];
+                if (GATE) f1 = p.sact[tl.y + et];
+            }
+            irho = rho[size_t(tl.x) * N + (it % R) * kRows + 32 * q + lane];
+        };
+        if (int(blockIdx.x) < items) factors(blockIdx.x, tile);
+        for (int it = blockIdx.x; it < items; it += step, turn ^= 1) {
             const int r = it % R, n = tile.z;
             float* f = fac + turn * 256;
             if (et < n) {
-                f[et] = GATE ? p.isx[tile.y + et] : inverse_pow2(p.sact[tile.y + et]);
-                if (GATE) f[128 + et] = p.sact[tile.y + et];
+                f[et] = GATE ? f0 : inverse_pow2(f0);
+                if (GATE) f[128 + et] = f1;
             }
-            const float irho = inverse_pow2(rho[size_t(tile.x) * N + r * kRows + 32 * q + lane]);
-            if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-            epilogue_bar();                                // factors in place, the previous tile's copies have read the buffer
+            const float ir = inverse_pow2(irho);
+            ahead = tile_of(it + step);
+            // factors in place, the previous tile's copies have read the buffer
+            auto ready = [&]() {
+                if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                epilogue_bar();
+            };
             // tokens c0 .. c0 + 15 of this lane's row
             auto finish = [&](int c0, const float (&v)[16]) {
                 if (GATE) {
@@ -565,39 +620,33 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     const int at = 2 * (i16 & 7) - (i16 & 1) + ((i16 >> 3) << 1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
-                        const float xa = __fmul_rn(v[j], __fmul_rn(irho, f[c0 + j]));
-                        const float xb = __fmul_rn(v[j + 1], __fmul_rn(irho, f[c0 + j + 1]));
+                        const float xa = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                        const float xb = __fmul_rn(v[j + 1], __fmul_rn(ir, f[c0 + j + 1]));
                         const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
                         const int c = c0 + j + (lo ? 0 : 1);
-                        float a = silu_mul(lo ? xa : other, lo ? other : xb);
+                        float a = silu_mul<NP == 1>(lo ? xa : other, lo ? other : xb);
                         a = __fmul_rn(a, f[128 + c]);
                         uint8_t* to = tbuf + size_t(c >> 3) * NP * 1024 + piece(c & 7, 2 * q + (at >> 3)) + (at & 7) * 2;
-                        float X = 0.f;
 #pragma unroll
                         for (int s = 0; s < NP; ++s) {
                             const __half hv = __float2half_rn(a);
-                            const float hf = __half2float(hv);
                             *reinterpret_cast<__half*>(to + s * 1024) = hv;
-                            X = __fadd_rn(X, hf);
-                            a = __fsub_rn(a, hf);
+                            a = __fsub_rn(a, __half2float(hv));
                         }
-                        X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 1));
-                        X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 2));
-                        X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 4));
-                        X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 16));
-                        if ((lane & 23) == 0) psum[q * 128 + c] = X;           // lanes 0 and 8
                     }
                 } else {
                     float* out = p.out + size_t(tile.y + c0) * N + r * kRows + 32 * q + lane;
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(irho, f[c0 + j]));
+                    for (int j = 0; j < 16; ++j) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
                 }
             };
             // (after a timeout nothing is stored any more, but the barriers are kept)
             if constexpr (NP == 1) {
+                ready();
                 ok = ok && warp_wait(&d_full[td.s], td.full());
+                if (it + step < items) factors(it + step, ahead);
                 tc_fence_after();
-                const uint32_t acc = taddr + td.s * 128 + (uint32_t(32 * q) << 16);
+                const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
                 for (int c0 = 0; c0 < n && ok; c0 += 16) {
                     float v[16];
                     tc_ld16(acc + uint32_t(c0), v);
@@ -606,30 +655,37 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&d_empty[td.s]);
-                td.next(2);
+                td.next(DB);
             } else {
+                // per group: the first terms' columns and the remainders', n further on
                 float sum[kTileTokens<NP> / 16][16];
 #pragma unroll
                 for (int i = 0; i < kTileTokens<NP> / 16; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
-                for (int g = 0; g < G; g += kChunk) {
+                for (int g = 0; g < G; ++g) {
                     ok = ok && warp_wait(&d_full[td.s], td.full());
                     tc_fence_after();
-                    const uint32_t acc = taddr + td.s * 128 + (uint32_t(32 * q) << 16);
+                    const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
 #pragma unroll
                     for (int i = 0; i < kTileTokens<NP> / 16; ++i) {
                         if (i * 16 >= n || !ok) continue;
-                        float v[16];
-                        tc_ld16(acc + uint32_t(i * 16), v);
+                        uint32_t v[16], w[16];
+                        tc_ld16_issue(acc + uint32_t(i * 16), v);
+                        tc_ld16_issue(acc + uint32_t(n + i * 16), w);
+                        tc_wait_ld16(v);
+                        tc_wait_ld16(w);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
+                        for (int j = 0; j < 16; ++j)
+                            sum[i][j] = __fadd_rn(sum[i][j], __fadd_rn(__uint_as_float(v[j]), __uint_as_float(w[j])));
                     }
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&d_empty[td.s]);
-                    td.next(2);
+                    td.next(DB);
                 }
+                ready();
+                if (it + step < items) factors(it + step, ahead);
 #pragma unroll
                 for (int i = 0; i < kTileTokens<NP> / 16; ++i)
                     if (i * 16 < n && ok) finish(i * 16, sum[i]);
@@ -637,37 +693,47 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             if (GATE) {
                 fence_proxy_async_smem();
                 epilogue_bar();
-                const int GA = p.w.I >> 7;                 // groups of the activations; this tile is half of group r / 2
                 const size_t ab = block_bytes(p.w.I, NP);
                 uint8_t* blk = p.as + size_t(tile.y >> 3) * ab;
                 if (ok && warp == kEpiWarp) {
                     if (lane < (n >> 3)) {
 #pragma unroll
                         for (int s = 0; s < NP; ++s)
-                            bulk_s2g(blk + lane * ab + (size_t(r >> 1) * NP + s) * 2048 + (r & 1) * 1024,
+                            bulk_s2g(blk + lane * ab + (size_t(s) * (p.w.I >> 6) + r) * 1024,
                                      tbuf + (size_t(lane) * NP + s) * 1024, 1024);
                     }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
                 if (ok && et < n) {
-                    float X = psum[et];
+                    // the sum of the tile's 64 activations as staged, in their order
+                    float X = 0.f;
 #pragma unroll
-                    for (int w = 1; w < 4; ++w) X = __fadd_rn(X, psum[w * 128 + et]);
-                    uint8_t* sums = blk + size_t(et >> 3) * ab + size_t(GA) * NP * 2048;
-                    put_sum(sums, p.w.I, et & 7, r, X);
-                    if (r == 0)
-                        for (int i = 0; i < 16; ++i) clear_sums(sums, p.w.I, et & 7, i);
+                    for (int s = 0; s < NP; ++s)
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            const uint4 h = *reinterpret_cast<const uint4*>(tbuf + (size_t(et >> 3) * NP + s) * 1024 + piece(et & 7, c));
+                            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                                X = __fadd_rn(X, __fadd_rn(v.x, v.y));
+                            }
+                        }
+                    uint8_t* sums = blk + size_t(et >> 3) * ab + sums_at(p.w.I, NP);
+                    put_sum(sums, et & 7, r, X);
+                    if (r == 0) clear_sums(sums, p.w.I, et & 7);
                 }
             }
+            tile = ahead;
         }
         if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
-    if (*abort_flag && lane == 0) {
+    if (*abort_flag) {
         // the copies still in flight: the latest round of every stage
-        if (warp == 0)
-            for (int s = 0; s < WS; ++s)
+        if (warp == 0 && lane == 0)
+            for (int s = 0; s < kWS; ++s)
                 if (tw.round > 0 || s < tw.s) mbar_wait(&w_full[s], (s < tw.s ? tw.round : tw.round - 1) & 1u, p.err, 50000000ull);
-        if (warp == kTokenWarp)
+        if (warp == kTokenWarp && lane == 0)
             for (int s = 0; s < BS; ++s)
                 if (tb.round > 0 || s < tb.s) mbar_wait(&b_full[s], (s < tb.s ? tb.round : tb.round - 1) & 1u, p.err, 50000000ull);
     }
@@ -754,7 +820,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     const void* stage = bf16 ? (const void*)moe_stage_kernel<uint16_t, 1> : (const void*)moe_stage_kernel<float, 2>;
     if ((e = launch_dependent(stage, dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
-        const size_t smem = layout(bf16 ? 1 : 2, gate, gate ? p.w.H : p.w.I).total;
+        const size_t smem = layout(gate).total;
         if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<uint16_t> : (const void*)moe_combine_kernel<float>;
@@ -773,8 +839,7 @@ cudaError_t moe_tc_set_attributes() {
     cudaError_t e;
     for (int b = 0; b < 2; ++b)
         for (int gate = 0; gate < 2; ++gate) {
-            e = cudaFuncSetAttribute(product_fn(b != 0, gate != 0), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     int(layout(b ? 1 : 2, gate != 0, kMoeMaxDim).total));
+            e = cudaFuncSetAttribute(product_fn(b != 0, gate != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
             if (e != cudaSuccess) return e;
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, (const void*)moe_stage_kernel<uint16_t, 1>,

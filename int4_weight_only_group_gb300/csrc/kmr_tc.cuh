@@ -45,6 +45,12 @@ __device__ __forceinline__ void tc_mma_ta(uint32_t taddr, uint32_t a_taddr, uint
         "r"(a_taddr), "l"(bd), "r"(idesc), "r"(acc)
         : "memory");
 }
+// One lane of a converged warp, in a form that tells the compiler so.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+    return p != 0;
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tc_commit(uint64_t* bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
