@@ -60,6 +60,7 @@ struct MoeTcParams {
     int32_t* pos;                            // [T][k]: the place's position, or -1
     float* isx;                              // [P] 1 / scale of the position's inputs
     float* sact;                             // [P] scale of its activations
+    size_t blocks;                           // P / 8
     uint8_t* xs;                             // staged inputs
     uint8_t* as;                             // staged activations
     float* out;                              // [P][H]
@@ -67,9 +68,9 @@ struct MoeTcParams {
     int resid;
     int* err;
 };
-// Byte offsets into the workspace (the tile count comes first).
+// Byte offsets into the workspace (the tile count comes first), and the blocks of 8 positions.
 struct MoeTcSizes {
-    size_t tiles, pos, isx, sact, xs, as, out, total;
+    size_t tiles, pos, isx, sact, xs, as, out, total, blocks;
 };
 int moe_tc_cap(long long places, int E, bool bf16);
 MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k);

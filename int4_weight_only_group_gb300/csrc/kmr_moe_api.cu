@@ -131,6 +131,7 @@ extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, con
     p.pos = reinterpret_cast<int32_t*>(ws + z.pos);
     p.isx = reinterpret_cast<float*>(ws + z.isx);
     p.sact = reinterpret_cast<float*>(ws + z.sact);
+    p.blocks = z.blocks;
     p.xs = ws + z.xs;
     p.as = ws + z.as;
     p.out = reinterpret_cast<float*>(ws + z.out);

@@ -9,8 +9,11 @@
 //   combine  y[t] = sum_j weights[t, j] * row of place (t, j), in the order of the places: no atomics on values
 //
 // The product, D[row][token] = sum_k w[row][k] x[token][k], w = (q - 8) s + z:
-//   * A = (q - 8) s rho: a 4-bit integer times a bf16 scale has 11 significant bits, so fp16 holds it exactly once a power of two
-//     rho per row (laid out once, moe_factors_kernel) has brought the row's scales into fp16's range.
+//   * A = (q - 8) s rho 2^-24: a 4-bit integer times a bf16 scale has 11 significant bits, so fp16 holds it exactly once a power of
+//     two rho per row (laid out once, moe_factors_kernel) has brought the row's scales into its range (groups whose scale is below
+//     2^-7 of the row's largest lose bits below 2^-20 of the row's largest weight).  A nibble under a zero mantissa is the
+//     fp16 number q 2^-24 as it stands, so a weight is one AND and half an HFMA2: q 2^-24 * (s rho) - 8 s rho 2^-24.  (With 1024
+//     + q, an addition and a multiplication the half-rate fp16 pipe is the bound.)
 //   * the zero points' share sum_g z_g X_g, X_g = sum of the group's inputs, goes through the same accumulator as one more MMA for
 //     every two groups: z rho 2^6 against X 2^-6 for every 64 inputs, X in two fp16 terms.
 //   * B = x sigma (a power of two per row): exact for bf16 inputs, two terms (the fp16 rounding and what it left, two
@@ -46,7 +49,7 @@ __device__ __forceinline__ int above(float v) { return int(__float_as_uint(v) >>
 __device__ __forceinline__ float inverse_pow2(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
 // ------------------------------------------------------------------ weights, once
-// Row factors rho (a power of two that brings max(8 |s|, 64 |z|) of the row to [2^13, 2^14)) and the largest row norm bound of
+// Row factors rho (a power of two that brings max(|s|, 2^-18 |z|) of the row to [2^13, 2^14)) and the largest row norm bound of
 // each expert's gate and up rows: |w|^2 <= sum over groups of 128 max(|z - 8 s|, |z + 7 s|)^2.
 __global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rho, float* norms) {
     const int row = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
@@ -56,7 +59,7 @@ __global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rh
     for (int g = 0; g < G; ++g) {
         const uint32_t sz = *reinterpret_cast<const uint32_t*>(at + size_t(g) * kGroupBytes);
         const float s = bf16_lo(sz), z = bf16_hi(sz);
-        m = fmaxf(m, fmaxf(8.f * fabsf(s), 64.f * fabsf(z)));
+        m = fmaxf(m, fmaxf(fabsf(s), 0x1p-18f * fabsf(z)));
         const float far = fmaxf(fabsf(__fmaf_rn(-8.f, s, z)), fabsf(__fmaf_rn(7.f, s, z)));
         n2 = __fmaf_rn(128.f * far, far, n2);
     }
@@ -123,24 +126,31 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
 }
 
 // ------------------------------------------------------------------ operand layout
-// Staged rows: blocks of 8 rows; within one, for each of the NP terms every group of 128 inputs as 2 atoms of [8 rows][64 inputs]
-// fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte swizzle), then for every pair of groups the
-// sums of their four 64 inputs, [8 rows][8]: per group the first terms of its two sums and their remainders.
+// Staged rows, `blocks` blocks of 8: for every pair of groups of 128 inputs and each of the NP terms all the blocks side by side,
+// each 4 atoms of [8 rows][64 inputs] fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte
+// swizzle), so that a tile's share of a pair is one run of memory.  Behind them, again by pairs, the sums of the four 64 inputs,
+// [8 rows][8]: per group the first terms of its two sums and their remainders.  (The second half of an odd last pair is
+// not written and not used, but its sums are zero.)
 // Input k of 16 sits at 2 (k % 8) - k % 2 + 2 (k / 8) (the order of A's columns in tensor memory).
-__host__ __device__ constexpr size_t sums_at(int K, int np) { return size_t(K / 128) * np * 2048; }
-__host__ __device__ constexpr size_t block_bytes(int K, int np) { return sums_at(K, np) + size_t(K / 128 + 1) / 2 * 128; }
+__host__ __device__ constexpr int pairs_of(int K) { return (K / 128 + 1) / 2; }
+__host__ __device__ constexpr size_t staged_bytes(int K, int np, size_t blocks) { return pairs_of(K) * blocks * (np * 4096 + 128); }
+__device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks, int block) {     // of 64 inputs number h
+    return ((size_t(h >> 2) * np + term) * blocks + block) * 4096 + (h & 3) * 1024;
+}
+__device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return pairs_of(K) * blocks * size_t(np) * 4096; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
-// Sum number h (of 64 inputs) of a row: its two terms.  `sums` are the block's.
-__device__ __forceinline__ void put_sum(uint8_t* sums, int row, int h, float X) {
+// Sum number h (of 64 inputs) of a row: its two terms.  `sums` is where the sums begin.
+__device__ __forceinline__ void put_sum(uint8_t* sums, size_t blocks, int at, int h, float X) {
     const float x = X * 0.015625f;
     const __half hi = __float2half_rn(x);
-    __half* at = reinterpret_cast<__half*>(sums + (h >> 2) * 128 + row * 16) + ((h >> 1) & 1) * 4 + (h & 1);
-    at[0] = hi;
-    at[2] = __float2half_rn(__fsub_rn(x, __half2float(hi)));
+    __half* to = reinterpret_cast<__half*>(sums + (size_t(h >> 2) * blocks + (at >> 3)) * 128 + (at & 7) * 16) + ((h >> 1) & 1) * 4 + (h & 1);
+    to[0] = hi;
+    to[2] = __float2half_rn(__fsub_rn(x, __half2float(hi)));
 }
 // An odd number of groups leaves half of the last pair's sums.
-__device__ __forceinline__ void clear_sums(uint8_t* sums, int K, int row) {
-    if ((K >> 7) & 1) *reinterpret_cast<uint2*>(sums + (K >> 8) * 128 + row * 16 + 8) = make_uint2(0u, 0u);
+__device__ __forceinline__ void clear_sums(uint8_t* sums, size_t blocks, int K, int at) {
+    if ((K >> 7) & 1)
+        *reinterpret_cast<uint2*>(sums + (size_t(K >> 8) * blocks + (at >> 3)) * 128 + (at & 7) * 16 + 8) = make_uint2(0u, 0u);
 }
 
 // ------------------------------------------------------------------ stage
@@ -189,7 +199,8 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
     float sig, isg;
     pow2_scale(__float_as_uint(m), sig, isg);
     float ss = 0.f;
-    const size_t bb = block_bytes(K, NP);
+    const size_t blocks = p.blocks;
+    uint8_t* sums = p.xs + sums_at(K, NP, blocks);
     auto h2u = [](__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -220,17 +231,16 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
         for (int o = 1; o < 16; o <<= 1) X = __fadd_rn(X, __shfl_xor_sync(kFull, X, o));
         for (int j = 0; j < n; ++j) {
             const int at = pos[j], row = at & 7;
-            uint8_t* blk = p.xs + size_t(at >> 3) * bb;
-            uint8_t* to = blk + size_t(k >> 6) * 1024 + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
+            uint8_t* to = p.xs + atom_at(k >> 6, 0, NP, blocks, at >> 3) + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + size_t(q) * K * 16) = out[q];
-            if ((lane & 15) == 0) put_sum(blk + sums_at(K, NP), row, k >> 6, X);
+            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 4096) = out[q];
+            if ((lane & 15) == 0) put_sum(sums, blocks, at, k >> 6, X);
         }
     }
     ss = warp_sum(ss);
     if (lane == 0) red[1][warp] = ss;
     __syncthreads();
-    if (tid < n) clear_sums(p.xs + size_t(pos[tid] >> 3) * bb + sums_at(K, NP), K, pos[tid] & 7);
+    if (tid < n) clear_sums(sums, blocks, K, pos[tid]);
     if (tid < p.k) {
         const int at = p.pos[size_t(t) * p.k + tid];
         if (at < 0) return;
@@ -343,8 +353,7 @@ struct Turn {
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
-// Roles.  Bulk copies overlap only within one instruction (some 0.33 us each otherwise, whatever their size), so a
-// producer's instruction fetches two groups, a lane per copy.  The unpack warps are two sets of four (one warp per quarter of
+// Roles.  Groups are handed over in pairs.  The unpack warps are two sets of four (one warp per quarter of
 // the tensor memory's lanes), one for each group of a pair: the chain wait - load - convert - store - hand over of one group
 // takes longer than its share of the issue slots, and two of them overlap.
 template <int NP, bool GATE>
@@ -408,55 +417,68 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const uint8_t* wsrc = GATE ? p.w.gate_up : p.w.down;
     const uint8_t* bsrc = GATE ? p.xs : p.as;
     const float* rho = GATE ? p.rho_gate_up : p.rho_down;
-    const size_t bb = block_bytes(K, NP);
     // what the tile of item `it` is (the next item's is always fetched ahead)
     auto tile_of = [&](int it) { return it < items ? p.tiles[it / R] : make_int4(0, 0, 0, 0); };
-    Turn tw, tb;                                           // the producers' own rings (also for draining)
+    Turn tw, tb;                                           // the producers' own rings
     bool ok = true;
+    // after a timeout: the copies still in flight, the latest round of every stage
+    auto drain = [&](uint64_t* full, int stages, const Turn& t) {
+        if (!*abort_flag) return;
+        for (int s = 0; s < stages; ++s)
+            if (t.round > 0 || s < t.s) mbar_wait(&full[s], (s < t.s ? t.round : t.round - 1) & 1u, p.err, 50000000ull);
+    };
+
+    auto one_wait = [&](uint64_t* b, uint32_t parity) { return wait_or_abort(b, parity, abort_flag, p.err); };
 
     if (warp == 0) {
-        // ---- weights: lane t < 8 copies two groups of tile t (they are neighbours in memory)
-        const uint64_t pol = policy_evict_first();
-        int4 tile = tile_of(blockIdx.x);
-        for (int it = blockIdx.x; it < items && ok; it += step) {
-            const int4 ahead = tile_of(it + step);
-            const uint8_t* src = wsrc + (size_t(tile.x) * (N / 16) + (it % R) * 8 + (lane & 7)) * G * kGroupBytes;
-            for (int g = 0; g < G; g += 2) {
-                if (tw.waits() && !(ok = warp_wait(&w_empty[tw.s], tw.empty()))) break;
-                const uint32_t bytes = uint32_t(min(2, G - g)) * kGroupBytes;
-                if (lane == 0) mbar_arrive_expect_tx(&w_full[tw.s], 8 * bytes);
-                __syncwarp();
-                fence_proxy_async_smem();                  // the unpack warps' reads of the stage come first
-                if (lane < 8)
-                    bulk_g2s_stream(smem + L.w + tw.s * kWBytes + lane * bytes, src + size_t(g) * kGroupBytes, bytes, &w_full[tw.s],
-                                    pol);
-                tw.next(kWS);
+        // ---- weights: two groups of each of the eight tiles (they are neighbours in memory)
+        if (elect_one()) {
+            const uint64_t pol = policy_evict_first();
+            int4 tile = tile_of(blockIdx.x);
+            for (int it = blockIdx.x; it < items && ok; it += step) {
+                const int4 ahead = tile_of(it + step);
+                const uint8_t* src = wsrc + (size_t(tile.x) * (N / 16) + (it % R) * 8) * G * kGroupBytes;
+#pragma unroll 1
+                for (int g = 0; g < G; g += 2) {
+                    if (tw.waits() && !(ok = one_wait(&w_empty[tw.s], tw.empty()))) break;
+                    const uint32_t bytes = uint32_t(min(2, G - g)) * kGroupBytes;
+                    mbar_arrive_expect_tx(&w_full[tw.s], 8 * bytes);
+                    fence_proxy_async_smem();              // the unpack warps' reads of the stage come first
+                    uint8_t* to = smem + L.w + tw.s * kWBytes;
+#pragma unroll
+                    for (int t = 0; t < 8; ++t)
+                        bulk_g2s_stream(to + t * bytes, src + (size_t(t) * G + g) * kGroupBytes, bytes, &w_full[tw.s], pol);
+                    tw.next(kWS);
+                }
+                tile = ahead;
             }
-            tile = ahead;
+            drain(w_full, kWS, tw);
         }
     } else if (warp == kTokenWarp) {
-        // ---- staged tokens: a lane copies two groups of a block of 8 rows and term (lanes 0..15) or their sums (16..31)
-        const int pairs = (G + 1) / 2;
-        const int block = NP == 2 && lane < 16 ? lane & 7 : lane & 15, term = NP == 2 ? (lane >> 3) & 1 : 0;
-        int4 tile = tile_of(blockIdx.x);
-        for (int it = blockIdx.x; it < items && ok; it += step) {
-            const int4 ahead = tile_of(it + step);
-            const int nb = tile.z >> 3;
-            const uint8_t* src = bsrc + size_t((tile.y >> 3) + block) * bb + (lane < 16 ? size_t(term) * G * 2048 : sums_at(K, NP));
-            for (int u = 0; u < pairs; ++u) {
-                if (tb.waits() && !(ok = warp_wait(&b_empty[tb.s], tb.empty()))) break;
-                const uint32_t bytes = uint32_t(min(2, G - 2 * u)) * 2048u;
-                if (lane == 0) mbar_arrive_expect_tx(&b_full[tb.s], (bytes * NP + 128u) * nb);
-                __syncwarp();
-                if (block < nb) {
+        // ---- staged tokens: a pair's share of the tile and its sums
+        if (elect_one()) {
+            const int pairs = pairs_of(K);
+            const size_t blocks = p.blocks;
+            const uint8_t* sums = bsrc + sums_at(K, NP, blocks);
+            int4 tile = tile_of(blockIdx.x);
+            for (int it = blockIdx.x; it < items && ok; it += step) {
+                const int4 ahead = tile_of(it + step);
+                const uint32_t nb = uint32_t(tile.z) >> 3;
+                const size_t first = size_t(tile.y >> 3);
+#pragma unroll 1
+                for (int u = 0; u < pairs; ++u) {
+                    if (tb.waits() && !(ok = one_wait(&b_empty[tb.s], tb.empty()))) break;
+                    mbar_arrive_expect_tx(&b_full[tb.s], (4096u * NP + 128u) * nb);
                     uint8_t* to = smem + size_t(tb.s) * bstage;
-                    if (lane < 16) to += (term * nb + block) * bytes;
-                    else to += dcols * 512u + block * 128u;
-                    bulk_g2s(to, src + size_t(u) * (lane < 16 ? 4096 : 128), lane < 16 ? bytes : 128u, &b_full[tb.s]);
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        bulk_g2s(to + q * nb * 4096, bsrc + ((size_t(u) * NP + q) * blocks + first) * 4096, nb * 4096, &b_full[tb.s]);
+                    bulk_g2s(to + dcols * 512u, sums + (size_t(u) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
+                    tb.next(BS);
                 }
-                tb.next(BS);
+                tile = ahead;
             }
-            tile = ahead;
+            drain(b_full, BS, tb);
         }
     } else if (warp == 1) {
         // ---- MMA issue, by one elected thread (elect.sync: with `lane == 0` the compiler does not know that the operands are
@@ -464,19 +486,20 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         if (elect_one()) {
             Turn ta, tt, td;
             int4 tile = tile_of(blockIdx.x);
-            auto wait = [&](uint64_t* b, uint32_t parity) { return wait_or_abort(b, parity, abort_flag, p.err); };
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
                 const uint32_t idesc = tc_idesc(kRows, NP * tile.z), sums = tc_idesc(kRows, tile.z);
                 uint32_t begun = 0;                        // the accumulator holds something
+#pragma unroll 1
                 for (int g = 0; g < G && ok; g += 2) {
                     const int both = min(2, G - g);
-                    ok = wait(&b_full[tt.s], tt.full()) && wait(&a_full[ta.s], ta.full());
+                    ok = one_wait(&b_full[tt.s], tt.full()) && one_wait(&a_full[ta.s], ta.full());
+#pragma unroll 1
                     for (int h = 0; h < both && ok; ++h) {
-                        if (!begun && td.waits() && !(ok = wait(&d_empty[td.s], td.empty()))) break;
+                        if (!begun && td.waits() && !(ok = one_wait(&d_empty[td.s], td.empty()))) break;
                         tc_fence_after();
                         const uint32_t b = sbase + tt.s * bstage, a = taddr + 256 + ta.s * 128 + h * 64, acc = taddr + td.s * dcols;
-                        const uint64_t desc = swizzled_desc(b + h * 2048u, both * 2048u);
+                        const uint64_t desc = swizzled_desc(b + h * 2048u, 4096u);
 #pragma unroll
                         for (int ks = 0; ks < 8; ++ks)
                             tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
@@ -502,7 +525,6 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     } else if (warp < kTokenWarp) {
         // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, one group of each pair
         const int lq = warp & 3, set = (warp - 2) >> 2, g8 = lane >> 2;
-        const __half2 m8 = __float2half2_rn(-1032.f), c16 = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
         // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero point this lane writes)
@@ -521,6 +543,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
             for (int i = 0; i < 5; ++i) rr[i] = rnext[i];
             ahead = tile_of(it + step);
+#pragma unroll 1
             for (int g0 = 0; g0 < G && ok; g0 += 2) {
                 const int both = min(2, G - g0), g = g0 + set;
                 if (g0 + 2 >= G && it + step < items) factors(it + step, ahead, rnext);
@@ -540,15 +563,16 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                 }
                 if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
-                const uint32_t z2 = u2(__float2half2_rn(__fmul_rn(bf16_hi(zrow), 64.f * rr[4])));
+                const uint32_t z2 = u2(__float2half2_rn(__fmul_rn(bf16_hi(zrow) * 0x1p-18f, rr[4])));
                 *reinterpret_cast<uint2*>(zto + ta.s * kZBytes) = make_uint2(z2, z2);
-                fence_proxy_async_smem();                  // (before the hand-over: the MMA reads them through the async proxy)
                 if (g < G) {
                     tc_fence_after();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const __half2 s0 = __float2half2_rn(__fmul_rn(bf16_lo(sz[2 * h]), rr[2 * h]));
-                        const __half2 s1 = __float2half2_rn(__fmul_rn(bf16_lo(sz[2 * h + 1]), rr[2 * h + 1]));
+                        // of rows g8 and g8 + 8: s rho, its 16th for the nibble one place up, and -8 of it 2^-24
+                        const float r0 = __fmul_rn(bf16_lo(sz[2 * h]), rr[2 * h]), r1 = __fmul_rn(bf16_lo(sz[2 * h + 1]), rr[2 * h + 1]);
+                        const __half2 s0 = __float2half2_rn(r0), n0 = __float2half2_rn(r0 * -0x1p-21f);
+                        const __half2 s1 = __float2half2_rn(r1 * 0x1p-4f), n1 = __float2half2_rn(r1 * -0x1p-21f);
                         const uint32_t acol = taddr + 256 + ta.s * 128 + set * 64 + (uint32_t(32 * lq + 16 * h) << 16);
 #pragma unroll
                         for (int kj = 0; kj < 2; ++kj) {
@@ -558,20 +582,17 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
                                 const uint32_t w = w4[k], wh = w >> 8;
-                                const __half2 qa = __hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), m8);
-                                const __half2 qb = __hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), c16, m72);
-                                const __half2 qc = __hadd2(h2(and_or(wh, 0x000F000Fu, 0x64006400u)), m8);
-                                const __half2 qd = __hfma2(h2(and_or(wh, 0x00F000F0u, 0x64006400u)), c16, m72);
-                                v[4 * k] = u2(__hmul2(qa, s0));
-                                v[4 * k + 1] = u2(__hmul2(qc, s0));
-                                v[4 * k + 2] = u2(__hmul2(qb, s1));
-                                v[4 * k + 3] = u2(__hmul2(qd, s1));
+                                v[4 * k] = u2(__hfma2(h2(w & 0x000F000Fu), s0, n0));
+                                v[4 * k + 1] = u2(__hfma2(h2(wh & 0x000F000Fu), s0, n0));
+                                v[4 * k + 2] = u2(__hfma2(h2(w & 0x00F000F0u), s1, n1));
+                                v[4 * k + 3] = u2(__hfma2(h2(wh & 0x00F000F0u), s1, n1));
                             }
                             tmem_store4(acol + kj * 32, v);
                         }
                     }
                 }
                 if (lane == 0) mbar_arrive(&w_empty[tt.s]);    // (all lanes' loads have been used by the stores above)
+                fence_proxy_async_smem();                      // the MMA reads the zero points through the async proxy
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
@@ -601,10 +622,10 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             const int r = it % R, n = tile.z;
             float* f = fac + turn * 256;
             if (et < n) {
-                f[et] = GATE ? f0 : inverse_pow2(f0);
+                f[et] = 0x1p12f * (GATE ? f0 : inverse_pow2(f0));
                 if (GATE) f[128 + et] = f1;
             }
-            const float ir = inverse_pow2(irho);
+            const float ir = 0x1p12f * inverse_pow2(irho);     // (the 2^24 of A, half of it with either factor)
             ahead = tile_of(it + step);
             // factors in place, the previous tile's copies have read the buffer
             auto ready = [&]() {
@@ -647,6 +668,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 if (it + step < items) factors(it + step, ahead);
                 tc_fence_after();
                 const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
+#pragma unroll 1
                 for (int c0 = 0; c0 < n && ok; c0 += 16) {
                     float v[16];
                     tc_ld16(acc + uint32_t(c0), v);
@@ -663,6 +685,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 for (int i = 0; i < kTileTokens<NP> / 16; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
+#pragma unroll 1
                 for (int g = 0; g < G; ++g) {
                     ok = ok && warp_wait(&d_full[td.s], td.full());
                     tc_fence_after();
@@ -686,30 +709,33 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 }
                 ready();
                 if (it + step < items) factors(it + step, ahead);
+                // (one copy of the code: the sums move down instead)
+#pragma unroll 1
+                for (int c0 = 0; c0 < n && ok; c0 += 16) {
+                    finish(c0, sum[0]);
 #pragma unroll
-                for (int i = 0; i < kTileTokens<NP> / 16; ++i)
-                    if (i * 16 < n && ok) finish(i * 16, sum[i]);
+                    for (int i = 0; i + 1 < kTileTokens<NP> / 16; ++i)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[i][j] = sum[i + 1][j];
+                }
             }
             if (GATE) {
                 fence_proxy_async_smem();
                 epilogue_bar();
-                const size_t ab = block_bytes(p.w.I, NP);
-                uint8_t* blk = p.as + size_t(tile.y >> 3) * ab;
+                const size_t blocks = p.blocks;            // this tile is the activations' 64 inputs number r
                 if (ok && warp == kEpiWarp) {
                     if (lane < (n >> 3)) {
 #pragma unroll
                         for (int s = 0; s < NP; ++s)
-                            bulk_s2g(blk + lane * ab + (size_t(s) * (p.w.I >> 6) + r) * 1024,
-                                     tbuf + (size_t(lane) * NP + s) * 1024, 1024);
+                            bulk_s2g(p.as + atom_at(r, s, NP, blocks, (tile.y >> 3) + lane), tbuf + (size_t(lane) * NP + s) * 1024, 1024);
                     }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
                 if (ok && et < n) {
                     // the sum of the tile's 64 activations as staged, in their order
                     float X = 0.f;
-#pragma unroll
                     for (int s = 0; s < NP; ++s)
-#pragma unroll
+#pragma unroll 2
                         for (int c = 0; c < 8; ++c) {
                             const uint4 h = *reinterpret_cast<const uint4*>(tbuf + (size_t(et >> 3) * NP + s) * 1024 + piece(et & 7, c));
                             const uint32_t w[4] = {h.x, h.y, h.z, h.w};
@@ -719,23 +745,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                                 X = __fadd_rn(X, __fadd_rn(v.x, v.y));
                             }
                         }
-                    uint8_t* sums = blk + size_t(et >> 3) * ab + sums_at(p.w.I, NP);
-                    put_sum(sums, et & 7, r, X);
-                    if (r == 0) clear_sums(sums, p.w.I, et & 7);
+                    uint8_t* sums = p.as + sums_at(p.w.I, NP, blocks);
+                    put_sum(sums, blocks, tile.y + et, r, X);
+                    if (r == 0) clear_sums(sums, blocks, p.w.I, tile.y + et);
                 }
             }
             tile = ahead;
         }
         if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
-    }
-    if (*abort_flag) {
-        // the copies still in flight: the latest round of every stage
-        if (warp == 0 && lane == 0)
-            for (int s = 0; s < kWS; ++s)
-                if (tw.round > 0 || s < tw.s) mbar_wait(&w_full[s], (s < tw.s ? tw.round : tw.round - 1) & 1u, p.err, 50000000ull);
-        if (warp == kTokenWarp && lane == 0)
-            for (int s = 0; s < BS; ++s)
-                if (tb.round > 0 || s < tb.s) mbar_wait(&b_full[s], (s < tb.s ? tb.round : tb.round - 1) & 1u, p.err, 50000000ull);
     }
     tc_fence_before();
     __syncthreads();
@@ -807,8 +824,9 @@ MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k) {
     z.isx = z.pos + up16(S * 4);
     z.sact = z.isx + up16(P * 4);
     z.xs = z.sact + up16(P * 4);
-    z.as = z.xs + P / 8 * block_bytes(w.H, np);
-    z.out = z.as + P / 8 * block_bytes(w.I, np);
+    z.blocks = P / 8;
+    z.as = z.xs + staged_bytes(w.H, np, P / 8);
+    z.out = z.as + staged_bytes(w.I, np, P / 8);
     z.total = z.out + P * w.H * 4;
     return z;
 }
