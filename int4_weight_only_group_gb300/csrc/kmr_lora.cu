@@ -39,12 +39,55 @@ __device__ __forceinline__ uint32_t take_term(float& lo, float& hi) {
 
 __device__ __forceinline__ void clear4(float (&d)[4]) { d[0] = d[1] = d[2] = d[3] = 0.f; }
 
-// Rows of a tile: MT m-tiles of 16 (R = 16 MT, or R = 1 with MT = 1: `rows` says how many are real).
-template <bool BF16, int RT, int MT>       // RT: 8-rank tiles
-__global__ void __launch_bounds__(kThr) lora_kernel(const LoraParams p, int R) {
+// The A operand of a step of 16 from fp32 values (rows g and g + 8, four consecutive k each): one of three terms, taken off.
+__device__ __forceinline__ void term_of(float (&fa)[4], float (&fb)[4], uint32_t (&A)[4]) {
+    A[0] = take_term(fa[0], fa[1]);
+    A[1] = take_term(fb[0], fb[1]);
+    A[2] = take_term(fa[2], fa[3]);
+    A[3] = take_term(fb[2], fb[3]);
+}
+
+// Four values of a row: fp32 or bf16.
+template <bool BF16>
+struct Four {
+    float4 v;
+    __device__ __forceinline__ void load(const void* p, size_t at, bool real) {
+        v = real ? *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = v; }
+    __device__ __forceinline__ void values(float (&f)[4]) const {
+        f[0] = v.x;
+        f[1] = v.y;
+        f[2] = v.z;
+        f[3] = v.w;
+    }
+};
+template <>
+struct Four<true> {
+    uint2 v;
+    __device__ __forceinline__ void load(const void* p, size_t at, bool real) {
+        v = real ? *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at) : make_uint2(0u, 0u);
+    }
+    __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = v; }
+    __device__ __forceinline__ void values(float (&f)[4]) const {
+        f[0] = bf16_lo(v.x);
+        f[1] = bf16_hi(v.x);
+        f[2] = bf16_lo(v.y);
+        f[3] = bf16_hi(v.y);
+    }
+};
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// Rows of a tile: MT m-tiles of 16 (R = 16 MT, or R = 1 with MT = 1: `rows` says how many are real).  RT: 8-rank tiles.
+template <bool BF16, int RT, int MT>
+__global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const LoraParams p, int R) {
     constexpr int RP = RT * 8;             // ranks, padded
+    constexpr int KS = (RT + 1) / 2;       // steps of 16 ranks
     constexpr int KW = kWarps / MT;        // warps that share an m-tile
-    __shared__ int ids[16 * MT];
+    constexpr int U = RT <= 2 ? (BF16 ? 8 : 4) : (RT == 4 ? 4 : (RT == 8 ? 2 : 1));       // steps of 16 inputs in flight
+    constexpr int UN = RT <= 4 ? 4 : (RT == 8 ? 2 : 1);                      // blocks of 16 outputs in flight
+    __shared__ __align__(16) int ids[16 * MT < 32 ? 32 : 16 * MT];
+    __shared__ uint32_t leads[2];          // rows that are the first with their adapter
     extern __shared__ __align__(16) float sm[];
     float* vpart = sm;                     // [KW][16 MT][RP]
     float* vloc = vpart + KW * 16 * MT * RP;   // [16 MT][RP]: this CTA's part of v, read by the cluster
@@ -66,73 +109,113 @@ __global__ void __launch_bounds__(kThr) lora_kernel(const LoraParams p, int R) {
         ids[threadIdx.x] = a;
     }
     __syncthreads();
+    if (warp < 2) {
+        const int i = threadIdx.x;
+        const int a = i < 16 * MT ? ids[i] : -1;
+        const uint32_t same = __match_any_sync(0xffffffffu, a);       // (by the whole warp, whatever a is)
+        bool lead = a >= 0 && __ffs(same) - 1 == lane;
+        if (MT > 2 && warp == 1) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int4 o = reinterpret_cast<const int4*>(ids)[j];
+                lead = lead && o.x != a && o.y != a && o.z != a && o.w != a;
+            }
+        }
+        const uint32_t m = __ballot_sync(0xffffffffu, lead);
+        if (lane == 0) leads[warp] = m;
+    }
+    __syncthreads();
     const int ra = 16 * mt + g, rb = ra + 8;              // this lane's rows
     const int ida = ids[ra], idb = ids[rb];
-    // this rank's columns of the output: whole blocks of 16
+    // this rank's columns of the output: whole blocks of 16, and this warp's part of its k-steps
     const int blocks = p.N >> 4;
     const int n0 = blocks * rank / kCluster, n1 = blocks * (rank + 1) / kCluster;
-    const int k0 = (p.K / 16) * rank / kCluster, k1 = (p.K / 16) * (rank + 1) / kCluster;      // k-steps of 16
+    const int k0 = (p.K / 16) * rank / kCluster, k1 = (p.K / 16) * (rank + 1) / kCluster;
+    const int kper = (k1 - k0 + KW - 1) / KW, kb = k0 + kw * kper, ke = min(k1, kb + kper);
 
     // rows without an adapter
     for (int r = warp; r < rows; r += kWarps) {
         if (ids[r] >= 0 || p.base == p.y) continue;
         const size_t at = size_t(row0 + r) * p.ldy;
-        for (int c = n0 * 16 + lane; c < n1 * 16; c += 32) {
-            if (BF16)
-                static_cast<uint16_t*>(p.y)[at + c] = p.base ? static_cast<const uint16_t*>(p.base)[at + c] : uint16_t(0);
-            else
-                static_cast<float*>(p.y)[at + c] = p.base ? static_cast<const float*>(p.base)[at + c] : 0.f;
+        for (int c = n0 * 16 + lane * 4; c < n1 * 16; c += 128) {
+            Four<BF16> f;
+            f.load(p.base, at + c, p.base != nullptr);
+            f.store(p.y, at + c);
         }
     }
 
-    for (int lead = 0; lead < rows; ++lead) {
-        const int a = ids[lead];
-        if (a < 0) continue;
-        bool first = true;
-        for (int r = 0; r < lead; ++r) first = first && ids[r] != a;
-        if (!first) continue;
+    bool pending = false;                  // the others may still read this CTA's part of v
+    for (uint64_t left = leads[0] | (uint64_t(leads[1]) << 32); left; left &= left - 1) {
+        const int a = ids[__ffsll(left) - 1];
         const int rank_a = p.ranks ? max(0, min(p.r, p.ranks[a])) : p.r;
+        const float scale = p.scales ? p.scales[a] : 1.f;
         const uint16_t* A = p.a + size_t(a) * p.r * p.K;
         const uint16_t* B = p.b + size_t(a) * p.N * p.r;
-        // ---- v = A x over this rank's k-steps
+        const bool ua = ida == a, ub = idb == a;
+        const size_t xa = size_t(row0 + ra) * p.ldx, xb = size_t(row0 + rb) * p.ldx;
+        const size_t ya = size_t(row0 + ra) * p.ldy, yb = size_t(row0 + rb) * p.ldy;
+
+        uint2 w2[UN][KS][2];
+        Four<BF16> oa[UN], ob[UN];
+        auto load_out = [&](int nb0) {
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                const int nb = nb0 + i;
+                const bool real = nb < n1;
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        // column g of n-tile h: output columns 4 (g / 2) + 2 h + g % 2 of the block; ranks k .. k + 3
+                        const int k = ks * 16 + 4 * t, n = nb * 16 + 4 * (g >> 1) + 2 * h + (g & 1);
+                        w2[i][ks][h] = real && k < p.r ? *reinterpret_cast<const uint2*>(B + size_t(n) * p.r + k) : make_uint2(0u, 0u);
+                    }
+                oa[i].load(p.base, ya + nb * 16 + 4 * t, real && ua && p.base);
+                ob[i].load(p.base, yb + nb * 16 + 4 * t, real && ub && p.base);
+            }
+        };
+        if (MT == 1) {                     // few rows: B's bytes are on their way while v is formed
+            const size_t from = size_t(n0) * 16 * p.r, to = size_t(n1) * 16 * p.r;
+            for (size_t i = from + threadIdx.x * 64; i < to; i += kThr * 64) prefetch_l2(B + i);
+        }
+
+        // ---- v = A x over this warp's k-steps
         float d[RT][4];
 #pragma unroll
         for (int j = 0; j < RT; ++j) clear4(d[j]);
-        const bool ua = ida == a, ub = idb == a;
-        const size_t xa = size_t(row0 + ra) * p.ldx, xb = size_t(row0 + rb) * p.ldx;
-        for (int ks = k0 + kw; ks < k1; ks += KW) {
-            const int k = ks * 16 + 4 * t;
-            float fa[4] = {0.f, 0.f, 0.f, 0.f}, fb[4] = {0.f, 0.f, 0.f, 0.f};
-            uint32_t A0[4] = {0, 0, 0, 0};
-            if (BF16) {
-                const uint16_t* x = static_cast<const uint16_t*>(p.x);
-                const uint2 va = ua ? *reinterpret_cast<const uint2*>(x + xa + k) : make_uint2(0, 0);
-                const uint2 vb = ub ? *reinterpret_cast<const uint2*>(x + xb + k) : make_uint2(0, 0);
-                A0[0] = va.x; A0[1] = vb.x; A0[2] = va.y; A0[3] = vb.y;
-            } else {
-                const float* x = static_cast<const float*>(p.x);
-                const float4 z = make_float4(0.f, 0.f, 0.f, 0.f);
-                const float4 va = ua ? *reinterpret_cast<const float4*>(x + xa + k) : z;
-                const float4 vb = ub ? *reinterpret_cast<const float4*>(x + xb + k) : z;
-                fa[0] = va.x; fa[1] = va.y; fa[2] = va.z; fa[3] = va.w;
-                fb[0] = vb.x; fb[1] = vb.y; fb[2] = vb.z; fb[3] = vb.w;
-            }
-            uint2 w[RT];
+        for (int ks = kb; ks < ke; ks += U) {
+            Four<BF16> va[U], vb[U];
+            uint2 w[U][RT];
 #pragma unroll
-            for (int j = 0; j < RT; ++j) {
-                const int n = 8 * j + g;
-                w[j] = n < rank_a ? *reinterpret_cast<const uint2*>(A + size_t(n) * p.K + k) : make_uint2(0, 0);
-            }
+            for (int u = 0; u < U; ++u) {
+                const int k = (ks + u) * 16 + 4 * t;
+                const bool real = ks + u < ke;
+                va[u].load(p.x, xa + k, real && ua);
+                vb[u].load(p.x, xb + k, real && ub);
 #pragma unroll
-            for (int term = 0; term < (BF16 ? 1 : 3); ++term) {
-                if (!BF16) {
-                    A0[0] = take_term(fa[0], fa[1]);
-                    A0[1] = take_term(fb[0], fb[1]);
-                    A0[2] = take_term(fa[2], fa[3]);
-                    A0[3] = take_term(fb[2], fb[3]);
+                for (int j = 0; j < RT; ++j) {
+                    const int n = 8 * j + g;
+                    w[u][j] = real && n < rank_a ? *reinterpret_cast<const uint2*>(A + size_t(n) * p.K + k) : make_uint2(0u, 0u);
                 }
+            }
 #pragma unroll
-                for (int j = 0; j < RT; ++j) mma_bf16(d[j], A0, w[j].x, w[j].y);
+            for (int u = 0; u < U; ++u) {
+                if constexpr (BF16) {
+                    const uint32_t A0[4] = {(va[u].v.x), (vb[u].v.x), (va[u].v.y), (vb[u].v.y)};
+#pragma unroll
+                    for (int j = 0; j < RT; ++j) mma_bf16(d[j], A0, w[u][j].x, w[u][j].y);
+                } else {
+                    float fa[4], fb[4];
+                    va[u].values(fa);
+                    vb[u].values(fb);
+#pragma unroll
+                    for (int term = 0; term < 3; ++term) {
+                        uint32_t A0[4];
+                        term_of(fa, fb, A0);
+#pragma unroll
+                        for (int j = 0; j < RT; ++j) mma_bf16(d[j], A0, w[u][j].x, w[u][j].y);
+                    }
+                }
             }
         }
 #pragma unroll
@@ -141,82 +224,95 @@ __global__ void __launch_bounds__(kThr) lora_kernel(const LoraParams p, int R) {
             *reinterpret_cast<float2*>(to) = make_float2(d[j][0], d[j][1]);
             *reinterpret_cast<float2*>(to + 8 * RP) = make_float2(d[j][2], d[j][3]);
         }
+        if (pending) cluster.barrier_wait();
         __syncthreads();
-        for (int i = threadIdx.x; i < 16 * MT * RP; i += kThr) {
+        const int live = min(16 * MT, rows) * RP;
+        for (int i = threadIdx.x; i < live; i += kThr) {
             float s = 0.f;
 #pragma unroll
             for (int w = 0; w < KW; ++w) s = __fadd_rn(s, vpart[size_t(w) * 16 * MT * RP + i]);
             vloc[i] = s;
         }
         cluster.sync();
-        for (int i = threadIdx.x; i < 16 * MT * RP; i += kThr) {
-            float s = 0.f;
+        for (int i = threadIdx.x; i < live; i += kThr) {
+            float q[kCluster];
 #pragma unroll
-            for (int q = 0; q < kCluster; ++q) s = __fadd_rn(s, cluster.map_shared_rank(vloc, q)[i]);
-            vsum[i] = s;
+            for (int c = 0; c < kCluster; ++c) q[c] = cluster.map_shared_rank(vloc, c)[i];
+            float s = q[0];
+#pragma unroll
+            for (int c = 1; c < kCluster; ++c) s = __fadd_rn(s, q[c]);
+            // (ranks past this adapter's: whatever its arrays hold there)
+            vsum[i] = int(unsigned(i) % RP) < rank_a ? s : 0.f;
         }
+        cluster.barrier_arrive();
+        pending = true;
         __syncthreads();
-        // ---- y = base + scale B v over this rank's columns: a warp takes blocks of 16
-        const float scale = p.scales ? p.scales[a] : 1.f;
-        for (int nb = n0 + kw; nb < n1; nb += KW) {
-            float e[2][4];
-            clear4(e[0]);
-            clear4(e[1]);
+
+        // ---- y = base + scale B v over this rank's columns: a warp takes UN blocks of 16 at a time
+        for (int nb0 = n0 + kw * UN; nb0 < n1; nb0 += KW * UN) {
+            load_out(nb0);
+            float e[UN][2][4];
 #pragma unroll
-            for (int ks = 0; ks < (RT + 1) / 2; ++ks) {
-                const int k = ks * 16 + 4 * t;                   // ranks k..k + 3
-                float fa[4], fb[4];
+            for (int i = 0; i < UN; ++i) {
+                clear4(e[i][0]);
+                clear4(e[i][1]);
+            }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const bool in = k + q < rank_a;
-                    fa[q] = in ? vsum[ra * RP + k + q] : 0.f;
-                    fb[q] = in ? vsum[rb * RP + k + q] : 0.f;
+            for (int ks = 0; ks < KS; ++ks) {
+                const int k = ks * 16 + 4 * t;
+                float fa[4] = {0.f, 0.f, 0.f, 0.f}, fb[4] = {0.f, 0.f, 0.f, 0.f};
+                if (k < RP) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        fa[q] = ra < rows ? vsum[ra * RP + k + q] : 0.f;
+                        fb[q] = rb < rows ? vsum[rb * RP + k + q] : 0.f;
+                    }
                 }
-                uint2 w[2];
+                if (p.ranks) {
+#pragma unroll
+                    for (int i = 0; i < UN; ++i)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (k + 0 >= rank_a) w2[i][ks][h].x &= 0xFFFF0000u;
+                            if (k + 1 >= rank_a) w2[i][ks][h].x &= 0x0000FFFFu;
+                            if (k + 2 >= rank_a) w2[i][ks][h].y &= 0xFFFF0000u;
+                            if (k + 3 >= rank_a) w2[i][ks][h].y &= 0x0000FFFFu;
+                        }
+                }
+                // (bf16 results: two terms hold 16 bits)
+#pragma unroll
+                for (int term = 0; term < (BF16 ? 2 : 3); ++term) {
+                    uint32_t A0[4];
+                    term_of(fa, fb, A0);
+#pragma unroll
+                    for (int i = 0; i < UN; ++i) {
+                        mma_bf16(e[i][0], A0, w2[i][ks][0].x, w2[i][ks][0].y);
+                        mma_bf16(e[i][1], A0, w2[i][ks][1].x, w2[i][ks][1].y);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < UN; ++i) {
+                if (nb0 + i >= n1) continue;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    // column g of n-tile h: output columns 4 (g / 2) + 2 h + g % 2 of the block
-                    const int n = nb * 16 + 4 * (g >> 1) + 2 * h + (g & 1);
-                    w[h] = k < p.r ? *reinterpret_cast<const uint2*>(B + size_t(n) * p.r + k) : make_uint2(0, 0);
-                    // ranks past this adapter's: whatever the array holds there
-                    if (k + 0 >= rank_a) w[h].x &= 0xFFFF0000u;
-                    if (k + 1 >= rank_a) w[h].x &= 0x0000FFFFu;
-                    if (k + 2 >= rank_a) w[h].y &= 0xFFFF0000u;
-                    if (k + 3 >= rank_a) w[h].y &= 0x0000FFFFu;
-                }
-#pragma unroll
-                for (int term = 0; term < 3; ++term) {
-                    uint32_t A0[4];
-                    A0[0] = take_term(fa[0], fa[1]);
-                    A0[1] = take_term(fb[0], fb[1]);
-                    A0[2] = take_term(fa[2], fa[3]);
-                    A0[3] = take_term(fb[2], fb[3]);
-                    mma_bf16(e[0], A0, w[0].x, w[0].y);
-                    mma_bf16(e[1], A0, w[1].x, w[1].y);
-                }
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (!(h ? ub : ua)) continue;
-                const size_t at = size_t(row0 + (h ? rb : ra)) * p.ldy + nb * 16 + 4 * t;
-                float o[4] = {e[0][2 * h], e[0][2 * h + 1], e[1][2 * h], e[1][2 * h + 1]};
-                if (BF16) {
-                    uint2 b = make_uint2(0, 0);
-                    if (p.base) b = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.base) + at);
-                    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at) =
-                        make_uint2(cvt2(__fmaf_rn(scale, o[0], bf16_lo(b.x)), __fmaf_rn(scale, o[1], bf16_hi(b.x))),
-                                   cvt2(__fmaf_rn(scale, o[2], bf16_lo(b.y)), __fmaf_rn(scale, o[3], bf16_hi(b.y))));
-                } else {
-                    float4 b = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (p.base) b = *reinterpret_cast<const float4*>(static_cast<const float*>(p.base) + at);
-                    *reinterpret_cast<float4*>(static_cast<float*>(p.y) + at) =
-                        make_float4(__fmaf_rn(scale, o[0], b.x), __fmaf_rn(scale, o[1], b.y), __fmaf_rn(scale, o[2], b.z),
-                                    __fmaf_rn(scale, o[3], b.w));
+                    if (!(h ? ub : ua)) continue;
+                    float o[4];
+                    (h ? ob[i] : oa[i]).values(o);
+                    o[0] = __fmaf_rn(scale, e[i][0][2 * h], o[0]);
+                    o[1] = __fmaf_rn(scale, e[i][0][2 * h + 1], o[1]);
+                    o[2] = __fmaf_rn(scale, e[i][1][2 * h], o[2]);
+                    o[3] = __fmaf_rn(scale, e[i][1][2 * h + 1], o[3]);
+                    const size_t at = (h ? yb : ya) + (nb0 + i) * 16 + 4 * t;
+                    Four<BF16> r;
+                    if constexpr (BF16) r.v = make_uint2(cvt2(o[0], o[1]), cvt2(o[2], o[3]));
+                    else r.v = make_float4(o[0], o[1], o[2], o[3]);
+                    r.store(p.y, at);
                 }
             }
         }
-        cluster.sync();                    // the others have read this CTA's part of v
     }
+    if (pending) cluster.barrier_wait();
 }
 
 template <bool BF16, int RT, int MT>

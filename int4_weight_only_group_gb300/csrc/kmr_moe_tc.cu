@@ -79,10 +79,16 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = p.T * p.k;
     count[tid] = 0;
     __syncthreads();
-    for (int i = tid; i < S; i += kPlanThr) {
-        const int e = p.ids[i];
-        if (e >= 0 && e < p.w.E) atomicAdd(&count[e], 1);
-        else if (e != -1) set_error(p.err, KMR_ERR_INVALID_ARG);
+    constexpr int kB = 8;                                            // ids in flight
+    for (int i0 = tid; i0 < S; i0 += kB * kPlanThr) {
+        int e[kB];
+#pragma unroll
+        for (int b = 0; b < kB; ++b) e[b] = i0 + b * kPlanThr < S ? p.ids[i0 + b * kPlanThr] : -1;
+#pragma unroll
+        for (int b = 0; b < kB; ++b) {
+            if (e[b] >= 0 && e[b] < p.w.E) atomicAdd(&count[e[b]], 1);
+            else if (e[b] != -1) set_error(p.err, KMR_ERR_INVALID_ARG);
+        }
     }
     __syncthreads();
     // thread e: its expert's padded positions and tiles, and those before it
@@ -119,9 +125,15 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     if (tid == kPlanThr - 1) *p.ntiles = pb + b;
     __syncthreads();
     // (which of its expert's positions a place gets does not change any result)
-    for (int i = tid; i < S; i += kPlanThr) {
-        const int e = p.ids[i];
-        p.pos[i] = e >= 0 && e < p.w.E ? atomicAdd(&at[e], 1) : -1;
+    for (int i0 = tid; i0 < S; i0 += kB * kPlanThr) {
+        int e[kB];
+#pragma unroll
+        for (int b = 0; b < kB; ++b) e[b] = i0 + b * kPlanThr < S ? p.ids[i0 + b * kPlanThr] : -1;
+#pragma unroll
+        for (int b = 0; b < kB; ++b) e[b] = e[b] >= 0 && e[b] < p.w.E ? atomicAdd(&at[e[b]], 1) : -1;
+#pragma unroll
+        for (int b = 0; b < kB; ++b)
+            if (i0 + b * kPlanThr < S) p.pos[i0 + b * kPlanThr] = e[b];
     }
 }
 
@@ -760,41 +772,55 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 }
 
 // ------------------------------------------------------------------ combine
-constexpr int kCombineThr = 256;
+constexpr int kCombineThr = 128;
 template <typename OUT>
 __global__ void __launch_bounds__(kCombineThr) moe_combine_kernel(const MoeTcParams p) {
+    __shared__ int pos[kMoeMaxTopK];
+    __shared__ float weight[kMoeMaxTopK];
     pdl_launch_dependents();
     pdl_wait();
-    const int t = blockIdx.x, H = p.w.H;
-    for (int h = threadIdx.x * 4; h < H; h += kCombineThr * 4) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < p.k; ++j) {
-            const int at = p.pos[size_t(t) * p.k + j];
-            if (at < 0) continue;
-            const float w = p.weights[size_t(t) * p.k + j];
-            const float4 o = *reinterpret_cast<const float4*>(p.out + size_t(at) * H + h);
-            v.x = __fmaf_rn(w, o.x, v.x);
-            v.y = __fmaf_rn(w, o.y, v.y);
-            v.z = __fmaf_rn(w, o.z, v.z);
-            v.w = __fmaf_rn(w, o.w, v.w);
+    const int t = blockIdx.x, H = p.w.H, h = (blockIdx.y * kCombineThr + threadIdx.x) * 4;
+    if (threadIdx.x < kMoeMaxTopK) {
+        const int at = int(threadIdx.x) < p.k ? p.pos[size_t(t) * p.k + threadIdx.x] : -1;
+        pos[threadIdx.x] = at;
+        weight[threadIdx.x] = at >= 0 ? p.weights[size_t(t) * p.k + threadIdx.x] : 0.f;
+    }
+    __syncthreads();
+    if (h >= H) return;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int j0 = 0; j0 < p.k; j0 += 8) {
+        float4 o[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int at = j0 + j < kMoeMaxTopK ? pos[j0 + j] : -1;
+            o[j] = at >= 0 ? __ldcs(reinterpret_cast<const float4*>(p.out + size_t(at) * H + h)) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        const size_t at = size_t(t) * H + h;
-        if constexpr (sizeof(OUT) == 4) {
-            float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
-            if (p.resid) {
-                const float4 o = *y;
-                v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
-            }
-            *y = v;
-        } else {
-            uint2* y = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at);
-            if (p.resid) {
-                const uint2 o = *y;
-                v = make_float4(__fadd_rn(bf16_lo(o.x), v.x), __fadd_rn(bf16_hi(o.x), v.y), __fadd_rn(bf16_lo(o.y), v.z),
-                                __fadd_rn(bf16_hi(o.y), v.w));
-            }
-            *y = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (j0 + j >= kMoeMaxTopK || pos[j0 + j] < 0) continue;
+            const float w = weight[j0 + j];
+            v.x = __fmaf_rn(w, o[j].x, v.x);
+            v.y = __fmaf_rn(w, o[j].y, v.y);
+            v.z = __fmaf_rn(w, o[j].z, v.z);
+            v.w = __fmaf_rn(w, o[j].w, v.w);
         }
+    }
+    const size_t at = size_t(t) * H + h;
+    if constexpr (sizeof(OUT) == 4) {
+        float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
+        if (p.resid) {
+            const float4 o = *y;
+            v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
+        }
+        *y = v;
+    } else {
+        uint2* y = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at);
+        if (p.resid) {
+            const uint2 o = *y;
+            v = make_float4(__fadd_rn(bf16_lo(o.x), v.x), __fadd_rn(bf16_hi(o.x), v.y), __fadd_rn(bf16_lo(o.y), v.z),
+                            __fadd_rn(bf16_hi(o.y), v.w));
+        }
+        *y = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
     }
 }
 
@@ -842,7 +868,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
         if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<uint16_t> : (const void*)moe_combine_kernel<float>;
-    return launch_dependent(combine, dim3(p.T), kCombineThr, 0, 1, q, st);
+    return launch_dependent(combine, dim3(p.T, (p.w.H / 4 + kCombineThr - 1) / kCombineThr), kCombineThr, 0, 1, q, st);
 }
 
 cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_down, float* norms, cudaStream_t st) {
