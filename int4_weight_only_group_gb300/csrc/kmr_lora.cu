@@ -21,7 +21,7 @@ namespace cg = cooperative_groups;
 
 namespace {
 
-constexpr int kThr = 256, kWarps = kThr / 32, kCluster = 8;
+constexpr int kThr = 256, kWarps = kThr / 32, kMaxCluster = 8;
 
 // {lo, hi} as bf16 (round to nearest), and what is left of them
 __device__ __forceinline__ uint32_t cvt2(float lo, float hi) {
@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
     float* vloc = vpart + KW * 16 * MT * RP;   // [16 MT][RP]: this CTA's part of v, read by the cluster
     float* vsum = vloc + 16 * MT * RP;     // [16 MT][RP]
     cg::cluster_group cluster = cg::this_cluster();
-    const int rank = int(cluster.block_rank());
+    const int rank = int(cluster.block_rank()), C = int(cluster.num_blocks());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int mt = warp / KW, kw = warp % KW;
-    const int row0 = int(blockIdx.x / kCluster) * R;
+    const int row0 = int(blockIdx.x / C) * R;
     const int rows = min(R, p.T - row0);
     pdl_launch_dependents();
     pdl_wait();
@@ -129,8 +129,8 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
     const int ida = ids[ra], idb = ids[rb];
     // this rank's columns of the output: whole blocks of 16, and this warp's part of its k-steps
     const int blocks = p.N >> 4;
-    const int n0 = blocks * rank / kCluster, n1 = blocks * (rank + 1) / kCluster;
-    const int k0 = (p.K / 16) * rank / kCluster, k1 = (p.K / 16) * (rank + 1) / kCluster;
+    const int n0 = blocks * rank / C, n1 = blocks * (rank + 1) / C;
+    const int k0 = (p.K / 16) * rank / C, k1 = (p.K / 16) * (rank + 1) / C;
     const int kper = (k1 - k0 + KW - 1) / KW, kb = k0 + kw * kper, ke = min(k1, kb + kper);
 
     // rows without an adapter
@@ -235,12 +235,12 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
         }
         cluster.sync();
         for (int i = threadIdx.x; i < live; i += kThr) {
-            float q[kCluster];
+            float q[kMaxCluster];
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) q[c] = cluster.map_shared_rank(vloc, c)[i];
+            for (int c = 0; c < kMaxCluster; ++c) q[c] = c < C ? cluster.map_shared_rank(vloc, c)[i] : 0.f;
             float s = q[0];
 #pragma unroll
-            for (int c = 1; c < kCluster; ++c) s = __fadd_rn(s, q[c]);
+            for (int c = 1; c < kMaxCluster; ++c) s = __fadd_rn(s, q[c]);
             // (ranks past this adapter's: whatever its arrays hold there)
             vsum[i] = int(unsigned(i) % RP) < rank_a ? s : 0.f;
         }
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
 }
 
 template <bool BF16, int RT, int MT>
-cudaError_t run(const LoraParams& p, int R, cudaStream_t st, bool set_only) {
+cudaError_t run(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
     const size_t smem = size_t(kWarps / MT + 2) * 16 * MT * RT * 8 * 4;
     const void* fn = (const void*)lora_kernel<BF16, RT, MT>;
     if (set_only) return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
@@ -324,10 +324,10 @@ cudaError_t run(const LoraParams& p, int R, cudaStream_t st, bool set_only) {
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.x = unsigned(C);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(unsigned((p.T + R - 1) / R) * kCluster);
+    cfg.gridDim = dim3(unsigned((p.T + R - 1) / R) * C);
     cfg.blockDim = dim3(kThr);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -336,34 +336,38 @@ cudaError_t run(const LoraParams& p, int R, cudaStream_t st, bool set_only) {
     return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, RT, MT>, p, R);
 }
 template <bool BF16, int RT>
-cudaError_t by_rows(const LoraParams& p, int R, cudaStream_t st, bool set_only) {
+cudaError_t by_rows(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
     if (set_only) {
-        const cudaError_t e = run<BF16, RT, 1>(p, R, st, true);
-        return e != cudaSuccess ? e : run<BF16, RT, 4>(p, R, st, true);
+        return run<BF16, RT, 1>(p, R, C, st, true);
     }
-    return R > 16 ? run<BF16, RT, 4>(p, R, st, false) : run<BF16, RT, 1>(p, R, st, false);
+    return run<BF16, RT, 1>(p, R, C, st, false);
 }
 template <bool BF16>
-cudaError_t by_rank(const LoraParams& p, int R, cudaStream_t st, bool set_only) {
-    if (p.r <= 8) return by_rows<BF16, 1>(p, R, st, set_only);
-    if (p.r <= 16) return by_rows<BF16, 2>(p, R, st, set_only);
-    if (p.r <= 32) return by_rows<BF16, 4>(p, R, st, set_only);
-    if (p.r <= 64) return by_rows<BF16, 8>(p, R, st, set_only);
-    return by_rows<BF16, 16>(p, R, st, set_only);
+cudaError_t by_rank(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
+    if (p.r <= 8) return by_rows<BF16, 1>(p, R, C, st, set_only);
+    if (p.r <= 16) return by_rows<BF16, 2>(p, R, C, st, set_only);
+    if (p.r <= 32) return by_rows<BF16, 4>(p, R, C, st, set_only);
+    if (p.r <= 64) return by_rows<BF16, 8>(p, R, C, st, set_only);
+    return by_rows<BF16, 16>(p, R, C, st, set_only);
 }
 
 }  // namespace
 
 cudaError_t launch_lora(const LoraParams& p, bool bf16, int sms, cudaStream_t st) {
-    const int R = p.T <= 64 ? 1 : (p.T < 2048 ? 16 : 64);
-    return bf16 ? by_rank<true>(p, R, st, false) : by_rank<false>(p, R, st, false);
+    // One row a tile up to two rows a SM: rows of a small batch have adapters of their own (64 rows of 64 adapters: 7 us against
+    // 55 with tiles of 16; of 4 adapters 8 against 9).  More rows are taken 16 at a time (32 and 64 are no faster even for one
+    // adapter: their phases overlap less).  Then the smallest cluster that gives every SM a CTA or two.
+    const int R = p.T <= 2 * sms ? 1 : 16, tiles = (p.T + R - 1) / R;
+    int C = kMaxCluster;
+    while (C > 1 && tiles * C > 2 * sms + sms / 2) C /= 2;
+    return bf16 ? by_rank<true>(p, R, C, st, false) : by_rank<false>(p, R, C, st, false);
 }
 
 cudaError_t lora_set_attributes() {
     LoraParams p = {};
     for (p.r = 8; p.r <= kLoraMaxRank; p.r *= 2) {
-        cudaError_t e = by_rank<true>(p, 0, nullptr, true);
-        if (e == cudaSuccess) e = by_rank<false>(p, 0, nullptr, true);
+        cudaError_t e = by_rank<true>(p, 0, 1, nullptr, true);
+        if (e == cudaSuccess) e = by_rank<false>(p, 0, 1, nullptr, true);
         if (e != cudaSuccess) return e;
     }
     return cudaSuccess;

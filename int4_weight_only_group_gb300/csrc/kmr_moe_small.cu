@@ -20,6 +20,7 @@
 
 #include "kmr_int4_mma.cuh"
 #include "kmr_moe.cuh"
+#include "kmr_tc.cuh"
 
 namespace kmr {
 
@@ -65,29 +66,27 @@ struct Frag {
     uint32_t b[16];
     float X0, is0, X1, is1;  // of columns 2t and 2t + 1: sum of the staged values, 1 / sigma
 };
-// row: this lane's row (column lane / 4, SPLIT: (lane / 4) % 4 with the remainders in columns 4..7) at the group's
-// first input, or null.
-template <typename IN, bool SPLIT>
-__device__ __forceinline__ void load_frag(Frag& f, const IN* row, int lane) {
+// This lane's inputs of one group: row (column lane / 4, SPLIT: (lane / 4) % 4 with the remainders in columns 4..7) at the
+// group's first input.  A lane without a row reads another's and takes zeros, so that all loads go out together.
+template <typename IN>
+__device__ __forceinline__ void load_raw(float (&v)[32], const IN* row, bool real, int lane) {
     const int t = lane & 3;
-    float v[32];
 #pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            float2 u = make_float2(0.f, 0.f);
-            if (row) {
-                if constexpr (sizeof(IN) == 4) {
-                    u = __ldcg(reinterpret_cast<const float2*>(row + 16 * ks + 8 * h + 2 * t));
-                } else {
-                    const uint32_t r = __ldcg(reinterpret_cast<const uint32_t*>(row + 16 * ks + 8 * h + 2 * t));
-                    u = make_float2(bf16_lo(r), bf16_hi(r));
-                }
-            }
-            v[4 * ks + 2 * h] = u.x;
-            v[4 * ks + 2 * h + 1] = u.y;
+    for (int i = 0; i < 16; ++i) {
+        float2 u;
+        if constexpr (sizeof(IN) == 4) {
+            u = __ldcg(reinterpret_cast<const float2*>(row + 8 * i + 2 * t));
+        } else {
+            const uint32_t r = __ldcg(reinterpret_cast<const uint32_t*>(row + 8 * i + 2 * t));
+            u = make_float2(bf16_lo(r), bf16_hi(r));
         }
+        v[2 * i] = real ? u.x : 0.f;
+        v[2 * i + 1] = real ? u.y : 0.f;
     }
+}
+template <bool SPLIT>
+__device__ __forceinline__ void make_frag(Frag& f, const float (&v)[32], int lane) {
+    const int t = lane & 3;
     float m = 0.f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
@@ -100,9 +99,10 @@ __device__ __forceinline__ void load_frag(Frag& f, const IN* row, int lane) {
     for (int i = 0; i < 16; ++i) {
         const float a = __fmul_rn(v[2 * i], sig), b = __fmul_rn(v[2 * i + 1], sig);
         __half2 h = __floats2half2_rn(a, b);
-        if (SPLIT && lane >= 16) {
+        if (SPLIT) {
             const float2 r = __half22float2(h);
-            h = __floats2half2_rn(__fsub_rn(a, r.x), __fsub_rn(b, r.y));
+            const __half2 l = __floats2half2_rn(__fsub_rn(a, r.x), __fsub_rn(b, r.y));
+            h = lane >= 16 ? l : h;
         }
         const float2 s = __half22float2(h);
         X = __fadd_rn(X, __fadd_rn(s.x, s.y));
@@ -167,24 +167,15 @@ struct Ring {
     uint64_t* full;
     int tile_bytes, stages;
 };
-template <typename Addr>
-__device__ __forceinline__ void fetch(const Ring& r, int from, int to, Addr&& addr, uint64_t pol) {
-    for (int i = from; i < to; ++i) {
-        const int s = i % r.stages;
-        mbar_arrive_expect_tx(&r.full[s], uint32_t(r.tile_bytes));
-        bulk_g2s_stream(r.data + size_t(s) * r.tile_bytes, addr(i), uint32_t(r.tile_bytes), &r.full[s], pol);
-    }
+__device__ __forceinline__ void fetch(const Ring& r, int i, const uint8_t* from, uint64_t pol) {      // by warp 0
+    if (!elect_one()) return;
+    const int s = i % r.stages;
+    mbar_arrive_expect_tx(&r.full[s], uint32_t(r.tile_bytes));
+    bulk_g2s_stream(r.data + size_t(s) * r.tile_bytes, from, uint32_t(r.tile_bytes), &r.full[s], pol);
 }
 
 __device__ __forceinline__ float silu_mul(float x, float up) {
     return __fmul_rn(__fdiv_rn(x, __fadd_rn(1.f, expf(-x))), up);
-}
-
-// Sum over the lanes of a half warp, the same order on every lane.
-__device__ __forceinline__ float half_sum(float v) {
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) v = __fadd_rn(v, __shfl_xor_sync(kFull, v, o));
-    return v;
 }
 
 // ------------------------------------------------------------------ gate_up
@@ -212,13 +203,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
     auto expert = [&](int i) { return __shfl_sync(kFull, pl.id, nth_bit(pl.leaders, u0 + (r0 + i) / tiles)); };
     __syncthreads();
     const uint64_t pol = policy_evict_first();
-    auto fill = [&](int from, int to) {                 // warp 0; lane 0 copies
-        for (int i = from; i < to; ++i) {
-            const int e = expert(i);
-            if (lane == 0)
-                fetch(ring, i, i + 1,
-                      [&](int j) { return p.w.gate_up + (size_t(e) * tiles + (r0 + j) % tiles) * ring.tile_bytes; }, pol);
-        }
+    auto fill = [&](int from, int to) {                 // warp 0
+        for (int i = from; i < to; ++i)
+            fetch(ring, i, p.w.gate_up + (size_t(expert(i)) * tiles + (r0 + i) % tiles) * ring.tile_bytes, pol);
     };
     if (warp == 0) fill(0, min(n, p.stages));
     Frag f[GPW];
@@ -242,15 +229,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
                     const int place = col < cols ? nth_bit(places, ps * CAP + col) : -1;
 #pragma unroll
                     for (int j = 0; j < GPW; ++j) {
-                        const int grp = wg + j * kWarps;
-                        const IN* row = place >= 0 && grp < G
-                                            ? static_cast<const IN*>(p.x) + size_t(place / p.k) * p.w.H + size_t(grp) * 128
-                                            : nullptr;
-                        load_frag<IN, SPLIT>(f[j], row, lane);
+                        const int grp = min(wg + j * kWarps, G - 1);
+                        float v[32];
+                        load_raw(v, static_cast<const IN*>(p.x) + size_t(max(place, 0) / p.k) * p.w.H + size_t(grp) * 128, place >= 0, lane);
+                        make_frag<SPLIT>(f[j], v, lane);
                     }
                 }
                 const int s = i % p.stages;
-                if (!mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err)) continue;
+                if (!__all_sync(kFull, mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err))) continue;
                 const uint8_t* tile = ring.data + size_t(s) * ring.tile_bytes;
                 float acc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -259,24 +245,29 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
                 store_part8(part + (size_t(i - b0) * GW + wg) * 128, lane, acc);
             }
             __syncthreads();
-            // one (tile, row pair, column) a warp at a time: lanes 0..15 sum the gate's partials, 16..31 the up's
+            // two (row, column) of a tile a warp at a time, eight lanes for each row of its gate and its up: a lane sums two of the
+            // (at most 16) partials, then the eight lanes' sums meet
+            int done = 0;                               // (row, column) pairs of the tiles before
             for (int i = 0; i < nb; ++i) {
-                const int e = expert(b0 + i);
-                const uint32_t places = __ballot_sync(kFull, pl.id == e);
-                const int cols = min(CAP, __popc(places) - ps * CAP);
+                const uint32_t places = __ballot_sync(kFull, pl.id == expert(b0 + i));
+                const int cols = max(0, min(CAP, __popc(places) - ps * CAP));
                 const int jt = (r0 + b0 + i) % tiles;
-                for (int o = warp; o < 8 * cols; o += kWarps) {
-                    const int r = o & 7, c = o >> 3, w = lane & 15;
+                for (int o = 2 * ((warp - (done >> 1)) & (kWarps - 1)); o < 8 * cols; o += 2 * kWarps) {
+                    const int r = (o & 7) + (lane >> 4), c = o >> 3, w = lane & 7;
+                    const float* at = part + size_t(i) * GW * 128 + (r + ((lane >> 3) & 1) * 8) * 8 + c;
                     float v = 0.f;
-                    if (w < GW && w < G) {
-                        const float* at = part + (size_t(i) * GW + w) * 128 + (r + (lane >> 4) * 8) * 8 + c;
-                        v = SPLIT ? __fadd_rn(at[0], at[4]) : at[0];
+                    if (w < GW && w < G) v = SPLIT ? __fadd_rn(at[w * 128], at[w * 128 + 4]) : at[w * 128];
+                    if (w + 8 < GW && w + 8 < G) {
+                        const float* b = at + (w + 8) * 128;
+                        v = __fadd_rn(v, SPLIT ? __fadd_rn(b[0], b[4]) : b[0]);
                     }
-                    v = half_sum(v);
-                    const float up = __shfl_sync(kFull, v, 16);
-                    const int place = nth_bit(places, ps * CAP + c);
-                    if (lane == 0) p.act[size_t(place) * p.w.I + jt * 8 + r] = silu_mul(v, up);
+                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 4));
+                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 2));
+                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 1));
+                    const float up = __shfl_sync(kFull, v, lane + 8);
+                    if ((lane & 15) == 0) p.act[size_t(nth_bit(places, ps * CAP + c)) * p.w.I + jt * 8 + r] = silu_mul(v, up);
                 }
+                done += 8 * cols;
             }
             __syncthreads();
         }
@@ -307,13 +298,10 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
     const int n = __popc(pl.leaders);
     __syncthreads();
     const uint64_t pol = policy_evict_first();
-    auto fill = [&](int from, int to) {                 // warp 0; lane 0 copies
-        for (int i = from; i < to; ++i) {
-            const int e = __shfl_sync(kFull, pl.id, nth_bit(pl.leaders, i));
-            if (lane == 0)
-                fetch(ring, i, i + 1,
-                      [&](int) { return p.w.down + (size_t(e) * tiles + blockIdx.x) * ring.tile_bytes; }, pol);
-        }
+    auto fill = [&](int from, int to) {                 // warp 0
+        for (int i = from; i < to; ++i)
+            fetch(ring, i, p.w.down + (size_t(__shfl_sync(kFull, pl.id, nth_bit(pl.leaders, i))) * tiles + blockIdx.x) * ring.tile_bytes,
+                  pol);
     };
     if (warp == 0) fill(0, min(n, p.stages));
     pdl_wait();
@@ -326,7 +314,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
             const uint32_t places = __ballot_sync(kFull, pl.id == e);
             const int used = __popc(places);
             const int s = i % p.stages;
-            bool there = false;
+            if (!__all_sync(kFull, mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err))) continue;
             for (int c0 = 0; c0 < used; c0 += CAP) {
                 const int col = SPLIT ? (lane >> 2) & 3 : lane >> 2;
                 const int place = c0 + col < used ? nth_bit(places, c0 + col) : -1;
@@ -336,9 +324,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
                     const int grp = wg + j * kWarps;
                     if (grp >= G) break;
                     Frag f;
-                    load_frag<float, SPLIT>(f, place >= 0 ? p.act + size_t(place) * p.w.I + size_t(grp) * 128 : nullptr, lane);
-                    if (!there && !mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err)) break;
-                    there = true;
+                    float v[32];
+                    load_raw(v, p.act + size_t(max(place, 0)) * p.w.I + size_t(grp) * 128, place >= 0, lane);
+                    make_frag<SPLIT>(f, v, lane);
                     block_product(ring.data + size_t(s) * ring.tile_bytes + grp * kGroupBytes, f, lane, acc);
                 }
                 // columns 2t and 2t + 1 of rows g and g + 8; the remainders' columns add to their token's
@@ -402,15 +390,18 @@ const void* small_fn(bool down, bool bf16, int K) {
 #undef KMR_SMALL
 }
 
-// Ring of `most` tiles at the most, a batch being half of it; `per_tile` and `fixed` bytes beside the tiles.
+// Ring of `most` tiles at the most, one batch where all of them fit and else two; `per_batch_tile` bytes for each tile of a batch
+// and `fixed` bytes beside the tiles.
 size_t plan_ring(int most, int K, size_t per_batch_tile, size_t fixed, int* stages, int* batch) {
     const size_t tile = size_t(K / 128) * kGroupBytes;
-    auto bytes = [&](int st) { return st * tile + (st + (st & 1)) * 8 + ((st + 1) / 2) * per_batch_tile + fixed; };
-    int st = most < 2 ? 2 : most + (most & 1);
-    while (st > 2 && bytes(st) > kSmem) st -= 2;
+    auto bytes = [&](int st, int batch) { return st * tile + (st + (st & 1)) * 8 + batch * per_batch_tile + fixed; };
+    *stages = *batch = most;
+    if (bytes(most, most) <= kSmem) return bytes(most, most);
+    int st = most + (most & 1);
+    while (st > 2 && bytes(st, st / 2) > kSmem) st -= 2;
     *stages = st;
     *batch = st / 2;
-    return bytes(st);
+    return bytes(st, st / 2);
 }
 
 }  // namespace
