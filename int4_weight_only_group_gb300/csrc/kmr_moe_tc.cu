@@ -267,7 +267,9 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
 }
 
 // ------------------------------------------------------------------ the grouped product
-constexpr int kUnpackWarps = 8, kTokenWarp = 10, kEpiWarp = 11, kEpiWarps = 4;
+// warps 0, 1, 2: weights, MMA, tokens; then the unpack warps and the epilogue warps, from multiples of four on (a warp reaches the
+// quarter warp % 4 of the tensor memory's lanes)
+constexpr int kTokenWarp = 2, kUnpackWarp = 4, kUnpackWarps = 8, kEpiWarp = kUnpackWarp + kUnpackWarps, kEpiWarps = 8;
 constexpr int kThr = (kEpiWarp + kEpiWarps) * 32;
 constexpr uint32_t kSmem = 227 * 1024;
 
@@ -365,9 +367,8 @@ struct Turn {
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
-// Roles.  Groups are handed over in pairs.  The unpack warps are two sets of four (one warp per quarter of
-// the tensor memory's lanes), one for each group of a pair: the chain wait - load - convert - store - hand over of one group
-// takes longer than its share of the issue slots, and two of them overlap.
+// Roles.  Groups are handed over in pairs; two unpack warps share each quarter of the tensor memory's lanes, one for each group of
+// the pair (four, for half a group each, were slower: the hand-overs' instructions double).
 template <int NP, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -534,9 +535,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 tile = ahead;
             }
         }
-    } else if (warp < kTokenWarp) {
+    } else if (warp >= kUnpackWarp && warp < kEpiWarp) {
         // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, one group of each pair
-        const int lq = warp & 3, set = (warp - 2) >> 2, g8 = lane >> 2;
+        const int lq = warp & 3, set = (warp - kUnpackWarp) >> 2, g8 = lane >> 2;
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
         // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero point this lane writes)
@@ -575,7 +576,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                 }
                 if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
-                const uint32_t z2 = u2(__float2half2_rn(__fmul_rn(bf16_hi(zrow) * 0x1p-18f, rr[4])));
+                const float z = __fmul_rn(bf16_hi(zrow) * 0x1p-18f, rr[4]);
+                const uint32_t z2 = u2(__floats2half2_rn(z, z));
                 *reinterpret_cast<uint2*>(zto + ta.s * kZBytes) = make_uint2(z2, z2);
                 if (g < G) {
                     tc_fence_after();
@@ -583,8 +585,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     for (int h = 0; h < 2; ++h) {
                         // of rows g8 and g8 + 8: s rho, its 16th for the nibble one place up, and -8 of it 2^-24
                         const float r0 = __fmul_rn(bf16_lo(sz[2 * h]), rr[2 * h]), r1 = __fmul_rn(bf16_lo(sz[2 * h + 1]), rr[2 * h + 1]);
-                        const __half2 s0 = __float2half2_rn(r0), n0 = __float2half2_rn(r0 * -0x1p-21f);
-                        const __half2 s1 = __float2half2_rn(r1 * 0x1p-4f), n1 = __float2half2_rn(r1 * -0x1p-21f);
+                        const __half2 s0 = __floats2half2_rn(r0, r0), n0 = __floats2half2_rn(r0 * -0x1p-21f, r0 * -0x1p-21f);
+                        const __half2 s1 = __floats2half2_rn(r1 * 0x1p-4f, r1 * 0x1p-4f), n1 = __floats2half2_rn(r1 * -0x1p-21f, r1 * -0x1p-21f);
                         const uint32_t acol = taddr + 256 + ta.s * 128 + set * 64 + (uint32_t(32 * lq + 16 * h) << 16);
 #pragma unroll
                         for (int kj = 0; kj < 2; ++kj) {
@@ -614,8 +616,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             }
         }
     } else if (warp >= kEpiWarp) {
-        // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its weight rows), all tokens
-        const int q = warp & 3, et = tid - kEpiWarp * 32;
+        // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its weight rows), every second sixteen of the tokens
+        const int q = warp & 3, et = tid - kEpiWarp * 32, half = (warp - kEpiWarp) >> 2;
         float* fac = reinterpret_cast<float*>(smem + L.fac);       // [2][2][128]
         uint8_t* tbuf = smem + L.tile;
         Turn td;
@@ -681,7 +683,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 tc_fence_after();
                 const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
 #pragma unroll 1
-                for (int c0 = 0; c0 < n && ok; c0 += 16) {
+                for (int c0 = half * 16; c0 < n && ok; c0 += 32) {
                     float v[16];
                     tc_ld16(acc + uint32_t(c0), v);
                     finish(c0, v);
@@ -692,9 +694,10 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 td.next(DB);
             } else {
                 // per group: the first terms' columns and the remainders', n further on
-                float sum[kTileTokens<NP> / 16][16];
+                constexpr int kSums = kTileTokens<NP> / 32;
+                float sum[kSums][16];
 #pragma unroll
-                for (int i = 0; i < kTileTokens<NP> / 16; ++i)
+                for (int i = 0; i < kSums; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
 #pragma unroll 1
@@ -703,16 +706,16 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     tc_fence_after();
                     const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
 #pragma unroll
-                    for (int i = 0; i < kTileTokens<NP> / 16; ++i) {
-                        if (i * 16 >= n || !ok) continue;
-                        uint32_t v[16], w[16];
-                        tc_ld16_issue(acc + uint32_t(i * 16), v);
-                        tc_ld16_issue(acc + uint32_t(n + i * 16), w);
-                        tc_wait_ld16(v);
-                        tc_wait_ld16(w);
+                    for (int i = 0; i < kSums; ++i) {
+                        const int c0 = i * 32 + half * 16;
+                        if (c0 >= n || !ok) continue;
+                        float v[16];
+                        tc_ld16(acc + uint32_t(c0), v);
 #pragma unroll
-                        for (int j = 0; j < 16; ++j)
-                            sum[i][j] = __fadd_rn(sum[i][j], __fadd_rn(__uint_as_float(v[j]), __uint_as_float(w[j])));
+                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
+                        tc_ld16(acc + uint32_t(n + c0), v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
                     }
                     tc_fence_before();
                     __syncwarp();
@@ -723,10 +726,10 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 if (it + step < items) factors(it + step, ahead);
                 // (one copy of the code: the sums move down instead)
 #pragma unroll 1
-                for (int c0 = 0; c0 < n && ok; c0 += 16) {
+                for (int c0 = half * 16; c0 < n && ok; c0 += 32) {
                     finish(c0, sum[0]);
 #pragma unroll
-                    for (int i = 0; i + 1 < kTileTokens<NP> / 16; ++i)
+                    for (int i = 0; i + 1 < kSums; ++i)
 #pragma unroll
                         for (int j = 0; j < 16; ++j) sum[i][j] = sum[i + 1][j];
                 }
