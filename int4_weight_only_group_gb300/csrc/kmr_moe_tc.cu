@@ -367,8 +367,10 @@ struct Turn {
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
-// Roles.  Groups are handed over in pairs; two unpack warps share each quarter of the tensor memory's lanes, one for each group of
-// the pair (four, for half a group each, were slower: the hand-overs' instructions double).
+// Roles.  Groups are handed over in pairs.  The unpack warps are two sets of four (one warp per quarter of the tensor memory's
+// lanes) on alternate pairs, each with its own place in tensor memory: one set's waits and hand-over, some 900 cycles, fall
+// under the other's arithmetic.  (Both sets on the two groups of one pair wait and work in step: 1650 cycles a pair instead of
+// 1000; twice as many warps doubled the hand-overs' instructions.)
 template <int NP, bool GATE>
 __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -397,14 +399,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         *abort_flag = 0;
         for (int s = 0; s < kWS; ++s) {
             mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], kUnpackWarps);
+            mbar_init(&w_empty[s], kUnpackWarps / 2);
         }
         for (int s = 0; s < BS; ++s) {
             mbar_init(&b_full[s], 1);
             mbar_init(&b_empty[s], 1);
         }
         for (int s = 0; s < kAQ; ++s) {
-            mbar_init(&a_full[s], kUnpackWarps);
+            mbar_init(&a_full[s], kUnpackWarps / 2);
             mbar_init(&a_empty[s], 1);
         }
         for (int s = 0; s < DB; ++s) {
@@ -536,19 +538,22 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             }
         }
     } else if (warp >= kUnpackWarp && warp < kEpiWarp) {
-        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, one group of each pair
+        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, every second pair of groups
         const int lq = warp & 3, set = (warp - kUnpackWarp) >> 2, g8 = lane >> 2;
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
-        // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero point this lane writes)
+        auto dup = [&](float v) { return __floats2half2_rn(v, v); };
+        // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero points this lane writes)
         auto factors = [&](int it, const int4& tile, float (&to)[5]) {
             const float* at = rho + size_t(tile.x) * N + (it % R) * kRows + 32 * lq;
 #pragma unroll
             for (int i = 0; i < 4; ++i) to[i] = at[g8 + 8 * i];
             to[4] = at[lane];
         };
-        uint8_t* zto = smem + L.z + (4 * lq + (lane >> 3)) * 128 + (lane & 7) * 16 + set * 8;
-        Turn tt, ta;
+        uint8_t* zto = smem + L.z + set * kZBytes + (4 * lq + (lane >> 3)) * 128 + (lane & 7) * 16;
+        const uint32_t aset = taddr + 256 + set * 128 + (uint32_t(32 * lq) << 16);
+        Turn tt;
+        uint32_t pair = 0, mine = 0;                       // pairs so far: all of them, and this set's
         float rr[5] = {1.f, 1.f, 1.f, 1.f, 1.f}, rnext[5] = {1.f, 1.f, 1.f, 1.f, 1.f};
         int4 ahead = tile_of(blockIdx.x);
         if (int(blockIdx.x) < items) factors(blockIdx.x, ahead, rnext);
@@ -557,37 +562,37 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             for (int i = 0; i < 5; ++i) rr[i] = rnext[i];
             ahead = tile_of(it + step);
 #pragma unroll 1
-            for (int g0 = 0; g0 < G && ok; g0 += 2) {
-                const int both = min(2, G - g0), g = g0 + set;
+            for (int g0 = 0; g0 < G; g0 += 2, ++pair, tt.next(kWS)) {
                 if (g0 + 2 >= G && it + step < items) factors(it + step, ahead, rnext);
+                if (int(pair & 1) != set) continue;
+                const int both = min(2, G - g0);
                 if (!(ok = warp_wait(&w_full[tt.s], tt.full()))) break;
-                const uint8_t* wst = smem + L.w + tt.s * kWBytes + (2 * lq * both + set) * kGroupBytes;
-                uint32_t sz[4], zrow = 0u;
+                const uint8_t* wst = smem + L.w + tt.s * kWBytes + 2 * lq * both * kGroupBytes;
+                // a group's words, scales and this lane's zero point
                 uint4 wq[4];
-                if (g < G) {
-                    zrow = *reinterpret_cast<const uint32_t*>(wst + (lane >> 4) * both * kGroupBytes + 1024 + (lane & 15) * 4);
+                uint32_t sz[4], zrow[2] = {0u, 0u};
+                auto fetch = [&](int j) {
+                    zrow[j] = *reinterpret_cast<const uint32_t*>(wst + ((lane >> 4) * both + j) * kGroupBytes + 1024 + (lane & 15) * 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint8_t* blk = wst + h * both * kGroupBytes;
+                        const uint8_t* blk = wst + (h * both + j) * kGroupBytes;
                         sz[2 * h] = *reinterpret_cast<const uint32_t*>(blk + 1024 + g8 * 4);
                         sz[2 * h + 1] = *reinterpret_cast<const uint32_t*>(blk + 1024 + (g8 + 8) * 4);
                         wq[2 * h] = *reinterpret_cast<const uint4*>(blk + lane * 16);
                         wq[2 * h + 1] = *reinterpret_cast<const uint4*>(blk + 512 + lane * 16);
                     }
-                }
-                if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
-                const float z = __fmul_rn(bf16_hi(zrow) * 0x1p-18f, rr[4]);
-                const uint32_t z2 = u2(__floats2half2_rn(z, z));
-                *reinterpret_cast<uint2*>(zto + ta.s * kZBytes) = make_uint2(z2, z2);
-                if (g < G) {
-                    tc_fence_after();
+                };
+                fetch(0);
+                if (mine > 0 && !(ok = warp_wait(&a_empty[set], (mine - 1) & 1))) break;
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = 0; j < both; ++j) {
+                    if (j > 0) fetch(1);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         // of rows g8 and g8 + 8: s rho, its 16th for the nibble one place up, and -8 of it 2^-24
                         const float r0 = __fmul_rn(bf16_lo(sz[2 * h]), rr[2 * h]), r1 = __fmul_rn(bf16_lo(sz[2 * h + 1]), rr[2 * h + 1]);
-                        const __half2 s0 = __floats2half2_rn(r0, r0), n0 = __floats2half2_rn(r0 * -0x1p-21f, r0 * -0x1p-21f);
-                        const __half2 s1 = __floats2half2_rn(r1 * 0x1p-4f, r1 * 0x1p-4f), n1 = __floats2half2_rn(r1 * -0x1p-21f, r1 * -0x1p-21f);
-                        const uint32_t acol = taddr + 256 + ta.s * 128 + set * 64 + (uint32_t(32 * lq + 16 * h) << 16);
+                        const __half2 s0 = dup(r0), n0 = dup(r0 * -0x1p-21f), s1 = dup(r1 * 0x1p-4f), n1 = dup(r1 * -0x1p-21f);
 #pragma unroll
                         for (int kj = 0; kj < 2; ++kj) {
                             const uint4 q4 = wq[2 * h + kj];
@@ -601,18 +606,20 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                                 v[4 * k + 2] = u2(__hfma2(h2(w & 0x00F000F0u), s1, n1));
                                 v[4 * k + 3] = u2(__hfma2(h2(wh & 0x00F000F0u), s1, n1));
                             }
-                            tmem_store4(acol + kj * 32, v);
+                            tmem_store4(aset + j * 64 + kj * 32 + (uint32_t(16 * h) << 16), v);
                         }
                     }
                 }
+                const uint32_t z0 = u2(dup(__fmul_rn(bf16_hi(zrow[0]) * 0x1p-18f, rr[4])));
+                const uint32_t z1 = u2(dup(__fmul_rn(bf16_hi(zrow[1]) * 0x1p-18f, rr[4])));
+                *reinterpret_cast<uint4*>(zto) = make_uint4(z0, z0, z1, z1);
                 if (lane == 0) mbar_arrive(&w_empty[tt.s]);    // (all lanes' loads have been used by the stores above)
                 fence_proxy_async_smem();                      // the MMA reads the zero points through the async proxy
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&a_full[ta.s]);
-                tt.next(kWS);
-                ta.next(kAQ);
+                if (lane == 0) mbar_arrive(&a_full[set]);
+                ++mine;
             }
         }
     } else if (warp >= kEpiWarp) {
