@@ -198,6 +198,12 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
                     w[u][j] = real && n < rank_a ? *reinterpret_cast<const uint2*>(A + size_t(n) * p.K + k) : make_uint2(0u, 0u);
                 }
             }
+            // (the tensor cores cut a running sum off rather than round it: fp32 sums are taken over in short runs)
+            float c[RT][4];
+            if (!BF16) {
+#pragma unroll
+                for (int j = 0; j < RT; ++j) clear4(c[j]);
+            }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 if constexpr (BF16) {
@@ -213,9 +219,15 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
                         uint32_t A0[4];
                         term_of(fa, fb, A0);
 #pragma unroll
-                        for (int j = 0; j < RT; ++j) mma_bf16(d[j], A0, w[u][j].x, w[u][j].y);
+                        for (int j = 0; j < RT; ++j) mma_bf16(c[j], A0, w[u][j].x, w[u][j].y);
                     }
                 }
+            }
+            if (!BF16) {
+#pragma unroll
+                for (int j = 0; j < RT; ++j)
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) d[j][q] = __fadd_rn(d[j][q], c[j][q]);
             }
         }
 #pragma unroll

@@ -56,7 +56,7 @@ struct MoeTcParams {
     const float* weights;                    // [T][k]
     int T, k, cap;                           // tokens of a tile: 16, 32, 64 or 128
     int* ntiles;
-    int4* tiles;                             // (expert, first position, tokens, -)
+    int4* tiles;                             // (expert, first position, tokens with padding, tokens)
     int32_t* pos;                            // [T][k]: the place's position, or -1
     float* isx;                              // [P] 1 / scale of the position's inputs
     float* sact;                             // [P] scale of its activations

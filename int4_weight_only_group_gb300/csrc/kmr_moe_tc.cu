@@ -118,8 +118,8 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     if (nt > 0) {
         const int each = ((n16 + nt - 1) / nt + 15) & ~15;           // even tiles, whole sixteens
         for (int i = 0; i < nt; ++i) {
-            const int len = min(each, n16 - i * each);
-            p.tiles[t0 + i] = make_int4(tid, p0 + i * each, max(len, 0), 0);
+            const int len = min(each, n16 - i * each);               // (above 0: each is at most cap)
+            p.tiles[t0 + i] = make_int4(tid, p0 + i * each, len, min(len, n - i * each));
         }
     }
     if (tid == kPlanThr - 1) *p.ntiles = pb + b;
@@ -302,12 +302,10 @@ static_assert(layout(true).total <= kSmem, "shared memory");
 // A stage of the token ring: two groups of `cap` tokens, and their sums.
 __host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 512u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
 
-// Shared-memory matrix descriptor: K-major, 128-byte swizzle, `stride` bytes between blocks of 8 rows.
-__device__ __forceinline__ uint64_t swizzled_desc(uint32_t addr, uint32_t stride) {
-    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t(1) << 16) | (uint64_t((stride >> 4) & 0x3FFFu) << 32) |
-           (uint64_t(1) << 46) | (uint64_t(2) << 61);
-}
-// ... no swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
+// Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 4 KB apart): the upper half is this
+// constant, the lower the address and 1 << 16.
+constexpr uint32_t kSwizzledHi = (4096u >> 4) | (1u << 14) | (2u << 29);
+// No swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
 __device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t further) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((further >> 4) & 0x3FFFu) << 16) | (uint64_t(128 >> 4) << 32) |
            (uint64_t(1) << 46);
@@ -338,18 +336,32 @@ __device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t by
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
                  : "memory");
 }
+__device__ __forceinline__ void commit_at(uint32_t bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool try_at(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
+}
 // Bounded wait; gives up at once when another warp has.
-__device__ __forceinline__ bool wait_or_abort(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err) {
-    if (mbar_try_wait(b, parity)) return true;
+__device__ __forceinline__ bool wait_at(uint32_t b, uint32_t parity, volatile int* abort_flag, int* err) {
+    if (try_at(b, parity)) return true;
     const long long c0 = clock64();
     for (uint32_t it = 1; it < (1u << 28); ++it) {
-        if (mbar_try_wait(b, parity)) return true;
+        if (try_at(b, parity)) return true;
         if (*abort_flag) return false;
         if (clock64() - c0 > 4000000000ll) break;
     }
     set_error(err, KMR_ERR_DEVICE_TIMEOUT);
     *abort_flag = 1;
     return false;
+}
+__device__ __forceinline__ bool wait_or_abort(uint64_t* b, uint32_t parity, volatile int* abort_flag, int* err) {
+    return wait_at(smem_u32(b), parity, abort_flag, err);
 }
 
 // A stage of a ring and how often the ring has come round.
@@ -497,43 +509,73 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         }
     } else if (warp == 1) {
         // ---- MMA issue, by one elected thread (elect.sync: with `lane == 0` the compiler does not know that the operands are
-        // uniform, and an MMA takes 55 cycles to issue instead of 6)
+        // uniform, and an MMA takes 55 cycles to issue instead of 6).  Alone on its path it takes some 6 cycles an instruction, so
+        // everything that can be is kept in running registers: a loop of Turns and pointers took 1600 cycles a pair.
         if (elect_one()) {
-            Turn ta, tt, td;
+            const uint32_t bars = smem_u32(b_full), bfull = bars, bempty = bars + 8 * kMaxStages, afull = smem_u32(a_full),
+                           aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
+            const uint32_t blo0 = ((sbase >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
+            const uint32_t z = sbase + L.z, xoff = dcols * 512u, zeros = z + 2 * kZBytes;
+            const uint64_t zd[2] = {plain_desc(z, 2 * kZBytes), plain_desc(z + kZBytes, kZBytes)};
+            uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
+            auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
+            auto eight = [&](uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
+                const uint64_t desc = (uint64_t(kSwizzledHi) << 32) | lo;
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
+            };
+            auto hand_over = [&]() {                       // the accumulator to the epilogue
+                commit_at(dfull + 8 * ds);
+                acc += dcols;
+                if (++ds == uint32_t(DB)) {
+                    ds = 0;
+                    dph ^= 1;
+                    acc = taddr;
+                }
+            };
             int4 tile = tile_of(blockIdx.x);
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
                 const uint32_t idesc = tc_idesc(kRows, NP * tile.z), sums = tc_idesc(kRows, tile.z);
+                if (!(ok = wait(dempty + 8 * ds, dph))) break;
                 uint32_t begun = 0;                        // the accumulator holds something
 #pragma unroll 1
-                for (int g = 0; g < G && ok; g += 2) {
-                    const int both = min(2, G - g);
-                    ok = one_wait(&b_full[tt.s], tt.full()) && one_wait(&a_full[ta.s], ta.full());
-#pragma unroll 1
-                    for (int h = 0; h < both && ok; ++h) {
-                        if (!begun && td.waits() && !(ok = one_wait(&d_empty[td.s], td.empty()))) break;
-                        tc_fence_after();
-                        const uint32_t b = sbase + tt.s * bstage, a = taddr + 256 + ta.s * 128 + h * 64, acc = taddr + td.s * dcols;
-                        const uint64_t desc = swizzled_desc(b + h * 2048u, 4096u);
-#pragma unroll
-                        for (int ks = 0; ks < 8; ++ks)
-                            tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
-                        if (h == both - 1) {               // the pair's zero points (to the first terms' columns)
-                            const uint32_t z = sbase + L.z, zeros = z + 2 * kZBytes, x = b + dcols * 512u;
-                            mma_ss(acc, plain_desc(z + ta.s * kZBytes, (2 - ta.s) * kZBytes), plain_desc(x, zeros - x), sums);
+                for (int g = 0; g < G; g += 2) {
+                    if (!(ok = wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
+                    tc_fence_after();
+                    const uint32_t a = taddr + 256 + as * 128;
+                    eight(a, blo, idesc, begun);
+                    if (g + 1 < G) {
+                        if (NP == 2) {
+                            hand_over();
+                            if (!(ok = wait(dempty + 8 * ds, dph))) break;
+                            tc_fence_after();
                         }
-                        begun = 1;
-                        if (NP == 2 || g + h + 1 == G) {
-                            tc_commit(&d_full[td.s]);
-                            td.next(DB);
-                            begun = 0;
-                        }
+                        eight(a + 64, blo + 128, idesc, NP == 2 ? 0u : 1u);
                     }
-                    tc_commit(&a_empty[ta.s]);
-                    tc_commit(&b_empty[tt.s]);
-                    ta.next(kAQ);
-                    tt.next(BS);
+                    // the pair's zero points (to the first terms' columns)
+                    const uint32_t x = sbase + bs * bstage + xoff;
+                    mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), sums);
+                    commit_at(aempty + 8 * as);
+                    commit_at(bempty + 8 * bs);
+                    begun = 1;
+                    if (NP == 2 && g + 2 < G) {
+                        hand_over();
+                        if (!(ok = wait(dempty + 8 * ds, dph))) break;
+                        begun = 0;
+                    }
+                    as ^= 1;
+                    aph ^= as ^ 1;
+                    blo += bstep;
+                    if (++bs == uint32_t(BS)) {
+                        bs = 0;
+                        bph ^= 1;
+                        blo = blo0;
+                    }
                 }
+                if (!ok) break;
+                hand_over();
                 tile = ahead;
             }
         }
@@ -552,8 +594,12 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         };
         uint8_t* zto = smem + L.z + set * kZBytes + (4 * lq + (lane >> 3)) * 128 + (lane & 7) * 16;
         const uint32_t aset = taddr + 256 + set * 128 + (uint32_t(32 * lq) << 16);
-        Turn tt;
-        uint32_t pair = 0, mine = 0;                       // pairs so far: all of them, and this set's
+        // this set's pairs are number set, set + 2, ... of all: their stage of the weight ring, its parity, the place's parity
+        static_assert(kWS == 3, "stages are stepped two at a time below");
+        uint32_t ws = set, wph = 0, aph = 1;
+        int skip = set;                                    // pairs of the item that come before this set's next
+        const int pairs = (G + 1) >> 1;
+        const uint32_t wfull = smem_u32(w_full), aempty = smem_u32(a_empty + set);
         float rr[5] = {1.f, 1.f, 1.f, 1.f, 1.f}, rnext[5] = {1.f, 1.f, 1.f, 1.f, 1.f};
         int4 ahead = tile_of(blockIdx.x);
         if (int(blockIdx.x) < items) factors(blockIdx.x, ahead, rnext);
@@ -561,13 +607,13 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
             for (int i = 0; i < 5; ++i) rr[i] = rnext[i];
             ahead = tile_of(it + step);
+            int pr = skip;
 #pragma unroll 1
-            for (int g0 = 0; g0 < G; g0 += 2, ++pair, tt.next(kWS)) {
-                if (g0 + 2 >= G && it + step < items) factors(it + step, ahead, rnext);
-                if (int(pair & 1) != set) continue;
-                const int both = min(2, G - g0);
-                if (!(ok = warp_wait(&w_full[tt.s], tt.full()))) break;
-                const uint8_t* wst = smem + L.w + tt.s * kWBytes + 2 * lq * both * kGroupBytes;
+            for (; pr < pairs; pr += 2) {
+                const int both = min(2, G - 2 * pr);
+                if (pr + 2 >= pairs && it + step < items) factors(it + step, ahead, rnext);
+                if (!(ok = __all_sync(kFull, wait_at(wfull + 8 * ws, wph, abort_flag, p.err)))) break;
+                const uint8_t* wst = smem + L.w + ws * kWBytes + 2 * lq * both * kGroupBytes;
                 // a group's words, scales and this lane's zero point
                 uint4 wq[4];
                 uint32_t sz[4], zrow[2] = {0u, 0u};
@@ -583,7 +629,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                 };
                 fetch(0);
-                if (mine > 0 && !(ok = warp_wait(&a_empty[set], (mine - 1) & 1))) break;
+                if (!(ok = __all_sync(kFull, wait_at(aempty, aph, abort_flag, p.err)))) break;
                 tc_fence_after();
 #pragma unroll 1
                 for (int j = 0; j < both; ++j) {
@@ -613,14 +659,21 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 const uint32_t z0 = u2(dup(__fmul_rn(bf16_hi(zrow[0]) * 0x1p-18f, rr[4])));
                 const uint32_t z1 = u2(dup(__fmul_rn(bf16_hi(zrow[1]) * 0x1p-18f, rr[4])));
                 *reinterpret_cast<uint4*>(zto) = make_uint4(z0, z0, z1, z1);
-                if (lane == 0) mbar_arrive(&w_empty[tt.s]);    // (all lanes' loads have been used by the stores above)
+                if (lane == 0) mbar_arrive(&w_empty[ws]);      // (all lanes' loads have been used by the stores above)
                 fence_proxy_async_smem();                      // the MMA reads the zero points through the async proxy
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&a_full[set]);
-                ++mine;
+                aph ^= 1;
+                ws += 2;
+                if (ws >= kWS) {
+                    ws -= kWS;
+                    wph ^= 1;
+                }
             }
+            if (skip >= pairs && it + step < items) factors(it + step, ahead, rnext);
+            skip = pr - pairs;
         }
     } else if (warp >= kEpiWarp) {
         // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its weight rows), every second sixteen of the tokens
@@ -632,7 +685,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         int4 tile = tile_of(blockIdx.x), ahead;
         float f0 = 0.f, f1 = 0.f, irho = 1.f;
         auto factors = [&](int it, const int4& tl) {
-            if (et < tl.z) {
+            if (et < tl.w) {
                 f0 = GATE ? p.isx[tl.y + et] : p.sact[tl.y + et];
                 if (GATE) f1 = p.sact[tl.y + et];
             }
@@ -640,9 +693,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         };
         if (int(blockIdx.x) < items) factors(blockIdx.x, tile);
         for (int it = blockIdx.x; it < items; it += step, turn ^= 1) {
-            const int r = it % R, n = tile.z;
+            const int r = it % R, n = tile.z, real = tile.w;
             float* f = fac + turn * 256;
-            if (et < n) {
+            if (et < real) {
                 f[et] = 0x1p12f * (GATE ? f0 : inverse_pow2(f0));
                 if (GATE) f[128 + et] = f1;
             }
@@ -662,6 +715,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     const int at = 2 * (i16 & 7) - (i16 & 1) + ((i16 >> 3) << 1);
 #pragma unroll
                     for (int j = 0; j < 16; j += 2) {
+                        if (c0 + j >= real) break;             // (padding: whatever the buffer holds)
                         const float xa = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
                         const float xb = __fmul_rn(v[j + 1], __fmul_rn(ir, f[c0 + j + 1]));
                         const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
@@ -678,8 +732,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                 } else {
                     float* out = p.out + size_t(tile.y + c0) * N + r * kRows + 32 * q + lane;
+                    if (c0 + 16 <= real) {
 #pragma unroll
-                    for (int j = 0; j < 16; ++j) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                        for (int j = 0; j < 16; ++j) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            if (c0 + j < real) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                    }
                 }
             };
             // (after a timeout nothing is stored any more, but the barriers are kept)
@@ -690,7 +750,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 tc_fence_after();
                 const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
 #pragma unroll 1
-                for (int c0 = half * 16; c0 < n && ok; c0 += 32) {
+                for (int c0 = half * 16; c0 < real && ok; c0 += 32) {
                     float v[16];
                     tc_ld16(acc + uint32_t(c0), v);
                     finish(c0, v);
@@ -715,7 +775,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
                     for (int i = 0; i < kSums; ++i) {
                         const int c0 = i * 32 + half * 16;
-                        if (c0 >= n || !ok) continue;
+                        if (c0 >= real || !ok) continue;
                         float v[16];
                         tc_ld16(acc + uint32_t(c0), v);
 #pragma unroll
@@ -733,7 +793,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 if (it + step < items) factors(it + step, ahead);
                 // (one copy of the code: the sums move down instead)
 #pragma unroll 1
-                for (int c0 = half * 16; c0 < n && ok; c0 += 32) {
+                for (int c0 = half * 16; c0 < real && ok; c0 += 32) {
                     finish(c0, sum[0]);
 #pragma unroll
                     for (int i = 0; i + 1 < kSums; ++i)
@@ -753,7 +813,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
-                if (ok && et < n) {
+                if (ok && et < real) {
                     // the sum of the tile's 64 activations as staged, in their order
                     float X = 0.f;
                     for (int s = 0; s < NP; ++s)
