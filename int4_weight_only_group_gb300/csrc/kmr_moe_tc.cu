@@ -40,7 +40,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                        // packed weight rows of a product (the MMA's M)
 constexpr uint32_t kWBytes = 16 * kGroupBytes;    // two groups of eight KMR4 tiles
 constexpr int kAQ = 2;                            // pairs of dequantised groups in tensor memory, 128 columns each
-constexpr int kMaxStages = 16;
+constexpr int kMaxStages = 8;
 constexpr int kMaxAcc = 8;                        // accumulators: as many as 256 columns hold
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(max(1, min(253, e + 127))) << 23); }
@@ -138,19 +138,18 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
 }
 
 // ------------------------------------------------------------------ operand layout
-// Staged rows, `blocks` blocks of 8: for every group of 128 inputs and each of the NP terms all the blocks side by side, each 2 atoms
-// of [8 rows][64 inputs] fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte swizzle), so that a
-// tile's share of a group is one run of memory.  Behind them, by pairs of groups, the sums of the four 64 inputs, [8
-// rows][8]: per group the first terms of its two sums and their remainders (zeros for the group an odd last pair lacks).
+// Staged rows, `blocks` blocks of 8: for every pair of groups of 128 inputs and each of the NP terms all the blocks side by side,
+// each 4 atoms of [8 rows][64 inputs] fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte
+// swizzle), so that a tile's share of a pair is one run of memory.  Behind them, again by pairs, the sums of the four 64 inputs,
+// [8 rows][8]: per group the first terms of its two sums and their remainders.  (The second half of an odd last pair is
+// not written and not used, but its sums are zero.)
 // Input k of 16 sits at 2 (k % 8) - k % 2 + 2 (k / 8) (the order of A's columns in tensor memory).
 __host__ __device__ constexpr int pairs_of(int K) { return (K / 128 + 1) / 2; }
-__host__ __device__ constexpr size_t staged_bytes(int K, int np, size_t blocks) {
-    return blocks * (size_t(K / 128) * np * 2048 + pairs_of(K) * 128);
-}
+__host__ __device__ constexpr size_t staged_bytes(int K, int np, size_t blocks) { return pairs_of(K) * blocks * (np * 4096 + 128); }
 __device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks, int block) {     // of 64 inputs number h
-    return ((size_t(h >> 1) * np + term) * blocks + block) * 2048 + (h & 1) * 1024;
+    return ((size_t(h >> 2) * np + term) * blocks + block) * 4096 + (h & 3) * 1024;
 }
-__device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return size_t(K / 128) * blocks * np * 2048; }
+__device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return pairs_of(K) * blocks * size_t(np) * 4096; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
 // Sum number h (of 64 inputs) of a row: its two terms.  `sums` is where the sums begin.
 __device__ __forceinline__ void put_sum(uint8_t* sums, size_t blocks, int at, int h, float X) {
@@ -246,7 +245,7 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
             const int at = pos[j], row = at & 7;
             uint8_t* to = p.xs + atom_at(k >> 6, 0, NP, blocks, at >> 3) + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 2048) = out[q];
+            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 4096) = out[q];
             if ((lane & 15) == 0) put_sum(sums, blocks, at, k >> 6, X);
         }
     }
@@ -300,12 +299,12 @@ __host__ __device__ constexpr Layout layout(bool gate) {
     return l;
 }
 static_assert(layout(true).total <= kSmem, "shared memory");
-// A stage of the token ring: a group of `cap` tokens, and room for the sums of its pair.
-__host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 256u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
+// A stage of the token ring: two groups of `cap` tokens, and their sums.
+__host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 512u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
 
 // Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 4 KB apart): the upper half is this
 // constant, the lower the address and 1 << 16.
-constexpr uint32_t kSwizzledHi = (2048u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kSwizzledHi = (4096u >> 4) | (1u << 14) | (2u << 29);
 // No swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
 __device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t further) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((further >> 4) & 0x3FFFu) << 16) | (uint64_t(128 >> 4) << 32) |
@@ -392,10 +391,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     constexpr Layout L = layout(GATE);
     const uint32_t bstage = stage_bytes(p.cap, NP);
     const int BS = min(kMaxStages, int(kRing / bstage));
-    // accumulators of a tile's tokens, and fp32's two for the remainders behind them (an item's is read with its last group's; the
-    // item after the next waits for that if it waits for an accumulator that was filled no earlier: G + 1 of them at most)
-    const int DB = min(min(kMaxAcc, 256 / NP / p.cap), NP == 2 ? G + 1 : kMaxAcc);
-    const uint32_t dcols = uint32_t(p.cap), rest = 128;
+    const int DB = min(kMaxAcc, 256 / (p.cap * NP));       // accumulators
+    const uint32_t dcols = uint32_t(p.cap) * NP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
     uint64_t* w_empty = w_full + kWS;
@@ -485,33 +482,31 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             drain(w_full, kWS, tw);
         }
     } else if (warp == kTokenWarp) {
-        // ---- staged tokens: a group's share of the tile, half a term a lane, and with every second group (and the last) the
-        // pair's sums
-        const int part = lane & 1, term = lane >> 1;
-        const size_t blocks = p.blocks;
-        const uint8_t* src = lane < 2 * NP ? bsrc + size_t(term) * blocks * 2048 : bsrc + sums_at(K, NP, blocks);
-        int4 tile = tile_of(blockIdx.x);
-        for (int it = blockIdx.x; it < items && ok; it += step) {
-            const int4 ahead = tile_of(it + step);
-            const uint32_t nb = uint32_t(tile.z) >> 3, first = uint32_t(tile.y) >> 3;
-            const uint32_t b0 = nb * part / 2, b1 = nb * (part + 1) / 2;
-            const uint32_t to = lane < 2 * NP ? (term * nb + b0) * 2048 : p.cap * 256u * NP;
-            const uint32_t bytes = lane < 2 * NP ? (b1 - b0) * 2048 : nb * 128;
-            const size_t from = lane < 2 * NP ? size_t(first + b0) * 2048 : size_t(first) * 128;
-            for (int g = 0; g < G; ++g) {
-                const bool sums = (g & 1) || g + 1 == G;
-                if (tb.waits() && !(ok = warp_wait(&b_empty[tb.s], tb.empty()))) break;
-                if (lane == 0) mbar_arrive_expect_tx(&b_full[tb.s], (2048u * NP + (sums ? 128u : 0u)) * nb);
-                __syncwarp();
-                if (lane < 2 * NP + (sums ? 1 : 0))
-                    bulk_g2s(smem + size_t(tb.s) * bstage + to,
-                             src + from + (lane < 2 * NP ? size_t(g) * NP * blocks * 2048 : size_t(g >> 1) * blocks * 128), bytes,
-                             &b_full[tb.s]);
-                tb.next(BS);
+        // ---- staged tokens: a pair's share of the tile and its sums
+        if (elect_one()) {
+            const int pairs = pairs_of(K);
+            const size_t blocks = p.blocks;
+            const uint8_t* sums = bsrc + sums_at(K, NP, blocks);
+            int4 tile = tile_of(blockIdx.x);
+            for (int it = blockIdx.x; it < items && ok; it += step) {
+                const int4 ahead = tile_of(it + step);
+                const uint32_t nb = uint32_t(tile.z) >> 3;
+                const size_t first = size_t(tile.y >> 3);
+#pragma unroll 1
+                for (int u = 0; u < pairs; ++u) {
+                    if (tb.waits() && !(ok = one_wait(&b_empty[tb.s], tb.empty()))) break;
+                    mbar_arrive_expect_tx(&b_full[tb.s], (4096u * NP + 128u) * nb);
+                    uint8_t* to = smem + size_t(tb.s) * bstage;
+#pragma unroll
+                    for (int q = 0; q < NP; ++q)
+                        bulk_g2s(to + q * nb * 4096, bsrc + ((size_t(u) * NP + q) * blocks + first) * 4096, nb * 4096, &b_full[tb.s]);
+                    bulk_g2s(to + dcols * 512u, sums + (size_t(u) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
+                    tb.next(BS);
+                }
+                tile = ahead;
             }
-            tile = ahead;
+            drain(b_full, BS, tb);
         }
-        if (lane == 0) drain(b_full, BS, tb);
     } else if (warp == 1) {
         // ---- MMA issue, by one elected thread (elect.sync: with `lane == 0` the compiler does not know that the operands are
         // uniform, and an MMA takes 55 cycles to issue instead of 6).  Alone on its path it takes some 6 cycles an instruction, so
@@ -520,17 +515,16 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             const uint32_t bars = smem_u32(b_full), bfull = bars, bempty = bars + 8 * kMaxStages, afull = smem_u32(a_full),
                            aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
             const uint32_t blo0 = ((sbase >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
-            const uint32_t z = sbase + L.z, xoff = p.cap * 256u * NP, zeros = z + 2 * kZBytes;
+            const uint32_t z = sbase + L.z, xoff = dcols * 512u, zeros = z + 2 * kZBytes;
             const uint64_t zd[2] = {plain_desc(z, 2 * kZBytes), plain_desc(z + kZBytes, kZBytes)};
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
-            auto eight = [&](uint32_t to, uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
+            auto eight = [&](uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
                 const uint64_t desc = (uint64_t(kSwizzledHi) << 32) | lo;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_ta(to, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
+                    tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
             };
-            uint32_t low = taddr + rest;                   // the remainders' accumulator
             auto hand_over = [&]() {                       // the accumulator to the epilogue
                 commit_at(dfull + 8 * ds);
                 acc += dcols;
@@ -543,41 +537,45 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             int4 tile = tile_of(blockIdx.x);
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
-                const uint32_t idesc = tc_idesc(kRows, tile.z), second = uint32_t(tile.z) * 16;     // (8 rows of 2 KB: n / 8 * 128)
+                const uint32_t idesc = tc_idesc(kRows, NP * tile.z), sums = tc_idesc(kRows, tile.z);
                 if (!(ok = wait(dempty + 8 * ds, dph))) break;
                 uint32_t begun = 0;                        // the accumulator holds something
 #pragma unroll 1
-                for (int g = 0; g < G; ++g) {
-                    if (!(ok = wait(bfull + 8 * bs, bph))) break;
-                    if ((g & 1) == 0 && !(ok = wait(afull + 8 * as, aph))) break;
+                for (int g = 0; g < G; g += 2) {
+                    if (!(ok = wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
                     tc_fence_after();
-                    const uint32_t a = taddr + 256 + as * 128 + (g & 1) * 64;
-                    eight(acc, a, blo, idesc, begun);
-                    if (NP == 2) eight(low, a, blo + second, idesc, g > 0 ? 1u : 0u);
-                    begun = 1;
-                    if ((g & 1) || g + 1 == G) {           // the pair's zero points (to the first terms' columns)
-                        const uint32_t x = sbase + bs * bstage + xoff;
-                        mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), idesc);
-                        commit_at(aempty + 8 * as);
-                        as ^= 1;
-                        aph ^= as ^ 1;
+                    const uint32_t a = taddr + 256 + as * 128;
+                    eight(a, blo, idesc, begun);
+                    if (g + 1 < G) {
+                        if (NP == 2) {
+                            hand_over();
+                            if (!(ok = wait(dempty + 8 * ds, dph))) break;
+                            tc_fence_after();
+                        }
+                        eight(a + 64, blo + 128, idesc, NP == 2 ? 0u : 1u);
                     }
+                    // the pair's zero points (to the first terms' columns)
+                    const uint32_t x = sbase + bs * bstage + xoff;
+                    mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), sums);
+                    commit_at(aempty + 8 * as);
                     commit_at(bempty + 8 * bs);
+                    begun = 1;
+                    if (NP == 2 && g + 2 < G) {
+                        hand_over();
+                        if (!(ok = wait(dempty + 8 * ds, dph))) break;
+                        begun = 0;
+                    }
+                    as ^= 1;
+                    aph ^= as ^ 1;
                     blo += bstep;
                     if (++bs == uint32_t(BS)) {
                         bs = 0;
                         bph ^= 1;
                         blo = blo0;
                     }
-                    if (NP == 2 && g + 1 < G) {
-                        hand_over();
-                        if (!(ok = wait(dempty + 8 * ds, dph))) break;
-                        begun = 0;
-                    }
                 }
                 if (!ok) break;
                 hand_over();
-                low ^= (taddr + rest) ^ (taddr + rest + 64);
                 tile = ahead;
             }
         }
@@ -769,23 +767,23 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 for (int i = 0; i < kSums; ++i)
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
-                auto add = [&](uint32_t acc) {
+#pragma unroll 1
+                for (int g = 0; g < G; ++g) {
+                    ok = ok && warp_wait(&d_full[td.s], td.full());
+                    tc_fence_after();
+                    const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
 #pragma unroll
                     for (int i = 0; i < kSums; ++i) {
                         const int c0 = i * 32 + half * 16;
                         if (c0 >= real || !ok) continue;
                         float v[16];
-                        tc_ld16(acc + (uint32_t(32 * q) << 16) + uint32_t(c0), v);
+                        tc_ld16(acc + uint32_t(c0), v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
+                        tc_ld16(acc + uint32_t(n + c0), v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
                     }
-                };
-#pragma unroll 1
-                for (int g = 0; g < G; ++g) {
-                    ok = ok && warp_wait(&d_full[td.s], td.full());
-                    tc_fence_after();
-                    add(taddr + td.s * dcols);
-                    if (g == G - 1) add(taddr + rest + turn * 64);      // (given back with the last buffer)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&d_empty[td.s]);
