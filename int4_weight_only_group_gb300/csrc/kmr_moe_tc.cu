@@ -40,7 +40,6 @@ constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                        // packed weight rows of a product (the MMA's M)
 constexpr uint32_t kWBytes = 16 * kGroupBytes;    // two groups of eight KMR4 tiles
 constexpr int kAQ = 2;                            // pairs of dequantised groups in tensor memory, 128 columns each
-constexpr int kMaxStages = 8;
 constexpr int kMaxAcc = 8;                        // accumulators: as many as 256 columns hold
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(max(1, min(253, e + 127))) << 23); }
@@ -267,9 +266,9 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
 }
 
 // ------------------------------------------------------------------ the grouped product
-// warps 0, 1, 2: weights, MMA, tokens; then the unpack warps and the epilogue warps, from multiples of four on (a warp reaches the
+// warps 0, 1, 2, 3: weights, MMA, tokens, zero points; then the unpack warps and the epilogue warps, from multiples of four on (a warp reaches the
 // quarter warp % 4 of the tensor memory's lanes)
-constexpr int kTokenWarp = 2, kUnpackWarp = 4, kUnpackWarps = 8, kEpiWarp = kUnpackWarp + kUnpackWarps, kEpiWarps = 8;
+constexpr int kTokenWarp = 2, kZeroWarp = 3, kUnpackWarp = 4, kUnpackWarps = 8, kEpiWarp = kUnpackWarp + kUnpackWarps, kEpiWarps = 8;
 constexpr int kThr = (kEpiWarp + kEpiWarps) * 32;
 constexpr uint32_t kSmem = 227 * 1024;
 
@@ -280,27 +279,32 @@ constexpr uint32_t kSmem = 227 * 1024;
 template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
-// Shared memory: the token ring, [gate_up: a tile of activations], the zero points (of two pairs of groups) and 2 KB of zeros behind
-// them, barriers, the tokens' factors, the weight ring.
-constexpr uint32_t kRing = 136 * 1024;
+// Shared memory: [gate_up: a tile of activations], the zero points (of two pairs of groups), barriers, the tokens' factors, the token
+// ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two groups of `cap` tokens and their sums;
+// small tiles leave more of the memory to the weights, whose latency they have less work to hide.
 constexpr uint32_t kZBytes = kRows * 16;
+constexpr int kMaxStages = 8, kMaxWS = 8;
 struct Layout {
-    uint32_t tile, z, bar, fac, w, total;
+    uint32_t tile, z, bar, fac, ring;
 };
-constexpr int kWS = 3;                             // weight stages
 __host__ __device__ constexpr Layout layout(bool gate) {
     Layout l = {};
-    l.tile = kRing;
-    l.z = l.tile + (gate ? 16384u : 0u);          // (128 rows of one term or 64 of two)
-    l.bar = l.z + 3 * kZBytes;
+    l.z = gate ? 16384u : 0u;                     // (128 rows of one term or 64 of two)
+    l.bar = l.z + 2 * kZBytes;
     l.fac = l.bar + 512;
-    l.w = l.fac + 2 * 2 * 128 * 4;
-    l.total = l.w + kWS * kWBytes;
+    l.ring = (l.fac + 2 * 2 * 128 * 4 + 1023u) & ~1023u;
     return l;
 }
-static_assert(layout(true).total <= kSmem, "shared memory");
-// A stage of the token ring: two groups of `cap` tokens, and their sums.
 __host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 512u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
+__host__ __device__ constexpr int token_stages(int cap, int np) {
+    const int n = int(72u * 1024u / stage_bytes(cap, np));
+    return n < 2 ? 2 : (n > kMaxStages ? kMaxStages : n);
+}
+__host__ __device__ constexpr int weight_stages(bool gate, int cap, int np) {
+    const int n = int((kSmem - layout(gate).ring - token_stages(cap, np) * stage_bytes(cap, np) - kZBytes) / kWBytes);
+    return n > kMaxWS ? kMaxWS : n;
+}
+static_assert(weight_stages(true, 128, 1) >= 3 && weight_stages(true, 64, 2) >= 3, "shared memory");
 
 // Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 4 KB apart): the upper half is this
 // constant, the lower the address and 1 << 16.
@@ -390,13 +394,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const int R = N / kRows;                               // row tiles of an expert
     constexpr Layout L = layout(GATE);
     const uint32_t bstage = stage_bytes(p.cap, NP);
-    const int BS = min(kMaxStages, int(kRing / bstage));
+    const int BS = token_stages(p.cap, NP), WS = weight_stages(GATE, p.cap, NP);
+    const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
     const int DB = min(kMaxAcc, 256 / (p.cap * NP));       // accumulators
     const uint32_t dcols = uint32_t(p.cap) * NP;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
-    uint64_t* w_empty = w_full + kWS;
-    uint64_t* b_full = w_empty + kWS;
+    uint64_t* w_empty = w_full + kMaxWS;
+    uint64_t* b_full = w_empty + kMaxWS;
     uint64_t* b_empty = b_full + kMaxStages;
     uint64_t* a_full = b_empty + kMaxStages;
     uint64_t* a_empty = a_full + kAQ;
@@ -404,21 +409,21 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     uint64_t* d_empty = d_full + kMaxAcc;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(d_empty + kMaxAcc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    static_assert(2 * (kWS + kMaxStages + kAQ + kMaxAcc) * 8 + 8 <= 512, "barrier area");
+    static_assert(2 * (kMaxWS + kMaxStages + kAQ + kMaxAcc) * 8 + 8 <= 512, "barrier area");
     const uint32_t sbase = smem_u32(smem);
 
     if (tid == 0) {
         *abort_flag = 0;
-        for (int s = 0; s < kWS; ++s) {
+        for (int s = 0; s < WS; ++s) {
             mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], kUnpackWarps / 2);
+            mbar_init(&w_empty[s], kUnpackWarps / 2 + 1);
         }
         for (int s = 0; s < BS; ++s) {
             mbar_init(&b_full[s], 1);
             mbar_init(&b_empty[s], 1);
         }
         for (int s = 0; s < kAQ; ++s) {
-            mbar_init(&a_full[s], kUnpackWarps / 2);
+            mbar_init(&a_full[s], kUnpackWarps / 2 + 1);
             mbar_init(&a_empty[s], 1);
         }
         for (int s = 0; s < DB; ++s) {
@@ -428,7 +433,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         fence_mbar_init();
     }
     if (warp == 0) tc_alloc(tslot, 512);
-    for (int i = tid; i < int(kZBytes) / 4; i += kThr) reinterpret_cast<uint32_t*>(smem + L.z + 2 * kZBytes)[i] = 0u;
+    for (int i = tid; i < int(kZBytes) / 4; i += kThr) reinterpret_cast<uint32_t*>(smem + zeros_at)[i] = 0u;
     fence_proxy_async_smem();
     tc_fence_before();
     __syncthreads();
@@ -471,15 +476,15 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     const uint32_t bytes = uint32_t(min(2, G - g)) * kGroupBytes;
                     mbar_arrive_expect_tx(&w_full[tw.s], 8 * bytes);
                     fence_proxy_async_smem();              // the unpack warps' reads of the stage come first
-                    uint8_t* to = smem + L.w + tw.s * kWBytes;
+                    uint8_t* to = smem + wring + tw.s * kWBytes;
 #pragma unroll
                     for (int t = 0; t < 8; ++t)
                         bulk_g2s_stream(to + t * bytes, src + (size_t(t) * G + g) * kGroupBytes, bytes, &w_full[tw.s], pol);
-                    tw.next(kWS);
+                    tw.next(WS);
                 }
                 tile = ahead;
             }
-            drain(w_full, kWS, tw);
+            drain(w_full, WS, tw);
         }
     } else if (warp == kTokenWarp) {
         // ---- staged tokens: a pair's share of the tile and its sums
@@ -496,7 +501,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 for (int u = 0; u < pairs; ++u) {
                     if (tb.waits() && !(ok = one_wait(&b_empty[tb.s], tb.empty()))) break;
                     mbar_arrive_expect_tx(&b_full[tb.s], (4096u * NP + 128u) * nb);
-                    uint8_t* to = smem + size_t(tb.s) * bstage;
+                    uint8_t* to = smem + L.ring + size_t(tb.s) * bstage;
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
                         bulk_g2s(to + q * nb * 4096, bsrc + ((size_t(u) * NP + q) * blocks + first) * 4096, nb * 4096, &b_full[tb.s]);
@@ -514,9 +519,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         if (elect_one()) {
             const uint32_t bars = smem_u32(b_full), bfull = bars, bempty = bars + 8 * kMaxStages, afull = smem_u32(a_full),
                            aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
-            const uint32_t blo0 = ((sbase >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
-            const uint32_t z = sbase + L.z, xoff = dcols * 512u, zeros = z + 2 * kZBytes;
-            const uint64_t zd[2] = {plain_desc(z, 2 * kZBytes), plain_desc(z + kZBytes, kZBytes)};
+            const uint32_t blo0 = (((sbase + L.ring) >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
+            const uint32_t z = sbase + L.z, xoff = dcols * 512u, zeros = sbase + zeros_at;
+            const uint64_t zd[2] = {plain_desc(z, zeros - z), plain_desc(z + kZBytes, zeros - z - kZBytes)};
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
             auto eight = [&](uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                         eight(a + 64, blo + 128, idesc, NP == 2 ? 0u : 1u);
                     }
                     // the pair's zero points (to the first terms' columns)
-                    const uint32_t x = sbase + bs * bstage + xoff;
+                    const uint32_t x = sbase + L.ring + bs * bstage + xoff;
                     mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), sums);
                     commit_at(aempty + 8 * as);
                     commit_at(bempty + 8 * bs);
@@ -579,33 +584,80 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 tile = ahead;
             }
         }
+    } else if (warp == kZeroWarp) {
+        // ---- zero points of the pair's rows, four rows a lane, off the unpack warps' path
+        auto dup = [&](uint32_t sz, float r) {
+            const float z = __fmul_rn(bf16_hi(sz) * 0x1p-18f, r);
+            const __half2 h = __floats2half2_rn(z, z);
+            return *reinterpret_cast<const uint32_t*>(&h);
+        };
+        auto factors = [&](int it, const int4& tile, float (&to)[4]) {
+            const float* at = rho + size_t(tile.x) * N + (it % R) * kRows + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = at[32 * i];
+        };
+        Turn tt, ta;
+        float rr[4] = {1.f, 1.f, 1.f, 1.f}, rnext[4] = {1.f, 1.f, 1.f, 1.f};
+        int4 ahead = tile_of(blockIdx.x);
+        if (int(blockIdx.x) < items) factors(blockIdx.x, ahead, rnext);
+        for (int it = blockIdx.x; it < items && ok; it += step) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) rr[i] = rnext[i];
+            ahead = tile_of(it + step);
+#pragma unroll 1
+            for (int g = 0; g < G; g += 2) {
+                const int both = min(2, G - g);
+                if (g + 2 >= G && it + step < items) factors(it + step, ahead, rnext);
+                if (!(ok = warp_wait(&w_full[tt.s], tt.full()))) break;
+                // row 32 i + lane: tile 2 i + lane / 16, row lane % 16
+                const uint8_t* at = smem + wring + tt.s * kWBytes + (lane >> 4) * both * kGroupBytes + 1024 + (lane & 15) * 4;
+                uint32_t sz[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+                        sz[i][j] = j < both ? *reinterpret_cast<const uint32_t*>(at + (2 * i * both + j) * kGroupBytes) : 0u;
+                if (ta.waits() && !(ok = warp_wait(&a_empty[ta.s], ta.empty()))) break;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t z0 = dup(sz[i][0], rr[i]), z1 = dup(sz[i][1], rr[i]);
+                    *reinterpret_cast<uint4*>(smem + L.z + ta.s * kZBytes + (4 * i + (lane >> 3)) * 128 + (lane & 7) * 16) =
+                        make_uint4(z0, z0, z1, z1);
+                }
+                fence_proxy_async_smem();                  // the MMA reads them through the async proxy
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&w_empty[tt.s]);
+                    mbar_arrive(&a_full[ta.s]);
+                }
+                tt.next(WS);
+                ta.next(kAQ);
+            }
+        }
     } else if (warp >= kUnpackWarp && warp < kEpiWarp) {
         // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, every second pair of groups
         const int lq = warp & 3, set = (warp - kUnpackWarp) >> 2, g8 = lane >> 2;
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
         auto dup = [&](float v) { return __floats2half2_rn(v, v); };
-        // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter, and of row `lane` (whose zero points this lane writes)
-        auto factors = [&](int it, const int4& tile, float (&to)[5]) {
+        // factors of rows g8, g8 + 8, g8 + 16, g8 + 24 of the quarter
+        auto factors = [&](int it, const int4& tile, float (&to)[4]) {
             const float* at = rho + size_t(tile.x) * N + (it % R) * kRows + 32 * lq;
 #pragma unroll
             for (int i = 0; i < 4; ++i) to[i] = at[g8 + 8 * i];
-            to[4] = at[lane];
         };
-        uint8_t* zto = smem + L.z + set * kZBytes + (4 * lq + (lane >> 3)) * 128 + (lane & 7) * 16;
         const uint32_t aset = taddr + 256 + set * 128 + (uint32_t(32 * lq) << 16);
         // this set's pairs are number set, set + 2, ... of all: their stage of the weight ring, its parity, the place's parity
-        static_assert(kWS == 3, "stages are stepped two at a time below");
         uint32_t ws = set, wph = 0, aph = 1;
         int skip = set;                                    // pairs of the item that come before this set's next
         const int pairs = (G + 1) >> 1;
         const uint32_t wfull = smem_u32(w_full), aempty = smem_u32(a_empty + set);
-        float rr[5] = {1.f, 1.f, 1.f, 1.f, 1.f}, rnext[5] = {1.f, 1.f, 1.f, 1.f, 1.f};
+        float rr[4] = {1.f, 1.f, 1.f, 1.f}, rnext[4] = {1.f, 1.f, 1.f, 1.f};
         int4 ahead = tile_of(blockIdx.x);
         if (int(blockIdx.x) < items) factors(blockIdx.x, ahead, rnext);
         for (int it = blockIdx.x; it < items && ok; it += step) {
 #pragma unroll
-            for (int i = 0; i < 5; ++i) rr[i] = rnext[i];
+            for (int i = 0; i < 4; ++i) rr[i] = rnext[i];
             ahead = tile_of(it + step);
             int pr = skip;
 #pragma unroll 1
@@ -613,12 +665,11 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 const int both = min(2, G - 2 * pr);
                 if (pr + 2 >= pairs && it + step < items) factors(it + step, ahead, rnext);
                 if (!(ok = __all_sync(kFull, wait_at(wfull + 8 * ws, wph, abort_flag, p.err)))) break;
-                const uint8_t* wst = smem + L.w + ws * kWBytes + 2 * lq * both * kGroupBytes;
-                // a group's words, scales and this lane's zero point
+                const uint8_t* wst = smem + wring + ws * kWBytes + 2 * lq * both * kGroupBytes;
+                // a group's words and scales
                 uint4 wq[4];
-                uint32_t sz[4], zrow[2] = {0u, 0u};
+                uint32_t sz[4];
                 auto fetch = [&](int j) {
-                    zrow[j] = *reinterpret_cast<const uint32_t*>(wst + ((lane >> 4) * both + j) * kGroupBytes + 1024 + (lane & 15) * 4);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const uint8_t* blk = wst + (h * both + j) * kGroupBytes;
@@ -656,19 +707,15 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                         }
                     }
                 }
-                const uint32_t z0 = u2(dup(__fmul_rn(bf16_hi(zrow[0]) * 0x1p-18f, rr[4])));
-                const uint32_t z1 = u2(dup(__fmul_rn(bf16_hi(zrow[1]) * 0x1p-18f, rr[4])));
-                *reinterpret_cast<uint4*>(zto) = make_uint4(z0, z0, z1, z1);
                 if (lane == 0) mbar_arrive(&w_empty[ws]);      // (all lanes' loads have been used by the stores above)
-                fence_proxy_async_smem();                      // the MMA reads the zero points through the async proxy
                 tc_wait_st();
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&a_full[set]);
                 aph ^= 1;
                 ws += 2;
-                if (ws >= kWS) {
-                    ws -= kWS;
+                if (ws >= uint32_t(WS)) {
+                    ws -= WS;
                     wph ^= 1;
                 }
             }
@@ -934,7 +981,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     const void* stage = bf16 ? (const void*)moe_stage_kernel<uint16_t, 1> : (const void*)moe_stage_kernel<float, 2>;
     if ((e = launch_dependent(stage, dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
-        const size_t smem = layout(gate).total;
+        const size_t smem = kSmem;
         if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<uint16_t> : (const void*)moe_combine_kernel<float>;
