@@ -391,7 +391,7 @@ int kmr_moe_prepare(const kmr_moe* moe, void* stream);
  *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
  *             workspaces of their own.
  * Products are exact and sums are held in fp32, whatever the type; between gate_up and down the activations keep 22 bits (fp32)
- * or 11 (bf16).  Up to 32 places (T top_k) are two launches, more are five for every 65536 places; within either form a
+ * or 11 (bf16).  Up to 32 places (T top_k) are two launches, more are five for every 32768 places; within either form a
  * token's result does not depend on the other tokens.  top_k 1..32.  Errors:
  * KMR_ERR_INVALID_ARG (pointers, dtype, epilogue), KMR_ERR_SHAPE, KMR_ERR_BATCH, KMR_ERR_BUFFER_SIZE; on the device
  * KMR_ERR_INVALID_ARG (an id outside -1..experts - 1). */

@@ -45,12 +45,12 @@ cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaSt
 cudaError_t moe_small_set_attributes();
 
 // Grouped form (kmr_moe_tc.cu).
-constexpr int kMoeChunkPlaces = 65536;       // places of one pass
+constexpr int kMoeChunkPlaces = 32768;       // places of one pass (a rank within an expert fits 16 bits)
 struct MoeTcParams {
     MoeView w;
     const float* rho_gate_up;                // [E][2I] row factors, packed row order
     const float* rho_down;                   // [E][H]
-    const float* norms;                      // [E][2] bounds of the gate and up rows' norms
+    const float* norms;                      // [E][3] bounds of the gate, up and down rows' norms
     const void* x;                           // [T][H]
     const int32_t* ids;                      // [T][k]
     const float* weights;                    // [T][k]
@@ -60,17 +60,18 @@ struct MoeTcParams {
     int32_t* pos;                            // [T][k]: the place's position, or -1
     float* isx;                              // [P] 1 / scale of the position's inputs
     float* sact;                             // [P] scale of its activations
+    float* sout;                             // [P] bf16: scale of its result while it waits for the sum
     size_t blocks;                           // P / 8
     uint8_t* xs;                             // staged inputs
     uint8_t* as;                             // staged activations
-    float* out;                              // [P][H]
+    void* out;                               // [P][H]: fp16 (bf16) or fp32
     void* y;                                 // [T][H]
     int resid;
     int* err;
 };
 // Byte offsets into the workspace (the tile count comes first), and the blocks of 8 positions.
 struct MoeTcSizes {
-    size_t tiles, pos, isx, sact, xs, as, out, total, blocks;
+    size_t tiles, pos, isx, sact, sout, xs, as, out, total, blocks;
 };
 int moe_tc_cap(long long places, int E, bool bf16);
 MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k);

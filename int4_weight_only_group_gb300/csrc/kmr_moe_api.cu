@@ -67,7 +67,7 @@ extern "C" int kmr_moe_route(const void* logits, int dtype, int T, int experts, 
 
 extern "C" size_t kmr_moe_factors_size(int experts, int hidden, int intermediate) {
     if (experts < 1 || experts > kMoeMaxExperts || !dim_ok(hidden) || !dim_ok(intermediate)) return 0;
-    return size_t(experts) * (2 * size_t(intermediate) + hidden + 2) * 4;
+    return size_t(experts) * (2 * size_t(intermediate) + hidden + 3) * 4;
 }
 
 extern "C" int kmr_moe_prepare(const kmr_moe* moe, void* stream) {
@@ -131,10 +131,11 @@ extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, con
     p.pos = reinterpret_cast<int32_t*>(ws + z.pos);
     p.isx = reinterpret_cast<float*>(ws + z.isx);
     p.sact = reinterpret_cast<float*>(ws + z.sact);
+    p.sout = reinterpret_cast<float*>(ws + z.sout);
     p.blocks = z.blocks;
     p.xs = ws + z.xs;
     p.as = ws + z.as;
-    p.out = reinterpret_cast<float*>(ws + z.out);
+    p.out = ws + z.out;
     p.resid = epilogue == KMR_EPI_RESIDUAL;
     p.err = err;
     for (int t = 0; t < T; t += chunk) {

@@ -28,6 +28,8 @@
 // remaining work, drains the copies in flight and frees tensor memory.
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "kmr_int4_mma.cuh"
 #include "kmr_moe.cuh"
 #include "kmr_tc.cuh"
@@ -49,8 +51,8 @@ __device__ __forceinline__ float inverse_pow2(float p) { return __uint_as_float(
 
 // ------------------------------------------------------------------ weights, once
 // Row factors rho (a power of two that brings max(|s|, 2^-18 |z|) of the row to [2^13, 2^14)) and the largest row norm bound of
-// each expert's gate and up rows: |w|^2 <= sum over groups of 128 max(|z - 8 s|, |z + 7 s|)^2.
-__global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rho, float* norms) {
+// each expert's gate, up and down rows (`which`: the matrix's first of the three): |w|^2 <= sum over groups of 128 max(|z - 8 s|, |z + 7 s|)^2.
+__global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rho, float* norms, int which) {
     const int row = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
     if (row >= tiles * 16) return;
     const uint8_t* at = w + (size_t(e) * tiles + row / 16) * G * kGroupBytes + 1024 + (row & 15) * 4;
@@ -66,7 +68,7 @@ __global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rh
     pow2_scale(__float_as_uint(m), r, ir);
     rho[size_t(e) * tiles * 16 + row] = r;
     // (a bound: rounded up; the bits of non-negative floats order like integers)
-    if (norms) atomicMax(reinterpret_cast<int*>(norms + 2 * e + ((row & 15) >> 3)), __float_as_int(sqrtf(n2) * 1.001f));
+    atomicMax(reinterpret_cast<int*>(norms + 3 * e + (which == 0 ? (row & 15) >> 3 : which)), __float_as_int(sqrtf(n2) * 1.001f));
 }
 
 // ------------------------------------------------------------------ plan
@@ -78,15 +80,23 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, S = p.T * p.k;
     count[tid] = 0;
     __syncthreads();
-    constexpr int kB = 8;                                            // ids in flight
-    for (int i0 = tid; i0 < S; i0 += kB * kPlanThr) {
+    // each place's expert and its rank among the expert's places (which rank it gets does not change any result)
+    constexpr int kPer = kMoeChunkPlaces / kPlanThr, kB = 8;
+    uint32_t mine[kPer];
+#pragma unroll
+    for (int b0 = 0; b0 < kPer; b0 += kB) {
+        if (b0 * kPlanThr >= S) break;
         int e[kB];
 #pragma unroll
-        for (int b = 0; b < kB; ++b) e[b] = i0 + b * kPlanThr < S ? p.ids[i0 + b * kPlanThr] : -1;
+        for (int b = 0; b < kB; ++b) {
+            const int i = (b0 + b) * kPlanThr + tid;
+            e[b] = i < S ? p.ids[i] : -1;
+        }
 #pragma unroll
         for (int b = 0; b < kB; ++b) {
-            if (e[b] >= 0 && e[b] < p.w.E) atomicAdd(&count[e[b]], 1);
-            else if (e[b] != -1) set_error(p.err, KMR_ERR_INVALID_ARG);
+            const bool real = e[b] >= 0 && e[b] < p.w.E;
+            if (!real && e[b] != -1) set_error(p.err, KMR_ERR_INVALID_ARG);
+            mine[b0 + b] = real ? uint32_t(e[b]) << 16 | uint32_t(atomicAdd(&count[e[b]], 1)) : 0xffffffffu;
         }
     }
     __syncthreads();
@@ -123,16 +133,10 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     }
     if (tid == kPlanThr - 1) *p.ntiles = pb + b;
     __syncthreads();
-    // (which of its expert's positions a place gets does not change any result)
-    for (int i0 = tid; i0 < S; i0 += kB * kPlanThr) {
-        int e[kB];
 #pragma unroll
-        for (int b = 0; b < kB; ++b) e[b] = i0 + b * kPlanThr < S ? p.ids[i0 + b * kPlanThr] : -1;
-#pragma unroll
-        for (int b = 0; b < kB; ++b) e[b] = e[b] >= 0 && e[b] < p.w.E ? atomicAdd(&at[e[b]], 1) : -1;
-#pragma unroll
-        for (int b = 0; b < kB; ++b)
-            if (i0 + b * kPlanThr < S) p.pos[i0 + b * kPlanThr] = e[b];
+    for (int b = 0; b < kPer; ++b) {
+        const int i = b * kPlanThr + tid;
+        if (i < S) p.pos[i] = mine[b] == 0xffffffffu ? -1 : at[mine[b] >> 16] + int(mine[b] & 0xffffu);
     }
 }
 
@@ -150,18 +154,13 @@ __device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks
 }
 __device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return pairs_of(K) * blocks * size_t(np) * 4096; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
-// Sum number h (of 64 inputs) of a row: its two terms.  `sums` is where the sums begin.
-__device__ __forceinline__ void put_sum(uint8_t* sums, size_t blocks, int at, int h, float X) {
+// Sum number h (of 64 inputs) of a row: its two terms, in the row's pieces of 8 numbers (`stride` bytes apart) for each pair of groups.
+__device__ __forceinline__ void put_sum(void* row, int h, float X, size_t stride = 16) {
     const float x = X * 0.015625f;
     const __half hi = __float2half_rn(x);
-    __half* to = reinterpret_cast<__half*>(sums + (size_t(h >> 2) * blocks + (at >> 3)) * 128 + (at & 7) * 16) + ((h >> 1) & 1) * 4 + (h & 1);
+    __half* to = reinterpret_cast<__half*>(static_cast<uint8_t*>(row) + (h >> 2) * stride) + ((h >> 1) & 1) * 4 + (h & 1);
     to[0] = hi;
     to[2] = __float2half_rn(__fsub_rn(x, __half2float(hi)));
-}
-// An odd number of groups leaves half of the last pair's sums.
-__device__ __forceinline__ void clear_sums(uint8_t* sums, size_t blocks, int K, int at) {
-    if ((K >> 7) & 1)
-        *reinterpret_cast<uint2*>(sums + (size_t(K >> 8) * blocks + (at >> 3)) * 128 + (at & 7) * 16 + 8) = make_uint2(0u, 0u);
 }
 
 // ------------------------------------------------------------------ stage
@@ -170,6 +169,7 @@ template <typename IN, int NP>
 __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams p) {
     __shared__ float red[2][kStageThr / 32];
     __shared__ int pos[kMoeMaxTopK];
+    __shared__ __align__(16) __half sums[kMoeMaxDim / 64 * 2];          // of the row, as a pair's 16 bytes
     pdl_launch_dependents();
     pdl_wait();
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -211,7 +211,6 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
     pow2_scale(__float_as_uint(m), sig, isg);
     float ss = 0.f;
     const size_t blocks = p.blocks;
-    uint8_t* sums = p.xs + sums_at(K, NP, blocks);
     auto h2u = [](__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); };
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
@@ -245,13 +244,19 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
             uint8_t* to = p.xs + atom_at(k >> 6, 0, NP, blocks, at >> 3) + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
 #pragma unroll
             for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 4096) = out[q];
-            if ((lane & 15) == 0) put_sum(sums, blocks, at, k >> 6, X);
         }
+        if ((lane & 15) == 0) put_sum(sums, k >> 6, X);
     }
     ss = warp_sum(ss);
     if (lane == 0) red[1][warp] = ss;
     __syncthreads();
-    if (tid < n) clear_sums(sums, blocks, K, pos[tid]);
+    // (the half of the last pair that an odd number of groups leaves is zero)
+    for (int i = tid; i < n * pairs_of(K); i += kStageThr) {
+        const int j = i / pairs_of(K), pr = i % pairs_of(K), at = pos[j];
+        uint4 v = reinterpret_cast<const uint4*>(sums)[pr];
+        if (2 * pr + 1 == K >> 7) v.z = v.w = 0u;
+        *reinterpret_cast<uint4*>(p.xs + sums_at(K, NP, blocks) + (size_t(pr) * blocks + (at >> 3)) * 128 + (at & 7) * 16) = v;
+    }
     if (tid < p.k) {
         const int at = p.pos[size_t(t) * p.k + tid];
         if (at < 0) return;
@@ -261,7 +266,10 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
         const int e = p.ids[size_t(t) * p.k + tid];
         const int ex = above(sqrtf(ss)) + above(isg) - 1;
         p.isx[at] = isg;
-        p.sact[at] = pow2(15 - (2 * ex + above(p.norms[2 * e]) + above(p.norms[2 * e + 1])));
+        const int ea = 2 * ex + above(p.norms[3 * e]) + above(p.norms[3 * e + 1]);
+        p.sact[at] = pow2(15 - ea);
+        // bf16: |down act| <= |act| max |row|, |act| <= sqrt(I) 2^ea
+        p.sout[at] = pow2(15 - (ea + (33 - __clz(p.w.I)) / 2 + above(p.norms[3 * e + 2])));
     }
 }
 
@@ -734,7 +742,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         auto factors = [&](int it, const int4& tl) {
             if (et < tl.w) {
                 f0 = GATE ? p.isx[tl.y + et] : p.sact[tl.y + et];
-                if (GATE) f1 = p.sact[tl.y + et];
+                f1 = GATE ? p.sact[tl.y + et] : p.sout[tl.y + et];
             }
             irho = rho[size_t(tl.x) * N + (it % R) * kRows + 32 * q + lane];
         };
@@ -744,7 +752,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             float* f = fac + turn * 256;
             if (et < real) {
                 f[et] = 0x1p12f * (GATE ? f0 : inverse_pow2(f0));
-                if (GATE) f[128 + et] = f1;
+                f[128 + et] = f1;
             }
             const float ir = 0x1p12f * inverse_pow2(irho);     // (the 2^24 of A, half of it with either factor)
             ahead = tile_of(it + step);
@@ -778,14 +786,22 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                         }
                     }
                 } else {
-                    float* out = p.out + size_t(tile.y + c0) * N + r * kRows + 32 * q + lane;
+                    // bf16: the rows wait for the weighted sum as fp16, scaled to their bound (half a step: 2^-12, a sixteenth
+                    // of the result's; fp32 rows would be 60% of the call's traffic)
+                    using Out = typename std::conditional<NP == 1, __half, float>::type;
+                    Out* out = static_cast<Out*>(p.out) + size_t(tile.y + c0) * N + r * kRows + 32 * q + lane;
+                    auto put = [&](int j) {
+                        const float x = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                        if constexpr (NP == 1) out[size_t(j) * N] = __float2half_rn(__fmul_rn(x, f[128 + c0 + j]));
+                        else out[size_t(j) * N] = x;
+                    };
                     if (c0 + 16 <= real) {
 #pragma unroll
-                        for (int j = 0; j < 16; ++j) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                        for (int j = 0; j < 16; ++j) put(j);
                     } else {
 #pragma unroll
                         for (int j = 0; j < 16; ++j)
-                            if (c0 + j < real) out[size_t(j) * N] = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
+                            if (c0 + j < real) put(j);
                     }
                 }
             };
@@ -874,9 +890,11 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                                 X = __fadd_rn(X, __fadd_rn(v.x, v.y));
                             }
                         }
-                    uint8_t* sums = p.as + sums_at(p.w.I, NP, blocks);
-                    put_sum(sums, blocks, tile.y + et, r, X);
-                    if (r == 0) clear_sums(sums, blocks, p.w.I, tile.y + et);
+                    const int at = tile.y + et;
+                    uint8_t* row = p.as + sums_at(p.w.I, NP, blocks) + size_t(at >> 3) * 128 + (at & 7) * 16;
+                    put_sum(row, r, X, blocks * 128);
+                    // the half that an odd number of groups leaves
+                    if (r == 0 && ((p.w.I >> 7) & 1)) *reinterpret_cast<uint2*>(row + (p.w.I >> 8) * blocks * 128 + 8) = make_uint2(0u, 0u);
                 }
             }
             tile = ahead;
@@ -889,56 +907,75 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 }
 
 // ------------------------------------------------------------------ combine
+// A CTA takes some columns of one token; rows of up to eight places are in flight.
 constexpr int kCombineThr = 128;
-template <typename OUT>
+template <bool BF16>
 __global__ void __launch_bounds__(kCombineThr) moe_combine_kernel(const MoeTcParams p) {
     __shared__ int pos[kMoeMaxTopK];
-    __shared__ float weight[kMoeMaxTopK];
+    __shared__ float weight[kMoeMaxTopK], unscale[kMoeMaxTopK];
+    constexpr int V = BF16 ? 8 : 4;                        // columns of a thread: 16 bytes of a row
     pdl_launch_dependents();
     pdl_wait();
-    const int t = blockIdx.x, H = p.w.H, h = (blockIdx.y * kCombineThr + threadIdx.x) * 4;
+    const int t = blockIdx.x, H = p.w.H, h = (blockIdx.y * kCombineThr + threadIdx.x) * V;
     if (threadIdx.x < kMoeMaxTopK) {
         const int at = int(threadIdx.x) < p.k ? p.pos[size_t(t) * p.k + threadIdx.x] : -1;
         pos[threadIdx.x] = at;
         weight[threadIdx.x] = at >= 0 ? p.weights[size_t(t) * p.k + threadIdx.x] : 0.f;
+        unscale[threadIdx.x] = BF16 && at >= 0 ? inverse_pow2(p.sout[at]) : 1.f;
     }
     __syncthreads();
     if (h >= H) return;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float v[V];
+#pragma unroll
+    for (int c = 0; c < V; ++c) v[c] = 0.f;
+    const size_t row = size_t(H) * (BF16 ? 2 : 4);
     for (int j0 = 0; j0 < p.k; j0 += 8) {
-        float4 o[8];
+        uint4 o[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int at = j0 + j < kMoeMaxTopK ? pos[j0 + j] : -1;
-            o[j] = at >= 0 ? __ldcs(reinterpret_cast<const float4*>(p.out + size_t(at) * H + h)) : make_float4(0.f, 0.f, 0.f, 0.f);
+            o[j] = at >= 0 ? __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.out) + at * row + size_t(h) * (16 / V)))
+                           : make_uint4(0u, 0u, 0u, 0u);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             if (j0 + j >= kMoeMaxTopK || pos[j0 + j] < 0) continue;
-            const float w = weight[j0 + j];
-            v.x = __fmaf_rn(w, o[j].x, v.x);
-            v.y = __fmaf_rn(w, o[j].y, v.y);
-            v.z = __fmaf_rn(w, o[j].z, v.z);
-            v.w = __fmaf_rn(w, o[j].w, v.w);
+            const float w = weight[j0 + j], u = unscale[j0 + j];
+            const uint32_t a[4] = {o[j].x, o[j].y, o[j].z, o[j].w};
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                if constexpr (BF16) {
+                    const float2 x = __half22float2(*reinterpret_cast<const __half2*>(&a[c]));
+                    v[2 * c] = __fmaf_rn(w, __fmul_rn(x.x, u), v[2 * c]);
+                    v[2 * c + 1] = __fmaf_rn(w, __fmul_rn(x.y, u), v[2 * c + 1]);
+                } else {
+                    v[c] = __fmaf_rn(w, __uint_as_float(a[c]), v[c]);
+                }
+            }
         }
     }
-    const size_t at = size_t(t) * H + h;
-    if constexpr (sizeof(OUT) == 4) {
-        float4* y = reinterpret_cast<float4*>(static_cast<float*>(p.y) + at);
-        if (p.resid) {
-            const float4 o = *y;
-            v = make_float4(__fadd_rn(o.x, v.x), __fadd_rn(o.y, v.y), __fadd_rn(o.z, v.z), __fadd_rn(o.w, v.w));
-        }
-        *y = v;
-    } else {
-        uint2* y = reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.y) + at);
-        if (p.resid) {
-            const uint2 o = *y;
-            v = make_float4(__fadd_rn(bf16_lo(o.x), v.x), __fadd_rn(bf16_hi(o.x), v.y), __fadd_rn(bf16_lo(o.y), v.z),
-                            __fadd_rn(bf16_hi(o.y), v.w));
-        }
-        *y = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
+    uint4* y = reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + t * row + size_t(h) * (16 / V));
+    uint32_t r[4] = {0u, 0u, 0u, 0u};
+    if (p.resid) {
+        const uint4 o = *y;
+        r[0] = o.x;
+        r[1] = o.y;
+        r[2] = o.z;
+        r[3] = o.w;
     }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        if constexpr (BF16) {
+            if (p.resid) {
+                v[2 * c] = __fadd_rn(bf16_lo(r[c]), v[2 * c]);
+                v[2 * c + 1] = __fadd_rn(bf16_hi(r[c]), v[2 * c + 1]);
+            }
+            r[c] = pack_bf16x2(v[2 * c], v[2 * c + 1]);
+        } else {
+            r[c] = __float_as_uint(p.resid ? __fadd_rn(__uint_as_float(r[c]), v[c]) : v[c]);
+        }
+    }
+    *y = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
 const void* product_fn(bool bf16, bool gate) {
@@ -966,11 +1003,12 @@ MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k) {
     z.pos = z.tiles + (experts + P / 16) * 16;
     z.isx = z.pos + up16(S * 4);
     z.sact = z.isx + up16(P * 4);
-    z.xs = z.sact + up16(P * 4);
+    z.sout = z.sact + up16(P * 4);
+    z.xs = z.sout + up16(P * 4);
     z.blocks = P / 8;
     z.as = z.xs + staged_bytes(w.H, np, P / 8);
     z.out = z.as + staged_bytes(w.I, np, P / 8);
-    z.total = z.out + P * w.H * 4;
+    z.total = z.out + P * w.H * (bf16 ? 2 : 4);
     return z;
 }
 
@@ -984,15 +1022,16 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
         const size_t smem = kSmem;
         if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
     }
-    const void* combine = bf16 ? (const void*)moe_combine_kernel<uint16_t> : (const void*)moe_combine_kernel<float>;
-    return launch_dependent(combine, dim3(p.T, (p.w.H / 4 + kCombineThr - 1) / kCombineThr), kCombineThr, 0, 1, q, st);
+    const void* combine = bf16 ? (const void*)moe_combine_kernel<true> : (const void*)moe_combine_kernel<false>;
+    const int cols = kCombineThr * (bf16 ? 8 : 4);
+    return launch_dependent(combine, dim3(p.T, (p.w.H + cols - 1) / cols), kCombineThr, 0, 1, q, st);
 }
 
 cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_down, float* norms, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(norms, 0, size_t(w.E) * 2 * 4, st);
+    cudaError_t e = cudaMemsetAsync(norms, 0, size_t(w.E) * 3 * 4, st);
     if (e != cudaSuccess) return e;
-    moe_factors_kernel<<<dim3((2 * w.I + 127) / 128, w.E), 128, 0, st>>>(w.gate_up, w.I / 8, w.H / 128, rho_gate_up, norms);
-    moe_factors_kernel<<<dim3((w.H + 127) / 128, w.E), 128, 0, st>>>(w.down, w.H / 16, w.I / 128, rho_down, nullptr);
+    moe_factors_kernel<<<dim3((2 * w.I + 127) / 128, w.E), 128, 0, st>>>(w.gate_up, w.I / 8, w.H / 128, rho_gate_up, norms, 0);
+    moe_factors_kernel<<<dim3((w.H + 127) / 128, w.E), 128, 0, st>>>(w.down, w.H / 16, w.I / 128, rho_down, norms, 2);
     return cudaGetLastError();
 }
 
@@ -1004,8 +1043,8 @@ cudaError_t moe_tc_set_attributes() {
             if (e != cudaSuccess) return e;
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, (const void*)moe_stage_kernel<uint16_t, 1>,
-                            (const void*)moe_stage_kernel<float, 2>, (const void*)moe_combine_kernel<uint16_t>,
-                            (const void*)moe_combine_kernel<float>};
+                            (const void*)moe_stage_kernel<float, 2>, (const void*)moe_combine_kernel<true>,
+                            (const void*)moe_combine_kernel<false>};
     for (const void* fn : others) {
         cudaFuncAttributes a;
         if ((e = cudaFuncGetAttributes(&a, fn)) != cudaSuccess) return e;

@@ -84,7 +84,7 @@ def test_prepare_and_factors(L):
         m = kmr.MoeStruct(**{**MOE, **kw})
         assert L.kmr_moe_prepare(ctypes.addressof(m), None) == code
     F = L.kmr_moe_factors_size
-    assert F(3, 256, 128) == 3 * (2 * 128 + 256 + 2) * 4
+    assert F(3, 256, 128) == 3 * (2 * 128 + 256 + 3) * 4
     assert F(0, 256, 128) == F(1025, 256, 128) == F(3, 200, 128) == F(3, 256, 8320) == 0
 
 
