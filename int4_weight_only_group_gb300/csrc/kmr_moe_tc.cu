@@ -81,23 +81,19 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
     count[tid] = 0;
     __syncthreads();
     // each place's expert and its rank among the expert's places (which rank it gets does not change any result)
-    constexpr int kPer = kMoeChunkPlaces / kPlanThr, kB = 8;
+    constexpr int kPer = kMoeChunkPlaces / kPlanThr;
     uint32_t mine[kPer];
 #pragma unroll
-    for (int b0 = 0; b0 < kPer; b0 += kB) {
-        if (b0 * kPlanThr >= S) break;
-        int e[kB];
+    for (int b = 0; b < kPer; ++b) {
+        const int i = b * kPlanThr + tid;
+        mine[b] = i < S ? uint32_t(p.ids[i]) : 0xffffffffu;
+    }
 #pragma unroll
-        for (int b = 0; b < kB; ++b) {
-            const int i = (b0 + b) * kPlanThr + tid;
-            e[b] = i < S ? p.ids[i] : -1;
-        }
-#pragma unroll
-        for (int b = 0; b < kB; ++b) {
-            const bool real = e[b] >= 0 && e[b] < p.w.E;
-            if (!real && e[b] != -1) set_error(p.err, KMR_ERR_INVALID_ARG);
-            mine[b0 + b] = real ? uint32_t(e[b]) << 16 | uint32_t(atomicAdd(&count[e[b]], 1)) : 0xffffffffu;
-        }
+    for (int b = 0; b < kPer; ++b) {
+        if (b * kPlanThr >= S) break;
+        const bool real = mine[b] < uint32_t(p.w.E);
+        if (!real && mine[b] != 0xffffffffu) set_error(p.err, KMR_ERR_INVALID_ARG);
+        mine[b] = real ? mine[b] << 16 | uint32_t(atomicAdd(&count[mine[b]], 1)) : 0xffffffffu;
     }
     __syncthreads();
     // thread e: its expert's padded positions and tiles, and those before it
@@ -165,31 +161,19 @@ __device__ __forceinline__ void put_sum(void* row, int h, float X, size_t stride
 
 // ------------------------------------------------------------------ stage
 constexpr int kStageThr = 256;
-template <typename IN, int NP>
+template <typename IN, int NP, int PER>
 __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams p) {
     __shared__ float red[2][kStageThr / 32];
-    __shared__ int pos[kMoeMaxTopK];
+    __shared__ int pos[kMoeMaxTopK], places;
     __shared__ __align__(16) __half sums[kMoeMaxDim / 64 * 2];          // of the row, as a pair's 16 bytes
     pdl_launch_dependents();
     pdl_wait();
     const int t = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int K = p.w.H, K4 = K >> 2;
-    int n = 0;
-    if (tid < 32) {
-        const int at = tid < p.k ? p.pos[size_t(t) * p.k + tid] : -1;
-        const uint32_t some = __ballot_sync(kFull, at >= 0);
-        if (at >= 0) pos[__popc(some & ((1u << lane) - 1u))] = at;
-        if (lane == 0) red[0][0] = __int_as_float(__popc(some));
-    }
-    __syncthreads();
-    n = __float_as_int(red[0][0]);
-    if (n == 0) return;
-    __syncthreads();
-    constexpr int kPer = kMoeMaxDim / 4 / kStageThr;
-    float4 v[kPer];
+    float4 v[PER];
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int k4 = tid + i * kStageThr;
         v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
         if (k4 >= K4) continue;
@@ -199,11 +183,20 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
             const uint2 r = reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.x) + size_t(t) * K)[k4];
             v[i] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
         }
-        m = fmaxf(m, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
     }
+    if (warp == 0) {
+        const int at = lane < p.k ? p.pos[size_t(t) * p.k + lane] : -1;
+        const uint32_t some = __ballot_sync(kFull, at >= 0);
+        if (at >= 0) pos[__popc(some & ((1u << lane) - 1u))] = at;
+        if (lane == 0) places = __popc(some);
+    }
+#pragma unroll
+    for (int i = 0; i < PER; ++i) m = fmaxf(m, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
     m = warp_max(m);
     if (lane == 0) red[0][warp] = m;
     __syncthreads();
+    const int n = places;
+    if (n == 0) return;
     m = red[0][0];
 #pragma unroll
     for (int w = 1; w < kStageThr / 32; ++w) m = fmaxf(m, red[0][w]);
@@ -213,7 +206,7 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
     const size_t blocks = p.blocks;
     auto h2u = [](__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); };
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
+    for (int i = 0; i < PER; ++i) {
         const int k4 = tid + i * kStageThr;
         if (k4 >= K4) break;                                        // (whole warps: K4 is a multiple of 32)
         const int k = k4 * 4, m4 = k4 & 3;
@@ -983,6 +976,17 @@ const void* product_fn(bool bf16, bool gate) {
     return gate ? (const void*)moe_product_kernel<2, true> : (const void*)moe_product_kernel<2, false>;
 }
 
+const void* stage_fn(bool bf16, int H) {
+#define KMR_STAGE(n) \
+    if (H <= n * kStageThr * 4) return bf16 ? (const void*)moe_stage_kernel<uint16_t, 1, n> : (const void*)moe_stage_kernel<float, 2, n>
+    KMR_STAGE(1);
+    KMR_STAGE(2);
+    KMR_STAGE(4);
+    KMR_STAGE(8);
+#undef KMR_STAGE
+    return nullptr;
+}
+
 size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
 
 }  // namespace
@@ -1016,8 +1020,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     const MoeTcParams* q = &p;
     cudaError_t e = launch_dependent((const void*)moe_plan_kernel, dim3(1), kPlanThr, 0, 1, q, st);
     if (e != cudaSuccess) return e;
-    const void* stage = bf16 ? (const void*)moe_stage_kernel<uint16_t, 1> : (const void*)moe_stage_kernel<float, 2>;
-    if ((e = launch_dependent(stage, dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
+    if ((e = launch_dependent(stage_fn(bf16, p.w.H), dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
         const size_t smem = kSmem;
         if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
@@ -1042,8 +1045,9 @@ cudaError_t moe_tc_set_attributes() {
             e = cudaFuncSetAttribute(product_fn(b != 0, gate != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
             if (e != cudaSuccess) return e;
         }
-    const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, (const void*)moe_stage_kernel<uint16_t, 1>,
-                            (const void*)moe_stage_kernel<float, 2>, (const void*)moe_combine_kernel<true>,
+    const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, stage_fn(true, 1024), stage_fn(true, 2048),
+                            stage_fn(true, 4096), stage_fn(true, 8192), stage_fn(false, 1024), stage_fn(false, 2048),
+                            stage_fn(false, 4096), stage_fn(false, 8192), (const void*)moe_combine_kernel<true>,
                             (const void*)moe_combine_kernel<false>};
     for (const void* fn : others) {
         cudaFuncAttributes a;
