@@ -10,7 +10,8 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxDim = 8192;             // hidden and intermediate sizes, multiples of 128
 constexpr int kMoeMaxTokens = 1 << 20;
-constexpr int kMoeSmallPlaces = 32;          // places (token, j) of one pass of the small form: a warp's lanes
+constexpr int kMoeSmallPlaces = 32;          // places (token, j) of the small form: a warp's lanes
+constexpr int kMoeSmallCtas = 128;           // CTAs at once that its sizes are made for (a GB300 has 152 SMs)
 
 // ------------------------------------------------------------------ router
 struct MoeRouteParams {
@@ -28,7 +29,7 @@ struct MoeView {
     const uint8_t* down;                     // [E] KMR4 matrices [H, I]
     int E, H, I;
 };
-// Small form: up to kMoeSmallPlaces places a pass.
+// Small form: up to kMoeSmallPlaces places whose rows fit into shared memory beside two tiles of weights.
 struct MoeSmallParams {
     MoeView w;
     const void* x;                           // [T][H]
@@ -38,9 +39,10 @@ struct MoeSmallParams {
     float* act;                              // [T * k][I]
     void* y;                                 // [T][H]
     int resid;                               // add to y
-    int stages, batch;                       // ring of `stages` tiles, `batch` of them at a time (set by the launch)
+    int stages, batch, list;                 // ring of `stages` tiles, `batch` of them at a time, `list` in all (set by the launch)
     int* err;
 };
+bool moe_small_fits(const MoeView& w, bool bf16, int T, int k);
 cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaStream_t st);
 cudaError_t moe_small_set_attributes();
 

@@ -29,7 +29,6 @@ int counts_ok(int T, int top_k) {
 }
 
 // The few-token form takes the calls whose places fit a warp's lanes.
-bool small(int T, int top_k) { return (long long)T * top_k <= kMoeSmallPlaces; }
 // Tokens of one pass of the grouped form: bounds the workspace.
 int chunk_of(int T, int top_k) {
     const int most = kMoeChunkPlaces / top_k;
@@ -82,7 +81,7 @@ extern "C" int kmr_moe_prepare(const kmr_moe* moe, void* stream) {
 extern "C" size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, int T, int top_k) {
     MoeView v;
     if (view_of(moe, &v) != KMR_OK || !dtype_ok(dtype) || counts_ok(T, top_k) != KMR_OK) return 0;
-    if (small(T, top_k)) return size_t(kMoeSmallPlaces) * v.I * 4;
+    if (moe_small_fits(v, dtype == KMR_BF16, T, top_k)) return size_t(T) * top_k * v.I * 4;
     return moe_tc_sizes(v, dtype == KMR_BF16, chunk_of(T, top_k), top_k).total;
 }
 
@@ -101,7 +100,7 @@ extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, con
     if (ensure_kernel_attributes() != cudaSuccess || !(err = standalone_error_word())) return KMR_ERR_CUDA;
     const bool bf16 = dtype == KMR_BF16;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
-    if (small(T, top_k)) {
+    if (moe_small_fits(v, bf16, T, top_k)) {
         MoeSmallParams p = {};
         p.w = v;
         p.x = x;

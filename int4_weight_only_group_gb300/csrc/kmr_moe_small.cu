@@ -32,6 +32,7 @@ constexpr uint32_t kFull = 0xffffffffu;
 // ------------------------------------------------------------------ the call's plan, in a warp's registers
 struct Plan {
     int id;                  // expert of place `lane`, or -1
+    uint32_t same;           // the places of that expert
     uint32_t leaders;        // first place of each distinct expert
 };
 __device__ __forceinline__ Plan make_plan(const int32_t* ids, int S, int E, int* err, bool report) {
@@ -42,11 +43,15 @@ __device__ __forceinline__ Plan make_plan(const int32_t* ids, int S, int E, int*
         if (report) set_error(err, KMR_ERR_INVALID_ARG);
         pl.id = -1;
     }
-    const uint32_t same = __match_any_sync(kFull, pl.id);
-    pl.leaders = __ballot_sync(kFull, pl.id >= 0 && __ffs(same) - 1 == lane);
+    pl.same = __match_any_sync(kFull, pl.id);
+    pl.leaders = __ballot_sync(kFull, pl.id >= 0 && __ffs(pl.same) - 1 == lane);
     return pl;
 }
-// The n-th set bit of m, n < popc(m).
+// Most places of one expert.
+__device__ __forceinline__ int most_places(const Plan& pl) {
+    return int(__reduce_max_sync(kFull, pl.id >= 0 ? uint32_t(__popc(pl.same)) : 0u));
+}
+// The n-th set bit of m (the last one, if it has no more).
 __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
     int at = 0;
 #pragma unroll
@@ -60,56 +65,94 @@ __device__ __forceinline__ int nth_bit(uint32_t m, int n) {
     return at;
 }
 
+// A tile of the CTA's sequence: its number among the experts' tiles and within its expert, and its expert's places.
+struct __align__(16) Tile {
+    int from, row;
+    uint32_t places;
+    int unused;
+};
+
 // ------------------------------------------------------------------ operands
+// The rows wait in shared memory as B fragments: per (row, group of 128) the four quarters t of the lanes, each the 16 registers of
+// its 8 steps (inputs 8 i + 2 t and + 1 in register i), in 16-byte pieces that two quarters exchange so that a load meets no
+// bank twice; SPLIT: the remainders behind them.  Beside them, for each term, its sum and 1 / sigma.
+template <bool SPLIT>
+constexpr int kItemBytes = SPLIT ? 512 : 256;
+template <typename IN, bool SPLIT>
+__device__ __forceinline__ void stage_rows(uint8_t* to, float4* fold, const IN* x, int items) {
+    constexpr int kAtOnce = 4;
+    const int lane = threadIdx.x & 31, i = lane >> 1;
+    const int at = (lane & 1) * 128 + ((((i >> 2) ^ (lane & 1)) << 2) + (i & 3)) * 4;     // quarter 2 (lane & 1), register i
+    for (int i0 = threadIdx.x >> 5; i0 < items; i0 += kWarps * kAtOnce) {
+        float4 v[kAtOnce];
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const size_t src = size_t(min(i0 + q * kWarps, items - 1)) * 128 + lane * 4;
+            if constexpr (sizeof(IN) == 4) {
+                v[q] = __ldcg(reinterpret_cast<const float4*>(x + src));
+            } else {
+                const uint2 r = __ldcg(reinterpret_cast<const uint2*>(x + src));
+                v[q] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < kAtOnce; ++q) {
+            const int item = i0 + q * kWarps;
+            if (item >= items) break;
+            const float m = fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w)));
+            float sig, isg;
+            pow2_scale(__reduce_max_sync(kFull, __float_as_uint(m)), sig, isg);
+            float r[4] = {__fmul_rn(v[q].x, sig), __fmul_rn(v[q].y, sig), __fmul_rn(v[q].z, sig), __fmul_rn(v[q].w, sig)};
+            float X[2] = {0.f, 0.f};
+            uint8_t* dst = to + size_t(item) * kItemBytes<SPLIT> + at;
+#pragma unroll
+            for (int term = 0; term < (SPLIT ? 2 : 1); ++term) {
+                const __half2 a = __floats2half2_rn(r[0], r[1]), b = __floats2half2_rn(r[2], r[3]);
+                const float2 fa = __half22float2(a), fb = __half22float2(b);
+                X[term] = __fadd_rn(__fadd_rn(fa.x, fa.y), __fadd_rn(fb.x, fb.y));
+                r[0] = __fsub_rn(r[0], fa.x);
+                r[1] = __fsub_rn(r[1], fa.y);
+                r[2] = __fsub_rn(r[2], fb.x);
+                r[3] = __fsub_rn(r[3], fb.y);
+                *reinterpret_cast<__half2*>(dst + term * 256) = a;
+                *reinterpret_cast<__half2*>(dst + term * 256 + 64) = b;
+            }
+            // the lower half of the lanes sums the first terms, the upper half the remainders
+            float sum = __fadd_rn(lane < 16 ? X[0] : X[1], __shfl_xor_sync(kFull, lane < 16 ? X[1] : X[0], 16));
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
+            if ((lane & 15) == 0) *reinterpret_cast<float2*>(reinterpret_cast<float*>(fold + item) + (lane >> 3)) = make_float2(sum, isg);
+        }
+    }
+}
+
 // B fragments of one 128-input group of up to 8 (SPLIT: 4) rows for this lane, and the group's fold constants.
 struct Frag {
     uint32_t b[16];
     float X0, is0, X1, is1;  // of columns 2t and 2t + 1: sum of the staged values, 1 / sigma
 };
-// This lane's inputs of one group: row (column lane / 4, SPLIT: (lane / 4) % 4 with the remainders in columns 4..7) at the
-// group's first input.  A lane without a row reads another's and takes zeros, so that all loads go out together.
-template <typename IN>
-__device__ __forceinline__ void load_raw(float (&v)[32], const IN* row, bool real, int lane) {
-    const int t = lane & 3;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        float2 u;
-        if constexpr (sizeof(IN) == 4) {
-            u = __ldcg(reinterpret_cast<const float2*>(row + 8 * i + 2 * t));
-        } else {
-            const uint32_t r = __ldcg(reinterpret_cast<const uint32_t*>(row + 8 * i + 2 * t));
-            u = make_float2(bf16_lo(r), bf16_hi(r));
-        }
-        v[2 * i] = real ? u.x : 0.f;
-        v[2 * i + 1] = real ? u.y : 0.f;
-    }
-}
+// Column lane / 4 takes staged item `item` (SPLIT: columns 4..7 its remainders), or zeros if that is negative.
 template <bool SPLIT>
-__device__ __forceinline__ void make_frag(Frag& f, const float (&v)[32], int lane) {
+__device__ __forceinline__ void load_frag(Frag& f, const uint8_t* staged, const float4* fold, int item, int lane) {
     const int t = lane & 3;
-    float m = 0.f;
+    const bool rest = SPLIT && lane >= 16;
+    float X = 0.f, isg = 1.f;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 1));
-    m = fmaxf(m, __shfl_xor_sync(kFull, m, 2));
-    float sig, isg;
-    pow2_scale(__float_as_uint(m), sig, isg);
-    float X = 0.f;
+    for (int c = 0; c < 16; ++c) f.b[c] = 0u;
+    if (item >= 0) {
+        const uint8_t* at = staged + size_t(item) * kItemBytes<SPLIT> + (rest ? 256 : 0) + t * 64;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const float a = __fmul_rn(v[2 * i], sig), b = __fmul_rn(v[2 * i + 1], sig);
-        __half2 h = __floats2half2_rn(a, b);
-        if (SPLIT) {
-            const float2 r = __half22float2(h);
-            const __half2 l = __floats2half2_rn(__fsub_rn(a, r.x), __fsub_rn(b, r.y));
-            h = lane >= 16 ? l : h;
+        for (int c = 0; c < 4; ++c) {
+            const uint4 v = *reinterpret_cast<const uint4*>(at + ((c ^ (t >> 1)) << 4));
+            f.b[4 * c] = v.x;
+            f.b[4 * c + 1] = v.y;
+            f.b[4 * c + 2] = v.z;
+            f.b[4 * c + 3] = v.w;
         }
-        const float2 s = __half22float2(h);
-        X = __fadd_rn(X, __fadd_rn(s.x, s.y));
-        f.b[i] = *reinterpret_cast<const uint32_t*>(&h);
+        const float2 k = reinterpret_cast<const float2*>(fold + item)[rest ? 1 : 0];
+        X = k.x;
+        isg = k.y;
     }
-    X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 1));
-    X = __fadd_rn(X, __shfl_xor_sync(kFull, X, 2));
     f.X0 = __shfl_sync(kFull, X, 8 * t);
     f.X1 = __shfl_sync(kFull, X, 8 * t + 4);
     f.is0 = __shfl_sync(kFull, isg, 8 * t);
@@ -117,11 +160,10 @@ __device__ __forceinline__ void make_frag(Frag& f, const float (&v)[32], int lan
 }
 
 // acc (rows g and g + 8, columns 2t and 2t + 1) += one (16-row tile, 128-input group) block times the fragments.
+// A code's four bits are themselves an fp16: q 2^-24, subnormal (rows g + 8: 16 q 2^-24), and the MMA takes it exactly, so that a
+// register of codes costs one AND.  w = q s + (z - 8 s); the group's sum is scaled back before s, exactly.
 __device__ __forceinline__ void block_product(const uint8_t* gb, const Frag& f, int lane, float (&acc)[4]) {
     const int g = lane >> 2;
-    const __half2 m8 = __float2half2_rn(-1032.f), c16 = __float2half2_rn(0.0625f), m72 = __float2half2_rn(-72.f);
-    auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
-    auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
     float d[2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) d[c][0] = d[c][1] = d[c][2] = d[c][3] = 0.f;
@@ -132,32 +174,56 @@ __device__ __forceinline__ void block_product(const uint8_t* gb, const Frag& f, 
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const uint32_t w = w4[ks], w2 = w >> 8;
-            // 1024 + q less 1032, and (1024 + 16 q) / 16 less 72: exact
-            mma16816(d[ks & 1], u2(__hadd2(h2(and_or(w, 0x000F000Fu, 0x64006400u)), m8)),
-                     u2(__hfma2(h2(and_or(w, 0x00F000F0u, 0x64006400u)), c16, m72)),
-                     u2(__hadd2(h2(and_or(w2, 0x000F000Fu, 0x64006400u)), m8)),
-                     u2(__hfma2(h2(and_or(w2, 0x00F000F0u, 0x64006400u)), c16, m72)), f.b[blk * 8 + 2 * ks],
+            mma16816(d[ks & 1], w & 0x000F000Fu, w & 0x00F000F0u, w2 & 0x000F000Fu, w2 & 0x00F000F0u, f.b[blk * 8 + 2 * ks],
                      f.b[blk * 8 + 2 * ks + 1]);
         }
     }
+    auto fold = [](uint32_t sz, float D, float X, float is, float a) {
+        const float s = bf16_lo(sz), z = __fmaf_rn(-8.f, s, bf16_hi(sz));
+        return __fmaf_rn(__fmaf_rn(s, D, __fmul_rn(z, X)), is, a);
+    };
     const uint32_t sz0 = *reinterpret_cast<const uint32_t*>(gb + 1024 + g * 4);
     const uint32_t sz1 = *reinterpret_cast<const uint32_t*>(gb + 1024 + (g + 8) * 4);
-    auto fold = [](uint32_t sz, float D, float X) { return __fmaf_rn(bf16_lo(sz), D, __fmul_rn(bf16_hi(sz), X)); };
-    acc[0] = __fmaf_rn(fold(sz0, __fadd_rn(d[0][0], d[1][0]), f.X0), f.is0, acc[0]);
-    acc[1] = __fmaf_rn(fold(sz0, __fadd_rn(d[0][1], d[1][1]), f.X1), f.is1, acc[1]);
-    acc[2] = __fmaf_rn(fold(sz1, __fadd_rn(d[0][2], d[1][2]), f.X0), f.is0, acc[2]);
-    acc[3] = __fmaf_rn(fold(sz1, __fadd_rn(d[0][3], d[1][3]), f.X1), f.is1, acc[3]);
+    acc[0] = fold(sz0, __fmul_rn(__fadd_rn(d[0][0], d[1][0]), 0x1p24f), f.X0, f.is0, acc[0]);
+    acc[1] = fold(sz0, __fmul_rn(__fadd_rn(d[0][1], d[1][1]), 0x1p24f), f.X1, f.is1, acc[1]);
+    acc[2] = fold(sz1, __fmul_rn(__fadd_rn(d[0][2], d[1][2]), 0x1p20f), f.X0, f.is0, acc[2]);
+    acc[3] = fold(sz1, __fmul_rn(__fadd_rn(d[0][3], d[1][3]), 0x1p20f), f.X1, f.is1, acc[3]);
 }
 
-// This warp's partial of a tile, [16 rows][8 columns].
-__device__ __forceinline__ void store_part8(float* to, int lane, const float (&acc)[4]) {
-    const int g = lane >> 2, c = 2 * (lane & 3);
-    *reinterpret_cast<float2*>(to + g * 8 + c) = make_float2(acc[0], acc[1]);
-    *reinterpret_cast<float2*>(to + (g + 8) * 8 + c) = make_float2(acc[2], acc[3]);
+// The columns' sums of one warp's groups of a tile: acc (rows g and g + 8, columns 2t and 2t + 1).  `row` is the staged row of column
+// lane / 4 (of 8, SPLIT: of 4 and again), or negative; SPLIT: the remainders' columns are added to their rows'.  `f` and `held`
+// keep the fragments from one tile to the next.
+template <bool SPLIT>
+__device__ __forceinline__ void tile_product(const uint8_t* tile, const uint8_t* staged, const float4* fold, int row, int G, int w,
+                                             int lane, Frag& f, int& held, float (&acc)[4]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q] = 0.f;
+    for (int grp = w; grp < G; grp += kWarps) {
+        const int item = row < 0 ? -1 : row * G + grp;
+        if (__any_sync(kFull, item != held)) {
+            load_frag<SPLIT>(f, staged, fold, item, lane);
+            held = item;
+        }
+        block_product(tile + grp * kGroupBytes, f, lane, acc);
+    }
+    if (SPLIT) {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) acc[q] = __fadd_rn(acc[q], __shfl_xor_sync(kFull, acc[q], 2));
+    }
 }
-
-// Warps that share a tile: the smallest power of two that covers its groups, 16 at most.
-__host__ __device__ constexpr int group_warps(int G) { return G >= kWarps ? kWarps : pow2_at_least(G); }
+// (tile i, part w) of a batch in the order of the warps, 16 at a time, without a division for each.
+struct Turn {
+    int i, w;
+};
+__device__ __forceinline__ Turn first_turn(int warp, int P) { return {warp / P, warp % P}; }
+__device__ __forceinline__ void next_turn(Turn& t, int P, int di, int dw) {
+    t.i += di;
+    t.w += dw;
+    if (t.w >= P) {
+        t.w -= P;
+        ++t.i;
+    }
+}
 
 // ------------------------------------------------------------------ the ring of tiles
 // Tile i of the CTA's sequence lives in stage i % stages; the tiles of a batch (half the ring) are fetched together
@@ -167,11 +233,27 @@ struct Ring {
     uint64_t* full;
     int tile_bytes, stages;
 };
-__device__ __forceinline__ void fetch(const Ring& r, int i, const uint8_t* from, uint64_t pol) {      // by warp 0
-    if (!elect_one()) return;
+__device__ __forceinline__ void fetch(const Ring& r, int i, const uint8_t* from, uint64_t pol) {      // by one lane
     const int s = i % r.stages;
     mbar_arrive_expect_tx(&r.full[s], uint32_t(r.tile_bytes));
     bulk_g2s_stream(r.data + size_t(s) * r.tile_bytes, from, uint32_t(r.tile_bytes), &r.full[s], pol);
+}
+// Where everything lies in shared memory: ring, barriers, tile list, fold constants, staged rows, partial sums.
+__host__ __device__ constexpr int parts_of(int G) { return G < kWarps ? G : kWarps; }
+struct Layout {
+    size_t full, list, fold, staged, part, total;
+};
+__host__ __device__ inline Layout layout_of(bool down, bool split, int K, int rows, int stages, int batch, int tiles) {
+    const int G = K >> 7;
+    Layout l;
+    l.full = size_t(stages) * G * kGroupBytes;
+    l.list = l.full + size_t(stages + (stages & 1)) * 8;
+    l.fold = l.list + size_t(tiles) * sizeof(Tile);
+    l.staged = l.fold + size_t(rows) * G * 16;
+    l.part = l.staged + size_t(rows) * G * (split ? 512 : 256);
+    // gate_up: [batch][part][16 rows][columns]; down: [place][part][16 rows]
+    l.total = l.part + size_t(down ? rows : batch * (split ? 4 : 8)) * parts_of(G) * 64;
+    return l;
 }
 
 __device__ __forceinline__ float silu_mul(float x, float up) {
@@ -179,169 +261,176 @@ __device__ __forceinline__ float silu_mul(float x, float up) {
 }
 
 // ------------------------------------------------------------------ gate_up
-template <typename IN, bool SPLIT, int GPW>
-__global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallParams p) {
+// (Two CTAs to an SM: the down kernel's start beside gate_up's, and their weights are on the way while it works.)
+template <typename IN, bool SPLIT>
+__global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int most;
     constexpr int CAP = SPLIT ? 4 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.w.H >> 7, GW = group_warps(G), NT = kWarps / GW, wg = warp & (GW - 1), wt = warp / GW;
+    const int G = p.w.H >> 7, P = parts_of(G);
     const int tiles = p.w.I >> 3;                       // 16-row tiles (8 gate, 8 up) of an expert
-    const Ring ring = {smem, reinterpret_cast<uint64_t*>(smem + size_t(p.stages) * G * kGroupBytes), G * kGroupBytes, p.stages};
-    float* part = reinterpret_cast<float*>(ring.full + p.stages + (p.stages & 1));   // [batch][GW][16][8]
+    const Layout l = layout_of(false, SPLIT, p.w.H, p.T, p.stages, p.batch, p.list);
+    const Ring ring = {smem, reinterpret_cast<uint64_t*>(smem + l.full), G * kGroupBytes, p.stages};
+    Tile* list = reinterpret_cast<Tile*>(smem + l.list);
+    float4* fold = reinterpret_cast<float4*>(smem + l.fold);
+    uint8_t* staged = smem + l.staged;
+    float* part = reinterpret_cast<float*>(smem + l.part);
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&ring.full[s], 1);
         fence_mbar_init();
     }
+    __syncwarp();
     pdl_wait();
     pdl_launch_dependents();                            // (after the wait: see the down kernel's prologue)
     const Plan pl = make_plan(p.ids, p.T * p.k, p.w.E, p.err, blockIdx.x == 0 && warp == 0);
     const long long W = (long long)__popc(pl.leaders) * tiles;
     const long long first = W * blockIdx.x / gridDim.x;
     const int n = int(W * (blockIdx.x + 1) / gridDim.x - first);
-    const int u0 = int(first / tiles), r0 = int(first % tiles);
-    // tile i of the sequence: row tile (r0 + i) % tiles of the (u0 + (r0 + i) / tiles)-th distinct expert
-    auto expert = [&](int i) { return __shfl_sync(kFull, pl.id, nth_bit(pl.leaders, u0 + (r0 + i) / tiles)); };
-    __syncthreads();
     const uint64_t pol = policy_evict_first();
-    auto fill = [&](int from, int to) {                 // warp 0
-        for (int i = from; i < to; ++i)
-            fetch(ring, i, p.w.gate_up + (size_t(expert(i)) * tiles + (r0 + i) % tiles) * ring.tile_bytes, pol);
-    };
-    if (warp == 0) fill(0, min(n, p.stages));
-    Frag f[GPW];
-    int staged = -1;                                    // expert and pass whose rows the fragments hold
-    for (int b0 = 0; b0 < n; b0 += p.batch) {
+    if (warp == 0) {
+        const int u0 = int(first / tiles), r0 = int(first % tiles);
+        for (int i0 = 0; i0 < n; i0 += 32) {            // tile i: row tile (r0 + i) % tiles of a distinct expert
+            const int i = min(i0 + lane, n - 1), at = nth_bit(pl.leaders, u0 + (r0 + i) / tiles);
+            Tile t;
+            t.row = (r0 + i) % tiles;
+            t.from = __shfl_sync(kFull, pl.id, at) * tiles + t.row;
+            t.places = __shfl_sync(kFull, pl.same, at);
+            t.unused = 0;
+            if (i0 + lane < n) {
+                list[i] = t;
+                if (i < p.stages) fetch(ring, i, p.w.gate_up + size_t(t.from) * ring.tile_bytes, pol);
+            }
+        }
+        const int m = most_places(pl);
+        if (lane == 0) most = m;
+    }
+    stage_rows<IN, SPLIT>(staged, fold, static_cast<const IN*>(p.x), p.T * G);
+    const int token = lane / p.k;                       // of place `lane`
+    __syncthreads();
+    const int columns = min(most, CAP), di = kWarps / P, dw = kWarps % P;
+    const Turn t0 = first_turn(warp, P);
+    Frag f;
+    int held = -2;
+    for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
-        int passes = 0;
-        for (int i = b0; i < b0 + nb; ++i) {
-            const int used = __popc(__ballot_sync(kFull, pl.id == expert(i)));
-            passes = max(passes, (used + CAP - 1) / CAP);
-        }
-        for (int ps = 0; ps < passes; ++ps) {
-            for (int i = b0 + wt; i < b0 + nb; i += NT) {
-                const int e = expert(i);
-                const uint32_t places = __ballot_sync(kFull, pl.id == e);
-                const int cols = __popc(places) - ps * CAP;
-                if (cols <= 0 || wg >= G) continue;
-                if (staged != e * kMoeSmallPlaces + ps) {
-                    staged = e * kMoeSmallPlaces + ps;
-                    const int col = SPLIT ? (lane >> 2) & 3 : lane >> 2;
-                    const int place = col < cols ? nth_bit(places, ps * CAP + col) : -1;
-#pragma unroll
-                    for (int j = 0; j < GPW; ++j) {
-                        const int grp = min(wg + j * kWarps, G - 1);
-                        float v[32];
-                        load_raw(v, static_cast<const IN*>(p.x) + size_t(max(place, 0) / p.k) * p.w.H + size_t(grp) * 128, place >= 0, lane);
-                        make_frag<SPLIT>(f[j], v, lane);
-                    }
+        for (int c0 = 0; c0 < most; c0 += CAP) {
+            for (Turn t = t0; t.i < nb; next_turn(t, P, di, dw)) {
+                const uint32_t places = list[b0 + t.i].places;
+                const int cols = __popc(places) - c0, col = SPLIT ? (lane >> 2) & 3 : lane >> 2;
+                if (cols <= 0) continue;
+                int at = 0;                             // column's token
+                if (p.T > 1) at = __shfl_sync(kFull, token, nth_bit(places, c0 + min(col, cols - 1)));
+                if (!__all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err))) continue;
+                float acc[4];
+                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, col < cols ? at : -1, G, t.w, lane, f, held, acc);
+                const int g = lane >> 2, c = 2 * (lane & 3);
+                if (c < CAP) {
+                    float* to = part + ((t.i * P + t.w) * 16 + g) * CAP + c;
+                    *reinterpret_cast<float2*>(to) = make_float2(acc[0], acc[1]);
+                    *reinterpret_cast<float2*>(to + 8 * CAP) = make_float2(acc[2], acc[3]);
                 }
-                const int s = i % p.stages;
-                if (!__all_sync(kFull, mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err))) continue;
-                const uint8_t* tile = ring.data + size_t(s) * ring.tile_bytes;
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < GPW; ++j)
-                    if (wg + j * kWarps < G) block_product(tile + (wg + j * kWarps) * kGroupBytes, f[j], lane, acc);
-                store_part8(part + (size_t(i - b0) * GW + wg) * 128, lane, acc);
             }
             __syncthreads();
-            // two (row, column) of a tile a warp at a time, eight lanes for each row of its gate and its up: a lane sums two of the
-            // (at most 16) partials, then the eight lanes' sums meet
-            int done = 0;                               // (row, column) pairs of the tiles before
-            for (int i = 0; i < nb; ++i) {
-                const uint32_t places = __ballot_sync(kFull, pl.id == expert(b0 + i));
-                const int cols = max(0, min(CAP, __popc(places) - ps * CAP));
-                const int jt = (r0 + b0 + i) % tiles;
-                for (int o = 2 * ((warp - (done >> 1)) & (kWarps - 1)); o < 8 * cols; o += 2 * kWarps) {
-                    const int r = (o & 7) + (lane >> 4), c = o >> 3, w = lane & 7;
-                    const float* at = part + size_t(i) * GW * 128 + (r + ((lane >> 3) & 1) * 8) * 8 + c;
-                    float v = 0.f;
-                    if (w < GW && w < G) v = SPLIT ? __fadd_rn(at[w * 128], at[w * 128 + 4]) : at[w * 128];
-                    if (w + 8 < GW && w + 8 < G) {
-                        const float* b = at + (w + 8) * 128;
-                        v = __fadd_rn(v, SPLIT ? __fadd_rn(b[0], b[4]) : b[0]);
-                    }
-                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 4));
-                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 2));
-                    v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 1));
-                    const float up = __shfl_sync(kFull, v, lane + 8);
-                    if ((lane & 15) == 0) p.act[size_t(nth_bit(places, ps * CAP + c)) * p.w.I + jt * 8 + r] = silu_mul(v, up);
-                }
-                done += 8 * cols;
+            // two outputs of a (tile, column) a warp at a time, eight lanes for each row of its gate and its up: a lane sums two of
+            // the (at most 16) partials, then the eight lanes' sums meet
+            for (int c = 0; c < columns; ++c)
+            for (int o = warp; o < nb * 4; o += kWarps) {
+                const int i = o >> 2;
+                const Tile t = list[b0 + i];
+                if (c0 + c >= __popc(t.places)) continue;
+                const int r = (o & 3) * 2 + (lane >> 4), w = lane & 7;
+                const float* at = part + (i * P * 16 + r + ((lane >> 3) & 1) * 8) * CAP + c;
+                float v = w < P ? at[w * 16 * CAP] : 0.f;
+                if (w + 8 < P) v = __fadd_rn(v, at[(w + 8) * 16 * CAP]);
+                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 4));
+                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 2));
+                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 1));
+                const float up = __shfl_sync(kFull, v, (lane + 8) & 31);
+                if ((lane & 15) == 0) p.act[size_t(nth_bit(t.places, c0 + c)) * p.w.I + t.row * 8 + r] = silu_mul(v, up);
             }
             __syncthreads();
         }
-        if (warp == 0 && b0 + p.stages < n) {
+        if (warp == 0) {
             fence_proxy_async_smem();
-            fill(b0 + p.stages, min(n, b0 + nb + p.stages));
+            for (int i = b0 + p.stages + lane; i < min(n, b0 + nb + p.stages); i += 32)
+                fetch(ring, i, p.w.gate_up + size_t(list[i].from) * ring.tile_bytes, pol);
+        }
+        s0 += p.batch;
+        if (s0 == p.stages) {
+            s0 = 0;
+            phase ^= 1;
         }
     }
 }
 
 // ------------------------------------------------------------------ down
-template <typename OUT, bool SPLIT, int GPW>
-__global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams p) {
+template <typename OUT, bool SPLIT>
+__global__ void __launch_bounds__(kThr, 2) moe_down_kernel(const MoeSmallParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int ids[32];
+    __shared__ float weights[32];
     constexpr int CAP = SPLIT ? 4 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int G = p.w.I >> 7, GW = group_warps(G), NT = kWarps / GW, wg = warp & (GW - 1), wt = warp / GW;
+    const int G = p.w.I >> 7, P = parts_of(G);
     const int tiles = p.w.H >> 4, S = p.T * p.k;
-    const Ring ring = {smem, reinterpret_cast<uint64_t*>(smem + size_t(p.stages) * G * kGroupBytes), G * kGroupBytes, p.stages};
-    float* part = reinterpret_cast<float*>(ring.full + p.stages + (p.stages & 1));   // [place][GW][16]
+    const Layout l = layout_of(true, SPLIT, p.w.I, S, p.stages, p.batch, p.list);
+    const Ring ring = {smem, reinterpret_cast<uint64_t*>(smem + l.full), G * kGroupBytes, p.stages};
+    Tile* list = reinterpret_cast<Tile*>(smem + l.list);
+    float4* fold = reinterpret_cast<float4*>(smem + l.fold);
+    uint8_t* staged = smem + l.staged;
+    float* part = reinterpret_cast<float*>(smem + l.part);
     if (threadIdx.x == 0) {
         for (int s = 0; s < p.stages; ++s) mbar_init(&ring.full[s], 1);
         fence_mbar_init();
     }
-    // The ids were written before gate_up began (it waited for them before it let this kernel start), and the weights
-    // are constant: both are read before the wait for gate_up's results.
+    __syncwarp();
+    // The ids and weights were written before gate_up began (it waited for them before it let this kernel start), and the
+    // experts are constant: they are read before the wait for gate_up's results.
     const Plan pl = make_plan(p.ids, S, p.w.E, p.err, false);
     const int n = __popc(pl.leaders);
-    __syncthreads();
     const uint64_t pol = policy_evict_first();
-    auto fill = [&](int from, int to) {                 // warp 0
-        for (int i = from; i < to; ++i)
-            fetch(ring, i, p.w.down + (size_t(__shfl_sync(kFull, pl.id, nth_bit(pl.leaders, i))) * tiles + blockIdx.x) * ring.tile_bytes,
-                  pol);
-    };
-    if (warp == 0) fill(0, min(n, p.stages));
+    if (warp == 0) {
+        const int at = nth_bit(pl.leaders, min(lane, max(n, 1) - 1)) & 31;
+        Tile t;
+        t.row = blockIdx.x;
+        t.from = __shfl_sync(kFull, pl.id, at) * tiles + t.row;
+        t.places = __shfl_sync(kFull, pl.same, at);
+        t.unused = 0;
+        if (lane < n) {
+            list[lane] = t;
+            if (lane < p.stages) fetch(ring, lane, p.w.down + size_t(t.from) * ring.tile_bytes, pol);
+        }
+        ids[lane] = pl.id;
+        weights[lane] = lane < S ? p.weights[lane] : 0.f;
+    }
     pdl_wait();
     pdl_launch_dependents();
-    for (int b0 = 0; b0 < n; b0 += p.batch) {
+    stage_rows<float, SPLIT>(staged, fold, p.act, S * G);
+    __syncthreads();
+    const int di = kWarps / P, dw = kWarps % P;
+    const Turn t0 = first_turn(warp, P);
+    Frag f;
+    int held = -2;
+    for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
-        for (int i = b0 + wt; i < b0 + nb; i += NT) {
-            if (wg >= G) break;
-            const int e = __shfl_sync(kFull, pl.id, nth_bit(pl.leaders, i));
-            const uint32_t places = __ballot_sync(kFull, pl.id == e);
+        for (Turn t = t0; t.i < nb; next_turn(t, P, di, dw)) {
+            const uint32_t places = list[b0 + t.i].places;
             const int used = __popc(places);
-            const int s = i % p.stages;
-            if (!__all_sync(kFull, mbar_wait(&ring.full[s], uint32_t((i / p.stages) & 1), p.err))) continue;
+            if (!__all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err))) continue;
             for (int c0 = 0; c0 < used; c0 += CAP) {
                 const int col = SPLIT ? (lane >> 2) & 3 : lane >> 2;
-                const int place = c0 + col < used ? nth_bit(places, c0 + col) : -1;
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                for (int j = 0; j < GPW; ++j) {
-                    const int grp = wg + j * kWarps;
-                    if (grp >= G) break;
-                    Frag f;
-                    float v[32];
-                    load_raw(v, p.act + size_t(max(place, 0)) * p.w.I + size_t(grp) * 128, place >= 0, lane);
-                    make_frag<SPLIT>(f, v, lane);
-                    block_product(ring.data + size_t(s) * ring.tile_bytes + grp * kGroupBytes, f, lane, acc);
-                }
-                // columns 2t and 2t + 1 of rows g and g + 8; the remainders' columns add to their token's
-                if (SPLIT) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) acc[q] = __fadd_rn(acc[q], __shfl_xor_sync(kFull, acc[q], 2));
-                }
-                const int t = lane & 3, g = lane >> 2;
+                int place = col == 0 ? __ffs(places) - 1 : -1;
+                if (used > 1) place = c0 + col < used ? nth_bit(places, c0 + col) : -1;
+                float acc[4];
+                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, place, G, t.w, lane, f, held, acc);
+                const int g = lane >> 2;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
-                    const int c = 2 * t + q;
-                    if (c < CAP && c0 + c < used) {
-                        float* to = part + (size_t(nth_bit(places, c0 + c)) * GW + wg) * 16;
-                        to[g] = acc[q];
-                        to[g + 8] = acc[2 + q];
+                    const int to = __shfl_sync(kFull, place, 8 * (lane & 3) + 4 * q);      // of column 2t + q
+                    if (to >= 0 && 2 * (lane & 3) < CAP) {
+                        part[(to * P + t.w) * 16 + g] = acc[q];
+                        part[(to * P + t.w) * 16 + g + 8] = acc[2 + q];
                     }
                 }
             }
@@ -350,24 +439,35 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
             __syncthreads();
             if (warp == 0) {
                 fence_proxy_async_smem();
-                fill(b0 + p.stages, min(n, b0 + nb + p.stages));
+                for (int i = b0 + p.stages + lane; i < min(n, b0 + nb + p.stages); i += 32)
+                    fetch(ring, i, p.w.down + size_t(list[i].from) * ring.tile_bytes, pol);
             }
+        }
+        s0 += p.batch;
+        if (s0 == p.stages) {
+            s0 = 0;
+            phase ^= 1;
         }
     }
     __syncthreads();
-    // y[t, r] = sum over places in order, each the sum of its groups' partials
+    // y[t, r] = sum over places in order, each the sum of its parts in order
+    for (int o = threadIdx.x; o < S * 16; o += kThr) {
+        if (ids[o >> 4] < 0) continue;
+        float* at = part + (o >> 4) * P * 16 + (o & 15);
+        float a = at[0];
+#pragma unroll 4
+        for (int w = 1; w < P; ++w) a = __fadd_rn(a, at[w * 16]);
+        at[0] = a;
+    }
+    __syncthreads();
     OUT* y = static_cast<OUT*>(p.y);
     for (int o = threadIdx.x; o < p.T * 16; o += kThr) {
         const int t = o >> 4, r = o & 15;
         float v = 0.f;
+#pragma unroll 4
         for (int j = 0; j < p.k; ++j) {
             const int place = t * p.k + j;
-            const int e = p.ids[place];
-            if (e < 0 || e >= p.w.E) continue;
-            float a = 0.f;
-            const int parts = GW < G ? GW : G;
-            for (int w = 0; w < parts; ++w) a = __fadd_rn(a, part[(size_t(place) * GW + w) * 16 + r]);
-            v = __fmaf_rn(p.weights[place], a, v);
+            if (ids[place] >= 0) v = __fmaf_rn(weights[place], part[place * P * 16 + r], v);
         }
         const size_t at = size_t(t) * p.w.H + blockIdx.x * 16 + r;
         if constexpr (sizeof(OUT) == 4) {
@@ -378,23 +478,16 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
     }
 }
 
-constexpr size_t kSmem = 227 * 1024;
+constexpr size_t kSmem = 227 * 1024 - 256;               // (less the kernels' static variables)
 
-const void* small_fn(bool down, bool bf16, int K) {
-    const int gpw = K <= 2048 ? 1 : (K <= 4096 ? 2 : 4);
-#define KMR_SMALL(kernel) \
-    (gpw == 1 ? (bf16 ? (const void*)kernel<uint16_t, false, 1> : (const void*)kernel<float, true, 1>) \
-     : gpw == 2 ? (bf16 ? (const void*)kernel<uint16_t, false, 2> : (const void*)kernel<float, true, 2>) \
-                : (bf16 ? (const void*)kernel<uint16_t, false, 4> : (const void*)kernel<float, true, 4>))
-    return down ? KMR_SMALL(moe_down_kernel) : KMR_SMALL(moe_gate_up_kernel);
-#undef KMR_SMALL
+const void* small_fn(bool down, bool bf16) {
+    if (down) return bf16 ? (const void*)moe_down_kernel<uint16_t, false> : (const void*)moe_down_kernel<float, true>;
+    return bf16 ? (const void*)moe_gate_up_kernel<uint16_t, false> : (const void*)moe_gate_up_kernel<float, true>;
 }
 
-// Ring of `most` tiles at the most, one batch where all of them fit and else two; `per_batch_tile` bytes for each tile of a batch
-// and `fixed` bytes beside the tiles.
-size_t plan_ring(int most, int K, size_t per_batch_tile, size_t fixed, int* stages, int* batch) {
-    const size_t tile = size_t(K / 128) * kGroupBytes;
-    auto bytes = [&](int st, int batch) { return st * tile + (st + (st & 1)) * 8 + batch * per_batch_tile + fixed; };
+// Ring of `most` tiles at the most, one batch where all of them fit and else two.
+size_t plan_ring(bool down, bool bf16, int K, int rows, int most, int* stages, int* batch) {
+    auto bytes = [&](int st, int b) { return layout_of(down, !bf16, K, rows, st, b, most).total; };
     *stages = *batch = most;
     if (bytes(most, most) <= kSmem) return bytes(most, most);
     int st = most + (most & 1);
@@ -403,31 +496,39 @@ size_t plan_ring(int most, int K, size_t per_batch_tile, size_t fixed, int* stag
     *batch = st / 2;
     return bytes(st, st / 2);
 }
+int distinct_of(const MoeView& w, int S) { return S < w.E ? S : w.E; }
+int gate_tiles(const MoeView& w, int S, int ctas) {      // the longest sequence of a CTA
+    const int all = distinct_of(w, S) * (w.I / 8);
+    return all <= ctas ? 1 : (all + ctas - 1) / ctas;
+}
 
 }  // namespace
 
+bool moe_small_fits(const MoeView& w, bool bf16, int T, int k) {
+    const int S = T * k;
+    int st, b;
+    return S <= kMoeSmallPlaces && plan_ring(false, bf16, w.H, T, gate_tiles(w, S, kMoeSmallCtas), &st, &b) <= kSmem &&
+           plan_ring(true, bf16, w.I, S, distinct_of(w, S), &st, &b) <= kSmem;
+}
+
 cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaStream_t st) {
-    const int S = p.T * p.k, distinct = S < p.w.E ? S : p.w.E;
+    const int S = p.T * p.k, all = distinct_of(p.w, S) * (p.w.I / 8);
+    if (sms < kMoeSmallCtas) return cudaErrorInvalidConfiguration;
     MoeSmallParams q = p;
-    // gate_up: at most `distinct` experts' tiles over the CTAs
-    const long long tiles = (long long)distinct * (p.w.I / 8);
-    const int grid = int(tiles < sms ? tiles : sms);
-    const int G = p.w.H / 128;
-    size_t smem = plan_ring(int((tiles + grid - 1) / grid), p.w.H, size_t(group_warps(G)) * 128 * 4, 0, &q.stages, &q.batch);
-    cudaError_t e = launch_dependent(small_fn(false, bf16, p.w.H), dim3(grid), kThr, smem, 1, &q, st);
+    q.list = gate_tiles(p.w, S, sms);
+    size_t smem = plan_ring(false, bf16, p.w.H, p.T, q.list, &q.stages, &q.batch);
+    cudaError_t e = launch_dependent(small_fn(false, bf16), dim3(all < sms ? all : sms), kThr, smem, 1, &q, st);
     if (e != cudaSuccess) return e;
-    smem = plan_ring(distinct, p.w.I, 0, size_t(S) * group_warps(p.w.I / 128) * 16 * 4, &q.stages, &q.batch);
-    return launch_dependent(small_fn(true, bf16, p.w.I), dim3(p.w.H / 16), kThr, smem, 1, &q, st);
+    q.list = distinct_of(p.w, S);
+    smem = plan_ring(true, bf16, p.w.I, S, q.list, &q.stages, &q.batch);
+    return launch_dependent(small_fn(true, bf16), dim3(p.w.H / 16), kThr, smem, 1, &q, st);
 }
 
 cudaError_t moe_small_set_attributes() {
-    for (int down = 0; down < 2; ++down)
-        for (int b = 0; b < 2; ++b)
-            for (int K = 2048; K <= kMoeMaxDim; K *= 2) {
-                const cudaError_t e = cudaFuncSetAttribute(small_fn(down != 0, b != 0, K),
-                                                           cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
-                if (e != cudaSuccess) return e;
-            }
+    for (int f = 0; f < 4; ++f) {
+        const cudaError_t e = cudaFuncSetAttribute(small_fn((f & 1) != 0, (f & 2) != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+        if (e != cudaSuccess) return e;
+    }
     return cudaSuccess;
 }
 
