@@ -26,7 +26,7 @@ namespace kmr {
 
 namespace {
 
-constexpr int kThr = 512, kWarps = kThr / 32;
+constexpr int kThr = 1024, kWarps = kThr / 32, kParts = 16;
 constexpr uint32_t kFull = 0xffffffffu;
 
 // ------------------------------------------------------------------ the call's plan, in a warp's registers
@@ -75,14 +75,18 @@ struct __align__(16) Tile {
 // ------------------------------------------------------------------ operands
 // The rows wait in shared memory as B fragments: per (row, group of 128) the four quarters t of the lanes, each the 16 registers of
 // its 8 steps (inputs 8 i + 2 t and + 1 in register i), in 16-byte pieces that two quarters exchange so that a load meets no
-// bank twice; SPLIT: the remainders behind them.  Beside them, for each term, its sum and 1 / sigma.
+// bank twice; SPLIT: the remainders behind them.  An item of zeros stands last.  Beside them, for each term, its sum and 1 / sigma.
 template <bool SPLIT>
 constexpr int kItemBytes = SPLIT ? 512 : 256;
 template <typename IN, bool SPLIT>
 __device__ __forceinline__ void stage_rows(uint8_t* to, float4* fold, const IN* x, int items) {
-    constexpr int kAtOnce = 4;
+    constexpr int kAtOnce = 2;
     const int lane = threadIdx.x & 31, i = lane >> 1;
     const int at = (lane & 1) * 128 + ((((i >> 2) ^ (lane & 1)) << 2) + (i & 3)) * 4;     // quarter 2 (lane & 1), register i
+    if (threadIdx.x >= kThr - 32) {
+        reinterpret_cast<uint4*>(to + size_t(items) * kItemBytes<SPLIT>)[lane & (kItemBytes<SPLIT> / 16 - 1)] = make_uint4(0u, 0u, 0u, 0u);
+        fold[items] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     for (int i0 = threadIdx.x >> 5; i0 < items; i0 += kWarps * kAtOnce) {
         float4 v[kAtOnce];
 #pragma unroll
@@ -131,32 +135,24 @@ struct Frag {
     uint32_t b[16];
     float X0, is0, X1, is1;  // of columns 2t and 2t + 1: sum of the staged values, 1 / sigma
 };
-// Column lane / 4 takes staged item `item` (SPLIT: columns 4..7 its remainders), or zeros if that is negative.
+// Column lane / 4 takes staged item `item` (SPLIT: columns 4..7 its remainders).
 template <bool SPLIT>
 __device__ __forceinline__ void load_frag(Frag& f, const uint8_t* staged, const float4* fold, int item, int lane) {
-    const int t = lane & 3;
-    const bool rest = SPLIT && lane >= 16;
-    float X = 0.f, isg = 1.f;
+    const int t = lane & 3, rest = SPLIT ? lane >> 4 : 0;
+    const uint8_t* at = staged + size_t(item) * kItemBytes<SPLIT> + rest * 256 + t * 64;
 #pragma unroll
-    for (int c = 0; c < 16; ++c) f.b[c] = 0u;
-    if (item >= 0) {
-        const uint8_t* at = staged + size_t(item) * kItemBytes<SPLIT> + (rest ? 256 : 0) + t * 64;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            const uint4 v = *reinterpret_cast<const uint4*>(at + ((c ^ (t >> 1)) << 4));
-            f.b[4 * c] = v.x;
-            f.b[4 * c + 1] = v.y;
-            f.b[4 * c + 2] = v.z;
-            f.b[4 * c + 3] = v.w;
-        }
-        const float2 k = reinterpret_cast<const float2*>(fold + item)[rest ? 1 : 0];
-        X = k.x;
-        isg = k.y;
+    for (int c = 0; c < 4; ++c) {
+        const uint4 v = *reinterpret_cast<const uint4*>(at + ((c ^ (t >> 1)) << 4));
+        f.b[4 * c] = v.x;
+        f.b[4 * c + 1] = v.y;
+        f.b[4 * c + 2] = v.z;
+        f.b[4 * c + 3] = v.w;
     }
-    f.X0 = __shfl_sync(kFull, X, 8 * t);
-    f.X1 = __shfl_sync(kFull, X, 8 * t + 4);
-    f.is0 = __shfl_sync(kFull, isg, 8 * t);
-    f.is1 = __shfl_sync(kFull, isg, 8 * t + 4);
+    const float2 k = reinterpret_cast<const float2*>(fold + item)[rest];
+    f.X0 = __shfl_sync(kFull, k.x, 8 * t);
+    f.X1 = __shfl_sync(kFull, k.x, 8 * t + 4);
+    f.is0 = __shfl_sync(kFull, k.y, 8 * t);
+    f.is1 = __shfl_sync(kFull, k.y, 8 * t + 4);
 }
 
 // acc (rows g and g + 8, columns 2t and 2t + 1) += one (16-row tile, 128-input group) block times the fragments.
@@ -190,20 +186,17 @@ __device__ __forceinline__ void block_product(const uint8_t* gb, const Frag& f, 
     acc[3] = fold(sz1, __fmul_rn(__fadd_rn(d[0][3], d[1][3]), 0x1p20f), f.X1, f.is1, acc[3]);
 }
 
-// The columns' sums of one warp's groups of a tile: acc (rows g and g + 8, columns 2t and 2t + 1).  `row` is the staged row of column
-// lane / 4 (of 8, SPLIT: of 4 and again), or negative; SPLIT: the remainders' columns are added to their rows'.  `f` and `held`
-// keep the fragments from one tile to the next.
+// The columns' sums of one warp's groups w, w + 16, ... of a tile: acc (rows g and g + 8, columns 2t and 2t + 1).  `row` is the
+// staged row of column lane / 4 (of 8, SPLIT: of 4 and again), `rows` (zeros) for none; SPLIT: the remainders' columns are
+// added to their rows'.
 template <bool SPLIT>
-__device__ __forceinline__ void tile_product(const uint8_t* tile, const uint8_t* staged, const float4* fold, int row, int G, int w,
-                                             int lane, Frag& f, int& held, float (&acc)[4]) {
+__device__ __forceinline__ void tile_product(const uint8_t* tile, const uint8_t* staged, const float4* fold, int row, int rows, int G,
+                                             int w, int lane, float (&acc)[4]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) acc[q] = 0.f;
-    for (int grp = w; grp < G; grp += kWarps) {
-        const int item = row < 0 ? -1 : row * G + grp;
-        if (__any_sync(kFull, item != held)) {
-            load_frag<SPLIT>(f, staged, fold, item, lane);
-            held = item;
-        }
+    for (int grp = w; grp < G; grp += kParts) {
+        Frag f;
+        load_frag<SPLIT>(f, staged, fold, row * G + (row < rows ? grp : 0), lane);
         block_product(tile + grp * kGroupBytes, f, lane, acc);
     }
     if (SPLIT) {
@@ -211,7 +204,7 @@ __device__ __forceinline__ void tile_product(const uint8_t* tile, const uint8_t*
         for (int q = 0; q < 4; ++q) acc[q] = __fadd_rn(acc[q], __shfl_xor_sync(kFull, acc[q], 2));
     }
 }
-// (tile i, part w) of a batch in the order of the warps, 16 at a time, without a division for each.
+// (tile i, part w) of a batch in the order of the warps, one for each at a time, without a division for each.
 struct Turn {
     int i, w;
 };
@@ -239,7 +232,7 @@ __device__ __forceinline__ void fetch(const Ring& r, int i, const uint8_t* from,
     bulk_g2s_stream(r.data + size_t(s) * r.tile_bytes, from, uint32_t(r.tile_bytes), &r.full[s], pol);
 }
 // Where everything lies in shared memory: ring, barriers, tile list, fold constants, staged rows, partial sums.
-__host__ __device__ constexpr int parts_of(int G) { return G < kWarps ? G : kWarps; }
+__host__ __device__ constexpr int parts_of(int G) { return G < kParts ? G : kParts; }
 struct Layout {
     size_t full, list, fold, staged, part, total;
 };
@@ -249,8 +242,8 @@ __host__ __device__ inline Layout layout_of(bool down, bool split, int K, int ro
     l.full = size_t(stages) * G * kGroupBytes;
     l.list = l.full + size_t(stages + (stages & 1)) * 8;
     l.fold = l.list + size_t(tiles) * sizeof(Tile);
-    l.staged = l.fold + size_t(rows) * G * 16;
-    l.part = l.staged + size_t(rows) * G * (split ? 512 : 256);
+    l.staged = l.fold + (size_t(rows) * G + 1) * 16;    // (one item more, of zeros)
+    l.part = l.staged + (size_t(rows) * G + 1) * (split ? 512 : 256);
     // gate_up: [batch][part][16 rows][columns]; down: [place][part][16 rows]
     l.total = l.part + size_t(down ? rows : batch * (split ? 4 : 8)) * parts_of(G) * 64;
     return l;
@@ -261,11 +254,10 @@ __device__ __forceinline__ float silu_mul(float x, float up) {
 }
 
 // ------------------------------------------------------------------ gate_up
-// (Two CTAs to an SM: the down kernel's start beside gate_up's, and their weights are on the way while it works.)
 template <typename IN, bool SPLIT>
-__global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallParams p) {
+__global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int most;
+    __shared__ int most, n_tiles;
     constexpr int CAP = SPLIT ? 4 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int G = p.w.H >> 7, P = parts_of(G);
@@ -283,35 +275,35 @@ __global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallPara
     __syncwarp();
     pdl_wait();
     pdl_launch_dependents();                            // (after the wait: see the down kernel's prologue)
-    const Plan pl = make_plan(p.ids, p.T * p.k, p.w.E, p.err, blockIdx.x == 0 && warp == 0);
-    const long long W = (long long)__popc(pl.leaders) * tiles;
-    const long long first = W * blockIdx.x / gridDim.x;
-    const int n = int(W * (blockIdx.x + 1) / gridDim.x - first);
     const uint64_t pol = policy_evict_first();
     if (warp == 0) {
-        const int u0 = int(first / tiles), r0 = int(first % tiles);
-        for (int i0 = 0; i0 < n; i0 += 32) {            // tile i: row tile (r0 + i) % tiles of a distinct expert
-            const int i = min(i0 + lane, n - 1), at = nth_bit(pl.leaders, u0 + (r0 + i) / tiles);
+        const Plan pl = make_plan(p.ids, p.T * p.k, p.w.E, p.err, blockIdx.x == 0);
+        const uint32_t W = uint32_t(__popc(pl.leaders) * tiles), first = uint32_t((unsigned long long)W * blockIdx.x / gridDim.x);
+        const int mine = int(uint32_t((unsigned long long)W * (blockIdx.x + 1) / gridDim.x) - first);
+        const int u0 = int(first / uint32_t(tiles)), r0 = int(first - uint32_t(u0 * tiles));
+        for (int i0 = 0; i0 < mine; i0 += 32) {         // tile i: row tile (r0 + i) % tiles of a distinct expert
+            const int i = min(i0 + lane, mine - 1), u = (r0 + i) / tiles, at = nth_bit(pl.leaders, u0 + u);
             Tile t;
-            t.row = (r0 + i) % tiles;
+            t.row = r0 + i - u * tiles;
             t.from = __shfl_sync(kFull, pl.id, at) * tiles + t.row;
             t.places = __shfl_sync(kFull, pl.same, at);
             t.unused = 0;
-            if (i0 + lane < n) {
+            if (i0 + lane < mine) {
                 list[i] = t;
                 if (i < p.stages) fetch(ring, i, p.w.gate_up + size_t(t.from) * ring.tile_bytes, pol);
             }
         }
         const int m = most_places(pl);
-        if (lane == 0) most = m;
+        if (lane == 0) {
+            most = m;
+            n_tiles = mine;
+        }
     }
     stage_rows<IN, SPLIT>(staged, fold, static_cast<const IN*>(p.x), p.T * G);
     const int token = lane / p.k;                       // of place `lane`
     __syncthreads();
-    const int columns = min(most, CAP), di = kWarps / P, dw = kWarps % P;
+    const int n = n_tiles, columns = min(most, CAP), di = kWarps / P, dw = kWarps % P;
     const Turn t0 = first_turn(warp, P);
-    Frag f;
-    int held = -2;
     for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
         for (int c0 = 0; c0 < most; c0 += CAP) {
@@ -323,7 +315,7 @@ __global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallPara
                 if (p.T > 1) at = __shfl_sync(kFull, token, nth_bit(places, c0 + min(col, cols - 1)));
                 if (!__all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err))) continue;
                 float acc[4];
-                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, col < cols ? at : -1, G, t.w, lane, f, held, acc);
+                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, col < cols ? at : p.T, p.T, G, t.w, lane, acc);
                 const int g = lane >> 2, c = 2 * (lane & 3);
                 if (c < CAP) {
                     float* to = part + ((t.i * P + t.w) * 16 + g) * CAP + c;
@@ -332,22 +324,23 @@ __global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallPara
                 }
             }
             __syncthreads();
-            // two outputs of a (tile, column) a warp at a time, eight lanes for each row of its gate and its up: a lane sums two of
-            // the (at most 16) partials, then the eight lanes' sums meet
-            for (int c = 0; c < columns; ++c)
-            for (int o = warp; o < nb * 4; o += kWarps) {
-                const int i = o >> 2;
-                const Tile t = list[b0 + i];
-                if (c0 + c >= __popc(t.places)) continue;
-                const int r = (o & 3) * 2 + (lane >> 4), w = lane & 7;
-                const float* at = part + (i * P * 16 + r + ((lane >> 3) & 1) * 8) * CAP + c;
-                float v = w < P ? at[w * 16 * CAP] : 0.f;
-                if (w + 8 < P) v = __fadd_rn(v, at[(w + 8) * 16 * CAP]);
-                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 4));
-                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 2));
-                v = __fadd_rn(v, __shfl_xor_sync(kFull, v, 1));
-                const float up = __shfl_sync(kFull, v, (lane + 8) & 31);
-                if ((lane & 15) == 0) p.act[size_t(nth_bit(t.places, c0 + c)) * p.w.I + t.row * 8 + r] = silu_mul(v, up);
+            // four outputs of a (tile, column) a warp at a time, four lanes for each row of its gate and its up: a lane sums four of
+            // the (at most 16) partials, then the four lanes' sums meet
+            for (int c = 0; c < columns; ++c) {
+                for (int o = warp; o < nb * 2; o += kWarps) {
+                    const Tile t = list[b0 + (o >> 1)];
+                    if (c0 + c >= __popc(t.places)) continue;
+                    const int r = (o & 1) * 4 + ((lane >> 2) & 3), w = lane & 3;
+                    const float* at = part + ((o >> 1) * P * 16 + r + (lane >> 4) * 8) * CAP + c;
+                    float v[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) v[q] = w + 4 * q < P ? at[(w + 4 * q) * 16 * CAP] : 0.f;
+                    float a = __fadd_rn(__fadd_rn(v[0], v[1]), __fadd_rn(v[2], v[3]));
+                    a = __fadd_rn(a, __shfl_xor_sync(kFull, a, 1));
+                    a = __fadd_rn(a, __shfl_xor_sync(kFull, a, 2));
+                    const float up = __shfl_sync(kFull, a, (lane + 16) & 31);
+                    if (lane < 16 && w == 0) p.act[size_t(nth_bit(t.places, c0 + c)) * p.w.I + t.row * 8 + r] = silu_mul(a, up);
+                }
             }
             __syncthreads();
         }
@@ -366,9 +359,9 @@ __global__ void __launch_bounds__(kThr, 2) moe_gate_up_kernel(const MoeSmallPara
 
 // ------------------------------------------------------------------ down
 template <typename OUT, bool SPLIT>
-__global__ void __launch_bounds__(kThr, 2) moe_down_kernel(const MoeSmallParams p) {
+__global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int ids[32];
+    __shared__ int ids[32], experts;
     __shared__ float weights[32];
     constexpr int CAP = SPLIT ? 4 : 8;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -387,31 +380,29 @@ __global__ void __launch_bounds__(kThr, 2) moe_down_kernel(const MoeSmallParams 
     __syncwarp();
     // The ids and weights were written before gate_up began (it waited for them before it let this kernel start), and the
     // experts are constant: they are read before the wait for gate_up's results.
-    const Plan pl = make_plan(p.ids, S, p.w.E, p.err, false);
-    const int n = __popc(pl.leaders);
     const uint64_t pol = policy_evict_first();
     if (warp == 0) {
-        const int at = nth_bit(pl.leaders, min(lane, max(n, 1) - 1)) & 31;
+        const Plan pl = make_plan(p.ids, S, p.w.E, p.err, false);
+        const int distinct = __popc(pl.leaders), at = nth_bit(pl.leaders, lane) & 31;
         Tile t;
         t.row = blockIdx.x;
         t.from = __shfl_sync(kFull, pl.id, at) * tiles + t.row;
         t.places = __shfl_sync(kFull, pl.same, at);
         t.unused = 0;
-        if (lane < n) {
+        if (lane < distinct) {
             list[lane] = t;
             if (lane < p.stages) fetch(ring, lane, p.w.down + size_t(t.from) * ring.tile_bytes, pol);
         }
         ids[lane] = pl.id;
         weights[lane] = lane < S ? p.weights[lane] : 0.f;
+        if (lane == 0) experts = distinct;
     }
     pdl_wait();
     pdl_launch_dependents();
     stage_rows<float, SPLIT>(staged, fold, p.act, S * G);
     __syncthreads();
-    const int di = kWarps / P, dw = kWarps % P;
+    const int n = experts, di = kWarps / P, dw = kWarps % P;
     const Turn t0 = first_turn(warp, P);
-    Frag f;
-    int held = -2;
     for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
         for (Turn t = t0; t.i < nb; next_turn(t, P, di, dw)) {
@@ -423,7 +414,7 @@ __global__ void __launch_bounds__(kThr, 2) moe_down_kernel(const MoeSmallParams 
                 int place = col == 0 ? __ffs(places) - 1 : -1;
                 if (used > 1) place = c0 + col < used ? nth_bit(places, c0 + col) : -1;
                 float acc[4];
-                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, place, G, t.w, lane, f, held, acc);
+                tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, place < 0 ? S : place, S, G, t.w, lane, acc);
                 const int g = lane >> 2;
 #pragma unroll
                 for (int q = 0; q < 2; ++q) {
@@ -478,7 +469,7 @@ __global__ void __launch_bounds__(kThr, 2) moe_down_kernel(const MoeSmallParams 
     }
 }
 
-constexpr size_t kSmem = 227 * 1024 - 256;               // (less the kernels' static variables)
+constexpr size_t kSmem = 227 * 1024 - 512;               // (less the kernels' static variables)
 
 const void* small_fn(bool down, bool bf16) {
     if (down) return bf16 ? (const void*)moe_down_kernel<uint16_t, false> : (const void*)moe_down_kernel<float, true>;
