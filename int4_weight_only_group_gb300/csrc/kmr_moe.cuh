@@ -11,6 +11,8 @@ constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxDim = 8192;             // hidden and intermediate sizes, multiples of 128
 constexpr int kMoeMaxTokens = 1 << 20;
 constexpr int kMoeSmallPlaces = 32;          // places (token, j) of the small form: a warp's lanes
+constexpr int kMoeSmallTokens = 16;          // its most tokens
+constexpr long long kMoeSmallWeights = 200000000;   // and weights of the places' experts, each counted by itself
 constexpr int kMoeSmallCtas = 128;           // CTAs at once that its sizes are made for (a GB300 has 152 SMs)
 
 // ------------------------------------------------------------------ router
@@ -40,6 +42,7 @@ struct MoeSmallParams {
     void* y;                                 // [T][H]
     int resid;                               // add to y
     int stages, batch, list;                 // ring of `stages` tiles, `batch` of them at a time, `list` in all (set by the launch)
+    uint32_t by_tiles, by_grid;              // 2^32 / gate_up tiles of an expert, 2^32 / CTAs, rounded up (set by the launch)
     int* err;
 };
 bool moe_small_fits(const MoeView& w, bool bf16, int T, int k);

@@ -278,11 +278,12 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
     const uint64_t pol = policy_evict_first();
     if (warp == 0) {
         const Plan pl = make_plan(p.ids, p.T * p.k, p.w.E, p.err, blockIdx.x == 0);
-        const uint32_t W = uint32_t(__popc(pl.leaders) * tiles), first = uint32_t((unsigned long long)W * blockIdx.x / gridDim.x);
-        const int mine = int(uint32_t((unsigned long long)W * (blockIdx.x + 1) / gridDim.x) - first);
-        const int u0 = int(first / uint32_t(tiles)), r0 = int(first - uint32_t(u0 * tiles));
+        // (products with the rounded-up 2^32 / d for divisions by d: exact, n * d stays below 2^32)
+        const int W = __popc(pl.leaders) * tiles, per = __umulhi(W, p.by_grid), more = W - per * int(gridDim.x);
+        const int first = int(blockIdx.x) * per + min(int(blockIdx.x), more), mine = per + (int(blockIdx.x) < more ? 1 : 0);
+        const int u0 = __umulhi(first, p.by_tiles), r0 = first - u0 * tiles;
         for (int i0 = 0; i0 < mine; i0 += 32) {         // tile i: row tile (r0 + i) % tiles of a distinct expert
-            const int i = min(i0 + lane, mine - 1), u = (r0 + i) / tiles, at = nth_bit(pl.leaders, u0 + u);
+            const int i = min(i0 + lane, mine - 1), u = __umulhi(r0 + i, p.by_tiles), at = nth_bit(pl.leaders, u0 + u);
             Tile t;
             t.row = r0 + i - u * tiles;
             t.from = __shfl_sync(kFull, pl.id, at) * tiles + t.row;
@@ -399,6 +400,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
     }
     pdl_wait();
     pdl_launch_dependents();
+    OUT* y = static_cast<OUT*>(p.y);
+    const size_t out = size_t(threadIdx.x >> 4) * p.w.H + blockIdx.x * 16 + (threadIdx.x & 15);     // (T * 16 <= kThr)
+    const bool mine = int(threadIdx.x) < p.T * 16;
+    float before = 0.f;
+    if (mine && p.resid) {
+        if constexpr (sizeof(OUT) == 4) before = y[out];
+        else before = bf16_to_f32(y[out]);
+    }
     stage_rows<float, SPLIT>(staged, fold, p.act, S * G);
     __syncthreads();
     const int n = experts, di = kWarps / P, dw = kWarps % P;
@@ -451,22 +460,16 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
         at[0] = a;
     }
     __syncthreads();
-    OUT* y = static_cast<OUT*>(p.y);
-    for (int o = threadIdx.x; o < p.T * 16; o += kThr) {
-        const int t = o >> 4, r = o & 15;
-        float v = 0.f;
+    if (!mine) return;
+    float v = 0.f;
 #pragma unroll 4
-        for (int j = 0; j < p.k; ++j) {
-            const int place = t * p.k + j;
-            if (ids[place] >= 0) v = __fmaf_rn(weights[place], part[place * P * 16 + r], v);
-        }
-        const size_t at = size_t(t) * p.w.H + blockIdx.x * 16 + r;
-        if constexpr (sizeof(OUT) == 4) {
-            y[at] = p.resid ? __fadd_rn(y[at], v) : v;
-        } else {
-            y[at] = f32_to_bf16_rn(p.resid ? __fadd_rn(bf16_to_f32(y[at]), v) : v);
-        }
+    for (int j = 0; j < p.k; ++j) {
+        const int place = int(threadIdx.x >> 4) * p.k + j;
+        if (ids[place] >= 0) v = __fmaf_rn(weights[place], part[place * P * 16 + (threadIdx.x & 15)], v);
     }
+    if (p.resid) v = __fadd_rn(before, v);
+    if constexpr (sizeof(OUT) == 4) y[out] = v;
+    else y[out] = f32_to_bf16_rn(v);
 }
 
 constexpr size_t kSmem = 227 * 1024 - 512;               // (less the kernels' static variables)
@@ -495,10 +498,13 @@ int gate_tiles(const MoeView& w, int S, int ctas) {      // the longest sequence
 
 }  // namespace
 
+// (a larger call, of weights or of tokens, is quicker in the grouped form, whose kernels cost 22 us in any case but read the
+// weights faster: 16 experts of 4096 x 2048, two a token, fp32: four tokens 48 us against 55, five 65 against 55; 64 experts of
+// 2048 x 768, one a token, bf16: 16 tokens 27 against 31, 32 tokens 49 against 35)
 bool moe_small_fits(const MoeView& w, bool bf16, int T, int k) {
     const int S = T * k;
     int st, b;
-    return S <= kMoeSmallPlaces && plan_ring(false, bf16, w.H, T, gate_tiles(w, S, kMoeSmallCtas), &st, &b) <= kSmem &&
+    return S <= kMoeSmallPlaces && T <= kMoeSmallTokens && (long long)S * w.H * w.I * 3 <= kMoeSmallWeights && plan_ring(false, bf16, w.H, T, gate_tiles(w, S, kMoeSmallCtas), &st, &b) <= kSmem &&
            plan_ring(true, bf16, w.I, S, distinct_of(w, S), &st, &b) <= kSmem;
 }
 
@@ -506,9 +512,12 @@ cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaSt
     const int S = p.T * p.k, all = distinct_of(p.w, S) * (p.w.I / 8);
     if (sms < kMoeSmallCtas) return cudaErrorInvalidConfiguration;
     MoeSmallParams q = p;
+    const int grid = all < sms ? all : sms;
     q.list = gate_tiles(p.w, S, sms);
+    q.by_tiles = uint32_t((0x100000000ull + p.w.I / 8 - 1) / (p.w.I / 8));
+    q.by_grid = uint32_t((0x100000000ull + grid - 1) / grid);
     size_t smem = plan_ring(false, bf16, p.w.H, p.T, q.list, &q.stages, &q.batch);
-    cudaError_t e = launch_dependent(small_fn(false, bf16), dim3(all < sms ? all : sms), kThr, smem, 1, &q, st);
+    cudaError_t e = launch_dependent(small_fn(false, bf16), dim3(grid), kThr, smem, 1, &q, st);
     if (e != cudaSuccess) return e;
     q.list = distinct_of(p.w, S);
     smem = plan_ring(true, bf16, p.w.I, S, q.list, &q.stages, &q.batch);
