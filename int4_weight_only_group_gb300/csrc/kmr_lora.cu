@@ -47,157 +47,191 @@ __device__ __forceinline__ void term_of(float (&fa)[4], float (&fb)[4], uint32_t
     A[3] = take_term(fb[2], fb[3]);
 }
 
-// Four values of a row: fp32 or bf16.
+// Eight consecutive values of a row: fp32 or bf16.
 template <bool BF16>
-struct Four {
-    float4 v;
-    __device__ __forceinline__ void load(const void* p, size_t at, bool real) {
-        v = real ? *reinterpret_cast<const float4*>(static_cast<const float*>(p) + at) : make_float4(0.f, 0.f, 0.f, 0.f);
+struct Eight {
+    float4 v[2];
+    __device__ __forceinline__ void values(float (&f)[8]) const {
+        f[0] = v[0].x, f[1] = v[0].y, f[2] = v[0].z, f[3] = v[0].w;
+        f[4] = v[1].x, f[5] = v[1].y, f[6] = v[1].z, f[7] = v[1].w;
     }
-    __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<float4*>(static_cast<float*>(p) + at) = v; }
-    __device__ __forceinline__ void values(float (&f)[4]) const {
-        f[0] = v.x;
-        f[1] = v.y;
-        f[2] = v.z;
-        f[3] = v.w;
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        v[0] = make_float4(f[0], f[1], f[2], f[3]);
+        v[1] = make_float4(f[4], f[5], f[6], f[7]);
+    }
+    __device__ __forceinline__ void store(void* p, size_t at) const {
+        float4* to = reinterpret_cast<float4*>(static_cast<float*>(p) + at);
+        to[0] = v[0];
+        to[1] = v[1];
     }
 };
 template <>
-struct Four<true> {
-    uint2 v;
-    __device__ __forceinline__ void load(const void* p, size_t at, bool real) {
-        v = real ? *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + at) : make_uint2(0u, 0u);
+struct Eight<true> {
+    uint4 v;
+    __device__ __forceinline__ void values(float (&f)[8]) const {
+        f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
+        f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
     }
-    __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p) + at) = v; }
-    __device__ __forceinline__ void values(float (&f)[4]) const {
-        f[0] = bf16_lo(v.x);
-        f[1] = bf16_hi(v.x);
-        f[2] = bf16_lo(v.y);
-        f[3] = bf16_hi(v.y);
-    }
+    __device__ __forceinline__ void set(const float (&f)[8]) { v = make_uint4(cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])); }
+    __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = v; }
 };
+// 16 bytes to shared memory, or zeros.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool real) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(real ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void commit_copies() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
-// Rows of a tile: MT m-tiles of 16 (R = 16 MT, or R = 1 with MT = 1: `rows` says how many are real).  RT: 8-rank tiles.
-template <bool BF16, int RT, int MT>
-__global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const LoraParams p, int R) {
-    constexpr int RP = RT * 8;             // ranks, padded
-    constexpr int KS = (RT + 1) / 2;       // steps of 16 ranks
-    constexpr int KW = kWarps / MT;        // warps that share an m-tile
-    constexpr int U = RT <= 2 ? (BF16 ? 8 : 4) : (RT == 4 ? 4 : (RT == 8 ? 2 : 1));       // steps of 16 inputs in flight
-    constexpr int UN = RT <= 4 ? 4 : (RT == 8 ? 2 : 1);                      // blocks of 16 outputs in flight
-    __shared__ __align__(16) int ids[16 * MT < 32 ? 32 : 16 * MT];
-    __shared__ uint32_t leads[2];          // rows that are the first with their adapter
-    extern __shared__ __align__(16) float sm[];
-    float* vpart = sm;                     // [KW][16 MT][RP]
-    float* vloc = vpart + KW * 16 * MT * RP;   // [16 MT][RP]: this CTA's part of v, read by the cluster
-    float* vsum = vloc + 16 * MT * RP;     // [16 MT][RP]
+// A warp's ring: `stages` units, each 16 rows of x (or base) and the same columns of A (or rows of B).  Wide rows of A (many ranks)
+// take shorter units, so that two CTAs fit to an SM as far as they can.
+template <bool BF16, int RT>
+struct Cfg {
+    static constexpr int RP = RT * 8;                                   // ranks, padded
+    static constexpr int KS = (RT + 1) / 2;                             // steps of 16 ranks
+    static constexpr int SZ = BF16 ? 2 : 4;
+    static constexpr int ROW = BF16 && RT >= 4 ? 64 : 128;             // bytes of a row of x or base in a unit
+    static constexpr int COLS = ROW / SZ, SUB = COLS / 32;              // its columns: 32 or 64, in runs of 32
+    static constexpr int AROW = COLS * 2;                               // bytes of a row of A in a unit
+    static constexpr int XBYTES = 16 * ROW, STAGE = XBYTES + RP * AROW;
+    static constexpr int STAGES = RT == 1 ? 4 : (RT <= 4 ? 3 : (RT == 8 && !BF16 ? 4 : 2));
+    static constexpr int CTAS = RT == 16 || (RT == 8 && !BF16) ? 1 : 2;     // to an SM
+    static constexpr int TERMS = BF16 ? 2 : 3;                          // of v (bf16 results: two terms hold 16 bits)
+    static constexpr size_t SMEM = size_t(kWarps) * STAGES * STAGE + size_t(kWarps / 2 + 2) * 16 * RP * 4;
+};
+// Where the 16-byte piece c of a row lies, so that eight lanes that read (two rows, four pieces) meet no bank twice: bf16 lanes
+// read pieces t, t + 4 of rows of 128 bytes, fp32 lanes 2 t and 2 t + 1.
+template <bool BF16, int ROW>
+__device__ __forceinline__ int swizzled(int c, int row) {
+    if (!BF16) return c ^ (row & 1);
+    return ROW == 128 ? c ^ ((row & 1) << 2) : c;
+}
+
+// R rows to a tile: 16, or 1.  RT: 8-rank tiles.
+template <bool BF16, int RT>
+__global__ void __launch_bounds__(kThr, Cfg<BF16, RT>::CTAS) lora_kernel(const LoraParams p, int R) {
+    using F = Cfg<BF16, RT>;
+    constexpr int RP = F::RP, KS = F::KS, SZ = F::SZ, ROW = F::ROW, COLS = F::COLS, SUB = F::SUB, AROW = F::AROW, S = F::STAGES;
+    constexpr int XP = ROW / 16, XR = 32 / XP, AP = AROW / 16, AR = 32 / AP;     // pieces of a row, rows of an instruction
+    __shared__ __align__(16) int ids[32];
+    __shared__ uint32_t leads;             // rows that are the first with their adapter
+    extern __shared__ __align__(128) uint8_t sm[];
+    float* vpart = reinterpret_cast<float*>(sm + size_t(kWarps) * S * F::STAGE);     // [kWarps / 2][16][RP]
+    float* vloc = vpart + kWarps / 2 * 16 * RP;      // [16][RP]: this CTA's part of v, read by the cluster
+    float* vsum = vloc + 16 * RP;          // [16][RP]
     cg::cluster_group cluster = cg::this_cluster();
     const int rank = int(cluster.block_rank()), C = int(cluster.num_blocks());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int mt = warp / KW, kw = warp % KW;
     const int row0 = int(blockIdx.x / C) * R;
     const int rows = min(R, p.T - row0);
+    uint8_t* ring = sm + size_t(warp) * S * F::STAGE;
+    const uint32_t ring32 = smem_u32(ring);
     pdl_launch_dependents();
     pdl_wait();
-    if (threadIdx.x < 16 * MT) {
-        int a = threadIdx.x < rows ? p.ids[row0 + threadIdx.x] : -1;
+    if (warp == 0) {
+        int a = lane < rows ? p.ids[row0 + lane] : -1;
         if (a < -1 || a >= p.L) {
             if (rank == 0) set_error(p.err, KMR_ERR_INVALID_ARG);
             a = -1;
         }
-        ids[threadIdx.x] = a;
-    }
-    __syncthreads();
-    if (warp < 2) {
-        const int i = threadIdx.x;
-        const int a = i < 16 * MT ? ids[i] : -1;
+        ids[lane] = a;
         const uint32_t same = __match_any_sync(0xffffffffu, a);       // (by the whole warp, whatever a is)
-        bool lead = a >= 0 && __ffs(same) - 1 == lane;
-        if (MT > 2 && warp == 1) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int4 o = reinterpret_cast<const int4*>(ids)[j];
-                lead = lead && o.x != a && o.y != a && o.z != a && o.w != a;
-            }
-        }
-        const uint32_t m = __ballot_sync(0xffffffffu, lead);
-        if (lane == 0) leads[warp] = m;
+        const uint32_t m = __ballot_sync(0xffffffffu, a >= 0 && __ffs(same) - 1 == lane);
+        if (lane == 0) leads = m;
     }
     __syncthreads();
-    const int ra = 16 * mt + g, rb = ra + 8;              // this lane's rows
-    const int ida = ids[ra], idb = ids[rb];
-    // this rank's columns of the output: whole blocks of 16, and this warp's part of its k-steps
-    const int blocks = p.N >> 4;
-    const int n0 = blocks * rank / C, n1 = blocks * (rank + 1) / C;
-    const int k0 = (p.K / 16) * rank / C, k1 = (p.K / 16) * (rank + 1) / C;
-    const int kper = (k1 - k0 + KW - 1) / KW, kb = k0 + kw * kper, ke = min(k1, kb + kper);
+    const int ida = ids[g], idb = ids[g + 8];             // of this lane's rows
+    // this rank's units of the inputs and of the outputs, and this warp's of them
+    auto share = [&](int n, int& from, int& to) {
+        const int units = (n + COLS - 1) / COLS, u0 = units * rank / C, u1 = units * (rank + 1) / C;
+        const int per = (u1 - u0 + kWarps - 1) / kWarps;
+        from = u0 + warp * per;
+        to = min(u1, from + per);
+    };
+    int kb, ke, nb, ne;
+    share(p.K, kb, ke);
+    share(p.N, nb, ne);
 
     // rows without an adapter
-    for (int r = warp; r < rows; r += kWarps) {
-        if (ids[r] >= 0 || p.base == p.y) continue;
-        const size_t at = size_t(row0 + r) * p.ldy;
-        for (int c = n0 * 16 + lane * 4; c < n1 * 16; c += 128) {
-            Four<BF16> f;
-            f.load(p.base, at + c, p.base != nullptr);
-            f.store(p.y, at + c);
+    if (p.base != p.y) {
+        for (int r = 0; r < rows; ++r) {
+            if (ids[r] >= 0) continue;
+            const size_t at = size_t(row0 + r) * p.ldy * SZ;
+            for (int c = nb * ROW + lane * 16; c < min(ne * ROW, p.N * SZ); c += 512) {
+                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                if (p.base) v = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.base) + at + c);
+                *reinterpret_cast<uint4*>(static_cast<uint8_t*>(p.y) + at + c) = v;
+            }
         }
     }
 
     bool pending = false;                  // the others may still read this CTA's part of v
-    for (uint64_t left = leads[0] | (uint64_t(leads[1]) << 32); left; left &= left - 1) {
-        const int a = ids[__ffsll(left) - 1];
+    for (uint32_t left = leads; left; left &= left - 1) {
+        const int a = ids[__ffs(left) - 1];
         const int rank_a = p.ranks ? max(0, min(p.r, p.ranks[a])) : p.r;
         const float scale = p.scales ? p.scales[a] : 1.f;
         const uint16_t* A = p.a + size_t(a) * p.r * p.K;
         const uint16_t* B = p.b + size_t(a) * p.N * p.r;
-        const bool ua = ida == a, ub = idb == a;
-        const size_t xa = size_t(row0 + ra) * p.ldx, xb = size_t(row0 + rb) * p.ldx;
-        const size_t ya = size_t(row0 + ra) * p.ldy, yb = size_t(row0 + rb) * p.ldy;
-
-        uint2 w2[UN][KS][2];
-        Four<BF16> oa[UN], ob[UN];
-        auto load_out = [&](int nb0) {
+        uint32_t mine = 0;                 // bit i: row lane / XP + XR i is one of the adapter's
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                const int nb = nb0 + i;
-                const bool real = nb < n1;
+        for (int i = 0; i < 16 / XR; ++i) mine |= (ids[lane / XP + XR * i] == a ? 1u : 0u) << i;
+        const int xrow = lane / XP, xpiece = lane % XP, arow = lane / AP, apiece = lane % AP;
+        // unit u of x or base, `n` columns wide
+        auto copy_rows = [&](const void* from, long long ld, int n, int u, uint32_t to) {
+            const int col = u * COLS + xpiece * (16 / SZ);
+            const bool real = col < n;
+            const uint8_t* at = static_cast<const uint8_t*>(from) + (size_t(row0 + xrow) * ld + (real ? col : 0)) * SZ;
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        // column g of n-tile h: output columns 4 (g / 2) + 2 h + g % 2 of the block; ranks k .. k + 3
-                        const int k = ks * 16 + 4 * t, n = nb * 16 + 4 * (g >> 1) + 2 * h + (g & 1);
-                        w2[i][ks][h] = real && k < p.r ? *reinterpret_cast<const uint2*>(B + size_t(n) * p.r + k) : make_uint2(0u, 0u);
-                    }
-                oa[i].load(p.base, ya + nb * 16 + 4 * t, real && ua && p.base);
-                ob[i].load(p.base, yb + nb * 16 + 4 * t, real && ub && p.base);
-            }
+            for (int i = 0; i < 16 / XR; ++i)
+                if (mine >> i & 1u) copy16(to + (xrow + XR * i) * ROW + swizzled<BF16, ROW>(xpiece, xrow + XR * i) * 16, at + size_t(XR * i) * ld * SZ, real);
         };
-        if (MT == 1) {                     // few rows: B's bytes are on their way while v is formed
-            const size_t from = size_t(n0) * 16 * p.r, to = size_t(n1) * 16 * p.r;
-            for (size_t i = from + threadIdx.x * 64; i < to; i += kThr * 64) prefetch_l2(B + i);
+        auto copy_in = [&](int u, int stage) {
+            if (u < ke) {
+                const uint32_t to = ring32 + stage * F::STAGE;
+                copy_rows(p.x, p.ldx, p.K, u, to);
+                const int col = u * COLS + apiece * 8;
+                const bool real = col < p.K;               // (past the inputs both sides are zero)
+                const uint16_t* at = A + size_t(arow) * p.K + (real ? col : 0);
+#pragma unroll
+                for (int i = 0; i < RP / AR; ++i) {
+                    const int n = arow + AR * i;
+                    if (n < rank_a) copy16(to + F::XBYTES + n * AROW + (BF16 ? swizzled<BF16, AROW>(apiece, n) : apiece) * 16, at + size_t(AR * i) * p.K, real);
+                }
+            }
+            commit_copies();
+        };
+        auto copy_out = [&](int u, int stage) {
+            if (u < ne) {
+                const uint32_t to = ring32 + stage * F::STAGE;
+                if (p.base) copy_rows(p.base, p.ldy, p.N, u, to);
+                const int pieces = min(COLS, p.N - u * COLS) * p.r >> 3;
+                const uint16_t* at = B + size_t(u) * COLS * p.r;
+#pragma unroll 4
+                for (int i = lane; i < pieces; i += 32) copy16(to + F::XBYTES + i * 16, at + i * 8, true);
+            }
+            commit_copies();
+        };
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < S - 1; ++i) copy_in(kb + i, i);
+        {                                  // B's bytes are on their way while v is formed
+            const size_t from = size_t(nb) * COLS * p.r, to = size_t(min(ne * COLS, p.N)) * p.r;
+            for (size_t i = from + lane * 64; i < to; i += 32 * 64) prefetch_l2(B + i);
         }
 
-        // ---- v = A x over this warp's k-steps
+        // ---- v = A x over this warp's units
         float d[RT][4];
 #pragma unroll
         for (int j = 0; j < RT; ++j) clear4(d[j]);
-        for (int ks = kb; ks < ke; ks += U) {
-            Four<BF16> va[U], vb[U];
-            uint2 w[U][RT];
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int k = (ks + u) * 16 + 4 * t;
-                const bool real = ks + u < ke;
-                va[u].load(p.x, xa + k, real && ua);
-                vb[u].load(p.x, xb + k, real && ub);
-#pragma unroll
-                for (int j = 0; j < RT; ++j) {
-                    const int n = 8 * j + g;
-                    w[u][j] = real && n < rank_a ? *reinterpret_cast<const uint2*>(A + size_t(n) * p.K + k) : make_uint2(0u, 0u);
-                }
-            }
+        for (int u = kb, stage = 0; u < ke; ++u) {
+            wait_copies<S - 2>();
+            __syncwarp();
+            copy_in(u + S - 1, stage == 0 ? S - 1 : stage - 1);
+            const uint8_t* at = ring + stage * F::STAGE;
+            stage = stage == S - 1 ? 0 : stage + 1;
             // (the tensor cores cut a running sum off rather than round it: fp32 sums are taken over in short runs)
             float c[RT][4];
             if (!BF16) {
@@ -205,21 +239,44 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
                 for (int j = 0; j < RT; ++j) clear4(c[j]);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int sub = 0; sub < SUB; ++sub) {
+                // a lane's eight inputs 8 t .. of 32 make two steps of 16 (any order of the inputs will do)
+                const uint8_t* wat = at + F::XBYTES + g * AROW + (BF16 ? swizzled<BF16, AROW>(sub * 4 + t, g) : t) * 16;
                 if constexpr (BF16) {
-                    const uint32_t A0[4] = {(va[u].v.x), (vb[u].v.x), (va[u].v.y), (vb[u].v.y)};
+                    const uint4 xa = *reinterpret_cast<const uint4*>(at + g * ROW + swizzled<BF16, ROW>(sub * 4 + t, g) * 16);
+                    const uint4 xb = *reinterpret_cast<const uint4*>(at + (g + 8) * ROW + swizzled<BF16, ROW>(sub * 4 + t, g) * 16);
+                    const uint32_t A0[4] = {xa.x, xb.x, xa.y, xb.y}, A1[4] = {xa.z, xb.z, xa.w, xb.w};
 #pragma unroll
-                    for (int j = 0; j < RT; ++j) mma_bf16(d[j], A0, w[u][j].x, w[u][j].y);
+                    for (int j = 0; j < RT; ++j) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(wat + j * 8 * AROW);
+                        mma_bf16(d[j], A0, w.x, w.y);
+                        mma_bf16(d[j], A1, w.z, w.w);
+                    }
                 } else {
-                    float fa[4], fb[4];
-                    va[u].values(fa);
-                    vb[u].values(fb);
+                    float fa[2][4], fb[2][4];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float4 xa = *reinterpret_cast<const float4*>(at + g * ROW + swizzled<BF16, ROW>(2 * t + h, g) * 16);
+                        const float4 xb = *reinterpret_cast<const float4*>(at + (g + 8) * ROW + swizzled<BF16, ROW>(2 * t + h, g) * 16);
+                        fa[h][0] = xa.x, fa[h][1] = xa.y, fa[h][2] = xa.z, fa[h][3] = xa.w;
+                        fb[h][0] = xb.x, fb[h][1] = xb.y, fb[h][2] = xb.z, fb[h][3] = xb.w;
+                    }
+                    uint4 w[RT <= 8 ? RT : 1];
+                    if (RT <= 8) {
+#pragma unroll
+                        for (int j = 0; j < RT; ++j) w[RT <= 8 ? j : 0] = *reinterpret_cast<const uint4*>(wat + j * 8 * AROW);
+                    }
 #pragma unroll
                     for (int term = 0; term < 3; ++term) {
-                        uint32_t A0[4];
-                        term_of(fa, fb, A0);
+                        uint32_t A0[4], A1[4];
+                        term_of(fa[0], fb[0], A0);
+                        term_of(fa[1], fb[1], A1);
 #pragma unroll
-                        for (int j = 0; j < RT; ++j) mma_bf16(c[j], A0, w[u][j].x, w[u][j].y);
+                        for (int j = 0; j < RT; ++j) {
+                            const uint4 wj = RT <= 8 ? w[RT <= 8 ? j : 0] : *reinterpret_cast<const uint4*>(wat + j * 8 * AROW);
+                            mma_bf16(c[j], A0, wj.x, wj.y);
+                            mma_bf16(c[j], A1, wj.z, wj.w);
+                        }
                     }
                 }
             }
@@ -230,108 +287,126 @@ __global__ void __launch_bounds__(kThr, RT >= 16 ? 1 : 2) lora_kernel(const Lora
                     for (int q = 0; q < 4; ++q) d[j][q] = __fadd_rn(d[j][q], c[j][q]);
             }
         }
+        wait_copies<0>();
+        __syncwarp();
 #pragma unroll
-        for (int j = 0; j < RT; ++j) {
-            float* to = vpart + (size_t(kw) * 16 * MT + ra) * RP + 8 * j + 2 * t;
-            *reinterpret_cast<float2*>(to) = make_float2(d[j][0], d[j][1]);
-            *reinterpret_cast<float2*>(to + 8 * RP) = make_float2(d[j][2], d[j][3]);
+        for (int i = 0; i < S - 1; ++i) copy_out(nb + i, i);
+
+        // the warps' parts meet: the upper four warps' with the lower four's, then those
+        float* slot = vpart + ((warp & (kWarps / 2 - 1)) * 16 + g) * RP + 2 * t;
+#pragma unroll
+        for (int step = 0; step < 2; ++step) {
+            if (step == 1) __syncthreads();
+            if ((warp < kWarps / 2) != (step == 1)) continue;
+#pragma unroll
+            for (int j = 0; j < RT; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float2* to = reinterpret_cast<float2*>(slot + h * 8 * RP + 8 * j);
+                    float2 v = make_float2(d[j][2 * h], d[j][2 * h + 1]);
+                    if (step == 1) v = make_float2(__fadd_rn(v.x, to->x), __fadd_rn(v.y, to->y));
+                    *to = v;
+                }
         }
         if (pending) cluster.barrier_wait();
         __syncthreads();
-        const int live = min(16 * MT, rows) * RP;
+        const int live = rows * RP;
         for (int i = threadIdx.x; i < live; i += kThr) {
-            float s = 0.f;
+            float v = 0.f;
 #pragma unroll
-            for (int w = 0; w < KW; ++w) s = __fadd_rn(s, vpart[size_t(w) * 16 * MT * RP + i]);
-            vloc[i] = s;
+            for (int w = 0; w < kWarps / 2; ++w) v = __fadd_rn(v, vpart[w * 16 * RP + i]);
+            vloc[i] = v;
         }
         cluster.sync();
         for (int i = threadIdx.x; i < live; i += kThr) {
             float q[kMaxCluster];
 #pragma unroll
             for (int c = 0; c < kMaxCluster; ++c) q[c] = c < C ? cluster.map_shared_rank(vloc, c)[i] : 0.f;
-            float s = q[0];
+            float v = q[0];
 #pragma unroll
-            for (int c = 1; c < kMaxCluster; ++c) s = __fadd_rn(s, q[c]);
-            // (ranks past this adapter's: whatever its arrays hold there)
-            vsum[i] = int(unsigned(i) % RP) < rank_a ? s : 0.f;
+            for (int c = 1; c < kMaxCluster; ++c) v = __fadd_rn(v, q[c]);
+            // (ranks past this adapter's: whatever the ring held there)
+            vsum[i] = int(unsigned(i) % RP) < rank_a ? v : 0.f;
         }
         cluster.barrier_arrive();
         pending = true;
         __syncthreads();
+        uint32_t V[KS][F::TERMS][4];
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+            const int k = ks * 16 + 4 * t;
+            float fa[4], fb[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                fa[q] = k < RP && g < rows ? vsum[g * RP + k + q] : 0.f;
+                fb[q] = k < RP && g + 8 < rows ? vsum[(g + 8) * RP + k + q] : 0.f;
+            }
+#pragma unroll
+            for (int term = 0; term < F::TERMS; ++term) term_of(fa, fb, V[ks][term]);
+        }
 
-        // ---- y = base + scale B v over this rank's columns: a warp takes UN blocks of 16 at a time
-        for (int nb0 = n0 + kw * UN; nb0 < n1; nb0 += KW * UN) {
-            load_out(nb0);
-            float e[UN][2][4];
+        // ---- y = base + scale B v over this warp's units of the outputs
+        for (int u = nb, stage = 0; u < ne; ++u) {
+            wait_copies<S - 2>();
+            __syncwarp();
+            copy_out(u + S - 1, stage == 0 ? S - 1 : stage - 1);
+            const uint8_t* at = ring + stage * F::STAGE;
+            stage = stage == S - 1 ? 0 : stage + 1;
 #pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                clear4(e[i][0]);
-                clear4(e[i][1]);
-            }
+            for (int sub = 0; sub < SUB; ++sub) {
+                float e[4][4];
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks) {
-                const int k = ks * 16 + 4 * t;
-                float fa[4] = {0.f, 0.f, 0.f, 0.f}, fb[4] = {0.f, 0.f, 0.f, 0.f};
-                if (k < RP) {
+                for (int h = 0; h < 4; ++h) clear4(e[h]);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        fa[q] = ra < rows ? vsum[ra * RP + k + q] : 0.f;
-                        fb[q] = rb < rows ? vsum[rb * RP + k + q] : 0.f;
-                    }
-                }
-                if (p.ranks) {
+                for (int ks = 0; ks < KS; ++ks) {
+                    const int k = ks * 16 + 4 * t;
 #pragma unroll
-                    for (int i = 0; i < UN; ++i)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (k + 0 >= rank_a) w2[i][ks][h].x &= 0xFFFF0000u;
-                            if (k + 1 >= rank_a) w2[i][ks][h].x &= 0x0000FFFFu;
-                            if (k + 2 >= rank_a) w2[i][ks][h].y &= 0xFFFF0000u;
-                            if (k + 3 >= rank_a) w2[i][ks][h].y &= 0x0000FFFFu;
+                    for (int h = 0; h < 4; ++h) {
+                        // column g of n-tile h: output column 8 (g / 2) + 2 h + g % 2 of the run; ranks k .. k + 3
+                        const int n = sub * 32 + 8 * (g >> 1) + 2 * h + (g & 1);
+                        uint2 w = k < p.r ? *reinterpret_cast<const uint2*>(at + F::XBYTES + (n * p.r + k) * 2) : make_uint2(0u, 0u);
+                        if (p.ranks) {
+                            if (k + 0 >= rank_a) w.x &= 0xFFFF0000u;
+                            if (k + 1 >= rank_a) w.x &= 0x0000FFFFu;
+                            if (k + 2 >= rank_a) w.y &= 0xFFFF0000u;
+                            if (k + 3 >= rank_a) w.y &= 0x0000FFFFu;
                         }
-                }
-                // (bf16 results: two terms hold 16 bits)
 #pragma unroll
-                for (int term = 0; term < (BF16 ? 2 : 3); ++term) {
-                    uint32_t A0[4];
-                    term_of(fa, fb, A0);
-#pragma unroll
-                    for (int i = 0; i < UN; ++i) {
-                        mma_bf16(e[i][0], A0, w2[i][ks][0].x, w2[i][ks][0].y);
-                        mma_bf16(e[i][1], A0, w2[i][ks][1].x, w2[i][ks][1].y);
+                        for (int term = 0; term < F::TERMS; ++term) mma_bf16(e[h], V[ks][term], w.x, w.y);
                     }
                 }
-            }
-#pragma unroll
-            for (int i = 0; i < UN; ++i) {
-                if (nb0 + i >= n1) continue;
+                const int col = u * COLS + sub * 32 + 8 * t;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (!(h ? ub : ua)) continue;
-                    float o[4];
-                    (h ? ob[i] : oa[i]).values(o);
-                    o[0] = __fmaf_rn(scale, e[i][0][2 * h], o[0]);
-                    o[1] = __fmaf_rn(scale, e[i][0][2 * h + 1], o[1]);
-                    o[2] = __fmaf_rn(scale, e[i][1][2 * h], o[2]);
-                    o[3] = __fmaf_rn(scale, e[i][1][2 * h + 1], o[3]);
-                    const size_t at = (h ? yb : ya) + (nb0 + i) * 16 + 4 * t;
-                    Four<BF16> r;
-                    if constexpr (BF16) r.v = make_uint2(cvt2(o[0], o[1]), cvt2(o[2], o[3]));
-                    else r.v = make_float4(o[0], o[1], o[2], o[3]);
-                    r.store(p.y, at);
+                    if ((h ? idb : ida) != a || col >= p.N) continue;
+                    Eight<BF16> v;
+                    float o[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    if (p.base) {
+                        const uint8_t* bat = at + (g + 8 * h) * ROW;
+                        if constexpr (BF16) {
+                            v.v = *reinterpret_cast<const uint4*>(bat + swizzled<BF16, ROW>(sub * 4 + t, g) * 16);
+                        } else {
+                            v.v[0] = *reinterpret_cast<const float4*>(bat + swizzled<BF16, ROW>(2 * t, g) * 16);
+                            v.v[1] = *reinterpret_cast<const float4*>(bat + swizzled<BF16, ROW>(2 * t + 1, g) * 16);
+                        }
+                        v.values(o);
+                    }
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) o[q] = __fmaf_rn(scale, e[q >> 1][2 * h + (q & 1)], o[q]);
+                    v.set(o);
+                    v.store(p.y, size_t(row0 + g + 8 * h) * p.ldy + col);
                 }
             }
         }
+        wait_copies<0>();
     }
     if (pending) cluster.barrier_wait();
 }
 
-template <bool BF16, int RT, int MT>
+template <bool BF16, int RT>
 cudaError_t run(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
-    const size_t smem = size_t(kWarps / MT + 2) * 16 * MT * RT * 8 * 4;
-    const void* fn = (const void*)lora_kernel<BF16, RT, MT>;
-    if (set_only) return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    const size_t smem = Cfg<BF16, RT>::SMEM;
+    if (set_only) return cudaFuncSetAttribute((const void*)lora_kernel<BF16, RT>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -345,22 +420,15 @@ cudaError_t run(const LoraParams& p, int R, int C, cudaStream_t st, bool set_onl
     cfg.stream = st;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, RT, MT>, p, R);
-}
-template <bool BF16, int RT>
-cudaError_t by_rows(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
-    if (set_only) {
-        return run<BF16, RT, 1>(p, R, C, st, true);
-    }
-    return run<BF16, RT, 1>(p, R, C, st, false);
+    return cudaLaunchKernelEx(&cfg, lora_kernel<BF16, RT>, p, R);
 }
 template <bool BF16>
 cudaError_t by_rank(const LoraParams& p, int R, int C, cudaStream_t st, bool set_only) {
-    if (p.r <= 8) return by_rows<BF16, 1>(p, R, C, st, set_only);
-    if (p.r <= 16) return by_rows<BF16, 2>(p, R, C, st, set_only);
-    if (p.r <= 32) return by_rows<BF16, 4>(p, R, C, st, set_only);
-    if (p.r <= 64) return by_rows<BF16, 8>(p, R, C, st, set_only);
-    return by_rows<BF16, 16>(p, R, C, st, set_only);
+    if (p.r <= 8) return run<BF16, 1>(p, R, C, st, set_only);
+    if (p.r <= 16) return run<BF16, 2>(p, R, C, st, set_only);
+    if (p.r <= 32) return run<BF16, 4>(p, R, C, st, set_only);
+    if (p.r <= 64) return run<BF16, 8>(p, R, C, st, set_only);
+    return run<BF16, 16>(p, R, C, st, set_only);
 }
 
 }  // namespace
