@@ -275,8 +275,8 @@ constexpr uint32_t kSmem = 227 * 1024;
 
 // The tensor cores cut a running sum off rather than round it, so a chain of n steps of 16 inputs comes out some n 2^-25 too
 // small (measured: 1040 steps, 2.3e-5).  bf16 results do not show it.  For fp32 the epilogue warps add up the groups' sums (8
-// steps) in registers, which limits a tile to 64 tokens: its two terms are 128 columns of one MMA.  (Four groups at a
-// time: 3.7e-6 of the result.)
+// steps) in registers, which limits a tile to 64 tokens.  (Four groups at a time: 3.7e-6 of the
+// result.)
 template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
@@ -397,8 +397,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const uint32_t bstage = stage_bytes(p.cap, NP);
     const int BS = token_stages(p.cap, NP), WS = weight_stages(GATE, p.cap, NP);
     const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
-    const int DB = min(kMaxAcc, 256 / (p.cap * NP));       // accumulators
-    const uint32_t dcols = uint32_t(p.cap) * NP;
+    const int DB = min(kMaxAcc, 256 / p.cap);              // accumulators
+    const uint32_t dcols = uint32_t(p.cap), xoff = dcols * 512u * NP;    // columns of one; where a stage's sums begin
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
     uint64_t* w_empty = w_full + kMaxWS;
@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
                     for (int q = 0; q < NP; ++q)
                         bulk_g2s(to + q * nb * 4096, bsrc + ((size_t(u) * NP + q) * blocks + first) * 4096, nb * 4096, &b_full[tb.s]);
-                    bulk_g2s(to + dcols * 512u, sums + (size_t(u) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
+                    bulk_g2s(to + xoff, sums + (size_t(u) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
                     tb.next(BS);
                 }
                 tile = ahead;
@@ -521,7 +521,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             const uint32_t bars = smem_u32(b_full), bfull = bars, bempty = bars + 8 * kMaxStages, afull = smem_u32(a_full),
                            aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
             const uint32_t blo0 = (((sbase + L.ring) >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
-            const uint32_t z = sbase + L.z, xoff = dcols * 512u, zeros = sbase + zeros_at;
+            const uint32_t z = sbase + L.z, zeros = sbase + zeros_at;
             const uint64_t zd[2] = {plain_desc(z, zeros - z), plain_desc(z + kZBytes, zeros - z - kZBytes)};
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
@@ -543,7 +543,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             int4 tile = tile_of(blockIdx.x);
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
-                const uint32_t idesc = tc_idesc(kRows, NP * tile.z), sums = tc_idesc(kRows, tile.z);
+                const uint32_t idesc = tc_idesc(kRows, tile.z), rest = uint32_t(tile.z) * 32;   // (of the second terms, in 16 bytes)
                 if (!(ok = wait(dempty + 8 * ds, dph))) break;
                 uint32_t begun = 0;                        // the accumulator holds something
 #pragma unroll 1
@@ -551,25 +551,27 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     if (!(ok = wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
                     tc_fence_after();
                     const uint32_t a = taddr + 256 + as * 128;
-                    eight(a, blo, idesc, begun);
+                    // (fp32: the small second terms first, so that only the first terms' 8 steps cut off from a sum of full size)
+                    if (NP == 2) eight(a, blo + rest, idesc, 0u);
+                    eight(a, blo, idesc, NP == 2 ? 1u : begun);
                     if (g + 1 < G) {
                         if (NP == 2) {
                             hand_over();
                             if (!(ok = wait(dempty + 8 * ds, dph))) break;
                             tc_fence_after();
                         }
-                        eight(a + 64, blo + 128, idesc, NP == 2 ? 0u : 1u);
+                        if (NP == 2) eight(a + 64, blo + rest + 128, idesc, 0u);
+                        eight(a + 64, blo + 128, idesc, 1u);
                     }
-                    // the pair's zero points (to the first terms' columns)
+                    // the pair's zero points
                     const uint32_t x = sbase + L.ring + bs * bstage + xoff;
-                    mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), sums);
+                    mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), idesc);
                     commit_at(aempty + 8 * as);
                     commit_at(bempty + 8 * bs);
                     begun = 1;
                     if (NP == 2 && g + 2 < G) {
                         hand_over();
                         if (!(ok = wait(dempty + 8 * ds, dph))) break;
-                        begun = 0;
                     }
                     as ^= 1;
                     aph ^= as ^ 1;
@@ -816,7 +818,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 if (lane == 0) mbar_arrive(&d_empty[td.s]);
                 td.next(DB);
             } else {
-                // per group: the first terms' columns and the remainders', n further on
+                // the groups' sums
                 constexpr int kSums = kTileTokens<NP> / 32;
                 float sum[kSums][16];
 #pragma unroll
@@ -834,9 +836,6 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                         if (c0 >= real || !ok) continue;
                         float v[16];
                         tc_ld16(acc + uint32_t(c0), v);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
-                        tc_ld16(acc + uint32_t(n + c0), v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
                     }
