@@ -397,8 +397,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const uint32_t bstage = stage_bytes(p.cap, NP);
     const int BS = token_stages(p.cap, NP), WS = weight_stages(GATE, p.cap, NP);
     const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
-    const int DB = min(kMaxAcc, 256 / p.cap);              // accumulators
-    const uint32_t dcols = uint32_t(p.cap), xoff = dcols * 512u * NP;    // columns of one; where a stage's sums begin
+    // accumulators: bf16 of a tile, fp32 of a pair's two groups side by side; where a token stage's sums begin
+    const uint32_t dcols = uint32_t(p.cap) * NP, xoff = dcols * 512u;
+    const int DB = min(kMaxAcc, 256 / int(dcols));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
     uint64_t* w_empty = w_full + kMaxWS;
@@ -525,11 +526,11 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             const uint64_t zd[2] = {plain_desc(z, zeros - z), plain_desc(z + kZBytes, zeros - z - kZBytes)};
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
-            auto eight = [&](uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
+            auto eight = [&](uint32_t d, uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
                 const uint64_t desc = (uint64_t(kSwizzledHi) << 32) | lo;
 #pragma unroll
                 for (int ks = 0; ks < 8; ++ks)
-                    tc_mma_ta(acc, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
+                    tc_mma_ta(d, a + ks * 8, desc + (ks >> 2) * 64 + (ks & 3) * 2, idesc, ks == 0 ? begun : 1u);
             };
             auto hand_over = [&]() {                       // the accumulator to the epilogue
                 commit_at(dfull + 8 * ds);
@@ -544,35 +545,26 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
                 const uint32_t idesc = tc_idesc(kRows, tile.z), rest = uint32_t(tile.z) * 32;   // (of the second terms, in 16 bytes)
-                if (!(ok = wait(dempty + 8 * ds, dph))) break;
-                uint32_t begun = 0;                        // the accumulator holds something
+                if (NP == 1 && !(ok = wait(dempty + 8 * ds, dph))) break;
 #pragma unroll 1
                 for (int g = 0; g < G; g += 2) {
-                    if (!(ok = wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
+                    if (!(ok = (NP == 1 || wait(dempty + 8 * ds, dph)) && wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
                     tc_fence_after();
                     const uint32_t a = taddr + 256 + as * 128;
                     // (fp32: the small second terms first, so that only the first terms' 8 steps cut off from a sum of full size)
-                    if (NP == 2) eight(a, blo + rest, idesc, 0u);
-                    eight(a, blo, idesc, NP == 2 ? 1u : begun);
+                    if (NP == 2) eight(acc, a, blo + rest, idesc, 0u);
+                    eight(acc, a, blo, idesc, NP == 2 || g > 0 ? 1u : 0u);
                     if (g + 1 < G) {
-                        if (NP == 2) {
-                            hand_over();
-                            if (!(ok = wait(dempty + 8 * ds, dph))) break;
-                            tc_fence_after();
-                        }
-                        if (NP == 2) eight(a + 64, blo + rest + 128, idesc, 0u);
-                        eight(a + 64, blo + 128, idesc, 1u);
+                        const uint32_t d = NP == 2 ? acc + (dcols >> 1) : acc;
+                        if (NP == 2) eight(d, a + 64, blo + rest + 128, idesc, 0u);
+                        eight(d, a + 64, blo + 128, idesc, 1u);
                     }
                     // the pair's zero points
                     const uint32_t x = sbase + L.ring + bs * bstage + xoff;
                     mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), idesc);
                     commit_at(aempty + 8 * as);
                     commit_at(bempty + 8 * bs);
-                    begun = 1;
-                    if (NP == 2 && g + 2 < G) {
-                        hand_over();
-                        if (!(ok = wait(dempty + 8 * ds, dph))) break;
-                    }
+                    if (NP == 2) hand_over();
                     as ^= 1;
                     aph ^= as ^ 1;
                     blo += bstep;
@@ -583,7 +575,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                 }
                 if (!ok) break;
-                hand_over();
+                if (NP == 1) hand_over();
                 tile = ahead;
             }
         }
@@ -826,7 +818,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
                     for (int j = 0; j < 16; ++j) sum[i][j] = 0.f;
 #pragma unroll 1
-                for (int g = 0; g < G; ++g) {
+                for (int g = 0; g < G; g += 2) {
                     ok = ok && warp_wait(&d_full[td.s], td.full());
                     tc_fence_after();
                     const uint32_t acc = taddr + td.s * dcols + (uint32_t(32 * q) << 16);
@@ -836,6 +828,10 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                         if (c0 >= real || !ok) continue;
                         float v[16];
                         tc_ld16(acc + uint32_t(c0), v);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
+                        if (g + 1 == G) continue;
+                        tc_ld16(acc + (dcols >> 1) + uint32_t(c0), v);
 #pragma unroll
                         for (int j = 0; j < 16; ++j) sum[i][j] = __fadd_rn(sum[i][j], v[j]);
                     }
