@@ -864,21 +864,28 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                     asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                 }
-                if (ok && et < real) {
-                    // the sum of the tile's 64 activations as staged, in their order
-                    float X = 0.f;
-                    for (int s = 0; s < NP; ++s)
-#pragma unroll 2
-                        for (int c = 0; c < 8; ++c) {
-                            const uint4 h = *reinterpret_cast<const uint4*>(tbuf + (size_t(et >> 3) * NP + s) * 1024 + piece(et & 7, c));
-                            const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+                // the sum of the tile's 64 activations as staged: 2 (bf16) or 4 lanes to a token
+                constexpr int kShare = kEpiWarps * 32 / kTileTokens<NP>;
+                const int c = et / kShare, c0 = (et % kShare) * (8 / kShare);
+                float X = 0.f;
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
-                                X = __fadd_rn(X, __fadd_rn(v.x, v.y));
-                            }
+                for (int s = 0; s < NP; ++s)
+#pragma unroll
+                    for (int i = 0; i < 8 / kShare; ++i) {
+                        const uint4 h = *reinterpret_cast<const uint4*>(tbuf + (size_t(c >> 3) * NP + s) * 1024 + piece(c & 7, c0 + i));
+                        const uint32_t w[4] = {h.x, h.y, h.z, h.w};
+                        float part = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
+                            part = __fadd_rn(part, __fadd_rn(v.x, v.y));
                         }
-                    const int at = tile.y + et;
+                        X = __fadd_rn(X, part);
+                    }
+#pragma unroll
+                for (int o = 1; o < kShare; o <<= 1) X = __fadd_rn(X, __shfl_xor_sync(kFull, X, o));
+                if (ok && c < real && et % kShare == 0) {
+                    const int at = tile.y + c;
                     uint8_t* row = p.as + sums_at(p.w.I, NP, blocks) + size_t(at >> 3) * 128 + (at & 7) * 16;
                     put_sum(row, r, X, blocks * 128);
                     // the half that an odd number of groups leaves
