@@ -137,18 +137,19 @@ __global__ void __launch_bounds__(kPlanThr) moe_plan_kernel(const MoeTcParams p)
 }
 
 // ------------------------------------------------------------------ operand layout
-// Staged rows, `blocks` blocks of 8: for every pair of groups of 128 inputs and each of the NP terms all the blocks side by side,
-// each 4 atoms of [8 rows][64 inputs] fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte
-// swizzle), so that a tile's share of a pair is one run of memory.  Behind them, again by pairs, the sums of the four 64 inputs,
-// [8 rows][8]: per group the first terms of its two sums and their remainders.  (The second half of an odd last pair is
-// not written and not used, but its sums are zero.)
+// Staged rows, `blocks` blocks of 8: for every group of 128 inputs and each of the NP terms all the blocks side by side, each 2 atoms
+// of [8 rows][64 inputs] fp16 with the 16-byte pieces of a row swizzled by the row (the MMA's 128-byte swizzle), so that a
+// tile's share of a group is one run of memory.  Behind them, by pairs of groups, the sums of the four 64 inputs, [8
+// rows][8]: per group the first terms of its two sums and their remainders (zeros for the group an odd last pair lacks).
 // Input k of 16 sits at 2 (k % 8) - k % 2 + 2 (k / 8) (the order of A's columns in tensor memory).
 __host__ __device__ constexpr int pairs_of(int K) { return (K / 128 + 1) / 2; }
-__host__ __device__ constexpr size_t staged_bytes(int K, int np, size_t blocks) { return pairs_of(K) * blocks * (np * 4096 + 128); }
-__device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks, int block) {     // of 64 inputs number h
-    return ((size_t(h >> 2) * np + term) * blocks + block) * 4096 + (h & 3) * 1024;
+__host__ __device__ constexpr size_t staged_bytes(int K, int np, size_t blocks) {
+    return blocks * (size_t(K / 128) * np * 2048 + pairs_of(K) * 128);
 }
-__device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return pairs_of(K) * blocks * size_t(np) * 4096; }
+__device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks, int block) {     // of 64 inputs number h
+    return ((size_t(h >> 1) * np + term) * blocks + block) * 2048 + (h & 1) * 1024;
+}
+__device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return size_t(K / 128) * blocks * np * 2048; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
 // Sum number h (of 64 inputs) of a row: its two terms, in the row's pieces of 8 numbers (`stride` bytes apart) for each pair of groups.
 __device__ __forceinline__ void put_sum(void* row, int h, float X, size_t stride = 16) {
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
             const int at = pos[j], row = at & 7;
             uint8_t* to = p.xs + atom_at(k >> 6, 0, NP, blocks, at >> 3) + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
 #pragma unroll
-            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 4096) = out[q];
+            for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 2048) = out[q];
         }
         if ((lane & 15) == 0) put_sum(sums, k >> 6, X);
     }
@@ -281,8 +282,10 @@ template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
 // Shared memory: [gate_up: a tile of activations], the zero points (of two pairs of groups), barriers, the tokens' factors, the token
-// ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two groups of `cap` tokens and their sums;
-// small tiles leave more of the memory to the weights, whose latency they have less work to hide.
+// ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two
+// groups of `cap` tokens and their sums; of 128 tokens one group, as two stages of 66 KB leave the MMAs waiting for the next (a
+// pair in 1600 cycles instead of @; for smaller tiles the second hand-over costs more than it gives).  Small tiles leave more of the
+// memory to the weights, whose latency they have less work to hide.
 constexpr uint32_t kZBytes = kRows * 16;
 constexpr int kMaxStages = 8, kMaxWS = 8;
 struct Layout {
@@ -296,10 +299,13 @@ __host__ __device__ constexpr Layout layout(bool gate) {
     l.ring = (l.fac + 2 * 2 * 128 * 4 + 1023u) & ~1023u;
     return l;
 }
-__host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) { return uint32_t(cap) * 512u * np + uint32_t(cap < 64 ? 1024 : cap * 16); }
+__host__ __device__ constexpr int stage_groups(int cap) { return cap == 128 ? 1 : 2; }
+__host__ __device__ constexpr uint32_t stage_bytes(int cap, int np) {
+    return uint32_t(cap) * 256u * np * stage_groups(cap) + uint32_t(cap < 64 ? 1024 : cap * 16);
+}
 __host__ __device__ constexpr int token_stages(int cap, int np) {
-    const int n = int(72u * 1024u / stage_bytes(cap, np));
-    return n < 2 ? 2 : (n > kMaxStages ? kMaxStages : n);
+    const int n = int(72u * 1024u / stage_bytes(cap, np)), least = stage_groups(cap) == 1 ? 4 : 2;
+    return n < least ? least : (n > kMaxStages ? kMaxStages : n);
 }
 __host__ __device__ constexpr int weight_stages(bool gate, int cap, int np) {
     const int n = int((kSmem - layout(gate).ring - token_stages(cap, np) * stage_bytes(cap, np) - kZBytes) / kWBytes);
@@ -307,9 +313,9 @@ __host__ __device__ constexpr int weight_stages(bool gate, int cap, int np) {
 }
 static_assert(weight_stages(true, 128, 1) >= 3 && weight_stages(true, 64, 2) >= 3, "shared memory");
 
-// Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 4 KB apart): the upper half is this
+// Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 2 KB apart): the upper half is this
 // constant, the lower the address and 1 << 16.
-constexpr uint32_t kSwizzledHi = (4096u >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t kSwizzledHi = (2048u >> 4) | (1u << 14) | (2u << 29);
 // No swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
 __device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t further) {
     return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((further >> 4) & 0x3FFFu) << 16) | (uint64_t(128 >> 4) << 32) |
@@ -388,7 +394,8 @@ struct Turn {
 // lanes) on alternate pairs, each with its own place in tensor memory: one set's waits and hand-over, some 900 cycles, fall
 // under the other's arithmetic.  (Both sets on the two groups of one pair wait and work in step: 1650 cycles a pair instead of
 // 1000; twice as many warps doubled the hand-overs' instructions.)
-template <int NP, bool GATE>
+// GS: groups of a stage of the token ring.
+template <int NP, bool GATE, int GS>
 __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const int K = GATE ? p.w.H : p.w.I, N = GATE ? 2 * p.w.I : p.w.H, G = K >> 7;
@@ -398,7 +405,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const int BS = token_stages(p.cap, NP), WS = weight_stages(GATE, p.cap, NP);
     const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
     // accumulators: bf16 of a tile, fp32 of a pair's two groups side by side; where a token stage's sums begin
-    const uint32_t dcols = uint32_t(p.cap) * NP, xoff = dcols * 512u;
+    const uint32_t dcols = uint32_t(p.cap) * NP, xoff = dcols * 256u * GS;
     const int DB = min(kMaxAcc, 256 / int(dcols));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
@@ -489,25 +496,33 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             drain(w_full, WS, tw);
         }
     } else if (warp == kTokenWarp) {
-        // ---- staged tokens: a pair's share of the tile and its sums
+        // ---- staged tokens: the groups' shares of the tile, and with the last of a pair its sums
         if (elect_one()) {
-            const int pairs = pairs_of(K);
-            const size_t blocks = p.blocks;
+            const size_t blocks = p.blocks, gstep = size_t(NP) * blocks * 2048;
             const uint8_t* sums = bsrc + sums_at(K, NP, blocks);
             int4 tile = tile_of(blockIdx.x);
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
                 const uint32_t nb = uint32_t(tile.z) >> 3;
                 const size_t first = size_t(tile.y >> 3);
+                const uint8_t* src = bsrc + first * 2048;
 #pragma unroll 1
-                for (int u = 0; u < pairs; ++u) {
+                for (int g = 0; g < G; g += GS) {
+                    const int both = min(GS, G - g);
+                    const bool last = GS == 2 || (g & 1) || g + 1 == G;
                     if (tb.waits() && !(ok = one_wait(&b_empty[tb.s], tb.empty()))) break;
-                    mbar_arrive_expect_tx(&b_full[tb.s], (4096u * NP + 128u) * nb);
+                    mbar_arrive_expect_tx(&b_full[tb.s], (2048u * NP * both + (last ? 128u : 0u)) * nb);
                     uint8_t* to = smem + L.ring + size_t(tb.s) * bstage;
 #pragma unroll
-                    for (int q = 0; q < NP; ++q)
-                        bulk_g2s(to + q * nb * 4096, bsrc + ((size_t(u) * NP + q) * blocks + first) * 4096, nb * 4096, &b_full[tb.s]);
-                    bulk_g2s(to + xoff, sums + (size_t(u) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
+                    for (int j = 0; j < GS; ++j) {
+                        if (j < both) {
+#pragma unroll
+                            for (int q = 0; q < NP; ++q)
+                                bulk_g2s(to + (j * NP + q) * nb * 2048, src + q * blocks * 2048, nb * 2048, &b_full[tb.s]);
+                        }
+                        src += gstep;
+                    }
+                    if (last) bulk_g2s(to + xoff, sums + (size_t(g >> 1) * blocks + first) * 128, nb * 128, &b_full[tb.s]);
                     tb.next(BS);
                 }
                 tile = ahead;
@@ -544,7 +559,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             int4 tile = tile_of(blockIdx.x);
             for (int it = blockIdx.x; it < items && ok; it += step) {
                 const int4 ahead = tile_of(it + step);
-                const uint32_t idesc = tc_idesc(kRows, tile.z), rest = uint32_t(tile.z) * 32;   // (of the second terms, in 16 bytes)
+                const uint32_t idesc = tc_idesc(kRows, tile.z), rest = uint32_t(tile.z) * 16;   // (to the second terms, in 16 bytes)
                 if (NP == 1 && !(ok = wait(dempty + 8 * ds, dph))) break;
 #pragma unroll 1
                 for (int g = 0; g < G; g += 2) {
@@ -554,25 +569,33 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     // (fp32: the small second terms first, so that only the first terms' 8 steps cut off from a sum of full size)
                     if (NP == 2) eight(acc, a, blo + rest, idesc, 0u);
                     eight(acc, a, blo, idesc, NP == 2 || g > 0 ? 1u : 0u);
+                    auto next_stage = [&]() {
+                        commit_at(bempty + 8 * bs);
+                        blo += bstep;
+                        if (++bs == uint32_t(BS)) {
+                            bs = 0;
+                            bph ^= 1;
+                            blo = blo0;
+                        }
+                    };
                     if (g + 1 < G) {
-                        const uint32_t d = NP == 2 ? acc + (dcols >> 1) : acc;
-                        if (NP == 2) eight(d, a + 64, blo + rest + 128, idesc, 0u);
-                        eight(d, a + 64, blo + 128, idesc, 1u);
+                        if (GS == 1) {
+                            next_stage();
+                            if (!(ok = wait(bfull + 8 * bs, bph))) break;
+                            tc_fence_after();
+                        }
+                        const uint32_t d = NP == 2 ? acc + (dcols >> 1) : acc, lo = GS == 1 ? blo : blo + NP * rest;
+                        if (NP == 2) eight(d, a + 64, lo + rest, idesc, 0u);
+                        eight(d, a + 64, lo, idesc, 1u);
                     }
                     // the pair's zero points
                     const uint32_t x = sbase + L.ring + bs * bstage + xoff;
                     mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), idesc);
                     commit_at(aempty + 8 * as);
-                    commit_at(bempty + 8 * bs);
+                    next_stage();
                     if (NP == 2) hand_over();
                     as ^= 1;
                     aph ^= as ^ 1;
-                    blo += bstep;
-                    if (++bs == uint32_t(BS)) {
-                        bs = 0;
-                        bph ^= 1;
-                        blo = blo0;
-                    }
                 }
                 if (!ok) break;
                 if (NP == 1) hand_over();
@@ -973,9 +996,10 @@ __global__ void __launch_bounds__(kCombineThr) moe_combine_kernel(const MoeTcPar
     *y = make_uint4(r[0], r[1], r[2], r[3]);
 }
 
-const void* product_fn(bool bf16, bool gate) {
-    if (bf16) return gate ? (const void*)moe_product_kernel<1, true> : (const void*)moe_product_kernel<1, false>;
-    return gate ? (const void*)moe_product_kernel<2, true> : (const void*)moe_product_kernel<2, false>;
+const void* product_fn(bool bf16, bool gate, int cap) {
+    if (!bf16) return gate ? (const void*)moe_product_kernel<2, true, 2> : (const void*)moe_product_kernel<2, false, 2>;
+    if (stage_groups(cap) == 1) return gate ? (const void*)moe_product_kernel<1, true, 1> : (const void*)moe_product_kernel<1, false, 1>;
+    return gate ? (const void*)moe_product_kernel<1, true, 2> : (const void*)moe_product_kernel<1, false, 2>;
 }
 
 const void* stage_fn(bool bf16, int H) {
@@ -1025,7 +1049,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     if ((e = launch_dependent(stage_fn(bf16, p.w.H), dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
         const size_t smem = kSmem;
-        if ((e = launch_dependent(product_fn(bf16, gate), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
+        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<true> : (const void*)moe_combine_kernel<false>;
     const int cols = kCombineThr * (bf16 ? 8 : 4);
@@ -1042,9 +1066,9 @@ cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_
 
 cudaError_t moe_tc_set_attributes() {
     cudaError_t e;
-    for (int b = 0; b < 2; ++b)
+    for (int f = 0; f < 3; ++f)
         for (int gate = 0; gate < 2; ++gate) {
-            e = cudaFuncSetAttribute(product_fn(b != 0, gate != 0), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+            e = cudaFuncSetAttribute(product_fn(f > 0, gate != 0, f == 2 ? 128 : 64), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
             if (e != cudaSuccess) return e;
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, stage_fn(true, 1024), stage_fn(true, 2048),
