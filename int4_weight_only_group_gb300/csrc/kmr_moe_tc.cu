@@ -745,6 +745,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
         const int q = warp & 3, et = tid - kEpiWarp * 32, half = (warp - kEpiWarp) >> 2;
         float* fac = reinterpret_cast<float*>(smem + L.fac);       // [2][2][128]
         uint8_t* tbuf = smem + L.tile;
+        // gate_up: where this lane's activation of tokens 0 (an up lane: 1), 2, 4, 6 of eight goes: its column of the warp's 16
+        const bool lo = (lane & 15) < 8;
+        uint32_t aoff[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i16 = (lane >> 4) * 8 + (lane & 7), at = 2 * (i16 & 7) - (i16 & 1) + ((i16 >> 3) << 1);
+            aoff[j] = piece(2 * j + (lo ? 0 : 1), 2 * q + (at >> 3)) + (at & 7) * 2;
+        }
         Turn td;
         int turn = 0;
         int4 tile = tile_of(blockIdx.x), ahead;
@@ -775,24 +783,24 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             auto finish = [&](int c0, const float (&v)[16]) {
                 if (GATE) {
                     // in pairs: the gate lanes (tile rows 0..7) finish token c, the up lanes token c + 1
-                    const bool lo = (lane & 15) < 8;
-                    const int i16 = (lane >> 4) * 8 + (lane & 7);              // column of the warp's 16
-                    const int at = 2 * (i16 & 7) - (i16 & 1) + ((i16 >> 3) << 1);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 2) {
-                        if (c0 + j >= real) break;             // (padding: whatever the buffer holds)
-                        const float xa = __fmul_rn(v[j], __fmul_rn(ir, f[c0 + j]));
-                        const float xb = __fmul_rn(v[j + 1], __fmul_rn(ir, f[c0 + j + 1]));
-                        const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
-                        const int c = c0 + j + (lo ? 0 : 1);
-                        float a = silu_mul<NP == 1>(lo ? xa : other, lo ? other : xb);
-                        a = __fmul_rn(a, f[128 + c]);
-                        uint8_t* to = tbuf + size_t(c >> 3) * NP * 1024 + piece(c & 7, 2 * q + (at >> 3)) + (at & 7) * 2;
+                    for (int j = 0; j < 16; j += 4) {
+                        if (c0 + j >= real) break;             // (padding: whatever the buffers hold)
+                        const float4 u4 = *reinterpret_cast<const float4*>(f + c0 + j), s4 = *reinterpret_cast<const float4*>(f + 128 + c0 + j);
+                        const float u[4] = {u4.x, u4.y, u4.z, u4.w}, sc[4] = {s4.x, s4.y, s4.z, s4.w};
 #pragma unroll
-                        for (int s = 0; s < NP; ++s) {
-                            const __half hv = __float2half_rn(a);
-                            *reinterpret_cast<__half*>(to + s * 1024) = hv;
-                            a = __fsub_rn(a, __half2float(hv));
+                        for (int h = 0; h < 4; h += 2) {
+                            const float xa = __fmul_rn(v[j + h], __fmul_rn(ir, u[h])), xb = __fmul_rn(v[j + h + 1], __fmul_rn(ir, u[h + 1]));
+                            const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
+                            float a = silu_mul<NP == 1>(lo ? xa : other, lo ? other : xb);
+                            a = __fmul_rn(a, lo ? sc[h] : sc[h + 1]);
+                            uint8_t* to = tbuf + ((c0 + j) >> 3) * NP * 1024 + aoff[((j + h) & 7) >> 1];
+#pragma unroll
+                            for (int s = 0; s < NP; ++s) {
+                                const __half hv = __float2half_rn(a);
+                                *reinterpret_cast<__half*>(to + s * 1024) = hv;
+                                a = __fsub_rn(a, __half2float(hv));
+                            }
                         }
                     }
                 } else {
