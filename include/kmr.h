@@ -391,8 +391,9 @@ int kmr_moe_prepare(const kmr_moe* moe, void* stream);
  *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
  *             workspaces of their own.
  * Products are exact and sums are held in fp32, whatever the type; between gate_up and down the activations keep 22 bits (fp32)
- * or 11 (bf16).  Up to 32 places (T top_k) are two launches, more are five for every 32768 places; within either form a
- * token's result does not depend on the other tokens.  top_k 1..32.  Errors:
+ * or 11 (bf16).  A few tokens (up to 32 places T top_k of up to 16 tokens, whose experts taken each by itself have up to 200
+ * million weights) are two launches, more are five for every 32768 places; within either form a token's result does not depend
+ * on the other tokens.  A workspace of the size for T tokens does for fewer.  top_k 1..32.  Errors:
  * KMR_ERR_INVALID_ARG (pointers, dtype, epilogue), KMR_ERR_SHAPE, KMR_ERR_BATCH, KMR_ERR_BUFFER_SIZE; on the device
  * KMR_ERR_INVALID_ARG (an id outside -1..experts - 1). */
 size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, int T, int top_k);

@@ -2,15 +2,21 @@
 //
 // Both products are skinny (rank r at most 128), so the call is bound by reading x and base and writing y once; for a
 // few rows by latency and the adapters' own bytes.
-//   * A cluster of 8 CTAs takes R consecutive rows.  Each CTA multiplies an eighth of K (v = A x, all r ranks), the eight
-//     partials meet through distributed shared memory in rank order, and each CTA adds its eighth of the N columns: x,
-//     base and y pass through once, v never leaves the chip, one launch.
-//   * A tile's distinct adapters are taken in turn, other rows masked: runs of rows of one request (a prompt) cost
-//     one turn.  A row's result does not hang on its neighbours (on R only by the order of the sums over K).
+//   * A cluster of C = 1..8 CTAs takes R consecutive rows.  Each CTA multiplies its share of K (v = A x, all r ranks), the
+//     partials meet through distributed shared memory in rank order, and each CTA adds its share of the N columns: x, base
+//     and y pass through once, v never leaves the chip, one launch.
+//   * Every warp has its own columns and streams them, rows of x (or base) and the same columns of A (or rows of B), through
+//     a ring of its own by 16-byte cp.async, two to four units of 128 bytes a row deep: nothing but a wait for its own copies
+//     stands between a warp and its products.  (Loads into registers, eight bytes a lane, held up by the L1's tags: 4077 rows
+//     42 us against 27.5.  A ring per CTA, fed by one warp with bulk copies of 512 bytes or by four with cp.async: 52 and 45
+//     us; a bulk copy costs the copy engine some 60 cycles, and 16 warps that all wait for each chunk proceed in step.)
+//   * A tile's distinct adapters are taken in turn, other rows left out: runs of rows of one request (a prompt) cost one turn.
+//     A row's result does not hang on its neighbours (on T only by the order of the sums over K).
 //   * mma.m16n8k16 in bf16 with fp32 sums.  fp32 operands (x, v) are cut into three bf16 terms, which hold their 24 bits
 //     whatever their exponent; the adapters are bf16 already, so the products are exact.
-//   * The k and n indexes are dealt to the lanes so that each loads 16 bytes of a row at a time (any order of the
-//     contraction will do, as long as both operands follow it).
+// Measured: one row, K 2048, N 4096, r 16: 4.5 us; 16 rows of 16 requests, K = N = 2048, r 64: 6.9 us; 4077 rows bf16, K 2048, N
+// 4096, r 16: 27.5 us (3.0 TB/s); 8192 rows fp32, K 6144, N 2048, r 32: 81 us (4.2 TB/s of 6.8: the cutting into terms and the
+// MMAs take half the issue slots).
 #include <cooperative_groups.h>
 
 #include "kmr_moe.cuh"
@@ -434,9 +440,10 @@ cudaError_t by_rank(const LoraParams& p, int R, int C, cudaStream_t st, bool set
 }  // namespace
 
 cudaError_t launch_lora(const LoraParams& p, bool bf16, int sms, cudaStream_t st) {
-    // One row a tile up to two rows a SM: rows of a small batch have adapters of their own (64 rows of 64 adapters: 7 us against
-    // 55 with tiles of 16; of 4 adapters 8 against 9).  More rows are taken 16 at a time (32 and 64 are no faster even for one
-    // adapter: their phases overlap less).  Then the smallest cluster that gives every SM a CTA or two.
+    // One row a tile up to two rows a SM: rows of a small batch have adapters of their own (64 rows of 64 adapters: 6.3 us against
+    // 44 with tiles of 16; of 4 adapters 6.3 against 8.3; 200 rows of 200: 14 against 50).  More rows are taken 16 at a time
+    // (4077 rows: 28 us, 8 at a time 36).  Then the largest cluster that still fits its CTAs to the SMs at once, or nearly
+    // (1000 rows: 11.5 us in clusters of 4, 21 by themselves, 15 in clusters of 8; 4077 rows: 28, and 36 in clusters of 4).
     const int R = p.T <= 2 * sms ? 1 : 16, tiles = (p.T + R - 1) / R;
     int C = kMaxCluster;
     while (C > 1 && tiles * C > 2 * sms + sms / 2) C /= 2;

@@ -10,7 +10,7 @@ constexpr int kMoeMaxExperts = 1024;
 constexpr int kMoeMaxTopK = 32;
 constexpr int kMoeMaxDim = 8192;             // hidden and intermediate sizes, multiples of 128
 constexpr int kMoeMaxTokens = 1 << 20;
-constexpr int kMoeSmallPlaces = 32;          // places (token, j) of the small form: a warp's lanes
+constexpr int kMoeSmallPlaces = 32;          // most places (token, j) of the small form: a warp's lanes
 constexpr int kMoeSmallTokens = 16;          // its most tokens
 constexpr long long kMoeSmallWeights = 200000000;   // and weights of the places' experts, each counted by itself
 constexpr int kMoeSmallCtas = 128;           // CTAs at once that its sizes are made for (a GB300 has 152 SMs)

@@ -82,7 +82,8 @@ extern "C" size_t kmr_moe_experts_workspace_size(const kmr_moe* moe, int dtype, 
     MoeView v;
     if (view_of(moe, &v) != KMR_OK || !dtype_ok(dtype) || counts_ok(T, top_k) != KMR_OK) return 0;
     if (moe_small_fits(v, dtype == KMR_BF16, T, top_k)) return size_t(T) * top_k * v.I * 4;
-    return moe_tc_sizes(v, dtype == KMR_BF16, chunk_of(T, top_k), top_k).total;
+    const size_t most = size_t(kMoeSmallPlaces) * v.I * 4, all = moe_tc_sizes(v, dtype == KMR_BF16, chunk_of(T, top_k), top_k).total;
+    return all > most ? all : most;                      // (never less than for fewer tokens)
 }
 
 extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, const int32_t* ids, const float* weights, int T,

@@ -4,18 +4,23 @@
 //   rows of gate_e, up_e, down_e: w = (q - 8) s + z in the KMR4 layout (include/kmr.h).
 //
 // What bounds it: every expert that a token is sent to is read once (1.0625 bytes per 2 weights), so HBM; for one
-// token the latency of two dependent kernels.  A warp plans the call by itself: its lanes hold the (at most 32)
-// expert ids, one match gives the distinct experts.
+// token the latency of two dependent kernels.
 //   * gate_up: (expert, 16-row tile) pairs are dealt out evenly over one CTA per SM, which fetches its tiles with
-//     cp.async.bulk into a ring of two halves.
+//     cp.async.bulk into a ring (of two halves, if they do not all fit).
 //   * down: a CTA owns 16 output columns and fetches that tile of every expert used, so a token's sum is formed in
-//     one place, in the order of its places, without atomics.  Its weights' copies start while gate_up still runs.
-//   * warp w multiplies the 128-input groups w, w + 16, ... of a tile (fewer groups: several tiles at once).  The codes
-//     are the A operand of mma.m16n8k16, as exact fp16 integers q - 8; the inputs are B, scaled by a power of two per
-//     (row, group): one column per token in bf16, two (the fp16 rounding and what it left) in fp32, so that products
-//     and sums keep single precision.  Per group, y += (s D + z X) / sigma with D = sum (q - 8) x and X = sum x.
+//     one place, in the order of its places, without atomics.  Its weights' copies start before its inputs are there.
+//   * One warp plans the call: its lanes hold the (at most 32) expert ids, one match gives the distinct experts, and each lane
+//     lists and fetches a tile.  The others meanwhile turn the rows into the MMAs' B fragments, once for the whole CTA.
+//   * (tile, 128-input group) products are dealt to 32 warps, at most 16 to a tile, which then take the groups w, w + 16, ...
+//     The codes are the A operand of mma.m16n8k16, as exact fp16 numbers; the inputs are B, scaled by a power of two per
+//     (row, group): one column per token in bf16, two (the fp16 rounding and what it left) in fp32, so that products and
+//     sums keep single precision.  Per group, y += (s D + z X) / sigma with D = sum (q - 8) x and X = sum x.
 //   * partial sums meet in shared memory and are added in a fixed order that hangs on K alone: a token's result does not
 //     change with the other tokens of the call.
+// Measured: one token, 8 of 128 experts of 2048 x 768 (20 MB), fp32: 14.9 us, gate_up 8 (its first weights arrive after 3.4: the
+// wait for the ids, the plan, HBM), down 5, launches; four tokens (32 places) 43 us.  With 16 warps, each of which made its own
+// fragments and took 8 off the codes (9 instructions for a step's A instead of 5): 25.7.  A product of one warp takes
+// 1,400 cycles with 16 warps at work, for some 150 instructions and 8 MMAs (64 cycles): latency, which 32 warps hide better.
 #include <cuda_fp16.h>
 
 #include "kmr_int4_mma.cuh"
@@ -75,7 +80,7 @@ struct __align__(16) Tile {
 // ------------------------------------------------------------------ operands
 // The rows wait in shared memory as B fragments: per (row, group of 128) the four quarters t of the lanes, each the 16 registers of
 // its 8 steps (inputs 8 i + 2 t and + 1 in register i), in 16-byte pieces that two quarters exchange so that a load meets no
-// bank twice; SPLIT: the remainders behind them.  An item of zeros stands last.  Beside them, for each term, its sum and 1 / sigma.
+// bank twice; SPLIT: the remainders behind them.  An item of zeros stands last.  Beside them, for each term, its sum and 1 / sigma, as the codes' 2^-9 needs them.
 template <bool SPLIT>
 constexpr int kItemBytes = SPLIT ? 512 : 256;
 template <typename IN, bool SPLIT>
@@ -125,7 +130,8 @@ __device__ __forceinline__ void stage_rows(uint8_t* to, float4* fold, const IN* 
             float sum = __fadd_rn(lane < 16 ? X[0] : X[1], __shfl_xor_sync(kFull, lane < 16 ? X[1] : X[0], 16));
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
-            if ((lane & 15) == 0) *reinterpret_cast<float2*>(reinterpret_cast<float*>(fold + item) + (lane >> 3)) = make_float2(sum, isg);
+            if ((lane & 15) == 0) *reinterpret_cast<float2*>(reinterpret_cast<float*>(fold + item) + (lane >> 3)) =
+                    make_float2(sum * 0x1p-9f, isg * 0x1p9f);      // (the 2^-9 of the codes; isg is 2^114 at the most)
         }
     }
 }
@@ -133,7 +139,7 @@ __device__ __forceinline__ void stage_rows(uint8_t* to, float4* fold, const IN* 
 // B fragments of one 128-input group of up to 8 (SPLIT: 4) rows for this lane, and the group's fold constants.
 struct Frag {
     uint32_t b[16];
-    float X0, is0, X1, is1;  // of columns 2t and 2t + 1: sum of the staged values, 1 / sigma
+    float X0, is0, X1, is1;  // of columns 2t and 2t + 1: sum of the staged values 2^-9, 2^9 / sigma
 };
 // Column lane / 4 takes staged item `item` (SPLIT: columns 4..7 its remainders).
 template <bool SPLIT>
@@ -156,10 +162,16 @@ __device__ __forceinline__ void load_frag(Frag& f, const uint8_t* staged, const 
 }
 
 // acc (rows g and g + 8, columns 2t and 2t + 1) += one (16-row tile, 128-input group) block times the fragments.
-// A code's four bits are themselves an fp16: q 2^-24, subnormal (rows g + 8: 16 q 2^-24), and the MMA takes it exactly, so that a
-// register of codes costs one AND.  w = q s + (z - 8 s); the group's sum is scaled back before s, exactly.
+// A code's four bits are themselves an fp16, q 2^-24 (rows g + 8: 16 q 2^-24), so that half an AND and half an HFMA2 give (q - 8)
+// 2^-9.  (The MMA takes the subnormal numbers as they are, too, but aligns their products as if they were 2^10 larger: 2.2e-6
+// of the result instead of 4e-7.)
 __device__ __forceinline__ void block_product(const uint8_t* gb, const Frag& f, int lane, float (&acc)[4]) {
     const int g = lane >> 2;
+    const __half2 m8 = __float2half2_rn(-0x1p-6f), up0 = __float2half2_rn(0x1p15f), up1 = __float2half2_rn(0x1p11f);
+    auto codes = [&](uint32_t v, __half2 up) {
+        const __half2 a = __hfma2(*reinterpret_cast<const __half2*>(&v), up, m8);
+        return *reinterpret_cast<const uint32_t*>(&a);
+    };
     float d[2][4];
 #pragma unroll
     for (int c = 0; c < 2; ++c) d[c][0] = d[c][1] = d[c][2] = d[c][3] = 0.f;
@@ -170,20 +182,19 @@ __device__ __forceinline__ void block_product(const uint8_t* gb, const Frag& f, 
 #pragma unroll
         for (int ks = 0; ks < 4; ++ks) {
             const uint32_t w = w4[ks], w2 = w >> 8;
-            mma16816(d[ks & 1], w & 0x000F000Fu, w & 0x00F000F0u, w2 & 0x000F000Fu, w2 & 0x00F000F0u, f.b[blk * 8 + 2 * ks],
-                     f.b[blk * 8 + 2 * ks + 1]);
+            mma16816(d[ks & 1], codes(w & 0x000F000Fu, up0), codes(w & 0x00F000F0u, up1), codes(w2 & 0x000F000Fu, up0),
+                     codes(w2 & 0x00F000F0u, up1), f.b[blk * 8 + 2 * ks], f.b[blk * 8 + 2 * ks + 1]);
         }
     }
     auto fold = [](uint32_t sz, float D, float X, float is, float a) {
-        const float s = bf16_lo(sz), z = __fmaf_rn(-8.f, s, bf16_hi(sz));
-        return __fmaf_rn(__fmaf_rn(s, D, __fmul_rn(z, X)), is, a);
+        return __fmaf_rn(__fmaf_rn(bf16_lo(sz), D, __fmul_rn(bf16_hi(sz), X)), is, a);
     };
     const uint32_t sz0 = *reinterpret_cast<const uint32_t*>(gb + 1024 + g * 4);
     const uint32_t sz1 = *reinterpret_cast<const uint32_t*>(gb + 1024 + (g + 8) * 4);
-    acc[0] = fold(sz0, __fmul_rn(__fadd_rn(d[0][0], d[1][0]), 0x1p24f), f.X0, f.is0, acc[0]);
-    acc[1] = fold(sz0, __fmul_rn(__fadd_rn(d[0][1], d[1][1]), 0x1p24f), f.X1, f.is1, acc[1]);
-    acc[2] = fold(sz1, __fmul_rn(__fadd_rn(d[0][2], d[1][2]), 0x1p20f), f.X0, f.is0, acc[2]);
-    acc[3] = fold(sz1, __fmul_rn(__fadd_rn(d[0][3], d[1][3]), 0x1p20f), f.X1, f.is1, acc[3]);
+    acc[0] = fold(sz0, __fadd_rn(d[0][0], d[1][0]), f.X0, f.is0, acc[0]);
+    acc[1] = fold(sz0, __fadd_rn(d[0][1], d[1][1]), f.X1, f.is1, acc[1]);
+    acc[2] = fold(sz1, __fadd_rn(d[0][2], d[1][2]), f.X0, f.is0, acc[2]);
+    acc[3] = fold(sz1, __fadd_rn(d[0][3], d[1][3]), f.X1, f.is1, acc[3]);
 }
 
 // The columns' sums of one warp's groups w, w + 16, ... of a tile: acc (rows g and g + 8, columns 2t and 2t + 1).  `row` is the

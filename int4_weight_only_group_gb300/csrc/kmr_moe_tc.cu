@@ -5,7 +5,7 @@
 //            of 16 and cut into tiles of at most `cap` (16..128) tokens
 //   stage    token rows as fp16 into the tiles' operand layout (a copy per place)
 //   gate_up  D = A B^T per (tile, 128 packed weight rows), silu(gate) * up, staged again for
-//   down     the same product, fp32 rows of every place
+//   down     the same product, a row for every place
 //   combine  y[t] = sum_j weights[t, j] * row of place (t, j), in the order of the places: no atomics on values
 //
 // The product, D[row][token] = sum_k w[row][k] x[token][k], w = (q - 8) s + z:
@@ -23,9 +23,15 @@
 //     fp16's range absorbs: the values stay far above its subnormals.
 //
 // Each CTA is persistent and warp-specialised: a weight producer and a token producer (cp.async.bulk rings), eight warps that turn
-// KMR4 blocks into A in tensor memory (kmr_tcgemm.cu describes that layout), one thread that issues the MMAs, four epilogue
-// warps on the other of two accumulators (for fp32 it also adds up chunks of a long sum, see kChunk).  Every wait is bounded; a timeout records KMR_ERR_DEVICE_TIMEOUT, skips the
-// remaining work, drains the copies in flight and frees tensor memory.
+// KMR4 blocks into A in tensor memory (kmr_tcgemm.cu describes that layout), one that lays out their zero points, one thread that
+// issues the MMAs, eight epilogue warps on the accumulators that are done (for fp32 they also add up the groups' sums).  Every wait
+// is bounded; a timeout records KMR_ERR_DEVICE_TIMEOUT, skips the remaining work, drains the copies in flight and frees
+// tensor memory.
+// Measured (us: plan, stage, gate_up, down, combine; 2048 inputs): 128 tokens of 128 experts of 768, 8 a token: fp32, 16 rows 5,
+// 6, 40, 25, 4 and 509 rows 6, 9.5, 108, 49, 9.5; bf16, 4096 rows 12, 52, 178, 102, 28.  1024 rows of 8 experts of 6144, 2 a
+// token, bf16: 6, 7, 94, 60, 7.  What bounds the products: for tiles of 16 the turning of KMR4 blocks into A (1,900 cycles for each of
+// two sets of warps a pair of groups, 13 bytes of weights a cycle on an SM); for 128 the MMAs' 1,090 cycles a pair and their
+// hand-overs (1,550 in all); fp32 tiles of 32 to 64 the epilogue, which reads every group's sums.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -276,16 +282,15 @@ constexpr uint32_t kSmem = 227 * 1024;
 
 // The tensor cores cut a running sum off rather than round it, so a chain of n steps of 16 inputs comes out some n 2^-25 too
 // small (measured: 1040 steps, 2.3e-5).  bf16 results do not show it.  For fp32 the epilogue warps add up the groups' sums (8
-// steps) in registers, which limits a tile to 64 tokens.  (Four groups at a time: 3.7e-6 of the
-// result.)
+// steps) in registers, which limits a tile to 64 tokens.  (Four groups at a time: 3.7e-6 of the result.)
 template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
 // Shared memory: [gate_up: a tile of activations], the zero points (of two pairs of groups), barriers, the tokens' factors, the token
 // ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two
-// groups of `cap` tokens and their sums; of 128 tokens one group, as two stages of 66 KB leave the MMAs waiting for the next (a
-// pair in 1600 cycles instead of @; for smaller tiles the second hand-over costs more than it gives).  Small tiles leave more of the
-// memory to the weights, whose latency they have less work to hide.
+// groups of `cap` tokens and their sums; of 128 tokens one group, as two stages of 66 KB leave the MMAs waiting for the next (1024
+// rows of 8 experts: 173 us against 163; for smaller tiles the second hand-over costs more than it gives, 80 rows: 87
+// against 80).  Small tiles leave more of the memory to the weights, whose latency they have less work to hide.
 constexpr uint32_t kZBytes = kRows * 16;
 constexpr int kMaxStages = 8, kMaxWS = 8;
 struct Layout {

@@ -121,6 +121,10 @@ SHAPES = [  # E, H, I, T, k
     (2, 2176, 128, 5, 2), (2, 256, 2176, 5, 2), (1, 8192, 128, 2, 1), (1, 128, 8192, 2, 1), (2, 4096, 4096, 1, 2), (3, 640, 1408, 40, 2),
     (8, 512, 256, 300, 2), (2, 256, 384, 257, 1), (2, 8192, 128, 40, 1), (2, 128, 8192, 40, 1), (3, 256, 2176, 700, 2),
     (40, 256, 128, 1200, 8), (200, 128, 128, 64, 6), (4, 2048, 768, 90, 2), (1, 128, 128, 2081, 32),
+    # few tokens whose tiles pass through the rings more than once, the most tokens and places of that form and one more of
+    # each; more places than one pass takes
+    (6, 4096, 1024, 4, 3), (12, 1024, 4096, 4, 3), (7, 640, 2560, 16, 2), (7, 640, 2560, 17, 1), (7, 640, 2560, 11, 3),
+    (2, 8192, 1024, 3, 2), (4, 128, 256, 17000, 2),
 ]
 
 
@@ -216,6 +220,35 @@ def test_a_token_by_itself(torch, dtype):
         assert torch.equal(run_experts(torch, layer, x[t:t + 1], ids[t:t + 1], w[t:t + 1], dtype)[0], few[t])
 
 
+@pytest.mark.parametrize("dtype", DT)
+def test_tokens_among_others_when_grouped(torch, dtype):
+    """The same for the grouped form, whose tiles hold other tokens and numbers of tokens in either call."""
+    r = np.random.default_rng(9)
+    layer = Layer(torch, r, 8, 512, 384)
+    x, _ = rounded(torch, r.standard_normal((700, 512)), dtype)
+    ids, w = places(r, 700, 8, 3, 0.0)
+    ids, w = i32(torch, ids), torch.from_numpy(w).cuda()
+    many = run_experts(torch, layer, x, ids, w, dtype)
+    for a, b in ((0, 12), (30, 130), (300, 650)):
+        assert torch.equal(run_experts(torch, layer, x[a:b], ids[a:b], w[a:b], dtype), many[a:b])
+
+
+def test_experts_in_a_larger_workspace(torch):
+    """A workspace for many tokens serves any number of them, whatever an earlier call has left in it."""
+    r = np.random.default_rng(22)
+    layer = Layer(torch, r, 6, 256, 2176)
+    n = kmr.kmr_moe_experts_workspace_size(layer.dev, kmr.KMR_BF16, 60, 2)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream()
+    for T in (60, 16, 1, 17, 59, 3):
+        x, xv = rounded(torch, r.standard_normal((T, 256)), kmr.KMR_BF16)
+        ids, w = places(r, T, 6, 2)
+        y = torch.full((T, 256), float("nan"), device="cuda", dtype=torch.bfloat16)
+        kmr.kmr_moe_experts(layer.dev, x, kmr.KMR_BF16, i32(torch, ids), torch.from_numpy(w).cuda(), T, 2, y, kmr.KMR_EPI_NONE, ws, n, stream)
+        rows_close(y, moe.experts(xv, ids, w, layer.gate_up, layer.down), TOL[kmr.KMR_BF16])
+    assert kmr.kmr_last_device_error() == 0
+
+
 def test_experts_captured_and_on_two_streams(torch):
     r = np.random.default_rng(21)
     layer = Layer(torch, r, 16, 512, 256)
@@ -277,7 +310,8 @@ def adapter_set(torch, r, L, K, N, rank, ranks=None):
 @pytest.mark.parametrize("dtype", DT)
 @pytest.mark.parametrize("T,K,N,rank,L", [(1, 128, 64, 8, 2), (3, 2048, 512, 16, 8), (16, 256, 4096, 64, 32), (64, 160, 48, 24, 3),
                                           (65, 512, 16, 128, 5), (77, 16, 272, 40, 4), (500, 256, 128, 16, 7), (2049, 128, 96, 32, 6),
-                                          (2300, 192, 144, 128, 3), (40, 6144, 32, 8, 2)])
+                                          (2300, 192, 144, 128, 3), (40, 6144, 32, 8, 2), (1, 16, 16, 8, 1), (305, 80, 144, 128, 5),
+                                          (1300, 1040, 272, 64, 9), (5000, 48, 16, 32, 700), (304, 2048, 1040, 56, 300)])
 def test_lora(torch, T, K, N, rank, L, dtype):
     r = np.random.default_rng(T + K)
     lora, host = adapter_set(torch, r, L, K, N, rank)
@@ -329,6 +363,42 @@ def test_lora_ranks_bad_ids_and_values(torch, T, dtype):
     assert torch.isnan(y[5]).all() and torch.equal(y[3:5], base[3:5])
     keep = [t for t in range(T) if t != 5]
     rows_close(y[keep], want[keep], TOL[dtype])
+
+
+@pytest.mark.parametrize("dtype", DT)
+def test_lora_captured_and_on_two_streams(torch, dtype):
+    r = np.random.default_rng(31)
+    K, N, L = 320, 208, 9
+    lora, _ = adapter_set(torch, r, L, K, N, 16)
+    cases = []
+    for T in (5, 900):
+        x, _ = rounded(torch, r.standard_normal((T, K)), dtype)
+        base, _ = rounded(torch, r.standard_normal((T, N)), dtype)
+        ids, want = i32(torch, r.integers(-1, L, T)), torch.empty_like(base)
+        kmr.kmr_lora_apply(lora, x, base, want, dtype, ids, T, K, N, torch.cuda.current_stream())
+        cases.append((x, base, ids, want))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.zeros_like(c[3]) for _ in range(8)] for c in cases]
+    torch.cuda.synchronize()
+    for i in range(8):
+        for s, c, o in zip(streams, cases, outs):
+            kmr.kmr_lora_apply(lora, c[0], c[1], o[i], dtype, c[2], len(c[2]), K, N, s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(y, c[3]) for c, o in zip(cases, outs) for y in o)
+    for x, base, ids, want in cases:                         # captured, with other values at replay
+        y = torch.zeros_like(want)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            kmr.kmr_lora_apply(lora, x, base, y, dtype, ids, len(ids), K, N, torch.cuda.current_stream())
+        for scale in (1.0, -0.5):
+            x.mul_(scale)
+            ids.copy_(torch.flip(ids, (0,)))
+            kmr.kmr_lora_apply(lora, x, base, want, dtype, ids, len(ids), K, N, torch.cuda.current_stream())
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(y, want)
+    assert kmr.kmr_last_device_error() == 0
 
 
 # ------------------------------------------------------------------ together
