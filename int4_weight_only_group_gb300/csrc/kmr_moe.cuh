@@ -12,7 +12,7 @@ constexpr int kMoeMaxDim = 8192;             // hidden and intermediate sizes, m
 constexpr int kMoeMaxTokens = 1 << 20;
 constexpr int kMoeSmallPlaces = 32;          // most places (token, j) of the small form: a warp's lanes
 constexpr int kMoeSmallTokens = 16;          // its most tokens
-constexpr long long kMoeSmallWeights = 200000000;   // and weights of the places' experts, each counted by itself
+constexpr long long kMoeSmallWeights = 3ll << 26;    // and weights of the places' experts, each counted by itself
 constexpr int kMoeSmallCtas = 128;           // CTAs at once that its sizes are made for (a GB300 has 152 SMs)
 
 // ------------------------------------------------------------------ router
@@ -59,7 +59,7 @@ struct MoeTcParams {
     const void* x;                           // [T][H]
     const int32_t* ids;                      // [T][k]
     const float* weights;                    // [T][k]
-    int T, k, cap;                           // tokens of a tile: 16, 32, 64 or 128
+    int T, k, cap;                           // most tokens of a tile: 16, 32, 64 or 128
     int* ntiles;
     int4* tiles;                             // (expert, first position, tokens with padding, tokens)
     int32_t* pos;                            // [T][k]: the place's position, or -1

@@ -510,8 +510,8 @@ int gate_tiles(const MoeView& w, int S, int ctas) {      // the longest sequence
 }  // namespace
 
 // (a larger call, of weights or of tokens, is quicker in the grouped form, whose kernels cost 22 us in any case but read the
-// weights faster: 16 experts of 4096 x 2048, two a token, fp32: four tokens 48 us against 55, five 65 against 55; 64 experts of
-// 2048 x 768, one a token, bf16: 16 tokens 27 against 31, 32 tokens 49 against 35)
+// weights faster: 16 experts of 4096 x 2048, two a token, fp32: four tokens 48 us against 52, five 65 against 53; 64 experts of
+// 2048 x 768, one a token, bf16: 16 tokens 27 against 31, 32 tokens 49 against 34)
 bool moe_small_fits(const MoeView& w, bool bf16, int T, int k) {
     const int S = T * k;
     int st, b;

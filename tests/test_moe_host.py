@@ -97,6 +97,15 @@ def test_workspace_size(L):
     assert W(ctypes.addressof(kmr.MoeStruct(**{**MOE, "hidden": 200})), 0, 1, 2) == 0
 
 
+@pytest.mark.parametrize("E,H,I", [(1, 128, 8192), (1, 8192, 128), (64, 2048, 768), (8, 4096, 4096)])
+def test_workspace_for_more_tokens_does_for_fewer(L, E, H, I):
+    m = kmr.MoeStruct(**{**MOE, "experts": E, "hidden": H, "intermediate": I})
+    for dtype in (kmr.KMR_F32, kmr.KMR_BF16):
+        for k in (1, 2, 8, 32):
+            sizes = [L.kmr_moe_experts_workspace_size(ctypes.addressof(m), dtype, T, k) for T in (*range(1, 80), 1000, 1024, 1025, 40000, 1 << 20)]
+            assert sizes[0] > 0 and sizes == sorted(sizes)
+
+
 def test_binding_checks_the_weights(L):
     torch = pytest.importorskip("torch")
     gu, dn = kmr.kmr_packed_size(256, 256), kmr.kmr_packed_size(256, 128)
