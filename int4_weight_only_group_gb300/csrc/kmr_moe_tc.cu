@@ -47,8 +47,7 @@ namespace {
 constexpr uint32_t kFull = 0xffffffffu;
 constexpr int kRows = 128;                        // packed weight rows of a product (the MMA's M)
 constexpr uint32_t kWBytes = 16 * kGroupBytes;    // two groups of eight KMR4 tiles
-constexpr int kAQ = 2;                            // pairs of dequantised groups in tensor memory, 128 columns each
-constexpr int kMaxAcc = 8;                        // accumulators: as many as 256 columns hold
+constexpr int kMaxAcc = 8;                        // accumulators: as many as the columns beside A hold
 
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(uint32_t(max(1, min(253, e + 127))) << 23); }
 // e such that |v| < 2^e, for v >= 0 (128 or more for what is not finite)
@@ -276,8 +275,9 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
 // ------------------------------------------------------------------ the grouped product
 // warps 0, 1, 2, 3: weights, MMA, tokens, zero points; then the unpack warps and the epilogue warps, from multiples of four on (a warp reaches the
 // quarter warp % 4 of the tensor memory's lanes)
-constexpr int kTokenWarp = 2, kZeroWarp = 3, kUnpackWarp = 4, kUnpackWarps = 8, kEpiWarp = kUnpackWarp + kUnpackWarps, kEpiWarps = 8;
-constexpr int kThr = (kEpiWarp + kEpiWarps) * 32;
+constexpr int kTokenWarp = 2, kZeroWarp = 3, kUnpackWarp = 4, kEpiWarps = 8, kMaxSets = 3;
+constexpr int epilogue_warp(int sets) { return kUnpackWarp + 4 * sets; }
+constexpr int product_threads(int sets) { return (epilogue_warp(sets) + kEpiWarps) * 32; }
 constexpr uint32_t kSmem = 227 * 1024;
 
 // The tensor cores cut a running sum off rather than round it, so a chain of n steps of 16 inputs comes out some n 2^-25 too
@@ -286,7 +286,7 @@ constexpr uint32_t kSmem = 227 * 1024;
 template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
-// Shared memory: [gate_up: a tile of activations], the zero points (of two pairs of groups), barriers, the tokens' factors, the token
+// Shared memory: [gate_up: a tile of activations], the zero points (of a pair of groups for each set), barriers, the tokens' factors, the token
 // ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two
 // groups of `cap` tokens and their sums; of 128 tokens one group, as two stages of 66 KB leave the MMAs waiting for the next (1024
 // rows of 8 experts: 173 us against 163; for smaller tiles the second hand-over costs more than it gives, 80 rows: 87
@@ -299,7 +299,7 @@ struct Layout {
 __host__ __device__ constexpr Layout layout(bool gate) {
     Layout l = {};
     l.z = gate ? 16384u : 0u;                     // (128 rows of one term or 64 of two)
-    l.bar = l.z + 2 * kZBytes;
+    l.bar = l.z + kMaxSets * kZBytes;
     l.fac = l.bar + 512;
     l.ring = (l.fac + 2 * 2 * 128 * 4 + 1023u) & ~1023u;
     return l;
@@ -395,13 +395,18 @@ struct Turn {
     __device__ __forceinline__ uint32_t empty() const { return (round - 1u) & 1u; }
 };
 
-// Roles.  Groups are handed over in pairs.  The unpack warps are two sets of four (one warp per quarter of the tensor memory's
-// lanes) on alternate pairs, each with its own place in tensor memory: one set's waits and hand-over, some 900 cycles, fall
-// under the other's arithmetic.  (Both sets on the two groups of one pair wait and work in step: 1650 cycles a pair instead of
-// 1000; twice as many warps doubled the hand-overs' instructions.)
+// Sets of unpack warps: three where tiles are small and that is what bounds the call, as far as the accumulators leave them tensor
+// memory (80 rows of 60 experts: 74 us, with two 76), else two.
+__host__ __device__ constexpr int unpack_sets(int cap, int np) { return cap * np <= 64 ? 3 : 2; }
+
+// Roles.  Groups are handed over in pairs.  The unpack warps are SETS sets of four (one warp per quarter of the tensor memory's
+// lanes) on every SETS-th pair, each with its own place in tensor memory: one set's waits and hand-over, some 900 cycles, fall
+// under the others' arithmetic.  (Two sets on the two groups of one pair wait and work in step: 1650 cycles a pair instead of
+// 1000; twice as many warps to a pair doubled the hand-overs' instructions.)
 // GS: groups of a stage of the token ring.
-template <int NP, bool GATE, int GS>
-__global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams p) {
+template <int NP, bool GATE, int GS, int SETS>
+__global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(const MoeTcParams p) {
+    constexpr int kEpiWarp = epilogue_warp(SETS), kThr = product_threads(SETS);
     extern __shared__ __align__(1024) uint8_t smem[];
     const int K = GATE ? p.w.H : p.w.I, N = GATE ? 2 * p.w.I : p.w.H, G = K >> 7;
     const int R = N / kRows;                               // row tiles of an expert
@@ -411,33 +416,33 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
     // accumulators: bf16 of a tile, fp32 of a pair's two groups side by side; where a token stage's sums begin
     const uint32_t dcols = uint32_t(p.cap) * NP, xoff = dcols * 256u * GS;
-    const int DB = min(kMaxAcc, 256 / int(dcols));
+    const int DB = min(kMaxAcc, (512 - 128 * SETS) / int(dcols));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t* w_full = reinterpret_cast<uint64_t*>(smem + L.bar);
     uint64_t* w_empty = w_full + kMaxWS;
     uint64_t* b_full = w_empty + kMaxWS;
     uint64_t* b_empty = b_full + kMaxStages;
     uint64_t* a_full = b_empty + kMaxStages;
-    uint64_t* a_empty = a_full + kAQ;
-    uint64_t* d_full = a_empty + kAQ;
+    uint64_t* a_empty = a_full + kMaxSets;
+    uint64_t* d_full = a_empty + kMaxSets;
     uint64_t* d_empty = d_full + kMaxAcc;
     uint32_t* tslot = reinterpret_cast<uint32_t*>(d_empty + kMaxAcc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
-    static_assert(2 * (kMaxWS + kMaxStages + kAQ + kMaxAcc) * 8 + 8 <= 512, "barrier area");
+    static_assert(2 * (kMaxWS + kMaxStages + kMaxSets + kMaxAcc) * 8 + 8 <= 512, "barrier area");
     const uint32_t sbase = smem_u32(smem);
 
     if (tid == 0) {
         *abort_flag = 0;
         for (int s = 0; s < WS; ++s) {
             mbar_init(&w_full[s], 1);
-            mbar_init(&w_empty[s], kUnpackWarps / 2 + 1);
+            mbar_init(&w_empty[s], 4 + 1);           // a set and the zero points' warp
         }
         for (int s = 0; s < BS; ++s) {
             mbar_init(&b_full[s], 1);
             mbar_init(&b_empty[s], 1);
         }
-        for (int s = 0; s < kAQ; ++s) {
-            mbar_init(&a_full[s], kUnpackWarps / 2 + 1);
+        for (int s = 0; s < SETS; ++s) {
+            mbar_init(&a_full[s], 4 + 1);
             mbar_init(&a_empty[s], 1);
         }
         for (int s = 0; s < DB; ++s) {
@@ -452,7 +457,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t taddr = *tslot;
+    const uint32_t taddr = *tslot, abase = taddr + 512 - 128 * SETS;
     pdl_wait();
     pdl_launch_dependents();
     // a warp waits as one
@@ -543,7 +548,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                            aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
             const uint32_t blo0 = (((sbase + L.ring) >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
             const uint32_t z = sbase + L.z, zeros = sbase + zeros_at;
-            const uint64_t zd[2] = {plain_desc(z, zeros - z), plain_desc(z + kZBytes, zeros - z - kZBytes)};
+            uint64_t zd[SETS];
+#pragma unroll
+            for (int i = 0; i < SETS; ++i) zd[i] = plain_desc(z + i * kZBytes, zeros - z - i * kZBytes);
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
             auto eight = [&](uint32_t d, uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
@@ -570,7 +577,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 for (int g = 0; g < G; g += 2) {
                     if (!(ok = (NP == 1 || wait(dempty + 8 * ds, dph)) && wait(bfull + 8 * bs, bph) && wait(afull + 8 * as, aph))) break;
                     tc_fence_after();
-                    const uint32_t a = taddr + 256 + as * 128;
+                    const uint32_t a = abase + as * 128;
                     // (fp32: the small second terms first, so that only the first terms' 8 steps cut off from a sum of full size)
                     if (NP == 2) eight(acc, a, blo + rest, idesc, 0u);
                     eight(acc, a, blo, idesc, NP == 2 || g > 0 ? 1u : 0u);
@@ -595,12 +602,14 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     }
                     // the pair's zero points
                     const uint32_t x = sbase + L.ring + bs * bstage + xoff;
-                    mma_ss(acc, as ? zd[1] : zd[0], plain_desc(x, zeros - x), idesc);
+                    mma_ss(acc, as == 0 ? zd[0] : (as == 1 ? zd[1] : zd[SETS - 1]), plain_desc(x, zeros - x), idesc);
                     commit_at(aempty + 8 * as);
                     next_stage();
                     if (NP == 2) hand_over();
-                    as ^= 1;
-                    aph ^= as ^ 1;
+                    if (++as == uint32_t(SETS)) {
+                        as = 0;
+                        aph ^= 1;
+                    }
                 }
                 if (!ok) break;
                 if (NP == 1) hand_over();
@@ -654,11 +663,11 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                     mbar_arrive(&a_full[ta.s]);
                 }
                 tt.next(WS);
-                ta.next(kAQ);
+                ta.next(SETS);
             }
         }
     } else if (warp >= kUnpackWarp && warp < kEpiWarp) {
-        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, every second pair of groups
+        // ---- unpack: the two tiles of tensor-memory lane quarter warp % 4, every SETS-th pair of groups
         const int lq = warp & 3, set = (warp - kUnpackWarp) >> 2, g8 = lane >> 2;
         auto h2 = [](uint32_t v) { return *reinterpret_cast<const __half2*>(&v); };
         auto u2 = [](__half2 v) { return *reinterpret_cast<const uint32_t*>(&v); };
@@ -669,8 +678,8 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
 #pragma unroll
             for (int i = 0; i < 4; ++i) to[i] = at[g8 + 8 * i];
         };
-        const uint32_t aset = taddr + 256 + set * 128 + (uint32_t(32 * lq) << 16);
-        // this set's pairs are number set, set + 2, ... of all: their stage of the weight ring, its parity, the place's parity
+        const uint32_t aset = abase + set * 128 + (uint32_t(32 * lq) << 16);
+        // this set's pairs are number set, set + SETS, ... of all: their stage of the weight ring, its parity, the place's parity
         uint32_t ws = set, wph = 0, aph = 1;
         int skip = set;                                    // pairs of the item that come before this set's next
         const int pairs = (G + 1) >> 1;
@@ -684,9 +693,9 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
             ahead = tile_of(it + step);
             int pr = skip;
 #pragma unroll 1
-            for (; pr < pairs; pr += 2) {
+            for (; pr < pairs; pr += SETS) {
                 const int both = min(2, G - 2 * pr);
-                if (pr + 2 >= pairs && it + step < items) factors(it + step, ahead, rnext);
+                if (pr + SETS >= pairs && it + step < items) factors(it + step, ahead, rnext);
                 if (!(ok = __all_sync(kFull, wait_at(wfull + 8 * ws, wph, abort_flag, p.err)))) break;
                 const uint8_t* wst = smem + wring + ws * kWBytes + 2 * lq * both * kGroupBytes;
                 // a group's words and scales
@@ -736,7 +745,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&a_full[set]);
                 aph ^= 1;
-                ws += 2;
+                ws += SETS;
                 if (ws >= uint32_t(WS)) {
                     ws -= WS;
                     wph ^= 1;
@@ -847,7 +856,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_product_kernel(const MoeTcParams 
                 td.next(DB);
             } else {
                 // the groups' sums
-                constexpr int kSums = kTileTokens<NP> / 32;
+                constexpr int kSums = SETS == 3 ? 1 : kTileTokens<NP> / 32;
                 float sum[kSums][16];
 #pragma unroll
                 for (int i = 0; i < kSums; ++i)
@@ -1010,9 +1019,10 @@ __global__ void __launch_bounds__(kCombineThr) moe_combine_kernel(const MoeTcPar
 }
 
 const void* product_fn(bool bf16, bool gate, int cap) {
-    if (!bf16) return gate ? (const void*)moe_product_kernel<2, true, 2> : (const void*)moe_product_kernel<2, false, 2>;
-    if (stage_groups(cap) == 1) return gate ? (const void*)moe_product_kernel<1, true, 1> : (const void*)moe_product_kernel<1, false, 1>;
-    return gate ? (const void*)moe_product_kernel<1, true, 2> : (const void*)moe_product_kernel<1, false, 2>;
+#define KMR_PRODUCT(np, gs, sets) (gate ? (const void*)moe_product_kernel<np, true, gs, sets> : (const void*)moe_product_kernel<np, false, gs, sets>)
+    if (!bf16) return unpack_sets(cap, 2) == 3 ? KMR_PRODUCT(2, 2, 3) : KMR_PRODUCT(2, 2, 2);
+    return stage_groups(cap) == 1 ? KMR_PRODUCT(1, 1, 2) : KMR_PRODUCT(1, 2, 3);
+#undef KMR_PRODUCT
 }
 
 const void* stage_fn(bool bf16, int H) {
@@ -1065,7 +1075,7 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     if ((e = launch_dependent(stage_fn(bf16, p.w.H), dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
         const size_t smem = kSmem;
-        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), kThr, smem, 1, q, st)) != cudaSuccess) return e;
+        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), product_threads(unpack_sets(p.cap, bf16 ? 1 : 2)), smem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<true> : (const void*)moe_combine_kernel<false>;
     const int cols = kCombineThr * (bf16 ? 8 : 4);
@@ -1082,9 +1092,9 @@ cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_
 
 cudaError_t moe_tc_set_attributes() {
     cudaError_t e;
-    for (int f = 0; f < 3; ++f)
+    for (int f = 0; f < 4; ++f)
         for (int gate = 0; gate < 2; ++gate) {
-            e = cudaFuncSetAttribute(product_fn(f > 0, gate != 0, f == 2 ? 128 : 64), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+            e = cudaFuncSetAttribute(product_fn(f > 1, gate != 0, f == 0 ? 32 : (f == 3 ? 128 : 64)), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
             if (e != cudaSuccess) return e;
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, stage_fn(true, 1024), stage_fn(true, 2048),
