@@ -25,7 +25,6 @@
 
 #include "kmr_int4_mma.cuh"
 #include "kmr_moe.cuh"
-#include "kmr_tc.cuh"
 
 namespace kmr {
 

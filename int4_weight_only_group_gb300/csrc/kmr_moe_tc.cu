@@ -29,8 +29,8 @@
 // tensor memory.
 // Measured (us: plan, stage, gate_up, down, combine; 2048 inputs): 128 tokens of 128 experts of 768, 8 a token: fp32, 16 rows 5,
 // 6, 40, 25, 4 and 509 rows 6, 9.5, 108, 49, 9.5; bf16, 4096 rows 12, 52, 178, 102, 28.  1024 rows of 8 experts of 6144, 2 a
-// token, bf16: 6, 7, 94, 60, 7.  What bounds the products: for tiles of 16 the turning of KMR4 blocks into A (1,900 cycles for each of
-// two sets of warps a pair of groups, 13 bytes of weights a cycle on an SM); for 128 the MMAs' 1,090 cycles a pair and their
+// token, bf16: 6, 7, 94, 60, 7.  What bounds the products: for small tiles the turning of KMR4 blocks into A (2,300 cycles for each of
+// three sets of warps a pair of groups, 14 bytes of weights a cycle on an SM) and its hand-overs; for 128 the MMAs' 1,090 cycles a pair and their
 // hand-overs (1,550 in all); fp32 tiles of 32 to 64 the epilogue, which reads every group's sums.
 #include <cuda_fp16.h>
 
@@ -322,10 +322,12 @@ static_assert(weight_stages(true, 128, 1) >= 3 && weight_stages(true, 64, 2) >= 
 // constant, the lower the address and 1 << 16.
 constexpr uint32_t kSwizzledHi = (2048u >> 4) | (1u << 14) | (2u << 29);
 // No swizzle: 8 rows x 16 bytes side by side for consecutive blocks of 8 rows, the second 16 bytes `further` on.
-__device__ __forceinline__ uint64_t plain_desc(uint32_t addr, uint32_t further) {
-    return uint64_t((addr >> 4) & 0x3FFFu) | (uint64_t((further >> 4) & 0x3FFFu) << 16) | (uint64_t(128 >> 4) << 32) |
-           (uint64_t(1) << 46);
+// The upper half is a constant; the lower one of the next address `step` on, with the same second 16 bytes, is plain_step on.
+constexpr uint32_t kPlainHi = (128u >> 4) | (1u << 14);
+__device__ __forceinline__ uint32_t plain_lo(uint32_t addr, uint32_t second) {
+    return ((addr >> 4) & 0x3FFFu) | (((second - addr) >> 4) & 0x3FFFu) << 16;
 }
+__device__ __forceinline__ constexpr uint32_t plain_step(uint32_t step) { return (step >> 4) - ((step >> 4) << 16); }
 // D += A B^T for one K = 16 step, both in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t taddr, uint64_t ad, uint64_t bd, uint32_t idesc) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, 0, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(taddr),
@@ -547,10 +549,9 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
             const uint32_t bars = smem_u32(b_full), bfull = bars, bempty = bars + 8 * kMaxStages, afull = smem_u32(a_full),
                            aempty = smem_u32(a_empty), dfull = smem_u32(d_full), dempty = smem_u32(d_empty);
             const uint32_t blo0 = (((sbase + L.ring) >> 4) & 0x3FFFu) | (1u << 16), bstep = bstage >> 4;
-            const uint32_t z = sbase + L.z, zeros = sbase + zeros_at;
-            uint64_t zd[SETS];
-#pragma unroll
-            for (int i = 0; i < SETS; ++i) zd[i] = plain_desc(z + i * kZBytes, zeros - z - i * kZBytes);
+            const uint32_t zeros = sbase + zeros_at, zlo0 = plain_lo(sbase + L.z, zeros), xlo0 = plain_lo(sbase + L.ring + xoff, zeros);
+            const uint32_t xstep = plain_step(bstage);
+            uint32_t zlo = zlo0, xlo = xlo0;               // descriptors of the pair's zero points and sums
             uint32_t bs = 0, bph = 0, blo = blo0, as = 0, aph = 0, ds = 0, dph = 1, acc = taddr;
             auto wait = [&](uint32_t bar, uint32_t parity) { return wait_at(bar, parity, abort_flag, p.err); };
             auto eight = [&](uint32_t d, uint32_t a, uint32_t lo, uint32_t idesc, uint32_t begun) {
@@ -584,10 +585,12 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
                     auto next_stage = [&]() {
                         commit_at(bempty + 8 * bs);
                         blo += bstep;
+                        xlo += xstep;
                         if (++bs == uint32_t(BS)) {
                             bs = 0;
                             bph ^= 1;
                             blo = blo0;
+                            xlo = xlo0;
                         }
                     };
                     if (g + 1 < G) {
@@ -601,14 +604,15 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
                         eight(d, a + 64, lo, idesc, 1u);
                     }
                     // the pair's zero points
-                    const uint32_t x = sbase + L.ring + bs * bstage + xoff;
-                    mma_ss(acc, as == 0 ? zd[0] : (as == 1 ? zd[1] : zd[SETS - 1]), plain_desc(x, zeros - x), idesc);
+                    mma_ss(acc, (uint64_t(kPlainHi) << 32) | zlo, (uint64_t(kPlainHi) << 32) | xlo, idesc);
                     commit_at(aempty + 8 * as);
                     next_stage();
                     if (NP == 2) hand_over();
+                    zlo += plain_step(kZBytes);
                     if (++as == uint32_t(SETS)) {
                         as = 0;
                         aph ^= 1;
+                        zlo = zlo0;
                     }
                 }
                 if (!ok) break;
