@@ -78,7 +78,9 @@ struct Eight<true> {
         f[0] = bf16_lo(v.x), f[1] = bf16_hi(v.x), f[2] = bf16_lo(v.y), f[3] = bf16_hi(v.y);
         f[4] = bf16_lo(v.z), f[5] = bf16_hi(v.z), f[6] = bf16_lo(v.w), f[7] = bf16_hi(v.w);
     }
-    __device__ __forceinline__ void set(const float (&f)[8]) { v = make_uint4(cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7])); }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        v = make_uint4(cvt2(f[0], f[1]), cvt2(f[2], f[3]), cvt2(f[4], f[5]), cvt2(f[6], f[7]));
+    }
     __device__ __forceinline__ void store(void* p, size_t at) const { *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + at) = v; }
 };
 // 16 bytes to shared memory, or zeros.
@@ -192,7 +194,10 @@ __global__ void __launch_bounds__(kThr, Cfg<BF16, RT>::CTAS) lora_kernel(const L
             const uint8_t* at = static_cast<const uint8_t*>(from) + (size_t(row0 + xrow) * ld + (real ? col : 0)) * SZ;
 #pragma unroll
             for (int i = 0; i < 16 / XR; ++i)
-                if (mine >> i & 1u) copy16(to + (xrow + XR * i) * ROW + swizzled<BF16, ROW>(xpiece, xrow + XR * i) * 16, at + size_t(XR * i) * ld * SZ, real);
+                if (mine >> i & 1u) {
+                    const int row = xrow + XR * i;
+                    copy16(to + row * ROW + swizzled<BF16, ROW>(xpiece, row) * 16, at + size_t(XR * i) * ld * SZ, real);
+                }
         };
         auto copy_in = [&](int u, int stage) {
             if (u < ke) {
@@ -204,7 +209,8 @@ __global__ void __launch_bounds__(kThr, Cfg<BF16, RT>::CTAS) lora_kernel(const L
 #pragma unroll
                 for (int i = 0; i < RP / AR; ++i) {
                     const int n = arow + AR * i;
-                    if (n < rank_a) copy16(to + F::XBYTES + n * AROW + (BF16 ? swizzled<BF16, AROW>(apiece, n) : apiece) * 16, at + size_t(AR * i) * p.K, real);
+                    const int c = BF16 ? swizzled<BF16, AROW>(apiece, n) : apiece;
+                    if (n < rank_a) copy16(to + F::XBYTES + n * AROW + c * 16, at + size_t(AR * i) * p.K, real);
                 }
             }
             commit_copies();

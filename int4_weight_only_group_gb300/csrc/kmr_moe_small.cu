@@ -79,7 +79,8 @@ struct __align__(16) Tile {
 // ------------------------------------------------------------------ operands
 // The rows wait in shared memory as B fragments: per (row, group of 128) the four quarters t of the lanes, each the 16 registers of
 // its 8 steps (inputs 8 i + 2 t and + 1 in register i), in 16-byte pieces that two quarters exchange so that a load meets no
-// bank twice; SPLIT: the remainders behind them.  An item of zeros stands last.  Beside them, for each term, its sum and 1 / sigma, as the codes' 2^-9 needs them.
+// bank twice; SPLIT: the remainders behind them.  An item of zeros stands last.  Beside them, for each term, its sum and 1 / sigma,
+// as the codes' 2^-9 needs them.
 template <bool SPLIT>
 constexpr int kItemBytes = SPLIT ? 512 : 256;
 template <typename IN, bool SPLIT>
@@ -514,7 +515,8 @@ int gate_tiles(const MoeView& w, int S, int ctas) {      // the longest sequence
 bool moe_small_fits(const MoeView& w, bool bf16, int T, int k) {
     const int S = T * k;
     int st, b;
-    return S <= kMoeSmallPlaces && T <= kMoeSmallTokens && (long long)S * w.H * w.I * 3 <= kMoeSmallWeights && plan_ring(false, bf16, w.H, T, gate_tiles(w, S, kMoeSmallCtas), &st, &b) <= kSmem &&
+    if (S > kMoeSmallPlaces || T > kMoeSmallTokens || (long long)S * w.H * w.I * 3 > kMoeSmallWeights) return false;
+    return plan_ring(false, bf16, w.H, T, gate_tiles(w, S, kMoeSmallCtas), &st, &b) <= kSmem &&
            plan_ring(true, bf16, w.I, S, distinct_of(w, S), &st, &b) <= kSmem;
 }
 

@@ -22,16 +22,17 @@
 //     (|x| max |up row|) bounds it from the row's norm and per-expert constants.  The bound is loose by 2^7 to 2^13, which
 //     fp16's range absorbs: the values stay far above its subnormals.
 //
-// Each CTA is persistent and warp-specialised: a weight producer and a token producer (cp.async.bulk rings), eight warps that turn
-// KMR4 blocks into A in tensor memory (kmr_tcgemm.cu describes that layout), one that lays out their zero points, one thread that
-// issues the MMAs, eight epilogue warps on the accumulators that are done (for fp32 they also add up the groups' sums).  Every wait
-// is bounded; a timeout records KMR_ERR_DEVICE_TIMEOUT, skips the remaining work, drains the copies in flight and frees
-// tensor memory.
-// Measured (us: plan, stage, gate_up, down, combine; 2048 inputs): 128 tokens of 128 experts of 768, 8 a token: fp32, 16 rows 5,
-// 6, 40, 25, 4 and 509 rows 6, 9.5, 108, 49, 9.5; bf16, 4096 rows 12, 52, 178, 102, 28.  1024 rows of 8 experts of 6144, 2 a
-// token, bf16: 6, 7, 94, 60, 7.  What bounds the products: for small tiles the turning of KMR4 blocks into A (2,300 cycles for each of
-// three sets of warps a pair of groups, 14 bytes of weights a cycle on an SM) and its hand-overs; for 128 the MMAs' 1,090 cycles a pair and their
-// hand-overs (1,550 in all); fp32 tiles of 32 to 64 the epilogue, which reads every group's sums.
+// Each CTA is persistent and warp-specialised: a weight producer and a token producer (cp.async.bulk rings), eight or twelve warps
+// that turn KMR4 blocks into A in tensor memory (kmr_tcgemm.cu describes that layout), one that lays out their zero points, one
+// thread that issues the MMAs, eight epilogue warps on the accumulators that are done (for fp32 they also add up the groups'
+// sums).  Every wait is bounded; a timeout records KMR_ERR_DEVICE_TIMEOUT, skips the remaining work, drains the copies in
+// flight and frees tensor memory.
+//
+// Measured (us: plan, stage, gate_up, down, combine; hidden 2048).  128 experts of 768, 8 a token: 16 rows fp32 5, 6, 40, 25, 4;
+// 509 rows fp32 6, 9.5, 108, 49, 9.5; 4096 rows bf16 12, 52, 178, 102, 28.  8 experts of 6144, 2 a token, bf16: 1024 rows 6, 7, 94,
+// 60, 7.  What bounds the products: for small tiles the turning of KMR4 blocks into A (2,300 cycles for each of three sets of
+// warps a pair of groups, 14 bytes of weights a cycle on an SM) and its hand-overs; for tiles of 128 the MMAs' 1,090 cycles a
+// pair and theirs (1,550 in all); for fp32 tiles of 32 to 64 the epilogue, which reads every group's sums.
 #include <cuda_fp16.h>
 
 #include <type_traits>
@@ -1078,8 +1079,8 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(stage_fn(bf16, p.w.H), dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
     for (const bool gate : {true, false}) {
-        const size_t smem = kSmem;
-        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), product_threads(unpack_sets(p.cap, bf16 ? 1 : 2)), smem, 1, q, st)) != cudaSuccess) return e;
+        const int threads = product_threads(unpack_sets(p.cap, bf16 ? 1 : 2));
+        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), threads, kSmem, 1, q, st)) != cudaSuccess) return e;
     }
     const void* combine = bf16 ? (const void*)moe_combine_kernel<true> : (const void*)moe_combine_kernel<false>;
     const int cols = kCombineThr * (bf16 ? 8 : 4);
@@ -1098,7 +1099,8 @@ cudaError_t moe_tc_set_attributes() {
     cudaError_t e;
     for (int f = 0; f < 4; ++f)
         for (int gate = 0; gate < 2; ++gate) {
-            e = cudaFuncSetAttribute(product_fn(f > 1, gate != 0, f == 0 ? 32 : (f == 3 ? 128 : 64)), cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+            const void* fn = product_fn(f > 1, gate != 0, f == 0 ? 32 : (f == 3 ? 128 : 64));
+            e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
             if (e != cudaSuccess) return e;
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, stage_fn(true, 1024), stage_fn(true, 2048),
