@@ -390,7 +390,8 @@ int kmr_moe_prepare(const kmr_moe* moe, void* stream);
  *   workspace device memory, 16-byte aligned, kmr_moe_experts_workspace_size(moe, dtype, T, top_k) bytes or more (0 for
  *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
  *             workspaces of their own.
- * Products are exact and sums are held in fp32, whatever the type; between gate_up and down the activations keep 22 bits (fp32)
+ * Products are exact and sums are held in fp32, whatever the type (more than a few tokens: where a weight row's scales lie within
+ * 2^7 of its largest; below, to 2^-20 of its largest weight); between gate_up and down the activations keep 22 bits (fp32)
  * or 11 (bf16).  A few tokens (up to 32 places T top_k of up to 16 tokens, whose experts taken each by itself have up to 3 x 2^26
  * weights) are two launches, more are five for every 32768 places; within either form a token's result does not depend
  * on the other tokens.  A workspace of the size for T tokens does for fewer.  top_k 1..32.  Errors:
