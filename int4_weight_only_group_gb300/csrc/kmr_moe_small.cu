@@ -316,6 +316,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
     __syncthreads();
     const int n = n_tiles, columns = min(most, CAP), di = kWarps / P, dw = kWarps % P;
     const Turn t0 = first_turn(warp, P);
+    bool ok = true;                                     // (a wait that ran out: no other is made)
     for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
         for (int c0 = 0; c0 < most; c0 += CAP) {
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
                 if (cols <= 0) continue;
                 int at = 0;                             // column's token
                 if (p.T > 1) at = __shfl_sync(kFull, token, nth_bit(places, c0 + min(col, cols - 1)));
-                if (!__all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err))) continue;
+                if (!(ok = ok && __all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err)))) continue;
                 float acc[4];
                 tile_product<SPLIT>(ring.data + size_t(s0 + t.i) * ring.tile_bytes, staged, fold, col < cols ? at : p.T, p.T, G, t.w, lane, acc);
                 const int g = lane >> 2, c = 2 * (lane & 3);
@@ -423,12 +424,13 @@ __global__ void __launch_bounds__(kThr, 1) moe_down_kernel(const MoeSmallParams 
     __syncthreads();
     const int n = experts, di = kWarps / P, dw = kWarps % P;
     const Turn t0 = first_turn(warp, P);
+    bool ok = true;                                     // (a wait that ran out: no other is made)
     for (int b0 = 0, s0 = 0, phase = 0; b0 < n; b0 += p.batch) {
         const int nb = min(p.batch, n - b0);
         for (Turn t = t0; t.i < nb; next_turn(t, P, di, dw)) {
             const uint32_t places = list[b0 + t.i].places;
             const int used = __popc(places);
-            if (!__all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err))) continue;
+            if (!(ok = ok && __all_sync(kFull, mbar_wait(&ring.full[s0 + t.i], uint32_t(phase), p.err)))) continue;
             for (int c0 = 0; c0 < used; c0 += CAP) {
                 const int col = SPLIT ? (lane >> 2) & 3 : lane >> 2;
                 int place = col == 0 ? __ffs(places) - 1 : -1;
