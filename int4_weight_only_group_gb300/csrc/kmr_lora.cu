@@ -6,7 +6,7 @@
 //     partials meet through distributed shared memory in rank order, and each CTA adds its share of the N columns: x, base
 //     and y pass through once, v never leaves the chip, one launch.
 //   * Every warp has its own columns and streams them, rows of x (or base) and the same columns of A (or rows of B), through
-//     a ring of its own by 16-byte cp.async, two to four units of 128 bytes a row deep: nothing but a wait for its own copies
+//     a ring of its own by 16-byte cp.async, two to four units of 64 or 128 bytes a row deep: nothing but a wait for its own copies
 //     stands between a warp and its products.  (Loads into registers, eight bytes a lane, held up by the L1's tags: 4077 rows
 //     42 us against 27.5.  A ring per CTA, fed by one warp with bulk copies of 512 bytes or by four with cp.async: 52 and 45
 //     us; a bulk copy costs the copy engine some 60 cycles, and 16 warps that all wait for each chunk proceed in step.)
@@ -95,7 +95,8 @@ __device__ __forceinline__ void wait_copies() {
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A warp's ring: `stages` units, each 16 rows of x (or base) and the same columns of A (or rows of B).  Wide rows of A (many ranks)
-// take shorter units, so that two CTAs fit to an SM as far as they can.
+// take shorter units, so that two CTAs fit to an SM as far as they can.  (Short units for all and four CTAs: 4077 rows 30.5 us
+// instead of 27.5; a unit's fixed instructions count for more than the warps that hide their latency.)
 template <bool BF16, int RT>
 struct Cfg {
     static constexpr int RP = RT * 8;                                   // ranks, padded
