@@ -352,9 +352,11 @@ __global__ void __launch_bounds__(kThr, 1) moe_gate_up_kernel(const MoeSmallPara
                     a = __fadd_rn(a, __shfl_xor_sync(kFull, a, 1));
                     a = __fadd_rn(a, __shfl_xor_sync(kFull, a, 2));
                     const float up = __shfl_sync(kFull, a, (lane + 16) & 31);
-                    if (lane < 16 && w == 0) p.act[size_t(nth_bit(t.places, c0 + c)) * p.w.I + t.row * 8 + r] = silu_mul(a, up);
+                    const int place = c0 + c == 0 ? __ffs(t.places) - 1 : nth_bit(t.places, c0 + c);
+                    if (lane < 16 && w == 0) p.act[size_t(place) * p.w.I + t.row * 8 + r] = silu_mul(a, up);
                 }
             }
+            if (c0 + CAP >= most && b0 + nb >= n) return;
             __syncthreads();
         }
         if (warp == 0) {
