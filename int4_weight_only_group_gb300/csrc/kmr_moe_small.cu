@@ -17,7 +17,7 @@
 //     sums keep single precision.  Per group, y += (s D + z X) / sigma with D = sum (q - 8) x and X = sum x.
 //   * partial sums meet in shared memory and are added in a fixed order that hangs on K alone: a token's result does not
 //     change with the other tokens of the call.
-// Measured: one token, 8 of 128 experts of 2048 x 768 (20 MB), fp32: 14.9 us, gate_up 8 (its first weights arrive after 3.4: the
+// Measured: one token, 8 of 128 experts of 2048 x 768 (20 MB), fp32: 14.8 us, gate_up 8 (its first weights arrive after 3.4: the
 // wait for the ids, the plan, HBM), down 5, launches; four tokens (32 places) 43 us.  With 16 warps, each of which made its own
 // fragments and took 8 off the codes (9 instructions for a step's A instead of 5): 25.7.  A product of one warp takes
 // 1,400 cycles with 16 warps at work, for some 150 instructions and 8 MMAs (64 cycles): latency, which 32 warps hide better.
@@ -85,54 +85,54 @@ template <bool SPLIT>
 constexpr int kItemBytes = SPLIT ? 512 : 256;
 template <typename IN, bool SPLIT>
 __device__ __forceinline__ void stage_rows(uint8_t* to, float4* fold, const IN* x, int items) {
-    constexpr int kAtOnce = 2;
-    const int lane = threadIdx.x & 31, i = lane >> 1;
-    const int at = (lane & 1) * 128 + ((((i >> 2) ^ (lane & 1)) << 2) + (i & 3)) * 4;     // quarter 2 (lane & 1), register i
+    const int lane = threadIdx.x & 31, i = lane & 15;      // half a warp to an item, a lane its inputs 8 i .. 8 i + 7: register i of each quarter
     if (threadIdx.x >= kThr - 32) {
         reinterpret_cast<uint4*>(to + size_t(items) * kItemBytes<SPLIT>)[lane & (kItemBytes<SPLIT> / 16 - 1)] = make_uint4(0u, 0u, 0u, 0u);
         fold[items] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    for (int i0 = threadIdx.x >> 5; i0 < items; i0 += kWarps * kAtOnce) {
-        float4 v[kAtOnce];
-#pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            const size_t src = size_t(min(i0 + q * kWarps, items - 1)) * 128 + lane * 4;
-            if constexpr (sizeof(IN) == 4) {
-                v[q] = __ldcg(reinterpret_cast<const float4*>(x + src));
-            } else {
-                const uint2 r = __ldcg(reinterpret_cast<const uint2*>(x + src));
-                v[q] = make_float4(bf16_lo(r.x), bf16_hi(r.x), bf16_lo(r.y), bf16_hi(r.y));
-            }
+    for (int i0 = (threadIdx.x >> 5) * 2; i0 < items; i0 += kWarps * 2) {
+        const int item = min(i0 + (lane >> 4), items - 1);
+        float r[8];
+        if constexpr (sizeof(IN) == 4) {
+            const float4* src = reinterpret_cast<const float4*>(x + size_t(item) * 128 + i * 8);
+            const float4 v0 = __ldcg(src), v1 = __ldcg(src + 1);
+            r[0] = v0.x, r[1] = v0.y, r[2] = v0.z, r[3] = v0.w, r[4] = v1.x, r[5] = v1.y, r[6] = v1.z, r[7] = v1.w;
+        } else {
+            const uint4 v = __ldcg(reinterpret_cast<const uint4*>(x + size_t(item) * 128 + i * 8));
+            r[0] = bf16_lo(v.x), r[1] = bf16_hi(v.x), r[2] = bf16_lo(v.y), r[3] = bf16_hi(v.y);
+            r[4] = bf16_lo(v.z), r[5] = bf16_hi(v.z), r[6] = bf16_lo(v.w), r[7] = bf16_hi(v.w);
         }
+        uint32_t m = 0u;                                   // (bits of non-negative numbers order like integers, NaN above all)
 #pragma unroll
-        for (int q = 0; q < kAtOnce; ++q) {
-            const int item = i0 + q * kWarps;
-            if (item >= items) break;
-            const float m = fmaxf(fmaxf(fabsf(v[q].x), fabsf(v[q].y)), fmaxf(fabsf(v[q].z), fabsf(v[q].w)));
-            float sig, isg;
-            pow2_scale(__reduce_max_sync(kFull, __float_as_uint(m)), sig, isg);
-            float r[4] = {__fmul_rn(v[q].x, sig), __fmul_rn(v[q].y, sig), __fmul_rn(v[q].z, sig), __fmul_rn(v[q].w, sig)};
-            float X[2] = {0.f, 0.f};
-            uint8_t* dst = to + size_t(item) * kItemBytes<SPLIT> + at;
+        for (int q = 0; q < 8; ++q) m = max(m, __float_as_uint(fabsf(r[q])));
 #pragma unroll
-            for (int term = 0; term < (SPLIT ? 2 : 1); ++term) {
-                const __half2 a = __floats2half2_rn(r[0], r[1]), b = __floats2half2_rn(r[2], r[3]);
-                const float2 fa = __half22float2(a), fb = __half22float2(b);
-                X[term] = __fadd_rn(__fadd_rn(fa.x, fa.y), __fadd_rn(fb.x, fb.y));
-                r[0] = __fsub_rn(r[0], fa.x);
-                r[1] = __fsub_rn(r[1], fa.y);
-                r[2] = __fsub_rn(r[2], fb.x);
-                r[3] = __fsub_rn(r[3], fb.y);
-                *reinterpret_cast<__half2*>(dst + term * 256) = a;
-                *reinterpret_cast<__half2*>(dst + term * 256 + 64) = b;
+        for (int o = 8; o > 0; o >>= 1) m = max(m, __shfl_xor_sync(kFull, m, o));
+        float sig, isg;
+        pow2_scale(m, sig, isg);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) r[q] = __fmul_rn(r[q], sig);
+        float X[2] = {0.f, 0.f};
+        uint8_t* dst = to + size_t(item) * kItemBytes<SPLIT> + (i & 3) * 4;
+#pragma unroll
+        for (int term = 0; term < (SPLIT ? 2 : 1); ++term) {
+            float part[4];
+#pragma unroll
+            for (int t = 0; t < 4; ++t) {
+                const __half2 h = __floats2half2_rn(r[2 * t], r[2 * t + 1]);
+                const float2 f = __half22float2(h);
+                part[t] = __fadd_rn(f.x, f.y);
+                r[2 * t] = __fsub_rn(r[2 * t], f.x);
+                r[2 * t + 1] = __fsub_rn(r[2 * t + 1], f.y);
+                *reinterpret_cast<__half2*>(dst + term * 256 + t * 64 + (((i >> 2) ^ (t >> 1)) << 4)) = h;
             }
-            // the lower half of the lanes sums the first terms, the upper half the remainders
-            float sum = __fadd_rn(lane < 16 ? X[0] : X[1], __shfl_xor_sync(kFull, lane < 16 ? X[1] : X[0], 16));
-#pragma unroll
-            for (int o = 8; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
-            if ((lane & 15) == 0) *reinterpret_cast<float2*>(reinterpret_cast<float*>(fold + item) + (lane >> 3)) =
-                    make_float2(sum * 0x1p-9f, isg * 0x1p9f);      // (the 2^-9 of the codes; isg is 2^114 at the most)
+            X[term] = __fadd_rn(__fadd_rn(part[0], part[1]), __fadd_rn(part[2], part[3]));
         }
+        // the lower lanes of the half sum the first terms, the upper ones the remainders
+        float sum = __fadd_rn(i < 8 ? X[0] : X[1], __shfl_xor_sync(kFull, i < 8 ? X[1] : X[0], 8));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(kFull, sum, o));
+        if ((i & 7) == 0)
+            reinterpret_cast<float2*>(fold + item)[i >> 3] = make_float2(sum * 0x1p-9f, isg * 0x1p9f);      // (isg is 2^114 at the most)
     }
 }
 
