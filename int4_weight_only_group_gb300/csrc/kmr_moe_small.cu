@@ -18,8 +18,8 @@
 //   * partial sums meet in shared memory and are added in a fixed order that hangs on K alone: a token's result does not
 //     change with the other tokens of the call.
 // Measured: one token, 8 of 128 experts of 2048 x 768 (20 MB), fp32: 14.8 us, gate_up 8 (its first weights arrive after 3.4: the
-// wait for the ids, the plan, HBM), down 5, launches; four tokens (32 places) 43 us.  With 16 warps, each of which made its own
-// fragments and took 8 off the codes (9 instructions for a step's A instead of 5): 25.7.  A product of one warp takes
+// wait for the ids, the plan, HBM), down 5, launches; four tokens (32 places) 43 us.  With 16 warps, each of which planned
+// the call, made its own fragments and divided for every tile: 25.7.  A product of one warp takes
 // 1,400 cycles with 16 warps at work, for some 150 instructions and 8 MMAs (64 cycles): latency, which 32 warps hide better.
 #include <cuda_fp16.h>
 
