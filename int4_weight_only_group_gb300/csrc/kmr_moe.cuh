@@ -64,19 +64,19 @@ struct MoeTcParams {
     int4* tiles;                             // (expert, first position, tokens with padding, tokens)
     int32_t* pos;                            // [T][k]: the place's position, or -1
     float* isx;                              // [P] 1 / scale of the position's inputs
-    float* sact;                             // [P] scale of its activations
+    float* isa;                              // [P] 1 / scale of its activations
     float* sout;                             // [P] bf16: scale of its result while it waits for the sum
     size_t blocks;                           // P / 8
     uint8_t* xs;                             // staged inputs
     uint8_t* as;                             // staged activations
-    void* out;                               // [P][H]: fp16 (bf16) or fp32
+    void* out;                               // [P][I] fp32: activations; then [P][H]: results, fp16 (bf16) or fp32
     void* y;                                 // [T][H]
     int resid;
     int* err;
 };
 // Byte offsets into the workspace (the tile count comes first), and the blocks of 8 positions.
 struct MoeTcSizes {
-    size_t tiles, pos, isx, sact, sout, xs, as, out, total, blocks;
+    size_t tiles, pos, isx, isa, sout, xs, as, out, total, blocks;
 };
 int moe_tc_cap(long long places, int E, bool bf16);
 MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k);

@@ -130,7 +130,7 @@ extern "C" int kmr_moe_experts(const kmr_moe* moe, const void* x, int dtype, con
     p.tiles = reinterpret_cast<int4*>(ws + z.tiles);
     p.pos = reinterpret_cast<int32_t*>(ws + z.pos);
     p.isx = reinterpret_cast<float*>(ws + z.isx);
-    p.sact = reinterpret_cast<float*>(ws + z.sact);
+    p.isa = reinterpret_cast<float*>(ws + z.isa);
     p.sout = reinterpret_cast<float*>(ws + z.sout);
     p.blocks = z.blocks;
     p.xs = ws + z.xs;

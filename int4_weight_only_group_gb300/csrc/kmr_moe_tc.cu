@@ -4,7 +4,8 @@
 //   plan     counts the places of every expert and gives each a position; an expert's positions are padded to a multiple
 //            of 16 and cut into tiles of at most `cap` (16..128) tokens
 //   stage    token rows as fp16 into the tiles' operand layout (a copy per place)
-//   gate_up  D = A B^T per (tile, 128 packed weight rows), silu(gate) * up, staged again for
+//   gate_up  D = A B^T per (tile, 128 packed weight rows), silu(gate) * up, in fp32
+//   act      the activations as fp16 in the operand layout, at the power of two of their row's largest
 //   down     the same product, a row for every place
 //   combine  y[t] = sum_j weights[t, j] * row of place (t, j), in the order of the places: no atomics on values
 //
@@ -18,9 +19,10 @@
 //     every two groups: z rho 2^6 against X 2^-6 for every 64 inputs, X in two fp16 terms.
 //   * B = x sigma (a power of two per row): exact for bf16 inputs, two terms (the fp16 rounding and what it left, two
 //     MMAs on the same A) for fp32 ones.  So products are exact and sums are fp32 in both types.
-//   * the activation's scale must be known before its row is complete: |silu(g) u| <= |g| |u| <= (|x| max |gate row|)
-//     (|x| max |up row|) bounds it from the row's norm and per-expert constants.  The bound is loose by 2^7 to 2^13, which
-//     fp16's range absorbs: the values stay far above its subnormals.
+//   * the accumulators of a tile take a row's whole sum, so an activation row has one scale: that of its largest value, which is
+//     known when all of its tiles are.  Hence act, a pass over the rows by itself.  (A scale from bounds, |silu(g) u| <= (|x|
+//     max |gate row|) (|x| max |up row|), needs no pass but is loose by the spread of the rows' sizes twice over, and by
+//     exp(-g) where the gates are shut: one gate and one up row of 256 times the others' size, fp32: 1.6e-2 of the result.)
 //
 // Each CTA is persistent and warp-specialised: a weight producer and a token producer (cp.async.bulk rings), eight or twelve warps
 // that turn KMR4 blocks into A in tensor memory (kmr_tcgemm.cu describes that layout), one that lays out their zero points, one
@@ -157,13 +159,48 @@ __device__ __forceinline__ size_t atom_at(int h, int term, int np, size_t blocks
 }
 __device__ __forceinline__ size_t sums_at(int K, int np, size_t blocks) { return size_t(K / 128) * blocks * np * 2048; }
 __device__ __forceinline__ uint32_t piece(int row, int c) { return uint32_t(row * 128 + ((c ^ row) << 4)); }
-// Sum number h (of 64 inputs) of a row: its two terms, in the row's pieces of 8 numbers (`stride` bytes apart) for each pair of groups.
-__device__ __forceinline__ void put_sum(void* row, int h, float X, size_t stride = 16) {
+// Sum number h (of 64 inputs) of a row: its two terms, in the row's pieces of 8 numbers for each pair of groups.
+__device__ __forceinline__ void put_sum(void* row, int h, float X) {
     const float x = X * 0.015625f;
     const __half hi = __float2half_rn(x);
-    __half* to = reinterpret_cast<__half*>(static_cast<uint8_t*>(row) + (h >> 2) * stride) + ((h >> 1) & 1) * 4 + (h & 1);
+    __half* to = reinterpret_cast<__half*>(static_cast<uint8_t*>(row) + (h >> 2) * 16) + ((h >> 1) & 1) * 4 + (h & 1);
     to[0] = hi;
     to[2] = __float2half_rn(__fsub_rn(x, __half2float(hi)));
+}
+
+// A lane's four inputs (k = 4 x its number), scaled, as NP terms: the 8 bytes of a piece that it writes (a 16-byte piece holds inputs
+// 0, 1, 8, 9, 2, 3, 10, 11 (or 4 more) of its 16: two lanes write its halves), and the sum of its 16 lanes' 64.  By whole warps.
+template <int NP>
+__device__ __forceinline__ float stage4(const float (&a)[4], int m4, uint2 (&out)[NP]) {
+    auto h2u = [](__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); };
+    float X = 0.f;
+    float r[4] = {a[0], a[1], a[2], a[3]};
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        const __half2 h0 = __floats2half2_rn(r[0], r[1]), h1 = __floats2half2_rn(r[2], r[3]);
+        const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
+        X = __fadd_rn(X, __fadd_rn(__fadd_rn(f0.x, f0.y), __fadd_rn(f1.x, f1.y)));
+        r[0] = __fsub_rn(r[0], f0.x);
+        r[1] = __fsub_rn(r[1], f0.y);
+        r[2] = __fsub_rn(r[2], f1.x);
+        r[3] = __fsub_rn(r[3], f1.y);
+        const uint32_t wa = h2u(h0), wb = h2u(h1);
+        const uint32_t got = __shfl_xor_sync(kFull, m4 < 2 ? wb : wa, 2);
+        out[q] = m4 < 2 ? make_uint2(wa, got) : make_uint2(got, wb);
+    }
+#pragma unroll
+    for (int o = 1; o < 16; o <<= 1) X = __fadd_rn(X, __shfl_xor_sync(kFull, X, o));
+    return X;
+}
+// Where they go: inputs k .. k + 3 of the row at position `at`.
+__device__ __forceinline__ size_t four_at(int k, int at, int np, size_t blocks) {
+    return atom_at(k >> 6, 0, np, blocks, at >> 3) + piece(at & 7, ((k & 63) >> 4) * 2 + ((k >> 2) & 1)) + ((k & 8) ? 8 : 0);
+}
+// A row's sums, from `sums` (put_sum's) to position `at`: pair number pr.
+__device__ __forceinline__ void store_sums(uint8_t* to, const void* sums, int pr, int K, int np, size_t blocks, int at) {
+    uint4 v = reinterpret_cast<const uint4*>(sums)[pr];
+    if (2 * pr + 1 == K >> 7) v.z = v.w = 0u;              // (the half of the last pair that an odd number of groups leaves)
+    *reinterpret_cast<uint4*>(to + sums_at(K, np, blocks) + (size_t(pr) * blocks + (at >> 3)) * 128 + (at & 7) * 16) = v;
 }
 
 // ------------------------------------------------------------------ stage
@@ -211,37 +248,18 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
     pow2_scale(__float_as_uint(m), sig, isg);
     float ss = 0.f;
     const size_t blocks = p.blocks;
-    auto h2u = [](__half2 h) { return *reinterpret_cast<const uint32_t*>(&h); };
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
         const int k4 = tid + i * kStageThr;
         if (k4 >= K4) break;                                        // (whole warps: K4 is a multiple of 32)
         const int k = k4 * 4, m4 = k4 & 3;
         const float a[4] = {__fmul_rn(v[i].x, sig), __fmul_rn(v[i].y, sig), __fmul_rn(v[i].z, sig), __fmul_rn(v[i].w, sig)};
-        float X = 0.f;
         uint2 out[NP];
-        float r[4] = {a[0], a[1], a[2], a[3]};
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            const __half2 h0 = __floats2half2_rn(r[0], r[1]), h1 = __floats2half2_rn(r[2], r[3]);
-            const float2 f0 = __half22float2(h0), f1 = __half22float2(h1);
-            X = __fadd_rn(X, __fadd_rn(__fadd_rn(f0.x, f0.y), __fadd_rn(f1.x, f1.y)));
-            r[0] = __fsub_rn(r[0], f0.x);
-            r[1] = __fsub_rn(r[1], f0.y);
-            r[2] = __fsub_rn(r[2], f1.x);
-            r[3] = __fsub_rn(r[3], f1.y);
-            // a 16-byte piece holds inputs 0, 1, 8, 9, 2, 3, 10, 11 (or 4 more) of its 16: two lanes write its halves
-            const uint32_t wa = h2u(h0), wb = h2u(h1);
-            const uint32_t got = __shfl_xor_sync(kFull, m4 < 2 ? wb : wa, 2);
-            out[q] = m4 < 2 ? make_uint2(wa, got) : make_uint2(got, wb);
-        }
+        const float X = stage4<NP>(a, m4, out);
 #pragma unroll
         for (int q = 0; q < 4; ++q) ss = __fmaf_rn(a[q], a[q], ss);
-#pragma unroll
-        for (int o = 1; o < 16; o <<= 1) X = __fadd_rn(X, __shfl_xor_sync(kFull, X, o));
         for (int j = 0; j < n; ++j) {
-            const int at = pos[j], row = at & 7;
-            uint8_t* to = p.xs + atom_at(k >> 6, 0, NP, blocks, at >> 3) + piece(row, ((k & 63) >> 4) * 2 + (m4 & 1)) + (m4 < 2 ? 0 : 8);
+            uint8_t* to = p.xs + four_at(k, pos[j], NP, blocks);
 #pragma unroll
             for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * blocks * 2048) = out[q];
         }
@@ -250,24 +268,17 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
     ss = warp_sum(ss);
     if (lane == 0) red[1][warp] = ss;
     __syncthreads();
-    // (the half of the last pair that an odd number of groups leaves is zero)
-    for (int i = tid; i < n * pairs_of(K); i += kStageThr) {
-        const int j = i / pairs_of(K), pr = i % pairs_of(K), at = pos[j];
-        uint4 v = reinterpret_cast<const uint4*>(sums)[pr];
-        if (2 * pr + 1 == K >> 7) v.z = v.w = 0u;
-        *reinterpret_cast<uint4*>(p.xs + sums_at(K, NP, blocks) + (size_t(pr) * blocks + (at >> 3)) * 128 + (at & 7) * 16) = v;
-    }
+    for (int i = tid; i < n * pairs_of(K); i += kStageThr) store_sums(p.xs, sums, i % pairs_of(K), K, NP, blocks, pos[i / pairs_of(K)]);
     if (tid < p.k) {
         const int at = p.pos[size_t(t) * p.k + tid];
         if (at < 0) return;
         ss = red[1][0];
         for (int w = 1; w < kStageThr / 32; ++w) ss = __fadd_rn(ss, red[1][w]);
-        // |x|, and the bound of the place's activations: below 2^15 once scaled
+        // |x|, and a bound of the place's activations
         const int e = p.ids[size_t(t) * p.k + tid];
         const int ex = above(sqrtf(ss)) + above(isg) - 1;
         p.isx[at] = isg;
         const int ea = 2 * ex + above(p.norms[3 * e]) + above(p.norms[3 * e + 1]);
-        p.sact[at] = pow2(15 - ea);
         // bf16: |down act| <= |act| max |row|, |act| <= sqrt(I) 2^ea
         p.sout[at] = pow2(15 - (ea + (33 - __clz(p.w.I)) / 2 + above(p.norms[3 * e + 2])));
     }
@@ -287,7 +298,7 @@ constexpr uint32_t kSmem = 227 * 1024;
 template <int NP>
 constexpr int kTileTokens = NP == 2 ? 64 : 128;
 
-// Shared memory: [gate_up: a tile of activations], the zero points (of a pair of groups for each set), barriers, the tokens' factors, the token
+// Shared memory: the zero points (of a pair of groups for each set), barriers, the tokens' factors, the token
 // ring, 2 KB of zeros (behind whatever needs them as its second 16 bytes), the weight ring.  A stage of the token ring holds two
 // groups of `cap` tokens and their sums; of 128 tokens one group, as two stages of 66 KB leave the MMAs waiting for the next (1024
 // rows of 8 experts: 173 us against 163; for smaller tiles the second hand-over costs more than it gives, 80 rows: 87
@@ -295,11 +306,10 @@ constexpr int kTileTokens = NP == 2 ? 64 : 128;
 constexpr uint32_t kZBytes = kRows * 16;
 constexpr int kMaxStages = 8, kMaxWS = 8;
 struct Layout {
-    uint32_t tile, z, bar, fac, ring;
+    uint32_t z, bar, fac, ring;
 };
-__host__ __device__ constexpr Layout layout(bool gate) {
+__host__ __device__ constexpr Layout layout() {
     Layout l = {};
-    l.z = gate ? 16384u : 0u;                     // (128 rows of one term or 64 of two)
     l.bar = l.z + kMaxSets * kZBytes;
     l.fac = l.bar + 512;
     l.ring = (l.fac + 2 * 2 * 128 * 4 + 1023u) & ~1023u;
@@ -313,11 +323,11 @@ __host__ __device__ constexpr int token_stages(int cap, int np) {
     const int n = int(72u * 1024u / stage_bytes(cap, np)), least = stage_groups(cap) == 1 ? 4 : 2;
     return n < least ? least : (n > kMaxStages ? kMaxStages : n);
 }
-__host__ __device__ constexpr int weight_stages(bool gate, int cap, int np) {
-    const int n = int((kSmem - layout(gate).ring - token_stages(cap, np) * stage_bytes(cap, np) - kZBytes) / kWBytes);
+__host__ __device__ constexpr int weight_stages(int cap, int np) {
+    const int n = int((kSmem - layout().ring - token_stages(cap, np) * stage_bytes(cap, np) - kZBytes) / kWBytes);
     return n > kMaxWS ? kMaxWS : n;
 }
-static_assert(weight_stages(true, 128, 1) >= 3 && weight_stages(true, 64, 2) >= 3, "shared memory");
+static_assert(weight_stages(128, 1) >= 3 && weight_stages(64, 2) >= 3, "shared memory");
 
 // Shared-memory matrix descriptors, K-major.  Staged rows (128-byte swizzle, blocks of 8 rows 2 KB apart): the upper half is this
 // constant, the lower the address and 1 << 16.
@@ -350,10 +360,6 @@ __device__ __forceinline__ void tmem_store4(uint32_t taddr, const uint32_t (&v)[
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]), "r"(v[10]),
         "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
-}
-__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(smem_u32(src)), "r"(bytes)
-                 : "memory");
 }
 __device__ __forceinline__ void commit_at(uint32_t bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -413,9 +419,9 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
     extern __shared__ __align__(1024) uint8_t smem[];
     const int K = GATE ? p.w.H : p.w.I, N = GATE ? 2 * p.w.I : p.w.H, G = K >> 7;
     const int R = N / kRows;                               // row tiles of an expert
-    constexpr Layout L = layout(GATE);
+    constexpr Layout L = layout();
     const uint32_t bstage = stage_bytes(p.cap, NP);
-    const int BS = token_stages(p.cap, NP), WS = weight_stages(GATE, p.cap, NP);
+    const int BS = token_stages(p.cap, NP), WS = weight_stages(p.cap, NP);
     const uint32_t zeros_at = L.ring + BS * bstage, wring = zeros_at + kZBytes;
     // accumulators: bf16 of a tile, fp32 of a pair's two groups side by side; where a token stage's sums begin
     const uint32_t dcols = uint32_t(p.cap) * NP, xoff = dcols * 256u * GS;
@@ -763,64 +769,41 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
         // ---- epilogue: warp w reads tensor-memory lanes 32 (w % 4) .. + 31 (its weight rows), every second sixteen of the tokens
         const int q = warp & 3, et = tid - kEpiWarp * 32, half = (warp - kEpiWarp) >> 2;
         float* fac = reinterpret_cast<float*>(smem + L.fac);       // [2][2][128]
-        uint8_t* tbuf = smem + L.tile;
-        // gate_up: where this lane's activation of tokens 0 (an up lane: 1), 2, 4, 6 of eight goes: its column of the warp's 16
-        const bool lo = (lane & 15) < 8;
-        uint32_t aoff[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i16 = (lane >> 4) * 8 + (lane & 7), at = 2 * (i16 & 7) - (i16 & 1) + ((i16 >> 3) << 1);
-            aoff[j] = piece(2 * j + (lo ? 0 : 1), 2 * q + (at >> 3)) + (at & 7) * 2;
-        }
+        const bool lo = (lane & 15) < 8;                           // gate_up: of the tile's 8 gate rows
         Turn td;
         int turn = 0;
         int4 tile = tile_of(blockIdx.x), ahead;
         float f0 = 0.f, f1 = 0.f, irho = 1.f;
         auto factors = [&](int it, const int4& tl) {
             if (et < tl.w) {
-                f0 = GATE ? p.isx[tl.y + et] : p.sact[tl.y + et];
-                f1 = GATE ? p.sact[tl.y + et] : p.sout[tl.y + et];
+                f0 = GATE ? p.isx[tl.y + et] : p.isa[tl.y + et];
+                if (!GATE) f1 = p.sout[tl.y + et];
             }
             irho = rho[size_t(tl.x) * N + (it % R) * kRows + 32 * q + lane];
         };
         if (int(blockIdx.x) < items) factors(blockIdx.x, tile);
         for (int it = blockIdx.x; it < items; it += step, turn ^= 1) {
-            const int r = it % R, n = tile.z, real = tile.w;
+            const int r = it % R, real = tile.w;
             float* f = fac + turn * 256;
             if (et < real) {
-                f[et] = 0x1p12f * (GATE ? f0 : inverse_pow2(f0));
-                f[128 + et] = f1;
+                f[et] = 0x1p12f * f0;
+                if (!GATE) f[128 + et] = f1;
             }
             const float ir = 0x1p12f * inverse_pow2(irho);     // (the 2^24 of A, half of it with either factor)
             ahead = tile_of(it + step);
-            // factors in place, the previous tile's copies have read the buffer
-            auto ready = [&]() {
-                if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                epilogue_bar();
-            };
             // tokens c0 .. c0 + 15 of this lane's row
             auto finish = [&](int c0, const float (&v)[16]) {
                 if (GATE) {
                     // in pairs: the gate lanes (tile rows 0..7) finish token c, the up lanes token c + 1
+                    float* to = static_cast<float*>(p.out) + size_t(tile.y + c0 + (lo ? 0 : 1)) * p.w.I + r * 64 + 16 * q + (lane >> 4) * 8 + (lane & 7);
 #pragma unroll
-                    for (int j = 0; j < 16; j += 4) {
-                        if (c0 + j >= real) break;             // (padding: whatever the buffers hold)
-                        const float4 u4 = *reinterpret_cast<const float4*>(f + c0 + j), s4 = *reinterpret_cast<const float4*>(f + 128 + c0 + j);
-                        const float u[4] = {u4.x, u4.y, u4.z, u4.w}, sc[4] = {s4.x, s4.y, s4.z, s4.w};
-#pragma unroll
-                        for (int h = 0; h < 4; h += 2) {
-                            const float xa = __fmul_rn(v[j + h], __fmul_rn(ir, u[h])), xb = __fmul_rn(v[j + h + 1], __fmul_rn(ir, u[h + 1]));
-                            const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
-                            float a = silu_mul<NP == 1>(lo ? xa : other, lo ? other : xb);
-                            a = __fmul_rn(a, lo ? sc[h] : sc[h + 1]);
-                            uint8_t* to = tbuf + ((c0 + j) >> 3) * NP * 1024 + aoff[((j + h) & 7) >> 1];
-#pragma unroll
-                            for (int s = 0; s < NP; ++s) {
-                                const __half hv = __float2half_rn(a);
-                                *reinterpret_cast<__half*>(to + s * 1024) = hv;
-                                a = __fsub_rn(a, __half2float(hv));
-                            }
-                        }
+                    for (int j = 0; j < 16; j += 2) {
+                        if (c0 + j >= real) break;
+                        const float2 u = *reinterpret_cast<const float2*>(f + c0 + j);
+                        const float xa = __fmul_rn(v[j], __fmul_rn(ir, u.x)), xb = __fmul_rn(v[j + 1], __fmul_rn(ir, u.y));
+                        const float other = __shfl_xor_sync(kFull, lo ? xb : xa, 8);
+                        const float a = silu_mul<NP == 1>(lo ? xa : other, lo ? other : xb);
+                        if (c0 + j + (lo ? 0 : 1) < real) to[size_t(j) * p.w.I] = a;
                     }
                 } else {
                     // bf16: the rows wait for the weighted sum as fp16, scaled to their bound (half a step: 2^-12, a sixteenth
@@ -844,7 +827,7 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
             };
             // (after a timeout nothing is stored any more, but the barriers are kept)
             if constexpr (NP == 1) {
-                ready();
+                epilogue_bar();                            // factors in place
                 ok = ok && warp_wait(&d_full[td.s], td.full());
                 if (it + step < items) factors(it + step, ahead);
                 tc_fence_after();
@@ -890,7 +873,7 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
                     if (lane == 0) mbar_arrive(&d_empty[td.s]);
                     td.next(DB);
                 }
-                ready();
+                epilogue_bar();                            // factors in place
                 if (it + step < items) factors(it + step, ahead);
                 // (one copy of the code: the sums move down instead)
 #pragma unroll 1
@@ -902,53 +885,61 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
                         for (int j = 0; j < 16; ++j) sum[i][j] = sum[i + 1][j];
                 }
             }
-            if (GATE) {
-                fence_proxy_async_smem();
-                epilogue_bar();
-                const size_t blocks = p.blocks;            // this tile is the activations' 64 inputs number r
-                if (ok && warp == kEpiWarp) {
-                    if (lane < (n >> 3)) {
-#pragma unroll
-                        for (int s = 0; s < NP; ++s)
-                            bulk_s2g(p.as + atom_at(r, s, NP, blocks, (tile.y >> 3) + lane), tbuf + (size_t(lane) * NP + s) * 1024, 1024);
-                    }
-                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                }
-                // the sum of the tile's 64 activations as staged: 2 (bf16) or 4 lanes to a token
-                constexpr int kShare = kEpiWarps * 32 / kTileTokens<NP>;
-                const int c = et / kShare, c0 = (et % kShare) * (8 / kShare);
-                float X = 0.f;
-#pragma unroll
-                for (int s = 0; s < NP; ++s)
-#pragma unroll
-                    for (int i = 0; i < 8 / kShare; ++i) {
-                        const uint4 h = *reinterpret_cast<const uint4*>(tbuf + (size_t(c >> 3) * NP + s) * 1024 + piece(c & 7, c0 + i));
-                        const uint32_t w[4] = {h.x, h.y, h.z, h.w};
-                        float part = 0.f;
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&w[j]));
-                            part = __fadd_rn(part, __fadd_rn(v.x, v.y));
-                        }
-                        X = __fadd_rn(X, part);
-                    }
-#pragma unroll
-                for (int o = 1; o < kShare; o <<= 1) X = __fadd_rn(X, __shfl_xor_sync(kFull, X, o));
-                if (ok && c < real && et % kShare == 0) {
-                    const int at = tile.y + c;
-                    uint8_t* row = p.as + sums_at(p.w.I, NP, blocks) + size_t(at >> 3) * 128 + (at & 7) * 16;
-                    put_sum(row, r, X, blocks * 128);
-                    // the half that an odd number of groups leaves
-                    if (r == 0 && ((p.w.I >> 7) & 1)) *reinterpret_cast<uint2*>(row + (p.w.I >> 8) * blocks * 128 + 8) = make_uint2(0u, 0u);
-                }
-            }
             tile = ahead;
         }
-        if (GATE && warp == kEpiWarp) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     tc_fence_before();
     __syncthreads();
     if (warp == 0) tc_dealloc(taddr, 512);
+}
+
+// ------------------------------------------------------------------ activations
+// From gate_up's fp32 rows to down's operand: W warps (1, 2, 4 or 8) take a place's row, which they read once and hold.
+constexpr int kActThr = 256, kActPer = 8;                  // float4 of a lane: W x 1024 values of a row
+template <int NP, int W>
+__global__ void __launch_bounds__(kActThr) moe_act_kernel(const MoeTcParams p) {
+    __shared__ float red[kActThr / 32];
+    __shared__ __align__(16) __half sums[kActThr / 32 / W][W * kActPer * 4];
+    pdl_launch_dependents();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = warp / W, l = (warp % W) * 32 + lane;
+    const int place = blockIdx.x * (kActThr / 32 / W) + row, K = p.w.I, K4 = K >> 2;
+    const int at = place < p.T * p.k ? p.pos[place] : -1;
+    const float4* src = reinterpret_cast<const float4*>(static_cast<const float*>(p.out) + size_t(max(at, 0)) * K);
+    float4 v[kActPer];
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < kActPer; ++i) {
+        v[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (at >= 0 && l + i * W * 32 < K4) v[i] = __ldcs(src + l + i * W * 32);
+        m = fmaxf(m, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
+    }
+    m = warp_max(m);
+    if (W > 1) {
+        if (lane == 0) red[warp] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < W; ++w) m = fmaxf(m, red[row * W + w]);
+    }
+    float sig, isg;
+    pow2_scale(__float_as_uint(m), sig, isg);
+#pragma unroll
+    for (int i = 0; i < kActPer; ++i) {
+        const int k4 = l + i * W * 32;
+        if (at < 0 || k4 >= K4) break;                     // (whole warps: K4 is a multiple of 32)
+        const float a[4] = {__fmul_rn(v[i].x, sig), __fmul_rn(v[i].y, sig), __fmul_rn(v[i].z, sig), __fmul_rn(v[i].w, sig)};
+        uint2 out[NP];
+        const float X = stage4<NP>(a, k4 & 3, out);
+        uint8_t* to = p.as + four_at(k4 * 4, at, NP, p.blocks);
+#pragma unroll
+        for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * p.blocks * 2048) = out[q];
+        if ((lane & 15) == 0) put_sum(sums[row], k4 >> 4, X);
+    }
+    if (W > 1) __syncthreads();
+    else __syncwarp();
+    if (at < 0) return;
+    for (int pr = l; pr < pairs_of(K); pr += W * 32) store_sums(p.as, sums[row], pr, K, NP, p.blocks, at);
+    if (l == 0) p.isa[at] = isg;
 }
 
 // ------------------------------------------------------------------ combine
@@ -1041,6 +1032,19 @@ const void* stage_fn(bool bf16, int H) {
     return nullptr;
 }
 
+// Warps to a row, and the kernel.
+int act_warps(int I) { return I <= 1024 ? 1 : (I <= 2048 ? 2 : (I <= 4096 ? 4 : 8)); }
+const void* act_fn(bool bf16, int I) {
+#define KMR_ACT(w) \
+    if (act_warps(I) == w) return bf16 ? (const void*)moe_act_kernel<1, w> : (const void*)moe_act_kernel<2, w>
+    KMR_ACT(1);
+    KMR_ACT(2);
+    KMR_ACT(4);
+    KMR_ACT(8);
+#undef KMR_ACT
+    return nullptr;
+}
+
 size_t up16(size_t n) { return (n + 15) & ~size_t(15); }
 
 }  // namespace
@@ -1063,13 +1067,14 @@ MoeTcSizes moe_tc_sizes(const MoeView& w, bool bf16, int T, int k) {
     z.tiles = 16;
     z.pos = z.tiles + (experts + P / 16) * 16;
     z.isx = z.pos + up16(S * 4);
-    z.sact = z.isx + up16(P * 4);
-    z.sout = z.sact + up16(P * 4);
+    z.isa = z.isx + up16(P * 4);
+    z.sout = z.isa + up16(P * 4);
     z.xs = z.sout + up16(P * 4);
     z.blocks = P / 8;
     z.as = z.xs + staged_bytes(w.H, np, P / 8);
     z.out = z.as + staged_bytes(w.I, np, P / 8);
-    z.total = z.out + P * w.H * (bf16 ? 2 : 4);
+    const size_t rows = size_t(w.H) * (bf16 ? 2 : 4), acts = size_t(w.I) * 4;      // (the activations are staged before the results come)
+    z.total = z.out + P * (rows > acts ? rows : acts);
     return z;
 }
 
@@ -1078,10 +1083,10 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
     cudaError_t e = launch_dependent((const void*)moe_plan_kernel, dim3(1), kPlanThr, 0, 1, q, st);
     if (e != cudaSuccess) return e;
     if ((e = launch_dependent(stage_fn(bf16, p.w.H), dim3(p.T), kStageThr, 0, 1, q, st)) != cudaSuccess) return e;
-    for (const bool gate : {true, false}) {
-        const int threads = product_threads(unpack_sets(p.cap, bf16 ? 1 : 2));
-        if ((e = launch_dependent(product_fn(bf16, gate, p.cap), dim3(sms), threads, kSmem, 1, q, st)) != cudaSuccess) return e;
-    }
+    const int threads = product_threads(unpack_sets(p.cap, bf16 ? 1 : 2)), rows = kActThr / 32 / act_warps(p.w.I);
+    if ((e = launch_dependent(product_fn(bf16, true, p.cap), dim3(sms), threads, kSmem, 1, q, st)) != cudaSuccess) return e;
+    if ((e = launch_dependent(act_fn(bf16, p.w.I), dim3((p.T * p.k + rows - 1) / rows), kActThr, 0, 1, q, st)) != cudaSuccess) return e;
+    if ((e = launch_dependent(product_fn(bf16, false, p.cap), dim3(sms), threads, kSmem, 1, q, st)) != cudaSuccess) return e;
     const void* combine = bf16 ? (const void*)moe_combine_kernel<true> : (const void*)moe_combine_kernel<false>;
     const int cols = kCombineThr * (bf16 ? 8 : 4);
     return launch_dependent(combine, dim3(p.T, (p.w.H + cols - 1) / cols), kCombineThr, 0, 1, q, st);
@@ -1105,7 +1110,9 @@ cudaError_t moe_tc_set_attributes() {
         }
     const void* others[] = {(const void*)moe_plan_kernel, (const void*)moe_factors_kernel, stage_fn(true, 1024), stage_fn(true, 2048),
                             stage_fn(true, 4096), stage_fn(true, 8192), stage_fn(false, 1024), stage_fn(false, 2048),
-                            stage_fn(false, 4096), stage_fn(false, 8192), (const void*)moe_combine_kernel<true>,
+                            stage_fn(false, 4096), stage_fn(false, 8192), act_fn(true, 1024), act_fn(true, 2048), act_fn(true, 4096),
+                            act_fn(true, 8192), act_fn(false, 1024), act_fn(false, 2048), act_fn(false, 4096), act_fn(false, 8192),
+                            (const void*)moe_combine_kernel<true>,
                             (const void*)moe_combine_kernel<false>};
     for (const void* fn : others) {
         cudaFuncAttributes a;
