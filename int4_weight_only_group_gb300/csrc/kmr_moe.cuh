@@ -55,7 +55,7 @@ struct MoeTcParams {
     MoeView w;
     const float* rho_gate_up;                // [E][2I] row factors, packed row order
     const float* rho_down;                   // [E][H]
-    const float* norms;                      // [E][3] bounds of the gate, up and down rows' norms
+    const float* norms;                      // [E] bounds of the down rows' norms
     const void* x;                           // [T][H]
     const int32_t* ids;                      // [T][k]
     const float* weights;                    // [T][k]

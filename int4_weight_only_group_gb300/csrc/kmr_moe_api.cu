@@ -66,7 +66,7 @@ extern "C" int kmr_moe_route(const void* logits, int dtype, int T, int experts, 
 
 extern "C" size_t kmr_moe_factors_size(int experts, int hidden, int intermediate) {
     if (experts < 1 || experts > kMoeMaxExperts || !dim_ok(hidden) || !dim_ok(intermediate)) return 0;
-    return size_t(experts) * (2 * size_t(intermediate) + hidden + 3) * 4;
+    return size_t(experts) * (2 * size_t(intermediate) + hidden + 3) * 4;      // (the last two words an expert are spare)
 }
 
 extern "C" int kmr_moe_prepare(const kmr_moe* moe, void* stream) {

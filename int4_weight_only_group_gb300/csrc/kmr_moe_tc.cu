@@ -58,9 +58,9 @@ __device__ __forceinline__ int above(float v) { return int(__float_as_uint(v) >>
 __device__ __forceinline__ float inverse_pow2(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 
 // ------------------------------------------------------------------ weights, once
-// Row factors rho (a power of two that brings max(|s|, 2^-18 |z|) of the row to [2^13, 2^14)) and the largest row norm bound of
-// each expert's gate, up and down rows (`which`: the matrix's first of the three): |w|^2 <= sum over groups of 128 max(|z - 8 s|, |z + 7 s|)^2.
-__global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rho, float* norms, int which) {
+// Row factors rho (a power of two that brings max(|s|, 2^-18 |z|) of the row to [2^13, 2^14)) and, where norms is given, the largest
+// row norm bound of each expert: |w|^2 <= sum over groups of 128 max(|z - 8 s|, |z + 7 s|)^2.
+__global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rho, float* norms) {
     const int row = blockIdx.x * blockDim.x + threadIdx.x, e = blockIdx.y;
     if (row >= tiles * 16) return;
     const uint8_t* at = w + (size_t(e) * tiles + row / 16) * G * kGroupBytes + 1024 + (row & 15) * 4;
@@ -76,7 +76,7 @@ __global__ void moe_factors_kernel(const uint8_t* w, int tiles, int G, float* rh
     pow2_scale(__float_as_uint(m), r, ir);
     rho[size_t(e) * tiles * 16 + row] = r;
     // (a bound: rounded up; the bits of non-negative floats order like integers)
-    atomicMax(reinterpret_cast<int*>(norms + 3 * e + (which == 0 ? (row & 15) >> 3 : which)), __float_as_int(sqrtf(n2) * 1.001f));
+    if (norms) atomicMax(reinterpret_cast<int*>(norms + e), __float_as_int(sqrtf(n2) * 1.001f));
 }
 
 // ------------------------------------------------------------------ plan
@@ -207,7 +207,7 @@ __device__ __forceinline__ void store_sums(uint8_t* to, const void* sums, int pr
 constexpr int kStageThr = 256;
 template <typename IN, int NP, int PER>
 __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams p) {
-    __shared__ float red[2][kStageThr / 32];
+    __shared__ float red[kStageThr / 32];
     __shared__ int pos[kMoeMaxTopK], places;
     __shared__ __align__(16) __half sums[kMoeMaxDim / 64 * 2];          // of the row, as a pair's 16 bytes
     pdl_launch_dependents();
@@ -237,16 +237,15 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
 #pragma unroll
     for (int i = 0; i < PER; ++i) m = fmaxf(m, fmaxf(fmaxf(fabsf(v[i].x), fabsf(v[i].y)), fmaxf(fabsf(v[i].z), fabsf(v[i].w))));
     m = warp_max(m);
-    if (lane == 0) red[0][warp] = m;
+    if (lane == 0) red[warp] = m;
     __syncthreads();
     const int n = places;
     if (n == 0) return;
-    m = red[0][0];
+    m = red[0];
 #pragma unroll
-    for (int w = 1; w < kStageThr / 32; ++w) m = fmaxf(m, red[0][w]);
+    for (int w = 1; w < kStageThr / 32; ++w) m = fmaxf(m, red[w]);
     float sig, isg;
     pow2_scale(__float_as_uint(m), sig, isg);
-    float ss = 0.f;
     const size_t blocks = p.blocks;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -256,8 +255,6 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
         const float a[4] = {__fmul_rn(v[i].x, sig), __fmul_rn(v[i].y, sig), __fmul_rn(v[i].z, sig), __fmul_rn(v[i].w, sig)};
         uint2 out[NP];
         const float X = stage4<NP>(a, m4, out);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ss = __fmaf_rn(a[q], a[q], ss);
         for (int j = 0; j < n; ++j) {
             uint8_t* to = p.xs + four_at(k, pos[j], NP, blocks);
 #pragma unroll
@@ -265,23 +262,9 @@ __global__ void __launch_bounds__(kStageThr) moe_stage_kernel(const MoeTcParams 
         }
         if ((lane & 15) == 0) put_sum(sums, k >> 6, X);
     }
-    ss = warp_sum(ss);
-    if (lane == 0) red[1][warp] = ss;
     __syncthreads();
     for (int i = tid; i < n * pairs_of(K); i += kStageThr) store_sums(p.xs, sums, i % pairs_of(K), K, NP, blocks, pos[i / pairs_of(K)]);
-    if (tid < p.k) {
-        const int at = p.pos[size_t(t) * p.k + tid];
-        if (at < 0) return;
-        ss = red[1][0];
-        for (int w = 1; w < kStageThr / 32; ++w) ss = __fadd_rn(ss, red[1][w]);
-        // |x|, and a bound of the place's activations
-        const int e = p.ids[size_t(t) * p.k + tid];
-        const int ex = above(sqrtf(ss)) + above(isg) - 1;
-        p.isx[at] = isg;
-        const int ea = 2 * ex + above(p.norms[3 * e]) + above(p.norms[3 * e + 1]);
-        // bf16: |down act| <= |act| max |row|, |act| <= sqrt(I) 2^ea
-        p.sout[at] = pow2(15 - (ea + (33 - __clz(p.w.I)) / 2 + above(p.norms[3 * e + 2])));
-    }
+    if (tid < n) p.isx[pos[tid]] = isg;
 }
 
 // ------------------------------------------------------------------ the grouped product
@@ -806,8 +789,11 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
                         if (c0 + j + (lo ? 0 : 1) < real) to[size_t(j) * p.w.I] = a;
                     }
                 } else {
-                    // bf16: the rows wait for the weighted sum as fp16, scaled to their bound (half a step: 2^-12, a sixteenth
-                    // of the result's; fp32 rows would be 60% of the call's traffic)
+                    // bf16: the rows wait for the weighted sum as fp16 (half a step: 2^-11, an eighth of the result's; fp32 rows would
+                    // be 60% of the call's traffic), scaled by |act| max |down row|.  A value is typically 2^-5 (I 128) to 2^-10 (I
+                    // 8192) of that bound, and fp16's normal range goes on for another 2^19: as far as that a row may be smaller than
+                    // the expert's largest.  (Scales from the results' own maxima, one warp reduction for every 32 columns of a token:
+                    // 4096 rows 406 -> 475 us.)
                     using Out = typename std::conditional<NP == 1, __half, float>::type;
                     Out* out = static_cast<Out*>(p.out) + size_t(tile.y + c0) * N + r * kRows + 32 * q + lane;
                     auto put = [&](int j) {
@@ -898,7 +884,7 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
 constexpr int kActThr = 256, kActPer = 8;                  // float4 of a lane: W x 1024 values of a row
 template <int NP, int W>
 __global__ void __launch_bounds__(kActThr) moe_act_kernel(const MoeTcParams p) {
-    __shared__ float red[kActThr / 32];
+    __shared__ float red[2][kActThr / 32];
     __shared__ __align__(16) __half sums[kActThr / 32 / W][W * kActPer * 4];
     pdl_launch_dependents();
     pdl_wait();
@@ -916,13 +902,14 @@ __global__ void __launch_bounds__(kActThr) moe_act_kernel(const MoeTcParams p) {
     }
     m = warp_max(m);
     if (W > 1) {
-        if (lane == 0) red[warp] = m;
+        if (lane == 0) red[0][warp] = m;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < W; ++w) m = fmaxf(m, red[row * W + w]);
+        for (int w = 0; w < W; ++w) m = fmaxf(m, red[0][row * W + w]);
     }
     float sig, isg;
     pow2_scale(__float_as_uint(m), sig, isg);
+    float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < kActPer; ++i) {
         const int k4 = l + i * W * 32;
@@ -930,16 +917,32 @@ __global__ void __launch_bounds__(kActThr) moe_act_kernel(const MoeTcParams p) {
         const float a[4] = {__fmul_rn(v[i].x, sig), __fmul_rn(v[i].y, sig), __fmul_rn(v[i].z, sig), __fmul_rn(v[i].w, sig)};
         uint2 out[NP];
         const float X = stage4<NP>(a, k4 & 3, out);
+        if (NP == 1) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ss = __fmaf_rn(a[q], a[q], ss);
+        }
         uint8_t* to = p.as + four_at(k4 * 4, at, NP, p.blocks);
 #pragma unroll
         for (int q = 0; q < NP; ++q) *reinterpret_cast<uint2*>(to + q * p.blocks * 2048) = out[q];
         if ((lane & 15) == 0) put_sum(sums[row], k4 >> 4, X);
     }
+    if (NP == 1) {
+        ss = warp_sum(ss);
+        if (W > 1 && lane == 0) red[1][warp] = ss;
+    }
     if (W > 1) __syncthreads();
     else __syncwarp();
     if (at < 0) return;
     for (int pr = l; pr < pairs_of(K); pr += W * 32) store_sums(p.as, sums[row], pr, K, NP, p.blocks, at);
-    if (l == 0) p.isa[at] = isg;
+    if (l == 0) {
+        p.isa[at] = isg;
+        if (NP == 1) {
+#pragma unroll
+            for (int w = 1; w < W; ++w) ss = __fadd_rn(ss, red[1][row * W + w]);
+            // the bound of the place's results: |act| |row| < 2^15 once scaled
+            p.sout[at] = pow2(15 - (above(sqrtf(ss)) + above(isg) - 1 + above(p.norms[p.ids[place]])));
+        }
+    }
 }
 
 // ------------------------------------------------------------------ combine
@@ -1093,10 +1096,10 @@ cudaError_t launch_moe_tc(const MoeTcParams& p, bool bf16, int sms, cudaStream_t
 }
 
 cudaError_t launch_moe_factors(const MoeView& w, float* rho_gate_up, float* rho_down, float* norms, cudaStream_t st) {
-    cudaError_t e = cudaMemsetAsync(norms, 0, size_t(w.E) * 3 * 4, st);
+    cudaError_t e = cudaMemsetAsync(norms, 0, size_t(w.E) * 4, st);
     if (e != cudaSuccess) return e;
-    moe_factors_kernel<<<dim3((2 * w.I + 127) / 128, w.E), 128, 0, st>>>(w.gate_up, w.I / 8, w.H / 128, rho_gate_up, norms, 0);
-    moe_factors_kernel<<<dim3((w.H + 127) / 128, w.E), 128, 0, st>>>(w.down, w.H / 16, w.I / 128, rho_down, norms, 2);
+    moe_factors_kernel<<<dim3((2 * w.I + 127) / 128, w.E), 128, 0, st>>>(w.gate_up, w.I / 8, w.H / 128, rho_gate_up, nullptr);
+    moe_factors_kernel<<<dim3((w.H + 127) / 128, w.E), 128, 0, st>>>(w.down, w.H / 16, w.I / 128, rho_down, norms);
     return cudaGetLastError();
 }
 

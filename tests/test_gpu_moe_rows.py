@@ -7,7 +7,7 @@ import int4_weight_only_group_gb300 as kmr
 from oracle import moe
 
 pytestmark = pytest.mark.gpu
-DT = [kmr.KMR_F32]
+DT = [kmr.KMR_F32, kmr.KMR_BF16]
 
 # A row's result against 64 bits, relative L2.
 # fp32: each of the three products takes, for every group of 128 inputs, at most 9 full-size steps of the tensor cores (8 of the
