@@ -1,4 +1,4 @@
-"""GPU parity of the int4 experts where weight rows, scales and inputs differ in size."""
+"""GPU parity of the int4 experts where weight rows, scales and inputs differ in size, and the adapters' last bits."""
 import numpy as np
 import pytest
 
@@ -182,3 +182,24 @@ def test_scales_that_differ_within_a_row(torch, T):
     want = moe.experts(xv, ids, w, layer.gate_up, layer.down)
     tol = TOL[kmr.KMR_F32] if T == 3 else 3 * 2.0 ** -16 * (H / 128) ** 0.5
     assert worst(run(torch, layer, x, ids, w, kmr.KMR_F32), want) <= tol
+
+
+# The adapters' fp32 sums.  v: runs of 32 inputs, in which the small terms come first and cost nothing, then 2 steps of the tensor cores that
+# cut off some 2^-25 of the run's sum each; the runs of the warps and CTAs are added in fp32 (four additions of half a 2^-24 at the
+# most, at random: 4e-8 rms).  The second product: the small terms first again, then rank / 16 steps of 2^-25.  The result's
+# own rounding: 2^-25 rms.
+@pytest.mark.parametrize("rank", [8, 16, 32, 64, 128])
+@pytest.mark.parametrize("T", [5, 700])
+def test_adapters_to_the_last_bits(torch, T, rank):
+    r = np.random.default_rng(rank + T)
+    K, N, L = 256, 512, 3
+    a = torch.from_numpy((r.standard_normal((L, rank, K)) * K ** -0.5).astype(np.float32)).bfloat16().cuda()
+    b = torch.from_numpy((r.standard_normal((L, N, rank)) * 0.3).astype(np.float32)).bfloat16().cuda()
+    x, xv = rounded(torch, r.standard_normal((T, K)), kmr.KMR_F32)
+    ids = np.repeat(r.integers(0, L, T), 40)[:T].astype(np.int32)
+    y = torch.full((T, N), float("nan"), device="cuda")
+    kmr.kmr_lora_apply(kmr.Lora(a, b), x, None, y, kmr.KMR_F32, torch.from_numpy(ids).cuda(), T, K, N, torch.cuda.current_stream())
+    assert kmr.kmr_last_device_error() == 0
+    want = moe.adapters(xv, np.zeros((T, N)), ids, a.float().cpu().numpy(), b.float().cpu().numpy(), np.full(L, rank), np.ones(L))
+    err = rel_l2(y.double().cpu().numpy(), want)
+    assert err <= 2 * 2.0 ** -25 + 4e-8 + rank / 16 * 2.0 ** -25 + 2.0 ** -25
