@@ -13,7 +13,7 @@ constexpr int kMoeMaxTokens = 1 << 20;
 constexpr int kMoeSmallPlaces = 32;          // most places (token, j) of the small form: a warp's lanes
 constexpr int kMoeSmallTokens = 16;          // its most tokens
 constexpr long long kMoeSmallWeights = 3ll << 26;    // and weights of the places' experts, each counted by itself
-constexpr int kMoeSmallCtas = 128;           // CTAs at once that its sizes are made for (a GB300 has 152 SMs)
+constexpr int kMoeSmallCtas = 128;           // fewest CTAs of gate_up, which its sizes are made for (a GB300 has 152 SMs)
 
 // ------------------------------------------------------------------ router
 struct MoeRouteParams {

@@ -526,10 +526,10 @@ bool moe_small_fits(const MoeView& w, bool bf16, int T, int k) {
 
 cudaError_t launch_moe_small(const MoeSmallParams& p, bool bf16, int sms, cudaStream_t st) {
     const int S = p.T * p.k, all = distinct_of(p.w, S) * (p.w.I / 8);
-    if (sms < kMoeSmallCtas) return cudaErrorInvalidConfiguration;
     MoeSmallParams q = p;
-    const int grid = all < sms ? all : sms;
-    q.list = gate_tiles(p.w, S, sms);
+    const int ctas = sms > kMoeSmallCtas ? sms : kMoeSmallCtas;      // (a CTA waits for no other: fewer SMs run them in turn)
+    const int grid = all < ctas ? all : ctas;
+    q.list = gate_tiles(p.w, S, ctas);
     q.by_tiles = uint32_t((0x100000000ull + p.w.I / 8 - 1) / (p.w.I / 8));
     q.by_grid = uint32_t((0x100000000ull + grid - 1) / grid);
     size_t smem = plan_ring(false, bf16, p.w.H, p.T, q.list, &q.stages, &q.batch);
