@@ -215,12 +215,20 @@ def _dev(a, kind: set, name: str) -> Optional[int]:
     return _dev_refused(a, kind, name)
 
 
+def _learn_types() -> bool:
+    """Fills the types' sets; whether they were empty."""
+    import torch
+    if _F32:
+        return False
+    _F32.add(torch.float32)
+    _I32.add(torch.int32)
+    _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
+    return True
+
+
 def _dev_refused(a, kind, name):
     import torch
-    if not _F32:
-        _F32.add(torch.float32)
-        _I32.add(torch.int32)
-        _BF16.update((torch.bfloat16, torch.int16, torch.uint16))
+    if _learn_types():
         return _dev(a, kind, name)
     if isinstance(a, int):
         return int(a)
@@ -466,6 +474,8 @@ def _rows(a, kind: set, ld: int, name: str) -> Optional[int]:
             raise ValueError(f"{name} has rows {a.stride(0)} values apart (and values {a.stride(1)}), not {ld} (and 1)")
     except AttributeError:
         pass
+    if not kind and _learn_types():              # (the first tensor of all)
+        return _rows(a, kind, ld, name)
     return _dev(a, kind, name)
 
 
