@@ -412,7 +412,7 @@ typedef struct kmr_lora {
                              /* not used, whatever it holds (values outside 0..max_rank are held within)  */
     const float* scales;     /* [adapters] or NULL (1)                                                    */
     int adapters;
-    int inputs, outputs;     /* K, N: multiples of 16                                                     */
+    int inputs, outputs;     /* K, N: multiples of 16 up to 2^28                                          */
     int max_rank;            /* a multiple of 8 up to 128                                                 */
 } kmr_lora;
 

@@ -86,6 +86,7 @@ cudaError_t moe_tc_set_attributes();
 
 // ------------------------------------------------------------------ adapters
 constexpr int kLoraMaxRank = 128;
+constexpr int kLoraMaxDim = 1 << 28;         // inputs and outputs: a row's byte offsets are 32-bit numbers
 struct LoraParams {
     const uint16_t* a;                       // bf16 [L][r][K]
     const uint16_t* b;                       // bf16 [L][N][r]

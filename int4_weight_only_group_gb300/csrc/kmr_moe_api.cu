@@ -157,7 +157,8 @@ extern "C" int kmr_lora_apply(const kmr_lora* lora, const void* x, const void* b
         !aligned(x, 16) || !aligned(base, 16) || !aligned(y, 16) || !aligned(adapter_ids, 4))
         return KMR_ERR_INVALID_ARG;
     if (T < 1 || T > kMoeMaxTokens) return KMR_ERR_BATCH;
-    if (lora->adapters < 1 || lora->inputs < 16 || lora->inputs % 16 || lora->outputs < 16 || lora->outputs % 16 ||
+    if (lora->adapters < 1 || lora->inputs < 16 || lora->inputs % 16 || lora->inputs > kLoraMaxDim || lora->outputs < 16 ||
+        lora->outputs % 16 || lora->outputs > kLoraMaxDim ||
         lora->max_rank < 8 || lora->max_rank > kLoraMaxRank || lora->max_rank % 8)
         return KMR_ERR_SHAPE;
     if (ldx < lora->inputs || ldx % 8 || ldy < lora->outputs || ldy % 8) return KMR_ERR_SHAPE;

@@ -1,4 +1,5 @@
 """The binding of the adapters and the experts, where the process has passed no tensor before."""
+import ctypes
 import os
 import subprocess
 import sys
@@ -27,3 +28,12 @@ def test_strided_rows_in_the_first_call_of_a_process():
         build()
     r = subprocess.run([sys.executable, "-c", FRESH], capture_output=True, text=True, cwd=ROOT)
     assert r.stdout.split() == ["library", str(kmr.KMR_ERR_INVALID_ARG)], r.stderr[-500:]
+
+
+@pytest.mark.parametrize("kw,code", [(dict(inputs=(1 << 28) + 16), -2), (dict(outputs=(1 << 28) + 16), -2), (dict(outputs=1 << 29), -2),
+                                     (dict(inputs=(1 << 31) - 16), -2), (dict(outputs=(1 << 31) - 16), -2)])
+def test_adapters_whose_rows_pass_32_bits(kw, code):
+    """A row's byte offsets are 32-bit numbers in the kernel: longer rows are refused (before any CUDA call)."""
+    shape = dict(a=16, b=16, ranks=None, scales=None, adapters=1, inputs=64, outputs=32, max_rank=16)
+    lora = kmr.LoraStruct(**{**shape, **kw})
+    assert kmr.lib().kmr_lora_apply(ctypes.addressof(lora), 16, 16, 16, kmr.KMR_F32, 16, 1, 1 << 32, 1 << 32, None) == code
