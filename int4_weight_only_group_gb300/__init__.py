@@ -247,6 +247,16 @@ def _stream(s) -> Optional[int]:
     return s.cuda_stream                  # torch.cuda.Stream
 
 
+def _torch_stream(s, device):
+    """The torch stream of a stream argument (None for tensors that are on no CUDA device)."""
+    import torch
+    if device.type != "cuda":
+        return None
+    if s is None or s == 0:
+        return torch.cuda.default_stream(device)
+    return torch.cuda.ExternalStream(s, device) if isinstance(s, int) else s
+
+
 def _check(code: int, where: str) -> None:
     if code != KMR_OK:
         raise KmrError(code, where)
@@ -435,7 +445,9 @@ class Moe:
         if gate_up.device != down.device:
             raise ValueError("the tensors of an expert layer are on one device")
         import torch
-        factors = torch.empty(kmr_moe_factors_size(experts, hidden, intermediate), dtype=torch.uint8, device=gate_up.device)
+        # memory of the stream that fills it: what is still queued on another one for a freed tensor's block does not reach it
+        with torch.cuda.stream(_torch_stream(stream, gate_up.device)):
+            factors = torch.empty(kmr_moe_factors_size(experts, hidden, intermediate), dtype=torch.uint8, device=gate_up.device)
         self.tensors = (gate_up, down, factors)
         self.experts, self.hidden, self.intermediate, self.group = experts, hidden, intermediate, group
         self._struct = MoeStruct(gate_up.data_ptr(), down.data_ptr(), experts, hidden, intermediate, group, factors.data_ptr())

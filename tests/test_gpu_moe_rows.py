@@ -203,3 +203,26 @@ def test_adapters_to_the_last_bits(torch, T, rank):
     want = moe.adapters(xv, np.zeros((T, N)), ids, a.float().cpu().numpy(), b.float().cpu().numpy(), np.full(L, rank), np.ones(L))
     err = rel_l2(y.double().cpu().numpy(), want)
     assert err <= 2 * 2.0 ** -25 + 4e-8 + rank / 16 * 2.0 ** -25 + 2.0 ** -25
+
+
+def test_weights_prepared_on_another_stream(torch):
+    """The factors' memory belongs to the stream that fills them: work still queued on the current stream, on memory freed there, does not
+    reach them."""
+    r = np.random.default_rng(41)
+    E, H, I, T = 2, 256, 256, 20
+    layer = Layer(torch, r, H, I, even(r, E, 2 * I, H), even(r, E, H, I))
+    x, xv = rounded(torch, r.standard_normal((T, H)), kmr.KMR_F32)
+    ids, w = places(r, T, E, 1)
+    want = moe.experts(xv, ids, w, layer.gate_up, layer.down)
+    gate_up, down, factors = layer.dev.tensors
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for stream in (side, side.cuda_stream):
+        freed = [torch.empty(factors.numel(), dtype=torch.uint8, device="cuda") for _ in range(8)]
+        torch.cuda._sleep(20_000_000)                        # some 10 ms
+        for f in freed:
+            f.fill_(255)                                     # NaN
+        del freed, f
+        layer.dev = kmr.Moe(gate_up, down, E, H, I, 128, stream)
+        torch.cuda.synchronize()
+        assert worst(run(torch, layer, x, ids, w, kmr.KMR_F32), want) <= TOL[kmr.KMR_F32]
