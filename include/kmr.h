@@ -390,11 +390,12 @@ int kmr_moe_prepare(const kmr_moe* moe, void* stream);
  *   workspace device memory, 16-byte aligned, kmr_moe_experts_workspace_size(moe, dtype, T, top_k) bytes or more (0 for
  *             arguments that the call would refuse); no initialisation.  Calls that may overlap on the device need
  *             workspaces of their own.
- * Products are exact and sums are held in fp32, whatever the type (more than a few tokens: where a weight row's scales lie within
- * 2^7 of its largest; below, to 2^-20 of its largest weight); between gate_up and down the activations are held as fp16
- * numbers, two (fp32: 22 bits) or one (bf16: 11 bits), scaled by their own largest (of the row or, of a few tokens, of 128).
- * bf16 results of more than a few tokens wait for the weighted sum as fp16 too, where a down row is not below 2^-18 of the expert's largest; every
- * other sum is fp32.  A few tokens (up to 32 places T top_k of up to 16 tokens, whose experts taken each by itself have up to 3 x 2^26
+ * What is held in fewer than 32 bits: the inputs of either product are fp16 numbers scaled by their own largest (of the row or, of a
+ * few tokens, of 128), two for fp32 (22 bits down to 2^-16 of the largest, 2^-39 of it below) and one for bf16 (inputs exactly down to
+ * 2^-30 of the largest, activations to 11 bits).  More than a few tokens: sums of 64 inputs, which the zero points take, as two fp16 numbers; a weight
+ * row whose scales lie within 2^6 of its largest exactly, else to 2^-16 of its largest weight; bf16 results that wait for
+ * the weighted sum as one fp16 number, for down rows down to 2^-18 of the expert's largest.  Sums are fp32.
+ * A few tokens (up to 32 places T top_k of up to 16 tokens, whose experts taken each by itself have up to 3 x 2^26
  * weights) are two launches, more are six for every 32768 places; within either form a token's result does not depend
  * on the other tokens.  A workspace of the size for T tokens does for fewer.  top_k 1..32.  Errors:
  * KMR_ERR_INVALID_ARG (pointers, dtype, epilogue), KMR_ERR_SHAPE, KMR_ERR_BATCH, KMR_ERR_BUFFER_SIZE; on the device

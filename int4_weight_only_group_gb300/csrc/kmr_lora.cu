@@ -14,8 +14,8 @@
 //     A row's result does not hang on its neighbours (on T only by the order of the sums over K).
 //   * mma.m16n8k16 in bf16 with fp32 sums.  fp32 operands (x, v) are cut into three bf16 terms, which hold their 24 bits
 //     whatever their exponent; the adapters are bf16 already, so the products are exact.
-// Measured: one row, K 2048, N 4096, r 16: 4.5 us; 16 rows of 16 requests, K = N = 2048, r 64: 6.9 us; 4077 rows bf16, K 2048, N
-// 4096, r 16: 27.5 us (3.0 TB/s); 8192 rows fp32, K 6144, N 2048, r 32: 81 us (4.2 TB/s of 6.8: the cutting into terms and the
+// Measured: one row, K 2048, N 4096, r 16: 4.5 us; 16 rows of 16 requests, K = N = 2048, r 64: 7.2 us; 4077 rows bf16, K 2048, N
+// 4096, r 16: 27.3 us (3.0 TB/s); 8192 rows fp32, K 6144, N 2048, r 32: 79 us (4.3 TB/s of 6.8: the cutting into terms and the
 // MMAs take half the issue slots).
 #include <cooperative_groups.h>
 
@@ -455,10 +455,16 @@ cudaError_t by_rank(const LoraParams& p, int R, int C, cudaStream_t st, bool set
 }  // namespace
 
 cudaError_t launch_lora(const LoraParams& p, bool bf16, int sms, cudaStream_t st) {
-    // One row a tile up to two rows a SM: rows of a small batch have adapters of their own (64 rows of 64 adapters: 6.3 us against
-    // 44 with tiles of 16; of 4 adapters 6.3 against 8.3; 200 rows of 200: 14 against 50).  More rows are taken 16 at a time
-    // (4077 rows: 28 us, 8 at a time 36).  Then the largest cluster that still fits its CTAs to the SMs at once, or nearly
-    // (1000 rows: 11.5 us in clusters of 4, 21 by themselves, 15 in clusters of 8; 4077 rows: 28, and 36 in clusters of 4).
+    // One row a tile up to two rows an SM, else 16.  The ids are on the device, so the rule does not know how rows share adapters: single
+    // rows read an adapter again for each, tiles of 16 take a tile's adapters in turn.  us, single rows against tiles (best cluster
+    // each; K 2048, N 4096), where every row has its own adapter / 16 requests / one:
+    //   bf16, rank 16    64 rows  6.3 : 43 / 6.2 : 18 / 4.9 : 5.6      256  15 : 59 / 14 : 14 / 10 : 6.2      400  26 : 63 / 23 : 14 / 17 : 6.4
+    //   fp32, rank 64    64 rows  17 : 113 / 16 : 44 / 16 : 9.7        256  56 : 154 / 53 : 27 / 53 : 13      400  82 : 156 / 70 : 33 / 79 : 13
+    //   fp32, rank 128   64 rows  29 : 169 / 27 : 77 / 19 : 10         256  98 : 268 / 94 : 48 / 63 : 14      400  150 : 274 / 140 : 47 / 94 : 14
+    // So the worst case decides for small batches (decoding: requests of their own), and short prompts of one request pay for it up
+    // to four times.  Then the largest cluster whose CTAs number up to 2.5 an SM: two places each, or for the ranks that take an SM to a
+    // CTA some waves (1000 rows of 16 requests, rank 16: 14 in clusters of 4, 27 by themselves, 16 in clusters of 8; fp32 rank 128: 66, 156,
+    // 79; 64 single rows of fp32 rank 64 are quicker in clusters of 2, 16 against 20; 4077 rows 28, and 36 in clusters of 4).
     const int R = p.T <= 2 * sms ? 1 : 16, tiles = (p.T + R - 1) / R;
     int C = kMaxCluster;
     while (C > 1 && tiles * C > 2 * sms + sms / 2) C /= 2;

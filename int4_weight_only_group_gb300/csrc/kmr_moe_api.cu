@@ -28,7 +28,6 @@ int counts_ok(int T, int top_k) {
     return top_k < 1 || top_k > kMoeMaxTopK ? KMR_ERR_SHAPE : KMR_OK;
 }
 
-// The few-token form takes the calls whose places fit a warp's lanes.
 // Tokens of one pass of the grouped form: bounds the workspace.
 int chunk_of(int T, int top_k) {
     const int most = kMoeChunkPlaces / top_k;

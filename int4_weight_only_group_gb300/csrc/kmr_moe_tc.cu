@@ -11,14 +11,14 @@
 //
 // The product, D[row][token] = sum_k w[row][k] x[token][k], w = (q - 8) s + z:
 //   * A = (q - 8) s rho 2^-24: a 4-bit integer times a bf16 scale has 11 significant bits, so fp16 holds it exactly once a power of
-//     two rho per row (laid out once, moe_factors_kernel) has brought the row's scales into its range (groups whose scale is below
-//     2^-7 of the row's largest lose bits below 2^-20 of the row's largest weight).  A nibble under a zero mantissa is the
+//     two rho per row (laid out once, moe_factors_kernel) has brought the row's scales into its range (a group whose scale is below
+//     2^-6 of the row's largest loses what lies below 2^-24, against a largest weight of 2^-8 or more).  A nibble under a zero mantissa is the
 //     fp16 number q 2^-24 as it stands, so a weight is one AND and half an HFMA2: q 2^-24 * (s rho) - 8 s rho 2^-24.  (With 1024
 //     + q, an addition and a multiplication the half-rate fp16 pipe is the bound.)
 //   * the zero points' share sum_g z_g X_g, X_g = sum of the group's inputs, goes through the same accumulator as one more MMA for
 //     every two groups: z rho 2^6 against X 2^-6 for every 64 inputs, X in two fp16 terms.
-//   * B = x sigma (a power of two per row): exact for bf16 inputs, two terms (the fp16 rounding and what it left, two
-//     MMAs on the same A) for fp32 ones.  So products are exact and sums are fp32 in both types.
+//   * B = x sigma (a power of two per row): exact for bf16 inputs down to 2^-30 of the row's largest, two terms (the fp16 rounding
+//     and what it left, 22 bits down to 2^-16, two MMAs on the same A) for fp32 ones.  The products of these are exact, sums are fp32.
 //   * the accumulators of a tile take a row's whole sum, so an activation row has one scale: that of its largest value, which is
 //     known when all of its tiles are.  Hence act, a pass over the rows by itself.  (A scale from bounds, |silu(g) u| <= (|x|
 //     max |gate row|) (|x| max |up row|), needs no pass but is loose by the spread of the rows' sizes twice over, and by
@@ -30,9 +30,9 @@
 // sums).  Every wait is bounded; a timeout records KMR_ERR_DEVICE_TIMEOUT, skips the remaining work, drains the copies in
 // flight and frees tensor memory.
 //
-// Measured (us: plan, stage, gate_up, down, combine; hidden 2048).  128 experts of 768, 8 a token: 16 rows fp32 5, 6, 40, 25, 4;
-// 509 rows fp32 6, 9.5, 108, 49, 9.5; 4096 rows bf16 12, 52, 178, 102, 28.  8 experts of 6144, 2 a token, bf16: 1024 rows 6, 7, 94,
-// 60, 7.  What bounds the products: for small tiles the turning of KMR4 blocks into A (2,300 cycles for each of three sets of
+// Measured (us: plan, stage, gate_up, act, down, combine; hidden 2048).  128 experts of 768, 8 a token: 16 rows fp32 5, 5, 37, 4.5, 25,
+// 4; 509 rows fp32 6, 9, 99, 8, 49, 9.5; 4096 rows bf16 10, 52, 165, 30, 103, 28.  8 experts of 6144, 2 a token, bf16: 1024 rows 5, 6,
+// 89, 18, 60, 7.  What bounds the products: for small tiles the turning of KMR4 blocks into A (2,300 cycles for each of three sets of
 // warps a pair of groups, 14 bytes of weights a cycle on an SM) and its hand-overs; for tiles of 128 the MMAs' 1,090 cycles a
 // pair and theirs (1,550 in all); for fp32 tiles of 32 to 64 the epilogue, which reads every group's sums.
 #include <cuda_fp16.h>
@@ -329,7 +329,8 @@ __device__ __forceinline__ void mma_ss(uint32_t taddr, uint64_t ad, uint64_t bd,
                  : "memory");
 }
 __device__ __forceinline__ void epilogue_bar() { asm volatile("bar.sync 1, %0;" ::"n"(kEpiWarps * 32) : "memory"); }
-// silu(x) * up.  bf16 results: the hardware's exponential and reciprocal, each good to 2^-21 or better.
+// silu(x) * up.  bf16 results: __expf, documented to 2 + |1.17 x| units of 2^-23 (2^-18 at |x| = 30, 2^-16 where silu leaves the range of
+// fp32), and __fdividef, to 2 units up to a divisor of 2^126 and 0 beyond (x below -87): far below the 11 bits that are kept.
 template <bool FAST>
 __device__ __forceinline__ float silu_mul(float x, float up) {
     if (FAST) return __fmul_rn(__fdividef(x, __fadd_rn(1.f, __expf(-x))), up);
@@ -880,7 +881,9 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
 }
 
 // ------------------------------------------------------------------ activations
-// From gate_up's fp32 rows to down's operand: W warps (1, 2, 4 or 8) take a place's row, which they read once and hold.
+// From gate_up's fp32 rows to down's operand: W warps (1, 2, 4 or 8) take a place's row, which they read once and hold.  4096 rows of
+// 8 x 768: 30 us (150 MB, most of it L2: 5 TB/s); 1024 of 2 x 6144: 18.  (Four float4 a lane and twice the warps: 38 and 20; a bound
+// of 48 or 40 registers spills.)
 constexpr int kActThr = 256, kActPer = 8;                  // float4 of a lane: W x 1024 values of a row
 template <int NP, int W>
 __global__ void __launch_bounds__(kActThr) moe_act_kernel(const MoeTcParams p) {

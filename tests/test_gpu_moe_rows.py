@@ -34,9 +34,9 @@ def rounded(torch, a, dtype):
 
 
 class Layer:
-    """Experts whose scales and zeros are given: s and z [E][N, K / 128] of gate_up and of down."""
+    """Experts whose scales and zeros are given: s and z [E][N, K / 128] of gate_up and of down; inputs `eights` have codes of 8."""
 
-    def __init__(self, torch, r, H, I, gate_up, down):
+    def __init__(self, torch, r, H, I, gate_up, down, eights=()):
         E = len(gate_up[0])
         self.shape, self.gate_up, self.down, packed = (E, H, I), [], [], []
         for (ss, zz), N, K, flags, keep in ((gate_up, 2 * I, H, kmr.KMR_PACK_GATE_UP, self.gate_up), (down, H, I, 0, self.down)):
@@ -44,6 +44,8 @@ class Layer:
             out = torch.empty((E, size), dtype=torch.uint8, device="cuda")
             for e in range(E):
                 q = r.integers(0, 16, (N, K), dtype=np.uint8)
+                if flags == kmr.KMR_PACK_GATE_UP:
+                    q[:, eights] = 8
                 s, z = (torch.from_numpy(np.ascontiguousarray(v[e], np.float32)).bfloat16() for v in (ss, zz))
                 keep.append(moe.dense(q, s.float().numpy(), z.float().numpy()))
                 kmr.kmr_pack_int4(torch.from_numpy(q).cuda(), s.cuda(), z.cuda(), N, K, 128, flags, out[e], size, True, torch.cuda.current_stream())
@@ -146,6 +148,24 @@ def test_inputs_and_weights_far_from_one(torch, T, x_size, w_size, dtype):
     ids, w = places(r, T, E, k)
     want = moe.experts(xv, ids, w, layer.gate_up, layer.down)
     assert 1e-30 < np.abs(want).max(1).min() and np.abs(want).max() < 1e30
+    assert worst(run(torch, layer, x, ids, w, dtype), want) <= TOL[dtype]
+
+
+@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("dtype,F", [(kmr.KMR_F32, 2.0 ** 10), (kmr.KMR_F32, 2.0 ** 14), (kmr.KMR_BF16, 2.0 ** 14), (kmr.KMR_BF16, 2.0 ** 26)])
+def test_inputs_of_unequal_size(torch, T, dtype, F):
+    """One input of every 128 some F times the others', of weights that are zero: the others keep their bits (they go down
+    to 2^-3 of each other, and 1/F of that of the largest)."""
+    r = np.random.default_rng(37)
+    E, H, I, k = 4, 512, 384, 2
+    (gs, gz), (ds, dz) = even(r, E, 2 * I, H), even(r, E, H, I)
+    big = np.arange(5, H, 128)
+    layer = Layer(torch, r, H, I, (gs, gz * 0), (ds, dz), big)
+    a = r.uniform(0.25, 2.0, (T, H)) * r.choice([-1.0, 1.0], (T, H))
+    a[:, big] *= F
+    x, xv = rounded(torch, a, dtype)
+    ids, w = places(r, T, E, k)
+    want = moe.experts(xv, ids, w, layer.gate_up, layer.down)
     assert worst(run(torch, layer, x, ids, w, dtype), want) <= TOL[dtype]
 
 
