@@ -424,7 +424,7 @@ typedef struct kmr_lora {
  *                a fused projection's rows (the v part of QKV, say); what lies between its rows is left as it was
  *   adapter_ids  device int32 [T]; -1: y[t] = base[t]
  * x, base and y are 16-byte aligned, ldx >= K and ldy >= N multiples of 8.  fp32 operands are multiplied to single
- * precision (magnitudes below 3.38e38).  Errors: KMR_ERR_INVALID_ARG (pointers, dtype), KMR_ERR_SHAPE, KMR_ERR_BATCH; on
+ * precision (magnitudes below 3.38e38); of bf16 rows A_a x[t] is held in two bf16 numbers (16 bits).  Sums are fp32.  Errors: KMR_ERR_INVALID_ARG (pointers, dtype), KMR_ERR_SHAPE, KMR_ERR_BATCH; on
  * the device KMR_ERR_INVALID_ARG (an id outside -1..adapters - 1, whose row is treated as -1). */
 int kmr_lora_apply(const kmr_lora* lora, const void* x, const void* base, void* y, int dtype,
                    const int32_t* adapter_ids, int T, long long ldx, long long ldy, void* stream);

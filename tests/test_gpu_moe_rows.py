@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from gpu_helpers import rel_l2, require_gpu
+from test_gpu_moe import SHAPES
 import int4_weight_only_group_gb300 as kmr
 from oracle import moe
 
@@ -132,6 +133,17 @@ def test_rows_of_unequal_size(torch, E, H, I, T, k, how, F, dtype):
     for scale, columns in ((size, size > 0), (np.ones(H), size <= 1.0)):
         for t in range(len(some)):
             assert rel_l2((got[some[t]] / scale)[columns], (want[t] / scale)[columns]) <= tol[t]
+
+
+@pytest.mark.parametrize("E,H,I,T,k", SHAPES)
+def test_single_precision_in_every_shape(torch, E, H, I, T, k):
+    r = np.random.default_rng(E + H + I + T)
+    layer = Layer(torch, r, H, I, even(r, E, 2 * I, H), even(r, E, H, I))
+    x, xv = rounded(torch, r.standard_normal((T, H)) * np.exp(r.standard_normal((T, 1))), kmr.KMR_F32)
+    ids, w = (np.concatenate(v, 1) for v in zip(*[places(r, T, E, min(k - i, E)) for i in range(0, k, E)]))
+    some = np.unique(r.integers(0, T, 48))
+    want = moe.experts(xv[some], ids[some], w[some], layer.gate_up, layer.down)
+    assert worst(run(torch, layer, x, np.ascontiguousarray(ids), np.ascontiguousarray(w), kmr.KMR_F32)[some], want) <= TOL[kmr.KMR_F32]
 
 
 @pytest.mark.parametrize("dtype", DT)
