@@ -65,7 +65,7 @@ struct MoeTcParams {
     int32_t* pos;                            // [T][k]: the place's position, or -1
     float* isx;                              // [P] 1 / scale of the position's inputs
     float* isa;                              // [P] 1 / scale of its activations
-    float* sout;                             // [P] bf16: scale of its result while it waits for the sum
+    float* sout;                             // [P] bf16: scale of its result while it waits for the sum (fp32: not used)
     size_t blocks;                           // P / 8
     uint8_t* xs;                             // staged inputs
     uint8_t* as;                             // staged activations

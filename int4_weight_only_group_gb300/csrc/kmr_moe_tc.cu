@@ -761,7 +761,7 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
         auto factors = [&](int it, const int4& tl) {
             if (et < tl.w) {
                 f0 = GATE ? p.isx[tl.y + et] : p.isa[tl.y + et];
-                if (!GATE) f1 = p.sout[tl.y + et];
+                if (!GATE && NP == 1) f1 = p.sout[tl.y + et];
             }
             irho = rho[size_t(tl.x) * N + (it % R) * kRows + 32 * q + lane];
         };
@@ -771,7 +771,7 @@ __global__ void __launch_bounds__(product_threads(SETS), 1) moe_product_kernel(c
             float* f = fac + turn * 256;
             if (et < real) {
                 f[et] = 0x1p12f * f0;
-                if (!GATE) f[128 + et] = f1;
+                if (!GATE && NP == 1) f[128 + et] = f1;
             }
             const float ir = 0x1p12f * inverse_pow2(irho);     // (the 2^24 of A, half of it with either factor)
             ahead = tile_of(it + step);
